@@ -55,7 +55,7 @@ enum kda_status {
     KDA_ERR_DEVICE_CHECK = 6   /* device-side validation failed (see code)      */
 };
 
-enum kda_dtype { KDA_BF16 = 0, KDA_F32 = 1 };
+enum kda_dtype { KDA_BF16 = 0, KDA_F32 = 1, KDA_E4M3 = 2 /* paged caches only */ };
 
 /* Input options (bit flags), the kernel-side options of the pages' chunk_kda /
  * fused_recurrent_kda ("Kimi K3 模型结构（2）", section "训练、prefill、decode
@@ -82,7 +82,11 @@ enum kda_device_error {
     KDA_DEVERR_NONE = 0,
     KDA_DEVERR_CU_SEQLENS = 1,     /* cu_seqlens not 0 .. T_total, non-decreasing */
     KDA_DEVERR_NUM_ACCEPTED = 2,   /* num_accepted[b] outside 0 .. W-1            */
-    KDA_DEVERR_TIMEOUT = 4         /* a bounded wait gave up                       */
+    KDA_DEVERR_TIMEOUT = 4,        /* a bounded wait gave up                       */
+    KDA_DEVERR_LENGTHS = 8,        /* a length of the paged calls is negative, past the block table, or the
+                                      new tokens do not add up to T_total           */
+    KDA_DEVERR_NO_PAGES = 16,      /* the list of free pages is too short          */
+    KDA_DEVERR_PAGE = 32           /* a page or slot outside the cache             */
 };
 
 /* Human-readable name of a kda_status. Never NULL. */
@@ -382,6 +386,116 @@ int kda_decode_step_fused(float *state,
                           const int32_t *num_accepted,
                           int N, int H, int D, int W, int dtype, float g_min,
                           void *o, int32_t *error_word, int flags, kda_stream_t stream);
+
+/* ==========================================================================
+ * The paged key/value cache of the full-attention layers that a hybrid model
+ * puts between its linear-attention layers ("Kimi K3 模型结构（7）", section
+ * "混合架构的前缀缓存": one page pool for the hybrid's layers, head-contiguous
+ * pages).  Per serving step: kda_paged_tables once, then for every
+ * full-attention layer kda_paged_append and kda_paged_attn.
+ *
+ * Conventions of the three calls
+ *   - A cache (K or V) is [n_pages, Hkv, page_size, D]: one head's part of a
+ *     page is contiguous.  Pages start page_stride elements apart
+ *     (page_stride >= Hkv * page_size * D, a multiple of 16 bytes), so K and V
+ *     may be two halves of one pool.  page_size is a multiple of 16, D is 128.
+ *   - slot = page * page_size + offset (int64).
+ *   - cache_dtype equals dtype, or is KDA_E4M3 with dtype KDA_BF16: the cache
+ *     then holds x / scale rounded to e4m3 (saturating at +-448), with one
+ *     fp32 scale per kv head for K and one for V.
+ *   - Lengths, tables and slots live on the device and are checked there:
+ *     what is wrong is OR-ed into error_word (device int32, or NULL), and is
+ *     never used as an address.
+ * ========================================================================== */
+
+/* --------------------------------------------------------------------------
+ * kda_paged_tables -- block tables, slot map, positions and offsets of a
+ * step's new tokens, from the requests' lengths and a list of free pages.
+ * Request i holds ctx_len[i] cached tokens and gains new_len[i]; with
+ *   had = ceil(ctx / page_size), have = ceil((ctx + new) / page_size)
+ * it takes have - had pages from the list, requests in order:
+ *   block_table[i][b] = free_pages[f_i + b - had], had <= b < have,
+ *   f_i = *free_head + sum_{j<i} (have_j - had_j).
+ * Token t of request i (the new tokens packed in request order):
+ *   positions[t] = ctx + t - cu_q[i],  slot_map[t] from block_table.
+ *
+ *   new_len, ctx_len (device) int32 [n_seqs], >= 0
+ *   n_seqs       1 .. 16384;  T_total = sum of new_len, 0 <= T_total < 2^31
+ *   block_table  (device) int32 [n_seqs, max_blocks]: entries 0 .. had - 1 are
+ *                read where a token falls into a page that is not new, entries
+ *                had .. have - 1 are written, the others are left alone
+ *   free_pages   (device) int32 [n_free] (may be NULL when n_free is 0)
+ *   free_head    (device) int32 [1]: entries of free_pages already taken
+ *   free_head_next (device) int32 [1], written: free_head plus the pages taken;
+ *                must not be free_head itself (blocks of one launch read the one
+ *                while another writes the other)
+ *   slot_map     (device) int64 [T_total], written
+ *   positions    (device) int32 [T_total] or NULL
+ *   cu_q         (device) int32 [n_seqs + 1], written;  kv_len (device) int32
+ *                [n_seqs], written: ctx + new
+ * Lengths that are negative, exceed max_blocks * page_size or do not add up to
+ * T_total record KDA_DEVERR_LENGTHS, too few free pages KDA_DEVERR_NO_PAGES;
+ * either leaves every output unwritten but free_head_next = *free_head.  A page
+ * outside 0 .. n_pages - 1 records KDA_DEVERR_PAGE; its tokens get slot -1 and
+ * a new entry becomes -1.
+ * ------------------------------------------------------------------------ */
+int kda_paged_tables(const int32_t *new_len, const int32_t *ctx_len, int n_seqs, int64_t T_total,
+                     int32_t *block_table, int max_blocks, const int32_t *free_pages, int n_free,
+                     const int32_t *free_head, int32_t *free_head_next, int page_size, int n_pages,
+                     int64_t *slot_map, int32_t *positions, int32_t *cu_q, int32_t *kv_len,
+                     int32_t *error_word, kda_stream_t stream);
+
+/* --------------------------------------------------------------------------
+ * kda_paged_append -- the new tokens' keys and values into the pages.
+ *   k, v         (device) [T_total, Hkv, D] dtype, 16-byte aligned
+ *   slot_map     (device) int64 [T_total]; a negative slot is skipped, one at or
+ *                past n_pages * page_size is skipped and records KDA_DEVERR_PAGE;
+ *                two tokens must not share a slot
+ *   k_scale, v_scale (device) fp32 [Hkv], KDA_E4M3 only (else NULL), > 0
+ *   k_cache, v_cache (device) the caches, written at the slots
+ * ------------------------------------------------------------------------ */
+int kda_paged_append(const void *k, const void *v, const int64_t *slot_map, int64_t T_total, int Hkv, int D,
+                     int dtype, int cache_dtype, const float *k_scale, const float *v_scale, void *k_cache,
+                     void *v_cache, int n_pages, int page_size, int64_t page_stride, int32_t *error_word,
+                     kda_stream_t stream);
+
+/* --------------------------------------------------------------------------
+ * kda_paged_attn -- attention of every request's new tokens over its cached
+ * keys (its new tokens' own keys among them: append first).
+ * Request i's n_i = cu_q[i+1] - cu_q[i] queries stand at the positions
+ * kv_len[i] - n_i .. kv_len[i] - 1; the query at position p sees the keys
+ * max(0, p - window + 1) .. p (window 0: all up to p).  Query head h reads kv
+ * head h / (Hq / Hkv).
+ *   o   = softmax(sm_scale q K^T) V,   lse = log sum exp(sm_scale q K^T)
+ * A query that sees no key (p < 0) gets o = 0, lse = -inf.
+ *
+ *   q            (device) [T_total, Hq, D] dtype, 16-byte aligned
+ *   k_cache, v_cache, k_scale, v_scale, page_size, page_stride: as above; what
+ *                the pages hold past kv_len (NaN included) has no influence
+ *   block_table  (device) int32 [n_seqs, max_blocks]; only the entries of pages
+ *                that hold a seen key are read
+ *   cu_q         (device) int32 [n_seqs + 1];  kv_len (device) int32 [n_seqs]
+ *   max_q        the most new tokens of one request (0: not known, T_total)
+ *   sm_scale     > 0 (1 / sqrt(128) is the usual one)
+ *   o            (device) [T_total, Hq, D] dtype, written, 16-byte aligned
+ *   lse          (device) fp32 [T_total, Hq] or NULL: natural logarithm
+ *   workspace    kda_paged_attn_workspace_size() bytes, 256-byte aligned; needs
+ *                no initialisation, not shared by calls in flight
+ * A request whose offsets are not 0 <= cu_q[i] <= cu_q[i+1] <= T_total, or
+ * that has over max_q tokens, records KDA_DEVERR_CU_SEQLENS and is left
+ * out (its outputs are not written); a kv_len outside 0 .. max_blocks *
+ * page_size records KDA_DEVERR_LENGTHS and counts as 0 (o = 0); a page outside
+ * the cache records KDA_DEVERR_PAGE and that request's outputs are undefined.
+ * The result does not depend on timing: the same call gives the same bits.
+ * ------------------------------------------------------------------------ */
+size_t kda_paged_attn_workspace_size(int64_t T_total, int n_seqs, int Hq, int Hkv);
+
+int kda_paged_attn(const void *q, const void *k_cache, const void *v_cache, const int32_t *block_table,
+                   const int32_t *cu_q, const int32_t *kv_len, int n_seqs, int64_t T_total, int max_q, int Hq,
+                   int Hkv, int D, int dtype, int cache_dtype, const float *k_scale, const float *v_scale,
+                   int n_pages, int page_size, int64_t page_stride, int max_blocks, float sm_scale, int window,
+                   void *o, float *lse, void *workspace, size_t workspace_bytes, int32_t *error_word,
+                   kda_stream_t stream);
 
 /* --------------------------------------------------------------------------
  * kda_read_device_error -- synchronise `stream` and read the device error

@@ -13,6 +13,7 @@
 #include <mutex>
 
 #include "kda_internal.cuh"
+#include "kda_paged.cuh"
 
 namespace kda {
 
@@ -56,6 +57,29 @@ int make_input_maps(const void *q, const void *k, const void *v, const float *z,
     if ((rc = encode_rows(&out->k, k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, T, H))) return rc;
     if ((rc = encode_rows(&out->v, v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, T, H))) return rc;
     return encode_rows(&out->z, z, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, T, H);
+}
+
+// Paged caches: {D, Hkv * page_size, pages}, one tile = box_rows keys of one
+// head of one page, 128 bytes of each row, stored with the 128-byte swizzle.
+int make_paged_maps(const void *k, const void *v, int cache_dtype, int Hkv, int page_size, int n_pages,
+                    int64_t page_stride, int box_rows, PagedMaps *out) {
+    const EncodeTiledFn fn = encode_tiled();
+    if (!fn) return KDA_ERR_CUDA;
+    const int el = cache_dtype == KDA_BF16 ? 2 : cache_dtype == KDA_F32 ? 4 : 1;
+    const CUtensorMapDataType type = cache_dtype == KDA_BF16  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                     : cache_dtype == KDA_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                                              : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    const cuuint64_t dim[3] = {(cuuint64_t)D, (cuuint64_t)Hkv * page_size, (cuuint64_t)n_pages};
+    const cuuint64_t stride[2] = {(cuuint64_t)D * el, (cuuint64_t)page_stride * el};
+    const cuuint32_t box[3] = {(cuuint32_t)(128 / el), (cuuint32_t)box_rows, 1u};
+    const cuuint32_t estride[3] = {1u, 1u, 1u};
+    for (int i = 0; i < 2; ++i) {
+        const CUresult r = fn(i ? &out->v : &out->k, type, 3, const_cast<void *>(i ? v : k), dim, stride, box, estride,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        if (r != CUDA_SUCCESS) return KDA_ERR_CUDA;
+    }
+    return KDA_OK;
 }
 
 }  // namespace kda

@@ -1,0 +1,344 @@
+"""The paged cache's operators against their plain 64-bit forms."""
+import pytest
+import torch
+
+import linear_attention_serving_gb300 as kda
+from linear_attention_serving_gb300 import paged
+from paged_testutil import D, attn_close, attn_ref, cdiv, make, tables_ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF16, F32, E4M3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+def errw():
+    return torch.zeros(1, dtype=torch.int32, device=DEV)
+
+
+# ------------------------------------------------------------------ tables
+TABLES = [
+    ([1], [0], 16), ([1], [15], 16), ([1], [16], 16), ([0, 0], [5, 0], 16),
+    ([3, 0, 17, 1], [14, 16, 0, 33], 16), ([64, 65, 63], [0, 1, 128], 64), ([1] * 700, list(range(700)), 32),
+    ([0, 5, 0, 0, 9, 0], [1, 2, 3, 4, 5, 6], 48), ([700, 0, 801], [3, 9, 0], 16),
+]
+
+
+def run_tables(new, ctx, ps, head=2, spare_free=3, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    width = max(1, max(cdiv(a + b, ps) for a, b in zip(new, ctx))) + 2
+    need = sum(cdiv(a + b, ps) - cdiv(b, ps) for a, b in zip(new, ctx))
+    had = [cdiv(c, ps) for c in ctx]
+    pages = sum(had) + head + need + spare_free
+    perm = torch.randperm(pages, generator=g).tolist()
+    table, at = [], 0
+    for h in had:
+        table.append(perm[at:at + h] + [-3] * (width - h))
+        at += h
+    free = perm[at:]
+    ref = tables_ref(new, ctx, table, free, head, ps)
+    t = i32(table)
+    e = errw()
+    out = kda.paged_tables(i32(new), i32(ctx), t, i32(free), i32([head]), sum(new), ps, pages, error_word=e)
+    return ref, t, out, int(e)
+
+
+@pytest.mark.parametrize("new,ctx,ps", TABLES)
+def test_tables(new, ctx, ps):
+    ref, table, (slots, pos, cu, kv, head), e = run_tables(new, ctx, ps)
+    assert e == 0
+    assert table.tolist() == ref[0]
+    assert slots.tolist() == ref[1] and pos.tolist() == ref[2]
+    assert cu.tolist() == ref[3] and kv.tolist() == ref[4] and head.tolist() == [ref[5]]
+
+
+def test_tables_many_tokens():
+    """Over the size where a thread takes four tokens, with ends that are not multiples of four."""
+    new, ctx = [120001, 0, 3, 80002, 1, 70006], [7, 2, 30, 0, 15, 100]
+    ref, table, (slots, pos, cu, kv, head), e = run_tables(new, ctx, 16)
+    assert e == 0 and table.tolist() == ref[0]
+    assert torch.equal(slots.cpu(), torch.tensor(ref[1])) and torch.equal(pos.cpu().long(), torch.tensor(ref[2]))
+    assert cu.tolist() == ref[3] and head.tolist() == [ref[5]]
+
+
+def test_tables_many_requests():
+    n = 5000
+    new, ctx = [(i * 7) % 4 for i in range(n)], [(i * 13) % 50 for i in range(n)]
+    ref, table, (slots, pos, cu, kv, head), e = run_tables(new, ctx, 16)
+    assert e == 0 and table.tolist() == ref[0] and slots.tolist() == ref[1] and cu.tolist() == ref[3]
+
+
+def _tables_fail(new, ctx, T, free_n, expect, head=0, table=None, pages=64):
+    n, ps = len(new), 16
+    t = i32(table or [[50] * 8] * n)
+    before = t.clone()
+    e = errw()
+    out = kda.paged_tables(i32(new), i32(ctx), t, i32(list(range(free_n))), i32([head]), T, ps, pages, error_word=e)
+    assert int(e) & expect, int(e)
+    return before, t, out
+
+
+@pytest.mark.parametrize("new,ctx,T,free_n,expect", [
+    ([3, -1], [0, 0], 2, 9, paged.DEVERR_LENGTHS), ([3], [-2], 3, 9, paged.DEVERR_LENGTHS),
+    ([3, 3], [0, 0], 7, 9, paged.DEVERR_LENGTHS), ([100], [100], 100, 99, paged.DEVERR_LENGTHS),
+    ([40, 1], [0, 0], 41, 3, paged.DEVERR_NO_PAGES)])
+def test_tables_refuses_on_the_device(new, ctx, T, free_n, expect):
+    before, t, (_, _, _, _, head) = _tables_fail(new, ctx, T, free_n, expect)
+    assert torch.equal(before, t) and head.tolist() == [0]
+
+
+def test_tables_bad_pages():
+    """A page outside the cache: its tokens get slot -1 and nothing else changes."""
+    t = i32([[2, -1, -1], [99, -1, -1]])
+    e = errw()
+    slots, *_ = kda.paged_tables(i32([10, 3]), i32([10, 4]), t, i32([1, 77, 3]), i32([1]), 13, 16, 8, error_word=e)
+    assert int(e) == paged.DEVERR_PAGE
+    assert slots.tolist() == [2 * 16 + 10 + j for j in range(6)] + [-1] * 7
+    assert t.tolist() == [[2, -1, -1], [99, -1, -1]]
+
+
+# ------------------------------------------------------------------ append
+@pytest.mark.parametrize("dtype,cache", [(BF16, BF16), (BF16, E4M3), (F32, F32)])
+@pytest.mark.parametrize("T,hkv,ps", [(1, 1, 16), (37, 3, 48), (300, 8, 64)])
+def test_append(T, hkv, ps, dtype, cache):
+    g = torch.Generator().manual_seed(T)
+    pages = cdiv(T, ps) + 4
+    slots = torch.randperm(pages * ps, generator=g)[:T]
+    slots[T // 2] = -1
+    k, v = (torch.randn(T, hkv, D, generator=g).to(dtype) for _ in range(2))
+    if T > 1:
+        k[0, 0, :4] = torch.tensor([float("inf"), -1e30, 0.0, 1e-30], dtype=dtype)
+    sc = {}
+    if cache == E4M3:
+        sc = {"k_scale": 0.01 + torch.rand(hkv, generator=g) / 50, "v_scale": 0.01 + torch.rand(hkv, generator=g) / 50}
+    raw = {BF16: torch.int16, F32: torch.int32, E4M3: torch.uint8}[cache]
+    # K and V as the two halves of one pool: pages lie apart
+    pool = torch.randint(0, 100, (pages, 2, hkv, ps, D), dtype=raw, generator=g).to(DEV)
+    want = pool.cpu().clone()
+    for half, x, s in ((0, k, sc.get("k_scale")), (1, v, sc.get("v_scale"))):
+        y = x.float() / s.view(1, -1, 1) if s is not None else x
+        y = (y.clamp(-448, 448) if s is not None else y).to(cache).view(raw)
+        for t in range(T):
+            if slots[t] >= 0:
+                want[slots[t] // ps, half, :, slots[t] % ps] = y[t]
+    halves = pool.view(cache)
+    e = errw()
+    kda.paged_append(k.to(DEV), v.to(DEV), slots.to(DEV), halves[:, 0], halves[:, 1],
+                     **{n: x.to(DEV) for n, x in sc.items()}, error_word=e)
+    assert int(e) == 0 and torch.equal(pool.cpu(), want)
+
+
+def test_append_skips_slots_outside_the_cache():
+    c = torch.zeros(2, 1, 16, D, dtype=BF16, device=DEV)
+    x = torch.ones(3, 1, D, dtype=BF16, device=DEV)
+    e = errw()
+    kda.paged_append(x, x, torch.tensor([32, 5, 1 << 40], device=DEV), c, c.clone(), error_word=e)
+    assert int(e) == paged.DEVERR_PAGE
+    assert c.sum().item() == D and c[0, 0, 5].sum().item() == D
+
+
+# ------------------------------------------------------------------ attention
+def run_attn(d, window=0, max_q=0, scale=D ** -0.5, **kw):
+    t = {n: (x.to(DEV) if isinstance(x, torch.Tensor) else x) for n, x in d.items()}
+    e = errw()
+    o, lse = kda.paged_attn(t["q"], t["k_cache"], t["v_cache"], i32(d["table"]), i32(d["cu"]), i32(d["kv"]), max_q=max_q,
+                            window=window, sm_scale=scale, k_scale=t["k_scale"], v_scale=t["v_scale"], error_word=e, **kw)
+    torch.cuda.synchronize()
+    return o, lse, int(e)
+
+
+def check(new, ctx, hkv, g, ps, cache, window=0, kv=None, scale=D ** -0.5, seed=0, **kw):
+    d = make(new, ctx, hkv, g, ps, cache, seed)
+    if kv is not None:
+        d["kv"] = kv
+    o, lse, e = run_attn(d, window, max(new), scale, **kw)
+    assert e == 0
+    ref = attn_ref(d["q"], d["k_cache"], d["v_cache"], d["table"], d["cu"], d["kv"], scale, window, d["k_scale"], d["v_scale"])
+    attn_close(o, lse, ref, d["q"].dtype, cache)
+    return d, o, lse
+
+
+CACHES = [BF16, E4M3, F32]
+NAMES = ["bf16", "e4m3", "f32"]
+
+
+@pytest.mark.parametrize("cache", CACHES, ids=NAMES)
+@pytest.mark.parametrize("ctx", [0, 1, 15, 16, 31, 32, 63, 64, 65, 127, 700])
+def test_attn_one_token(ctx, cache):
+    check([1], [ctx], 2, 4, 16, cache)
+
+
+@pytest.mark.parametrize("cache", CACHES, ids=NAMES)
+@pytest.mark.parametrize("hkv,g", [(1, 1), (3, 5), (2, 16), (1, 17), (1, 33), (2, 8), (1, 96)])
+def test_attn_head_layouts(hkv, g, cache):
+    check([1, 2, 1], [40, 3, 130], hkv, g, 32, cache)
+
+
+@pytest.mark.parametrize("cache", CACHES, ids=NAMES)
+@pytest.mark.parametrize("ps", [16, 32, 48, 64, 80, 128, 256])
+def test_attn_page_sizes(ps, cache):
+    check([1, 5, 20, 0, 3], [300, 0, 77, 50, 129], 2, 3, ps, cache)
+
+
+@pytest.mark.parametrize("cache", CACHES, ids=NAMES)
+@pytest.mark.parametrize("new,ctx", [([33], [0]), ([70, 1], [5, 200]), ([130], [131]), ([1, 140, 2, 65], [90, 0, 0, 64])])
+def test_attn_chunks(new, ctx, cache):
+    check(new, ctx, 2, 3, 16, cache)
+
+
+@pytest.mark.parametrize("cache", CACHES, ids=NAMES)
+@pytest.mark.parametrize("window", [1, 2, 16, 33, 100, 1000])
+def test_attn_window(window, cache):
+    check([1, 4, 90], [300, 150, 60], 1, 2, 16, cache, window=window)
+
+
+@pytest.mark.parametrize("cache", CACHES, ids=NAMES)
+def test_attn_window_pages_given_back(cache):
+    """Pages that hold no seen key may have left the table."""
+    d = make([1, 3], [500, 201], 2, 2, 16, cache)
+    d2 = {**d, "table": [list(r) for r in d["table"]]}
+    for i, (n, kv) in enumerate(zip([1, 3], d["kv"])):
+        for b in range((kv - n - 50 + 1) // 16):
+            d2["table"][i][b] = -9
+    o, lse, e = run_attn(d, window=50)
+    o2, lse2, e2 = run_attn(d2, window=50)
+    assert e == 0 and e2 == 0 and torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("cache", CACHES, ids=NAMES)
+def test_attn_rows_that_see_nothing(cache):
+    """Fewer keys than new tokens: the first queries stand before position 0."""
+    d, o, lse = check([5, 3, 40], [0, 0, 0], 2, 3, 16, cache, kv=[2, 0, 7])
+    assert (o[:3] == 0).all() and (o[5:8] == 0).all() and torch.isinf(lse[5:8]).all()
+
+
+@pytest.mark.parametrize("cache", CACHES, ids=NAMES)
+def test_attn_split_over_blocks(cache):
+    """Long contexts beside short ones: items cut by many block borders, and whole ones between."""
+    check([1, 1, 2, 1], [9000, 10, 4100, 0], 2, 4, 64, cache, seed=3)
+
+
+@pytest.mark.parametrize("cache", CACHES, ids=NAMES)
+def test_attn_large_scores(cache):
+    """A wide softmax range: probabilities far below the largest, and a maximum that moves late."""
+    d = make([2], [600], 1, 2, 16, cache, q_std=6.0)
+    o, lse, e = run_attn(d)
+    attn_close(o, lse, attn_ref(d["q"], d["k_cache"], d["v_cache"], d["table"], d["cu"], d["kv"], k_scale=d["k_scale"],
+                                v_scale=d["v_scale"]), d["q"].dtype, cache)
+
+
+def test_attn_small_queries_e4m3():
+    """q far below fp16's range: scaled by powers of two, nothing is lost."""
+    d = make([1], [100], 1, 4, 16, E4M3)
+    d["q"] = (d["q"].float() * 2.0 ** -40).bfloat16()
+    scale = D ** -0.5 * 2.0 ** 40
+    o, lse, e = run_attn(d, scale=scale)
+    attn_close(o, lse, attn_ref(d["q"], d["k_cache"], d["v_cache"], d["table"], d["cu"], d["kv"], scale, 0, d["k_scale"],
+                                d["v_scale"]), BF16, E4M3)
+
+
+@pytest.mark.parametrize("cache", CACHES, ids=NAMES)
+def test_attn_nan_stays_in_its_request(cache):
+    d = make([1, 2], [50, 70], 1, 2, 16, cache)
+    o, lse, _ = run_attn(d)
+    d["k_cache"][d["table"][1][1], 0, 3, 5] = float("nan")
+    o2, lse2, _ = run_attn(d)
+    assert torch.equal(o[0], o2[0]) and torch.equal(lse[0], lse2[0])
+    assert torch.isnan(o2[1:]).all()
+
+
+@pytest.mark.parametrize("cache", CACHES, ids=NAMES)
+def test_attn_pages_apart_and_same_bits(cache):
+    """K and V as halves of one pool give the same bits as separate caches, run after run."""
+    d = make([1, 40, 3], [3000, 60, 500], 2, 4, 32, cache, filler=0.0)
+    o, lse, _ = run_attn(d)
+    pool = torch.stack([d["k_cache"].view(torch.uint8), d["v_cache"].view(torch.uint8)], 1).to(DEV).view(cache)
+    d2 = {**d, "k_cache": pool[:, 0], "v_cache": pool[:, 1]}
+    for _ in range(3):
+        o2, lse2, _ = run_attn(d2)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_attn_other_stream_and_graph():
+    d = make([1, 33], [700, 100], 2, 4, 16, BF16)
+    o, lse, _ = run_attn(d)
+    t = {n: (x.to(DEV) if isinstance(x, torch.Tensor) else x) for n, x in d.items()}
+    args = (t["q"], t["k_cache"], t["v_cache"], i32(d["table"]), i32(d["cu"]), i32(d["kv"]))
+    ws = torch.empty(kda.paged_attn_workspace_size(34, 2, 8, 2), dtype=torch.uint8, device=DEV)
+    out, ol = torch.empty_like(o), torch.empty_like(lse)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        kda.paged_attn(*args, out=out, lse=ol, workspace=ws)
+    side.synchronize()
+    assert torch.equal(out, o) and torch.equal(ol, lse)
+    out.zero_()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kda.paged_attn(*args, out=out, lse=ol, workspace=ws)
+    for _ in range(2):
+        out.zero_()
+        ws.fill_(255)  # the workspace needs no initialisation
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, o) and torch.equal(ol, lse)
+
+
+def test_attn_bad_lengths_are_recorded():
+    """A request that cannot be is left out or counts as empty; the others are untouched."""
+    d = make([1, 2, 1], [40, 50, 60], 1, 2, 16, BF16)
+    o, lse, _ = run_attn(d)
+    d2 = {**d, "kv": [d["kv"][0], 10 ** 6, d["kv"][2]]}
+    o2, lse2, e2 = run_attn(d2)
+    assert e2 == paged.DEVERR_LENGTHS
+    assert torch.equal(o2[0], o[0]) and torch.equal(o2[3], o[3]) and (o2[1:3] == 0).all() and torch.isinf(lse2[1:3]).all()
+    out = torch.full_like(o, 7.0)
+    o3, _, e3 = run_attn({**d, "cu": [0, 1, 300, 4]}, out=out)
+    assert e3 == 1 and torch.equal(o3[0], o[0]) and (o3[1:] == 7).all()
+    out = torch.full_like(o, 7.0)
+    o4, _, e4 = run_attn(d, max_q=1, out=out)
+    assert e4 == 1 and torch.equal(o4[0], o[0]) and torch.equal(o4[3], o[3]) and (o4[1:3] == 7).all()
+
+
+def test_step_runs_together():
+    """tables, append and attention as a serving step calls them, over several
+    steps: the cache ends as if the whole stream had been given at once."""
+    hkv, g, ps, n = 2, 4, 16, 3
+    gen = torch.Generator().manual_seed(9)
+    steps = [[20, 5, 1], [1, 1, 1], [4, 0, 30], [1, 1, 1]]
+    total = [sum(s[i] for s in steps) for i in range(n)]
+    k = [torch.randn(t, hkv, D, generator=gen).bfloat16() for t in total]
+    v = [torch.randn(t, hkv, D, generator=gen).bfloat16() for t in total]
+    pages = 12
+    kc, vc = (torch.full((pages, hkv, ps, D), float("nan"), dtype=BF16, device=DEV) for _ in range(2))
+    table = torch.full((n, 8), -1, dtype=torch.int32, device=DEV)
+    free, head, ctx = i32(torch.randperm(pages, generator=gen).tolist()), i32([0]), i32([0] * n)
+    done = [0] * n
+    for s in steps:
+        T = sum(s)
+        slots, pos, cu, kv, head = kda.paged_tables(i32(s), ctx, table, free, head, T, ps, pages)
+        pick = lambda x: torch.cat([x[i][done[i]:done[i] + s[i]] for i in range(n)]).to(DEV)  # noqa: E731
+        kda.paged_append(pick(k), pick(v), slots, kc, vc)
+        q = torch.randn(T, hkv * g, D, generator=gen).bfloat16()
+        o, lse = kda.paged_attn(q.to(DEV), kc, vc, table, cu, kv, max_q=max(s))
+        ref = attn_ref(q, kc, vc, table.tolist(), cu.tolist(), kv.tolist())
+        attn_close(o, lse, ref, BF16, BF16)
+        ctx, done = kv, [a + b for a, b in zip(done, s)]
+    assert head.tolist() == [sum(cdiv(t, ps) for t in total)]
+    for i in range(n):
+        got = kc[table[i, :cdiv(total[i], ps)].long()].permute(0, 2, 1, 3).reshape(-1, hkv, D)[:total[i]]
+        assert torch.equal(got.cpu(), k[i])
+
+
+def test_attn_page_outside_the_cache():
+    """Recorded and never read; the other requests keep their results."""
+    d = make([1, 1], [100, 100], 1, 2, 16, BF16)
+    o, lse, _ = run_attn(d)
+    for bad in (-1, 10 ** 6, d["k_cache"].shape[0]):
+        t = [list(r) for r in d["table"]]
+        t[1][2] = bad
+        o2, lse2, e = run_attn({**d, "table": t})
+        assert e == paged.DEVERR_PAGE and torch.equal(o2[0], o[0]) and torch.equal(lse2[0], lse[0])
