@@ -8,21 +8,136 @@
 namespace kda {
 namespace {
 
+// ---------------------------------------------------------------- workspace
+// [leads][slots] of the rows kernel, then of the tile kernel: per block one lead
+// (two int4) and two slots
+struct PagedSet {
+    size_t off_lead, off_slots;
+    int blocks, slot_rows;
+};
 struct PagedWs {
-    size_t off_slots, total;
-    int slot_rows;
+    PagedSet rows, tile;
+    size_t total;
 };
 
-// [leads][slots]: two leads' int4 and two slots per block of the rows kernel
+PagedSet paged_set(size_t &off, int blocks, int64_t rows, int cap) {
+    PagedSet p;
+    p.blocks = blocks;
+    p.slot_rows = rows >= cap ? cap : rows < 16 ? 16 : (int)((rows + 15) / 16 * 16);
+    p.off_lead = off;
+    off = align_up(off + (size_t)blocks * 2 * sizeof(int4), 256);
+    p.off_slots = off;
+    off = align_up(off + (size_t)blocks * 2 * paged_slot_floats(p.slot_rows) * sizeof(float), 256);
+    return p;
+}
+
 PagedWs paged_ws(int64_t T, int Hq, int Hkv) {
     PagedWs w;
     const int64_t rows = T * (Hq / Hkv);
-    w.slot_rows = rows >= PAGED_ROWS_CAP ? PAGED_ROWS_CAP : rows < 1 ? 16 : (int)((rows + 15) / 16 * 16);
-    const int blocks = paged_rows_blocks();
-    w.off_slots = align_up((size_t)blocks * 2 * sizeof(int4), 256);
-    w.total = align_up(w.off_slots + (size_t)blocks * 2 * paged_slot_floats(w.slot_rows) * sizeof(float), 256);
+    w.total = 0;
+    w.rows = paged_set(w.total, paged_rows_blocks(), rows, PAGED_ROWS_CAP);
+    w.tile = paged_set(w.total, paged_tile_blocks(), rows, PAGED_TILE_CAP);
     return w;
 }
+
+// ---------------------------------------------------------------- join
+// Merges the pieces of the items that block borders cut.  Blocks (c, y), all y,
+// take the item whose first piece the attention's block c left.  Few pieces: a
+// warp to a row.  Many: a block to a row, its warps taking every eighth piece
+// and meeting in shared memory.  Pieces are taken in block order either way.
+constexpr int JOIN_WARPS = 8;
+constexpr int JOIN_FEW = 12;
+
+struct JoinSet {
+    const int4 *lead;
+    float *parts;
+    int blocks, slot_rows;
+};
+
+__global__ void __launch_bounds__(JOIN_WARPS * 32) paged_join_kernel(PagedAttn a, const JoinSet s0, const JoinSet s1, int f32) {
+    __shared__ float4 acc_s[JOIN_WARPS][32];
+    __shared__ float2 ml_s[JOIN_WARPS];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const JoinSet &js = (int)blockIdx.x < s0.blocks ? s0 : s1;
+    const int c = (int)blockIdx.x < s0.blocks ? blockIdx.x : blockIdx.x - s0.blocks;
+    const int4 y = js.lead[2 * c + 1];
+    if (!y.w) return;
+    const int4 x = js.lead[2 * c];
+    a.parts = js.parts;
+    a.slot_rows = js.slot_rows;
+    const int h = x.y, r0 = x.z, R = x.w, c0 = y.y, np = y.z - y.y + 1;
+    const float vs = a.v_scale ? a.v_scale[h] : 1.f;
+    const bool few = np <= JOIN_FEW;
+    auto slot = [&](int p) { return paged_slot(a, p == 0 ? y.x : 2 * (c0 + p)); };
+    const int step = few ? 1 : JOIN_WARPS, p0 = few ? 0 : warp;
+    for (int r = few ? blockIdx.y * JOIN_WARPS + warp : blockIdx.y; r < R; r += gridDim.y * (few ? JOIN_WARPS : 1)) {
+        float M = -INFINITY, L = 0.f;
+#pragma unroll 4
+        for (int p = p0; p < np; p += step) M = fmaxf(M, reinterpret_cast<const float2 *>(slot(p))[r].x);
+        const float ref = M == -INFINITY ? 0.f : M;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int p = p0; p < np; p += step) {
+            const float *sp = slot(p);
+            const float2 ml = reinterpret_cast<const float2 *>(sp)[r];
+            const float4 v = reinterpret_cast<const float4 *>(sp + 2 * a.slot_rows)[r * (D / 4) + lane];
+            const float f = tc::ex2(ml.x - ref);
+            L += f * ml.y;
+            acc.x += f * v.x;
+            acc.y += f * v.y;
+            acc.z += f * v.z;
+            acc.w += f * v.w;
+        }
+        if (!few) {
+            acc_s[warp][lane] = acc;
+            if (lane == 0) ml_s[warp] = make_float2(M, L);
+            __syncthreads();
+            if (warp == 0) {
+                M = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < JOIN_WARPS; ++w) M = fmaxf(M, ml_s[w].x);
+                const float rf = M == -INFINITY ? 0.f : M;
+                acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                L = 0.f;
+#pragma unroll
+                for (int w = 0; w < JOIN_WARPS; ++w) {
+                    const float f = tc::ex2(ml_s[w].x - rf);
+                    const float4 v = acc_s[w][lane];
+                    L += f * ml_s[w].y;
+                    acc.x += f * v.x;
+                    acc.y += f * v.y;
+                    acc.z += f * v.z;
+                    acc.w += f * v.w;
+                }
+            }
+        }
+        if (few || warp == 0) {
+            const int rr = r0 + r, j = rr / a.G;
+            paged_store_row(a, f32, x.x + j, h * a.G + (rr - j * a.G), lane, acc, M, L, vs);
+        }
+        if (!few) __syncthreads();
+    }
+}
+
+int launch_join(const PagedAttn &a, const JoinSet &s0, const JoinSet &s1, int64_t max_rows, bool f32, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(s0.blocks + s1.blocks, (unsigned)(max_rows < 16 ? max_rows : 16));
+    cfg.blockDim = dim3(JOIN_WARPS * 32);
+    cfg.stream = s;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_join_kernel, a, s0, s1, (int)f32);
+    note_launch("paged_join", s);
+    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+// The most rows (new tokens x heads of a kv head) of a request that the rows
+// kernel takes when the tile kernel could.
+constexpr int ROWS_MAX = 16;
 
 }  // namespace
 }  // namespace kda
@@ -80,14 +195,32 @@ int kda_paged_attn(const void *q, const void *k_cache, const void *v_cache, cons
     a.max_blocks = max_blocks;
     a.window = window;
     a.scale_log2 = sm_scale * 1.4426950408889634f;
-    a.row_lo = 0;
-    a.row_hi = INT32_MAX;
-    a.lead = (int4 *)workspace;
-    a.parts = (float *)((char *)workspace + w.off_slots);
-    a.slot_rows = w.slot_rows;
-    if ((rc = launch_paged_rows(a, cache_dtype, k_cache, v_cache, page_stride, s))) return rc;
-    const int64_t rows = (int64_t)a.max_q * a.G;
-    return launch_paged_join(a, paged_rows_blocks(), dtype == KDA_F32, (int)(rows < PAGED_ROWS_CAP ? rows : PAGED_ROWS_CAP), s);
+    char *ws = (char *)workspace;
+    const int64_t max_rows = (int64_t)a.max_q * a.G;
+    const bool tiles = cache_dtype == KDA_BF16 && a.G <= 128 && max_rows > ROWS_MAX;
+    // every request long enough for the tile kernel: one of T_total tokens, or all
+    // of max_q (the offsets may still say less: the tile kernel then takes that too)
+    const bool rows = !tiles || !(n_seqs == 1 || T_total == (int64_t)n_seqs * a.max_q);
+    JoinSet js[2] = {{nullptr, nullptr, 0, 1}, {nullptr, nullptr, 0, 1}};
+    if (rows) {
+        a.row_lo = 0;
+        a.row_hi = tiles ? ROWS_MAX : INT32_MAX;
+        a.lead = (int4 *)(ws + w.rows.off_lead);
+        a.parts = (float *)(ws + w.rows.off_slots);
+        a.slot_rows = w.rows.slot_rows;
+        js[0] = JoinSet{a.lead, a.parts, w.rows.blocks, a.slot_rows};
+        if ((rc = launch_paged_rows(a, cache_dtype, k_cache, v_cache, page_stride, s))) return rc;
+    }
+    if (tiles) {
+        a.row_lo = rows ? ROWS_MAX : 0;
+        a.row_hi = INT32_MAX;
+        a.lead = (int4 *)(ws + w.tile.off_lead);
+        a.parts = (float *)(ws + w.tile.off_slots);
+        a.slot_rows = w.tile.slot_rows;
+        js[1] = JoinSet{a.lead, a.parts, w.tile.blocks, a.slot_rows};
+        if ((rc = launch_paged_tile(a, k_cache, v_cache, page_stride, rows, s))) return rc;
+    }
+    return launch_join(a, js[0], js[1], max_rows, dtype == KDA_F32, s);
 }
 
 }  // extern "C"

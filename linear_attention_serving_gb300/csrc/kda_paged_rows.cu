@@ -499,7 +499,6 @@ __device__ __forceinline__ void consume(const PagedAttn &a, uint8_t *sm) {
     float o[16][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, sc[2] = {0.f, 0.f};
     int last[2] = {0, 0};  // position of the thread's two rows
     int stage = 0, phase = 0;
-    bool has_lead = false;
     uint64_t *meet = reinterpret_cast<uint64_t *>(sm + OFF_MEET);
     int meet_phase = 0;
     // (a bounded wait, unlike a named barrier: a warp that gave up never comes)
@@ -646,17 +645,13 @@ __device__ __forceinline__ void consume(const PagedAttn &a, uint8_t *sm) {
                     reinterpret_cast<float4 *>(slot + 2 * a.slot_rows)[r * (D / 4) + lane] = acc;
                 }
             }
-            if (!(d.flags & WHOLE) && d.c0 == (int)blockIdx.x) {
-                has_lead = true;  // the item's first piece: this block's join merges it
-                if (threadIdx.x == 0) {
-                    a.lead[2 * blockIdx.x] = make_int4(d.tok0, d.h, d.r0, d.R);
-                    a.lead[2 * blockIdx.x + 1] = make_int4(d.slot, d.c0, d.c1, 1);
-                }
+            if (!(d.flags & WHOLE) && d.c0 == (int)blockIdx.x && threadIdx.x == 0) {  // the item's first piece
+                a.lead[2 * blockIdx.x] = make_int4(d.tok0, d.h, d.r0, d.R);
+                a.lead[2 * blockIdx.x + 1] = make_int4(d.slot, d.c0, d.c1, 1);
             }
             if (!meet_all()) break;
         }
     }
-    if (!has_lead && threadIdx.x == 0) a.lead[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
 }
 
 template <int KIND>
@@ -675,6 +670,7 @@ __global__ void __launch_bounds__(THREADS, 2)
         mbar_init(reinterpret_cast<uint64_t *>(sm + OFF_MEET), CONS);
         mbar_fence_init();
         *reinterpret_cast<int *>(sm + OFF_ABORT) = 0;
+        a.lead[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);  // (no piece of this block leads, so far)
     }
     int64_t *scratch = reinterpret_cast<int64_t *>(sm + OFF_RED);
     auto tiles = [&](int i, int *err) { return line_tiles<KIND>(a, i, err); };
@@ -682,10 +678,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     int64_t per = (total + gridDim.x - 1) / gridDim.x;
     if (per < min_per) per = min_per;
     const int64_t P0 = (int64_t)blockIdx.x * per, P1 = P0 + per < total ? P0 + per : total;
-    if (P0 >= P1) {
-        if (tid == 0) a.lead[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
-        return;
-    }
+    if (P0 >= P1) return;
     int req;
     int64_t before;
     paged_find<THREADS>(a, P0, scratch, req, before, tiles);
@@ -693,65 +686,6 @@ __global__ void __launch_bounds__(THREADS, 2)
         produce<KIND>(a, maps, sm, P0, P1, per, req, before);
     else
         consume<KIND>(a, sm);
-}
-
-// ---------------------------------------------------------------- join
-// Merges the pieces of the items that block borders cut.  Block (c, y) takes
-// the item whose first piece the attention's block c left, rows y, y + gridDim.y
-// ...; its warps take every eighth piece and meet in shared memory.
-constexpr int JOIN_WARPS = 8;
-__global__ void __launch_bounds__(JOIN_WARPS * 32) paged_join_kernel(const PagedAttn a, int f32) {
-    __shared__ float4 acc_s[JOIN_WARPS][32];
-    __shared__ float2 ml_s[JOIN_WARPS];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int4 y = a.lead[2 * blockIdx.x + 1];
-    if (!y.w) return;
-    const int4 x = a.lead[2 * blockIdx.x];
-    const int h = x.y, r0 = x.z, R = x.w, c0 = y.y, np = y.z - y.y + 1;
-    const float vs = a.v_scale ? a.v_scale[h] : 1.f;
-    for (int r = blockIdx.y; r < R; r += gridDim.y) {
-        auto slot = [&](int p) { return paged_slot(a, p == 0 ? y.x : 2 * (c0 + p)); };
-        float M = -INFINITY, L = 0.f;
-        for (int p = warp; p < np; p += JOIN_WARPS) M = fmaxf(M, reinterpret_cast<const float2 *>(slot(p))[r].x);
-        const float ref = M == -INFINITY ? 0.f : M;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int p = warp; p < np; p += JOIN_WARPS) {
-            const float *s = slot(p);
-            const float2 ml = reinterpret_cast<const float2 *>(s)[r];
-            const float4 v = reinterpret_cast<const float4 *>(s + 2 * a.slot_rows)[r * (D / 4) + lane];
-            const float f = tc::ex2(ml.x - ref);
-            L += f * ml.y;
-            acc.x += f * v.x;
-            acc.y += f * v.y;
-            acc.z += f * v.z;
-            acc.w += f * v.w;
-        }
-        acc_s[warp][lane] = acc;
-        if (lane == 0) ml_s[warp] = make_float2(M, L);
-        __syncthreads();
-        if (warp == 0) {
-            float MM = -INFINITY, LL = 0.f;
-#pragma unroll
-            for (int w = 0; w < JOIN_WARPS; ++w) MM = fmaxf(MM, ml_s[w].x);
-            const float rf = MM == -INFINITY ? 0.f : MM;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int w = 0; w < JOIN_WARPS; ++w) {
-                const float f = tc::ex2(ml_s[w].x - rf);
-                const float4 v = acc_s[w][lane];
-                LL += f * ml_s[w].y;
-                o.x += f * v.x;
-                o.y += f * v.y;
-                o.z += f * v.z;
-                o.w += f * v.w;
-            }
-            const int rr = r0 + r, j = rr / a.G;
-            paged_store_row(a, f32, x.x + j, h * a.G + (rr - j * a.G), lane, o, MM, LL, vs);
-        }
-        __syncthreads();
-    }
 }
 
 template <int KIND>
@@ -783,21 +717,6 @@ int launch_paged_rows(const PagedAttn &a, int cache_dtype, const void *k, const 
         case KDA_E4M3: return launch_kind<E4M3>(a, k, v, cache_dtype, page_stride, s);
         default: return launch_kind<F32>(a, k, v, cache_dtype, page_stride, s);
     }
-}
-
-int launch_paged_join(const PagedAttn &a, int n_blocks, bool f32, int max_rows, cudaStream_t s) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(n_blocks, max_rows < 8 ? max_rows : 8);
-    cfg.blockDim = dim3(JOIN_WARPS * 32);
-    cfg.stream = s;
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_join_kernel, a, (int)f32);
-    note_launch("paged_join", s);
-    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 }  // namespace kda

@@ -82,4 +82,19 @@ int make_paged_maps(const void *k, const void *v, int cache_dtype, int Hkv, int 
     return KDA_OK;
 }
 
+// Queries [T, Hq, D]: one tile = 64 channels of G heads of `tokens` tokens, so that
+// its rows are the G heads of one token after another.
+int make_paged_q_map(const void *q, int64_t T, int Hq, int G, int tokens, CUtensorMap *out) {
+    const EncodeTiledFn fn = encode_tiled();
+    if (!fn) return KDA_ERR_CUDA;
+    const cuuint64_t dim[3] = {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)T};
+    const cuuint64_t stride[2] = {(cuuint64_t)D * 2, (cuuint64_t)Hq * D * 2};
+    const cuuint32_t box[3] = {64u, (cuuint32_t)G, (cuuint32_t)tokens};
+    const cuuint32_t estride[3] = {1u, 1u, 1u};
+    const CUresult r = fn(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), dim, stride, box, estride,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? KDA_OK : KDA_ERR_CUDA;
+}
+
 }  // namespace kda

@@ -189,6 +189,35 @@ def test_attn_chunks(new, ctx, cache):
     check(new, ctx, 2, 3, 16, cache)
 
 
+@pytest.mark.parametrize("hkv,g,new,ctx,ps,window", [
+    (1, 1, [129], [0], 16, 0), (1, 1, [128, 257], [1, 127], 128, 0), (2, 4, [32, 33, 64, 65], [300, 0, 127, 128], 64, 0),
+    (1, 8, [513], [1000], 48, 0), (1, 12, [5, 21, 22, 10], [130, 700, 0, 256], 16, 0), (2, 3, [300, 1], [511, 511], 32, 200),
+    (1, 5, [260], [40], 16, 64), (1, 128, [1, 3], [200, 129], 16, 0), (1, 100, [2], [383], 96, 130), (4, 2, [400, 7, 90], [0, 900, 33], 256, 0)])
+def test_attn_row_tiles(hkv, g, new, ctx, ps, window):
+    """bf16 chunks around the sizes where rows and key tiles of 128 begin and end."""
+    check(new, ctx, hkv, g, ps, BF16, window=window)
+
+
+@pytest.mark.parametrize("new,ctx", [([40, 3, 64], [20000, 9000, 0]), ([2] * 9 + [150], [3000] * 9 + [10])])
+def test_attn_row_tiles_split(new, ctx):
+    """Few row tiles over long contexts: every item is cut by block borders."""
+    d = make(new, ctx, 1, 8, 64, BF16, seed=5)
+    o, lse, e = run_attn(d, max_q=max(new))
+    assert e == 0
+    attn_close(o, lse, attn_ref(d["q"], d["k_cache"], d["v_cache"], d["table"], d["cu"], d["kv"]), BF16, BF16)
+
+
+def test_attn_row_tiles_rising_scores():
+    """Scores that grow with the key: the running maximum moves at every tile."""
+    d = make([3], [1500], 1, 16, 32, BF16, q_std=1.0)
+    k = d["k_cache"].float()
+    for j in range(1503):
+        k[d["table"][0][j // 32], 0, j % 32] = 0.02 * j * d["q"][0, 0].float() / 11.3 + 0.1 * k[d["table"][0][j // 32], 0, j % 32]
+    d["k_cache"] = k.bfloat16()
+    o, lse, e = run_attn(d)
+    attn_close(o, lse, attn_ref(d["q"], d["k_cache"], d["v_cache"], d["table"], d["cu"], d["kv"]), BF16, BF16)
+
+
 @pytest.mark.parametrize("cache", CACHES, ids=NAMES)
 @pytest.mark.parametrize("window", [1, 2, 16, 33, 100, 1000])
 def test_attn_window(window, cache):
