@@ -79,14 +79,25 @@ __device__ __forceinline__ int64_t paged_warp_scan(int64_t x, int lane) {
     return x;
 }
 
-// Where block c's tiles begin.  All NTHR threads of the block call it;
-// `tiles(i)` counts request i's tiles.  Returns the total.
+// Where this block's part of the line begins.
+struct PagedLine {
+    int64_t P0, P1, per;  // the block's units, units per block
+    int64_t before;       // units before the request that holds P0
+    int64_t units;        // and that request's
+    int req;
+};
+
+// All NTHR threads of the block call it; `units(i, err)` counts request i's.  `per`
+// is at least min_per and a multiple of `even`.  scratch: NTHR / 32 + 3 words.
 template <int NTHR, class F>
-__device__ __forceinline__ int64_t paged_total(const PagedAttn &a, int64_t *scratch, F tiles) {
+__device__ __forceinline__ PagedLine paged_line(const PagedAttn &a, int64_t *scratch, int64_t min_per, int even, F units) {
+    constexpr int W = NTHR / 32;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    int64_t sum = 0;
+    int64_t *found = scratch + W;
+    // this thread's requests: the first round's count stays in a register
     int err = 0;
-    for (int i = tid; i < a.n_seqs; i += NTHR) sum += tiles(i, &err);
+    int64_t first = tid < a.n_seqs ? units(tid, &err) : 0, sum = first;
+    for (int i = tid + NTHR; i < a.n_seqs; i += NTHR) sum += units(i, &err);
     if (err && blockIdx.x == 0 && a.err) atomicOr(a.err, err);
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -94,42 +105,47 @@ __device__ __forceinline__ int64_t paged_total(const PagedAttn &a, int64_t *scra
     __syncthreads();
     sum = 0;
 #pragma unroll
-    for (int w = 0; w < NTHR / 32; ++w) sum += scratch[w];
+    for (int w = 0; w < W; ++w) sum += scratch[w];
     __syncthreads();
-    return sum;
-}
-
-// The request that holds tile P (< total) and the number of tiles before it.
-template <int NTHR, class F>
-__device__ __forceinline__ void paged_find(const PagedAttn &a, int64_t P, int64_t *scratch, int &req, int64_t &before,
-                                           F tiles) {
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    int64_t *found = scratch + NTHR / 32;
-    if (tid == 0) found[0] = -1;
+    PagedLine r;
+    // (units fit 32 bits in all but the longest lines: a short division)
+    r.per = sum < INT32_MAX ? (int64_t)(((uint32_t)sum + gridDim.x - 1) / gridDim.x) : (sum + gridDim.x - 1) / gridDim.x;
+    if (r.per < min_per) r.per = min_per;
+    r.per = (r.per + even - 1) / even * even;
+    r.P0 = (int64_t)blockIdx.x * r.per;
+    r.P1 = r.P0 + r.per < sum ? r.P0 + r.per : sum;
+    r.req = 0;
+    r.before = r.units = 0;
+    if (r.P0 >= r.P1) return r;
     int64_t carry = 0;
-    for (int base = 0; base < a.n_seqs; base += NTHR) {
+    for (int base = 0;; base += NTHR) {
         const int i = base + tid;
-        const int64_t t = i < a.n_seqs ? tiles(i, nullptr) : 0;
+        const int64_t t = base == 0 ? first : i < a.n_seqs ? units(i, nullptr) : 0;
         const int64_t inc = paged_warp_scan(t, lane);
         if (lane == 31) scratch[warp] = inc;
+        if (tid == 0) found[0] = -1;
         __syncthreads();
         int64_t off = carry, all = 0;
 #pragma unroll
-        for (int w = 0; w < NTHR / 32; ++w) {
+        for (int w = 0; w < W; ++w) {
             if (w < warp) off += scratch[w];
             all += scratch[w];
         }
-        if (P >= off + inc - t && P < off + inc) {
+        if (r.P0 >= off + inc - t && r.P0 < off + inc) {
             found[0] = i;
             found[1] = off + inc - t;
+            found[2] = t;
         }
         carry += all;
         __syncthreads();
-        if (found[0] >= 0) break;
+        if (found[0] >= 0 || base + NTHR >= a.n_seqs) break;
+        __syncthreads();
     }
-    req = (int)found[0];
-    before = found[1];
+    r.req = (int)found[0];
+    r.before = found[1];
+    r.units = found[2];
     __syncthreads();
+    return r;
 }
 
 // ---------------------------------------------------------------- pieces

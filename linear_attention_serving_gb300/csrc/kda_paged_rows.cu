@@ -41,6 +41,7 @@ constexpr int OFF_BAR = OFF_DESC + STAGES * 64;
 constexpr int OFF_MEET = OFF_BAR + 2 * STAGES * 8;  // the consumer warps' meeting at an item's end
 constexpr int OFF_ABORT = OFF_MEET + 8;
 constexpr int SMEM = OFF_ABORT + 16;
+static_assert(OFF_RED % 1024 == 0 && OFF_ML % 16 == 0 && OFF_DESC % 16 == 0 && OFF_BAR % 8 == 0, "shared memory layout");
 
 constexpr int BF16 = 0, E4M3 = 1, F32 = 2;   // kinds
 template <int KIND> struct Kind;
@@ -674,16 +675,10 @@ __global__ void __launch_bounds__(THREADS, 2)
     }
     int64_t *scratch = reinterpret_cast<int64_t *>(sm + OFF_RED);
     auto tiles = [&](int i, int *err) { return line_tiles<KIND>(a, i, err); };
-    const int64_t total = paged_total<THREADS>(a, scratch, tiles);
-    int64_t per = (total + gridDim.x - 1) / gridDim.x;
-    if (per < min_per) per = min_per;
-    const int64_t P0 = (int64_t)blockIdx.x * per, P1 = P0 + per < total ? P0 + per : total;
-    if (P0 >= P1) return;
-    int req;
-    int64_t before;
-    paged_find<THREADS>(a, P0, scratch, req, before, tiles);
+    const PagedLine line = paged_line<THREADS>(a, scratch, min_per, 1, tiles);
+    if (line.P0 >= line.P1) return;
     if (tid >= CONS * 32)
-        produce<KIND>(a, maps, sm, P0, P1, per, req, before);
+        produce<KIND>(a, maps, sm, line.P0, line.P1, line.per, line.req, line.before);
     else
         consume<KIND>(a, sm);
 }

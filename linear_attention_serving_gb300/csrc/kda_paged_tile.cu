@@ -11,10 +11,10 @@
 //         group reads a row of S into registers, so nothing of S is needed)
 //   O_w += P_w V    128 x 128 fp32 in TMEM, P_w read from TMEM
 // The two groups w take turns: while one works out probabilities, the tensor
-// cores run the other's products.  With over 128 rows the groups are the two
-// halves of the rows and share each key tile; with fewer they take every other
-// key tile of the same rows and are merged at the end (each group then has its
-// own maximum, sum and O).
+// cores run the other's products.  They are the two halves of the rows and share
+// each key tile.  An item of one half has the first group alone, whose S takes
+// both buffers in turn, so that the next S is formed while this one's
+// probabilities are worked out.
 //
 // The reference `ref` of a row's exponents follows its maximum only when that
 // has grown by more than 2^8: until then probabilities up to 256 are as precise
@@ -33,15 +33,16 @@ constexpr int SLOT = BK * D * 2;               // 32 KB: two 64-channel blocks o
 constexpr int QHALF = BM * D * 2;
 constexpr int OFF_Q = 0;
 constexpr int OFF_KV = 2 * QHALF;
-constexpr int OFF_ML = OFF_KV + SLOTS * SLOT;  // [2][128] float2
-constexpr int OFF_BAR = OFF_ML + 2 * BM * 8;
-constexpr int NBAR = 2 * SLOTS + 14 + 2 * 4;
+constexpr int OFF_SCAN = OFF_KV + SLOTS * SLOT;  // the start's sums
+constexpr int OFF_BAR = OFF_SCAN + 256;
+constexpr int NBAR = 2 * SLOTS + 19 + 2 * 4;
 constexpr int SEGS = 4;                        // ring of segments ahead of the roles
-constexpr int OFF_MISC = OFF_BAR + NBAR * 8;   // TMEM address, abort flag, start of the block's line
+constexpr int OFF_MISC = (OFF_BAR + NBAR * 8 + 63) / 64 * 64;  // TMEM address, abort flag, start of the block's line
 constexpr int OFF_SEG = OFF_MISC + 64;
 constexpr int SMEM = OFF_SEG + SEGS * 64;
+static_assert(OFF_SCAN % 16 == 0 && OFF_BAR % 8 == 0 && OFF_SEG % 64 == 0 && SMEM <= 232448, "shared memory layout");
 constexpr int SOFT = 8;                        // softmax warps
-constexpr int THREADS = (SOFT + 4) * 32;       // (registers are given out by four warps: the last one has nothing to do)
+constexpr int THREADS = (SOFT + 4) * 32;       // (registers are given out by four warps)
 // registers a thread: 168 at launch (384 x 168 = 64,512), then 208 for the softmax
 // warps, which hold a row of S, and 88 for the others: 256 x 208 + 128 x 88 = 64,512
 constexpr int REGS_SOFT = 208, REGS_AUX = 88;
@@ -51,19 +52,23 @@ constexpr uint32_t COL_S = 0, COL_O = 256;     // + 128 w
 constexpr float GROW = 8.f;                    // log2 growth of a maximum that ref follows
 
 struct Bars {
-    uint64_t *kv_full, *kv_empty, *q_full, *q_empty, *s_full, *p_ready, *pv_done, *o_free, *meet, *seg_full, *seg_empty;
+    uint64_t *kv_full, *kv_empty, *q_full, *q_empty, *s_full, *p_ready, *p_rest, *pv_done, *o_free, *last, *seg_full, *seg_empty;
     __device__ explicit Bars(uint8_t *sm) {
         uint64_t *b = reinterpret_cast<uint64_t *>(sm + OFF_BAR);
         kv_full = b;
         kv_empty = b + SLOTS;
         q_full = b + 2 * SLOTS;      // [2]
         q_empty = q_full + 2;        // [2]
-        s_full = q_empty + 2;        // [2]
-        p_ready = s_full + 2;        // [2]
-        pv_done = p_ready + 2;       // [2]
-        o_free = pv_done + 2;        // [2]
-        meet = o_free + 2;           // [1], then one for products in flight when a wait ran out
-        seg_full = meet + 2;
+        // by S buffer and the group that works on it: 0 and 1 the groups' own, 2 the
+        // second buffer when the first group has both (each barrier has one group to
+        // wait on it, which sees every phase)
+        s_full = q_empty + 2;        // [3]
+        p_ready = s_full + 3;        // [3]
+        p_rest = p_ready + 3;        // [3] keys 64 .. 127 of P
+        pv_done = p_rest + 3;        // [3]
+        o_free = pv_done + 3;        // [2]
+        last = o_free + 2;           // [1] products in flight when a wait ran out
+        seg_full = last + 1;
         seg_empty = seg_full + SEGS;
     }
 };
@@ -73,20 +78,21 @@ struct Bars {
 // line by rows instead of columns gives
 //   K (n - 1) - sum_{j < K} floor((m j + m - b - 1) / a),
 // the same kind of sum on smaller numbers (Euclid's steps on a and m).
-__device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+// a (n - 1) + b < 2^32: key positions are below 2^31.
+__device__ __forceinline__ int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
     int64_t s = 0, sign = 1;
     while (n > 0) {
-        const int64_t qa = a / m, qb = b / m;
-        s += sign * (qa * (n * (n - 1) / 2) + qb * n);
+        const uint32_t qa = a / m, qb = b / m;
+        s += sign * ((int64_t)qa * ((int64_t)n * (n - 1) / 2) + (int64_t)qb * n);
         a -= qa * m;
         b -= qb * m;
-        const int64_t K = (a * (n - 1) + b) / m;
+        const uint32_t K = (a * (n - 1) + b) / m;
         if (K == 0) break;
-        s += sign * K * (n - 1);
+        s += sign * ((int64_t)K * (n - 1));
         sign = -sign;
         b = m - b - 1;
         n = K;
-        const int64_t t = m;
+        const uint32_t t = m;
         m = a;
         a = t;
     }
@@ -116,30 +122,34 @@ __device__ __forceinline__ void key_tiles(const PagedAttn &a, const PagedReq &r,
     t0 = lo / BK;
     t1 = (hi + BK - 1) / BK;
 }
-// Length of an item in the line: two units a tile (one product pair per half), one
-// where the groups split the tiles, always even so that every cut falls on a tile
-// of either kind; an item without keys takes the place of one tile.
+// Length of an item in the line: HEAD units for what an item costs besides its
+// tiles (Q, the first S, O on its way out: about two tiles' time), then two units a
+// tile, one where it is for one half, always
+// even so that every cut falls on a tile of either kind; an item without keys takes
+// the place of one tile.  A cut inside the fixed part leaves the item to the next
+// block.
+constexpr int HEAD = 4;
 __device__ __forceinline__ int item_units(const PagedAttn &a, const TileReq &q, int g, int th) {
     const int j0 = g * 2 * th, j1 = min(q.n, j0 + 2 * th) - 1;
     int lo, hi, t0, t1;
     key_tiles(a, q.r, j0, j1, lo, hi, t0, t1);
     const int nt = max(1, t1 - t0);
-    return j1 - j0 + 1 > th ? 2 * nt : (nt + 1) & ~1;
+    return HEAD + (j1 - j0 + 1 > th ? 2 * nt : (nt + 1) & ~1);
 }
 // Units of the row tiles before g (closed form: a long request has thousands).
 __device__ __forceinline__ int64_t units_before(const PagedAttn &a, const TileReq &q, int g, int th) {
     const int TT = 2 * th, full = min(g, q.n / TT);
-    const int64_t pos0 = q.r.pos0;
-    int64_t neg = pos0 < 0 ? -pos0 / TT : 0;  // tiles whose last query stands before position 0
+    const int pos0 = q.r.pos0;
+    int neg = pos0 < 0 ? -pos0 / TT : 0;  // tiles whose last query stands before position 0
     if (neg > full) neg = full;
     int64_t tiles = neg + floor_sum(full - neg, BK, TT, pos0 + (neg + 1) * TT + BK - 1);
     if (a.window > 0) {
-        const int64_t d = a.window - 1 - pos0;  // lo > 0 from g TT > d on
-        int64_t gw = d < 0 ? 0 : d / TT + 1;
+        const int d = a.window - 1 - pos0;  // lo > 0 from g TT > d on
+        int gw = d < 0 ? 0 : d / TT + 1;
         if (gw < neg) gw = neg;
         if (gw < full) tiles -= floor_sum(full - gw, BK, TT, gw * TT - d);
     }
-    int64_t u = 2 * tiles;
+    int64_t u = 2 * tiles + (int64_t)HEAD * full;
     if (g > full) u += item_units(a, q, full, th);  // the last, shorter row tile
     return u;
 }
@@ -153,17 +163,18 @@ struct __align__(16) Seg {
     int tok, ntok;           // first token, tokens
     int h, pos;              // kv head, first token's position
     int lo, hi, t0, nt;      // keys seen, first key tile of the segment, its tiles (0: nothing to read)
-    int req, alt, whole, slot, c0, c1, pad;
+    int req, alt, whole, slot, c0, c1, half;  // half of Q's buffer (alt)
 };
 static_assert(sizeof(Seg) == 64, "segment size");
 
 // The line's items from the block's start on.
 struct Walk {
     int64_t pos, end, per, before, A;
-    int req, h, g;
+    int req, h, g, alts;
     TileReq q;
     bool fresh;
     __device__ bool next(const PagedAttn &a, int th, int64_t P0, Seg &s) {
+      while (true) {
         if (pos >= end) return false;
         if (fresh) {
             while (true) {
@@ -180,7 +191,8 @@ struct Walk {
         key_tiles(a, q.r, j0, j1, s.lo, s.hi, t0, t1);
         s.alt = j1 - j0 + 1 <= th;
         const int sh = s.alt ? 0 : 1;
-        const int b = (int)(pos - A) >> sh, e = min((int)(stop - A) >> sh, t1 - t0);
+        const int b = max(0, (int)(pos - A) - HEAD) >> sh, e = min(max(0, (int)(stop - A) - HEAD) >> sh, t1 - t0);
+        const bool some = stop - A > HEAD;
         s.t0 = t0 + b;
         s.nt = max(0, e - b);
         s.tok = q.r.tok0 + j0;
@@ -188,9 +200,9 @@ struct Walk {
         s.h = h;
         s.pos = q.r.pos0 + j0;
         s.req = req;
-        s.whole = pos == A && stop == B;
+        s.whole = b == 0 && stop == B;
         s.slot = 2 * (int)blockIdx.x + (pos == P0 ? 0 : 1);
-        s.c0 = (int)(A / per);
+        s.c0 = (int)((A + HEAD) / per);
         s.c1 = (int)((B - 1) / per);
         pos = stop;
         if (stop == B) {
@@ -204,12 +216,16 @@ struct Walk {
                 }
             }
         }
+        if (!some) continue;
+        s.half = 0;
+        if (s.alt && s.nt > 0) s.half = alts++ & 1;
         return true;
+      }
     }
 };
 
 // Place of K_j and V_j in the order of loading, counted from the item's first:
-// shared tiles K0 V0 K1 V1 ..; alternating K0 K1 V0 K2 V1 .. (two K tiles are
+// two halves K0 V0 K1 V1 ..; one half K0 K1 V0 K2 V1 .. (two K tiles are
 // multiplied before the first V).
 __device__ __forceinline__ int seq_k(bool alt, int j) { return alt ? (j == 0 ? 0 : 2 * j - 1) : 2 * j; }
 __device__ __forceinline__ int seq_v(bool alt, int j, int nt) { return alt ? (j == nt - 1 ? 2 * nt - 1 : 2 * j + 2) : 2 * j + 1; }
@@ -233,12 +249,46 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *o) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(r[i]);
 }
+// The loads above have arrived: nothing that uses the values moves before this.
+__device__ __forceinline__ void tmem_arrived(float *o) {
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(o[i]));
+}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *o) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
         "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7]), "r"(o[8]), "r"(o[9]), "r"(o[10]),
         "r"(o[11]), "r"(o[12]), "r"(o[13]), "r"(o[14]), "r"(o[15])
         : "memory");
+}
+// two fp32 operations at once, and the largest of three
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t r, float &x, float &y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(r)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+__device__ __forceinline__ float max3(float x, float y, float z) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
+}
+// 32 bytes of one thread at once (dst 32-byte aligned)
+__device__ __forceinline__ void store32(void *dst, const uint32_t (&u)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]),
+                 "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+                 : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -291,24 +341,52 @@ __device__ __forceinline__ bool next_seg(uint8_t *sm, const Bars &bar, int &i, c
 }
 
 // ---------------------------------------------------------------- loads
-__device__ __forceinline__ void load_role(const PagedAttn &a, const PagedMaps &maps, const CUtensorMap &qmap, uint8_t *sm,
-                                          int th, const Gate &gate) {
+// Queries.  Items of one half take the two halves of the buffer in turn, so the
+// next one's queries arrive while this one is worked on.
+__device__ __forceinline__ void query_role(const PagedAttn &a, const CUtensorMap &qmap, uint8_t *sm, int th, const Gate &gate) {
+    const int lane = threadIdx.x & 31;
+    const Bars bar(sm);
+    int n0 = 0, n1 = 0;  // loads of each half
+    Seg s;
+    int iseg = 0;
+    while (next_seg(sm, bar, iseg, gate, s)) {
+        if (s.nt == 0) continue;
+        for (int x = 0; x < 2; ++x) {
+            if (s.alt && x != s.half) continue;
+            if (!gate(&bar.q_empty[x], ((x ? n1 : n0) & 1) ^ 1)) {  // let the copies in flight land
+                if (n0) mbar_wait(&bar.q_full[0], (n0 - 1) & 1);
+                if (n1) mbar_wait(&bar.q_full[1], (n1 - 1) & 1);
+                __syncwarp();
+                return;
+            }
+            if (lane == 0) {
+                mbar_expect_tx(&bar.q_full[x], (uint32_t)(2 * th * a.G * 128));
+                uint8_t *dst = sm + OFF_Q + x * QHALF;
+                const int tok = s.tok + (s.alt ? 0 : x * th);
+                tma_load_3d(dst, &qmap, 0, s.h * a.G, tok, &bar.q_full[x]);
+                tma_load_3d(dst + QHALF / 2, &qmap, 64, s.h * a.G, tok, &bar.q_full[x]);
+            }
+            __syncwarp();
+            if (x) ++n1;
+            else ++n0;
+        }
+    }
+}
+
+// Keys and values.
+__device__ __forceinline__ void load_role(const PagedAttn &a, const PagedMaps &maps, uint8_t *sm, const Gate &gate) {
     const int lane = threadIdx.x & 31;
     const Bars bar(sm);
     const int box = a.box, nbx = BK / box;
     int64_t seq = 0;   // K / V tiles so far
-    int qn[2] = {0, 0};
     auto drain = [&]() {  // a wait ran out: let the copies in flight land before the block ends
         for (int64_t u = seq - 1; u >= 0 && u >= seq - SLOTS; --u) mbar_wait(&bar.kv_full[u % SLOTS], (u / SLOTS) & 1);
-        for (int x = 0; x < 2; ++x)
-            if (qn[x]) mbar_wait(&bar.q_full[x], (qn[x] - 1) & 1);
         __syncwarp();
     };
     Seg s;
     int iseg = 0;
     while (next_seg(sm, bar, iseg, gate, s)) {
         if (s.nt == 0) continue;
-        const int nh = s.ntok > th ? 2 : 1;
         int cbase = -64, page = 0;
         const int lob = s.lo & ~(box - 1);  // boxes before this one hold no seen key (their pages may be gone)
         // one K or V tile
@@ -343,17 +421,6 @@ __device__ __forceinline__ void load_role(const PagedAttn &a, const PagedMaps &m
             ++seq;
             return true;
         };
-        for (int x = 0; x < nh; ++x) {
-            if (!gate(&bar.q_empty[x], (qn[x] & 1) ^ 1)) return drain();
-            if (lane == 0) {
-                mbar_expect_tx(&bar.q_full[x], (uint32_t)(2 * th * a.G * 128));
-                uint8_t *dst = sm + OFF_Q + x * QHALF;
-                tma_load_3d(dst, &qmap, 0, s.h * a.G, s.tok + x * th, &bar.q_full[x]);
-                tma_load_3d(dst + QHALF / 2, &qmap, 64, s.h * a.G, s.tok + x * th, &bar.q_full[x]);
-            }
-            __syncwarp();
-            ++qn[x];
-        }
         for (int j = 0; j < s.nt; ++j) {
             if (!s.alt) {
                 if (!tile(j, false) || !tile(j, true)) return drain();
@@ -372,20 +439,20 @@ __device__ __forceinline__ void mma_role(const PagedAttn &a, uint8_t *sm, uint32
     constexpr uint32_t ID_QK = idesc_bf16_f32(BM, BK), ID_PV = idesc_bf16_f32_bmn(BM, D);
     const uint32_t base = smem_u32(sm);
     int64_t seq0 = 0;
-    int qn[2] = {0, 0}, np[2] = {0, 0}, ni[2] = {0, 0};  // halves of Q, products P V, items, by group
+    int q0 = 0, q1 = 0, p0 = 0, p1 = 0, p2 = 0, i0 = 0, i1 = 0;  // halves of Q; products P V by barrier, items by group
     Seg s;
     int iseg = 0;
     while (next_seg(sm, bar, iseg, gate, s)) {
         if (s.nt == 0) continue;
         const bool alt = s.alt;
-        const int ne = alt ? s.nt : 2 * s.nt;  // events: one S and one P V of one group
+        const int ne = alt ? s.nt : 2 * s.nt;  // events: one S and one P V, S buffers in turn
         auto kv_ready = [&](int64_t q) { return gate(&bar.kv_full[q % SLOTS], (int)((q / SLOTS) & 1)); };
         auto qk = [&](int e) -> bool {
             const int x = e & 1, j = alt ? e : e >> 1;
             const int64_t q = seq0 + seq_k(alt, j);
-            const int half = alt ? 0 : x;
+            const int half = alt ? s.half : x;
             if (e == 0 || (!alt && e == 1))
-                if (!gate(&bar.q_full[half], qn[half] & 1)) return false;
+                if (!gate(&bar.q_full[half], (half ? q1 : q0) & 1)) return false;
             if ((alt || x == 0) && !kv_ready(q)) return false;
             tc_fence_after();
             const uint32_t qa = base + OFF_Q + half * QHALF, ka = base + OFF_KV + (uint32_t)(q % SLOTS) * SLOT;
@@ -394,11 +461,12 @@ __device__ __forceinline__ void mma_role(const PagedAttn &a, uint8_t *sm, uint32
                 const uint32_t off = (uint32_t)(k >> 2) * (SLOT / 2) + (uint32_t)(k & 3) * 32;
                 mma_bf16_w(tmem + COL_S + x * 128, sdesc_sw128(qa + off), sdesc_sw128(ka + off), ID_QK, k > 0);
             }
-            mma_commit_w(&bar.s_full[x]);
+            mma_commit_w(&bar.s_full[alt && x ? 2 : x]);
             if (alt || x == 1) mma_commit_w(&bar.kv_empty[q % SLOTS]);
             if (alt ? e == ne - 1 : e >= ne - 2) {
                 mma_commit_w(&bar.q_empty[half]);
-                ++qn[half];
+                if (half) ++q1;
+                else ++q0;
             }
             return true;
         };
@@ -406,26 +474,37 @@ __device__ __forceinline__ void mma_role(const PagedAttn &a, uint8_t *sm, uint32
             const int x = e & 1, j = alt ? e : e >> 1;
             const int64_t q = seq0 + seq_v(alt, j, s.nt);
             if ((alt || x == 0) && !kv_ready(q)) return false;
-            if (!gate(&bar.p_ready[x], np[x] & 1)) return false;
-            if (e < 2) {  // the group's last item must have left O
-                if (!gate(&bar.o_free[x], (ni[x] & 1) ^ 1)) return false;
-                ++ni[x];
+            const int b = alt && x ? 2 : x, np = b == 0 ? p0 : b == 1 ? p1 : p2;
+            if (!gate(&bar.p_ready[b], np & 1)) return false;
+            const int g = alt ? 0 : x;  // group, whose O it is
+            const bool head = alt ? e == 0 : e < 2;
+            if (head) {  // the group's last item must have left O
+                if (!gate(&bar.o_free[g], ((g ? i1 : i0) & 1) ^ 1)) return false;
+                if (g) ++i1;
+                else ++i0;
             }
             tc_fence_after();
             const uint32_t va = base + OFF_KV + (uint32_t)(q % SLOTS) * SLOT;
 #pragma unroll
-            for (int k = 0; k < BK / 16; ++k)
-                mma_ta_w(tmem + COL_O + x * 128, tmem + COL_S + x * 128 + k * 8, sdesc_mn(va + k * 2048, SLOT / 2, 1024, SWZ_128B),
-                         ID_PV, e >= 2 || k > 0);
-            mma_commit_w(&bar.pv_done[x]);
-            ++np[x];
+            for (int k = 0; k < BK / 16; ++k) {
+                if (k == BK / 32) {  // the first keys' product runs while the others' probabilities are worked out
+                    if (!gate(&bar.p_rest[b], np & 1)) return false;
+                    tc_fence_after();
+                }
+                mma_ta_w(tmem + COL_O + g * 128, tmem + COL_S + x * 128 + k * 8, sdesc_mn(va + k * 2048, SLOT / 2, 1024, SWZ_128B),
+                         ID_PV, !head || k > 0);
+            }
+            mma_commit_w(&bar.pv_done[b]);
+            if (b == 0) ++p0;
+            else if (b == 1) ++p1;
+            else ++p2;
             if (alt || x == 1) mma_commit_w(&bar.kv_empty[q % SLOTS]);
             return true;
         };
         bool ok = qk(0) && (ne < 2 || qk(1));
         for (int e = 0; ok && e < ne; ++e) ok = pv(e) && (e + 2 >= ne || qk(e + 2));
         if (!ok) {  // let the products in flight end before TMEM is given back
-            uint64_t *last = bar.meet + 1;
+            uint64_t *last = bar.last;
             mma_commit_w(last);
             mbar_wait(last, 0);
             __syncwarp();
@@ -436,52 +515,134 @@ __device__ __forceinline__ void mma_role(const PagedAttn &a, uint8_t *sm, uint32
 }
 
 // ---------------------------------------------------------------- softmax
+// 32 channels of one row, 32 bytes at a time: a row is one thread's, so narrower
+// stores would each touch 32 lines for less
+__device__ __forceinline__ void store_bf16(const PagedAttn &a, int64_t row, int c, const float (&o)[32]) {
+    char *dst = (char *)a.o + (row * D + c) * 2;
+    if ((uintptr_t)a.o & 31u) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t u[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(o[8 * i + 2 * k], o[8 * i + 2 * k + 1]);
+                u[k] = *reinterpret_cast<const uint32_t *>(&b);
+            }
+            reinterpret_cast<uint4 *>(dst)[i] = make_uint4(u[0], u[1], u[2], u[3]);
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        uint32_t u[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(o[16 * i + 2 * k], o[16 * i + 2 * k + 1]);
+            u[k] = *reinterpret_cast<const uint32_t *>(&b);
+        }
+        store32(dst + 32 * i, u);
+    }
+}
+__device__ __forceinline__ void store_f32(float *dst, const float (&o)[32]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t u[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) u[k] = __float_as_uint(o[8 * i + k]);
+        store32(dst + 8 * i, u);
+    }
+}
+
+// The segment's end of one group: O, normalised or as a piece.
+__device__ __forceinline__ void finish(const PagedAttn &a, uint32_t to, int th, const volatile Seg *s, int x, float ref, float l) {
+    const int row = threadIdx.x & 127, G = a.G;
+    const int half = s->alt ? 0 : x, nt = s->nt;
+    const int jt = row / G, local = half * th * G + row;  // token within the half, row of the item
+    const bool live = row < min(th, s->ntok - half * th) * G, whole = s->whole;
+    const int64_t out = (int64_t)(s->tok + half * th + jt) * a.Hq + s->h * G + (row - jt * G);
+    float *slot = paged_slot(a, s->slot);
+    const bool dead = nt == 0 || l == 0.f;  // (NaN passes through)
+    const float f = whole ? 1.f / l : 1.f;
+#pragma unroll 1
+    for (int c = 0; c < D; c += 32) {
+        float o[32];
+        tmem_ld32(to + c, o);
+        tmem_arrived(o);
+        if (live) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = dead ? 0.f : o[i] * f;
+            if (whole)
+                store_bf16(a, out, c, o);
+            else
+                store_f32(slot + 2 * a.slot_rows + (size_t)local * D + c, o);
+        }
+    }
+    if (live) {
+        if (!whole)
+            reinterpret_cast<float2 *>(slot)[local] = make_float2(dead ? -INFINITY : ref, dead ? 0.f : l);
+        else if (a.lse)
+            a.lse[out] = dead ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
+    }
+    if (threadIdx.x == 0 && !whole && s->c0 == (int)blockIdx.x) {
+        a.lead[2 * blockIdx.x] = make_int4(s->tok, s->h, 0, s->ntok * G);
+        a.lead[2 * blockIdx.x + 1] = make_int4(s->slot, s->c0, s->c1, 1);
+    }
+}
+
 __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, uint32_t tmem, int th, const Gate &gate) {
     const Bars bar(sm);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, x = warp >> 2;  // group
     const int row = threadIdx.x & 127;                                         // row of the half = TMEM lane
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;                         // 32 (warp % 4) << 16
-    const uint32_t ts = tmem + lanes + COL_S + x * 128, to = tmem + lanes + COL_O + x * 128;
-    float2 *ml = reinterpret_cast<float2 *>(sm + OFF_ML);
+    const uint32_t to = tmem + lanes + COL_O + x * 128;
     const float sc = a.scale_log2;
     const int box = a.box;
-    int nev = 0, meets = 0;  // events of this group so far
+    int n0 = 0, n2 = 0;  // this group's events by barrier: its own, and the first group's on the second buffer
     int64_t seq0 = 0;
-    Seg s;
-    int iseg = 0;
-    while (next_seg(sm, bar, iseg, gate, s)) {
-        const bool alt = s.alt;
-        const int half = alt ? 0 : x;
-        const int hrows = min(th, s.ntok - half * th) * a.G;  // rows of this half
-        const int jt = row / a.G, pos = s.pos + half * th + jt;
+    for (int iseg = 0;; ++iseg) {
+        if (!gate(&bar.seg_full[iseg % SEGS], (iseg / SEGS) & 1)) return;
+        const Seg *seg = reinterpret_cast<const Seg *>(sm + OFF_SEG + (iseg % SEGS) * 64);
+        struct {
+            int lo, hi, t0, nt;
+        } s{seg->lo, seg->hi, seg->t0, seg->nt};
+        if (s.nt < 0) return;
+        const bool alt = seg->alt;
+        const int pos = seg->pos + (alt ? 0 : x) * th + row / a.G;
         const int first_key = a.window > 0 ? pos - a.window + 1 : 0;  // keys first_key .. pos, all below hi
         float ref = 0.f, l = 0.f, top = -INFINITY;
-        int mine = 0;  // events of this item
-        for (int j = alt ? x : 0; j < s.nt; j += alt ? 2 : 1) {
+        const int ne = alt ? (x ? 0 : s.nt) : 2 * s.nt;
+        uint64_t *prev = nullptr;  // the group's last product
+        int prevp = 0;
+        for (int e = alt ? 0 : x; e < ne; e += alt ? 1 : 2) {
+            const int j = alt ? e : e >> 1, b = alt && (e & 1) ? 2 : x, ph = ((b == 2 ? n2 : n0) + (e >> 1)) & 1;
+            const uint32_t ts = tmem + lanes + COL_S + (e & 1) * 128;
             const int key0 = (s.t0 + j) * BK;
-            if (!gate(&bar.s_full[x], nev & 1)) return;
+            if (!gate(&bar.s_full[b], ph)) return;
             tc_fence_after();
             float v[BK];
 #pragma unroll
             for (int c = 0; c < BK; c += 32) tmem_ld32(ts + c, v + c);
-            tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < BK; c += 32) tmem_arrived(v + c);
             // keys of the tile that this row sees: [c0, c1)
             const int c1 = min(pos + 1, s.hi) - key0, c0 = first_key - key0;
             if (__any_sync(0xffffffffu, c1 < BK || c0 > 0)) {
 #pragma unroll
                 for (int c = 0; c < BK; ++c) v[c] = c < c1 && c >= c0 ? v[c] : -INFINITY;
             }
-            float m0 = v[0], m1 = v[1], m2 = v[2], m3 = v[3];
+            float m0 = max3(v[0], v[1], v[2]), m1 = max3(v[3], v[4], v[5]), m2 = max3(v[6], v[7], v[8]), m3 = max3(v[9], v[10], v[11]);
 #pragma unroll
-            for (int c = 4; c < BK; c += 4) {
-                m0 = fmaxf(m0, v[c]);
-                m1 = fmaxf(m1, v[c + 1]);
-                m2 = fmaxf(m2, v[c + 2]);
-                m3 = fmaxf(m3, v[c + 3]);
+            for (int c = 12; c + 8 <= BK; c += 8) {
+                m0 = max3(m0, v[c], v[c + 1]);
+                m1 = max3(m1, v[c + 2], v[c + 3]);
+                m2 = max3(m2, v[c + 4], v[c + 5]);
+                m3 = max3(m3, v[c + 6], v[c + 7]);
             }
+            m0 = max3(m0, v[BK - 4], v[BK - 3]);
+            m1 = max3(m1, v[BK - 2], v[BK - 1]);
             const float mt = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * sc;
             float corr = 1.f;
-            if (mine == 0) {
+            if (!prev) {
                 top = mt;
                 ref = mt == -INFINITY ? 0.f : mt;
             } else {
@@ -492,38 +653,23 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
                     ref = nref;
                     l *= corr;
                     // the group's last product must have left O
-                    if (!gate(&bar.pv_done[x], (nev - 1) & 1)) return;
+                    if (!gate(prev, prevp)) return;
                     tc_fence_after();
 #pragma unroll
-                    for (int c = 0; c < D; c += 16) {
-                        float o[16];
-                        tmem_ld16(to + c, o);
-                        tmem_ld_wait();
-                        uint32_t u[16];
+                    for (int c = 0; c < D; c += 32) {
+                        float o[32];
+                        tmem_ld32(to + c, o);
+                        tmem_arrived(o);
+                        uint32_t u[32];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(o[i] * corr);
+                        for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(o[i] * corr);
                         tmem_st16(to + c, u);
+                        tmem_st16(to + c + 16, u + 16);
                     }
                     tmem_st_wait();
                 }
                 top = fmaxf(top, mt);
             }
-            // probabilities, 32 at a time over S's own columns
-            float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-            for (int c = 0; c < BK; c += 32) {
-                uint32_t p[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float e0 = ex2(fmaf(v[c + 2 * i], sc, -ref)), e1 = ex2(fmaf(v[c + 2 * i + 1], sc, -ref));
-                    l0 += e0;
-                    l1 += e1;
-                    const __nv_bfloat162 b = __floats2bfloat162_rn(e0, e1);
-                    p[i] = *reinterpret_cast<const uint32_t *>(&b);
-                }
-                tmem_st16(ts + c / 2, p);
-            }
-            l += l0 + l1;
             // rows of V that no key of this item stands in may hold anything: zero
             // them (0 x NaN is NaN); the group whose product comes first does it
             const int z0 = max(0, (s.lo & ~(box - 1)) - key0), z1 = min(BK, s.hi - key0);
@@ -538,160 +684,62 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
                 }
                 fence_async_smem();
             }
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.p_ready[x]);
-            ++nev;
-            ++mine;
+            // probabilities, 32 at a time over S's own columns
+            const uint64_t sc2 = pack2(sc, sc), ref2 = pack2(-ref, -ref);
+            uint64_t sum2 = 0;
+#pragma unroll
+            for (int c = 0; c < BK; c += 32) {
+                uint32_t p[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    float e0, e1;
+                    unpack2(fma2(pack2(v[c + 2 * i], v[c + 2 * i + 1]), sc2, ref2), e0, e1);
+                    e0 = ex2(e0);
+                    e1 = ex2(e1);
+                    sum2 = add2(sum2, pack2(e0, e1));
+                    const __nv_bfloat162 b = __floats2bfloat162_rn(e0, e1);
+                    p[i] = *reinterpret_cast<const uint32_t *>(&b);
+                }
+                tmem_st16(ts + c / 2, p);
+                if (c == BK / 2 - 32 || c == BK - 32) {
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(c == BK - 32 ? &bar.p_rest[b] : &bar.p_ready[b]);
+                }
+            }
+            float l0, l1;
+            unpack2(sum2, l0, l1);
+            l += l0 + l1;
+            prev = &bar.pv_done[b];
+            prevp = ph;
         }
         seq0 += 2 * s.nt;
-
-        // ---- the segment's end: O, normalised or as a piece
-        const int G = a.G;
-        // row `row` of this half -> local row of the item
-        const int local = half * th * G + row;
-        const bool live = row < hrows;
-        const int64_t tok = s.tok + half * th + jt;
-        const int head = s.h * G + (row - jt * G);
-        if (!alt) {
-            if (s.nt > 0) {
-                if (!gate(&bar.pv_done[x], (nev - 1) & 1)) return;
+        if (!alt) n0 += s.nt;
+        else if (x == 0) n0 += (s.nt + 1) / 2, n2 += s.nt / 2;
+        if (!(alt && x)) {
+            if (prev) {
+                if (!gate(prev, prevp)) return;
                 tc_fence_after();
             }
-            float *slot = paged_slot(a, s.slot);
-            const float f = l > 0.f || l != l ? (s.whole ? 1.f / l : 1.f) : 0.f;
-#pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-                float o[32];
-                if (s.nt > 0) {
-                    tmem_ld32(to + c, o);
-                    tmem_ld_wait();
-                }
-                if (live) {
-                    const bool dead = s.nt == 0 || l == 0.f;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = dead ? 0.f : o[i] * f;
-                    if (s.whole) {
-                        uint4 *dst = reinterpret_cast<uint4 *>((__nv_bfloat16 *)a.o + (tok * a.Hq + head) * D + c);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t u[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const __nv_bfloat162 b = __floats2bfloat162_rn(o[8 * i + 2 * k], o[8 * i + 2 * k + 1]);
-                                u[k] = *reinterpret_cast<const uint32_t *>(&b);
-                            }
-                            dst[i] = make_uint4(u[0], u[1], u[2], u[3]);
-                        }
-                    } else {
-                        float4 *dst = reinterpret_cast<float4 *>(slot + 2 * a.slot_rows + (size_t)local * D + c);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-                    }
-                }
-            }
-            if (live) {
-                if (s.whole) {
-                    if (a.lse) a.lse[tok * a.Hq + head] = l == 0.f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
-                } else {
-                    reinterpret_cast<float2 *>(slot)[local] = make_float2(l == 0.f ? -INFINITY : ref, l);
-                }
-            }
-            if (s.nt > 0) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.o_free[x]);
-            }
-        } else {
-            // both groups hold every row: exchange (reference, sum), then each group
-            // writes half of the channels of the merged row
-            if (mine == 0) l = 0.f, top = -INFINITY;
-            ml[x * BM + row] = make_float2(l == 0.f ? -INFINITY : ref, l);
-            __syncwarp();
-            if (mine > 0) {
-                if (!gate(&bar.pv_done[x], (nev - 1) & 1)) return;
-            }
-            // (this warp has seen its own group's last product end; the meeting
-            // passes that on to the other group's warps)
-            tc_fence_before();
-            if (lane == 0) mbar_arrive(bar.meet);
-            if (!gate(bar.meet, meets & 1)) return;
-            ++meets;
-            tc_fence_after();
-            const float2 y0 = ml[row], y1 = ml[BM + row];
-            const float m = fmaxf(y0.x, y1.x), rf = m == -INFINITY ? 0.f : m;
-            const float f0 = y0.y == 0.f ? 0.f : ex2(y0.x - rf), f1 = y1.y == 0.f ? 0.f : ex2(y1.x - rf);
-            const float L = f0 * y0.y + f1 * y1.y;
-            float *slot = paged_slot(a, s.slot);
-            const bool dead = L == 0.f;
-            const float inv = s.whole && !dead ? 1.f / L : 1.f;
-            const uint32_t o0 = tmem + lanes + COL_O;
-#pragma unroll 1
-            for (int c = x * 64; c < x * 64 + 64; c += 32) {
-                float o[32], p[32];
-                if (s.nt > 0) {
-                    tmem_ld32(o0 + c, o);
-                    if (s.nt > 1) tmem_ld32(o0 + 128 + c, p);
-                    tmem_ld_wait();
-                }
-                if (live) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        float z = 0.f;
-                        if (s.nt > 0 && f0 != 0.f) z = f0 * o[i];
-                        if (s.nt > 1 && f1 != 0.f) z += f1 * p[i];
-                        o[i] = dead ? 0.f : z * inv;
-                    }
-                    if (s.whole) {
-                        uint4 *dst = reinterpret_cast<uint4 *>((__nv_bfloat16 *)a.o + (tok * a.Hq + head) * D + c);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t u[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const __nv_bfloat162 b = __floats2bfloat162_rn(o[8 * i + 2 * k], o[8 * i + 2 * k + 1]);
-                                u[k] = *reinterpret_cast<const uint32_t *>(&b);
-                            }
-                            dst[i] = make_uint4(u[0], u[1], u[2], u[3]);
-                        }
-                    } else {
-                        float4 *dst = reinterpret_cast<float4 *>(slot + 2 * a.slot_rows + (size_t)local * D + c);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-                    }
-                }
-            }
-            if (live && x == 0) {
-                if (s.whole) {
-                    if (a.lse) a.lse[tok * a.Hq + head] = dead ? -INFINITY : (rf + log2f(L)) * 0.6931471805599453f;
-                } else {
-                    reinterpret_cast<float2 *>(slot)[local] = make_float2(dead ? -INFINITY : rf, L);
-                }
-            }
-            // O of both groups is read by both: second meeting, then each frees its own
+            finish(a, to, th, seg, x, ref, l);
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar.meet);
-            if (!gate(bar.meet, meets & 1)) return;
-            ++meets;
-            if (mine > 0 && lane == 0) mbar_arrive(&bar.o_free[x]);
+            if (prev && lane == 0) mbar_arrive(&bar.o_free[x]);
         }
-        if (!s.whole && s.c0 == (int)blockIdx.x && threadIdx.x == 0) {
-            a.lead[2 * blockIdx.x] = make_int4(s.tok, s.h, 0, s.ntok * a.G);
-            a.lead[2 * blockIdx.x + 1] = make_int4(s.slot, s.c0, s.c1, 1);
-        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.seg_empty[iseg % SEGS]);
     }
 }
 
 __global__ void __launch_bounds__(THREADS, 1)
-    paged_tile_kernel(const __grid_constant__ PagedMaps maps, const __grid_constant__ CUtensorMap qmap, const PagedAttn a, int th,
+    paged_tile_kernel(const __grid_constant__ PagedMaps maps, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ PagedAttn a, int th,
                       int min_per) {
     extern __shared__ __align__(1024) uint8_t sm[];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     Shared *sh = reinterpret_cast<Shared *>(sm + OFF_MISC);
-    int64_t *scratch = reinterpret_cast<int64_t *>(sm + OFF_ML);
+    int64_t *scratch = reinterpret_cast<int64_t *>(sm + OFF_SCAN);
     const Bars bar(sm);
     if (tid == 0) {
         for (int i = 0; i < SLOTS; ++i) {
@@ -701,37 +749,34 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.q_full[i], 1);
             mbar_init(&bar.q_empty[i], 1);
+            mbar_init(&bar.o_free[i], 4);
+        }
+        for (int i = 0; i < 3; ++i) {
             mbar_init(&bar.s_full[i], 1);
             mbar_init(&bar.p_ready[i], 4);
+            mbar_init(&bar.p_rest[i], 4);
             mbar_init(&bar.pv_done[i], 1);
-            mbar_init(&bar.o_free[i], 4);
         }
         for (int i = 0; i < SEGS; ++i) {
             mbar_init(&bar.seg_full[i], 1);
-            mbar_init(&bar.seg_empty[i], SOFT + 2);
+            mbar_init(&bar.seg_empty[i], SOFT + 3);
         }
-        mbar_init(bar.meet, SOFT);
-        mbar_init(bar.meet + 1, 1);
+        mbar_init(bar.last, 1);
         mbar_fence_init();
         sh->abort = 0;
         a.lead[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
     }
     auto units = [&](int i, int *err) { return line_units(a, i, th, err); };
-    const int64_t total = paged_total<THREADS>(a, scratch, units);
-    int64_t per = (total + gridDim.x - 1) / gridDim.x;
-    if (per < min_per) per = min_per;
-    per = (per + 1) & ~(int64_t)1;
-    const int64_t P0 = (int64_t)blockIdx.x * per, P1 = P0 + per < total ? P0 + per : total;
+    const PagedLine line = paged_line<THREADS>(a, scratch, min_per, 2, units);
+    const int64_t P0 = line.P0, P1 = line.P1, per = line.per, before = line.before;
+    const int req = line.req;
     if (P0 >= P1) {
         asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
     }
-    int req;
-    int64_t before;
-    paged_find<THREADS>(a, P0, scratch, req, before, units);
     if (warp == 0) {  // kv head and row tile of the block's first unit
         const TileReq q = tile_req(a, req, th, nullptr);
-        const int64_t head = units_before(a, q, q.ng, th);
+        const int64_t head = line.units / a.Hkv;
         const int h = (int)((P0 - before) / head);
         const int64_t rem = P0 - before - h * head;
         // the last row tile that begins at or before rem, 32 candidates at a time
@@ -764,6 +809,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     w.h = sh->h;
     w.g = sh->g;
     w.fresh = true;
+    w.alts = 0;
     const Gate gate{&sh->abort, a.err};
     if (warp < SOFT) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFT));
@@ -773,9 +819,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (warp == SOFT)
             mma_role(a, sm, tmem, th, gate);
         else if (warp == SOFT + 1)
-            load_role(a, maps, qmap, sm, th, gate);
+            load_role(a, maps, sm, gate);
         else if (warp == SOFT + 2)
             walk_role(a, sm, w, th, P0, gate);
+        else
+            query_role(a, qmap, sm, th, gate);
     }
     tc_fence_before();
     __syncthreads();
