@@ -1,8 +1,8 @@
 // kda_paged_tile.cu -- paged attention on tcgen05 tensor cores, for bf16 caches
 // and requests with more rows than the rows kernel takes.
 //
-// One block per SM: eight softmax warps (two groups of 128 threads, a thread to
-// a row), one warp that issues the products, one that has the tensor memory
+// One block per SM: sixteen softmax warps (two groups of 256 threads, two threads
+// to a row, each with half of its keys), one warp that issues the products, one that has the tensor memory
 // accelerator load Q, K and V.  An item is up to two halves of 128 rows (whole
 // tokens: floor(128 / G) of them times G heads) of one kv head; key tiles are
 // 128 keys.
@@ -39,14 +39,15 @@ constexpr int NBAR = 2 * SLOTS + 19 + 2 * 4;
 constexpr int SEGS = 4;                        // ring of segments ahead of the roles
 constexpr int OFF_MISC = (OFF_BAR + NBAR * 8 + 63) / 64 * 64;  // TMEM address, abort flag, start of the block's line
 constexpr int OFF_SEG = OFF_MISC + 64;
-constexpr int SMEM = OFF_SEG + SEGS * 64;
+constexpr int OFF_MX = OFF_SEG + SEGS * 64;    // [group][half of the keys][row] maximum, sum
+constexpr int SMEM = OFF_MX + 4 * BM * 4;
 static_assert(OFF_SCAN % 16 == 0 && OFF_BAR % 8 == 0 && OFF_SEG % 64 == 0 && SMEM <= 232448, "shared memory layout");
-constexpr int SOFT = 8;                        // softmax warps
+constexpr int SOFT = 16;                       // softmax warps
 constexpr int THREADS = (SOFT + 4) * 32;       // (registers are given out by four warps)
-// registers a thread: 168 at launch (384 x 168 = 64,512), then 208 for the softmax
-// warps, which hold a row of S, and 88 for the others: 256 x 208 + 128 x 88 = 64,512
-constexpr int REGS_SOFT = 208, REGS_AUX = 88;
-static_assert(SOFT * 32 * REGS_SOFT + 128 * REGS_AUX <= THREADS * 168, "register split");
+// registers a thread: 96 at launch (640 x 96 = 61,440), then 104 for the softmax
+// warps, which hold half a row of S, and 64 for the others: 512 x 104 + 128 x 64 = 61,440
+constexpr int REGS_SOFT = 104, REGS_AUX = 64;
+static_assert(SOFT * 32 * REGS_SOFT + 128 * REGS_AUX <= THREADS * 96, "register split");
 constexpr int TCOLS = 512;
 constexpr uint32_t COL_S = 0, COL_O = 256;     // + 128 w
 constexpr float GROW = 8.f;                    // log2 growth of a maximum that ref follows
@@ -553,10 +554,20 @@ __device__ __forceinline__ void store_f32(float *dst, const float (&o)[32]) {
     }
 }
 
-// The segment's end of one group: O, normalised or as a piece.
-__device__ __forceinline__ void finish(const PagedAttn &a, uint32_t to, int th, const volatile Seg *s, int x, float ref, float l) {
-    const int row = threadIdx.x & 127, G = a.G;
-    const int half = s->alt ? 0 : x, nt = s->nt;
+// How many of the two warps' threads say so (a barrier of the two).
+__device__ __forceinline__ int pair_count(int id, bool pred) {
+    int n;
+    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %1, 0;\n barrier.red.popc.u32 %0, %2, 64, p;\n}\n"
+                 : "=r"(n)
+                 : "r"((uint32_t)pred), "r"(id)
+                 : "memory");
+    return n;
+}
+
+// The segment's end of one group: half of O's channels, normalised or as a piece.
+__device__ __forceinline__ void finish(const PagedAttn &a, uint32_t to, int th, const volatile Seg *s, int x, int hf, int row,
+                                       float ref, float l) {
+    const int G = a.G, half = s->alt ? 0 : x, nt = s->nt;
     const int jt = row / G, local = half * th * G + row;  // token within the half, row of the item
     const bool live = row < min(th, s->ntok - half * th) * G, whole = s->whole;
     const int64_t out = (int64_t)(s->tok + half * th + jt) * a.Hq + s->h * G + (row - jt * G);
@@ -564,7 +575,7 @@ __device__ __forceinline__ void finish(const PagedAttn &a, uint32_t to, int th, 
     const bool dead = nt == 0 || l == 0.f;  // (NaN passes through)
     const float f = whole ? 1.f / l : 1.f;
 #pragma unroll 1
-    for (int c = 0; c < D; c += 32) {
+    for (int c = 64 * hf; c < 64 * hf + 64; c += 32) {
         float o[32];
         tmem_ld32(to + c, o);
         tmem_arrived(o);
@@ -577,7 +588,7 @@ __device__ __forceinline__ void finish(const PagedAttn &a, uint32_t to, int th, 
                 store_f32(slot + 2 * a.slot_rows + (size_t)local * D + c, o);
         }
     }
-    if (live) {
+    if (live && hf == 0) {
         if (!whole)
             reinterpret_cast<float2 *>(slot)[local] = make_float2(dead ? -INFINITY : ref, dead ? 0.f : l);
         else if (a.lse)
@@ -589,27 +600,38 @@ __device__ __forceinline__ void finish(const PagedAttn &a, uint32_t to, int th, 
     }
 }
 
+// Two threads, of two warps that meet at a barrier of their own, share a row.  A
+// wait that runs out is passed on at the next meeting, so both leave together.
 __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, uint32_t tmem, int th, const Gate &gate) {
+    constexpr int HK = BK / 2;  // keys of one thread
     const Bars bar(sm);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, x = warp >> 2;  // group
-    const int row = threadIdx.x & 127;                                         // row of the half = TMEM lane
-    const uint32_t lanes = (uint32_t)(warp & 3) << 21;                         // 32 (warp % 4) << 16
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, x = warp >> 3, hf = (warp >> 2) & 1;
+    const int row = (warp & 3) * 32 + lane;             // row of the half = TMEM lane
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // 32 (warp % 4) << 16
     const uint32_t to = tmem + lanes + COL_O + x * 128;
+    const int id = 1 + x * 4 + (warp & 3);
+    float *mx = reinterpret_cast<float *>(sm + OFF_MX) + x * 2 * BM + row;  // + BM hf
     const float sc = a.scale_log2;
-    const int box = a.box;
     int n0 = 0, n2 = 0;  // this group's events by barrier: its own, and the first group's on the second buffer
     int64_t seq0 = 0;
+    bool failed = false;
     for (int iseg = 0;; ++iseg) {
-        if (!gate(&bar.seg_full[iseg % SEGS], (iseg / SEGS) & 1)) return;
+        if (!gate(&bar.seg_full[iseg % SEGS], (iseg / SEGS) & 1)) {
+            pair_count(id, true);
+            return;
+        }
         const Seg *seg = reinterpret_cast<const Seg *>(sm + OFF_SEG + (iseg % SEGS) * 64);
         struct {
             int lo, hi, t0, nt;
         } s{seg->lo, seg->hi, seg->t0, seg->nt};
-        if (s.nt < 0) return;
+        if (s.nt < 0) {
+            pair_count(id, false);
+            return;
+        }
         const bool alt = seg->alt;
         const int pos = seg->pos + (alt ? 0 : x) * th + row / a.G;
         const int first_key = a.window > 0 ? pos - a.window + 1 : 0;  // keys first_key .. pos, all below hi
-        float ref = 0.f, l = 0.f, top = -INFINITY;
+        float ref = 0.f, l = 0.f, top = -INFINITY;  // (top: of all the row's keys at the last change of ref, then of this half's)
         const int ne = alt ? (x ? 0 : s.nt) : 2 * s.nt;
         uint64_t *prev = nullptr;  // the group's last product
         int prevp = 0;
@@ -617,67 +639,70 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
             const int j = alt ? e : e >> 1, b = alt && (e & 1) ? 2 : x, ph = ((b == 2 ? n2 : n0) + (e >> 1)) & 1;
             const uint32_t ts = tmem + lanes + COL_S + (e & 1) * 128;
             const int key0 = (s.t0 + j) * BK;
-            if (!gate(&bar.s_full[b], ph)) return;
+            if (!gate(&bar.s_full[b], ph)) failed = true;
             tc_fence_after();
-            float v[BK];
+            float v[HK];
+            tmem_ld32(ts + HK * hf, v);
+            tmem_ld32(ts + HK * hf + 32, v + 32);
+            tmem_arrived(v);
+            tmem_arrived(v + 32);
+            // of this thread's keys, the row sees [c0, c1)
+            const int c1 = min(pos + 1, s.hi) - key0 - HK * hf, c0 = first_key - key0 - HK * hf;
+            if (__any_sync(0xffffffffu, c1 < HK || c0 > 0)) {
 #pragma unroll
-            for (int c = 0; c < BK; c += 32) tmem_ld32(ts + c, v + c);
-#pragma unroll
-            for (int c = 0; c < BK; c += 32) tmem_arrived(v + c);
-            // keys of the tile that this row sees: [c0, c1)
-            const int c1 = min(pos + 1, s.hi) - key0, c0 = first_key - key0;
-            if (__any_sync(0xffffffffu, c1 < BK || c0 > 0)) {
-#pragma unroll
-                for (int c = 0; c < BK; ++c) v[c] = c < c1 && c >= c0 ? v[c] : -INFINITY;
+                for (int c = 0; c < HK; ++c) v[c] = c < c1 && c >= c0 ? v[c] : -INFINITY;
             }
             float m0 = max3(v[0], v[1], v[2]), m1 = max3(v[3], v[4], v[5]), m2 = max3(v[6], v[7], v[8]), m3 = max3(v[9], v[10], v[11]);
 #pragma unroll
-            for (int c = 12; c + 8 <= BK; c += 8) {
+            for (int c = 12; c + 8 <= HK; c += 8) {
                 m0 = max3(m0, v[c], v[c + 1]);
                 m1 = max3(m1, v[c + 2], v[c + 3]);
                 m2 = max3(m2, v[c + 4], v[c + 5]);
                 m3 = max3(m3, v[c + 6], v[c + 7]);
             }
-            m0 = max3(m0, v[BK - 4], v[BK - 3]);
-            m1 = max3(m1, v[BK - 2], v[BK - 1]);
+            m0 = max3(m0, v[HK - 4], v[HK - 3]);
+            m1 = max3(m1, v[HK - 2], v[HK - 1]);
             const float mt = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * sc;
-            float corr = 1.f;
-            if (!prev) {
-                top = mt;
-                ref = mt == -INFINITY ? 0.f : mt;
-            } else {
-                const bool grow = mt > (top == -INFINITY ? -INFINITY : ref + GROW);
-                if (__any_sync(0xffffffffu, grow)) {
-                    const float m = fmaxf(top, mt), nref = m == -INFINITY ? 0.f : fmaxf(m, top == -INFINITY ? m : ref);
-                    corr = top == -INFINITY ? 0.f : ex2(ref - nref);  // (nothing summed yet: whatever O holds is zero)
-                    ref = nref;
-                    l *= corr;
-                    // the group's last product must have left O
-                    if (!gate(prev, prevp)) return;
+            // Meet: both have read S, whose columns P overwrites from here on; and does
+            // ref have to follow?  (a warp that gave up counts 32, one that asks for it 1)
+            const bool grow = __any_sync(0xffffffffu, !prev || mt > (top == -INFINITY ? -INFINITY : ref + GROW));
+            const int said = pair_count(id, failed || (grow && lane == 0));
+            if (said >= 32) return;
+            if (said) {
+                mx[BM * hf] = mt;
+                pair_count(id, false);
+                const float both = fmaxf(fmaxf(mt, mx[BM * (1 - hf)]), top);
+                const float nref = both == -INFINITY ? 0.f : top == -INFINITY ? both : fmaxf(both, ref);
+                const float corr = top == -INFINITY ? 0.f : ex2(ref - nref);  // (nothing summed yet: what O holds is zero)
+                top = both;
+                ref = nref;
+                l *= corr;
+                if (prev) {  // the group's last product must have left O
+                    if (!gate(prev, prevp)) failed = true;
                     tc_fence_after();
+#pragma unroll 1
+                    for (int c = 64 * hf; c < 64 * hf + 64; c += 16) {
+                        float o[16];
+                        tmem_ld16(to + c, o);
+                        tmem_ld_wait();
+                        uint32_t u[16];
 #pragma unroll
-                    for (int c = 0; c < D; c += 32) {
-                        float o[32];
-                        tmem_ld32(to + c, o);
-                        tmem_arrived(o);
-                        uint32_t u[32];
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(o[i] * corr);
+                        for (int i = 0; i < 16; ++i) {
+                            asm volatile("" : "+f"(o[i]));
+                            u[i] = __float_as_uint(o[i] * corr);
+                        }
                         tmem_st16(to + c, u);
-                        tmem_st16(to + c + 16, u + 16);
                     }
-                    tmem_st_wait();
                 }
-                top = fmaxf(top, mt);
             }
             // rows of V that no key of this item stands in may hold anything: zero
             // them (0 x NaN is NaN); the group whose product comes first does it
-            const int z0 = max(0, (s.lo & ~(box - 1)) - key0), z1 = min(BK, s.hi - key0);
-            if ((z0 > 0 || z1 < BK) && (alt || x == 0)) {
+            const int z0 = max(0, (s.lo & ~(a.box - 1)) - key0), z1 = min(BK, s.hi - key0);
+            if ((z0 > 0 || z1 < BK) && x == 0) {
                 const int64_t q = seq0 + seq_v(alt, j, s.nt);
-                if (!gate(&bar.kv_full[q % SLOTS], (int)((q / SLOTS) & 1))) return;
+                if (!gate(&bar.kv_full[q % SLOTS], (int)((q / SLOTS) & 1))) failed = true;
                 uint8_t *vt = sm + OFF_KV + (q % SLOTS) * SLOT;
-                for (int u = row; u < BK * 16; u += BM) {
+                for (int u = threadIdx.x; u < BK * 16; u += 2 * BM) {
                     const int r = u >> 4, c = u & 15;
                     if (r < z0 || r >= z1)
                         *reinterpret_cast<uint4 *>(vt + (c >> 3) * (SLOT / 2) + r * 128 + ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
@@ -688,7 +713,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
             const uint64_t sc2 = pack2(sc, sc), ref2 = pack2(-ref, -ref);
             uint64_t sum2 = 0;
 #pragma unroll
-            for (int c = 0; c < BK; c += 32) {
+            for (int c = 0; c < HK; c += 32) {
                 uint32_t p[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
@@ -697,17 +722,15 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
                     e0 = ex2(e0);
                     e1 = ex2(e1);
                     sum2 = add2(sum2, pack2(e0, e1));
-                    const __nv_bfloat162 b = __floats2bfloat162_rn(e0, e1);
-                    p[i] = *reinterpret_cast<const uint32_t *>(&b);
+                    const __nv_bfloat162 w = __floats2bfloat162_rn(e0, e1);
+                    p[i] = *reinterpret_cast<const uint32_t *>(&w);
                 }
-                tmem_st16(ts + c / 2, p);
-                if (c == BK / 2 - 32 || c == BK - 32) {
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(c == BK - 32 ? &bar.p_rest[b] : &bar.p_ready[b]);
-                }
+                tmem_st16(ts + (HK * hf + c) / 2, p);
             }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(hf ? &bar.p_rest[b] : &bar.p_ready[b]);
             float l0, l1;
             unpack2(sum2, l0, l1);
             l += l0 + l1;
@@ -718,11 +741,15 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
         if (!alt) n0 += s.nt;
         else if (x == 0) n0 += (s.nt + 1) / 2, n2 += s.nt / 2;
         if (!(alt && x)) {
+            float sum = 0.f;
             if (prev) {
-                if (!gate(prev, prevp)) return;
+                if (!gate(prev, prevp)) failed = true;
                 tc_fence_after();
+                mx[BM * hf] = l;  // (both are past the maxima that stood there: P V has been)
+                if (pair_count(id, failed) >= 32) return;
+                sum = mx[0] + mx[BM];
             }
-            finish(a, to, th, seg, x, ref, l);
+            finish(a, to, th, seg, x, hf, row, ref, sum);
             tc_fence_before();
             __syncwarp();
             if (prev && lane == 0) mbar_arrive(&bar.o_free[x]);
@@ -749,7 +776,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.q_full[i], 1);
             mbar_init(&bar.q_empty[i], 1);
-            mbar_init(&bar.o_free[i], 4);
+            mbar_init(&bar.o_free[i], 8);
         }
         for (int i = 0; i < 3; ++i) {
             mbar_init(&bar.s_full[i], 1);
