@@ -2,8 +2,9 @@
 // and requests with more rows than the rows kernel takes.
 //
 // One block per SM: sixteen softmax warps (two groups of 256 threads, two threads
-// to a row, each with half of its keys), one warp that issues the products, one that has the tensor memory
-// accelerator load Q, K and V.  An item is up to two halves of 128 rows (whole
+// to a row, each with half of its keys), a warp that issues each group's products,
+// one that has the tensor memory accelerator load K and V, and one that walks the
+// block's items and has Q loaded.  An item is up to two halves of 128 rows (whole
 // tokens: floor(128 / G) of them times G heads) of one kv head; key tiles are
 // 128 keys.
 //   S_w = Q_w K^T   128 x 128 fp32 in TMEM
@@ -35,7 +36,7 @@ constexpr int OFF_Q = 0;
 constexpr int OFF_KV = 2 * QHALF;
 constexpr int OFF_SCAN = OFF_KV + SLOTS * SLOT;  // the start's sums
 constexpr int OFF_BAR = OFF_SCAN + 256;
-constexpr int NBAR = 2 * SLOTS + 19 + 2 * 4;
+constexpr int NBAR = 2 * SLOTS + 17 + 2 * 4;
 constexpr int SEGS = 4;                        // ring of segments ahead of the roles
 constexpr int OFF_MISC = (OFF_BAR + NBAR * 8 + 63) / 64 * 64;  // TMEM address, abort flag, start of the block's line
 constexpr int OFF_SEG = OFF_MISC + 64;
@@ -53,7 +54,7 @@ constexpr uint32_t COL_S = 0, COL_O = 256;     // + 128 w
 constexpr float GROW = 8.f;                    // log2 growth of a maximum that ref follows
 
 struct Bars {
-    uint64_t *kv_full, *kv_empty, *q_full, *q_empty, *s_full, *p_ready, *p_rest, *pv_done, *o_free, *last, *seg_full, *seg_empty;
+    uint64_t *kv_full, *kv_empty, *q_full, *q_empty, *s_full, *p_ready, *pv_done, *o_free, *last, *seg_full, *seg_empty;
     __device__ explicit Bars(uint8_t *sm) {
         uint64_t *b = reinterpret_cast<uint64_t *>(sm + OFF_BAR);
         kv_full = b;
@@ -65,11 +66,10 @@ struct Bars {
         // wait on it, which sees every phase)
         s_full = q_empty + 2;        // [3]
         p_ready = s_full + 3;        // [3]
-        p_rest = p_ready + 3;        // [3] keys 64 .. 127 of P
-        pv_done = p_rest + 3;        // [3]
+        pv_done = p_ready + 3;       // [3]
         o_free = pv_done + 3;        // [2]
-        last = o_free + 2;           // [1] products in flight when a wait ran out
-        seg_full = last + 1;
+        last = o_free + 2;           // [2] products in flight when a wait ran out
+        seg_full = last + 2;
         seg_empty = seg_full + SEGS;
     }
 };
@@ -225,17 +225,50 @@ struct Walk {
     }
 };
 
-// Place of K_j and V_j in the order of loading, counted from the item's first:
-// two halves K0 V0 K1 V1 ..; one half K0 K1 V0 K2 V1 .. (two K tiles are
-// multiplied before the first V).
-__device__ __forceinline__ int seq_k(bool alt, int j) { return alt ? (j == 0 ? 0 : 2 * j - 1) : 2 * j; }
+// K and V tiles are loaded in the order of their first use, K0 V0 K1 V1 .. (one
+// half: K0 K1 V0 K2 V1 .., two S being formed before the first P V).  Place of V_j,
+// counted from the item's first.
 __device__ __forceinline__ int seq_v(bool alt, int j, int nt) { return alt ? (j == nt - 1 ? 2 * nt - 1 : 2 * j + 2) : 2 * j + 1; }
 
-__device__ __forceinline__ void mma_ta_w(uint32_t d, uint32_t ta, uint64_t b, uint32_t idesc, bool acc) {
+// The products are issued by a whole converged warp, one elected lane of which
+// does it, in batches of straight code: the issuing warp is on the path of every
+// tile (with a descriptor built and a lane elected for each product it took some
+// 2,200 cycles a tile and half, more than the products themselves).
+//
+// S = Q K^T: eight steps of 16 channels; q, k are the descriptors of the first
+// step, each step 32 bytes on, the second 64 channels one block on.
+__device__ __forceinline__ void issue_qk(uint32_t d, uint64_t q, uint64_t k, uint32_t idesc) {
     asm volatile(
-        "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xffffffff;\n"
-        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-        "r"(ta), "l"(b), "r"(idesc), "r"((uint32_t)acc));
+        "{\n .reg .pred e, t, f;\n .reg .b64 a, b;\n"
+        " setp.eq.u32 t, 0, 0;\n setp.ne.u32 f, 0, 0;\n elect.sync _|e, 0xffffffff;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, f;\n"
+        " add.s64 a, %1, 2;\n add.s64 b, %2, 2;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+        " add.s64 a, %1, 4;\n add.s64 b, %2, 4;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+        " add.s64 a, %1, 6;\n add.s64 b, %2, 6;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+        " add.s64 a, %1, 1024;\n add.s64 b, %2, 1024;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+        " add.s64 a, %1, 1026;\n add.s64 b, %2, 1026;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+        " add.s64 a, %1, 1028;\n add.s64 b, %2, 1028;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+        " add.s64 a, %1, 1030;\n add.s64 b, %2, 1030;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+        "}\n" ::"r"(d),
+        "l"(q), "l"(k), "r"(idesc)
+        : "memory");
+}
+// O (+)= P V: eight steps of 16 keys, P 8 columns of TMEM on, V 2 KB on.
+__device__ __forceinline__ void issue_pv(uint32_t d, uint32_t p, uint64_t v, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n .reg .pred e, t, f;\n .reg .b32 a;\n .reg .b64 b;\n"
+        " setp.eq.u32 t, 0, 0;\n setp.ne.u32 f, %4, 0;\n elect.sync _|e, 0xffffffff;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, f;\n"
+        " add.u32 a, %1, 8;\n add.s64 b, %2, 128;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
+        " add.u32 a, %1, 16;\n add.s64 b, %2, 256;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
+        " add.u32 a, %1, 24;\n add.s64 b, %2, 384;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
+        " add.u32 a, %1, 32;\n add.s64 b, %2, 512;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
+        " add.u32 a, %1, 40;\n add.s64 b, %2, 640;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
+        " add.u32 a, %1, 48;\n add.s64 b, %2, 768;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
+        " add.u32 a, %1, 56;\n add.s64 b, %2, 896;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
+        "}\n" ::"r"(d),
+        "r"(p), "l"(v), "r"(idesc), "r"((uint32_t)acc)
+        : "memory");
 }
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *o) {
     uint32_t r[32];
@@ -314,21 +347,46 @@ struct Gate {  // bounded waits that stop the whole block when one runs out
     }
 };
 
-// One warp walks the line ahead of the others; a segment with nt < 0 ends it.
-__device__ __forceinline__ void walk_role(const PagedAttn &a, uint8_t *sm, Walk w, int th, int64_t P0, const Gate &gate) {
+// One warp walks the line ahead of the others, and has each segment's queries
+// loaded; a segment with nt < 0 ends it.  Items of one half take the two halves of
+// the buffer in turn, so the next one's queries arrive while this one is worked on.
+__device__ __forceinline__ void walk_role(const PagedAttn &a, const CUtensorMap &qmap, uint8_t *sm, Walk w, int th, int64_t P0,
+                                          const Gate &gate) {
     const int lane = threadIdx.x & 31;
     const Bars bar(sm);
+    int n0 = 0, n1 = 0;  // loads of each half of Q
     for (int i = 0;; ++i) {
         Seg s;
         const bool more = w.next(a, th, P0, s);
         if (!more) s.nt = -1;
-        if (!gate(&bar.seg_empty[i % SEGS], ((i / SEGS) & 1) ^ 1)) return;
-        if (lane == 0) {
+        bool ok = gate(&bar.seg_empty[i % SEGS], ((i / SEGS) & 1) ^ 1);
+        if (ok && lane == 0) {
             *reinterpret_cast<Seg *>(sm + OFF_SEG + (i % SEGS) * 64) = s;
             mbar_arrive(&bar.seg_full[i % SEGS]);
         }
         __syncwarp();
-        if (!more) return;
+        if (ok && !more) return;
+        for (int x = 0; ok && s.nt > 0 && x < 2; ++x) {
+            if (s.alt && x != s.half) continue;
+            ok = gate(&bar.q_empty[x], ((x ? n1 : n0) & 1) ^ 1);
+            if (ok && lane == 0) {
+                mbar_expect_tx(&bar.q_full[x], (uint32_t)(2 * th * a.G * 128));
+                uint8_t *dst = sm + OFF_Q + x * QHALF;
+                const int tok = s.tok + (s.alt ? 0 : x * th);
+                tma_load_3d(dst, &qmap, 0, s.h * a.G, tok, &bar.q_full[x]);
+                tma_load_3d(dst + QHALF / 2, &qmap, 64, s.h * a.G, tok, &bar.q_full[x]);
+            }
+            __syncwarp();
+            if (!ok) break;
+            if (x) ++n1;
+            else ++n0;
+        }
+        if (!ok) {  // let the copies in flight land
+            if (n0) mbar_wait(&bar.q_full[0], (n0 - 1) & 1);
+            if (n1) mbar_wait(&bar.q_full[1], (n1 - 1) & 1);
+            __syncwarp();
+            return;
+        }
     }
 }
 // The next segment, for a whole warp; false at the line's end.
@@ -342,46 +400,15 @@ __device__ __forceinline__ bool next_seg(uint8_t *sm, const Bars &bar, int &i, c
 }
 
 // ---------------------------------------------------------------- loads
-// Queries.  Items of one half take the two halves of the buffer in turn, so the
-// next one's queries arrive while this one is worked on.
-__device__ __forceinline__ void query_role(const PagedAttn &a, const CUtensorMap &qmap, uint8_t *sm, int th, const Gate &gate) {
-    const int lane = threadIdx.x & 31;
-    const Bars bar(sm);
-    int n0 = 0, n1 = 0;  // loads of each half
-    Seg s;
-    int iseg = 0;
-    while (next_seg(sm, bar, iseg, gate, s)) {
-        if (s.nt == 0) continue;
-        for (int x = 0; x < 2; ++x) {
-            if (s.alt && x != s.half) continue;
-            if (!gate(&bar.q_empty[x], ((x ? n1 : n0) & 1) ^ 1)) {  // let the copies in flight land
-                if (n0) mbar_wait(&bar.q_full[0], (n0 - 1) & 1);
-                if (n1) mbar_wait(&bar.q_full[1], (n1 - 1) & 1);
-                __syncwarp();
-                return;
-            }
-            if (lane == 0) {
-                mbar_expect_tx(&bar.q_full[x], (uint32_t)(2 * th * a.G * 128));
-                uint8_t *dst = sm + OFF_Q + x * QHALF;
-                const int tok = s.tok + (s.alt ? 0 : x * th);
-                tma_load_3d(dst, &qmap, 0, s.h * a.G, tok, &bar.q_full[x]);
-                tma_load_3d(dst + QHALF / 2, &qmap, 64, s.h * a.G, tok, &bar.q_full[x]);
-            }
-            __syncwarp();
-            if (x) ++n1;
-            else ++n0;
-        }
-    }
-}
-
 // Keys and values.
 __device__ __forceinline__ void load_role(const PagedAttn &a, const PagedMaps &maps, uint8_t *sm, const Gate &gate) {
     const int lane = threadIdx.x & 31;
     const Bars bar(sm);
     const int box = a.box, nbx = BK / box;
-    int64_t seq = 0;   // K / V tiles so far
+    int ring = 0, ringp = 0;
+    uint32_t seq = 0;  // K / V tiles so far
     auto drain = [&]() {  // a wait ran out: let the copies in flight land before the block ends
-        for (int64_t u = seq - 1; u >= 0 && u >= seq - SLOTS; --u) mbar_wait(&bar.kv_full[u % SLOTS], (u / SLOTS) & 1);
+        for (uint32_t i = 1; i <= SLOTS && i <= seq; ++i) mbar_wait(&bar.kv_full[(seq - i) % SLOTS], ((seq - i) / SLOTS) & 1);
         __syncwarp();
     };
     Seg s;
@@ -405,8 +432,8 @@ __device__ __forceinline__ void load_role(const PagedAttn &a, const PagedMaps &m
                     }
                 }
             }
-            const int slot = (int)(seq % SLOTS);
-            if (!gate(&bar.kv_empty[slot], (int)((seq / SLOTS) & 1) ^ 1)) return false;
+            const int slot = ring;
+            if (!gate(&bar.kv_empty[slot], ringp ^ 1)) return false;
             const int f = max(0, (lob - key0) / box), e = min(nbx, (s.hi - key0 + box - 1) / box);
             if (lane == 0) mbar_expect_tx(&bar.kv_full[slot], (uint32_t)((e - f) * box * D * 2));
             __syncwarp();
@@ -420,6 +447,10 @@ __device__ __forceinline__ void load_role(const PagedAttn &a, const PagedMaps &m
             }
             __syncwarp();
             ++seq;
+            if (++ring == SLOTS) {
+                ring = 0;
+                ringp ^= 1;
+            }
             return true;
         };
         for (int j = 0; j < s.nt; ++j) {
@@ -435,83 +466,99 @@ __device__ __forceinline__ void load_role(const PagedAttn &a, const PagedMaps &m
 }
 
 // ---------------------------------------------------------------- products
-__device__ __forceinline__ void mma_role(const PagedAttn &a, uint8_t *sm, uint32_t tmem, int th, const Gate &gate) {
+// One warp for each group's products (an item of one half is the first warp's
+// alone): what one of them spends on waits and on issuing hides behind the other's
+// products.  Both see every K, V and Q tile, so that no barrier's phase passes one
+// of them by: whoever has no product on a tile gives it back as soon as it came.
+__device__ __forceinline__ void mma_role(const PagedAttn &a, uint8_t *sm, uint32_t tmem, int x, const Gate &gate) {
     const Bars bar(sm);
     constexpr uint32_t ID_QK = idesc_bf16_f32(BM, BK), ID_PV = idesc_bf16_f32_bmn(BM, D);
-    const uint32_t base = smem_u32(sm);
-    int64_t seq0 = 0;
-    int q0 = 0, q1 = 0, p0 = 0, p1 = 0, p2 = 0, i0 = 0, i1 = 0;  // halves of Q; products P V by barrier, items by group
+    const int lane = threadIdx.x & 31;
+    const uint32_t base = smem_u32(sm), to = tmem + COL_O + x * 128;
+    const uint64_t dq = sdesc_sw128(base + OFF_Q), dk = sdesc_sw128(base + OFF_KV),
+                   dv = sdesc_mn(base + OFF_KV, SLOT / 2, 1024, SWZ_128B);
+    // tiles are first used in the order in which they are loaded
+    int ring = 0, ringp = 0;
+    auto take = [&](int &slot) -> bool {
+        slot = ring;
+        const bool ok = gate(&bar.kv_full[ring], ringp);
+        if (++ring == SLOTS) {
+            ring = 0;
+            ringp ^= 1;
+        }
+        return ok;
+    };
+    auto give = [&](uint64_t *b) {
+        if (lane == 0) mbar_arrive(b);
+        __syncwarp();
+    };
+    uint32_t par = 0;  // parity bits: 0, 1 halves of Q; 2..4 P by barrier; 5 O
+    bool ok = true;
     Seg s;
     int iseg = 0;
-    while (next_seg(sm, bar, iseg, gate, s)) {
+    while (ok && next_seg(sm, bar, iseg, gate, s)) {
         if (s.nt == 0) continue;
         const bool alt = s.alt;
-        const int ne = alt ? s.nt : 2 * s.nt;  // events: one S and one P V, S buffers in turn
-        auto kv_ready = [&](int64_t q) { return gate(&bar.kv_full[q % SLOTS], (int)((q / SLOTS) & 1)); };
-        auto qk = [&](int e) -> bool {
-            const int x = e & 1, j = alt ? e : e >> 1;
-            const int64_t q = seq0 + seq_k(alt, j);
-            const int half = alt ? s.half : x;
-            if (e == 0 || (!alt && e == 1))
-                if (!gate(&bar.q_full[half], (half ? q1 : q0) & 1)) return false;
-            if ((alt || x == 0) && !kv_ready(q)) return false;
-            tc_fence_after();
-            const uint32_t qa = base + OFF_Q + half * QHALF, ka = base + OFF_KV + (uint32_t)(q % SLOTS) * SLOT;
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                const uint32_t off = (uint32_t)(k >> 2) * (SLOT / 2) + (uint32_t)(k & 3) * 32;
-                mma_bf16_w(tmem + COL_S + x * 128, sdesc_sw128(qa + off), sdesc_sw128(ka + off), ID_QK, k > 0);
-            }
-            mma_commit_w(&bar.s_full[alt && x ? 2 : x]);
-            if (alt || x == 1) mma_commit_w(&bar.kv_empty[q % SLOTS]);
-            if (alt ? e == ne - 1 : e >= ne - 2) {
-                mma_commit_w(&bar.q_empty[half]);
-                if (half) ++q1;
-                else ++q0;
-            }
-            return true;
+        const int nt = s.nt, half = alt ? s.half : x;
+        auto query = [&](int h) -> bool {
+            const bool got = gate(&bar.q_full[h], (par >> h) & 1);
+            par ^= 1u << h;
+            return got;
         };
-        auto pv = [&](int e) -> bool {
-            const int x = e & 1, j = alt ? e : e >> 1;
-            const int64_t q = seq0 + seq_v(alt, j, s.nt);
-            if ((alt || x == 0) && !kv_ready(q)) return false;
-            const int b = alt && x ? 2 : x, np = b == 0 ? p0 : b == 1 ? p1 : p2;
-            if (!gate(&bar.p_ready[b], np & 1)) return false;
-            const int g = alt ? 0 : x;  // group, whose O it is
-            const bool head = alt ? e == 0 : e < 2;
-            if (head) {  // the group's last item must have left O
-                if (!gate(&bar.o_free[g], ((g ? i1 : i0) & 1) ^ 1)) return false;
-                if (g) ++i1;
-                else ++i0;
+        if (alt && x) {  // the other warp's item
+            ok = query(half);
+            give(&bar.q_empty[half]);
+            for (int i = 0; ok && i < 2 * nt; ++i) {
+                int slot;
+                ok = take(slot);
+                give(&bar.kv_empty[slot]);
             }
-            tc_fence_after();
-            const uint32_t va = base + OFF_KV + (uint32_t)(q % SLOTS) * SLOT;
-#pragma unroll
-            for (int k = 0; k < BK / 16; ++k) {
-                if (k == BK / 32) {  // the first keys' product runs while the others' probabilities are worked out
-                    if (!gate(&bar.p_rest[b], np & 1)) return false;
-                    tc_fence_after();
-                }
-                mma_ta_w(tmem + COL_O + g * 128, tmem + COL_S + x * 128 + k * 8, sdesc_mn(va + k * 2048, SLOT / 2, 1024, SWZ_128B),
-                         ID_PV, !head || k > 0);
-            }
-            mma_commit_w(&bar.pv_done[b]);
-            if (b == 0) ++p0;
-            else if (b == 1) ++p1;
-            else ++p2;
-            if (alt || x == 1) mma_commit_w(&bar.kv_empty[q % SLOTS]);
-            return true;
-        };
-        bool ok = qk(0) && (ne < 2 || qk(1));
-        for (int e = 0; ok && e < ne; ++e) ok = pv(e) && (e + 2 >= ne || qk(e + 2));
-        if (!ok) {  // let the products in flight end before TMEM is given back
-            uint64_t *last = bar.last;
-            mma_commit_w(last);
-            mbar_wait(last, 0);
-            __syncwarp();
-            return;
+            continue;
         }
-        seq0 += 2 * s.nt;
+        int kslot = 0, vslot = 0;
+        ok = query(half);
+        if (!alt) {  // the other half's queries
+            ok = query(half ^ 1) && ok;
+            give(&bar.q_empty[half ^ 1]);
+        }
+        const uint64_t q = dq + (uint32_t)half * (QHALF >> 4);
+        auto qk = [&](int j) {  // S of key tile j, into this warp's buffer or, for one half, both in turn
+            const int buf = alt ? j & 1 : x;
+            issue_qk(tmem + COL_S + buf * 128, q, dk + (uint32_t)kslot * (SLOT >> 4), ID_QK);
+            mma_commit_w(&bar.s_full[alt && buf ? 2 : buf]);
+            mma_commit_w(&bar.kv_empty[kslot]);
+            if (j == nt - 1) mma_commit_w(&bar.q_empty[half]);
+        };
+        const int ahead = alt ? 2 : 1;  // S buffers
+        for (int j = 0; ok && j < ahead && j < nt; ++j) {
+            ok = take(kslot);
+            tc_fence_after();
+            if (ok) qk(j);
+        }
+        for (int j = 0; ok && j < nt; ++j) {
+            // all waits come before the products, P's last: then P V and the next S are
+            // issued in one go
+            const int buf = alt ? j & 1 : x, b = alt && buf ? 2 : buf;
+            ok = take(vslot);
+            if (j + ahead < nt) ok = take(kslot) && ok;
+            if (j == 0) {  // the group's last item must have left O
+                ok = gate(&bar.o_free[x], ((par >> 5) & 1) ^ 1) && ok;
+                par ^= 1u << 5;
+            }
+            ok = gate(&bar.p_ready[b], (par >> (2 + b)) & 1) && ok;
+            par ^= 1u << (2 + b);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(to, tmem + COL_S + buf * 128, dv + (uint32_t)vslot * (SLOT >> 4), ID_PV, j > 0);
+            mma_commit_w(&bar.pv_done[b]);
+            mma_commit_w(&bar.kv_empty[vslot]);
+            if (j + ahead < nt) qk(j + ahead);
+        }
+    }
+    if (!ok || *gate.abort) {  // let the products in flight end before TMEM is given back
+        mma_commit_w(bar.last + x);
+        mbar_wait(bar.last + x, 0);
+        __syncwarp();
     }
 }
 
@@ -613,7 +660,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
     float *mx = reinterpret_cast<float *>(sm + OFF_MX) + x * 2 * BM + row;  // + BM hf
     const float sc = a.scale_log2;
     int n0 = 0, n2 = 0;  // this group's events by barrier: its own, and the first group's on the second buffer
-    int64_t seq0 = 0;
+    uint32_t seq0 = 0;  // K / V tiles before this segment's
     bool failed = false;
     for (int iseg = 0;; ++iseg) {
         if (!gate(&bar.seg_full[iseg % SEGS], (iseg / SEGS) & 1)) {
@@ -696,13 +743,13 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
                 }
             }
             // rows of V that no key of this item stands in may hold anything: zero
-            // them (0 x NaN is NaN); the group whose product comes first does it
+            // them (0 x NaN is NaN); each group before its own product
             const int z0 = max(0, (s.lo & ~(a.box - 1)) - key0), z1 = min(BK, s.hi - key0);
-            if ((z0 > 0 || z1 < BK) && x == 0) {
-                const int64_t q = seq0 + seq_v(alt, j, s.nt);
+            if (z0 > 0 || z1 < BK) {
+                const uint32_t q = seq0 + seq_v(alt, j, s.nt);
                 if (!gate(&bar.kv_full[q % SLOTS], (int)((q / SLOTS) & 1))) failed = true;
                 uint8_t *vt = sm + OFF_KV + (q % SLOTS) * SLOT;
-                for (int u = threadIdx.x; u < BK * 16; u += 2 * BM) {
+                for (int u = threadIdx.x & (2 * BM - 1); u < BK * 16; u += 2 * BM) {
                     const int r = u >> 4, c = u & 15;
                     if (r < z0 || r >= z1)
                         *reinterpret_cast<uint4 *>(vt + (c >> 3) * (SLOT / 2) + r * 128 + ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
@@ -730,7 +777,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(hf ? &bar.p_rest[b] : &bar.p_ready[b]);
+            if (lane == 0) mbar_arrive(&bar.p_ready[b]);
             float l0, l1;
             unpack2(sum2, l0, l1);
             l += l0 + l1;
@@ -771,17 +818,16 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (tid == 0) {
         for (int i = 0; i < SLOTS; ++i) {
             mbar_init(&bar.kv_full[i], 1);
-            mbar_init(&bar.kv_empty[i], 1);
+            mbar_init(&bar.kv_empty[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.q_full[i], 1);
-            mbar_init(&bar.q_empty[i], 1);
+            mbar_init(&bar.q_empty[i], 2);
             mbar_init(&bar.o_free[i], 8);
         }
         for (int i = 0; i < 3; ++i) {
             mbar_init(&bar.s_full[i], 1);
-            mbar_init(&bar.p_ready[i], 4);
-            mbar_init(&bar.p_rest[i], 4);
+            mbar_init(&bar.p_ready[i], 8);
             mbar_init(&bar.pv_done[i], 1);
         }
         for (int i = 0; i < SEGS; ++i) {
@@ -789,6 +835,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(&bar.seg_empty[i], SOFT + 3);
         }
         mbar_init(bar.last, 1);
+        mbar_init(bar.last + 1, 1);
         mbar_fence_init();
         sh->abort = 0;
         a.lead[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
@@ -843,14 +890,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         softmax_role(a, sm, tmem, th, gate);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_AUX));
-        if (warp == SOFT)
-            mma_role(a, sm, tmem, th, gate);
-        else if (warp == SOFT + 1)
-            load_role(a, maps, sm, gate);
+        if (warp < SOFT + 2)
+            mma_role(a, sm, tmem, warp - SOFT, gate);
         else if (warp == SOFT + 2)
-            walk_role(a, sm, w, th, P0, gate);
+            load_role(a, maps, sm, gate);
         else
-            query_role(a, qmap, sm, th, gate);
+            walk_role(a, qmap, sm, w, th, P0, gate);
     }
     tc_fence_before();
     __syncthreads();
