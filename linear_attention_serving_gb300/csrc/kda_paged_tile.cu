@@ -123,19 +123,20 @@ __device__ __forceinline__ void key_tiles(const PagedAttn &a, const PagedReq &r,
     t0 = lo / BK;
     t1 = (hi + BK - 1) / BK;
 }
-// Length of an item in the line: HEAD units for what an item costs besides its
-// tiles (Q, the first S, O on its way out: about two tiles' time), then two units a
-// tile, one where it is for one half, always
-// even so that every cut falls on a tile of either kind; an item without keys takes
-// the place of one tile.  A cut inside the fixed part leaves the item to the next
-// block.
-constexpr int HEAD = 4;
+// Length of an item in the line: first some units for what an item costs besides
+// its tiles (the first S, O on its way out: measured, 5 us where the tensor cores
+// wait for it, 2.5 us where an item of one half waits for memory all the same), then
+// two units (1.7 us) a tile, one (1.3 us) for one half; always even, so that every
+// cut falls on a tile of either kind.  An item without keys takes the place of one
+// tile.  A cut inside the fixed part leaves the item to the next block.
+__host__ __device__ constexpr int item_head(bool alt) { return alt ? 2 : 6; }
 __device__ __forceinline__ int item_units(const PagedAttn &a, const TileReq &q, int g, int th) {
     const int j0 = g * 2 * th, j1 = min(q.n, j0 + 2 * th) - 1;
     int lo, hi, t0, t1;
     key_tiles(a, q.r, j0, j1, lo, hi, t0, t1);
     const int nt = max(1, t1 - t0);
-    return HEAD + (j1 - j0 + 1 > th ? 2 * nt : (nt + 1) & ~1);
+    const bool alt = j1 - j0 + 1 <= th;
+    return item_head(alt) + (alt ? (nt + 1) & ~1 : 2 * nt);
 }
 // Units of the row tiles before g (closed form: a long request has thousands).
 __device__ __forceinline__ int64_t units_before(const PagedAttn &a, const TileReq &q, int g, int th) {
@@ -150,7 +151,7 @@ __device__ __forceinline__ int64_t units_before(const PagedAttn &a, const TileRe
         if (gw < neg) gw = neg;
         if (gw < full) tiles -= floor_sum(full - gw, BK, TT, gw * TT - d);
     }
-    int64_t u = 2 * tiles + (int64_t)HEAD * full;
+    int64_t u = 2 * tiles + (int64_t)item_head(false) * full;
     if (g > full) u += item_units(a, q, full, th);  // the last, shorter row tile
     return u;
 }
@@ -192,8 +193,9 @@ struct Walk {
         key_tiles(a, q.r, j0, j1, s.lo, s.hi, t0, t1);
         s.alt = j1 - j0 + 1 <= th;
         const int sh = s.alt ? 0 : 1;
-        const int b = max(0, (int)(pos - A) - HEAD) >> sh, e = min(max(0, (int)(stop - A) - HEAD) >> sh, t1 - t0);
-        const bool some = stop - A > HEAD;
+        const int head = item_head(s.alt);
+        const int b = max(0, (int)(pos - A) - head) >> sh, e = min(max(0, (int)(stop - A) - head) >> sh, t1 - t0);
+        const bool some = stop - A > head;
         s.t0 = t0 + b;
         s.nt = max(0, e - b);
         s.tok = q.r.tok0 + j0;
@@ -203,7 +205,7 @@ struct Walk {
         s.req = req;
         s.whole = b == 0 && stop == B;
         s.slot = 2 * (int)blockIdx.x + (pos == P0 ? 0 : 1);
-        s.c0 = (int)((A + HEAD) / per);
+        s.c0 = (int)((A + head) / per);
         s.c1 = (int)((B - 1) / per);
         pos = stop;
         if (stop == B) {
