@@ -3,7 +3,10 @@ slot maps from request lengths, the append of new keys and values, and the
 attention of each request's new tokens over its cached keys.
 
 As in ``kda.py``, argument marshalling only: outputs and the workspace are
-allocated with torch, everything else runs in the library's CUDA kernels.
+allocated with torch, everything else runs in the library's CUDA kernels.  The
+smallest calls take a few microseconds on the GPU, so the checks here are
+written to cost little: one pass over the tensors, messages put together only
+when something is wrong, addresses handed over as plain integers.
 """
 from __future__ import annotations
 
@@ -11,79 +14,96 @@ import ctypes
 
 import torch
 
-from .kda import D, KDA_BF16, KDA_F32, KDAError, _check, _dtype_code, _p, _stream, load
+from .kda import D, KDA_BF16, KDA_F32, KDAError, _check, load
 
 KDA_E4M3 = 2
 DEVERR_LENGTHS, DEVERR_NO_PAGES, DEVERR_PAGE = 8, 16, 32
 
-_declared = False
+_I32, _I64, _F32, _E4M3 = torch.int32, torch.int64, torch.float32, torch.float8_e4m3fn
+_CODE = {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32}
+_CACHE_CODE = {**_CODE, _E4M3: KDA_E4M3}
+_declared = None
 
 
 def _lib():
     global _declared
-    lib = load()
-    if not _declared:
+    if _declared is None:
+        lib = load()
         P, I, L, F, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
         lib.kda_paged_tables.argtypes = [P, P, I, L, P, I, P, I, P, P, I, I, P, P, P, P, P, P]
         lib.kda_paged_append.argtypes = [P, P, P, L, I, I, I, I, P, P, P, P, I, I, L, P, P]
         lib.kda_paged_attn.argtypes = [P, P, P, P, P, P, I, L, I, I, I, I, I, I, P, P, I, I, L, I, F, I, P, P, P, S, P, P]
         lib.kda_paged_attn_workspace_size.argtypes = [L, I, I, I]
         lib.kda_paged_attn_workspace_size.restype = S
-        _declared = True
-    return lib
+        _declared = lib
+    return _declared
+
+
+try:  # the stream's address without a Stream object around it
+    _raw_stream = torch._C._cuda_getCurrentRawStream
+except AttributeError:
+    def _raw_stream(index):
+        return torch.cuda.current_stream(index).cuda_stream
 
 
 def _on_device(*ts):
-    """Every tensor contiguous and on one CUDA device (the caches are checked by
-    _cache: their pages may lie apart)."""
-    dev = None
+    """Every tensor contiguous and on one CUDA device; returns its index.  (The
+    caches are checked by _cache: their pages may lie apart.)"""
+    index = ts[0].get_device()
     for t in ts:
-        if t is None:
-            continue
-        if not t.is_cuda:
+        if t is not None and (t.get_device() != index or not t.is_contiguous()):
+            index = -1
+    if index < 0:
+        given = [t for t in ts if t is not None]
+        if not all(t.is_cuda for t in given):
             raise KDAError("all tensors must be CUDA tensors")
-        if not t.is_contiguous():
+        if not all(t.is_contiguous() for t in given):
             raise KDAError("all tensors must be contiguous")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise KDAError("all tensors must be on the same CUDA device")
+        raise KDAError("all tensors must be on the same CUDA device")
+    return index
 
 
-def _typed(dtype, **ts):
-    for name, t in ts.items():
-        if t is not None and t.dtype != dtype:
+def _typed(dtype, names, *ts):
+    for name, t in zip(names.split(), ts):
+        if t is not None and t.dtype is not dtype:
             raise KDAError(f"{name} must be {str(dtype).replace('torch.', '')}")
 
 
-def _cache_code(t) -> int:
-    if t.dtype == torch.float8_e4m3fn:
-        return KDA_E4M3
-    return _dtype_code(t)
+def _p(t):
+    return None if t is None else t.data_ptr()
 
 
-def _cache(x, k_cache, v_cache, k_scale, v_scale):
-    """Geometry of the two caches, checked: (n_pages, Hkv, page_size, page stride)."""
-    if k_cache.dim() != 4 or k_cache.shape[3] != D or k_cache.shape != v_cache.shape:
+def _cache(index, k_cache, v_cache, k_scale, v_scale):
+    """Geometry of the two caches, checked: (n_pages, Hkv, page_size, page stride, type)."""
+    shape = k_cache.shape
+    if len(shape) != 4 or shape[3] != D or shape != v_cache.shape:
         raise KDAError("k_cache and v_cache must both be [pages, kv heads, page size, 128]")
-    if k_cache.dtype != v_cache.dtype:
+    dtype = k_cache.dtype
+    if dtype is not v_cache.dtype:
         raise KDAError("k_cache and v_cache must have the same dtype")
-    n, h, ps, _ = k_cache.shape
-    for t in (k_cache, v_cache):
-        if not t.is_cuda or t.device != x.device:
-            raise KDAError("the caches must be CUDA tensors on the inputs' device")
-        if (n and h and ps) and t[0].is_contiguous() is False:
+    if dtype not in _CACHE_CODE:
+        raise KDAError(f"unsupported cache dtype {dtype}: bfloat16, float32 or float8_e4m3fn")
+    if k_cache.get_device() != index or v_cache.get_device() != index:
+        raise KDAError("the caches must be CUDA tensors on the inputs' device")
+    n, h, ps, _ = shape
+    if k_cache.is_contiguous() and v_cache.is_contiguous():
+        stride = h * ps * D
+    else:
+        a, b = k_cache.stride(), v_cache.stride()
+        if a[1:] != (ps * D, D, 1) or b[1:] != a[1:]:
             raise KDAError("each page of a cache must be contiguous (pages may lie apart)")
-    stride = k_cache.stride(0) if n > 1 else max(k_cache.stride(0), h * ps * D)
-    if n > 1 and v_cache.stride(0) != stride:
-        raise KDAError("k_cache and v_cache must have the same page stride")
-    scales = (k_scale, v_scale)
-    if (k_cache.dtype == torch.float8_e4m3fn) != all(s is not None for s in scales) or (k_scale is None) != (v_scale is None):
-        raise KDAError("an e4m3 cache takes k_scale and v_scale, other caches none")
-    for s in scales:
-        if s is not None and (s.dtype != torch.float32 or tuple(s.shape) != (h,)):
-            raise KDAError("k_scale and v_scale must be float32 [kv heads]")
-    return n, h, ps, stride
+        if n > 1 and a[0] != b[0]:
+            raise KDAError("k_cache and v_cache must have the same page stride")
+        stride = a[0] if n > 1 else max(a[0], h * ps * D)
+    if dtype is _E4M3:
+        if k_scale is None or v_scale is None:
+            raise KDAError("an e4m3 cache takes k_scale and v_scale")
+        _typed(_F32, "k_scale v_scale", k_scale, v_scale)
+        if k_scale.numel() != h or v_scale.numel() != h:
+            raise KDAError("k_scale and v_scale must be [kv heads]")
+    elif k_scale is not None or v_scale is not None:
+        raise KDAError("k_scale and v_scale belong to an e4m3 cache")
+    return n, h, ps, stride, _CACHE_CODE[dtype]
 
 
 def paged_tables(new_len, ctx_len, block_table, free_pages, free_head, T_total, page_size, n_pages, error_word=None):
@@ -91,24 +111,25 @@ def paged_tables(new_len, ctx_len, block_table, free_pages, free_head, T_total, 
     place.  new_len, ctx_len int32 [n]; free_pages int32 [n_free]; free_head int32 [1].
     Returns (slot_map int64 [T], positions int32 [T], cu_q int32 [n + 1], kv_len
     int32 [n], free_head_next int32 [1])."""
-    lib = _lib()
-    _on_device(new_len, ctx_len, block_table, free_pages, free_head, error_word)
-    _typed(torch.int32, new_len=new_len, ctx_len=ctx_len, block_table=block_table, free_pages=free_pages,
-           free_head=free_head, error_word=error_word)
+    lib = _declared or _lib()
+    index = _on_device(new_len, ctx_len, block_table, free_pages, free_head, error_word)
+    _typed(_I32, "new_len ctx_len block_table free_pages free_head error_word", new_len, ctx_len, block_table, free_pages,
+           free_head, error_word)
     n = new_len.numel()
     if ctx_len.numel() != n or block_table.dim() != 2 or block_table.shape[0] != n or free_head.numel() != 1:
         raise KDAError("new_len and ctx_len must be [n], block_table [n, max_blocks], free_head [1]")
-    dev = new_len.device
     T = int(T_total)
-    slot_map = torch.empty(max(T, 0), dtype=torch.int64, device=dev)
-    # one allocation for the int32 outputs; positions first (16-byte aligned)
-    pad = (max(T, 0) + 3) // 4 * 4
-    ints = torch.empty(pad + 2 * n + 2, dtype=torch.int32, device=dev)
-    positions, cu_q, kv_len, head = ints[:max(T, 0)], ints[pad:pad + n + 1], ints[pad + n + 1:pad + 2 * n + 1], ints[pad + 2 * n + 1:]
-    rc = lib.kda_paged_tables(_p(new_len), _p(ctx_len), n, T, _p(block_table), block_table.shape[1], _p(free_pages),
-                              free_pages.numel(), _p(free_head), _p(head), int(page_size), int(n_pages), _p(slot_map),
-                              _p(positions), _p(cu_q), _p(kv_len), _p(error_word), _stream(dev))
-    _check(rc, "kda_paged_tables")
+    if T < 0:
+        raise KDAError("T_total must not be negative")
+    new = new_len.new_empty
+    slot_map = new(T, dtype=_I64)
+    positions, cu_q, kv_len, head = new(T), new(n + 1), new(n), new(1)
+    rc = lib.kda_paged_tables(new_len.data_ptr(), ctx_len.data_ptr(), n, T, block_table.data_ptr(), block_table.shape[1],
+                              free_pages.data_ptr(), free_pages.numel(), free_head.data_ptr(), head.data_ptr(), page_size,
+                              n_pages, slot_map.data_ptr(), positions.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(),
+                              _p(error_word), _raw_stream(index))
+    if rc:
+        _check(rc, "kda_paged_tables")
     return slot_map, positions, cu_q, kv_len, head
 
 
@@ -116,22 +137,28 @@ def paged_append(k, v, slot_map, k_cache, v_cache, k_scale=None, v_scale=None, e
     """kda_paged_append: k, v [T, Hkv, 128] into the caches [pages, Hkv, page size,
     128] at slot_map int64 [T] (negative: skipped).  An e4m3 cache takes k_scale and
     v_scale float32 [Hkv]."""
-    lib = _lib()
-    _on_device(k, v, slot_map, k_scale, v_scale, error_word)
-    _typed(torch.int64, slot_map=slot_map)
-    _typed(torch.int32, error_word=error_word)
-    n, h, ps, stride = _cache(k, k_cache, v_cache, k_scale, v_scale)
-    if k.dim() != 3 or k.shape != v.shape or k.dtype != v.dtype or tuple(k.shape[1:]) != (h, D):
-        raise KDAError("k and v must both be [T, kv heads, 128]")
-    if slot_map.numel() != k.shape[0]:
+    lib = _declared or _lib()
+    index = _on_device(k, v, slot_map, k_scale, v_scale, error_word)
+    n, h, ps, stride, code = _cache(index, k_cache, v_cache, k_scale, v_scale)
+    _typed(_I64, "slot_map", slot_map)
+    _typed(_I32, "error_word", error_word)
+    shape = k.shape
+    if len(shape) != 3 or shape[1] != h or shape[2] != D or v.shape != shape or k.dtype is not v.dtype:
+        raise KDAError("k and v must both be [T, kv heads, 128], of one dtype")
+    if k.dtype not in _CODE:
+        raise KDAError(f"unsupported dtype {k.dtype}: k and v must be bfloat16 or float32")
+    T = shape[0]
+    if slot_map.numel() != T:
         raise KDAError("slot_map must be [T]")
-    rc = lib.kda_paged_append(_p(k), _p(v), _p(slot_map), k.shape[0], h, D, _dtype_code(k), _cache_code(k_cache),
-                              _p(k_scale), _p(v_scale), _p(k_cache), _p(v_cache), n, ps, stride, _p(error_word),
-                              _stream(k.device))
-    _check(rc, "kda_paged_append")
+    rc = lib.kda_paged_append(k.data_ptr(), v.data_ptr(), slot_map.data_ptr(), T, h, D, _CODE[k.dtype], code, _p(k_scale),
+                              _p(v_scale), k_cache.data_ptr(), v_cache.data_ptr(), n, ps, stride, _p(error_word),
+                              _raw_stream(index))
+    if rc:
+        _check(rc, "kda_paged_append")
 
 
 def paged_attn_workspace_size(T_total: int, n_seqs: int, Hq: int, Hkv: int) -> int:
+    """Bytes of workspace that paged_attn needs (0 for shapes it does not take)."""
     return int(_lib().kda_paged_attn_workspace_size(T_total, n_seqs, Hq, Hkv))
 
 
@@ -141,29 +168,33 @@ def paged_attn(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q=0, sm_scale
     through block_table int32 [n, max_blocks]; cu_q int32 [n + 1] and kv_len int32 [n]
     as paged_tables gives them.  max_q: the most new tokens of one request (0: not
     known).  Returns (o in q's dtype, lse float32 [T, Hq])."""
-    lib = _lib()
-    _on_device(q, block_table, cu_q, kv_len, k_scale, v_scale, out, lse, workspace, error_word)
-    _typed(torch.int32, block_table=block_table, cu_q=cu_q, kv_len=kv_len, error_word=error_word)
-    _typed(torch.float32, lse=lse)
-    n_pages, hkv, ps, stride = _cache(q, k_cache, v_cache, k_scale, v_scale)
-    if q.dim() != 3 or q.shape[2] != D:
+    lib = _declared or _lib()
+    index = _on_device(q, block_table, cu_q, kv_len, k_scale, v_scale, out, lse, workspace, error_word)
+    n_pages, hkv, ps, stride, code = _cache(index, k_cache, v_cache, k_scale, v_scale)
+    _typed(_I32, "block_table cu_q kv_len error_word", block_table, cu_q, kv_len, error_word)
+    shape, dtype = q.shape, q.dtype
+    if len(shape) != 3 or shape[2] != D:
         raise KDAError("q must be [T, heads, 128]")
-    T, hq, _ = q.shape
+    if dtype not in _CODE:
+        raise KDAError(f"unsupported dtype {dtype}: q must be bfloat16 or float32")
+    T, hq, _ = shape
     n = kv_len.numel()
     if cu_q.numel() != n + 1 or block_table.dim() != 2 or block_table.shape[0] != n:
         raise KDAError("cu_q must be [n + 1], kv_len [n] and block_table [n, max_blocks]")
-    o = out if out is not None else torch.empty_like(q)
-    if o.shape != q.shape or o.dtype != q.dtype:
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != shape or out.dtype is not dtype:
         raise KDAError("out must have q's shape and dtype")
     if lse is None:
-        lse = torch.empty((T, hq), dtype=torch.float32, device=q.device)
-    elif tuple(lse.shape) != (T, hq):
-        raise KDAError("lse must be [T, heads]")
+        lse = q.new_empty(T, hq, dtype=_F32)
+    elif lse.shape != shape[:2] or lse.dtype is not _F32:
+        raise KDAError("lse must be float32 [T, heads]")
     if workspace is None:
-        workspace = torch.empty(lib.kda_paged_attn_workspace_size(T, n, hq, hkv), dtype=torch.uint8, device=q.device)
-    rc = lib.kda_paged_attn(_p(q), _p(k_cache), _p(v_cache), _p(block_table), _p(cu_q), _p(kv_len), n, T, int(max_q), hq,
-                            hkv, D, _dtype_code(q), _cache_code(k_cache), _p(k_scale), _p(v_scale), n_pages, ps, stride,
-                            block_table.shape[1], float(sm_scale), int(window), _p(o), _p(lse), _p(workspace),
-                            workspace.numel() * workspace.element_size(), _p(error_word), _stream(q.device))
-    _check(rc, "kda_paged_attn")
-    return o, lse
+        workspace = q.new_empty(lib.kda_paged_attn_workspace_size(T, n, hq, hkv), dtype=torch.uint8)
+    rc = lib.kda_paged_attn(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), cu_q.data_ptr(),
+                            kv_len.data_ptr(), n, T, max_q, hq, hkv, D, _CODE[dtype], code, _p(k_scale), _p(v_scale), n_pages,
+                            ps, stride, block_table.shape[1], sm_scale, window, out.data_ptr(), lse.data_ptr(),
+                            workspace.data_ptr(), workspace.nbytes, _p(error_word), _raw_stream(index))
+    if rc:
+        _check(rc, "kda_paged_attn")
+    return out, lse
