@@ -18,8 +18,11 @@
 //         bf16 (2^-9 relative each, averaging out below the output's rounding)
 //   e4m3  widened to fp16 in registers, which is exact; q is scaled by a power
 //         of two per row so that fp16 holds it as precisely as bf16 did
-//   fp32  each operand as two tf32 parts, three products (what is dropped is
-//         2^-22 of a term)
+//   fp32  plain fp32 multiply-adds: tf32 parts would lose digits that the fp32
+//         path of this library keeps (three products of two parts each left 2.5e-6
+//         where this leaves 4e-7), and with up to 16 rows a warp the memory's time
+//         covers them.  A lane holds half a key's channels for the scores and four
+//         channels of all keys for the output
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -35,6 +38,7 @@ constexpr int STAGES = 5;
 constexpr int HALF = 8192;                   // bytes of K (and of V) of one tile
 constexpr int STAGE = 2 * HALF;
 constexpr int OFF_RED = STAGES * STAGE;      // [4][16][128] fp32
+constexpr int OFF_P = (STAGES - 1) * STAGE;    // fp32: probabilities [4][16][16], in place of the last stage
 constexpr int OFF_ML = OFF_RED + CONS * 16 * D * 4;
 constexpr int OFF_DESC = OFF_ML + CONS * 16 * 8;
 constexpr int OFF_BAR = OFF_DESC + STAGES * 64;
@@ -45,9 +49,9 @@ static_assert(OFF_RED % 1024 == 0 && OFF_ML % 16 == 0 && OFF_DESC % 16 == 0 && O
 
 constexpr int BF16 = 0, E4M3 = 1, F32 = 2;   // kinds
 template <int KIND> struct Kind;
-template <> struct Kind<BF16> { static constexpr int TK = 32, ES = 2; };
-template <> struct Kind<E4M3> { static constexpr int TK = 64, ES = 1; };
-template <> struct Kind<F32> { static constexpr int TK = 16, ES = 4; };
+template <> struct Kind<BF16> { static constexpr int TK = 32, ES = 2, NST = STAGES; };
+template <> struct Kind<E4M3> { static constexpr int TK = 64, ES = 1, NST = STAGES; };
+template <> struct Kind<F32> { static constexpr int TK = 16, ES = 4, NST = STAGES - 1; };
 
 // what the producer says about a tile
 struct __align__(16) Desc {
@@ -75,7 +79,7 @@ __device__ __forceinline__ int64_t line_tiles(const PagedAttn &a, int i, int *er
 template <int KIND>
 __device__ __forceinline__ void produce(const PagedAttn &a, const PagedMaps &maps, uint8_t *sm, int64_t P0, int64_t P1,
                                         int64_t per, int req, int64_t before) {
-    constexpr int TK = Kind<KIND>::TK, ES = Kind<KIND>::ES, NSUB = D * ES / 128;
+    constexpr int TK = Kind<KIND>::TK, ES = Kind<KIND>::ES, NSUB = D * ES / 128, NST = Kind<KIND>::NST;
     const int lane = threadIdx.x & 31;
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + OFF_BAR), *empty = full + STAGES;
     volatile int *abort = reinterpret_cast<volatile int *>(sm + OFF_ABORT);
@@ -88,9 +92,9 @@ __device__ __forceinline__ void produce(const PagedAttn &a, const PagedMaps &map
                 *abort = 1;
                 if (a.err) atomicOr(a.err, KDA_DEVERR_TIMEOUT);
                 // let the copies in flight land before the block ends
-                for (int i = 1; i <= STAGES && i <= issued; ++i) {
+                for (int i = 1; i <= NST && i <= issued; ++i) {
                     const int u = issued - i;
-                    mbar_wait(&full[u % STAGES], (u / STAGES) & 1);
+                    mbar_wait(&full[u % NST], (u / NST) & 1);
                 }
             }
             __syncwarp();
@@ -100,7 +104,7 @@ __device__ __forceinline__ void produce(const PagedAttn &a, const PagedMaps &map
         return true;
     };
     auto advance = [&]() {
-        if (++stage == STAGES) {
+        if (++stage == NST) {
             stage = 0;
             phase ^= 1;
         }
@@ -228,16 +232,6 @@ __device__ __forceinline__ void mma_h(float (&c)[4], const uint32_t (&x)[4], uin
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void mma_t(float (&c)[4], const uint32_t (&x)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void split_tf32(float x, uint32_t &hi, uint32_t &lo) {
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
-    lo = __float_as_uint(x - __uint_as_float(hi));
-    if ((hi & 0x7f800000u) == 0x7f800000u) lo = 0;  // inf, NaN: the first part carries them alone
 }
 __device__ __forceinline__ uint32_t pack_bf16(float x, float y) {
     const __nv_bfloat162 p = __floats2bfloat162_rn(x, y);
@@ -414,91 +408,222 @@ template <> struct Rows<E4M3> {
     static __device__ __forceinline__ void put(float *red, int g, int t, const float (&o)[16][4]) { put_relabelled(red, g, t, o); }
 };
 
-template <> struct Rows<F32> {
-    float q[16][4];
-    // k-steps 2 m, 2 m + 1 of thread t hold channels 4 (t + 4 m) + 0, 1 and + 2, 3
-    __device__ __forceinline__ void load(const void *p0, const void *p1, int t, float &f0, float &f1) {
-        const float4 *a = (const float4 *)p0, *b = (const float4 *)p1;
-        const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+// fp32: lane = (key lane % 16, half of the channels lane / 16) for the scores, four
+// channels for the output; maxima and sums of row r in lane r.
+struct RowsF32 {
+    float o[16][4], m, l;
+    __device__ __forceinline__ void tile(const float *q, float *ps, const uint8_t *k, const uint8_t *v, int lane, int R, float sc,
+                                         const Desc &d, int row0, int G, int window, bool mask) {
+        const int key = lane & 15, hf = lane >> 4;
+        float4 kr[16];
 #pragma unroll
-        for (int m = 0; m < 8; ++m) {
-            const float4 x = a ? a[t + 4 * m] : z, y = b ? b[t + 4 * m] : z;
-            q[2 * m][0] = x.x, q[2 * m][2] = x.y, q[2 * m + 1][0] = x.z, q[2 * m + 1][2] = x.w;
-            q[2 * m][1] = y.x, q[2 * m][3] = y.y, q[2 * m + 1][1] = y.z, q[2 * m + 1][3] = y.w;
+        for (int c = 0; c < 16; ++c) {
+            const int ch = 16 * hf + c;
+            kr[c] = *reinterpret_cast<const float4 *>(k + (ch >> 3) * 2048 + key * 128 + (((ch & 7) ^ (key & 7)) << 4));
         }
-        f0 = f1 = 1.f;
-    }
-    static __device__ __forceinline__ int key(int c) { return key_of_col(c); }
-    static __device__ __forceinline__ void mma3(float (&c)[4], const uint32_t (&xh)[4], const uint32_t (&xl)[4], float b0, float b1) {
-        uint32_t h0, l0, h1, l1;
-        split_tf32(b0, h0, l0);
-        split_tf32(b1, h1, l1);
-        mma_t(c, xl, h0, h1);
-        mma_t(c, xh, l0, l1);
-        mma_t(c, xh, h0, h1);
-    }
-    __device__ __forceinline__ void qk(const uint8_t *k, int lane, float (&s)[2][4]) {
-        const int g = lane >> 2, t = lane & 3;
+        float corr = 1.f;  // of row `lane`
+#pragma unroll 1
+        for (int r = 0; r < R; ++r) {
+            const float4 *qr = reinterpret_cast<const float4 *>(q + r * D) + 16 * hf;
+            float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+            for (int c = 0; c < 16; ++c) {
+                const float4 x = qr[c];
+                a0 = fmaf(x.x, kr[c].x, a0);
+                a1 = fmaf(x.y, kr[c].y, a1);
+                a2 = fmaf(x.z, kr[c].z, a2);
+                a3 = fmaf(x.w, kr[c].w, a3);
+            }
+            float s = (a0 + a1) + (a2 + a3);
+            s += __shfl_xor_sync(0xffffffffu, s, 16);
+            if (mask) {
+                const int pos = d.pos0 + (row0 + r) / G, at = d.key0 + key;
+                if (!(at <= pos && (window <= 0 || at > pos - window) && key < d.kvalid)) s = -INFINITY;
+            }
+            float top = s;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[j][e] = 0.f;
+            for (int x = 8; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+            const float old = __shfl_sync(0xffffffffu, m, r), mn = fmaxf(old, top * sc);
+            const float ref = mn == -INFINITY ? 0.f : mn;
+            if (lane == r) {
+                corr = ex2(m - ref);
+                m = mn;
+            }
+            const float p = ex2(fmaf(s, sc, -ref));
+            if (lane < 16) ps[r * 16 + lane] = p;
+        }
+        __syncwarp();
+        const bool moved = __any_sync(0xffffffffu, corr != 1.f);
+        l *= corr;
 #pragma unroll
-        for (int m = 0; m < 8; ++m) {
-            uint32_t xh[2][4], xl[2][4];
+        for (int r = 0; r < 16; ++r) {
+            if (r < R && moved) {
+                const float f = __shfl_sync(0xffffffffu, corr, r);
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) split_tf32(q[2 * m + u][e], xh[u][e], xl[u][e]);
-            const int ch = t + 4 * m;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int row = 8 * j + key_of_col(g);
-                const float4 w = *reinterpret_cast<const float4 *>(k + (ch >> 3) * 2048 + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
-                mma3(s[j], xh[0], xl[0], w.x, w.y);
-                mma3(s[j], xh[1], xl[1], w.z, w.w);
+                for (int e = 0; e < 4; ++e) o[r][e] *= f;
             }
         }
-    }
-    __device__ __forceinline__ void pv(const uint8_t *v, int lane, const float (&p)[2][4], float (&o)[16][4]) {
-        const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            // index t of the contraction is the key of column 2t, t + 4 that of column 2t + 1
-            uint32_t xh[4], xl[4];
-            split_tf32(p[ks][0], xh[0], xl[0]);
-            split_tf32(p[ks][2], xh[1], xl[1]);
-            split_tf32(p[ks][1], xh[2], xl[2]);
-            split_tf32(p[ks][3], xh[3], xl[3]);
-            const int ra = 8 * ks + key_of_col(2 * t), rb = 8 * ks + key_of_col(2 * t + 1);
+        for (int kk = 0; kk < 16; kk += 4) {
+            float4 vv[4];
 #pragma unroll
-            for (int jq = 0; jq < 4; ++jq) {
-                const float4 x = *reinterpret_cast<const float4 *>(v + jq * 2048 + ra * 128 + ((g ^ (ra & 7)) << 4));
-                const float4 y = *reinterpret_cast<const float4 *>(v + jq * 2048 + rb * 128 + ((g ^ (rb & 7)) << 4));
-                mma3(o[4 * jq], xh, xl, x.x, y.x);
-                mma3(o[4 * jq + 1], xh, xl, x.y, y.y);
-                mma3(o[4 * jq + 2], xh, xl, x.z, y.z);
-                mma3(o[4 * jq + 3], xh, xl, x.w, y.w);
+            for (int e = 0; e < 4; ++e)
+                vv[e] = *reinterpret_cast<const float4 *>(v + (lane >> 3) * 2048 + (kk + e) * 128 + (((lane & 7) ^ ((kk + e) & 7)) << 4));
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                if (r < R) {
+                    const float4 p = *reinterpret_cast<const float4 *>(ps + r * 16 + kk);
+                    o[r][0] = fmaf(p.w, vv[3].x, fmaf(p.z, vv[2].x, fmaf(p.y, vv[1].x, fmaf(p.x, vv[0].x, o[r][0]))));
+                    o[r][1] = fmaf(p.w, vv[3].y, fmaf(p.z, vv[2].y, fmaf(p.y, vv[1].y, fmaf(p.x, vv[0].y, o[r][1]))));
+                    o[r][2] = fmaf(p.w, vv[3].z, fmaf(p.z, vv[2].z, fmaf(p.y, vv[1].z, fmaf(p.x, vv[0].z, o[r][2]))));
+                    o[r][3] = fmaf(p.w, vv[3].w, fmaf(p.z, vv[2].w, fmaf(p.y, vv[1].w, fmaf(p.x, vv[0].w, o[r][3]))));
+                    const float sum = (p.x + p.y) + (p.z + p.w);
+                    if (lane == r) l += sum;
+                }
             }
         }
+        __syncwarp();  // (ps is written again at the next tile)
     }
-    static __device__ __forceinline__ void put(float *red, int g, int t, const float (&o)[16][4]) { put_relabelled(red, g, t, o); }
 };
 
 // ---------------------------------------------------------------- consumers
+// V rows past the keys may hold anything (0 x NaN is NaN): zero them.
+template <int KIND>
+__device__ __forceinline__ void zero_past(uint8_t *vt, int kvalid, int lane) {
+    constexpr int TK = Kind<KIND>::TK, NSUB = D * Kind<KIND>::ES / 128;
+    for (int x = lane; x < (TK - kvalid) * NSUB * 8; x += 32) {
+        const int row = kvalid + x / (NSUB * 8), c = x % (NSUB * 8);
+        *reinterpret_cast<uint4 *>(vt + (c >> 3) * TK * 128 + row * 128 + ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
+    }
+    fence_async_smem();
+    __syncwarp();
+}
+
+// A warp's 16 rows in mma.sync fragments (bf16, e4m3).
+template <int KIND> struct Work {
+    static constexpr int TK = Kind<KIND>::TK, NT = TK / 8;
+    Rows<KIND> rows;
+    float o[16][4], m[2], l[2], sc[2];
+    int last[2];  // position of the thread's two rows
+
+    __device__ __forceinline__ void begin(const PagedAttn &a, const Desc &d, int wrow, int lane, float *) {
+        const int g = lane >> 2, t = lane & 3;
+        const char *p[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = 16 * wrow + g + 8 * e, rr = d.r0 + r, j = rr / a.G;
+            last[e] = d.pos0 + j;
+            p[e] = r < d.R ? (const char *)a.q + ((int64_t)(d.tok0 + j) * a.Hq + d.h * a.G + (rr - j * a.G)) * D * 2 : nullptr;
+            m[e] = -INFINITY;
+            l[e] = 0.f;
+        }
+        rows.load(p[0], p[1], t, sc[0], sc[1]);
+        const float f = a.scale_log2 * (KIND == E4M3 ? a.k_scale[d.h] : 1.f);
+        sc[0] *= f;
+        sc[1] *= f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
+    }
+    __device__ __forceinline__ void tile(const PagedAttn &a, const Desc &d, int, int lane, const uint8_t *kt, const uint8_t *vt,
+                                         const float *, float *) {
+        const int t = lane & 3;
+        float s[NT][4];
+        rows.qk(kt, lane, s);
+        if (d.flags & MASK) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int at = 8 * j + Rows<KIND>::key(2 * t + (e & 1)), key = d.key0 + at, pos = last[e >> 1];
+                    const bool seen = key <= pos && (a.window <= 0 || key > pos - a.window) && at < d.kvalid;
+                    if (!seen) s[j][e] = -INFINITY;
+                }
+        }
+        float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top[e >> 1] = fmaxf(top[e >> 1], s[j][e]);
+        float ref[2], corr[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
+            top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
+            const float mn = fmaxf(m[e], top[e] * sc[e]);
+            ref[e] = mn == -INFINITY ? 0.f : mn;
+            corr[e] = ex2(m[e] - ref[e]);
+            m[e] = mn;
+            l[e] *= corr[e];
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s[j][e] = ex2(fmaf(s[j][e], sc[e >> 1], -ref[e >> 1]));
+                l[e >> 1] += s[j][e];
+            }
+        if (__any_sync(0xffffffffu, corr[0] != 1.f || corr[1] != 1.f)) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[j][e] *= corr[e >> 1];
+        }
+        rows.pv(vt, lane, s, o);
+    }
+    __device__ __forceinline__ void end(int lane, float *red, float2 *ml) {
+        const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+            if (t == 0) ml[g + 8 * e] = make_float2(m[e], l[e]);
+        }
+        Rows<KIND>::put(red, g, t, o);
+    }
+};
+template <> struct Work<F32> {
+    RowsF32 w;
+    __device__ __forceinline__ void begin(const PagedAttn &a, const Desc &d, int wrow, int lane, float *q) {
+        w.m = -INFINITY;
+        w.l = 0.f;
+        const int R = min(16, d.R - 16 * wrow);
+        for (int r = 0; r < R; ++r) {  // the queries stand where the output goes at the end
+            const int rr = d.r0 + 16 * wrow + r, j = rr / a.G;
+            const float4 *src = (const float4 *)a.q + ((int64_t)(d.tok0 + j) * a.Hq + d.h * a.G + (rr - j * a.G)) * (D / 4);
+            reinterpret_cast<float4 *>(q + r * D)[lane] = src[lane];
+        }
+        __syncwarp();
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w.o[r][e] = 0.f;
+    }
+    __device__ __forceinline__ void tile(const PagedAttn &a, const Desc &d, int wrow, int lane, const uint8_t *kt, const uint8_t *vt,
+                                         const float *q, float *ps) {
+        w.tile(q, ps, kt, vt, lane, min(16, d.R - 16 * wrow), a.scale_log2, d, d.r0 + 16 * wrow, a.G, a.window, d.flags & MASK);
+    }
+    __device__ __forceinline__ void end(int lane, float *red, float2 *ml) {
+        if (lane < 16) ml[lane] = make_float2(w.m, w.l);
+        __syncwarp();
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+            *reinterpret_cast<float4 *>(red + r * D + ((lane ^ (r & 7)) << 2)) = make_float4(w.o[r][0], w.o[r][1], w.o[r][2], w.o[r][3]);
+    }
+};
+
 template <int KIND>
 __device__ __forceinline__ void consume(const PagedAttn &a, uint8_t *sm) {
-    constexpr int TK = Kind<KIND>::TK, ES = Kind<KIND>::ES, NT = TK / 8, NSUB = D * ES / 128;
-    constexpr int QES = KIND == F32 ? 4 : 2;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    constexpr int TK = Kind<KIND>::TK, NST = Kind<KIND>::NST;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + OFF_BAR), *empty = full + STAGES;
     volatile int *abort = reinterpret_cast<volatile int *>(sm + OFF_ABORT);
-    float *red = reinterpret_cast<float *>(sm + OFF_RED);
+    float *red = reinterpret_cast<float *>(sm + OFF_RED), *mine = red + warp * 16 * D;
+    float *ps = reinterpret_cast<float *>(sm + OFF_P) + warp * 256;
     float2 *ml = reinterpret_cast<float2 *>(sm + OFF_ML);
 
-    Rows<KIND> rows;
-    float o[16][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, sc[2] = {0.f, 0.f};
-    int last[2] = {0, 0};  // position of the thread's two rows
+    Work<KIND> work;
     int stage = 0, phase = 0;
     uint64_t *meet = reinterpret_cast<uint64_t *>(sm + OFF_MEET);
     int meet_phase = 0;
@@ -523,101 +648,21 @@ __device__ __forceinline__ void consume(const PagedAttn &a, uint8_t *sm) {
         const Desc d = *reinterpret_cast<const Desc *>(sm + OFF_DESC + stage * 64);
         if (d.flags & END) break;
         const int wrow = warp % d.wr, wk = CONS / d.wr, wpart = warp / d.wr;
-        if (d.flags & FIRST) {
-            const char *p[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int r = 16 * wrow + g + 8 * e, rr = d.r0 + r, j = rr / a.G;
-                last[e] = d.pos0 + j;
-                p[e] = r < d.R ? (const char *)a.q + ((int64_t)(d.tok0 + j) * a.Hq + d.h * a.G + (rr - j * a.G)) * D * QES
-                               : nullptr;
-                m[e] = -INFINITY;
-                l[e] = 0.f;
-            }
-            rows.load(p[0], p[1], t, sc[0], sc[1]);
-            const float f = a.scale_log2 * (KIND == E4M3 ? a.k_scale[d.h] : 1.f);
-            sc[0] *= f;
-            sc[1] *= f;
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
-        }
+        if (d.flags & FIRST) work.begin(a, d, wrow, lane, mine);
         if (d.ord % wk == wpart && d.kvalid > 0) {
             uint8_t *kt = sm + stage * STAGE, *vt = kt + HALF;
-            float s[NT][4];
-            rows.qk(kt, lane, s);
-            float top[2] = {-INFINITY, -INFINITY};
-            if (d.flags & MASK) {
-                // what lies past the keys may be anything: zero V there (0 x NaN is NaN)
-                if (d.kvalid < TK) {
-                    const int dead = TK - d.kvalid;
-                    for (int x = lane; x < dead * NSUB * 8; x += 32) {
-                        const int row = d.kvalid + x / (NSUB * 8), c = x % (NSUB * 8);
-                        *reinterpret_cast<uint4 *>(vt + (c >> 3) * TK * 128 + row * 128 + ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
-                    }
-                    fence_async_smem();
-                    __syncwarp();
-                }
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int key = d.key0 + 8 * j + Rows<KIND>::key(2 * t + (e & 1)), pos = last[e >> 1];
-                        const bool seen = key <= pos && (a.window <= 0 || key > pos - a.window) && key < d.key0 + d.kvalid;
-                        s[j][e] = seen ? s[j][e] * sc[e >> 1] : -INFINITY;
-                    }
-            } else {
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) s[j][e] *= sc[e >> 1];
-            }
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) top[e >> 1] = fmaxf(top[e >> 1], s[j][e]);
-            float ref[2], corr[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
-                top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
-                const float mn = fmaxf(m[e], top[e]);
-                ref[e] = mn == -INFINITY ? 0.f : mn;
-                corr[e] = ex2(m[e] - ref[e]);
-                m[e] = mn;
-                l[e] *= corr[e];
-            }
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    s[j][e] = ex2(s[j][e] - ref[e >> 1]);
-                    l[e >> 1] += s[j][e];
-                }
-            if (__any_sync(0xffffffffu, corr[0] != 1.f || corr[1] != 1.f)) {
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[j][e] *= corr[e >> 1];
-            }
-            rows.pv(vt, lane, s, o);
+            if (d.kvalid < TK) zero_past<KIND>(vt, d.kvalid, lane);
+            work.tile(a, d, wrow, lane, kt, vt, mine, ps);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[stage]);
-        if (++stage == STAGES) {
+        if (++stage == NST) {
             stage = 0;
             phase ^= 1;
         }
         if (d.flags & LAST) {
             // merge the warps that share rows, in warp order
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
-                l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
-                if (t == 0) ml[warp * 16 + g + 8 * e] = make_float2(m[e], l[e]);
-            }
-            Rows<KIND>::put(red + warp * 16 * D, g, t, o);
+            work.end(lane, mine, ml + warp * 16);
             if (!meet_all()) break;
             float *slot = paged_slot(a, d.slot);
             const float vs = KIND == E4M3 ? a.v_scale[d.h] : 1.f;

@@ -121,9 +121,8 @@ def paged_tables(new_len, ctx_len, block_table, free_pages, free_head, T_total, 
     T = int(T_total)
     if T < 0:
         raise KDAError("T_total must not be negative")
-    new = new_len.new_empty
-    slot_map = new(T, dtype=_I64)
-    positions, cu_q, kv_len, head = new(T), new(n + 1), new(n), new(1)
+    slot_map = new_len.new_empty(T, dtype=_I64)
+    positions, cu_q, kv_len, head = new_len.new_empty(T + 2 * n + 2).split_with_sizes((T, n + 1, n, 1))
     rc = lib.kda_paged_tables(new_len.data_ptr(), ctx_len.data_ptr(), n, T, block_table.data_ptr(), block_table.shape[1],
                               free_pages.data_ptr(), free_pages.numel(), free_head.data_ptr(), head.data_ptr(), page_size,
                               n_pages, slot_map.data_ptr(), positions.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(),
