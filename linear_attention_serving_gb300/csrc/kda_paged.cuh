@@ -179,14 +179,18 @@ int make_paged_maps(const void *k, const void *v, int cache_dtype, int Hkv, int 
 
 int make_paged_q_map(const void *q, int64_t T, int Hq, int G, int tokens, CUtensorMap *out);
 
-constexpr int PAGED_ROWS_CAP = 64;   // rows of one item of the rows kernel
+constexpr int PAGED_ROWS_CAP = 64;   // rows of one item of the rows kernel (fp32) and of the few-rows kernel
 constexpr int PAGED_TILE_CAP = 256;  // and of the tile kernel
 
 int check_paged_cache(int Hkv, int Dm, int dtype, int cache_dtype, const float *k_scale, const float *v_scale,
                       const void *k_cache, const void *v_cache, int n_pages, int page_size, int64_t page_stride);
 int paged_rows_blocks();
+int paged_few_blocks();
 int paged_tile_blocks();
-int launch_paged_rows(const PagedAttn &a, int cache_dtype, const void *k, const void *v, int64_t page_stride, cudaStream_t s);
+int launch_paged_rows(PagedAttn a, const void *k, const void *v, int64_t page_stride, cudaStream_t s);
+// max_rows: the most rows that one of its requests can have
+int launch_paged_few(PagedAttn a, int cache_dtype, const void *k, const void *v, int64_t page_stride, int64_t max_rows,
+                     cudaStream_t s);
 // after_rows: the launch before it on the stream is the rows kernel of the same call (they may overlap)
 int launch_paged_tile(PagedAttn a, const void *k, const void *v, int64_t page_stride, bool after_rows, cudaStream_t s);
 

@@ -9,8 +9,8 @@ namespace kda {
 namespace {
 
 // ---------------------------------------------------------------- workspace
-// [leads][slots] of the rows kernel, then of the tile kernel: per block one lead
-// (two int4) and two slots
+// [leads][slots] of the kernel for few rows (or fp32), then of the tile kernel: per
+// block one lead (two int4) and two slots
 struct PagedSet {
     size_t off_lead, off_slots;
     int blocks, slot_rows;
@@ -35,7 +35,7 @@ PagedWs paged_ws(int64_t T, int Hq, int Hkv) {
     PagedWs w;
     const int64_t rows = T * (Hq / Hkv);
     w.total = 0;
-    w.rows = paged_set(w.total, paged_rows_blocks(), rows, PAGED_ROWS_CAP);
+    w.rows = paged_set(w.total, paged_rows_blocks(), rows, PAGED_ROWS_CAP);  // (the most blocks of the two)
     w.tile = paged_set(w.total, paged_tile_blocks(), rows, PAGED_TILE_CAP);
     return w;
 }
@@ -135,10 +135,6 @@ int launch_join(const PagedAttn &a, const JoinSet &s0, const JoinSet &s1, int64_
     return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
-// The most rows (new tokens x heads of a kv head) of a request that the rows
-// kernel takes when the tile kernel could.
-constexpr int ROWS_MAX = 16;
-
 }  // namespace
 }  // namespace kda
 
@@ -197,28 +193,39 @@ int kda_paged_attn(const void *q, const void *k_cache, const void *v_cache, cons
     a.scale_log2 = sm_scale * 1.4426950408889634f;
     char *ws = (char *)workspace;
     const int64_t max_rows = (int64_t)a.max_q * a.G;
-    const bool tiles = cache_dtype == KDA_BF16 && a.G <= 128 && max_rows > ROWS_MAX;
+    JoinSet js[2] = {{nullptr, nullptr, 0, 1}, {nullptr, nullptr, 0, 1}};
+    auto use = [&](const PagedSet &p, int blocks) {
+        a.lead = (int4 *)(ws + p.off_lead);
+        a.parts = (float *)(ws + p.off_slots);
+        a.slot_rows = p.slot_rows;
+        return JoinSet{a.lead, a.parts, blocks, p.slot_rows};
+    };
+    a.row_lo = 0;
+    a.row_hi = INT32_MAX;
+    if (dtype == KDA_F32) {
+        js[0] = use(w.rows, paged_rows_blocks());
+        if ((rc = launch_paged_rows(a, k_cache, v_cache, page_stride, s))) return rc;
+        return launch_join(a, js[0], js[1], max_rows, true, s);
+    }
+    // Up to 64 rows of a kv head fit the few-rows kernel at once.  With longer
+    // requests in the call, the tile kernel takes them, and the few-rows kernel the
+    // single tokens (rows up to the next of 16, 32, 64 from G on); requests in between
+    // are the tile kernel's too, which has room for 128 rows at one cost.
+    const bool tiles = cache_dtype == KDA_BF16 && a.G <= 128 && max_rows > PAGED_ROWS_CAP;
+    const int few_rows = a.G <= 16 ? 16 : a.G <= 32 ? 32 : 64;
     // every request long enough for the tile kernel: one of T_total tokens, or all
     // of max_q (the offsets may still say less: the tile kernel then takes that too)
-    const bool rows = !tiles || !(n_seqs == 1 || T_total == (int64_t)n_seqs * a.max_q);
-    JoinSet js[2] = {{nullptr, nullptr, 0, 1}, {nullptr, nullptr, 0, 1}};
-    if (rows) {
-        a.row_lo = 0;
-        a.row_hi = tiles ? ROWS_MAX : INT32_MAX;
-        a.lead = (int4 *)(ws + w.rows.off_lead);
-        a.parts = (float *)(ws + w.rows.off_slots);
-        a.slot_rows = w.rows.slot_rows;
-        js[0] = JoinSet{a.lead, a.parts, w.rows.blocks, a.slot_rows};
-        if ((rc = launch_paged_rows(a, cache_dtype, k_cache, v_cache, page_stride, s))) return rc;
+    const bool few = !tiles || (a.G <= PAGED_ROWS_CAP && n_seqs > 1 && T_total != (int64_t)n_seqs * a.max_q);
+    if (few) {
+        if (tiles) a.row_hi = few_rows;
+        js[0] = use(w.rows, paged_few_blocks());
+        if ((rc = launch_paged_few(a, cache_dtype, k_cache, v_cache, page_stride, tiles ? few_rows : max_rows, s))) return rc;
     }
     if (tiles) {
-        a.row_lo = rows ? ROWS_MAX : 0;
+        a.row_lo = few ? few_rows : 0;
         a.row_hi = INT32_MAX;
-        a.lead = (int4 *)(ws + w.tile.off_lead);
-        a.parts = (float *)(ws + w.tile.off_slots);
-        a.slot_rows = w.tile.slot_rows;
-        js[1] = JoinSet{a.lead, a.parts, w.tile.blocks, a.slot_rows};
-        if ((rc = launch_paged_tile(a, k_cache, v_cache, page_stride, rows, s))) return rc;
+        js[1] = use(w.tile, paged_tile_blocks());
+        if ((rc = launch_paged_tile(a, k_cache, v_cache, page_stride, few, s))) return rc;
     }
     return launch_join(a, js[0], js[1], max_rows, dtype == KDA_F32, s);
 }

@@ -21,13 +21,13 @@
 // has grown by more than 2^8: until then probabilities up to 256 are as precise
 // in bf16 and the sums stay in fp32, and O needs no rescaling (which would mean
 // reading and writing 128 columns of TMEM between two products).
-#include "kda_paged.cuh"
+#include "kda_paged_tc.cuh"
 
 namespace kda {
 namespace {
 using namespace tc;
 
-constexpr int BK = 128;                        // keys per tile
+constexpr int BK = KEY_TILE;                   // keys per tile
 constexpr int BM = 128;                        // rows per half
 constexpr int SLOTS = 5;                       // ring of K / V tiles
 constexpr int SLOT = BK * D * 2;               // 32 KB: two 64-channel blocks of 128 rows x 128 B
@@ -74,32 +74,6 @@ struct Bars {
     }
 };
 
-// sum_{i < n} floor((a i + b) / m) for a, b >= 0: whole parts of a / m and b / m
-// first; then, with K = floor((a (n - 1) + b) / m), counting the points below the
-// line by rows instead of columns gives
-//   K (n - 1) - sum_{j < K} floor((m j + m - b - 1) / a),
-// the same kind of sum on smaller numbers (Euclid's steps on a and m).
-// a (n - 1) + b < 2^32: key positions are below 2^31.
-__device__ __forceinline__ int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
-    int64_t s = 0, sign = 1;
-    while (n > 0) {
-        const uint32_t qa = a / m, qb = b / m;
-        s += sign * ((int64_t)qa * ((int64_t)n * (n - 1) / 2) + (int64_t)qb * n);
-        a -= qa * m;
-        b -= qb * m;
-        const uint32_t K = (a * (n - 1) + b) / m;
-        if (K == 0) break;
-        s += sign * ((int64_t)K * (n - 1));
-        sign = -sign;
-        b = m - b - 1;
-        n = K;
-        const uint32_t t = m;
-        m = a;
-        a = t;
-    }
-    return s;
-}
-
 // One request's row tiles: TT = 2 th tokens each (th = floor(128 / G)).
 struct TileReq {
     PagedReq r;
@@ -111,17 +85,6 @@ __device__ __forceinline__ TileReq tile_req(const PagedAttn &a, int i, int th, i
     q.n = q.r.rows / a.G;
     q.ng = (q.n + 2 * th - 1) / (2 * th);
     return q;
-}
-// Key tiles [t0, t1) of the tokens j0 .. j1 of a request (none: t1 = t0).
-__device__ __forceinline__ void key_tiles(const PagedAttn &a, const PagedReq &r, int j0, int j1, int &lo, int &hi, int &t0, int &t1) {
-    hi = r.pos0 + j1 + 1;
-    lo = a.window > 0 ? max(0, r.pos0 + j0 - a.window + 1) : 0;
-    if (hi <= 0) {
-        t0 = t1 = 0;
-        return;
-    }
-    t0 = lo / BK;
-    t1 = (hi + BK - 1) / BK;
 }
 // Length of an item in the line: first some units for what an item costs besides
 // its tiles (the first S, O on its way out: measured, 5 us where the tensor cores
@@ -272,81 +235,12 @@ __device__ __forceinline__ void issue_pv(uint32_t d, uint32_t p, uint64_t v, uin
         "r"(p), "l"(v), "r"(idesc), "r"((uint32_t)acc)
         : "memory");
 }
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *o) {
-    uint32_t r[32];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
-          "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]),
-          "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr));
-#pragma unroll
-    for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(r[i]);
-}
-// The loads above have arrived: nothing that uses the values moves before this.
-__device__ __forceinline__ void tmem_arrived(float *o) {
-    tmem_ld_wait();
-#pragma unroll
-    for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(o[i]));
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *o) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-        "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7]), "r"(o[8]), "r"(o[9]), "r"(o[10]),
-        "r"(o[11]), "r"(o[12]), "r"(o[13]), "r"(o[14]), "r"(o[15])
-        : "memory");
-}
-// two fp32 operations at once, and the largest of three
-__device__ __forceinline__ uint64_t pack2(float x, float y) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-    return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t r, float &x, float &y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(r)); }
-__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
-    return r;
-}
-__device__ __forceinline__ float max3(float x, float y, float z) {
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
-    return r;
-}
-// 32 bytes of one thread at once (dst 32-byte aligned)
-__device__ __forceinline__ void store32(void *dst, const uint32_t (&u)[8]) {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]),
-                 "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
-                 : "memory");
-}
-__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
 struct Shared {
     uint32_t tmem;
     int abort;
     int req, h, g;
     int pad;
     int64_t A;
-};
-
-struct Gate {  // bounded waits that stop the whole block when one runs out
-    volatile int *abort;
-    int32_t *err;
-    __device__ bool operator()(uint64_t *bar, int parity) const {
-        const bool ok = __all_sync(0xffffffffu, mbar_wait_ab(bar, parity, abort));
-        if (!ok && (threadIdx.x & 31) == 0) {
-            *abort = 1;
-            if (err) atomicOr(err, KDA_DEVERR_TIMEOUT);
-        }
-        return ok;
-    }
 };
 
 // One warp walks the line ahead of the others, and has each segment's queries
@@ -603,16 +497,6 @@ __device__ __forceinline__ void store_f32(float *dst, const float (&o)[32]) {
     }
 }
 
-// How many of the two warps' threads say so (a barrier of the two).
-__device__ __forceinline__ int pair_count(int id, bool pred) {
-    int n;
-    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %1, 0;\n barrier.red.popc.u32 %0, %2, 64, p;\n}\n"
-                 : "=r"(n)
-                 : "r"((uint32_t)pred), "r"(id)
-                 : "memory");
-    return n;
-}
-
 // The segment's end of one group: half of O's channels, normalised or as a piece.
 __device__ __forceinline__ void finish(const PagedAttn &a, uint32_t to, int th, const volatile Seg *s, int x, int hf, int row,
                                        float ref, float l) {
@@ -666,7 +550,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
     bool failed = false;
     for (int iseg = 0;; ++iseg) {
         if (!gate(&bar.seg_full[iseg % SEGS], (iseg / SEGS) & 1)) {
-            pair_count(id, true);
+            meet_count<64>(id, true);
             return;
         }
         const Seg *seg = reinterpret_cast<const Seg *>(sm + OFF_SEG + (iseg % SEGS) * 64);
@@ -674,7 +558,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
             int lo, hi, t0, nt;
         } s{seg->lo, seg->hi, seg->t0, seg->nt};
         if (s.nt < 0) {
-            pair_count(id, false);
+            meet_count<64>(id, false);
             return;
         }
         const bool alt = seg->alt;
@@ -715,11 +599,11 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
             // Meet: both have read S, whose columns P overwrites from here on; and does
             // ref have to follow?  (a warp that gave up counts 32, one that asks for it 1)
             const bool grow = __any_sync(0xffffffffu, !prev || mt > (top == -INFINITY ? -INFINITY : ref + GROW));
-            const int said = pair_count(id, failed || (grow && lane == 0));
+            const int said = meet_count<64>(id, failed || (grow && lane == 0));
             if (said >= 32) return;
             if (said) {
                 mx[BM * hf] = mt;
-                pair_count(id, false);
+                meet_count<64>(id, false);
                 const float both = fmaxf(fmaxf(mt, mx[BM * (1 - hf)]), top);
                 const float nref = both == -INFINITY ? 0.f : top == -INFINITY ? both : fmaxf(both, ref);
                 const float corr = top == -INFINITY ? 0.f : ex2(ref - nref);  // (nothing summed yet: what O holds is zero)
@@ -795,7 +679,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
                 if (!gate(prev, prevp)) failed = true;
                 tc_fence_after();
                 mx[BM * hf] = l;  // (both are past the maxima that stood there: P V has been)
-                if (pair_count(id, failed) >= 32) return;
+                if (meet_count<64>(id, failed) >= 32) return;
                 sum = mx[0] + mx[BM];
             }
             finish(a, to, th, seg, x, hf, row, ref, sum);
