@@ -11,16 +11,18 @@
 //   P^T = exp2(S^T scale - ref): thread = key, NR values, stored as the [key][row]
 //         operand of the second product (bf16; fp16 for e4m3 caches)
 //   O^T += V^T P^T 128 channels x NR fp32 in TMEM, V from shared memory as loaded
-// Products of S run two tiles ahead of those of O, across items.
+// Products of S, issued by one warp, run up to two tiles ahead of those of O, issued by
+// another, across items (one warp for both took 1,900 cycles a tile: too long for e4m3).
 //
 // `ref` follows a row's maximum only when that has grown by more than 2^8 (kept
 // probabilities are then as precise in 16 bits, sums are fp32): most tiles need no
 // maximum over their keys at all, which would go across lanes, and no rescaling; one
 // barrier tells the four softmax warps whether any of them saw such growth.
 //
-// e4m3 caches: the copies bring 16 KB tiles, eight warps widen them to fp16, which is
-// exact, into the operands' buffers; q is scaled by a power of two per row so that
-// fp16 holds it as precisely as bf16 did.
+// e4m3 caches: S^T multiplies K as it was loaded (8-bit products) by two e4m3 parts of
+// q, which hold a bf16 value's eight bits; V is widened to fp16, which is exact, by
+// four warps beside the copies (K too would be too much: the conversions run at 16 a
+// cycle and SM, some 500 cycles a tile).
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -36,22 +38,27 @@ constexpr int RAW = BK * D;            // an e4m3 tile as loaded
 constexpr int SEGS = 4;                // segments ahead of the roles
 constexpr int HEAD = 1;                // an item's cost besides its tiles, in tiles
 constexpr float GROW = 8.f, NOTHING = -1e30f;
-constexpr int SOFT = 4;                // softmax warps (0..3), then products, loads, walk, idle, and the widening warps
-constexpr int W_MMA = 4, W_LOAD = 5, W_WALK = 6, W_WIDEN = 8, WIDEN = 8;
+constexpr int WIDEN = 4;                // warps that widen V
 
-// Buffers: K and V operand tiles, raw e4m3 tiles.
+// Warps: the softmax groups of four warps (each up to 32 rows), then one for the
+// products of S, loads, the walk, the products of O, and those that widen V.
+// Buffers: K tiles (e4m3: as loaded), V operand tiles, e4m3 V tiles as loaded.
 template <bool E4, int NR> struct Cfg {
-    static constexpr int KS = E4 ? 1 : NR == 64 ? 2 : 3, VS = E4 ? 2 : 3, RS = E4 ? (NR == 64 ? 4 : NR == 32 ? 6 : 7) : 0;
+    static constexpr int GR = NR == 64 ? 32 : NR, GROUPS = NR / GR, SOFT = 4 * GROUPS;
+    static constexpr int W_S = SOFT, W_LOAD = SOFT + 1, W_WALK = SOFT + 2, W_O = SOFT + 3, W_WIDEN = SOFT + 4;
+    static constexpr int KT = E4 ? RAW : TILE;  // bytes of a K tile
+    static constexpr int KS = E4 ? (NR == 64 ? 3 : NR == 32 ? 4 : 5) : NR == 64 ? 2 : 3, VS = E4 ? 2 : 3,
+                         RS = E4 ? (NR == 64 ? 3 : 4) : 0;
     static constexpr int PB = BK * NR * 2, QB = NR * D * 2;
-    static constexpr int OFF_K = 0, OFF_V = OFF_K + KS * TILE, OFF_R = OFF_V + VS * TILE, OFF_Q = OFF_R + RS * RAW,
+    static constexpr int OFF_K = 0, OFF_V = OFF_K + KS * KT, OFF_R = OFF_V + VS * TILE, OFF_Q = OFF_R + RS * RAW,
                          OFF_P = OFF_Q + 2 * QB, OFF_REF = OFF_P + 2 * PB, OFF_CORR = OFF_REF + NR * 4,
                          OFF_SC = OFF_CORR + NR * 4, OFF_SEG = OFF_SC + SEGS * NR * 4, OFF_DESC = OFF_SEG + SEGS * 64,
-                         OFF_BAR = OFF_DESC + 128;
-    static constexpr int NBAR = 2 * (KS + VS + RS) + 4 + 8 + 1 + 2 * SEGS;
+                         OFF_BAR = OFF_DESC + 32;
+    static constexpr int NBAR = 2 * (KS + VS + RS) + 4 + 8 + 2 + 2 * SEGS;
     static constexpr int OFF_MISC = (OFF_BAR + NBAR * 8 + 15) / 16 * 16, SMEM = OFF_MISC + 64;
     static constexpr int THREADS = (W_WIDEN + (E4 ? WIDEN : 0)) * 32;
     static constexpr int TCOLS = 4 * NR;
-    static_assert(SMEM <= 232448 && OFF_SEG % 16 == 0 && OFF_BAR % 8 == 0, "shared memory layout");
+    static_assert(SMEM <= 232448 && OFF_SEG % 16 == 0 && OFF_BAR % 8 == 0 && RS <= 8 && OFF_V % 1024 == 0, "shared memory layout");
 };
 
 template <class C> struct Bars {
@@ -62,7 +69,7 @@ template <class C> struct Bars {
         k_empty = k_full + C::KS;
         v_full = k_empty + C::KS;
         v_empty = v_full + C::VS;
-        r_full = v_empty + C::VS;
+        r_full = v_empty + C::VS;  // V tiles as loaded
         r_empty = r_full + C::RS;
         q_full = r_empty + C::RS;  // [2] by item
         q_empty = q_full + 2;
@@ -71,7 +78,7 @@ template <class C> struct Bars {
         pv_done = p_ready + 2;
         o_free = pv_done + 2;      // [2] by item
         last = o_free + 2;
-        seg_full = last + 1;
+        seg_full = last + 2;       // (last: products in flight when a wait ran out)
         seg_empty = seg_full + SEGS;
     }
 };
@@ -243,24 +250,51 @@ __device__ __forceinline__ void walk_role(const PagedAttn &a, uint8_t *sm, Walk 
                     v = __ldg((const uint4 *)a.q + ((int64_t)(s.tok + j) * a.Hq + s.h * a.G + (rr - j * a.G)) * (D / 8) + c);
                 }
                 if (E4) {
-                    uint32_t u[4] = {v.x, v.y, v.z, v.w};
-                    float top = 0.f;
+                    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+                    float y[8], top = 0.f;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) top = fmaxf(top, fmaxf(fabsf(bf_lo(u[k])), fabsf(bf_hi(u[k]))));
+                    for (int k = 0; k < 4; ++k) {
+                        y[2 * k] = bf_lo(u[k]);
+                        y[2 * k + 1] = bf_hi(u[k]);
+                        // (e4m3 has no infinity: NaN says that there is no answer)
+                        if (fabsf(y[2 * k]) == INFINITY) y[2 * k] = NAN;
+                        if (fabsf(y[2 * k + 1]) == INFINITY) y[2 * k + 1] = NAN;
+                        top = fmaxf(top, fmaxf(fabsf(y[2 * k]), fabsf(y[2 * k + 1])));
+                    }
 #pragma unroll
                     for (int o = 8; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    // 2^-e with e the exponent of the row's largest value (none for 0, inf and the ends of the range)
+                    // the row's largest value goes to 128 .. 256 (not for 0, inf and the ends of the
+                    // range): parts of 2^-9 and more are then exact for values over 2^-9 of it
                     const int e = (int)(__float_as_uint(top) >> 23) - 127;
-                    const bool ok = e > -120 && e < 120;
-                    const float down = ok ? __uint_as_float((uint32_t)(127 - e) << 23) : 1.f;
-                    if (c == 0) sc[r] = ks * (ok ? __uint_as_float((uint32_t)(127 + e) << 23) : 1.f);
+                    const bool ok = e > -110 && e < 110;
+                    const float down = ok ? __uint_as_float((uint32_t)(127 + 7 - e) << 23) : 1.f;
+                    if (c == 0) sc[r] = ks * (ok ? __uint_as_float((uint32_t)(127 + e - 7) << 23) : 1.f);
+                    uint32_t p1[2], p2[2];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) u[k] = pack_f16(bf_lo(u[k]) * down, bf_hi(u[k]) * down);
-                    v = make_uint4(u[0], u[1], u[2], u[3]);
-                } else if (c == 0) {
-                    sc[r] = ks;
+                    for (int k = 0; k < 2; ++k) {
+                        uint32_t a1 = 0, a2 = 0;
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {
+                            const float2 z = make_float2(y[4 * k + 2 * g] * down, y[4 * k + 2 * g + 1] * down);
+                            const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(z, __NV_SATFINITE, __NV_E4M3);
+                            const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(hi, __NV_E4M3);
+                            const float2 back = __half22float2(*reinterpret_cast<const __half2 *>(&hr));
+                            const __nv_fp8x2_storage_t lo =
+                                __nv_cvt_float2_to_fp8x2(make_float2(z.x - back.x, z.y - back.y), __NV_SATFINITE, __NV_E4M3);
+                            a1 |= (uint32_t)hi << (16 * g);
+                            a2 |= (uint32_t)lo << (16 * g);
+                        }
+                        p1[k] = a1;
+                        p2[k] = a2;
+                    }
+                    // two [row][channel] e4m3 operands, 128 bytes a row: this lane's 8 channels
+                    uint8_t *at = qb + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + 8 * (c & 1);
+                    *reinterpret_cast<uint2 *>(at) = make_uint2(p1[0], p1[1]);
+                    *reinterpret_cast<uint2 *>(at + NR * 128) = make_uint2(p2[0], p2[1]);
+                } else {
+                    if (c == 0) sc[r] = ks;
+                    *reinterpret_cast<uint4 *>(qb + (c >> 3) * NR * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
                 }
-                *reinterpret_cast<uint4 *>(qb + (c >> 3) * NR * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
             }
             fence_async_smem();
             __syncwarp();
@@ -277,23 +311,21 @@ __device__ __forceinline__ void walk_role(const PagedAttn &a, uint8_t *sm, Walk 
 
 // ---------------------------------------------------------------- loads
 // Tiles go in the order K0, K1, V0, K2, V1 .. through all items: K is used two tiles
-// before V is.  bf16: straight into the operands' buffers.  e4m3: into the ring of
-// raw tiles, with a word that says what it is.
+// before V is.  e4m3's V goes into a ring of its own, with a word that says which rows
+// hold keys.
 template <bool E4, int NR>
 __device__ __forceinline__ void load_role(const PagedAttn &a, const PagedMaps &maps, uint8_t *sm, const Gate &gate) {
     using C = Cfg<E4, NR>;
-    constexpr int ES = E4 ? 1 : 2, RING = E4 ? C::RS : 1;
+    constexpr int ES = E4 ? 1 : 2, NV = E4 ? C::RS : C::VS;
     const int lane = threadIdx.x & 31;
     const Bars<C> bar(sm);
     const int box = a.box, nbx = BK / box;
-    int nk = 0, nv = 0, nr = 0;  // tiles of K, V, raw so far
-    auto drain = [&]() {         // a wait ran out: let the copies in flight land before the block ends
-        if (E4) {
-            for (int u = nr - 1; u >= 0 && u >= nr - RING; --u) mbar_wait(&bar.r_full[u % RING], (u / RING) & 1);
-        } else {
-            for (int u = nk - 1; u >= 0 && u >= nk - C::KS; --u) mbar_wait(&bar.k_full[u % C::KS], (u / C::KS) & 1);
-            for (int u = nv - 1; u >= 0 && u >= nv - C::VS; --u) mbar_wait(&bar.v_full[u % C::VS], (u / C::VS) & 1);
-        }
+    uint64_t *vf = E4 ? bar.r_full : bar.v_full, *ve = E4 ? bar.r_empty : bar.v_empty;
+    uint8_t *kb = sm + C::OFF_K, *vb = sm + (E4 ? C::OFF_R : C::OFF_V);
+    int nk = 0, nv = 0;    // tiles of K and V so far
+    auto drain = [&]() {   // a wait ran out: let the copies in flight land before the block ends
+        for (int u = nk - 1; u >= 0 && u >= nk - C::KS; --u) mbar_wait(&bar.k_full[u % C::KS], (u / C::KS) & 1);
+        for (int u = nv - 1; u >= 0 && u >= nv - NV; --u) mbar_wait(&vf[u % NV], (u / NV) & 1);
         __syncwarp();
     };
     // boxes f .. e - 1 of a tile: this lane's page and row
@@ -301,28 +333,13 @@ __device__ __forceinline__ void load_role(const PagedAttn &a, const PagedMaps &m
         int f, e, page, y, z;  // z: first and one past the last row that holds a key (e4m3)
     };
     auto load = [&](const Tile &t, bool v) -> bool {
-        uint8_t *dst;
-        uint64_t *full;
-        if (E4) {
-            const int slot = nr % RING;
-            if (!gate(&bar.r_empty[slot], ((nr / RING) & 1) ^ 1)) return false;
-            dst = sm + C::OFF_R + slot * RAW;
-            full = &bar.r_full[slot];
-            if (lane == 0) reinterpret_cast<int *>(sm + C::OFF_DESC)[slot] = t.z | (v ? 1 << 16 : 0);
-            ++nr;
-        } else if (v) {
-            const int slot = nv % C::VS;
-            if (!gate(&bar.v_empty[slot], ((nv / C::VS) & 1) ^ 1)) return false;
-            dst = sm + C::OFF_V + slot * TILE;
-            full = &bar.v_full[slot];
-            ++nv;
-        } else {
-            const int slot = nk % C::KS;
-            if (!gate(&bar.k_empty[slot], ((nk / C::KS) & 1) ^ 1)) return false;
-            dst = sm + C::OFF_K + slot * TILE;
-            full = &bar.k_full[slot];
-            ++nk;
-        }
+        const int slot = v ? nv % NV : nk % C::KS;
+        if (!gate(v ? &ve[slot] : &bar.k_empty[slot], ((v ? nv / NV : nk / C::KS) & 1) ^ 1)) return false;
+        uint8_t *dst = (v ? vb : kb) + slot * C::KT;
+        uint64_t *full = v ? &vf[slot] : &bar.k_full[slot];
+        if (E4 && v && lane == 0) reinterpret_cast<int *>(sm + C::OFF_DESC)[slot] = t.z;
+        if (v) ++nv;
+        else ++nk;
         if (lane == 0) mbar_expect_tx(full, (uint32_t)((t.e - t.f) * box * D * ES));
         __syncwarp();
         if (lane >= t.f && lane < t.e) {
@@ -368,12 +385,12 @@ __device__ __forceinline__ void load_role(const PagedAttn &a, const PagedMaps &m
         }
     }
     if (have && !*gate.abort && !load(prev, true)) return drain();
-    if (E4) {
-        const int slot = nr % RING;
-        if (!gate(&bar.r_empty[slot], ((nr / RING) & 1) ^ 1)) return drain();
+    if (E4) {  // the end, for the widening warps
+        const int slot = nv % NV;
+        if (!gate(&ve[slot], ((nv / NV) & 1) ^ 1)) return drain();
         if (lane == 0) {
             reinterpret_cast<int *>(sm + C::OFF_DESC)[slot] = -1;
-            mbar_arrive(&bar.r_full[slot]);
+            mbar_arrive(&vf[slot]);
         }
         __syncwarp();
     }
@@ -381,58 +398,60 @@ __device__ __forceinline__ void load_role(const PagedAttn &a, const PagedMaps &m
 }
 
 // ---------------------------------------------------------------- widening
-// e4m3 to fp16, 256 threads: a thread takes 64 of a row's 128 channels.  Rows that no
-// key stands in become zeros (V: 0 x NaN is NaN).
+// V from e4m3 to fp16: a thread to a row.  Rows that no key stands in become zeros
+// (0 x NaN is NaN).
 template <int NR>
 __device__ __forceinline__ void widen_role(uint8_t *sm, const Gate &gate) {
     using C = Cfg<true, NR>;
     const Bars<C> bar(sm);
-    const int tid = threadIdx.x - W_WIDEN * 32, lane = tid & 31, row = tid & 127, hf = tid >> 7;
-    int nk = 0, nv = 0;
-    for (int n = 0;; ++n) {
-        const int slot = n % C::RS;
-        if (!gate(&bar.r_full[slot], (n / C::RS) & 1)) return;
-        const int z = reinterpret_cast<const volatile int *>(sm + C::OFF_DESC)[slot];
+    const int row = threadIdx.x & 127, lane = threadIdx.x & 31, x = row & 7;
+    const uint8_t *raw = sm + C::OFF_R + row * 128;
+    uint8_t *out = sm + C::OFF_V + row * 128;
+    const volatile int *desc = reinterpret_cast<const volatile int *>(sm + C::OFF_DESC);
+    int slot = 0, ph = 0, os = 0, oph = 0;
+    while (true) {
+        if (!gate(&bar.r_full[slot], ph)) return;
+        const int z = desc[slot];
         if (z < 0) return;
-        const bool v = z >> 16;
-        const uint8_t *src = sm + C::OFF_R + slot * RAW + row * 128;
-        uint4 w[4];
+        const uint8_t *src = raw + slot * RAW;
+        uint4 w[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint4 *>(src + (((4 * hf + i) ^ (row & 7)) << 4));
-        const bool live = row >= (z & 255) && row < ((z >> 8) & 255);
-        uint8_t *dst;
-        if (v) {
-            const int s = nv % C::VS;
-            if (!gate(&bar.v_empty[s], ((nv / C::VS) & 1) ^ 1)) return;
-            dst = sm + C::OFF_V + s * TILE;
-        } else {
-            const int s = nk % C::KS;
-            if (!gate(&bar.k_empty[s], ((nk / C::KS) & 1) ^ 1)) return;
-            dst = sm + C::OFF_K + s * TILE;
+        for (int i = 0; i < 8; ++i) w[i] = *reinterpret_cast<const uint4 *>(src + ((i ^ x) << 4));
+        if (row < (z & 255) || row >= (z >> 8)) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = make_uint4(0, 0, 0, 0);
         }
-        dst += hf * (TILE / 2) + row * 128;
+        if (!gate(&bar.v_empty[os], oph ^ 1)) return;
+        uint8_t *dst = out + os * TILE;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t y[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
             uint32_t h[8];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(x[k] & 0xffff), __NV_E4M3);
-                const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(x[k] >> 16), __NV_E4M3);
-                h[2 * k] = live ? (uint32_t)lo.x | ((uint32_t)lo.y << 16) : 0u;
-                h[2 * k + 1] = live ? (uint32_t)hi.x | ((uint32_t)hi.y << 16) : 0u;
+                const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(y[k] & 0xffff), __NV_E4M3);
+                const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(y[k] >> 16), __NV_E4M3);
+                h[2 * k] = (uint32_t)lo.x | ((uint32_t)lo.y << 16);
+                h[2 * k + 1] = (uint32_t)hi.x | ((uint32_t)hi.y << 16);
             }
-            *reinterpret_cast<uint4 *>(dst + (((2 * i) ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-            *reinterpret_cast<uint4 *>(dst + (((2 * i + 1) ^ (row & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+            uint8_t *at = dst + (i >> 2) * (TILE / 2);
+            *reinterpret_cast<uint4 *>(at + (((2 * (i & 3)) ^ x) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4 *>(at + (((2 * (i & 3) + 1) ^ x) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
         }
         fence_async_smem();
         __syncwarp();
         if (lane == 0) {
+            mbar_arrive(&bar.v_full[os]);
             mbar_arrive(&bar.r_empty[slot]);
-            mbar_arrive(v ? &bar.v_full[nv % C::VS] : &bar.k_full[nk % C::KS]);
         }
-        if (v) ++nv;
-        else ++nk;
+        if (++slot == C::RS) {
+            slot = 0;
+            ph ^= 1;
+        }
+        if (++os == C::VS) {
+            os = 0;
+            oph ^= 1;
+        }
     }
 }
 
@@ -455,6 +474,23 @@ __device__ __forceinline__ void issue_s(uint32_t d, uint64_t k, uint64_t q, uint
         "l"(k), "l"(q), "l"(q2), "r"(idesc)
         : "memory");
 }
+// The same with 8-bit K and the two parts of Q: four steps of 32 channels each.
+__device__ __forceinline__ void issue_s8(uint32_t d, uint64_t k, uint64_t q, uint64_t q2, uint32_t idesc) {
+    asm volatile(
+        "{\n .reg .pred e, t, f;\n .reg .b64 a, b;\n"
+        " setp.eq.u32 t, 0, 0;\n setp.ne.u32 f, 0, 0;\n elect.sync _|e, 0xffffffff;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %4, f;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %3, %4, t;\n"
+        " add.s64 a, %1, 2;\n add.s64 b, %2, 2;\n @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %4, t;\n"
+        " add.s64 b, %3, 2;\n @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %4, t;\n"
+        " add.s64 a, %1, 4;\n add.s64 b, %2, 4;\n @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %4, t;\n"
+        " add.s64 b, %3, 4;\n @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %4, t;\n"
+        " add.s64 a, %1, 6;\n add.s64 b, %2, 6;\n @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %4, t;\n"
+        " add.s64 b, %3, 6;\n @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %4, t;\n"
+        "}\n" ::"r"(d),
+        "l"(k), "l"(q), "l"(q2), "r"(idesc)
+        : "memory");
+}
 // O^T (+)= V^T P^T: eight steps of 16 keys, V 2 KB on, P 512 bytes on.
 __device__ __forceinline__ void issue_o(uint32_t d, uint64_t v, uint64_t p, uint32_t idesc, bool acc) {
     asm volatile(
@@ -473,82 +509,115 @@ __device__ __forceinline__ void issue_o(uint32_t d, uint64_t v, uint64_t p, uint
         : "memory");
 }
 
+// types: e4m3 0 (8-bit products), fp16 0, bf16 1 (16-bit ones); K and Q are K-major, V^T
+// and P^T run along M and N
 template <bool E4, int NR>
-__device__ __forceinline__ void mma_role(uint8_t *sm, uint32_t tmem, const Gate &gate) {
+constexpr uint32_t ID_S = (1u << 4) | (E4 ? 0u : (1u << 7) | (1u << 10)) | ((uint32_t)(NR >> 3) << 17) | ((128u >> 4) << 24);
+template <bool E4, int NR> constexpr uint32_t ID_O = ID_S<E4, NR> | (1u << 15) | (1u << 16);
+
+template <class C>
+__device__ __forceinline__ void drain_products(const Bars<C> &bar, int i) {  // before TMEM is given back
+    mma_commit_w(bar.last + i);
+    mbar_wait(bar.last + i, 0);
+    __syncwarp();
+}
+
+template <bool E4, int NR>
+__device__ __forceinline__ void s_role(uint8_t *sm, uint32_t tmem, const Gate &gate) {
     using C = Cfg<E4, NR>;
     const Bars<C> bar(sm);
-    // fp16 operands have type 0 where bf16 has 1; K and Q are K-major, V^T and P^T run along M and N
-    constexpr uint32_t TYPES = E4 ? 0u : (1u << 7) | (1u << 10);
-    constexpr uint32_t ID_S = (1u << 4) | TYPES | ((uint32_t)(NR >> 3) << 17) | ((128u >> 4) << 24);
-    constexpr uint32_t ID_O = ID_S | (1u << 15) | (1u << 16);
-    const uint32_t base = smem_u32(sm);
-    const uint64_t dk = sdesc_sw128(base + C::OFF_K), dq = sdesc_sw128(base + C::OFF_Q),
-                   dv = sdesc_mn(base + C::OFF_V, TILE / 2, 1024, SWZ_128B), dp = sdesc_mn(base + C::OFF_P, BK * 32, 256, SWZ_32B);
-    int nk = 0, nv = 0;              // S and O products issued
-    int nt = 0, j = 0, item = -1, iseg = 0;
-    int first0 = 0, first1 = 0, ob0 = 0, ob1 = 0;  // of the two tiles ahead: does it begin its item, whose O
-    bool ok = true, more = true;
-    auto ahead = [&]() {             // the next tile's S
-        while (more && j == nt) {
-            Seg s;
-            if (!next_seg<C>(sm, bar, iseg, gate, s)) {
-                more = false;
-                ok = ok && !*gate.abort;
-                return;
-            }
-            if (s.nt == 0) continue;
-            nt = s.nt;
-            j = 0;
-            ++item;
-            ok = gate(&bar.q_full[item & 1], (item >> 1) & 1) && ok;
-        }
-        if (!more || !ok) return;
-        const int b = nk & 1, slot = nk % C::KS, x = item & 1;
-        ok = gate(&bar.k_full[slot], (nk / C::KS) & 1);
-        if (!ok) return;
-        tc_fence_after();
+    const uint64_t dk = sdesc_sw128(smem_u32(sm) + C::OFF_K), dq = sdesc_sw128(smem_u32(sm) + C::OFF_Q);
+    int n = 0, slot = 0, ph = 0, item = 0, iseg = 0;
+    Seg s;
+    while (next_seg<C>(sm, bar, iseg, gate, s)) {
+        if (s.nt == 0) continue;
+        const int x = item & 1, nt = s.nt;
+        bool ok = gate(&bar.q_full[x], (item >> 1) & 1);
         const uint64_t q = dq + (uint32_t)x * (C::QB >> 4);
-        issue_s(tmem + b * NR, dk + (uint32_t)slot * (TILE >> 4), q, q + (NR * 128 >> 4), ID_S);
-        mma_commit_w(&bar.s_full[b]);
-        mma_commit_w(&bar.k_empty[slot]);
-        if (j == nt - 1) mma_commit_w(&bar.q_empty[x]);
-        if (b) first1 = j == 0, ob1 = x;
-        else first0 = j == 0, ob0 = x;
-        ++j;
-        ++nk;
-    };
-    int items = 0;  // whose O has begun
-    ahead();
-    ahead();
-    while (ok && nv < nk) {
-        const int b = nv & 1, slot = nv % C::VS, first = b ? first1 : first0, ob = b ? ob1 : ob0;
-        ok = gate(&bar.v_full[slot], (nv / C::VS) & 1);
-        if (first) {  // the item before last must have left this O
-            ok = gate(&bar.o_free[ob], ((items >> 1) & 1) ^ 1) && ok;
-            ++items;
+        for (int j = 0; ok && j < nt; ++j, ++n) {
+            const int b = n & 1;
+            ok = gate(&bar.k_full[slot], ph);
+            if (n >= 2) ok = gate(&bar.p_ready[b], ((n >> 1) - 1) & 1) && ok;  // the S before last has been read
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t k = dk + (uint32_t)slot * (C::KT >> 4);
+            if constexpr (E4)
+                issue_s8(tmem + b * NR, k, q, q + (NR * 128 >> 4), ID_S<E4, NR>);
+            else
+                issue_s(tmem + b * NR, k, q, q + (NR * 128 >> 4), ID_S<E4, NR>);
+            mma_commit_w(&bar.s_full[b]);
+            mma_commit_w(&bar.k_empty[slot]);
+            if (++slot == C::KS) {
+                slot = 0;
+                ph ^= 1;
+            }
         }
-        ok = gate(&bar.p_ready[b], (nv >> 1) & 1) && ok;
         if (!ok) break;
-        tc_fence_after();
-        issue_o(tmem + 2 * NR + ob * NR, dv + (uint32_t)slot * (TILE >> 4), dp + (uint32_t)b * (C::PB >> 4), ID_O, !first);
-        mma_commit_w(&bar.pv_done[b]);
-        mma_commit_w(&bar.v_empty[slot]);
-        ++nv;
-        ahead();
+        mma_commit_w(&bar.q_empty[x]);
+        ++item;
     }
-    if (!ok || *gate.abort) {  // let the products in flight end before TMEM is given back
-        mma_commit_w(bar.last);
-        mbar_wait(bar.last, 0);
-        __syncwarp();
+    if (*gate.abort) drain_products<C>(bar, 0);
+}
+template <bool E4, int NR>
+__device__ __forceinline__ void o_role(uint8_t *sm, uint32_t tmem, const Gate &gate) {
+    using C = Cfg<E4, NR>;
+    const Bars<C> bar(sm);
+    const uint64_t dv = sdesc_mn(smem_u32(sm) + C::OFF_V, TILE / 2, 1024, SWZ_128B),
+                   dp = sdesc_mn(smem_u32(sm) + C::OFF_P, BK * 32, 256, SWZ_32B);
+    int n = 0, slot = 0, ph = 0, item = 0, iseg = 0;
+    Seg s;
+    while (next_seg<C>(sm, bar, iseg, gate, s)) {
+        if (s.nt == 0) continue;
+        const int nt = s.nt;
+        bool ok = gate(&bar.o_free[item & 1], ((item >> 1) & 1) ^ 1);  // the item before last has left this O
+        const uint32_t to = tmem + 2 * NR + (item & 1) * NR;
+        for (int j = 0; ok && j < nt; ++j, ++n) {
+            const int b = n & 1;
+            ok = gate(&bar.v_full[slot], ph);
+            ok = gate(&bar.p_ready[b], (n >> 1) & 1) && ok;
+            if (!ok) break;
+            tc_fence_after();
+            issue_o(to, dv + (uint32_t)slot * (TILE >> 4), dp + (uint32_t)b * (C::PB >> 4), ID_O<E4, NR>, j > 0);
+            mma_commit_w(&bar.pv_done[b]);
+            mma_commit_w(&bar.v_empty[slot]);
+            if (++slot == C::VS) {
+                slot = 0;
+                ph ^= 1;
+            }
+        }
+        if (!ok) break;
+        ++item;
     }
+    if (*gate.abort) drain_products<C>(bar, 1);
 }
 
 // ---------------------------------------------------------------- softmax
-__device__ __forceinline__ int ordered(float x) {  // the same order among integers
-    const int i = __float_as_int(x);
-    return i ^ ((i >> 31) & 0x7fffffff);
+// Every lane brings NR = 16 or 32 values; afterwards lane's v[0] is the maximum (or sum)
+// over the lanes of value first_of(lane): each step hands half of the values to the lane
+// across.
+template <int NR, bool MAX>
+__device__ __forceinline__ void across(float (&v)[NR], int lane) {
+    int n = NR;
+#pragma unroll
+    for (int s = 16; s; s >>= 1) {
+        if (n > 1) {
+            n >>= 1;
+#pragma unroll
+            for (int i = 0; i < NR / 2; ++i) {
+                if (i < n) {
+                    const bool up = lane & s;
+                    const float keep = up ? v[i + n] : v[i], give = up ? v[i] : v[i + n];
+                    const float got = __shfl_xor_sync(0xffffffffu, give, s);
+                    v[i] = MAX ? fmaxf(keep, got) : keep + got;
+                }
+            }
+        } else {
+            const float got = __shfl_xor_sync(0xffffffffu, v[0], s);
+            v[0] = MAX ? fmaxf(v[0], got) : v[0] + got;
+        }
+    }
 }
-__device__ __forceinline__ float unordered(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
+template <int NR> __device__ __forceinline__ int first_of(int lane) { return NR == 32 ? lane : lane >> 1; }
 
 // NR columns of this thread's lane
 template <int NR>
@@ -567,52 +636,55 @@ __device__ __forceinline__ void tmem_row(uint32_t taddr, float *o) {
 }
 
 // Thread = key of a tile, and channel of O.  A wait that runs out is passed on at the
-// next meeting, so that all four warps leave together.
+// next meeting (every meeting looks for it), so that a group's warps leave together.  A group has
+// GR rows from row g GR on.
 template <bool E4, int NR>
 __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, uint32_t tmem, const Gate &gate) {
     using C = Cfg<E4, NR>;
+    constexpr int GR = C::GR;
     const Bars<C> bar(sm);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int grp = C::GROUPS == 1 ? 0 : threadIdx.x >> 7, tid = threadIdx.x & 127, warp = tid >> 5, lane = tid & 31;
+    const int row0 = grp * GR, id = 1 + grp;
     const uint32_t lanes = (uint32_t)warp << 21;  // 32 warp << 16
-    float *refs = reinterpret_cast<float *>(sm + C::OFF_REF), *corrs = reinterpret_cast<float *>(sm + C::OFF_CORR);
+    float *refs = reinterpret_cast<float *>(sm + C::OFF_REF) + row0, *corrs = reinterpret_cast<float *>(sm + C::OFF_CORR) + row0;
     const int G = a.G;
     int n = 0, item = 0;  // tiles, items with tiles so far
     bool failed = false;
     for (int iseg = 0;; ++iseg) {
         if (!gate(&bar.seg_full[iseg % SEGS], (iseg / SEGS) & 1)) {
-            meet_count<SOFT * 32>(1, true);
+            meet_count<128>(id, true);
             return;
         }
         const Seg *sg = reinterpret_cast<const Seg *>(sm + C::OFF_SEG + (iseg % SEGS) * 64);
         const int nt = sg->nt;
         if (nt < 0) {
-            meet_count<SOFT * 32>(1, false);
+            meet_count<128>(id, false);
             return;
         }
-        const float *sc = reinterpret_cast<const float *>(sm + C::OFF_SC) + (iseg % SEGS) * NR;
-        const int lo = sg->lo, hi = sg->hi, t0 = sg->t0, pos = sg->pos, R = sg->R, r0 = sg->r0;
-        const uint32_t to = tmem + lanes + 2 * NR + (item & 1) * NR;
-        float l[NR], top = -INFINITY;  // sums of this thread's keys; row tid's maximum at the last change of ref
+        const float *sc = reinterpret_cast<const float *>(sm + C::OFF_SC) + (iseg % SEGS) * NR + row0;
+        const int lo = sg->lo, hi = sg->hi, t0 = sg->t0, pos = sg->pos, R = min(GR, sg->R - row0), r0 = sg->r0 + row0;  // (R < 1: none for this group)
+        const uint32_t to = tmem + lanes + 2 * NR + (item & 1) * NR + row0;
+        float l[GR], top = -INFINITY;  // sums of this thread's keys; row tid's maximum at the last change of ref
 #pragma unroll
-        for (int r = 0; r < NR; ++r) l[r] = 0.f;
+        for (int r = 0; r < GR; ++r) l[r] = 0.f;
         for (int j = 0; j < nt; ++j, ++n) {
             const int b = n & 1, key0 = (t0 + j) * BK, key = key0 + tid;
             if (!gate(&bar.s_full[b], (n >> 1) & 1)) failed = true;
             tc_fence_after();
-            float t[NR];
-            tmem_row<NR>(tmem + lanes + b * NR, t);
+            float t[GR];
+            tmem_row<GR>(tmem + lanes + b * NR + row0, t);
             // rows that see this key: [first, last)
             const int d = min(max(key - pos, 0), NR + 1), u = a.window > 0 ? min(max(key - pos + a.window, 0), NR + 1) : NR + 1;
-            const int first = key < hi ? d * G - r0 : NR, last = u > NR ? NR : u * G - r0;
+            const int first = key < hi ? d * G - r0 : GR, last = u > NR ? GR : u * G - r0;
             if (__any_sync(0xffffffffu, first > 0 || last < R)) {
 #pragma unroll
-                for (int r = 0; r < NR; ++r) t[r] = r >= first && r < last ? t[r] : -INFINITY;
+                for (int r = 0; r < GR; ++r) t[r] = r >= first && r < last ? t[r] : -INFINITY;
             }
             bool grow = j == 0;
             if (j > 0) {
                 float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
-                for (int r = 0; r < NR; r += 4) {
+                for (int r = 0; r < GR; r += 4) {
                     const float4 f = *reinterpret_cast<const float4 *>(sc + r), g = *reinterpret_cast<const float4 *>(refs + r);
                     m0 = max3(m0, fmaf(t[r], f.x, -g.x), fmaf(t[r + 1], f.y, -g.y));
                     m1 = max3(m1, fmaf(t[r + 2], f.z, -g.z), fmaf(t[r + 3], f.w, -g.w));
@@ -621,24 +693,27 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
             }
             grow = __any_sync(0xffffffffu, grow);
             // a warp that gave up counts 32, one that saw a maximum grow 1
-            const int said = meet_count<SOFT * 32>(1, failed || (grow && lane == 0));
+            const int said = meet_count<128>(id, failed || (grow && lane == 0));
             if (said >= 32) return;
-            uint8_t *pb = sm + C::OFF_P + b * C::PB;
+            uint8_t *pb = sm + C::OFF_P + b * C::PB + grp * (GR >> 4) * BK * 32;  // this group's blocks of 16 rows
+            if (n >= 2 && !gate(&bar.pv_done[b], ((n >> 1) - 1) & 1)) failed = true;  // its last product has read P's buffer
             if (said) {
-                // largest score of each row over the tile (P's buffer is free: it holds the warps' maxima)
-                float *wm = reinterpret_cast<float *>(pb) + warp * NR;
+                // largest score of each row over the tile (the warps' maxima meet in P's buffer)
+                float *wm = reinterpret_cast<float *>(pb) + warp * GR;
+                {
+                    float m[GR];
 #pragma unroll
-                for (int r = 0; r < NR; ++r) {
-                    const int m = __reduce_max_sync(0xffffffffu, ordered(t[r] * sc[r]));
-                    if (lane == (r & 31)) wm[r] = unordered(m);
+                    for (int r = 0; r < GR; ++r) m[r] = t[r] * sc[r];
+                    across<GR, true>(m, lane);
+                    wm[first_of<GR>(lane)] = m[0];
                 }
-                meet_count<SOFT * 32>(1, false);
-                if (tid < NR) {
+                if (meet_count<128>(id, failed) >= 32) return;
+                if (tid < GR) {
                     const float *all = reinterpret_cast<const float *>(pb);
                     const float was = j == 0 ? -INFINITY : top, ref = refs[tid];
                     float m = was;
 #pragma unroll
-                    for (int w = 0; w < SOFT; ++w) m = fmaxf(m, all[w * NR + tid]);
+                    for (int w = 0; w < 4; ++w) m = fmaxf(m, all[w * GR + tid]);
                     // a row that had seen nothing has zeros in O and in its sums, and a reference
                     // that its first score will be far above
                     const float next = m == -INFINITY ? NOTHING : was == -INFINITY ? m : fmaxf(m, ref);
@@ -646,12 +721,12 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
                     refs[tid] = next;
                     top = m;
                 }
-                meet_count<SOFT * 32>(1, false);
+                if (meet_count<128>(id, failed) >= 32) return;
                 if (j > 0) {
                     if (!gate(&bar.pv_done[b ^ 1], ((n - 1) >> 1) & 1)) failed = true;  // the last product must have left O
                     tc_fence_after();
 #pragma unroll 1
-                    for (int c = 0; c < NR; c += 16) {
+                    for (int c = 0; c < GR; c += 16) {
                         float o[16];
                         uint32_t w[16];
                         tmem_ld16(to + c, o);
@@ -665,12 +740,12 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
                     }
                     tmem_st_wait();
 #pragma unroll
-                    for (int r = 0; r < NR; ++r) l[r] *= corrs[r];
+                    for (int r = 0; r < GR; ++r) l[r] *= corrs[r];
                 }
             }
-            uint32_t p[NR / 2];
+            uint32_t p[GR / 2];
 #pragma unroll
-            for (int r = 0; r < NR; r += 4) {
+            for (int r = 0; r < GR; r += 4) {
                 const float4 f = *reinterpret_cast<const float4 *>(sc + r), g = *reinterpret_cast<const float4 *>(refs + r);
                 const float e0 = ex2(fmaf(t[r], f.x, -g.x)), e1 = ex2(fmaf(t[r + 1], f.y, -g.y));
                 const float e2 = ex2(fmaf(t[r + 2], f.z, -g.z)), e3 = ex2(fmaf(t[r + 3], f.w, -g.w));
@@ -683,7 +758,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
             }
             // [key][row], blocks of 16 rows, the two 16-byte halves swapped on every other group of four keys
 #pragma unroll
-            for (int c = 0; c < NR / 8; ++c)
+            for (int c = 0; c < GR / 8; ++c)
                 *reinterpret_cast<uint4 *>(pb + (c >> 1) * BK * 32 + tid * 32 + (((c & 1) ^ ((tid >> 2) & 1)) << 4)) =
                     make_uint4(p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]);
             if (!E4) {
@@ -706,67 +781,64 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
         }
 
         // ---- the segment's end: sums over the keys, then O, normalised or as a piece
+        // (a thread has one channel of every row)
         const bool whole = sg->whole;
-        const int64_t tok = sg->tok;
-        const int head0 = sg->h * G;
+        const int h = sg->h;
         float *slot = paged_slot(a, sg->slot);
-        float *sums = reinterpret_cast<float *>(sm + C::OFF_P);  // [NR][128]: both P buffers, their products done
         if (nt > 0) {
             if (!gate(&bar.pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1)) failed = true;
             tc_fence_after();
+            float *all = reinterpret_cast<float *>(sm + C::OFF_P + grp * (GR >> 4) * BK * 32);  // [warp][row], over P: its products are done
+            across<GR, false>(l, lane);
+            all[warp * GR + first_of<GR>(lane)] = l[0];
+            if (meet_count<128>(id, failed) >= 32) return;
+        }
+        const int64_t out0 = (int64_t)sg->tok * a.Hq + h * G;  // row rr = r0 + r of the token's heads, the next token Hq on
+        if (tid < R) {
+            float L = 0.f;
+            if (nt > 0) {
+                const float *all = reinterpret_cast<const float *>(sm + C::OFF_P + grp * (GR >> 4) * BK * 32);
 #pragma unroll
-            for (int r = 0; r < NR; ++r) sums[r * 128 + tid] = l[r];
-            if (meet_count<SOFT * 32>(1, failed) >= 32) return;
-#pragma unroll 4
-            for (int r = warp; r < NR; r += SOFT) {
-                const float4 x = *reinterpret_cast<const float4 *>(sums + r * 128 + 4 * lane);
-                float y = (x.x + x.y) + (x.z + x.w);
-#pragma unroll
-                for (int o = 16; o; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-                if (lane == 0) corrs[r] = y;
+                for (int w = 0; w < 4; ++w) L += all[w * GR + tid];
             }
-            meet_count<SOFT * 32>(1, false);
-            const float vs = E4 ? a.v_scale[sg->h] : 1.f;
+            const float ref = nt > 0 ? refs[tid] : 0.f;
+            corrs[tid] = L == 0.f ? 0.f : whole ? (E4 ? a.v_scale[h] : 1.f) / L : 1.f;
+            if (!whole) {
+                reinterpret_cast<float2 *>(slot)[row0 + tid] = make_float2(L == 0.f ? -INFINITY : ref, L);
+            } else if (a.lse) {
+                const int rr = r0 + tid, jt = rr / G;
+                a.lse[out0 + (int64_t)jt * a.Hq + rr - jt * G] = L == 0.f ? -INFINITY : (ref + log2f(L)) * 0.6931471805599453f;
+            }
+        }
+        if (meet_count<128>(id, failed) >= 32) return;
+        const int j0 = r0 / G;
+        int hh = r0 - j0 * G;  // head within the token's group
+        int64_t at = (out0 + (int64_t)j0 * a.Hq + hh) * D + tid;
 #pragma unroll 1
-            for (int c = 0; c < NR; c += 16) {
-                if (c >= R) break;
-                float o[16];
-                tmem_ld16(to + c, o);
-                tmem_ld_wait();
+        for (int c = 0; c < R; c += 16) {
+            float o[16];
+            tmem_ld16(to + c, o);
+            tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    asm volatile("" : "+f"(o[i]));
-                    const int r = c + i;
-                    if (r >= R) continue;
-                    const float L = corrs[r];
+            for (int i = 0; i < 16; ++i) {
+                asm volatile("" : "+f"(o[i]));
+                if (c + i < R) {
+                    const float f = corrs[c + i], y = f == 0.f ? 0.f : o[i] * f;  // (nothing seen: zero whatever O holds)
                     if (whole) {
-                        const int rr = r0 + r, jt = rr / G;
-                        const float y = L == 0.f ? 0.f : o[i] * (vs / L);
-                        reinterpret_cast<__nv_bfloat16 *>(a.o)[((tok + jt) * a.Hq + head0 + rr - jt * G) * D + tid] = __float2bfloat16_rn(y);
+                        reinterpret_cast<__nv_bfloat16 *>(a.o)[at] = __float2bfloat16_rn(y);
+                        at += D;
+                        if (++hh == G) {
+                            hh = 0;
+                            at += (int64_t)(a.Hq - G) * D;
+                        }
                     } else {
-                        slot[2 * a.slot_rows + r * D + tid] = o[i];
+                        slot[2 * a.slot_rows + (row0 + c + i) * D + tid] = y;
                     }
                 }
             }
-        } else if (whole) {
-            for (int r = 0; r < R; ++r) {
-                const int rr = r0 + r, jt = rr / G;
-                reinterpret_cast<__nv_bfloat16 *>(a.o)[((tok + jt) * a.Hq + head0 + rr - jt * G) * D + tid] = __float2bfloat16_rn(0.f);
-            }
-        } else {
-            for (int r = 0; r < R; ++r) slot[2 * a.slot_rows + r * D + tid] = 0.f;
         }
-        if (tid < R) {
-            const float L = nt > 0 ? corrs[tid] : 0.f, ref = nt > 0 ? refs[tid] : 0.f;
-            if (!whole) {
-                reinterpret_cast<float2 *>(slot)[tid] = make_float2(L == 0.f ? -INFINITY : ref, L);
-            } else if (a.lse) {
-                const int rr = r0 + tid, jt = rr / G;
-                a.lse[(tok + jt) * a.Hq + head0 + rr - jt * G] = L == 0.f ? -INFINITY : (ref + log2f(L)) * 0.6931471805599453f;
-            }
-        }
-        if (tid == 0 && !whole && sg->c0 == (int)blockIdx.x) {
-            a.lead[2 * blockIdx.x] = make_int4((int)tok, sg->h, r0, R);
+        if (threadIdx.x == 0 && !whole && sg->c0 == (int)blockIdx.x) {
+            a.lead[2 * blockIdx.x] = make_int4(sg->tok, h, sg->r0, sg->R);
             a.lead[2 * blockIdx.x + 1] = make_int4(sg->slot, sg->c0, sg->c1, 1);
         }
         tc_fence_before();
@@ -775,8 +847,10 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
             if (nt > 0) mbar_arrive(&bar.o_free[item & 1]);
             mbar_arrive(&bar.seg_empty[iseg % SEGS]);
         }
-        // (refs, corrs and the sums are written again only past the next tile's meeting)
+        // (refs and the sums are written again only past the next meeting; corrs too, unless
+        // an item without tiles follows)
         if (nt > 0) ++item;
+        else if (meet_count<128>(id, failed) >= 32) return;
     }
 }
 
@@ -793,7 +867,7 @@ __global__ void __launch_bounds__(Cfg<E4, NR>::THREADS, 1)
     const Rows rw(a.G, NR);
     if (tid == 0) {
         for (int i = 0; i < C::KS; ++i) {
-            mbar_init(&bar.k_full[i], E4 ? WIDEN : 1);
+            mbar_init(&bar.k_full[i], 1);
             mbar_init(&bar.k_empty[i], 1);
         }
         for (int i = 0; i < C::VS; ++i) {
@@ -808,15 +882,16 @@ __global__ void __launch_bounds__(Cfg<E4, NR>::THREADS, 1)
             mbar_init(&bar.q_full[i], 1);
             mbar_init(&bar.q_empty[i], 1);
             mbar_init(&bar.s_full[i], 1);
-            mbar_init(&bar.p_ready[i], SOFT);
+            mbar_init(&bar.p_ready[i], C::SOFT);
             mbar_init(&bar.pv_done[i], 1);
-            mbar_init(&bar.o_free[i], SOFT);
+            mbar_init(&bar.o_free[i], C::SOFT);
         }
         for (int i = 0; i < SEGS; ++i) {
             mbar_init(&bar.seg_full[i], 1);
-            mbar_init(&bar.seg_empty[i], SOFT + 2);
+            mbar_init(&bar.seg_empty[i], C::SOFT + 3);
         }
         mbar_init(bar.last, 1);
+        mbar_init(bar.last + 1, 1);
         mbar_fence_init();
         sh->abort = 0;
         a.lead[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
@@ -845,26 +920,21 @@ __global__ void __launch_bounds__(Cfg<E4, NR>::THREADS, 1)
             sh->A = line.before + vh * head + units_before(a, q, lo, rw);
         }
     }
-    if (warp == W_MMA) tmem_alloc(&sh->tmem, C::TCOLS);
+    if (warp == C::W_S) tmem_alloc(&sh->tmem, C::TCOLS);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh->tmem;
     const Gate gate{&sh->abort, a.err};
-    // e4m3 with 64 rows: 128 registers a thread at launch (512 x 128 = 65,536), 200 for
-    // the softmax warps' 64 scores and sums, 104 for the others: 128 x 200 + 384 x 104
-    constexpr bool SPLIT = E4 && NR == 64;
-    if (warp < SOFT) {
-        if constexpr (SPLIT) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    if (warp < C::SOFT) {
         softmax_role<E4, NR>(a, sm, tmem, gate);
-    } else {
-        if constexpr (SPLIT) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-    }
-    if (warp == W_MMA) {
-        mma_role<E4, NR>(sm, tmem, gate);
-    } else if (warp == W_LOAD) {
+    } else if (warp == C::W_S) {
+        s_role<E4, NR>(sm, tmem, gate);
+    } else if (warp == C::W_O) {
+        o_role<E4, NR>(sm, tmem, gate);
+    } else if (warp == C::W_LOAD) {
         load_role<E4, NR>(a, maps, sm, gate);
-    } else if (warp == W_WALK) {
+    } else if (warp == C::W_WALK) {
         Walk w;
         w.pos = line.P0;
         w.end = line.P1;
@@ -875,12 +945,12 @@ __global__ void __launch_bounds__(Cfg<E4, NR>::THREADS, 1)
         w.g = sh->g;
         w.fresh = true;
         walk_role<E4, NR>(a, sm, w, line.P0, gate);
-    } else if (E4 && warp >= W_WIDEN) {
+    } else {
         if constexpr (E4) widen_role<NR>(sm, gate);
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == W_MMA) {
+    if (warp == C::W_S) {
         tc_fence_after();
         tmem_dealloc(tmem, C::TCOLS);
     }
