@@ -120,6 +120,8 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) paged_join_kernel(PagedAttn a
     }
 }
 
+constexpr int FEW_ROWS = 32;
+
 int launch_join(const PagedAttn &a, const JoinSet &s0, const JoinSet &s1, int64_t max_rows, bool f32, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(s0.blocks + s1.blocks, (unsigned)(max_rows < 16 ? max_rows : 16));
@@ -207,15 +209,16 @@ int kda_paged_attn(const void *q, const void *k_cache, const void *v_cache, cons
         if ((rc = launch_paged_rows(a, k_cache, v_cache, page_stride, s))) return rc;
         return launch_join(a, js[0], js[1], max_rows, true, s);
     }
-    // Up to 64 rows of a kv head fit the few-rows kernel at once.  With longer
-    // requests in the call, the tile kernel takes them, and the few-rows kernel the
-    // single tokens (rows up to the next of 16, 32, 64 from G on); requests in between
-    // are the tile kernel's too, which has room for 128 rows at one cost.
-    const bool tiles = cache_dtype == KDA_BF16 && a.G <= 128 && max_rows > PAGED_ROWS_CAP;
-    const int few_rows = a.G <= 16 ? 16 : a.G <= 32 ? 32 : 64;
+    // Up to 32 rows of a kv head fit the few-rows kernel at once; over that the tile
+    // kernel, which has room for 128 rows at one cost, is faster (256 windows of 60 rows:
+    // 306 us against 470 us in pieces of 64).  With longer requests in the call it takes
+    // them, and the few-rows kernel the single tokens (rows up to the next of 16, 32 from
+    // G on).
+    const bool tiles = cache_dtype == KDA_BF16 && a.G <= 128 && max_rows > FEW_ROWS;
+    const int few_rows = a.G <= 16 ? 16 : FEW_ROWS;
     // every request long enough for the tile kernel: one of T_total tokens, or all
     // of max_q (the offsets may still say less: the tile kernel then takes that too)
-    const bool few = !tiles || (a.G <= PAGED_ROWS_CAP && n_seqs > 1 && T_total != (int64_t)n_seqs * a.max_q);
+    const bool few = !tiles || (a.G <= FEW_ROWS && n_seqs > 1 && T_total != (int64_t)n_seqs * a.max_q);
     if (few) {
         if (tiles) a.row_hi = few_rows;
         js[0] = use(w.rows, paged_few_blocks());

@@ -1,8 +1,7 @@
 // kda_paged_few.cu -- paged attention on tcgen05 for few rows (single tokens,
-// draft windows, short chunks; bf16 and e4m3 caches): up to NR = 16, 32 or 64 rows
-// of one kv head at a time.  Each key and value is read for few rows, so the time is
-// the pages' bytes over HBM; what the kernel has to do is keep copies in flight and
-// stay out of their way.
+// draft windows; bf16 and e4m3 caches): NR = 16 or 32 rows of one kv head at a time.
+// Each key and value is read for few rows, so the time is the pages' bytes over HBM;
+// what the kernel has to do is keep copies in flight and stay out of their way.
 //
 // The products are taken the other way round than for many rows, so that the 128
 // lanes of TMEM are keys (and channels) and only the NR columns in use cost
@@ -11,18 +10,21 @@
 //   P^T = exp2(S^T scale - ref): thread = key, NR values, stored as the [key][row]
 //         operand of the second product (bf16; fp16 for e4m3 caches)
 //   O^T += V^T P^T 128 channels x NR fp32 in TMEM, V from shared memory as loaded
+// Two groups of four softmax warps take every other tile, each with its own buffers,
+// references, sums and O, merged at the item's end: one group alone needs 2,000 cycles
+// a tile, nearly all of it latency, more than an e4m3 tile takes to arrive.
 // Products of S, issued by one warp, run up to two tiles ahead of those of O, issued by
-// another, across items (one warp for both took 1,900 cycles a tile: too long for e4m3).
+// another, across items.
 //
 // `ref` follows a row's maximum only when that has grown by more than 2^8 (kept
 // probabilities are then as precise in 16 bits, sums are fp32): most tiles need no
 // maximum over their keys at all, which would go across lanes, and no rescaling; one
-// barrier tells the four softmax warps whether any of them saw such growth.
+// barrier tells a group's warps whether any of them saw such growth.
 //
 // e4m3 caches: S^T multiplies K as it was loaded (8-bit products) by two e4m3 parts of
 // q, which hold a bf16 value's eight bits; V is widened to fp16, which is exact, by
-// four warps beside the copies (K too would be too much: the conversions run at 16 a
-// cycle and SM, some 500 cycles a tile).
+// warps beside the copies (K too would be too much: the conversions run at 16 a cycle
+// and SM, some 500 cycles a tile).
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -38,32 +40,29 @@ constexpr int RAW = BK * D;            // an e4m3 tile as loaded
 constexpr int SEGS = 4;                // segments ahead of the roles
 constexpr int HEAD = 1;                // an item's cost besides its tiles, in tiles
 constexpr float GROW = 8.f, NOTHING = -1e30f;
-constexpr int WIDEN = 4;                // warps that widen V
-
-// Warps: the softmax groups of four warps (each up to 32 rows), then one for the
-// products of S, loads, the walk, the products of O, and those that widen V.
+// Warps: two softmax groups of four, then one each for the products of S, loads, the
+// walk and the products of O, and those that widen V.
 // Buffers: K tiles (e4m3: as loaded), V operand tiles, e4m3 V tiles as loaded.
 template <bool E4, int NR> struct Cfg {
-    static constexpr int GR = NR == 64 ? 32 : NR, GROUPS = NR / GR, SOFT = 4 * GROUPS;
-    static constexpr int W_S = SOFT, W_LOAD = SOFT + 1, W_WALK = SOFT + 2, W_O = SOFT + 3, W_WIDEN = SOFT + 4;
-    static constexpr int KT = E4 ? RAW : TILE;  // bytes of a K tile
-    static constexpr int KS = E4 ? (NR == 64 ? 3 : NR == 32 ? 4 : 5) : NR == 64 ? 2 : 3, VS = E4 ? 2 : 3,
-                         RS = E4 ? (NR == 64 ? 3 : 4) : 0;
+    static constexpr int SOFT = 8, W_S = 8, W_LOAD = 9, W_WALK = 10, W_O = 11, W_WIDEN = 12;
+    static constexpr int WIDEN = !E4 ? 0 : NR == 16 ? 8 : 4;  // (512 threads leave 128 registers for NR = 32)
+    static constexpr int KT = E4 ? RAW : TILE;                // bytes of a K tile
+    static constexpr int KS = E4 ? (NR == 32 ? 4 : 5) : 3, VS = E4 ? 2 : 3, RS = E4 ? 4 : 0;
     static constexpr int PB = BK * NR * 2, QB = NR * D * 2;
     static constexpr int OFF_K = 0, OFF_V = OFF_K + KS * KT, OFF_R = OFF_V + VS * TILE, OFF_Q = OFF_R + RS * RAW,
-                         OFF_P = OFF_Q + 2 * QB, OFF_REF = OFF_P + 2 * PB, OFF_CORR = OFF_REF + NR * 4,
-                         OFF_SC = OFF_CORR + NR * 4, OFF_SEG = OFF_SC + SEGS * NR * 4, OFF_DESC = OFF_SEG + SEGS * 64,
-                         OFF_BAR = OFF_DESC + 32;
-    static constexpr int NBAR = 2 * (KS + VS + RS) + 4 + 8 + 2 + 2 * SEGS;
+                         OFF_P = OFF_Q + 2 * QB, OFF_REF = OFF_P + 2 * PB, OFF_FAC = OFF_REF + 2 * NR * 4,
+                         OFF_MRG = OFF_FAC + 2 * NR * 4, OFF_SUM = OFF_MRG + 2 * NR * 4, OFF_SC = OFF_SUM + 8 * NR * 4, OFF_SEG = OFF_SC + SEGS * NR * 4,
+                         OFF_DESC = OFF_SEG + SEGS * 64, OFF_BAR = OFF_DESC + 32;
+    static constexpr int NBAR = 2 * (KS + VS + RS) + 4 + 8 + 3 + 2 * SEGS;
     static constexpr int OFF_MISC = (OFF_BAR + NBAR * 8 + 15) / 16 * 16, SMEM = OFF_MISC + 64;
-    static constexpr int THREADS = (W_WIDEN + (E4 ? WIDEN : 0)) * 32;
-    static constexpr int TCOLS = 4 * NR;
+    static constexpr int THREADS = (W_WIDEN + WIDEN) * 32;
+    static constexpr int TCOLS = NR == 16 ? 128 : 256;        // S [2][NR], O [item parity][group][NR]
     static_assert(SMEM <= 232448 && OFF_SEG % 16 == 0 && OFF_BAR % 8 == 0 && RS <= 8 && OFF_V % 1024 == 0, "shared memory layout");
 };
 
 template <class C> struct Bars {
     uint64_t *k_full, *k_empty, *v_full, *v_empty, *r_full, *r_empty, *q_full, *q_empty, *s_full, *p_ready, *pv_done, *o_free,
-        *last, *seg_full, *seg_empty;
+        *last, *joint, *seg_full, *seg_empty;
     __device__ explicit Bars(uint8_t *sm) {
         k_full = reinterpret_cast<uint64_t *>(sm + C::OFF_BAR);
         k_empty = k_full + C::KS;
@@ -78,7 +77,8 @@ template <class C> struct Bars {
         pv_done = p_ready + 2;
         o_free = pv_done + 2;      // [2] by item
         last = o_free + 2;
-        seg_full = last + 2;       // (last: products in flight when a wait ran out)
+        joint = last + 2;          // (last: products in flight when a wait ran out)
+        seg_full = joint + 1;      // (joint: the two groups at an item's end)
         seg_empty = seg_full + SEGS;
     }
 };
@@ -398,13 +398,14 @@ __device__ __forceinline__ void load_role(const PagedAttn &a, const PagedMaps &m
 }
 
 // ---------------------------------------------------------------- widening
-// V from e4m3 to fp16: a thread to a row.  Rows that no key stands in become zeros
-// (0 x NaN is NaN).
+// V from e4m3 to fp16, 32 WIDEN / 128 threads to a row.  Rows that no key stands in
+// become zeros (0 x NaN is NaN).
 template <int NR>
 __device__ __forceinline__ void widen_role(uint8_t *sm, const Gate &gate) {
     using C = Cfg<true, NR>;
+    constexpr int W = 32 / C::WIDEN;  // 16-byte pieces of a row for one thread: 8 of them to a row
     const Bars<C> bar(sm);
-    const int row = threadIdx.x & 127, lane = threadIdx.x & 31, x = row & 7;
+    const int tid = threadIdx.x - C::W_WIDEN * 32, row = tid & 127, lane = tid & 31, x = row & 7, p0 = (tid >> 7) * W;
     const uint8_t *raw = sm + C::OFF_R + row * 128;
     uint8_t *out = sm + C::OFF_V + row * 128;
     const volatile int *desc = reinterpret_cast<const volatile int *>(sm + C::OFF_DESC);
@@ -414,17 +415,17 @@ __device__ __forceinline__ void widen_role(uint8_t *sm, const Gate &gate) {
         const int z = desc[slot];
         if (z < 0) return;
         const uint8_t *src = raw + slot * RAW;
-        uint4 w[8];
+        uint4 w[W];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = *reinterpret_cast<const uint4 *>(src + ((i ^ x) << 4));
+        for (int i = 0; i < W; ++i) w[i] = *reinterpret_cast<const uint4 *>(src + (((p0 + i) ^ x) << 4));
         if (row < (z & 255) || row >= (z >> 8)) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = make_uint4(0, 0, 0, 0);
+            for (int i = 0; i < W; ++i) w[i] = make_uint4(0, 0, 0, 0);
         }
         if (!gate(&bar.v_empty[os], oph ^ 1)) return;
         uint8_t *dst = out + os * TILE;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < W; ++i) {
             const uint32_t y[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
             uint32_t h[8];
 #pragma unroll
@@ -434,9 +435,10 @@ __device__ __forceinline__ void widen_role(uint8_t *sm, const Gate &gate) {
                 h[2 * k] = (uint32_t)lo.x | ((uint32_t)lo.y << 16);
                 h[2 * k + 1] = (uint32_t)hi.x | ((uint32_t)hi.y << 16);
             }
-            uint8_t *at = dst + (i >> 2) * (TILE / 2);
-            *reinterpret_cast<uint4 *>(at + (((2 * (i & 3)) ^ x) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-            *reinterpret_cast<uint4 *>(at + (((2 * (i & 3) + 1) ^ x) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+            const int p = p0 + i;  // piece of 16 channels: two of the 16-bit row
+            uint8_t *at = dst + (p >> 2) * (TILE / 2);
+            *reinterpret_cast<uint4 *>(at + (((2 * (p & 3)) ^ x) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4 *>(at + (((2 * (p & 3) + 1) ^ x) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
         }
         fence_async_smem();
         __syncwarp();
@@ -570,14 +572,14 @@ __device__ __forceinline__ void o_role(uint8_t *sm, uint32_t tmem, const Gate &g
         if (s.nt == 0) continue;
         const int nt = s.nt;
         bool ok = gate(&bar.o_free[item & 1], ((item >> 1) & 1) ^ 1);  // the item before last has left this O
-        const uint32_t to = tmem + 2 * NR + (item & 1) * NR;
+        const uint32_t to = tmem + 2 * NR + (item & 1) * 2 * NR;
         for (int j = 0; ok && j < nt; ++j, ++n) {
             const int b = n & 1;
             ok = gate(&bar.v_full[slot], ph);
             ok = gate(&bar.p_ready[b], (n >> 1) & 1) && ok;
             if (!ok) break;
             tc_fence_after();
-            issue_o(to, dv + (uint32_t)slot * (TILE >> 4), dp + (uint32_t)b * (C::PB >> 4), ID_O<E4, NR>, j > 0);
+            issue_o(to + b * NR, dv + (uint32_t)slot * (TILE >> 4), dp + (uint32_t)b * (C::PB >> 4), ID_O<E4, NR>, j > 1);
             mma_commit_w(&bar.pv_done[b]);
             mma_commit_w(&bar.v_empty[slot]);
             if (++slot == C::VS) {
@@ -635,138 +637,152 @@ __device__ __forceinline__ void tmem_row(uint32_t taddr, float *o) {
     }
 }
 
-// Thread = key of a tile, and channel of O.  A wait that runs out is passed on at the
-// next meeting (every meeting looks for it), so that a group's warps leave together.  A group has
-// GR rows from row g GR on.
+// Thread = key of a tile, and channel of O; group g has the tiles of its parity.  A wait
+// that runs out is passed on at the group's next meeting (every segment begins with one,
+// every meeting looks for it), so that a group's warps leave together; the groups wait
+// for each other with bounded waits only.
 template <bool E4, int NR>
 __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, uint32_t tmem, const Gate &gate) {
     using C = Cfg<E4, NR>;
-    constexpr int GR = C::GR;
     const Bars<C> bar(sm);
-    const int grp = C::GROUPS == 1 ? 0 : threadIdx.x >> 7, tid = threadIdx.x & 127, warp = tid >> 5, lane = tid & 31;
-    const int row0 = grp * GR, id = 1 + grp;
-    const uint32_t lanes = (uint32_t)warp << 21;  // 32 warp << 16
-    float *refs = reinterpret_cast<float *>(sm + C::OFF_REF) + row0, *corrs = reinterpret_cast<float *>(sm + C::OFF_CORR) + row0;
+    const int g = threadIdx.x >> 7, tid = threadIdx.x & 127, warp = tid >> 5, lane = tid & 31, id = 1 + g;
+    const uint32_t lanes = (uint32_t)warp << 21, ts = tmem + lanes + g * NR;  // 32 warp << 16
+    float *refs = reinterpret_cast<float *>(sm + C::OFF_REF), *ref = refs + g * NR;  // this group's references
+    float *fac = reinterpret_cast<float *>(sm + C::OFF_FAC) + g * NR;                // and factors
+    float *sums = reinterpret_cast<float *>(sm + C::OFF_SUM);                        // [group][warp][NR]
+    uint8_t *pb = sm + C::OFF_P + g * C::PB;
     const int G = a.G;
-    int n = 0, item = 0;  // tiles, items with tiles so far
+    int n = 0, k = 0, item = 0, joint = 0;  // tiles, this group's, items with tiles, joint meetings so far
     bool failed = false;
+    auto together = [&]() {  // the two groups
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar.joint);
+        if (!gate(bar.joint, joint & 1)) failed = true;
+        ++joint;
+    };
     for (int iseg = 0;; ++iseg) {
-        if (!gate(&bar.seg_full[iseg % SEGS], (iseg / SEGS) & 1)) {
-            meet_count<128>(id, true);
-            return;
-        }
+        if (!gate(&bar.seg_full[iseg % SEGS], (iseg / SEGS) & 1)) failed = true;
+        if (meet_count<128>(id, failed) >= 32) return;
         const Seg *sg = reinterpret_cast<const Seg *>(sm + C::OFF_SEG + (iseg % SEGS) * 64);
         const int nt = sg->nt;
-        if (nt < 0) {
-            meet_count<128>(id, false);
-            return;
-        }
-        const float *sc = reinterpret_cast<const float *>(sm + C::OFF_SC) + (iseg % SEGS) * NR + row0;
-        const int lo = sg->lo, hi = sg->hi, t0 = sg->t0, pos = sg->pos, R = min(GR, sg->R - row0), r0 = sg->r0 + row0;  // (R < 1: none for this group)
-        const uint32_t to = tmem + lanes + 2 * NR + (item & 1) * NR + row0;
-        float l[GR], top = -INFINITY;  // sums of this thread's keys; row tid's maximum at the last change of ref
+        if (nt < 0) return;
+        const float *sc = reinterpret_cast<const float *>(sm + C::OFF_SC) + (iseg % SEGS) * NR;
+        const int lo = sg->lo, hi = sg->hi, t0 = sg->t0, pos = sg->pos, R = sg->R, r0 = sg->r0;
+        const uint32_t to = tmem + lanes + 2 * NR + (item & 1) * 2 * NR;  // + NR g
+        float l[NR], top = -INFINITY;  // sums of this thread's keys; row tid's maximum at the last change of ref
 #pragma unroll
-        for (int r = 0; r < GR; ++r) l[r] = 0.f;
-        for (int j = 0; j < nt; ++j, ++n) {
-            const int b = n & 1, key0 = (t0 + j) * BK, key = key0 + tid;
-            if (!gate(&bar.s_full[b], (n >> 1) & 1)) failed = true;
+        for (int r = 0; r < NR; ++r) l[r] = 0.f;
+        int mine = 0;
+        for (int j = (n & 1) ^ g; j < nt; j += 2, ++k, ++mine) {
+            const int key0 = (t0 + j) * BK, key = key0 + tid;
+            if (!gate(&bar.s_full[g], k & 1)) failed = true;
             tc_fence_after();
-            float t[GR];
-            tmem_row<GR>(tmem + lanes + b * NR + row0, t);
-            // rows that see this key: [first, last)
-            const int d = min(max(key - pos, 0), NR + 1), u = a.window > 0 ? min(max(key - pos + a.window, 0), NR + 1) : NR + 1;
-            const int first = key < hi ? d * G - r0 : GR, last = u > NR ? GR : u * G - r0;
-            if (__any_sync(0xffffffffu, first > 0 || last < R)) {
+            float t[NR];
+            // scores; -inf where a row does not see this key (rows that do: [first, last))
+            auto scores = [&]() {
+                tmem_row<NR>(ts, t);
+                if (key0 + BK - 1 > pos || key0 + BK > hi || a.window > 0) {
+                    const int d = min(max(key - pos, 0), NR + 1), u = a.window > 0 ? min(max(key - pos + a.window, 0), NR + 1) : NR + 1;
+                    const int first = key < hi ? d * G - r0 : NR, last = u > NR ? NR : u * G - r0;
 #pragma unroll
-                for (int r = 0; r < GR; ++r) t[r] = r >= first && r < last ? t[r] : -INFINITY;
-            }
-            bool grow = j == 0;
-            if (j > 0) {
-                float m0 = -INFINITY, m1 = -INFINITY;
+                    for (int r = 0; r < NR; ++r) t[r] = r >= first && r < last ? t[r] : -INFINITY;
+                }
+            };
+            // the exponents: t sc - ref
+            auto exponents = [&]() {
 #pragma unroll
-                for (int r = 0; r < GR; r += 4) {
-                    const float4 f = *reinterpret_cast<const float4 *>(sc + r), g = *reinterpret_cast<const float4 *>(refs + r);
-                    m0 = max3(m0, fmaf(t[r], f.x, -g.x), fmaf(t[r + 1], f.y, -g.y));
-                    m1 = max3(m1, fmaf(t[r + 2], f.z, -g.z), fmaf(t[r + 3], f.w, -g.w));
+                for (int r = 0; r < NR; r += 4) {
+                    const float4 y = *reinterpret_cast<const float4 *>(ref + r);
+                    const float4 f = E4 ? *reinterpret_cast<const float4 *>(sc + r)
+                                        : make_float4(a.scale_log2, a.scale_log2, a.scale_log2, a.scale_log2);
+                    t[r] = fmaf(t[r], f.x, -y.x);
+                    t[r + 1] = fmaf(t[r + 1], f.y, -y.y);
+                    t[r + 2] = fmaf(t[r + 2], f.z, -y.z);
+                    t[r + 3] = fmaf(t[r + 3], f.w, -y.w);
+                }
+            };
+            scores();
+            bool grow = mine == 0;
+            if (mine > 0) {
+                exponents();
+                float m0 = max3(t[0], t[1], t[2]), m1 = t[3];
+#pragma unroll
+                for (int r = 4; r < NR; r += 4) {
+                    m0 = max3(m0, t[r], t[r + 1]);
+                    m1 = max3(m1, t[r + 2], t[r + 3]);
                 }
                 grow = fmaxf(m0, m1) > GROW;
             }
             grow = __any_sync(0xffffffffu, grow);
+            if (k > 0 && !gate(&bar.pv_done[g], (k - 1) & 1)) failed = true;  // P's buffer, O: the last product is done
             // a warp that gave up counts 32, one that saw a maximum grow 1
             const int said = meet_count<128>(id, failed || (grow && lane == 0));
             if (said >= 32) return;
-            uint8_t *pb = sm + C::OFF_P + b * C::PB + grp * (GR >> 4) * BK * 32;  // this group's blocks of 16 rows
-            if (n >= 2 && !gate(&bar.pv_done[b], ((n >> 1) - 1) & 1)) failed = true;  // its last product has read P's buffer
             if (said) {
+                if (mine > 0) scores();
                 // largest score of each row over the tile (the warps' maxima meet in P's buffer)
-                float *wm = reinterpret_cast<float *>(pb) + warp * GR;
                 {
-                    float m[GR];
+                    float m[NR];
 #pragma unroll
-                    for (int r = 0; r < GR; ++r) m[r] = t[r] * sc[r];
-                    across<GR, true>(m, lane);
-                    wm[first_of<GR>(lane)] = m[0];
+                    for (int r = 0; r < NR; ++r) m[r] = t[r] * (E4 ? sc[r] : a.scale_log2);
+                    across<NR, true>(m, lane);
+                    reinterpret_cast<float *>(pb)[warp * NR + first_of<NR>(lane)] = m[0];
                 }
                 if (meet_count<128>(id, failed) >= 32) return;
-                if (tid < GR) {
-                    const float *all = reinterpret_cast<const float *>(pb);
-                    const float was = j == 0 ? -INFINITY : top, ref = refs[tid];
+                if (tid < NR) {
+                    const float was = mine == 0 ? -INFINITY : top, old = ref[tid];
                     float m = was;
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) m = fmaxf(m, all[w * GR + tid]);
+                    for (int w = 0; w < 4; ++w) m = fmaxf(m, reinterpret_cast<const float *>(pb)[w * NR + tid]);
                     // a row that had seen nothing has zeros in O and in its sums, and a reference
                     // that its first score will be far above
-                    const float next = m == -INFINITY ? NOTHING : was == -INFINITY ? m : fmaxf(m, ref);
-                    corrs[tid] = was == -INFINITY ? 0.f : ex2(ref - next);
-                    refs[tid] = next;
+                    const float next = m == -INFINITY ? NOTHING : was == -INFINITY ? m : fmaxf(m, old);
+                    fac[tid] = was == -INFINITY ? 0.f : ex2(old - next);
+                    ref[tid] = next;
                     top = m;
                 }
                 if (meet_count<128>(id, failed) >= 32) return;
-                if (j > 0) {
-                    if (!gate(&bar.pv_done[b ^ 1], ((n - 1) >> 1) & 1)) failed = true;  // the last product must have left O
+                if (mine > 0) {
                     tc_fence_after();
 #pragma unroll 1
-                    for (int c = 0; c < GR; c += 16) {
+                    for (int c = 0; c < NR; c += 16) {
                         float o[16];
                         uint32_t w[16];
-                        tmem_ld16(to + c, o);
+                        tmem_ld16(to + g * NR + c, o);
                         tmem_ld_wait();
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             asm volatile("" : "+f"(o[i]));
-                            w[i] = __float_as_uint(o[i] * corrs[c + i]);
+                            w[i] = __float_as_uint(o[i] * fac[c + i]);
                         }
-                        tmem_st16(to + c, w);
+                        tmem_st16(to + g * NR + c, w);
                     }
                     tmem_st_wait();
 #pragma unroll
-                    for (int r = 0; r < GR; ++r) l[r] *= corrs[r];
+                    for (int r = 0; r < NR; ++r) l[r] *= fac[r];
                 }
+                exponents();
             }
-            uint32_t p[GR / 2];
+            uint32_t p[NR / 2];
 #pragma unroll
-            for (int r = 0; r < GR; r += 4) {
-                const float4 f = *reinterpret_cast<const float4 *>(sc + r), g = *reinterpret_cast<const float4 *>(refs + r);
-                const float e0 = ex2(fmaf(t[r], f.x, -g.x)), e1 = ex2(fmaf(t[r + 1], f.y, -g.y));
-                const float e2 = ex2(fmaf(t[r + 2], f.z, -g.z)), e3 = ex2(fmaf(t[r + 3], f.w, -g.w));
+            for (int r = 0; r < NR; r += 2) {
+                const float e0 = ex2(t[r]), e1 = ex2(t[r + 1]);
                 l[r] += e0;
                 l[r + 1] += e1;
-                l[r + 2] += e2;
-                l[r + 3] += e3;
                 p[r / 2] = E4 ? pack_f16(e0, e1) : pack_bf16(e0, e1);
-                p[r / 2 + 1] = E4 ? pack_f16(e2, e3) : pack_bf16(e2, e3);
             }
             // [key][row], blocks of 16 rows, the two 16-byte halves swapped on every other group of four keys
 #pragma unroll
-            for (int c = 0; c < GR / 8; ++c)
+            for (int c = 0; c < NR / 8; ++c)
                 *reinterpret_cast<uint4 *>(pb + (c >> 1) * BK * 32 + tid * 32 + (((c & 1) ^ ((tid >> 2) & 1)) << 4)) =
                     make_uint4(p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]);
             if (!E4) {
                 // a row of V that no key stands in may hold anything: zero it (0 x NaN is NaN)
                 const bool none = key >= hi || key < (lo & ~(a.box - 1));
                 if (__any_sync(0xffffffffu, none)) {
-                    if (!gate(&bar.v_full[n % C::VS], (n / C::VS) & 1)) failed = true;
-                    uint8_t *vt = sm + C::OFF_V + (n % C::VS) * TILE + tid * 128;
+                    const int v = n + j;
+                    if (!gate(&bar.v_full[v % C::VS], (v / C::VS) & 1)) failed = true;
+                    uint8_t *vt = sm + C::OFF_V + (v % C::VS) * TILE + tid * 128;
                     if (none) {
 #pragma unroll
                         for (int c = 0; c < 16; ++c)
@@ -777,63 +793,88 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
             fence_async_smem();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.p_ready[b]);
+            if (lane == 0) mbar_arrive(&bar.p_ready[g]);
         }
+        n += nt;
 
-        // ---- the segment's end: sums over the keys, then O, normalised or as a piece
-        // (a thread has one channel of every row)
+        // ---- the segment's end: the groups' sums and O merged, normalised or as a piece
         const bool whole = sg->whole;
         const int h = sg->h;
         float *slot = paged_slot(a, sg->slot);
-        if (nt > 0) {
-            if (!gate(&bar.pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1)) failed = true;
-            tc_fence_after();
-            float *all = reinterpret_cast<float *>(sm + C::OFF_P + grp * (GR >> 4) * BK * 32);  // [warp][row], over P: its products are done
-            across<GR, false>(l, lane);
-            all[warp * GR + first_of<GR>(lane)] = l[0];
-            if (meet_count<128>(id, failed) >= 32) return;
-        }
+        float *f0 = reinterpret_cast<float *>(sm + C::OFF_MRG), *f1 = f0 + NR;
         const int64_t out0 = (int64_t)sg->tok * a.Hq + h * G;  // row rr = r0 + r of the token's heads, the next token Hq on
-        if (tid < R) {
-            float L = 0.f;
-            if (nt > 0) {
-                const float *all = reinterpret_cast<const float *>(sm + C::OFF_P + grp * (GR >> 4) * BK * 32);
+        if (nt > 0) {
+            if (mine > 0 && !gate(&bar.pv_done[g], (k - 1) & 1)) failed = true;
+            across<NR, false>(l, lane);
+            sums[(g * 4 + warp) * NR + first_of<NR>(lane)] = l[0];
+            tc_fence_before();
+            together();
+            tc_fence_after();
+            if (g == 0 && tid < NR) {
+                float L0 = 0.f, L1 = 0.f;
 #pragma unroll
-                for (int w = 0; w < 4; ++w) L += all[w * GR + tid];
+                for (int w = 0; w < 4; ++w) {
+                    L0 += sums[w * NR + tid];
+                    L1 += sums[(4 + w) * NR + tid];
+                }
+                const float m0 = L0 == 0.f ? -INFINITY : refs[tid], m1 = L1 == 0.f ? -INFINITY : refs[NR + tid];
+                const float m = fmaxf(m0, m1), base = m == -INFINITY ? 0.f : m;
+                const float e0 = L0 == 0.f ? 0.f : ex2(m0 - base), e1 = L1 == 0.f ? 0.f : ex2(m1 - base);
+                const float L = e0 * L0 + e1 * L1, s = L == 0.f ? 0.f : whole ? (E4 ? a.v_scale[h] : 1.f) / L : 1.f;
+                f0[tid] = e0 * s;
+                f1[tid] = e1 * s;
+                if (tid < R) {
+                    if (!whole) {
+                        reinterpret_cast<float2 *>(slot)[tid] = make_float2(L == 0.f ? -INFINITY : base, L);
+                    } else if (a.lse) {
+                        const int rr = r0 + tid, jt = rr / G;
+                        a.lse[out0 + (int64_t)jt * a.Hq + rr - jt * G] =
+                            L == 0.f ? -INFINITY : (base + log2f(L)) * 0.6931471805599453f;
+                    }
+                }
             }
-            const float ref = nt > 0 ? refs[tid] : 0.f;
-            corrs[tid] = L == 0.f ? 0.f : whole ? (E4 ? a.v_scale[h] : 1.f) / L : 1.f;
+            together();
+        } else if (g == 0 && tid < R) {
             if (!whole) {
-                reinterpret_cast<float2 *>(slot)[row0 + tid] = make_float2(L == 0.f ? -INFINITY : ref, L);
+                reinterpret_cast<float2 *>(slot)[tid] = make_float2(-INFINITY, 0.f);
             } else if (a.lse) {
                 const int rr = r0 + tid, jt = rr / G;
-                a.lse[out0 + (int64_t)jt * a.Hq + rr - jt * G] = L == 0.f ? -INFINITY : (ref + log2f(L)) * 0.6931471805599453f;
+                a.lse[out0 + (int64_t)jt * a.Hq + rr - jt * G] = -INFINITY;
             }
         }
-        if (meet_count<128>(id, failed) >= 32) return;
-        const int j0 = r0 / G;
-        int hh = r0 - j0 * G;  // head within the token's group
-        int64_t at = (out0 + (int64_t)j0 * a.Hq + hh) * D + tid;
-#pragma unroll 1
-        for (int c = 0; c < R; c += 16) {
-            float o[16];
+        {  // a thread has one channel of every row; group g writes the rows from NR / 2 g on
+            const int rb = g * (NR / 2), j0 = (r0 + rb) / G;
+            int hh = r0 + rb - j0 * G;  // head within the token's group
+            int64_t at = (out0 + (int64_t)j0 * a.Hq + hh) * D + tid;
+            float o[16], q[16];  // the groups' O (where a group had no tile its factor is zero)
+            const int c = NR == 32 ? rb : 0;
             tmem_ld16(to + c, o);
+            tmem_ld16(to + NR + c, q);
             tmem_ld_wait();
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 asm volatile("" : "+f"(o[i]));
-                if (c + i < R) {
-                    const float f = corrs[c + i], y = f == 0.f ? 0.f : o[i] * f;  // (nothing seen: zero whatever O holds)
-                    if (whole) {
-                        reinterpret_cast<__nv_bfloat16 *>(a.o)[at] = __float2bfloat16_rn(y);
-                        at += D;
-                        if (++hh == G) {
-                            hh = 0;
-                            at += (int64_t)(a.Hq - G) * D;
-                        }
-                    } else {
-                        slot[2 * a.slot_rows + (row0 + c + i) * D + tid] = y;
+                asm volatile("" : "+f"(q[i]));
+            }
+#pragma unroll
+            for (int i = 0; i < NR / 2; ++i) {
+                const int r = rb + i;
+                if (r >= R) break;
+                const float u = NR == 16 && g ? o[(i + 8) & 15] : o[i], w = NR == 16 && g ? q[(i + 8) & 15] : q[i];
+                float y = 0.f;
+                if (nt > 0) {
+                    if (f0[r] != 0.f) y = u * f0[r];  // (nothing seen: zero whatever O holds)
+                    if (f1[r] != 0.f) y += w * f1[r];
+                }
+                if (whole) {
+                    reinterpret_cast<__nv_bfloat16 *>(a.o)[at] = __float2bfloat16_rn(y);
+                    at += D;
+                    if (++hh == G) {
+                        hh = 0;
+                        at += (int64_t)(a.Hq - G) * D;
                     }
+                } else {
+                    slot[2 * a.slot_rows + r * D + tid] = y;
                 }
             }
         }
@@ -847,10 +888,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
             if (nt > 0) mbar_arrive(&bar.o_free[item & 1]);
             mbar_arrive(&bar.seg_empty[iseg % SEGS]);
         }
-        // (refs and the sums are written again only past the next meeting; corrs too, unless
-        // an item without tiles follows)
         if (nt > 0) ++item;
-        else if (meet_count<128>(id, failed) >= 32) return;
     }
 }
 
@@ -871,18 +909,18 @@ __global__ void __launch_bounds__(Cfg<E4, NR>::THREADS, 1)
             mbar_init(&bar.k_empty[i], 1);
         }
         for (int i = 0; i < C::VS; ++i) {
-            mbar_init(&bar.v_full[i], E4 ? WIDEN : 1);
+            mbar_init(&bar.v_full[i], E4 ? C::WIDEN : 1);
             mbar_init(&bar.v_empty[i], 1);
         }
         for (int i = 0; i < C::RS; ++i) {
             mbar_init(&bar.r_full[i], 1);
-            mbar_init(&bar.r_empty[i], WIDEN);
+            mbar_init(&bar.r_empty[i], C::WIDEN);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.q_full[i], 1);
             mbar_init(&bar.q_empty[i], 1);
             mbar_init(&bar.s_full[i], 1);
-            mbar_init(&bar.p_ready[i], C::SOFT);
+            mbar_init(&bar.p_ready[i], C::SOFT / 2);
             mbar_init(&bar.pv_done[i], 1);
             mbar_init(&bar.o_free[i], C::SOFT);
         }
@@ -892,6 +930,7 @@ __global__ void __launch_bounds__(Cfg<E4, NR>::THREADS, 1)
         }
         mbar_init(bar.last, 1);
         mbar_init(bar.last + 1, 1);
+        mbar_init(bar.joint, C::SOFT);
         mbar_fence_init();
         sh->abort = 0;
         a.lead[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
@@ -980,8 +1019,7 @@ int launch_paged_few(PagedAttn a, int cache_dtype, const void *k, const void *v,
     if (rc) return rc;
     const bool e4 = cache_dtype == KDA_E4M3;
     if (max_rows <= 16) return e4 ? launch<true, 16>(a, maps, s) : launch<false, 16>(a, maps, s);
-    if (max_rows <= 32) return e4 ? launch<true, 32>(a, maps, s) : launch<false, 32>(a, maps, s);
-    return e4 ? launch<true, 64>(a, maps, s) : launch<false, 64>(a, maps, s);
+    return e4 ? launch<true, 32>(a, maps, s) : launch<false, 32>(a, maps, s);
 }
 
 }  // namespace kda
