@@ -30,7 +30,7 @@ struct PagedAttn {
     int n_seqs, T, max_q, Hq, Hkv, G, page_size, n_pages, max_blocks, window;
     float scale_log2;                // sm_scale * log2(e)
     int row_lo, row_hi;              // this launch takes the requests with row_lo < rows <= row_hi
-    int box;                         // keys that one copy takes from a page (a power of two, divides page_size)
+    int box, box_log;                // keys that one copy takes from a page (a power of two, divides page_size)
     // pieces: lead[c] describes the item whose first piece block c left last;
     // slot 2 c is the piece of block c's first segment, 2 c + 1 of its last
     int4 *lead;

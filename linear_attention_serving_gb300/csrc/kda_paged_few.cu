@@ -319,10 +319,11 @@ __device__ __forceinline__ void load_role(const PagedAttn &a, const PagedMaps &m
     constexpr int ES = E4 ? 1 : 2, NV = E4 ? C::RS : C::VS;
     const int lane = threadIdx.x & 31;
     const Bars<C> bar(sm);
-    const int box = a.box, nbx = BK / box;
+    const int box = a.box, lg = a.box_log, nbx = BK >> lg;
     uint64_t *vf = E4 ? bar.r_full : bar.v_full, *ve = E4 ? bar.r_empty : bar.v_empty;
     uint8_t *kb = sm + C::OFF_K, *vb = sm + (E4 ? C::OFF_R : C::OFF_V);
-    int nk = 0, nv = 0;    // tiles of K and V so far
+    int nk = 0, nv = 0;                                 // tiles of K and V so far
+    int kslot = 0, kph = 1, vslot = 0, vph = 1;         // their places in the rings, and the parity to wait for
     auto drain = [&]() {   // a wait ran out: let the copies in flight land before the block ends
         for (int u = nk - 1; u >= 0 && u >= nk - C::KS; --u) mbar_wait(&bar.k_full[u % C::KS], (u / C::KS) & 1);
         for (int u = nv - 1; u >= 0 && u >= nv - NV; --u) mbar_wait(&vf[u % NV], (u / NV) & 1);
@@ -333,19 +334,24 @@ __device__ __forceinline__ void load_role(const PagedAttn &a, const PagedMaps &m
         int f, e, page, y, z;  // z: first and one past the last row that holds a key (e4m3)
     };
     auto load = [&](const Tile &t, bool v) -> bool {
-        const int slot = v ? nv % NV : nk % C::KS;
-        if (!gate(v ? &ve[slot] : &bar.k_empty[slot], ((v ? nv / NV : nk / C::KS) & 1) ^ 1)) return false;
+        const int slot = v ? vslot : kslot;
+        if (!gate(v ? &ve[slot] : &bar.k_empty[slot], v ? vph : kph)) return false;
         uint8_t *dst = (v ? vb : kb) + slot * C::KT;
         uint64_t *full = v ? &vf[slot] : &bar.k_full[slot];
         if (E4 && v && lane == 0) reinterpret_cast<int *>(sm + C::OFF_DESC)[slot] = t.z;
-        if (v) ++nv;
-        else ++nk;
-        if (lane == 0) mbar_expect_tx(full, (uint32_t)((t.e - t.f) * box * D * ES));
+        if (v) {
+            ++nv;
+            if (++vslot == NV) vslot = 0, vph ^= 1;
+        } else {
+            ++nk;
+            if (++kslot == C::KS) kslot = 0, kph ^= 1;
+        }
+        if (lane == 0) mbar_expect_tx(full, (uint32_t)((t.e - t.f) << lg) * (D * ES));
         __syncwarp();
         if (lane >= t.f && lane < t.e) {
             const CUtensorMap *m = v ? &maps.v : &maps.k;
-            tma_load_3d(dst + lane * box * 128, m, 0, t.y, t.page, full);
-            if (!E4) tma_load_3d(dst + TILE / 2 + lane * box * 128, m, 64, t.y, t.page, full);
+            tma_load_3d(dst + (lane << lg) * 128, m, 0, t.y, t.page, full);
+            if (!E4) tma_load_3d(dst + TILE / 2 + (lane << lg) * 128, m, 64, t.y, t.page, full);
         }
         __syncwarp();
         return true;
@@ -356,16 +362,17 @@ __device__ __forceinline__ void load_role(const PagedAttn &a, const PagedMaps &m
     bool have = false;
     while (next_seg<C>(sm, bar, iseg, gate, s)) {
         if (s.nt == 0) continue;
-        int cbase = 0, page = 0;
+        int cbase = 0, page = 0, off = 0;
         const int lob = s.lo & ~(box - 1);  // boxes before this one hold no seen key (their pages may be gone)
         for (int j = 0; j < s.nt; ++j) {
-            const int key0 = (s.t0 + j) * BK, b0 = key0 / box;
+            const int key0 = (s.t0 + j) * BK, b0 = key0 >> lg;
             if (j == 0 || b0 + nbx > cbase + 32) {  // pages of the next 32 boxes, one per lane
                 cbase = b0;
-                const int key = (cbase + lane) * box;
+                const int key = (cbase + lane) << lg, blk = key / a.page_size;
                 page = 0;
+                off = s.h * a.page_size + key - blk * a.page_size;
                 if (key >= lob && key < s.hi) {
-                    page = a.table[(int64_t)s.req * a.max_blocks + key / a.page_size];
+                    page = a.table[(int64_t)s.req * a.max_blocks + blk];
                     if (page < 0 || page >= a.n_pages) {
                         if (a.err) atomicOr(a.err, KDA_DEVERR_PAGE);
                         page = 0;
@@ -373,10 +380,10 @@ __device__ __forceinline__ void load_role(const PagedAttn &a, const PagedMaps &m
                 }
             }
             Tile t;
-            t.f = max(0, (lob - key0) / box);
-            t.e = min(nbx, (s.hi - key0 + box - 1) / box);
+            t.f = max(0, (lob - key0) >> lg);
+            t.e = min(nbx, (s.hi - key0 + box - 1) >> lg);
             t.page = __shfl_sync(0xffffffffu, page, (b0 - cbase + lane) & 31);
-            t.y = s.h * a.page_size + (key0 + lane * box) % a.page_size;
+            t.y = __shfl_sync(0xffffffffu, off, (b0 - cbase + lane) & 31);
             t.z = max(0, lob - key0) | (min(BK, s.hi - key0) << 8);
             if (!load(t, false)) return drain();
             if (have && !load(prev, true)) return drain();
@@ -386,11 +393,10 @@ __device__ __forceinline__ void load_role(const PagedAttn &a, const PagedMaps &m
     }
     if (have && !*gate.abort && !load(prev, true)) return drain();
     if (E4) {  // the end, for the widening warps
-        const int slot = nv % NV;
-        if (!gate(&ve[slot], ((nv / NV) & 1) ^ 1)) return drain();
+        if (!gate(&ve[vslot], vph)) return drain();
         if (lane == 0) {
-            reinterpret_cast<int *>(sm + C::OFF_DESC)[slot] = -1;
-            mbar_arrive(&vf[slot]);
+            reinterpret_cast<int *>(sm + C::OFF_DESC)[vslot] = -1;
+            mbar_arrive(&vf[vslot]);
         }
         __syncwarp();
     }
@@ -1014,6 +1020,7 @@ int launch_paged_few(PagedAttn a, int cache_dtype, const void *k, const void *v,
     int box = 16;
     while (box < BK && a.page_size % (2 * box) == 0) box *= 2;
     a.box = box;
+    a.box_log = __builtin_ctz(box);
     PagedMaps maps;
     const int rc = make_paged_maps(k, v, cache_dtype, a.Hkv, a.page_size, a.n_pages, page_stride, box, &maps);
     if (rc) return rc;

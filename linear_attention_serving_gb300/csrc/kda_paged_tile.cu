@@ -300,7 +300,7 @@ __device__ __forceinline__ bool next_seg(uint8_t *sm, const Bars &bar, int &i, c
 __device__ __forceinline__ void load_role(const PagedAttn &a, const PagedMaps &maps, uint8_t *sm, const Gate &gate) {
     const int lane = threadIdx.x & 31;
     const Bars bar(sm);
-    const int box = a.box, nbx = BK / box;
+    const int box = a.box, lg = a.box_log, nbx = BK >> lg;
     int ring = 0, ringp = 0;
     uint32_t seq = 0;  // K / V tiles so far
     auto drain = [&]() {  // a wait ran out: let the copies in flight land before the block ends
@@ -311,17 +311,18 @@ __device__ __forceinline__ void load_role(const PagedAttn &a, const PagedMaps &m
     int iseg = 0;
     while (next_seg(sm, bar, iseg, gate, s)) {
         if (s.nt == 0) continue;
-        int cbase = -64, page = 0;
+        int cbase = -64, page = 0, off = 0;
         const int lob = s.lo & ~(box - 1);  // boxes before this one hold no seen key (their pages may be gone)
         // one K or V tile
         auto tile = [&](int j, bool v) -> bool {
-            const int key0 = (s.t0 + j) * BK, b0 = key0 / box;
+            const int key0 = (s.t0 + j) * BK, b0 = key0 >> lg;
             if (cbase < 0 || b0 < cbase || b0 + nbx > cbase + 32) {  // pages of the next 32 boxes, one per lane
                 cbase = b0;
-                const int key = (cbase + lane) * box;
+                const int key = (cbase + lane) << lg, blk = key / a.page_size;
                 page = 0;
+                off = s.h * a.page_size + key - blk * a.page_size;
                 if (key >= lob && key < s.hi) {
-                    page = a.table[(int64_t)s.req * a.max_blocks + key / a.page_size];
+                    page = a.table[(int64_t)s.req * a.max_blocks + blk];
                     if (page < 0 || page >= a.n_pages) {
                         if (a.err) atomicOr(a.err, KDA_DEVERR_PAGE);
                         page = 0;
@@ -330,13 +331,13 @@ __device__ __forceinline__ void load_role(const PagedAttn &a, const PagedMaps &m
             }
             const int slot = ring;
             if (!gate(&bar.kv_empty[slot], ringp ^ 1)) return false;
-            const int f = max(0, (lob - key0) / box), e = min(nbx, (s.hi - key0 + box - 1) / box);
-            if (lane == 0) mbar_expect_tx(&bar.kv_full[slot], (uint32_t)((e - f) * box * D * 2));
+            const int f = max(0, (lob - key0) >> lg), e = min(nbx, (s.hi - key0 + box - 1) >> lg);
+            if (lane == 0) mbar_expect_tx(&bar.kv_full[slot], (uint32_t)((e - f) << lg) * (D * 2));
             __syncwarp();
             const int pg = __shfl_sync(0xffffffffu, page, (b0 - cbase + lane) & 31);
+            const int y = __shfl_sync(0xffffffffu, off, (b0 - cbase + lane) & 31);
             if (lane >= f && lane < e) {
-                const int key = key0 + lane * box, y = s.h * a.page_size + key % a.page_size;
-                uint8_t *dst = sm + OFF_KV + slot * SLOT + lane * box * 128;
+                uint8_t *dst = sm + OFF_KV + slot * SLOT + (lane << lg) * 128;
                 const CUtensorMap *m = v ? &maps.v : &maps.k;
                 tma_load_3d(dst, m, 0, y, pg, &bar.kv_full[slot]);
                 tma_load_3d(dst + SLOT / 2, m, 64, y, pg, &bar.kv_full[slot]);
@@ -802,6 +803,7 @@ int launch_paged_tile(PagedAttn a, const void *k, const void *v, int64_t page_st
     int box = 16;
     while (box < BK && a.page_size % (2 * box) == 0) box *= 2;
     a.box = box;
+    a.box_log = __builtin_ctz(box);
     const int th = BM / a.G;
     PagedMaps maps;
     CUtensorMap qmap;
