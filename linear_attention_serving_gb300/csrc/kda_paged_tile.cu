@@ -36,7 +36,7 @@ constexpr int OFF_Q = 0;
 constexpr int OFF_KV = 2 * QHALF;
 constexpr int OFF_SCAN = OFF_KV + SLOTS * SLOT;  // the start's sums
 constexpr int OFF_BAR = OFF_SCAN + 256;
-constexpr int NBAR = 2 * SLOTS + 17 + 2 * 4;
+constexpr int NBAR = 2 * SLOTS + 19 + 2 * 4;
 constexpr int SEGS = 4;                        // ring of segments ahead of the roles
 constexpr int OFF_MISC = (OFF_BAR + NBAR * 8 + 63) / 64 * 64;  // TMEM address, abort flag, start of the block's line
 constexpr int OFF_SEG = OFF_MISC + 64;
@@ -54,7 +54,7 @@ constexpr uint32_t COL_S = 0, COL_O = 256;     // + 128 w
 constexpr float GROW = 8.f;                    // log2 growth of a maximum that ref follows
 
 struct Bars {
-    uint64_t *kv_full, *kv_empty, *q_full, *q_empty, *s_full, *p_ready, *pv_done, *o_free, *last, *seg_full, *seg_empty;
+    uint64_t *kv_full, *kv_empty, *q_full, *q_empty, *s_full, *p_ready, *pv_done, *o_free, *last, *turn, *seg_full, *seg_empty;
     __device__ explicit Bars(uint8_t *sm) {
         uint64_t *b = reinterpret_cast<uint64_t *>(sm + OFF_BAR);
         kv_full = b;
@@ -69,7 +69,8 @@ struct Bars {
         pv_done = p_ready + 3;       // [3]
         o_free = pv_done + 3;        // [2]
         last = o_free + 2;           // [2] products in flight when a wait ran out
-        seg_full = last + 2;
+        turn = last + 2;             // [2] the other group's probabilities are done
+        seg_full = turn + 2;
         seg_empty = seg_full + SEGS;
     }
 };
@@ -643,6 +644,12 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
                 }
                 fence_async_smem();
             }
+            // The groups work out their probabilities in turn: left to themselves they
+            // drift into step, and the tensor cores then wait for both at once.
+            if (!alt) {
+                const int k = n0 + (e >> 1);  // this group's tiles of two halves so far
+                if (x ? !gate(&bar.turn[1], k & 1) : k > 0 && !gate(&bar.turn[0], (k - 1) & 1)) failed = true;
+            }
             // probabilities, 32 at a time over S's own columns
             const uint64_t sc2 = pack2(sc, sc), ref2 = pack2(-ref, -ref);
             uint64_t sum2 = 0;
@@ -664,7 +671,10 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.p_ready[b]);
+            if (lane == 0) {
+                mbar_arrive(&bar.p_ready[b]);
+                if (!alt) mbar_arrive(&bar.turn[x ^ 1]);
+            }
             float l0, l1;
             unpack2(sum2, l0, l1);
             l += l0 + l1;
@@ -711,6 +721,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(&bar.q_full[i], 1);
             mbar_init(&bar.q_empty[i], 2);
             mbar_init(&bar.o_free[i], 8);
+            mbar_init(&bar.turn[i], SOFT / 2);
         }
         for (int i = 0; i < 3; ++i) {
             mbar_init(&bar.s_full[i], 1);
