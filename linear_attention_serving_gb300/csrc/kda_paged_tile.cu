@@ -548,6 +548,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
     float *mx = reinterpret_cast<float *>(sm + OFF_MX) + x * 2 * BM + row;  // + BM hf
     const float sc = a.scale_log2;
     int n0 = 0, n2 = 0;  // this group's events by barrier: its own, and the first group's on the second buffer
+    int nboth = 0;       // tiles of two halves
     uint32_t seq0 = 0;  // K / V tiles before this segment's
     bool failed = false;
     for (int iseg = 0;; ++iseg) {
@@ -647,7 +648,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
             // The groups work out their probabilities in turn: left to themselves they
             // drift into step, and the tensor cores then wait for both at once.
             if (!alt) {
-                const int k = n0 + (e >> 1);  // this group's tiles of two halves so far
+                const int k = nboth + j;
                 if (x ? !gate(&bar.turn[1], k & 1) : k > 0 && !gate(&bar.turn[0], (k - 1) & 1)) failed = true;
             }
             // probabilities, 32 at a time over S's own columns
@@ -682,7 +683,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
             prevp = ph;
         }
         seq0 += 2 * s.nt;
-        if (!alt) n0 += s.nt;
+        if (!alt) n0 += s.nt, nboth += s.nt;
         else if (x == 0) n0 += (s.nt + 1) / 2, n2 += s.nt / 2;
         if (!(alt && x)) {
             float sum = 0.f;

@@ -207,6 +207,15 @@ def test_attn_row_tiles_split(new, ctx):
     attn_close(o, lse, attn_ref(d["q"], d["k_cache"], d["v_cache"], d["table"], d["cu"], d["kv"]), BF16, BF16)
 
 
+def test_attn_row_tiles_of_both_kinds_in_one_block():
+    """So many items that each block has several of one half and of two halves in turn."""
+    new, ctx = [70, 20, 64, 33, 1, 90] * 25, [10, 150, 0, 300, 40, 5] * 25
+    d = make(new, ctx, 2, 4, 16, BF16, seed=7)
+    o, lse, e = run_attn(d, max_q=max(new))
+    assert e == 0
+    attn_close(o, lse, attn_ref(d["q"], d["k_cache"], d["v_cache"], d["table"], d["cu"], d["kv"]), BF16, BF16)
+
+
 def test_attn_row_tiles_rising_scores():
     """Scores that grow with the key: the running maximum moves at every tile."""
     d = make([3], [1500], 1, 16, 32, BF16, q_std=1.0)
