@@ -94,29 +94,21 @@ __device__ __forceinline__ PagedLine paged_line(const PagedAttn &a, int64_t *scr
     constexpr int W = NTHR / 32;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     int64_t *found = scratch + W;
-    // this thread's requests: the first round's count stays in a register
     int err = 0;
-    int64_t first = tid < a.n_seqs ? units(tid, &err) : 0, sum = first;
-    for (int i = tid + NTHR; i < a.n_seqs; i += NTHR) sum += units(i, &err);
+    int64_t first = tid < a.n_seqs ? units(tid, &err) : 0, total = 0;
+    if (a.n_seqs > NTHR) {  // the line's length, when one round does not see all requests
+        int64_t sum = first;
+        for (int i = tid + NTHR; i < a.n_seqs; i += NTHR) sum += units(i, &err);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == 0) scratch[warp] = sum;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < W; ++w) total += scratch[w];
+        __syncthreads();
+    }
     if (err && blockIdx.x == 0 && a.err) atomicOr(a.err, err);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) scratch[warp] = sum;
-    __syncthreads();
-    sum = 0;
-#pragma unroll
-    for (int w = 0; w < W; ++w) sum += scratch[w];
-    __syncthreads();
     PagedLine r;
-    // (units fit 32 bits in all but the longest lines: a short division)
-    r.per = sum < INT32_MAX ? (int64_t)(((uint32_t)sum + gridDim.x - 1) / gridDim.x) : (sum + gridDim.x - 1) / gridDim.x;
-    if (r.per < min_per) r.per = min_per;
-    r.per = (r.per + even - 1) / even * even;
-    r.P0 = (int64_t)blockIdx.x * r.per;
-    r.P1 = r.P0 + r.per < sum ? r.P0 + r.per : sum;
-    r.req = 0;
-    r.before = r.units = 0;
-    if (r.P0 >= r.P1) return r;
     int64_t carry = 0;
     for (int base = 0;; base += NTHR) {
         const int i = base + tid;
@@ -131,6 +123,19 @@ __device__ __forceinline__ PagedLine paged_line(const PagedAttn &a, int64_t *scr
             if (w < warp) off += scratch[w];
             all += scratch[w];
         }
+        if (base == 0) {
+            if (a.n_seqs <= NTHR) total = all;
+            // (units fit 32 bits in all but the longest lines: a short division)
+            r.per = total < INT32_MAX ? (int64_t)(((uint32_t)total + gridDim.x - 1) / gridDim.x)
+                                      : (total + gridDim.x - 1) / gridDim.x;
+            if (r.per < min_per) r.per = min_per;
+            r.per = (r.per + even - 1) / (uint32_t)even * even;
+            r.P0 = (int64_t)blockIdx.x * r.per;
+            r.P1 = r.P0 + r.per < total ? r.P0 + r.per : total;
+            r.req = 0;
+            r.before = r.units = 0;
+            if (r.P0 >= r.P1) return r;
+        }
         if (r.P0 >= off + inc - t && r.P0 < off + inc) {
             found[0] = i;
             found[1] = off + inc - t;
@@ -144,7 +149,6 @@ __device__ __forceinline__ PagedLine paged_line(const PagedAttn &a, int64_t *scr
     r.req = (int)found[0];
     r.before = found[1];
     r.units = found[2];
-    __syncthreads();
     return r;
 }
 

@@ -61,9 +61,8 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) paged_join_kernel(PagedAttn a
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const JoinSet &js = (int)blockIdx.x < s0.blocks ? s0 : s1;
     const int c = (int)blockIdx.x < s0.blocks ? blockIdx.x : blockIdx.x - s0.blocks;
-    const int4 y = js.lead[2 * c + 1];
+    const int4 y = js.lead[2 * c + 1], x = js.lead[2 * c];
     if (!y.w) return;
-    const int4 x = js.lead[2 * c];
     a.parts = js.parts;
     a.slot_rows = js.slot_rows;
     const int h = x.y, r0 = x.z, R = x.w, c0 = y.y, np = y.z - y.y + 1;
@@ -73,21 +72,37 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) paged_join_kernel(PagedAttn a
     const int step = few ? 1 : JOIN_WARPS, p0 = few ? 0 : warp;
     for (int r = few ? blockIdx.y * JOIN_WARPS + warp : blockIdx.y; r < R; r += gridDim.y * (few ? JOIN_WARPS : 1)) {
         float M = -INFINITY, L = 0.f;
-#pragma unroll 4
-        for (int p = p0; p < np; p += step) M = fmaxf(M, reinterpret_cast<const float2 *>(slot(p))[r].x);
-        const float ref = M == -INFINITY ? 0.f : M;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int p = p0; p < np; p += step) {
-            const float *sp = slot(p);
-            const float2 ml = reinterpret_cast<const float2 *>(sp)[r];
-            const float4 v = reinterpret_cast<const float4 *>(sp + 2 * a.slot_rows)[r * (D / 4) + lane];
-            const float f = tc::ex2(ml.x - ref);
-            L += f * ml.y;
-            acc.x += f * v.x;
-            acc.y += f * v.y;
-            acc.z += f * v.z;
-            acc.w += f * v.w;
+        // four pieces at a time, all their loads in flight at once
+        for (int p = p0; p < np; p += 4 * step) {
+            float2 ml[4];
+            float4 v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bool have = p + i * step < np;
+                const float *sp = slot(have ? p + i * step : p);
+                ml[i] = reinterpret_cast<const float2 *>(sp)[r];
+                v[i] = reinterpret_cast<const float4 *>(sp + 2 * a.slot_rows)[r * (D / 4) + lane];
+                if (!have) ml[i] = make_float2(-INFINITY, 0.f);
+            }
+            const float m = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), M);
+            const float ref = m == -INFINITY ? 0.f : m, f0 = tc::ex2(M - ref);
+            L *= f0;
+            acc.x *= f0;
+            acc.y *= f0;
+            acc.z *= f0;
+            acc.w *= f0;
+            M = m;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (ml[i].x == -INFINITY) continue;  // (what an empty piece holds has no say)
+                const float f = tc::ex2(ml[i].x - ref);
+                L += f * ml[i].y;
+                acc.x += f * v[i].x;
+                acc.y += f * v[i].y;
+                acc.z += f * v[i].z;
+                acc.w += f * v[i].w;
+            }
         }
         if (!few) {
             acc_s[warp][lane] = acc;

@@ -53,7 +53,7 @@ template <bool E4, int NR> struct Cfg {
                          OFF_P = OFF_Q + 2 * QB, OFF_REF = OFF_P + 2 * PB, OFF_FAC = OFF_REF + 2 * NR * 4,
                          OFF_MRG = OFF_FAC + 2 * NR * 4, OFF_SUM = OFF_MRG + 2 * NR * 4, OFF_SC = OFF_SUM + 8 * NR * 4, OFF_SEG = OFF_SC + SEGS * NR * 4,
                          OFF_DESC = OFF_SEG + SEGS * 64, OFF_BAR = OFF_DESC + 32;
-    static constexpr int NBAR = 2 * (KS + VS + RS) + 4 + 8 + 3 + 2 * SEGS;
+    static constexpr int NBAR = 2 * (KS + VS + RS) + 4 + 8 + 3 + 3 * SEGS;
     static constexpr int OFF_MISC = (OFF_BAR + NBAR * 8 + 15) / 16 * 16, SMEM = OFF_MISC + 64;
     static constexpr int THREADS = (W_WIDEN + WIDEN) * 32;
     static constexpr int TCOLS = NR == 16 ? 128 : 256;        // S [2][NR], O [item parity][group][NR]
@@ -62,7 +62,7 @@ template <bool E4, int NR> struct Cfg {
 
 template <class C> struct Bars {
     uint64_t *k_full, *k_empty, *v_full, *v_empty, *r_full, *r_empty, *q_full, *q_empty, *s_full, *p_ready, *pv_done, *o_free,
-        *last, *joint, *seg_full, *seg_empty;
+        *last, *joint, *seg_full, *seg_ready, *seg_empty;
     __device__ explicit Bars(uint8_t *sm) {
         k_full = reinterpret_cast<uint64_t *>(sm + C::OFF_BAR);
         k_empty = k_full + C::KS;
@@ -79,7 +79,8 @@ template <class C> struct Bars {
         last = o_free + 2;
         joint = last + 2;          // (last: products in flight when a wait ran out)
         seg_full = joint + 1;      // (joint: the two groups at an item's end)
-        seg_empty = seg_full + SEGS;
+        seg_ready = seg_full + SEGS;  // its queries and their scales are there too
+        seg_empty = seg_ready + SEGS;
     }
 };
 
@@ -172,8 +173,9 @@ struct Walk {
             s.req = req;
             s.whole = b == 0 && stop == B;
             s.slot = 2 * (int)blockIdx.x + (pos == P0 ? 0 : 1);
-            s.c0 = (int)((A + HEAD) / per);
-            s.c1 = (int)((B - 1) / per);
+            s.c0 = A + HEAD >= P0 ? (int)blockIdx.x : -1;  // block of the item's first tile: this one, or one before
+            s.c1 = (int)blockIdx.x;                       // block of its last
+            if (B > end) s.c1 = (int)((B - 1) / per);
             pos = stop;
             if (stop == B) {
                 A = B;
@@ -220,8 +222,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float x, float y) {
 }
 
 // ---------------------------------------------------------------- walk, queries
-// One warp walks the line and puts each item's queries (rows past R zero) into the
-// buffer of its turn before it tells the others of the segment.
+// One warp walks the line, tells the others of each segment (the loads begin on it) and
+// puts its queries (rows past R zero) into the buffer of their turn.
 template <bool E4, int NR>
 __device__ __forceinline__ void walk_role(const PagedAttn &a, uint8_t *sm, Walk w, int64_t P0, const Gate &gate) {
     using C = Cfg<E4, NR>;
@@ -234,6 +236,11 @@ __device__ __forceinline__ void walk_role(const PagedAttn &a, uint8_t *sm, Walk 
         const bool more = w.next(a, rw, NR, P0, s);
         if (!more) s.nt = -1;
         if (!gate(&bar.seg_empty[i % SEGS], ((i / SEGS) & 1) ^ 1)) return;
+        if (lane == 0) {
+            *reinterpret_cast<Seg *>(sm + C::OFF_SEG + (i % SEGS) * 64) = s;
+            mbar_arrive(&bar.seg_full[i % SEGS]);
+        }
+        __syncwarp();
         if (s.nt > 0) {
             const int x = item & 1;
             if (!gate(&bar.q_empty[x], ((item >> 1) & 1) ^ 1)) return;
@@ -300,10 +307,7 @@ __device__ __forceinline__ void walk_role(const PagedAttn &a, uint8_t *sm, Walk 
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.q_full[x]);
         }
-        if (lane == 0) {
-            *reinterpret_cast<Seg *>(sm + C::OFF_SEG + (i % SEGS) * 64) = s;
-            mbar_arrive(&bar.seg_full[i % SEGS]);
-        }
+        if (lane == 0) mbar_arrive(&bar.seg_ready[i % SEGS]);
         __syncwarp();
         if (!more) return;
     }
@@ -667,7 +671,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
         ++joint;
     };
     for (int iseg = 0;; ++iseg) {
-        if (!gate(&bar.seg_full[iseg % SEGS], (iseg / SEGS) & 1)) failed = true;
+        if (!gate(&bar.seg_ready[iseg % SEGS], (iseg / SEGS) & 1)) failed = true;
         if (meet_count<128>(id, failed) >= 32) return;
         const Seg *sg = reinterpret_cast<const Seg *>(sm + C::OFF_SEG + (iseg % SEGS) * 64);
         const int nt = sg->nt;
@@ -932,6 +936,7 @@ __global__ void __launch_bounds__(Cfg<E4, NR>::THREADS, 1)
         }
         for (int i = 0; i < SEGS; ++i) {
             mbar_init(&bar.seg_full[i], 1);
+            mbar_init(&bar.seg_ready[i], 1);
             mbar_init(&bar.seg_empty[i], C::SOFT + 3);
         }
         mbar_init(bar.last, 1);

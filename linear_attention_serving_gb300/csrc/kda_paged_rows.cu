@@ -416,6 +416,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     auto tiles = [&](int i, int *err) { return line_tiles(a, i, err); };
     const PagedLine line = paged_line<THREADS>(a, scratch, min_per, 1, tiles);
     if (line.P0 >= line.P1) return;
+    __syncthreads();  // (the sums stood where the consumers' rows will)
     if (tid >= CONS * 32)
         produce(a, maps, sm, line.P0, line.P1, line.per, line.req, line.before);
     else

@@ -17,6 +17,7 @@ constexpr int KEY_TILE = 128;
 // the same kind of sum on smaller numbers (Euclid's steps on a and m).
 // a (n - 1) + b < 2^32: key positions are below 2^31.
 __device__ __forceinline__ int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
+    if (n == 1) return b / m;
     int64_t s = 0, sign = 1;
     while (n > 0) {
         const uint32_t qa = a / m, qb = b / m;

@@ -169,8 +169,9 @@ struct Walk {
         s.req = req;
         s.whole = b == 0 && stop == B;
         s.slot = 2 * (int)blockIdx.x + (pos == P0 ? 0 : 1);
-        s.c0 = (int)((A + head) / per);
-        s.c1 = (int)((B - 1) / per);
+        s.c0 = A + head >= P0 ? (int)blockIdx.x : -1;  // block of the item's first tile: this one, or one before
+        s.c1 = (int)blockIdx.x;                       // block of its last
+        if (B > end) s.c1 = (int)((B - 1) / per);
         pos = stop;
         if (stop == B) {
             A = B;
