@@ -48,16 +48,25 @@ __device__ __forceinline__ void key_tiles(const PagedAttn &a, const PagedReq &r,
     t0 = lo / KEY_TILE;
     t1 = (hi + KEY_TILE - 1) / KEY_TILE;
 }
-struct Gate {  // bounded waits that stop the whole block when one runs out
+// Bounded waits of a whole converged warp that stop the block when one runs out.  The
+// clock and the abort flag are looked at on every 64th try only: the waits are on the
+// path of every tile.
+struct Gate {
     volatile int *abort;
     int32_t *err;
     __device__ bool operator()(uint64_t *bar, int parity) const {
-        const bool ok = __all_sync(0xffffffffu, mbar_wait_ab(bar, parity, abort));
-        if (!ok && (threadIdx.x & 31) == 0) {
-            *abort = 1;
-            if (err) atomicOr(err, KDA_DEVERR_TIMEOUT);
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        const long long t0 = clock64();
+        for (uint32_t n = 1;; ++n) {
+            if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+            if (n % 64 == 0 && __any_sync(0xffffffffu, *abort || clock64() - t0 > WAIT_BUDGET_CYCLES)) break;
         }
-        return ok;
+        if ((threadIdx.x & 31) == 0) {
+            if (!*abort && err) atomicOr(err, KDA_DEVERR_TIMEOUT);
+            *abort = 1;
+        }
+        __syncwarp();
+        return false;
     }
 };
 

@@ -424,7 +424,7 @@ __device__ __forceinline__ void mma_role(const PagedAttn &a, uint8_t *sm, uint32
         auto qk = [&](int j) {  // S of key tile j, into this warp's buffer or, for one half, both in turn
             const int buf = alt ? j & 1 : x;
             issue_qk(tmem + COL_S + buf * 128, q, dk + (uint32_t)kslot * (SLOT >> 4), ID_QK);
-            mma_commit_w(&bar.s_full[alt && buf ? 2 : buf]);
+            mma_commit_w(&bar.s_full[alt && buf ? 2 : buf]);  // (first: it is waited for; a commit covers all before it)
             mma_commit_w(&bar.kv_empty[kslot]);
             if (j == nt - 1) mma_commit_w(&bar.q_empty[half]);
         };
