@@ -84,13 +84,16 @@ struct PagedLine {
     int64_t P0, P1, per;  // the block's units, units per block
     int64_t before;       // units before the request that holds P0
     int64_t units;        // and that request's
+    int64_t total;        // the line's
     int req;
 };
 
-// All NTHR threads of the block call it; `units(i, err)` counts request i's.  `per`
-// is at least min_per and a multiple of `even`.  scratch: NTHR / 32 + 3 words.
-template <int NTHR, class F>
-__device__ __forceinline__ PagedLine paged_line(const PagedAttn &a, int64_t *scratch, int64_t min_per, int even, F units) {
+// All NTHR threads of the block call it; `units(i, err)` counts request i's, `parts(total)`
+// says how many parts a block takes, a grid's length apart (this is the first).  `per` is
+// at least min_per and a multiple of `even`.  scratch: NTHR / 32 + 3 words.
+template <int NTHR, class F, class S>
+__device__ __forceinline__ PagedLine paged_line(const PagedAttn &a, int64_t *scratch, int64_t min_per, int even, F units,
+                                                S parts) {
     constexpr int W = NTHR / 32;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     int64_t *found = scratch + W;
@@ -126,8 +129,9 @@ __device__ __forceinline__ PagedLine paged_line(const PagedAttn &a, int64_t *scr
         if (base == 0) {
             if (a.n_seqs <= NTHR) total = all;
             // (units fit 32 bits in all but the longest lines: a short division)
-            r.per = total < INT32_MAX ? (int64_t)(((uint32_t)total + gridDim.x - 1) / gridDim.x)
-                                      : (total + gridDim.x - 1) / gridDim.x;
+            const uint32_t n = gridDim.x * (uint32_t)parts(total);
+            r.total = total;
+            r.per = total < INT32_MAX ? (int64_t)(((uint32_t)total + n - 1) / n) : (total + n - 1) / n;
             if (r.per < min_per) r.per = min_per;
             r.per = (r.per + even - 1) / (uint32_t)even * even;
             r.P0 = (int64_t)blockIdx.x * r.per;
@@ -195,7 +199,9 @@ int launch_paged_rows(PagedAttn a, const void *k, const void *v, int64_t page_st
 // max_rows: the most rows that one of its requests can have
 int launch_paged_few(PagedAttn a, int cache_dtype, const void *k, const void *v, int64_t page_stride, int64_t max_rows,
                      cudaStream_t s);
-// after_rows: the launch before it on the stream is the rows kernel of the same call (they may overlap)
-int launch_paged_tile(PagedAttn a, const void *k, const void *v, int64_t page_stride, bool after_rows, cudaStream_t s);
+// after_rows: the launch before it on the stream is another kernel of the same call (they may overlap);
+// max_parts: leads and slots are there for so many parts of a block's work
+int launch_paged_tile(PagedAttn a, const void *k, const void *v, int64_t page_stride, int max_parts, bool after_rows,
+                      cudaStream_t s);
 
 }  // namespace kda

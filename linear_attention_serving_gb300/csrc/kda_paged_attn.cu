@@ -17,6 +17,7 @@ struct PagedSet {
 };
 struct PagedWs {
     PagedSet rows, tile;
+    int parts;  // of a tile block's work
     size_t total;
 };
 
@@ -36,7 +37,9 @@ PagedWs paged_ws(int64_t T, int Hq, int Hkv) {
     const int64_t rows = T * (Hq / Hkv);
     w.total = 0;
     w.rows = paged_set(w.total, paged_rows_blocks(), rows, PAGED_ROWS_CAP);  // (the most blocks of the two)
-    w.tile = paged_set(w.total, paged_tile_blocks(), rows, PAGED_TILE_CAP);
+    // (a call of fewer rows has not the work that makes parts pay)
+    w.parts = rows >= 2048 ? 4 : 1;
+    w.tile = paged_set(w.total, paged_tile_blocks() * w.parts, rows, PAGED_TILE_CAP);
     return w;
 }
 
@@ -242,8 +245,11 @@ int kda_paged_attn(const void *q, const void *k_cache, const void *v_cache, cons
     if (tiles) {
         a.row_lo = few ? few_rows : 0;
         a.row_hi = INT32_MAX;
-        js[1] = use(w.tile, paged_tile_blocks());
-        if ((rc = launch_paged_tile(a, k_cache, v_cache, page_stride, few, s))) return rc;
+        // (the kernel takes parts by the bytes that the lengths say; a table that cannot
+        // hold as many asks for none, which spares the join their leads)
+        const int parts = (int64_t)n_seqs * max_blocks * page_size * Hkv * D * 4 > (64 << 20) ? w.parts : 1;
+        js[1] = use(w.tile, paged_tile_blocks() * parts);
+        if ((rc = launch_paged_tile(a, k_cache, v_cache, page_stride, parts, few, s))) return rc;
     }
     return launch_join(a, js[0], js[1], max_rows, dtype == KDA_F32, s);
 }

@@ -135,7 +135,8 @@ static_assert(sizeof(Seg) == 64, "segment size");
 
 // The line's items from the block's start on.
 struct Walk {
-    int64_t pos, end, per, before, A;
+    int64_t pos, end, per, A;
+    int vb;                  // number of the part: its lead and slots
     int req, h, g, alts;
     TileReq q;
     bool fresh;
@@ -168,9 +169,9 @@ struct Walk {
         s.pos = q.r.pos0 + j0;
         s.req = req;
         s.whole = b == 0 && stop == B;
-        s.slot = 2 * (int)blockIdx.x + (pos == P0 ? 0 : 1);
-        s.c0 = A + head >= P0 ? (int)blockIdx.x : -1;  // block of the item's first tile: this one, or one before
-        s.c1 = (int)blockIdx.x;                       // block of its last
+        s.slot = 2 * vb + (pos == P0 ? 0 : 1);
+        s.c0 = A + head >= P0 ? vb : -1;  // part with the item's first tile: this one, or one before
+        s.c1 = vb;                        // part with its last
         if (B > end) s.c1 = (int)((B - 1) / per);
         pos = stop;
         if (stop == B) {
@@ -191,6 +192,48 @@ struct Walk {
       }
     }
 };
+
+// Sets the walk to P0, in request `req` of `units` units that `before` precede; a whole
+// warp.
+__device__ __forceinline__ void walk_from(const PagedAttn &a, Walk &w, int th, int64_t P0, int req, int64_t before, int64_t units) {
+    const int lane = threadIdx.x & 31;
+    const TileReq q = tile_req(a, req, th, nullptr);
+    const int64_t head = units / a.Hkv;
+    const int h = (int)((P0 - before) / head);
+    const int64_t rem = P0 - before - h * head;
+    // the last row tile that begins at or before rem, 32 candidates at a time
+    int lo = 0, n = q.ng;
+    while (n > 1) {
+        const int step = (n + 31) / 32, g = lo + lane * step;
+        const bool at = lane * step < n && units_before(a, q, g, th) <= rem;
+        const int k = 31 - __clz(__ballot_sync(0xffffffffu, at));
+        lo += k * step;
+        n = min(step, n - k * step);
+    }
+    w.A = before + h * head + units_before(a, q, lo, th);
+    w.req = req;
+    w.h = h;
+    w.g = lo;
+    w.fresh = true;
+    w.pos = P0;
+}
+// The same with the request to be found yet.
+__device__ __forceinline__ void walk_to(const PagedAttn &a, Walk &w, int th, int64_t P0) {
+    const int lane = threadIdx.x & 31;
+    int64_t carry = 0;
+    for (int base = 0; base < a.n_seqs; base += 32) {
+        const int64_t t = base + lane < a.n_seqs ? line_units(a, base + lane, th, nullptr) : 0;
+        const int64_t inc = paged_warp_scan(t, lane);
+        const uint32_t at = __ballot_sync(0xffffffffu, P0 >= carry + inc - t && P0 < carry + inc);
+        if (at) {
+            const int k = __ffs(at) - 1;
+            const int64_t before = carry + __shfl_sync(0xffffffffu, inc - t, k), units = __shfl_sync(0xffffffffu, t, k);
+            walk_from(a, w, th, P0, base + k, before, units);
+            return;
+        }
+        carry += __shfl_sync(0xffffffffu, inc, 31);
+    }
+}
 
 // K and V tiles are loaded in the order of their first use, K0 V0 K1 V1 .. (one
 // half: K0 K1 V0 K2 V1 .., two S being formed before the first P V).  Place of V_j,
@@ -240,22 +283,27 @@ __device__ __forceinline__ void issue_pv(uint32_t d, uint32_t p, uint64_t v, uin
 struct Shared {
     uint32_t tmem;
     int abort;
-    int req, h, g;
-    int pad;
-    int64_t A;
 };
 
 // One warp walks the line ahead of the others, and has each segment's queries
 // loaded; a segment with nt < 0 ends it.  Items of one half take the two halves of
 // the buffer in turn, so the next one's queries arrive while this one is worked on.
 __device__ __forceinline__ void walk_role(const PagedAttn &a, const CUtensorMap &qmap, uint8_t *sm, Walk w, int th, int64_t P0,
-                                          const Gate &gate) {
+                                          int64_t total, const Gate &gate) {
     const int lane = threadIdx.x & 31;
     const Bars bar(sm);
     int n0 = 0, n1 = 0;  // loads of each half of Q
     for (int i = 0;; ++i) {
         Seg s;
-        const bool more = w.next(a, th, P0, s);
+        bool more = w.next(a, th, P0, s);
+        while (!more) {  // the block's next part, if there is one
+            P0 += gridDim.x * w.per;
+            if (P0 >= total) break;
+            w.vb += gridDim.x;
+            w.end = P0 + w.per < total ? P0 + w.per : total;
+            walk_to(a, w, th, P0);
+            more = w.next(a, th, P0, s);
+        }
         if (!more) s.nt = -1;
         bool ok = gate(&bar.seg_empty[i % SEGS], ((i / SEGS) & 1) ^ 1);
         if (ok && lane == 0) {
@@ -530,9 +578,9 @@ __device__ __forceinline__ void finish(const PagedAttn &a, uint32_t to, int th, 
         else if (a.lse)
             a.lse[out] = dead ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
     }
-    if (threadIdx.x == 0 && !whole && s->c0 == (int)blockIdx.x) {
-        a.lead[2 * blockIdx.x] = make_int4(s->tok, s->h, 0, s->ntok * G);
-        a.lead[2 * blockIdx.x + 1] = make_int4(s->slot, s->c0, s->c1, 1);
+    if (threadIdx.x == 0 && !whole && s->c0 >= 0) {  // the item's first piece is here
+        a.lead[2 * s->c0] = make_int4(s->tok, s->h, 0, s->ntok * G);
+        a.lead[2 * s->c0 + 1] = make_int4(s->slot, s->c0, s->c1, 1);
     }
 }
 
@@ -707,7 +755,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
 
 __global__ void __launch_bounds__(THREADS, 1)
     paged_tile_kernel(const __grid_constant__ PagedMaps maps, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ PagedAttn a, int th,
-                      int min_per) {
+                      int min_per, int max_parts) {
     extern __shared__ __align__(1024) uint8_t sm[];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -738,52 +786,43 @@ __global__ void __launch_bounds__(THREADS, 1)
         mbar_init(bar.last + 1, 1);
         mbar_fence_init();
         sh->abort = 0;
-        a.lead[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
+        for (int i = 0; i < max_parts; ++i) a.lead[2 * (blockIdx.x + i * gridDim.x) + 1] = make_int4(0, 0, 0, 0);
     }
     auto units = [&](int i, int *err) { return line_units(a, i, th, err); };
-    const PagedLine line = paged_line<THREADS>(a, scratch, min_per, 2, units);
-    const int64_t P0 = line.P0, P1 = line.P1, per = line.per, before = line.before;
-    const int req = line.req;
+    int64_t kv_tiles = 0;
+    if (max_parts > 1) {
+        int64_t n = 0;
+        for (int i = tid; i < a.n_seqs; i += THREADS) {
+            const PagedReq r = paged_req(a, i, nullptr);
+            if (r.rows) n += (int64_t)a.Hkv * ((r.kend - r.k0 + BK - 1) / BK);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+        if (lane == 0) scratch[warp] = n;
+        __syncthreads();
+        for (int w = 0; w < THREADS / 32; ++w) kv_tiles += scratch[w];
+        __syncthreads();
+    }
+    // Keys and values over 64 MB are taken in parts, so that those that the blocks read
+    // at any time stay in the L2 cache (2,048 tokens over 65,536 keys of 8 heads, 268 MB:
+    // read 23 times from HBM otherwise); each part should be worth the pieces that its
+    // borders cost.
+    auto parts = [&](int64_t total) -> int {
+        const int64_t by_size = (kv_tiles * (2 * SLOT) + (64 << 20) - 1) >> 26, by_work = total / (gridDim.x * 256);
+        const int64_t n = by_size < by_work ? by_size : by_work;
+        return n < 1 ? 1 : n > max_parts ? max_parts : (int)n;
+    };
+    const PagedLine line = paged_line<THREADS>(a, scratch, min_per, 2, units, parts);
+    const int64_t P0 = line.P0, P1 = line.P1;
     if (P0 >= P1) {
         asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
-    }
-    if (warp == 0) {  // kv head and row tile of the block's first unit
-        const TileReq q = tile_req(a, req, th, nullptr);
-        const int64_t head = line.units / a.Hkv;
-        const int h = (int)((P0 - before) / head);
-        const int64_t rem = P0 - before - h * head;
-        // the last row tile that begins at or before rem, 32 candidates at a time
-        int lo = 0, n = q.ng;
-        while (n > 1) {
-            const int step = (n + 31) / 32, g = lo + lane * step;
-            const bool at = lane * step < n && units_before(a, q, g, th) <= rem;
-            const int k = 31 - __clz(__ballot_sync(0xffffffffu, at));
-            lo += k * step;
-            n = min(step, n - k * step);
-        }
-        if (lane == 0) {
-            sh->req = req;
-            sh->h = h;
-            sh->g = lo;
-            sh->A = before + h * head + units_before(a, q, lo, th);
-        }
     }
     if (warp == SOFT) tmem_alloc(&sh->tmem, TCOLS);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh->tmem;
-    Walk w;
-    w.pos = P0;
-    w.end = P1;
-    w.per = per;
-    w.A = sh->A;
-    w.req = sh->req;
-    w.h = sh->h;
-    w.g = sh->g;
-    w.fresh = true;
-    w.alts = 0;
     const Gate gate{&sh->abort, a.err};
     if (warp < SOFT) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFT));
@@ -794,8 +833,15 @@ __global__ void __launch_bounds__(THREADS, 1)
             mma_role(a, sm, tmem, warp - SOFT, gate);
         else if (warp == SOFT + 2)
             load_role(a, maps, sm, gate);
-        else
-            walk_role(a, qmap, sm, w, th, P0, gate);
+        else {
+            Walk w;
+            w.end = P1;
+            w.per = line.per;
+            w.vb = blockIdx.x;
+            w.alts = 0;
+            walk_from(a, w, th, P0, line.req, line.before, line.units);
+            walk_role(a, qmap, sm, w, th, P0, line.total, gate);
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -812,7 +858,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 int paged_tile_blocks() { return device_sm_count(); }
 
-int launch_paged_tile(PagedAttn a, const void *k, const void *v, int64_t page_stride, bool after_rows, cudaStream_t s) {
+int launch_paged_tile(PagedAttn a, const void *k, const void *v, int64_t page_stride, int max_parts, bool after_rows, cudaStream_t s) {
     int box = 16;
     while (box < BK && a.page_size % (2 * box) == 0) box *= 2;
     a.box = box;
@@ -835,7 +881,7 @@ int launch_paged_tile(PagedAttn a, const void *k, const void *v, int64_t page_st
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = after_rows ? 1 : 0;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_tile_kernel, maps, qmap, a, th, 8);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_tile_kernel, maps, qmap, a, th, 8, max_parts);
     note_launch("paged_tile", s);
     return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
