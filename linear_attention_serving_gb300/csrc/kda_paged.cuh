@@ -185,6 +185,8 @@ __device__ __forceinline__ void paged_store_row(const PagedAttn &a, bool f32, in
 int make_paged_maps(const void *k, const void *v, int cache_dtype, int Hkv, int page_size, int n_pages,
                     int64_t page_stride, int box_rows, PagedMaps *out);
 
+int make_paged_row_maps(const void *k, const void *v, int Hkv, int page_size, int n_pages, int64_t page_stride, int box_rows,
+                        PagedMaps *out);
 int make_paged_q_map(const void *q, int64_t T, int Hq, int G, int tokens, CUtensorMap *out);
 
 constexpr int PAGED_ROWS_CAP = 64;   // rows of one item of the rows kernel (fp32) and of the few-rows kernel

@@ -58,12 +58,20 @@ __device__ __forceinline__ int64_t line_tiles(const PagedAttn &a, int i, int *er
 }
 
 // ---------------------------------------------------------------- producer
+// One tile (16 keys of one head of one page) in one copy: the map's third dimension is
+// the row's four 128-byte pieces, which land in blocks of their own.
+__device__ __forceinline__ void load_tile(void *dst, const void *map, int y, int z, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(0), "r"(y), "r"(0), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
 __device__ __forceinline__ void produce(const PagedAttn &a, const PagedMaps &maps, uint8_t *sm, int64_t P0, int64_t P1,
                                         int64_t per, int req, int64_t before) {
     const int lane = threadIdx.x & 31;
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + OFF_BAR), *empty = full + STAGES;
     volatile int *abort = reinterpret_cast<volatile int *>(sm + OFF_ABORT);
-    const int box = a.box, nbx = TK / box;
     int stage = 0, phase = 0, issued = 0;
     auto next_stage = [&]() -> bool {
         const bool ok = mbar_wait_ab(&empty[stage], phase ^ 1, abort);
@@ -136,15 +144,15 @@ __device__ __forceinline__ void produce(const PagedAttn &a, const PagedMaps &map
             }
             advance();
         }
-        int cbase = -32, page = 0;
+        int cbase = 0, page = 0, off = 0;
         for (int t = tb; t < te; ++t) {
-            const int b0 = t * nbx;
-            if (t == tb || b0 + nbx > cbase + 32) {  // pages of the next 32 boxes, one per lane
-                cbase = b0;
-                const int key = r.k0 + (cbase + lane) * box;
+            if (t == tb || t >= cbase + 32) {  // pages of the next 32 tiles, one per lane
+                cbase = t;
+                const int key = r.k0 + (cbase + lane) * TK, blk = key / a.page_size;
                 page = 0;
+                off = h * a.page_size + key - blk * a.page_size;
                 if (key < hi) {
-                    page = a.table[(int64_t)req * a.max_blocks + key / a.page_size];
+                    page = a.table[(int64_t)req * a.max_blocks + blk];
                     if (page < 0 || page >= a.n_pages) {
                         if (a.err) atomicOr(a.err, KDA_DEVERR_PAGE);
                         page = 0;
@@ -152,8 +160,7 @@ __device__ __forceinline__ void produce(const PagedAttn &a, const PagedMaps &map
                 }
             }
             const int key0 = r.k0 + t * TK, kvalid = min(TK, hi - key0);
-            const int nb = (kvalid + box - 1) / box;
-            const int pg = __shfl_sync(0xffffffffu, page, (b0 - cbase + lane) & 31);
+            const int pg = __shfl_sync(0xffffffffu, page, t - cbase), y = __shfl_sync(0xffffffffu, off, t - cbase);
             if (!next_stage()) return;
             if (lane == 0) {
                 d.flags = (t == tb ? FIRST : 0) | (t == te - 1 ? LAST : 0) | whole;
@@ -162,17 +169,9 @@ __device__ __forceinline__ void produce(const PagedAttn &a, const PagedMaps &map
                 d.key0 = key0;
                 d.kvalid = kvalid;
                 *reinterpret_cast<Desc *>(sm + OFF_DESC + stage * 64) = d;
-                mbar_expect_tx(&full[stage], (uint32_t)(nb * box * D * 8));
-            }
-            __syncwarp();
-            if (lane < nb) {
-                const int key = key0 + lane * box, y = h * a.page_size + key % a.page_size;
-                uint8_t *dst = sm + stage * STAGE + lane * box * 128;
-#pragma unroll
-                for (int sub = 0; sub < NSUB; ++sub) {
-                    tma_load_3d(dst + sub * TK * 128, &maps.k, sub * 32, y, pg, &full[stage]);
-                    tma_load_3d(dst + HALF + sub * TK * 128, &maps.v, sub * 32, y, pg, &full[stage]);
-                }
+                mbar_expect_tx(&full[stage], 2 * HALF);
+                load_tile(sm + stage * STAGE, &maps.k, y, pg, &full[stage]);
+                load_tile(sm + stage * STAGE + HALF, &maps.v, y, pg, &full[stage]);
             }
             __syncwarp();
             advance();
@@ -430,7 +429,7 @@ int paged_rows_blocks() { return 2 * device_sm_count(); }
 int launch_paged_rows(PagedAttn a, const void *k, const void *v, int64_t page_stride, cudaStream_t s) {
     a.box = TK;  // (page sizes are multiples of 16)
     PagedMaps maps;
-    int rc = make_paged_maps(k, v, KDA_F32, a.Hkv, a.page_size, a.n_pages, page_stride, TK, &maps);
+    int rc = make_paged_row_maps(k, v, a.Hkv, a.page_size, a.n_pages, page_stride, TK, &maps);
     if (rc) return rc;
     if ((rc = prepare_kernel((const void *)paged_rows_kernel, SMEM, THREADS, nullptr))) return rc;
     // at least 8 tiles a block (two for each warp): below that the pieces cost more than they save

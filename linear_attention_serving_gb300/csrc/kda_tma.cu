@@ -82,6 +82,25 @@ int make_paged_maps(const void *k, const void *v, int cache_dtype, int Hkv, int 
     return KDA_OK;
 }
 
+// fp32 caches as {32 channels, Hkv * page_size, 4 pieces of a row, pages}: one tile =
+// box_rows keys with all their channels, piece by piece, each with the 128-byte swizzle.
+int make_paged_row_maps(const void *k, const void *v, int Hkv, int page_size, int n_pages, int64_t page_stride, int box_rows,
+                        PagedMaps *out) {
+    const EncodeTiledFn fn = encode_tiled();
+    if (!fn) return KDA_ERR_CUDA;
+    const cuuint64_t dim[4] = {32u, (cuuint64_t)Hkv * page_size, 4u, (cuuint64_t)n_pages};
+    const cuuint64_t stride[3] = {(cuuint64_t)D * 4, 128u, (cuuint64_t)page_stride * 4};
+    const cuuint32_t box[4] = {32u, (cuuint32_t)box_rows, 4u, 1u};
+    const cuuint32_t estride[4] = {1u, 1u, 1u, 1u};
+    for (int i = 0; i < 2; ++i) {
+        const CUresult r = fn(i ? &out->v : &out->k, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, const_cast<void *>(i ? v : k), dim,
+                              stride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        if (r != CUDA_SUCCESS) return KDA_ERR_CUDA;
+    }
+    return KDA_OK;
+}
+
 // Queries [T, Hq, D]: one tile = 64 channels of G heads of `tokens` tokens, so that
 // its rows are the G heads of one token after another.
 int make_paged_q_map(const void *q, int64_t T, int Hq, int G, int tokens, CUtensorMap *out) {
