@@ -194,6 +194,8 @@ __device__ __forceinline__ void produce(const PagedAttn &a, const PagedMaps &map
 // channels for the output; maxima and sums of row r in lane r.
 struct RowsF32 {
     float o[16][4], m, l;
+    // RM: rows that the code is laid out for (R <= RM)
+    template <int RM>
     __device__ __forceinline__ void tile(const float *q, float *ps, const uint8_t *k, const uint8_t *v, int lane, int R, float sc,
                                          const Desc &d, int row0, int G, int window, bool mask) {
         const int key = lane & 15, hf = lane >> 4;
@@ -205,7 +207,7 @@ struct RowsF32 {
         }
         float corr = 1.f;  // of row `lane`
 #pragma unroll 1
-        for (int r = 0; r < R; ++r) {
+        for (int r = 0; r < (RM == 1 ? 1 : R); ++r) {
             const float4 *qr = reinterpret_cast<const float4 *>(q + r * D) + 16 * hf;
             float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
 #pragma unroll
@@ -238,7 +240,7 @@ struct RowsF32 {
         const bool moved = __any_sync(0xffffffffu, corr != 1.f);
         l *= corr;
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
+        for (int r = 0; r < RM; ++r) {
             if (r < R && moved) {
                 const float f = __shfl_sync(0xffffffffu, corr, r);
 #pragma unroll
@@ -252,8 +254,8 @@ struct RowsF32 {
             for (int e = 0; e < 4; ++e)
                 vv[e] = *reinterpret_cast<const float4 *>(v + (lane >> 3) * 2048 + (kk + e) * 128 + (((lane & 7) ^ ((kk + e) & 7)) << 4));
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                if (r < R) {
+            for (int r = 0; r < RM; ++r) {
+                if (RM == 1 || r < R) {
                     const float4 p = *reinterpret_cast<const float4 *>(ps + r * 16 + kk);
                     o[r][0] = fmaf(p.w, vv[3].x, fmaf(p.z, vv[2].x, fmaf(p.y, vv[1].x, fmaf(p.x, vv[0].x, o[r][0]))));
                     o[r][1] = fmaf(p.w, vv[3].y, fmaf(p.z, vv[2].y, fmaf(p.y, vv[1].y, fmaf(p.x, vv[0].y, o[r][1]))));
@@ -298,7 +300,14 @@ struct Work {
     }
     __device__ __forceinline__ void tile(const PagedAttn &a, const Desc &d, int wrow, int lane, const uint8_t *kt, const uint8_t *vt,
                                          const float *q, float *ps) {
-        w.tile(q, ps, kt, vt, lane, min(16, d.R - 16 * wrow), a.scale_log2, d, d.r0 + 16 * wrow, a.G, a.window, d.flags & MASK);
+        const int R = min(16, d.R - 16 * wrow), row0 = d.r0 + 16 * wrow;
+        const bool mask = d.flags & MASK;
+        if (R == 1)
+            w.tile<1>(q, ps, kt, vt, lane, R, a.scale_log2, d, row0, a.G, a.window, mask);
+        else if (R <= 4)
+            w.tile<4>(q, ps, kt, vt, lane, R, a.scale_log2, d, row0, a.G, a.window, mask);
+        else
+            w.tile<16>(q, ps, kt, vt, lane, R, a.scale_log2, d, row0, a.G, a.window, mask);
     }
     __device__ __forceinline__ void end(int lane, float *red, float2 *ml) {
         if (lane < 16) ml[lane] = make_float2(w.m, w.l);
@@ -339,11 +348,22 @@ __device__ __forceinline__ void consume(const PagedAttn &a, uint8_t *sm) {
             }
             break;
         }
-        const Desc d = *reinterpret_cast<const Desc *>(sm + OFF_DESC + stage * 64);
-        if (d.flags & END) break;
-        const int wrow = warp % d.wr, wk = CONS / d.wr, wpart = warp / d.wr;
+        const Desc *ds = reinterpret_cast<const Desc *>(sm + OFF_DESC + stage * 64);
+        const int4 head = *reinterpret_cast<const int4 *>(ds);  // flags, ord, wr, key0
+        if (head.x & END) break;
+        // wr = 1, 2 or 4 warps side by side on the rows, wk = 4 / wr on the tiles in turn
+        const int wl = head.z >> 1, wrow = warp & (head.z - 1), wk = CONS >> wl, wpart = warp >> wl;
+        if (!(head.x & (FIRST | LAST)) && (head.y & (wk - 1)) != wpart) {  // another warp's tile
+            if (lane == 0) mbar_arrive(&empty[stage]);
+            if (++stage == STAGES) {
+                stage = 0;
+                phase ^= 1;
+            }
+            continue;
+        }
+        const Desc d = *ds;
         if (d.flags & FIRST) work.begin(a, d, wrow, lane, mine);
-        if (d.ord % wk == wpart && d.kvalid > 0) {
+        if ((d.ord & (wk - 1)) == wpart && d.kvalid > 0) {
             uint8_t *kt = sm + stage * STAGE, *vt = kt + HALF;
             if (d.kvalid < TK) zero_past(vt, d.kvalid, lane);
             work.tile(a, d, wrow, lane, kt, vt, mine, ps);
