@@ -4,16 +4,19 @@ attention of each request's new tokens over its cached keys.
 
 As in ``kda.py``, argument marshalling only: outputs and the workspace are
 allocated with torch, everything else runs in the library's CUDA kernels.  The
-smallest calls take a few microseconds on the GPU, so the checks here are
-written to cost little: one pass over the tensors, messages put together only
-when something is wrong, addresses handed over as plain integers.
+smallest calls take a few microseconds on the GPU, so a call first goes through
+``_paged_fast`` (csrc_py/paged_fast.cpp), which makes the same checks and the same
+call of the library in compiled code.  What it does not take, it leaves undone
+and answers None; the checks here then say what is wrong, or make the call.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 
 import torch
 
+from . import _build
 from .kda import D, KDA_BF16, KDA_F32, KDAError, _check, load
 
 KDA_E4M3 = 2
@@ -23,6 +26,24 @@ _I32, _I64, _F32, _E4M3 = torch.int32, torch.int64, torch.float32, torch.float8_
 _CODE = {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32}
 _CACHE_CODE = {**_CODE, _E4M3: KDA_E4M3}
 _declared = None
+
+
+def _not_loaded(*args):
+    """Stands where the compiled calls will be until the first call loads them."""
+    _lib()
+
+
+_fast_tables = _fast_append = _fast_attn = _not_loaded
+
+
+def _load_fast(lib):
+    global _fast_tables, _fast_append, _fast_attn
+    spec = importlib.util.spec_from_file_location("_paged_fast", _build.build_fast())
+    fast = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(fast)
+    fast.init(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        lib.kda_paged_tables, lib.kda_paged_append, lib.kda_paged_attn, lib.kda_paged_attn_workspace_size)))
+    _fast_tables, _fast_append, _fast_attn = fast.tables, fast.append, fast.attn
 
 
 def _lib():
@@ -35,6 +56,7 @@ def _lib():
         lib.kda_paged_attn.argtypes = [P, P, P, P, P, P, I, L, I, I, I, I, I, I, P, P, I, I, L, I, F, I, P, P, P, S, P, P]
         lib.kda_paged_attn_workspace_size.argtypes = [L, I, I, I]
         lib.kda_paged_attn_workspace_size.restype = S
+        _load_fast(lib)
         _declared = lib
     return _declared
 
@@ -111,6 +133,9 @@ def paged_tables(new_len, ctx_len, block_table, free_pages, free_head, T_total, 
     place.  new_len, ctx_len int32 [n]; free_pages int32 [n_free]; free_head int32 [1].
     Returns (slot_map int64 [T], positions int32 [T], cu_q int32 [n + 1], kv_len
     int32 [n], free_head_next int32 [1])."""
+    done = _fast_tables(new_len, ctx_len, block_table, free_pages, free_head, T_total, page_size, n_pages, error_word)
+    if done is not None:
+        return done
     lib = _declared or _lib()
     index = _on_device(new_len, ctx_len, block_table, free_pages, free_head, error_word)
     _typed(_I32, "new_len ctx_len block_table free_pages free_head error_word", new_len, ctx_len, block_table, free_pages,
@@ -136,6 +161,8 @@ def paged_append(k, v, slot_map, k_cache, v_cache, k_scale=None, v_scale=None, e
     """kda_paged_append: k, v [T, Hkv, 128] into the caches [pages, Hkv, page size,
     128] at slot_map int64 [T] (negative: skipped).  An e4m3 cache takes k_scale and
     v_scale float32 [Hkv]."""
+    if _fast_append(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, error_word) is not None:
+        return
     lib = _declared or _lib()
     index = _on_device(k, v, slot_map, k_scale, v_scale, error_word)
     n, h, ps, stride, code = _cache(index, k_cache, v_cache, k_scale, v_scale)
@@ -167,6 +194,10 @@ def paged_attn(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q=0, sm_scale
     through block_table int32 [n, max_blocks]; cu_q int32 [n + 1] and kv_len int32 [n]
     as paged_tables gives them.  max_q: the most new tokens of one request (0: not
     known).  Returns (o in q's dtype, lse float32 [T, Hq])."""
+    done = _fast_attn(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q, sm_scale, window, k_scale, v_scale, out, lse,
+                      workspace, error_word)
+    if done is not None:
+        return done
     lib = _declared or _lib()
     index = _on_device(q, block_table, cu_q, kv_len, k_scale, v_scale, out, lse, workspace, error_word)
     n_pages, hkv, ps, stride, code = _cache(index, k_cache, v_cache, k_scale, v_scale)
