@@ -36,8 +36,8 @@ constexpr int OFF_Q = 0;
 constexpr int OFF_KV = 2 * QHALF;
 constexpr int OFF_SCAN = OFF_KV + SLOTS * SLOT;  // the start's sums
 constexpr int OFF_BAR = OFF_SCAN + 256;
-constexpr int NBAR = 2 * SLOTS + 19 + 2 * 4;
 constexpr int SEGS = 4;                        // ring of segments ahead of the roles
+constexpr int NBAR = 2 * SLOTS + 21 + 2 * SEGS;
 constexpr int OFF_MISC = (OFF_BAR + NBAR * 8 + 63) / 64 * 64;  // TMEM address, abort flag, start of the block's line
 constexpr int OFF_SEG = OFF_MISC + 64;
 constexpr int OFF_MX = OFF_SEG + SEGS * 64;    // [group][half of the keys][row] maximum, sum
@@ -54,7 +54,7 @@ constexpr uint32_t COL_S = 0, COL_O = 256;     // + 128 w
 constexpr float GROW = 8.f;                    // log2 growth of a maximum that ref follows
 
 struct Bars {
-    uint64_t *kv_full, *kv_empty, *q_full, *q_empty, *s_full, *p_ready, *pv_done, *o_free, *last, *turn, *seg_full, *seg_empty;
+    uint64_t *kv_full, *kv_empty, *q_full, *q_empty, *s_full, *p_ready, *pv_done, *o_free, *last, *turn, *hand, *seg_full, *seg_empty;
     __device__ explicit Bars(uint8_t *sm) {
         uint64_t *b = reinterpret_cast<uint64_t *>(sm + OFF_BAR);
         kv_full = b;
@@ -70,7 +70,8 @@ struct Bars {
         o_free = pv_done + 3;        // [2]
         last = o_free + 2;           // [2] products in flight when a wait ran out
         turn = last + 2;             // [2] the other group's probabilities are done
-        seg_full = turn + 2;
+        hand = turn + 2;             // [2] the second S is the first (second) warp's from here on
+        seg_full = hand + 2;
         seg_empty = seg_full + SEGS;
     }
 };
@@ -439,13 +440,24 @@ __device__ __forceinline__ void mma_role(const PagedAttn &a, uint8_t *sm, uint32
         if (lane == 0) mbar_arrive(b);
         __syncwarp();
     };
-    uint32_t par = 0;  // parity bits: 0, 1 halves of Q; 2..4 P by barrier; 5 O
-    bool ok = true;
+    uint32_t par = 0;  // parity bits: 0, 1 halves of Q; 2..4 P by barrier; 5 O; 6 the second S handed over
+    bool ok = true, was_alt = false;
     Seg s;
     int iseg = 0;
+    // The second S belongs to the second warp, but in items of one half to the first.
+    // Where the kinds change, the owner's products on it end before the other's begin:
+    // whoever had it commits what it has issued to hand[0] (to the first warp) or
+    // hand[1], and the other waits.  The two are passed in turn, so no phase is missed.
+    auto handed = [&]() -> bool {
+        const bool got = gate(&bar.hand[x], (par >> 6) & 1);
+        par ^= 1u << 6;
+        return got;
+    };
     while (ok && next_seg(sm, bar, iseg, gate, s)) {
         if (s.nt == 0) continue;
-        const bool alt = s.alt;
+        const bool alt = s.alt, change = alt != was_alt;
+        was_alt = alt;
+        if (change && (alt ? x == 1 : x == 0)) mma_commit_w(&bar.hand[x ^ 1]);
         const int nt = s.nt, half = alt ? s.half : x;
         auto query = [&](int h) -> bool {
             const bool got = gate(&bar.q_full[h], (par >> h) & 1);
@@ -478,10 +490,12 @@ __device__ __forceinline__ void mma_role(const PagedAttn &a, uint8_t *sm, uint32
         };
         const int ahead = alt ? 2 : 1;  // S buffers
         for (int j = 0; ok && j < ahead && j < nt; ++j) {
-            ok = take(kslot);
+            if (j == 1 - x && change && alt == (x == 0)) ok = handed();
+            ok = take(kslot) && ok;
             tc_fence_after();
             if (ok) qk(j);
         }
+        if (nt == 1 && alt && change) ok = ok && handed();
         for (int j = 0; ok && j < nt; ++j) {
             // all waits come before the products, P's last: then P V and the next S are
             // issued in one go
@@ -772,6 +786,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(&bar.q_empty[i], 2);
             mbar_init(&bar.o_free[i], 8);
             mbar_init(&bar.turn[i], SOFT / 2);
+            mbar_init(&bar.hand[i], 1);
         }
         for (int i = 0; i < 3; ++i) {
             mbar_init(&bar.s_full[i], 1);

@@ -5,6 +5,7 @@ import torch
 import linear_attention_serving_gb300 as kda
 from linear_attention_serving_gb300 import paged
 from paged_testutil import D, attn_close, attn_ref, cdiv, make, tables_ref
+from test_gpu_canaries import Guarded
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -216,6 +217,22 @@ def test_attn_row_tiles_of_both_kinds_in_one_block():
     attn_close(o, lse, attn_ref(d["q"], d["k_cache"], d["v_cache"], d["table"], d["cu"], d["kv"]), BF16, BF16)
 
 
+@pytest.mark.parametrize("new,ctx", [([197, 100], [3, 19]), ([132, 20, 196, 32], [500, 700, 0, 1000])])
+def test_attn_row_tiles_of_both_kinds_in_turn(new, ctx):
+    """Items of one half, over several tiles, right before and after items of two halves,
+    again and again: each kind's scores stay its own."""
+    k = 6
+    d = make(new * k, ctx * k, 8, 4, 16, BF16, seed=14)
+    ref = attn_ref(d["q"], d["k_cache"], d["v_cache"], d["table"], d["cu"], d["kv"])
+    first = None
+    for _ in range(10):
+        o, lse, e = run_attn(d, max_q=max(new))
+        assert e == 0
+        first = first or (o, lse)
+        assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
+    attn_close(o, lse, ref, BF16, BF16)
+
+
 def test_attn_row_tiles_rising_scores():
     """Scores that grow with the key: the running maximum moves at every tile."""
     d = make([3], [1500], 1, 16, 32, BF16, q_std=1.0)
@@ -380,3 +397,138 @@ def test_attn_page_outside_the_cache():
         t[1][2] = bad
         o2, lse2, e = run_attn({**d, "table": t})
         assert e == paged.DEVERR_PAGE and torch.equal(o2[0], o[0]) and torch.equal(lse2[0], lse[0])
+
+
+# ------------------------------------------------------------------ many requests, long contexts
+@pytest.mark.parametrize("cache", CACHES, ids=NAMES)
+def test_attn_many_requests(cache):
+    """More requests than a block has threads: the line is scanned in several rounds."""
+    n = 1500
+    check([1] * n, [(7 * i) % 40 for i in range(n)], 1, 2, 16, cache, seed=11)
+
+
+def test_attn_many_requests_of_both_kinds():
+    n = 1400
+    check([40 if i % 90 == 3 else i % 3 for i in range(n)], [(5 * i) % 30 for i in range(n)], 1, 2, 16, BF16, seed=12)
+
+
+def _attn_ref_one(q, k, v, pos0, window):
+    """One request's (o, lse, sum p |v|, largest score magnitude) in 64 bits on the GPU; k, v [S, D] of its one kv head."""
+    T, g, _ = q.shape
+    q, k, v = q.double(), k.double(), v.double()
+    s = D ** -0.5 * (q.reshape(T * g, D) @ k.T)
+    j = torch.arange(len(k), device=q.device)[None]
+    p = (pos0 + torch.arange(T, device=q.device)).repeat_interleave(g)[:, None]
+    s.masked_fill_((j > p) | ((j <= p - window) if window else (j < 0)), float("-inf"))
+    lse = torch.logsumexp(s, 1)
+    w = torch.exp_(s - lse[:, None])
+    mag = D ** -0.5 * torch.stack([(x.abs() @ k.abs().T).amax(1) for x in q])
+    return tuple(x.view(T, g, -1).cpu() for x in (w @ v, lse, w @ v.abs(), mag))
+
+
+@pytest.mark.parametrize("window", [0, 90001])
+def test_attn_context_longer_than_the_cache_of_the_gpu_holds(window):
+    """Keys and values that a block's work passes in several parts, beside a short request."""
+    new, ctx, g, ps = [300, 70], [140003, 21], 8, 64
+    d = make(new, ctx, 1, g, ps, BF16, seed=13)
+    o, lse, e = run_attn(d, window=window, max_q=max(new))
+    assert e == 0
+    ref = []
+    for i in range(2):
+        pages = torch.tensor(d["table"][i][:cdiv(d["kv"][i], ps)])
+        k, v = (d[x][pages, 0].reshape(-1, D)[:d["kv"][i]].to(DEV) for x in ("k_cache", "v_cache"))
+        ref.append(_attn_ref_one(d["q"][d["cu"][i]:d["cu"][i + 1]].to(DEV), k, v, ctx[i], window))
+    o_ref, l_ref, a, mag = (torch.cat(x) for x in zip(*ref))
+    attn_close(o, lse, (o_ref, l_ref[..., 0], a, mag[..., 0]), BF16, BF16)
+
+
+# ------------------------------------------------------------------ the two ways into the library
+@pytest.mark.parametrize("cache", CACHES, ids=NAMES)
+def test_compiled_and_plain_binding_agree(cache, monkeypatch):
+    """What the compiled way returns is what the plain one returns, and it does take these calls."""
+    def go():
+        new, ctx, hkv, g, ps, pages = [3, 0, 20], [14, 5, 0], 2, 4, 16, 8
+        table, e = i32([[6, -1, -1], [7, -1, -1], [-1, -1, -1]]), errw()
+        slots, pos, cu, kv, head = kda.paged_tables(i32(new), i32(ctx), table, i32([3, 1, 2, 0, 4]), i32([1]), 23, ps, pages,
+                                                    error_word=e)
+        gen = torch.Generator().manual_seed(2)
+        qt = F32 if cache is F32 else BF16
+        q = torch.randn(23, hkv * g, D, generator=gen).to(qt).to(DEV)
+        k, v = (torch.randn(23, hkv, D, generator=gen).to(qt).to(DEV) for _ in range(2))
+        kc, vc = (torch.zeros(pages, hkv, ps, D, device=DEV).to(cache) for _ in range(2))
+        sc = dict(k_scale=torch.full((hkv,), 0.02, device=DEV), v_scale=torch.full((hkv,), 0.03, device=DEV)) if cache is E4M3 else {}
+        kda.paged_append(k, v, slots, kc, vc, error_word=e, **sc)
+        o, lse = kda.paged_attn(q, kc, vc, table, cu, kv, max_q=20, error_word=e, **sc)
+        out, ol = torch.empty_like(o), torch.empty_like(lse)
+        o2, lse2 = kda.paged_attn(q, kc, vc, table, cu, kv, out=out, lse=ol, **sc)
+        assert o2.data_ptr() == out.data_ptr() and lse2.data_ptr() == ol.data_ptr()
+        return table, slots, pos, cu, kv, head, kc.view(torch.uint8), vc.view(torch.uint8), o, lse, o2, lse2, e
+
+    paged._lib()
+    taken = []
+    for name in ("tables", "append", "attn"):
+        f = getattr(paged, "_fast_" + name)
+        monkeypatch.setattr(paged, "_fast_" + name, lambda *a, f=f: (taken.append(r := f(*a)), r)[1])
+    compiled = go()
+    assert len(taken) == 4 and all(r is not None for r in taken)
+    for name in ("tables", "append", "attn"):
+        monkeypatch.setattr(paged, "_fast_" + name, lambda *a: None)
+    for x, y in zip(compiled, go()):
+        assert x.dtype == y.dtype and x.shape == y.shape and torch.equal(x, y)
+
+
+def test_refusals_of_both_ways():
+    """What the compiled way leaves undone, the plain one refuses, with its message."""
+    d = make([2], [20], 2, 2, 16, BF16)
+    t = {n: d[n].to(DEV) for n in ("q", "k_cache", "v_cache")}
+    args = dict(q=t["q"], k_cache=t["k_cache"], v_cache=t["v_cache"], block_table=i32(d["table"]), cu_q=i32(d["cu"]),
+                kv_len=i32(d["kv"]))
+    kda.paged_attn(**args)
+    for change, says in [
+            (dict(q=t["q"][:, :3]), "contiguous"), (dict(q=t["q"].half()), "unsupported dtype"),
+            (dict(cu_q=args["cu_q"].long()), "int32"), (dict(kv_len=i32([1, 2])), "cu_q must be"),
+            (dict(block_table=args["block_table"].cpu()), "CUDA"), (dict(v_cache=t["v_cache"].float()), "same dtype"),
+            (dict(k_scale=torch.ones(2, device=DEV)), "e4m3"), (dict(out=torch.empty_like(t["q"], dtype=F32)), "out must"),
+            (dict(workspace=torch.empty(256, dtype=torch.uint8, device=DEV)), "WORKSPACE"), (dict(window=-1), "kda_paged_attn"),
+            (dict(q=t["q"][:, :3].contiguous()), "kda_paged_attn")]:
+        with pytest.raises(kda.KDAError, match=says):
+            kda.paged_attn(**{**args, **change})
+
+
+# ------------------------------------------------------------------ guard bytes
+@pytest.mark.parametrize("cache", CACHES, ids=NAMES)
+@pytest.mark.parametrize("new,ctx", [([1, 1], [0, 3000]), ([37, 0, 1], [5, 9, 700]), ([130, 33], [2000, 0])])
+def test_writes_only_its_buffers(new, ctx, cache):
+    """The step's outputs, caches and workspace between pattern bytes, which stay; and the bits of a plain call."""
+    hkv, g, ps, n, T = 2, 3, 16, len(new), sum(new)
+    d = make(new, ctx, hkv, g, ps, cache, seed=17)
+    qt = d["q"].dtype
+    width, pages = len(d["table"][0]), d["k_cache"].shape[0]
+    table = Guarded((n, width), torch.int32, i32(d["table"]))
+    kc, vc = (Guarded(d[x].shape, cache, d[x].to(DEV)) for x in ("k_cache", "v_cache"))
+    o, lse = Guarded(d["q"].shape, qt), Guarded((T, hkv * g), F32)
+    ws = Guarded((kda.paged_attn_workspace_size(T, n, hkv * g, hkv),), torch.uint8)
+    slots, pos = Guarded((T,), torch.int64), Guarded((T,), torch.int32)
+    cu, kv, head = Guarded((n + 1,), torch.int32), Guarded((n,), torch.int32), Guarded((1,), torch.int32)
+    err = Guarded((1,), torch.int32, i32([0]))
+    bufs = [table, kc, vc, o, lse, ws, slots, pos, cu, kv, head, err]
+    first_new = [t[cdiv(c, ps):cdiv(c + a, ps)] for t, a, c in zip(d["table"], new, ctx)]
+    free = i32([p for ps_ in first_new for p in ps_] + [0])
+    lib, stream, p = paged._lib(), torch.cuda.current_stream().cuda_stream, lambda x: x.t.data_ptr()
+    nw, cx, h0 = i32(new), i32(ctx), i32([0])
+    assert lib.kda_paged_tables(nw.data_ptr(), cx.data_ptr(), n, T, p(table), width, free.data_ptr(), free.numel(),
+                                h0.data_ptr(), p(head), ps, pages, p(slots), p(pos), p(cu), p(kv), p(err), stream) == 0
+    torch.cuda.synchronize()
+    assert table.t.tolist() == d["table"] and kv.t.tolist() == d["kv"] and cu.t.tolist() == d["cu"] and int(err.t) == 0
+    rest, lrest, _ = run_attn(d, max_q=max(new))
+    k, v = (torch.randn(T, hkv, D, device=DEV).to(qt) for _ in range(2))
+    ks, vs = (None if d[x] is None else d[x].to(DEV) for x in ("k_scale", "v_scale"))
+    q = d["q"].to(DEV)
+    o2, lse2 = kda.paged_attn(q, kc.t, vc.t, table.t, cu.t, kv.t, max_q=max(new), k_scale=ks, v_scale=vs, out=o.t, lse=lse.t,
+                              workspace=ws.t, error_word=err.t)
+    torch.cuda.synchronize()
+    assert torch.equal(o2, rest) and torch.equal(lse2, lrest) and int(err.t) == 0
+    kda.paged_append(k, v, slots.t, kc.t, vc.t, k_scale=ks, v_scale=vs, error_word=err.t)
+    torch.cuda.synchronize()
+    assert int(err.t) == 0 and all(b.intact() for b in bufs)
+    assert torch.equal(q, d["q"].to(DEV))
