@@ -233,6 +233,18 @@ def test_attn_row_tiles_of_both_kinds_in_turn(new, ctx):
     attn_close(o, lse, ref, BF16, BF16)
 
 
+@pytest.mark.parametrize("g", [3, 5, 7])
+def test_attn_row_tiles_same_bits(g):
+    """Rows of a tile that are no query's hold what an earlier call left there: it has no say."""
+    d = make([300, 33], [40, 900], 2, g, 16, BF16, seed=15)
+    other = make([200, 200], [300, 0], 4, 1, 16, BF16, seed=16, q_std=40.0)
+    o, lse, _ = run_attn(d)
+    for i in range(30):
+        run_attn({**other, "q": other["q"] * (1 + i % 7)})
+        o2, lse2, _ = run_attn(d)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
 def test_attn_row_tiles_rising_scores():
     """Scores that grow with the key: the running maximum moves at every tile."""
     d = make([3], [1500], 1, 16, 32, BF16, q_std=1.0)
