@@ -630,9 +630,10 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
         const bool alt = seg->alt;
         const int pos = seg->pos + (alt ? 0 : x) * th + row / a.G;
         const int first_key = a.window > 0 ? pos - a.window + 1 : 0;  // keys first_key .. pos, all below hi
-        // (the half's other rows hold the next request's queries, or what was there before)
-        const bool live = row < min(th, seg->ntok - (alt ? 0 : x) * th) * a.G;
         float ref = 0.f, l = 0.f, top = -INFINITY;  // (top: of all the row's keys at the last change of ref, then of this half's)
+        // ref follows the maximum once that has passed this (never for the half's rows past the
+        // item's tokens: they hold the next request's queries, or what was there before)
+        float bound = row < min(th, seg->ntok - (alt ? 0 : x) * th) * a.G ? -INFINITY : INFINITY;
         const int ne = alt ? (x ? 0 : s.nt) : 2 * s.nt;
         uint64_t *prev = nullptr;  // the group's last product
         int prevp = 0;
@@ -666,7 +667,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
             const float mt = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * sc;
             // Meet: both have read S, whose columns P overwrites from here on; and does
             // ref have to follow?  (a warp that gave up counts 32, one that asks for it 1)
-            const bool grow = __any_sync(0xffffffffu, !prev || (live && mt > (top == -INFINITY ? -INFINITY : ref + GROW)));
+            const bool grow = __any_sync(0xffffffffu, mt > bound);
             const int said = meet_count<64>(id, failed || (grow && lane == 0));
             if (said >= 32) return;
             if (said) {
@@ -678,6 +679,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
                 top = both;
                 ref = nref;
                 l *= corr;
+                if (bound != INFINITY && both != -INFINITY) bound = nref + GROW;
                 if (prev) {  // the group's last product must have left O
                     if (!gate(prev, prevp)) failed = true;
                     tc_fence_after();
