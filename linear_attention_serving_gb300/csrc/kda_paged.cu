@@ -13,10 +13,14 @@ namespace {
 // new tokens, new pages), so that one launch suffices and no block waits for
 // another; then each thread places TPT consecutive tokens.  The token that
 // opens a page writes that page's table entry: a new page's first token is
-// always new.  With few tokens the time is the chain of dependent loads and the
-// launch (3.4 us for 256 requests); with many it is the 12 bytes a token written.
-constexpr int TAB_THREADS = 512;
-constexpr int TAB_MAX_SEQS = 16384;  // two int32 per request in shared memory
+// always new.  With few tokens the time is the launch and the chain of dependent
+// loads (3.5 us for 256 requests); with many the same chain and the 12 bytes a token
+// written, which the L2 cache takes (1.1 M tokens of 150 requests: 7.4 us, 1.7 TB/s).
+// Small blocks finish their scan sooner, and no more of them are started than are
+// resident at once, each of which scans once (512 threads in two waves: 11.7 us).
+constexpr int TAB_THREADS = 256;
+constexpr int TAB_BLOCKS = 4;  // an SM
+constexpr int TAB_MAX_SEQS = 16384;  // three int32 per request in shared memory
 
 struct TablesArgs {
     const int32_t *new_len, *ctx_len, *free_pages, *free_head;
@@ -39,6 +43,7 @@ __global__ void __launch_bounds__(TAB_THREADS) tables_kernel(const TablesArgs a)
     extern __shared__ int32_t tab_sm[];
     int32_t *cu = tab_sm;                      // [n + 1] first token of each request
     int32_t *first = tab_sm + a.n_seqs + 1;    // [n] free-list index of block 0 if all blocks were new: f_i - had
+    int32_t *ctx = first + a.n_seqs;           // [n]
     __shared__ int64_t wtok[TAB_THREADS / 32], wpage[TAB_THREADS / 32];
     __shared__ int bad;
 
@@ -85,6 +90,7 @@ __global__ void __launch_bounds__(TAB_THREADS) tables_kernel(const TablesArgs a)
             const int64_t c = tb + t - nw, f = head + pb + p - (have - had) - had;
             cu[i] = (int)(c > INT32_MAX ? INT32_MAX : c);
             first[i] = (int)(f > INT32_MAX ? INT32_MAX : f);  // (an overflow fails the checks below)
+            ctx[i] = cx;
         }
         tok0 += tsum;
         page0 += psum;
@@ -104,7 +110,7 @@ __global__ void __launch_bounds__(TAB_THREADS) tables_kernel(const TablesArgs a)
     const int gid = blockIdx.x * TAB_THREADS + tid, gsize = gridDim.x * TAB_THREADS;
     for (int i = gid; i <= n; i += gsize) {
         a.cu_q[i] = cu[i];
-        if (i < n) a.kv_len[i] = a.ctx_len[i] + cu[i + 1] - cu[i];
+        if (i < n) a.kv_len[i] = ctx[i] + cu[i + 1] - cu[i];
     }
 
     bool badpage = false;
@@ -136,7 +142,7 @@ __global__ void __launch_bounds__(TAB_THREADS) tables_kernel(const TablesArgs a)
                     fresh = true;
                 }
                 if (fresh) {
-                    pos = a.ctx_len[i] + (int)(t - cu[i]);
+                    pos = ctx[i] + (int)(t - cu[i]);
                     b = pos / ps;
                     off = pos - b * ps;
                 } else {
@@ -147,7 +153,7 @@ __global__ void __launch_bounds__(TAB_THREADS) tables_kernel(const TablesArgs a)
                     }
                 }
                 if (fresh || off == 0) {
-                    const int had = (int)(((int64_t)a.ctx_len[i] + ps - 1) / ps);
+                    const int had = (int)(((uint32_t)ctx[i] + (uint32_t)ps - 1) / (uint32_t)ps);
                     const bool is_new = b >= had;
                     int32_t *entry = a.block_table + (int64_t)i * a.max_blocks + b;
                     page = is_new ? a.free_pages[first[i] + b] : *entry;
@@ -313,18 +319,18 @@ int kda_paged_tables(const int32_t *new_len, const int32_t *ctx_len, int n_seqs,
     const TablesArgs a{new_len,  ctx_len,   free_pages, free_head,  block_table, free_head_next, positions,
                        cu_q,     kv_len,    error_word, slot_map,   n_seqs,      (int)T_total,   max_blocks,
                        n_free,   page_size, n_pages};
-    // One token a thread while that fits two blocks an SM (the dependent loads
-    // of a thread's tokens would only add up), else four with 16-byte stores.
-    const int n_sm = device_sm_count();
-    const bool four = T_total > (int64_t)2 * n_sm * TAB_THREADS;
+    // One token a thread while that fits the blocks that are resident at once (the
+    // dependent loads of a thread's tokens would only add up), else four with 16-byte stores.
+    const int most = TAB_BLOCKS * device_sm_count();
+    const bool four = T_total > (int64_t)most * TAB_THREADS;
     const int64_t threads = four ? (T_total + 3) / 4 : T_total;
     int64_t blocks = (threads + TAB_THREADS - 1) / TAB_THREADS;
     if (blocks < 1) blocks = 1;
-    if (blocks > 4 * n_sm) blocks = 4 * n_sm;
+    if (blocks > most) blocks = most;
     const void *f = four ? (const void *)tables_kernel<4> : (const void *)tables_kernel<1>;
-    const int smem = (2 * n_seqs + 1) * (int)sizeof(int32_t);
+    const int smem = (3 * n_seqs + 1) * (int)sizeof(int32_t);
     // (one entry of the launch-preparation cache per kernel, not one per batch size)
-    const int rc = prepare_kernel(f, (2 * TAB_MAX_SEQS + 1) * (int)sizeof(int32_t), TAB_THREADS, nullptr);
+    const int rc = prepare_kernel(f, (3 * TAB_MAX_SEQS + 1) * (int)sizeof(int32_t), TAB_THREADS, nullptr);
     if (rc) return rc;
     if (four)
         tables_kernel<4><<<(int)blocks, TAB_THREADS, smem, s>>>(a);
