@@ -6,13 +6,18 @@
 // two blocks on an SM: 128 KB in flight.  A consumer warp holds up to 16 rows.  Few
 // rows (<= 16): the four warps take every fourth tile, each with its own running
 // maximum and sum, merged in shared memory at the item's end.  More rows: the warps
-// take 16 rows each (two by two up to 32) and share the tiles.
+// take a quarter each (two by two, a half, up to 32) and share the tiles.
 //
 // Products are plain fp32 multiply-adds: tf32 parts would lose digits that the fp32
 // path of this library keeps (three products of two parts each left 2.5e-6 where this
 // leaves 3.2e-7).  A lane holds half a key's channels for the scores and four channels
 // of all keys for the output, so a warp reads each key and value once from shared
 // memory whatever its rows are.
+//
+// Measured: one token of 16 requests, 16 heads of up to 3,000 keys, 4.6 TB/s (46 us), where the copies in flight and the
+// start and the join bound it.  Many rows are bound by the chains of loads and shuffles of
+// two warps a scheduler (8 requests of 40 rows over 2,040 keys of 8 heads: 10.9 TFLOP/s,
+// 244 us; a row at a time 320 us).
 #include "kda_paged.cuh"
 
 namespace kda {
@@ -39,7 +44,7 @@ constexpr int NSUB = D * 4 / 128;            // 128-byte pieces of a row, each a
 
 // what the producer says about a tile
 struct __align__(16) Desc {
-    int flags, ord, wr, key0, kvalid, tok0, h, r0, R, pos0, slot, c0, c1, pad0, pad1, pad2;
+    int flags, ord, wr, key0, kvalid, tok0, h, r0, R, pos0, slot, c0, c1, rpw, pad0, pad1;  // rpw: rows of a warp
 };
 static_assert(sizeof(Desc) == 64, "descriptor size");
 constexpr int FIRST = 1, LAST = 2, WHOLE = 4, END = 8, MASK = 16;
@@ -123,6 +128,7 @@ __device__ __forceinline__ void produce(const PagedAttn &a, const PagedMaps &map
         }
         Desc d;
         d.wr = grp / 16;
+        d.rpw = (R + d.wr - 1) / d.wr;  // (the same for each, or one waits for the others)
         d.tok0 = r.tok0;
         d.h = h;
         d.r0 = r0;
@@ -206,35 +212,58 @@ struct RowsF32 {
             kr[c] = *reinterpret_cast<const float4 *>(k + (ch >> 3) * 2048 + key * 128 + (((ch & 7) ^ (key & 7)) << 4));
         }
         float corr = 1.f;  // of row `lane`
+        // Four rows at a time, so that a chain of sums or shuffles does not wait for itself
+        // (rows past R hold an earlier item's queries; nothing of theirs is read).
+        constexpr int U = RM == 1 ? 1 : 4;
 #pragma unroll 1
-        for (int r = 0; r < (RM == 1 ? 1 : R); ++r) {
-            const float4 *qr = reinterpret_cast<const float4 *>(q + r * D) + 16 * hf;
-            float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
+        for (int r0 = 0; r0 < (RM <= 4 ? 1 : R); r0 += U) {
+            const float4 *qr = reinterpret_cast<const float4 *>(q + r0 * D) + 16 * hf;
+            float2 acc[U];
+            float s[U], top[U], p[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) acc[u] = make_float2(0.f, 0.f);
 #pragma unroll
             for (int c = 0; c < 16; ++c) {
-                const float4 x = qr[c];
-                a0 = fmaf(x.x, kr[c].x, a0);
-                a1 = fmaf(x.y, kr[c].y, a1);
-                a2 = fmaf(x.z, kr[c].z, a2);
-                a3 = fmaf(x.w, kr[c].w, a3);
-            }
-            float s = (a0 + a1) + (a2 + a3);
-            s += __shfl_xor_sync(0xffffffffu, s, 16);
-            if (mask) {
-                const int pos = d.pos0 + (row0 + r) / G, at = d.key0 + key;
-                if (!(at <= pos && (window <= 0 || at > pos - window) && key < d.kvalid)) s = -INFINITY;
-            }
-            float top = s;
 #pragma unroll
-            for (int x = 8; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-            const float old = __shfl_sync(0xffffffffu, m, r), mn = fmaxf(old, top * sc);
-            const float ref = mn == -INFINITY ? 0.f : mn;
-            if (lane == r) {
-                corr = ex2(m - ref);
-                m = mn;
+                for (int u = 0; u < U; ++u) {
+                    const float4 x = qr[u * (D / 4) + c];
+                    acc[u].x = fmaf(x.x, kr[c].x, acc[u].x);
+                    acc[u].y = fmaf(x.y, kr[c].y, acc[u].y);
+                    acc[u].x = fmaf(x.z, kr[c].z, acc[u].x);
+                    acc[u].y = fmaf(x.w, kr[c].w, acc[u].y);
+                }
             }
-            const float p = ex2(fmaf(s, sc, -ref));
-            if (lane < 16) ps[r * 16 + lane] = p;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                s[u] = acc[u].x + acc[u].y;
+                s[u] += __shfl_xor_sync(0xffffffffu, s[u], 16);
+            }
+            if (mask) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int pos = d.pos0 + (row0 + r0 + u) / G, at = d.key0 + key;
+                    if (!(at <= pos && (window <= 0 || at > pos - window) && key < d.kvalid)) s[u] = -INFINITY;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) top[u] = s[u];
+#pragma unroll
+            for (int x = 8; x; x >>= 1)
+#pragma unroll
+                for (int u = 0; u < U; ++u) top[u] = fmaxf(top[u], __shfl_xor_sync(0xffffffffu, top[u], x));
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const float old = __shfl_sync(0xffffffffu, m, r0 + u), mn = fmaxf(old, top[u] * sc);
+                const float ref = mn == -INFINITY ? 0.f : mn;
+                if (lane == r0 + u) {
+                    corr = ex2(m - ref);
+                    m = mn;
+                }
+                p[u] = ex2(fmaf(s[u], sc, -ref));
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (lane < 16) ps[(r0 + u) * 16 + lane] = p[u];
         }
         __syncwarp();
         const bool moved = __any_sync(0xffffffffu, corr != 1.f);
@@ -286,9 +315,9 @@ struct Work {
     __device__ __forceinline__ void begin(const PagedAttn &a, const Desc &d, int wrow, int lane, float *q) {
         w.m = -INFINITY;
         w.l = 0.f;
-        const int R = min(16, d.R - 16 * wrow);
+        const int R = min(d.rpw, d.R - d.rpw * wrow);
         for (int r = 0; r < R; ++r) {  // the queries stand where the output goes at the end
-            const int rr = d.r0 + 16 * wrow + r, j = rr / a.G;
+            const int rr = d.r0 + d.rpw * wrow + r, j = rr / a.G;
             const float4 *src = (const float4 *)a.q + ((int64_t)(d.tok0 + j) * a.Hq + d.h * a.G + (rr - j * a.G)) * (D / 4);
             reinterpret_cast<float4 *>(q + r * D)[lane] = src[lane];
         }
@@ -300,8 +329,9 @@ struct Work {
     }
     __device__ __forceinline__ void tile(const PagedAttn &a, const Desc &d, int wrow, int lane, const uint8_t *kt, const uint8_t *vt,
                                          const float *q, float *ps) {
-        const int R = min(16, d.R - 16 * wrow), row0 = d.r0 + 16 * wrow;
+        const int R = min(d.rpw, d.R - d.rpw * wrow), row0 = d.r0 + d.rpw * wrow;
         const bool mask = d.flags & MASK;
+        if (R <= 0) return;  // (a last, short row group)
         if (R == 1)
             w.tile<1>(q, ps, kt, vt, lane, R, a.scale_log2, d, row0, a.G, a.window, mask);
         else if (R <= 4)
@@ -381,7 +411,7 @@ __device__ __forceinline__ void consume(const PagedAttn &a, uint8_t *sm) {
             float *slot = paged_slot(a, d.slot);
             const float vs = 1.f;
             for (int r = warp; r < d.R; r += CONS) {
-                const int rb = r >> 4, rl = r & 15;
+                const int rb = r / d.rpw, rl = r - rb * d.rpw;
                 float M = -INFINITY, L = 0.f;
                 for (int w = 0; w < wk; ++w) M = fmaxf(M, ml[(rb + w * d.wr) * 16 + rl].x);
                 const float refm = M == -INFINITY ? 0.f : M;
