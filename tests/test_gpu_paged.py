@@ -544,3 +544,17 @@ def test_writes_only_its_buffers(new, ctx, cache):
     torch.cuda.synchronize()
     assert int(err.t) == 0 and all(b.intact() for b in bufs)
     assert torch.equal(q, d["q"].to(DEV))
+
+
+# ------------------------------------------------------------------ together
+def test_hybrid_example():
+    """Chunks and single tokens through both kinds of layer against one pass: a few roundings
+    to bf16 (2^-9 on average) on the way of each output."""
+    import importlib.util
+    import os
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "hybrid_serving.py")
+    spec = importlib.util.spec_from_file_location("hybrid_serving", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    assert example.main() < 1e-2
