@@ -15,7 +15,7 @@ namespace {
 // opens a page writes that page's table entry: a new page's first token is
 // always new.  With few tokens the time is the launch and the chain of dependent
 // loads (3.5 us for 256 requests); with many the same chain and the 12 bytes a token
-// written, which the L2 cache takes (1.1 M tokens of 150 requests: 7.4 us, 1.7 TB/s).
+// written, which the L2 cache takes (1.0 M tokens of 150 requests: 7.4 us, 1.7 TB/s).
 // Small blocks finish their scan sooner, and no more of them are started than are
 // resident at once, each of which scans once (512 threads in two waves: 11.7 us).
 constexpr int TAB_THREADS = 256;

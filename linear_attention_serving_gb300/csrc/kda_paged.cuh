@@ -189,7 +189,7 @@ int make_paged_row_maps(const void *k, const void *v, int Hkv, int page_size, in
                         PagedMaps *out);
 int make_paged_q_map(const void *q, int64_t T, int Hq, int G, int tokens, CUtensorMap *out);
 
-constexpr int PAGED_ROWS_CAP = 64;   // rows of one item of the rows kernel (fp32) and of the few-rows kernel
+constexpr int PAGED_ROWS_CAP = 64;   // rows of one item of the fp32 kernel (the kernel for few rows takes 32 at most)
 constexpr int PAGED_TILE_CAP = 256;  // and of the tile kernel
 
 int check_paged_cache(int Hkv, int Dm, int dtype, int cache_dtype, const float *k_scale, const float *v_scale,

@@ -229,7 +229,7 @@ int kda_paged_attn(const void *q, const void *k_cache, const void *v_cache, cons
     }
     // Up to 32 rows of a kv head fit the few-rows kernel at once; over that the tile
     // kernel, which has room for 128 rows at one cost, is faster (256 windows of 60 rows:
-    // 306 us against 470 us in pieces of 64).  With longer requests in the call it takes
+    // 311 us against 470 us in pieces of 64).  With longer requests in the call it takes
     // them, and the few-rows kernel the single tokens (rows up to the next of 16, 32 from
     // G on).
     const bool tiles = cache_dtype == KDA_BF16 && a.G <= 128 && max_rows > FEW_ROWS;
