@@ -90,10 +90,9 @@ struct PagedLine {
 
 // All NTHR threads of the block call it; `units(i, err)` counts request i's, `parts(total)`
 // says how many parts a block takes, a grid's length apart (this is the first).  `per` is
-// at least min_per and a multiple of `even`.  scratch: NTHR / 32 + 3 words.
+// at least min_per.  scratch: NTHR / 32 + 3 words.
 template <int NTHR, class F, class S>
-__device__ __forceinline__ PagedLine paged_line(const PagedAttn &a, int64_t *scratch, int64_t min_per, int even, F units,
-                                                S parts) {
+__device__ __forceinline__ PagedLine paged_line(const PagedAttn &a, int64_t *scratch, int64_t min_per, F units, S parts) {
     constexpr int W = NTHR / 32;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     int64_t *found = scratch + W;
@@ -133,7 +132,6 @@ __device__ __forceinline__ PagedLine paged_line(const PagedAttn &a, int64_t *scr
             r.total = total;
             r.per = total < INT32_MAX ? (int64_t)(((uint32_t)total + n - 1) / n) : (total + n - 1) / n;
             if (r.per < min_per) r.per = min_per;
-            r.per = (r.per + even - 1) / (uint32_t)even * even;
             r.P0 = (int64_t)blockIdx.x * r.per;
             r.P1 = r.P0 + r.per < total ? r.P0 + r.per : total;
             r.req = 0;

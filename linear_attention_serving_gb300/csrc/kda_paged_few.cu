@@ -951,7 +951,7 @@ __global__ void __launch_bounds__(Cfg<E4, NR>::THREADS, 1)
         a.lead[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
     }
     auto units = [&](int i, int *err) { return line_units(a, i, rw, err); };
-    const PagedLine line = paged_line<C::THREADS>(a, scratch, min_per, 1, units, [](int64_t) { return 1; });
+    const PagedLine line = paged_line<C::THREADS>(a, scratch, min_per, units, [](int64_t) { return 1; });
     if (line.P0 >= line.P1) return;
     if (warp == 0) {  // virtual head and row group of the block's first unit
         const Req q = few_req(a, line.req, rw, nullptr);

@@ -463,7 +463,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     }
     int64_t *scratch = reinterpret_cast<int64_t *>(sm + OFF_RED);
     auto tiles = [&](int i, int *err) { return line_tiles(a, i, err); };
-    const PagedLine line = paged_line<THREADS>(a, scratch, min_per, 1, tiles, [](int64_t) { return 1; });
+    const PagedLine line = paged_line<THREADS>(a, scratch, min_per, tiles, [](int64_t) { return 1; });
     if (line.P0 >= line.P1) return;
     __syncthreads();  // (the sums stood where the consumers' rows will)
     if (tid >= CONS * 32)

@@ -11,24 +11,26 @@
 //   P_w = exp2(S_w scale - ref) as bf16 over S_w's own columns (the softmax
 //         group reads a row of S into registers, so nothing of S is needed)
 //   O_w += P_w V    128 x 128 fp32 in TMEM, P_w read from TMEM
-// The two groups w take turns: while one works out probabilities, the tensor
-// cores run the other's products.  They are the two halves of the rows and share
-// each key tile.  An item of one half has the first group alone, whose S takes
-// both buffers in turn, so that the next S is formed while this one's
-// probabilities are worked out.
+// The two groups w are the two halves of the rows and share each key tile; an item
+// of one half has the first group alone.  Each group takes a tile in two steps of 64
+// keys, whose S stand side by side: while it works out the probabilities of one, the
+// tensor cores run the other's P V and, over the same columns, the next S.  (Whole
+// tiles, one S a group: prompt 242 us, windows 311 us; the groups made to take turns:
+// 234 and 292 us.)
 //
 // The reference `ref` of a row's exponents follows its maximum only when that
 // has grown by more than 2^8: until then probabilities up to 256 are as precise
 // in bf16 and the sums stay in fp32, and O needs no rescaling (which would mean
 // reading and writing 128 columns of TMEM between two products).
 //
-// Measured: a prompt of 8,192 tokens, 16 heads over two kv heads, 242 us (1,136
-// TFLOP/s of the pairs that the mask leaves; 7% more are multiplied in the tiles that it
-// crosses); 2,048 tokens, 32 heads, over 65,536 keys 1,545 us (1,400 TFLOP/s); 256 windows
-// of 60 rows 311 us (4.8 TB/s).  Bound by the way round from a tile's scores over its
-// probabilities to its product: the tensor cores are busy half of the time, each group's
-// sixteen exponentials a cycle and SM and the loads from TMEM take nearly as long as its
-// products, and what one group waits for the other does not always fill.
+// Measured: a prompt of 8,192 tokens, 16 heads over two kv heads, 223 us (1,230
+// TFLOP/s of the pairs that the mask leaves; some tiles more are multiplied where it
+// crosses them); 2,048 tokens, 32 heads, over 65,536 keys 1,515 us (1,430 TFLOP/s, the
+// clock falling under the load); 256 windows of 60 rows 258 us (5.8 TB/s).  Bound by the
+// products, of which S for 64 keys is fed by shared memory at three quarters of its
+// rate, and by what the way from S to P leaves between them.  (A share of the
+// exponentials by a polynomial made it slower, 250 to 276 us for 242 us: the special
+// function unit is not what it waits for.)
 #include "kda_paged_tc.cuh"
 
 namespace kda {
@@ -40,46 +42,38 @@ constexpr int BM = 128;                        // rows per half
 constexpr int SLOTS = 5;                       // ring of K / V tiles
 constexpr int SLOT = BK * D * 2;               // 32 KB: two 64-channel blocks of 128 rows x 128 B
 constexpr int QHALF = BM * D * 2;
+constexpr int HALF_K = (BK / 2 * 128) >> 4;    // from a K or V tile's first 64 keys to the others, in descriptor units
 constexpr int OFF_Q = 0;
 constexpr int OFF_KV = 2 * QHALF;
 constexpr int OFF_SCAN = OFF_KV + SLOTS * SLOT;  // the start's sums
 constexpr int OFF_BAR = OFF_SCAN + 256;
 constexpr int SEGS = 4;                        // ring of segments ahead of the roles
-constexpr int NBAR = 2 * SLOTS + 21 + 2 * SEGS;
+constexpr int NBAR = 2 * SLOTS + 20 + 2 * SEGS;
 constexpr int OFF_MISC = (OFF_BAR + NBAR * 8 + 63) / 64 * 64;  // TMEM address, abort flag, start of the block's line
 constexpr int OFF_SEG = OFF_MISC + 64;
 constexpr int OFF_MX = OFF_SEG + SEGS * 64;    // [group][half of the keys][row] maximum, sum
 constexpr int SMEM = OFF_MX + 4 * BM * 4;
 static_assert(OFF_SCAN % 16 == 0 && OFF_BAR % 8 == 0 && OFF_SEG % 64 == 0 && SMEM <= 232448, "shared memory layout");
 constexpr int SOFT = 16;                       // softmax warps
-constexpr int THREADS = (SOFT + 4) * 32;       // (registers are given out by four warps)
-// registers a thread: 96 at launch (640 x 96 = 61,440), then 104 for the softmax
-// warps, which hold half a row of S, and 64 for the others: 512 x 104 + 128 x 64 = 61,440
-constexpr int REGS_SOFT = 104, REGS_AUX = 64;
-static_assert(SOFT * 32 * REGS_SOFT + 128 * REGS_AUX <= THREADS * 96, "register split");
+constexpr int THREADS = (SOFT + 4) * 32;
 constexpr int TCOLS = 512;
 constexpr uint32_t COL_S = 0, COL_O = 256;     // + 128 w
 constexpr float GROW = 8.f;                    // log2 growth of a maximum that ref follows
 
 struct Bars {
-    uint64_t *kv_full, *kv_empty, *q_full, *q_empty, *s_full, *p_ready, *pv_done, *o_free, *last, *turn, *hand, *seg_full, *seg_empty;
+    uint64_t *kv_full, *kv_empty, *q_full, *q_empty, *s_full, *p_ready, *pv_done, *o_free, *last, *seg_full, *seg_empty;
     __device__ explicit Bars(uint8_t *sm) {
         uint64_t *b = reinterpret_cast<uint64_t *>(sm + OFF_BAR);
         kv_full = b;
         kv_empty = b + SLOTS;
         q_full = b + 2 * SLOTS;      // [2]
         q_empty = q_full + 2;        // [2]
-        // by S buffer and the group that works on it: 0 and 1 the groups' own, 2 the
-        // second buffer when the first group has both (each barrier has one group to
-        // wait on it, which sees every phase)
-        s_full = q_empty + 2;        // [3]
-        p_ready = s_full + 3;        // [3]
-        pv_done = p_ready + 3;       // [3]
-        o_free = pv_done + 3;        // [2]
+        s_full = q_empty + 2;        // [group][half of a tile's keys]
+        p_ready = s_full + 4;        // the same
+        pv_done = p_ready + 4;       // the same
+        o_free = pv_done + 4;        // [2]
         last = o_free + 2;           // [2] products in flight when a wait ran out
-        turn = last + 2;             // [2] the other group's probabilities are done
-        hand = turn + 2;             // [2] the second S is the first (second) warp's from here on
-        seg_full = hand + 2;
+        seg_full = last + 2;
         seg_empty = seg_full + SEGS;
     }
 };
@@ -97,19 +91,19 @@ __device__ __forceinline__ TileReq tile_req(const PagedAttn &a, int i, int th, i
     return q;
 }
 // Length of an item in the line: first some units for what an item costs besides
-// its tiles (the first S, O on its way out: measured, 5 us where the tensor cores
-// wait for it, 2.5 us where an item of one half waits for memory all the same), then
-// two units (1.7 us) a tile, one (1.3 us) for one half; always even, so that every
-// cut falls on a tile of either kind.  An item without keys takes the place of one
-// tile.  A cut inside the fixed part leaves the item to the next block.
-__host__ __device__ constexpr int item_head(bool alt) { return alt ? 2 : 6; }
+// its tiles (the first S, O on its way out), then one for each tile, of one half or
+// two: alone, a half is no sooner through its way from S to P V.  (Heads of 1 and 2,
+// 2 and 2, 2 and 4, 3 and 4 tiles: each slower on windows or on prompts by 2 to 8%.)
+// An item without keys takes the place of one tile.  A cut inside the fixed part
+// leaves the item to the next block.
+__host__ __device__ constexpr int item_head(bool alt) { return alt ? 1 : 3; }
 __device__ __forceinline__ int item_units(const PagedAttn &a, const TileReq &q, int g, int th) {
     const int j0 = g * 2 * th, j1 = min(q.n, j0 + 2 * th) - 1;
     int lo, hi, t0, t1;
     key_tiles(a, q.r, j0, j1, lo, hi, t0, t1);
     const int nt = max(1, t1 - t0);
     const bool alt = j1 - j0 + 1 <= th;
-    return item_head(alt) + (alt ? (nt + 1) & ~1 : 2 * nt);
+    return item_head(alt) + nt;
 }
 // Units of the row tiles before g (closed form: a long request has thousands).
 __device__ __forceinline__ int64_t units_before(const PagedAttn &a, const TileReq &q, int g, int th) {
@@ -124,7 +118,7 @@ __device__ __forceinline__ int64_t units_before(const PagedAttn &a, const TileRe
         if (gw < neg) gw = neg;
         if (gw < full) tiles -= floor_sum(full - gw, BK, TT, gw * TT - d);
     }
-    int64_t u = 2 * tiles + (int64_t)item_head(false) * full;
+    int64_t u = tiles + (int64_t)item_head(false) * full;
     if (g > full) u += item_units(a, q, full, th);  // the last, shorter row tile
     return u;
 }
@@ -166,9 +160,8 @@ struct Walk {
         int t0, t1;
         key_tiles(a, q.r, j0, j1, s.lo, s.hi, t0, t1);
         s.alt = j1 - j0 + 1 <= th;
-        const int sh = s.alt ? 0 : 1;
         const int head = item_head(s.alt);
-        const int b = max(0, (int)(pos - A) - head) >> sh, e = min(max(0, (int)(stop - A) - head) >> sh, t1 - t0);
+        const int b = max(0, (int)(pos - A) - head), e = min(max(0, (int)(stop - A) - head), t1 - t0);
         const bool some = stop - A > head;
         s.t0 = t0 + b;
         s.nt = max(0, e - b);
@@ -244,18 +237,13 @@ __device__ __forceinline__ void walk_to(const PagedAttn &a, Walk &w, int th, int
     }
 }
 
-// K and V tiles are loaded in the order of their first use, K0 V0 K1 V1 .. (one
-// half: K0 K1 V0 K2 V1 .., two S being formed before the first P V).  Place of V_j,
-// counted from the item's first.
-__device__ __forceinline__ int seq_v(bool alt, int j, int nt) { return alt ? (j == nt - 1 ? 2 * nt - 1 : 2 * j + 2) : 2 * j + 1; }
-
 // The products are issued by a whole converged warp, one elected lane of which
 // does it, in batches of straight code: the issuing warp is on the path of every
 // tile (with a descriptor built and a lane elected for each product it took some
 // 2,200 cycles a tile and half, more than the products themselves).
 //
-// S = Q K^T: eight steps of 16 channels; q, k are the descriptors of the first
-// step, each step 32 bytes on, the second 64 channels one block on.
+// S = Q K^T for 64 keys: eight steps of 16 channels; q, k are the descriptors of the
+// first step, each step 32 bytes on, the second 64 channels one block on.
 __device__ __forceinline__ void issue_qk(uint32_t d, uint64_t q, uint64_t k, uint32_t idesc) {
     asm volatile(
         "{\n .reg .pred e, t, f;\n .reg .b64 a, b;\n"
@@ -272,19 +260,16 @@ __device__ __forceinline__ void issue_qk(uint32_t d, uint64_t q, uint64_t k, uin
         "l"(q), "l"(k), "r"(idesc)
         : "memory");
 }
-// O (+)= P V: eight steps of 16 keys, P 8 columns of TMEM on, V 2 KB on.
+// O (+)= P V for 64 keys: four steps of 16 keys, V 2 KB on; P stands in the first 16 of
+// each 32 columns of S.
 __device__ __forceinline__ void issue_pv(uint32_t d, uint32_t p, uint64_t v, uint32_t idesc, bool acc) {
     asm volatile(
         "{\n .reg .pred e, t, f;\n .reg .b32 a;\n .reg .b64 b;\n"
         " setp.eq.u32 t, 0, 0;\n setp.ne.u32 f, %4, 0;\n elect.sync _|e, 0xffffffff;\n"
         " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, f;\n"
         " add.u32 a, %1, 8;\n add.s64 b, %2, 128;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
-        " add.u32 a, %1, 16;\n add.s64 b, %2, 256;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
-        " add.u32 a, %1, 24;\n add.s64 b, %2, 384;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
-        " add.u32 a, %1, 32;\n add.s64 b, %2, 512;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
-        " add.u32 a, %1, 40;\n add.s64 b, %2, 640;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
-        " add.u32 a, %1, 48;\n add.s64 b, %2, 768;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
-        " add.u32 a, %1, 56;\n add.s64 b, %2, 896;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
+        " add.u32 a, %1, 32;\n add.s64 b, %2, 256;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
+        " add.u32 a, %1, 40;\n add.s64 b, %2, 384;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
         "}\n" ::"r"(d),
         "r"(p), "l"(v), "r"(idesc), "r"((uint32_t)acc)
         : "memory");
@@ -410,13 +395,7 @@ __device__ __forceinline__ void load_role(const PagedAttn &a, const PagedMaps &m
             return true;
         };
         for (int j = 0; j < s.nt; ++j) {
-            if (!s.alt) {
-                if (!tile(j, false) || !tile(j, true)) return drain();
-            } else {
-                if (j == 0 && !tile(0, false)) return drain();
-                if (j + 1 < s.nt && !tile(j + 1, false)) return drain();
-                if (!tile(j, true)) return drain();
-            }
+            if (!tile(j, false) || !tile(j, true)) return drain();
         }
     }
 }
@@ -428,7 +407,7 @@ __device__ __forceinline__ void load_role(const PagedAttn &a, const PagedMaps &m
 // of them by: whoever has no product on a tile gives it back as soon as it came.
 __device__ __forceinline__ void mma_role(const PagedAttn &a, uint8_t *sm, uint32_t tmem, int x, const Gate &gate) {
     const Bars bar(sm);
-    constexpr uint32_t ID_QK = idesc_bf16_f32(BM, BK), ID_PV = idesc_bf16_f32_bmn(BM, D);
+    constexpr uint32_t ID_QK = idesc_bf16_f32(BM, BK / 2), ID_PV = idesc_bf16_f32_bmn(BM, D);
     const int lane = threadIdx.x & 31;
     const uint32_t base = smem_u32(sm), to = tmem + COL_O + x * 128;
     const uint64_t dq = sdesc_sw128(base + OFF_Q), dk = sdesc_sw128(base + OFF_KV),
@@ -448,24 +427,13 @@ __device__ __forceinline__ void mma_role(const PagedAttn &a, uint8_t *sm, uint32
         if (lane == 0) mbar_arrive(b);
         __syncwarp();
     };
-    uint32_t par = 0;  // parity bits: 0, 1 halves of Q; 2..4 P by barrier; 5 O; 6 the second S handed over
-    bool ok = true, was_alt = false;
+    uint32_t par = 0;  // parity bits: 0, 1 halves of Q; 2, 3 P by half of the tile; 5 O
+    bool ok = true;
     Seg s;
     int iseg = 0;
-    // The second S belongs to the second warp, but in items of one half to the first.
-    // Where the kinds change, the owner's products on it end before the other's begin:
-    // whoever had it commits what it has issued to hand[0] (to the first warp) or
-    // hand[1], and the other waits.  The two are passed in turn, so no phase is missed.
-    auto handed = [&]() -> bool {
-        const bool got = gate(&bar.hand[x], (par >> 6) & 1);
-        par ^= 1u << 6;
-        return got;
-    };
     while (ok && next_seg(sm, bar, iseg, gate, s)) {
         if (s.nt == 0) continue;
-        const bool alt = s.alt, change = alt != was_alt;
-        was_alt = alt;
-        if (change && (alt ? x == 1 : x == 0)) mma_commit_w(&bar.hand[x ^ 1]);
+        const bool alt = s.alt;
         const int nt = s.nt, half = alt ? s.half : x;
         auto query = [&](int h) -> bool {
             const bool got = gate(&bar.q_full[h], (par >> h) & 1);
@@ -489,39 +457,49 @@ __device__ __forceinline__ void mma_role(const PagedAttn &a, uint8_t *sm, uint32
             give(&bar.q_empty[half ^ 1]);
         }
         const uint64_t q = dq + (uint32_t)half * (QHALF >> 4);
-        auto qk = [&](int j) {  // S of key tile j, into this warp's buffer or, for one half, both in turn
-            const int buf = alt ? j & 1 : x;
-            issue_qk(tmem + COL_S + buf * 128, q, dk + (uint32_t)kslot * (SLOT >> 4), ID_QK);
-            mma_commit_w(&bar.s_full[alt && buf ? 2 : buf]);  // (first: it is waited for; a commit covers all before it)
+        // S of half a tile's keys
+        const uint32_t sb = tmem + COL_S + x * 128;
+        auto qk = [&](int u) {
+            issue_qk(sb + u * 64, q, dk + (uint32_t)(kslot * (SLOT >> 4) + u * HALF_K), ID_QK);
+            mma_commit_w(&bar.s_full[2 * x + u]);  // (first: it is waited for; a commit covers all before it)
+        };
+        auto k_done = [&](int j) {
             mma_commit_w(&bar.kv_empty[kslot]);
             if (j == nt - 1) mma_commit_w(&bar.q_empty[half]);
         };
-        const int ahead = alt ? 2 : 1;  // S buffers
-        for (int j = 0; ok && j < ahead && j < nt; ++j) {
-            if (j == 1 - x && change && alt == (x == 0)) ok = handed();
-            ok = take(kslot) && ok;
-            tc_fence_after();
-            if (ok) qk(j);
+        ok = take(kslot) && ok;
+        tc_fence_after();
+        if (ok) {
+            qk(0);
+            qk(1);
+            k_done(0);
         }
-        if (nt == 1 && alt && change) ok = ok && handed();
         for (int j = 0; ok && j < nt; ++j) {
-            // all waits come before the products, P's last: then P V and the next S are
-            // issued in one go
-            const int buf = alt ? j & 1 : x, b = alt && buf ? 2 : buf;
             ok = take(vslot);
-            if (j + ahead < nt) ok = take(kslot) && ok;
             if (j == 0) {  // the group's last item must have left O
                 ok = gate(&bar.o_free[x], ((par >> 5) & 1) ^ 1) && ok;
                 par ^= 1u << 5;
             }
-            ok = gate(&bar.p_ready[b], (par >> (2 + b)) & 1) && ok;
-            par ^= 1u << (2 + b);
-            if (!ok) break;
-            tc_fence_after();
-            issue_pv(to, tmem + COL_S + buf * 128, dv + (uint32_t)vslot * (SLOT >> 4), ID_PV, j > 0);
-            mma_commit_w(&bar.pv_done[b]);
-            mma_commit_w(&bar.kv_empty[vslot]);
-            if (j + ahead < nt) qk(j + ahead);
+            // P V of each half, and after it S of the next tile's half over the same columns
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                ok = gate(&bar.p_ready[2 * x + u], (par >> (2 + u)) & 1) && ok;
+                par ^= 1u << (2 + u);
+                if (!ok) break;
+                tc_fence_after();
+                issue_pv(to, sb + u * 64, dv + (uint32_t)(vslot * (SLOT >> 4) + u * HALF_K), ID_PV, j + u > 0);
+                mma_commit_w(&bar.pv_done[2 * x + u]);
+                if (u) mma_commit_w(&bar.kv_empty[vslot]);
+                if (j + 1 < nt) {
+                    if (u == 0) {
+                        ok = take(kslot);
+                        tc_fence_after();
+                        if (!ok) break;
+                    }
+                    qk(u);
+                    if (u) k_done(j + 1);
+                }
+            }
         }
     }
     if (!ok || *gate.abort) {  // let the products in flight end before TMEM is given back
@@ -609,7 +587,7 @@ __device__ __forceinline__ void finish(const PagedAttn &a, uint32_t to, int th, 
 // Two threads, of two warps that meet at a barrier of their own, share a row.  A
 // wait that runs out is passed on at the next meeting, so both leave together.
 __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, uint32_t tmem, int th, const Gate &gate) {
-    constexpr int HK = BK / 2;  // keys of one thread
+    constexpr int HK = BK / 4;  // keys of one thread: a half of half a tile
     const Bars bar(sm);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, x = warp >> 3, hf = (warp >> 2) & 1;
     const int row = (warp & 3) * 32 + lane;             // row of the half = TMEM lane
@@ -618,8 +596,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
     const int id = 1 + x * 4 + (warp & 3);
     float *mx = reinterpret_cast<float *>(sm + OFF_MX) + x * 2 * BM + row;  // + BM hf
     const float sc = a.scale_log2;
-    int n0 = 0, n2 = 0;  // this group's events by barrier: its own, and the first group's on the second buffer
-    int nboth = 0;       // tiles of two halves
+    int n = 0;       // this group's tiles before this segment's
     uint32_t seq0 = 0;  // K / V tiles before this segment's
     bool failed = false;
     for (int iseg = 0;; ++iseg) {
@@ -642,20 +619,18 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
         // ref follows the maximum once that has passed this (never for the half's rows past the
         // item's tokens: they hold the next request's queries, or what was there before)
         float bound = row < min(th, seg->ntok - (alt ? 0 : x) * th) * a.G ? -INFINITY : INFINITY;
-        const int ne = alt ? (x ? 0 : s.nt) : 2 * s.nt;
+        const int ne = alt && x ? 0 : 2 * s.nt;  // halves of tiles
         uint64_t *prev = nullptr;  // the group's last product
         int prevp = 0;
-        for (int e = alt ? 0 : x; e < ne; e += alt ? 1 : 2) {
-            const int j = alt ? e : e >> 1, b = alt && (e & 1) ? 2 : x, ph = ((b == 2 ? n2 : n0) + (e >> 1)) & 1;
-            const uint32_t ts = tmem + lanes + COL_S + (e & 1) * 128;
-            const int key0 = (s.t0 + j) * BK;
+        for (int e = 0; e < ne; ++e) {
+            const int j = e >> 1, u = e & 1, b = 2 * x + u, ph = (n + j) & 1;
+            const uint32_t ts = tmem + lanes + COL_S + x * 128 + u * 64 + HK * hf;  // this thread's scores, and P
+            const int key0 = (s.t0 + j) * BK + u * (BK / 2);
             if (!gate(&bar.s_full[b], ph)) failed = true;
             tc_fence_after();
             float v[HK];
-            tmem_ld32(ts + HK * hf, v);
-            tmem_ld32(ts + HK * hf + 32, v + 32);
+            tmem_ld32(ts, v);
             tmem_arrived(v);
-            tmem_arrived(v + 32);
             // of this thread's keys, the row sees [c0, c1)
             const int c1 = min(pos + 1, s.hi) - key0 - HK * hf, c0 = first_key - key0 - HK * hf;
             if (__any_sync(0xffffffffu, c1 < HK || c0 > 0)) {
@@ -673,8 +648,8 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
             m0 = max3(m0, v[HK - 4], v[HK - 3]);
             m1 = max3(m1, v[HK - 2], v[HK - 1]);
             const float mt = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * sc;
-            // Meet: both have read S, whose columns P overwrites from here on; and does
-            // ref have to follow?  (a warp that gave up counts 32, one that asks for it 1)
+            // Meet: does ref have to follow?  (a warp that gave up counts 32, one that asks
+            // for it 1)
             const bool grow = __any_sync(0xffffffffu, mt > bound);
             const int said = meet_count<64>(id, failed || (grow && lane == 0));
             if (said >= 32) return;
@@ -709,48 +684,36 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
             // rows of V that no key of this item stands in may hold anything: zero
             // them (0 x NaN is NaN); each group before its own product
             const int z0 = max(0, (s.lo & ~(a.box - 1)) - key0), z1 = min(BK, s.hi - key0);
-            if (z0 > 0 || z1 < BK) {
-                const uint32_t q = seq0 + seq_v(alt, j, s.nt);
+            if (u == 0 && (z0 > 0 || z1 < BK)) {
+                const uint32_t q = seq0 + 2 * j + 1;
                 if (!gate(&bar.kv_full[q % SLOTS], (int)((q / SLOTS) & 1))) failed = true;
                 uint8_t *vt = sm + OFF_KV + (q % SLOTS) * SLOT;
-                for (int u = threadIdx.x & (2 * BM - 1); u < BK * 16; u += 2 * BM) {
-                    const int r = u >> 4, c = u & 15;
+                for (int w = threadIdx.x & (2 * BM - 1); w < BK * 16; w += 2 * BM) {
+                    const int r = w >> 4, c = w & 15;
                     if (r < z0 || r >= z1)
                         *reinterpret_cast<uint4 *>(vt + (c >> 3) * (SLOT / 2) + r * 128 + ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
                 }
                 fence_async_smem();
             }
-            // The groups work out their probabilities in turn: left to themselves they
-            // drift into step, and the tensor cores then wait for both at once.
-            if (!alt) {
-                const int k = nboth + j;
-                if (x ? !gate(&bar.turn[1], k & 1) : k > 0 && !gate(&bar.turn[0], (k - 1) & 1)) failed = true;
-            }
-            // probabilities, 32 at a time over S's own columns
+            // probabilities, over the scores that they come from
             const uint64_t sc2 = pack2(sc, sc), ref2 = pack2(-ref, -ref);
             uint64_t sum2 = 0;
+            uint32_t p[HK / 2];
 #pragma unroll
-            for (int c = 0; c < HK; c += 32) {
-                uint32_t p[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    float e0, e1;
-                    unpack2(fma2(pack2(v[c + 2 * i], v[c + 2 * i + 1]), sc2, ref2), e0, e1);
-                    e0 = ex2(e0);
-                    e1 = ex2(e1);
-                    sum2 = add2(sum2, pack2(e0, e1));
-                    const __nv_bfloat162 w = __floats2bfloat162_rn(e0, e1);
-                    p[i] = *reinterpret_cast<const uint32_t *>(&w);
-                }
-                tmem_st16(ts + (HK * hf + c) / 2, p);
+            for (int i = 0; i < HK / 2; ++i) {
+                float e0, e1;
+                unpack2(fma2(pack2(v[2 * i], v[2 * i + 1]), sc2, ref2), e0, e1);
+                e0 = ex2(e0);
+                e1 = ex2(e1);
+                sum2 = add2(sum2, pack2(e0, e1));
+                const __nv_bfloat162 w = __floats2bfloat162_rn(e0, e1);
+                p[i] = *reinterpret_cast<const uint32_t *>(&w);
             }
+            tmem_st16(ts, p);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&bar.p_ready[b]);
-                if (!alt) mbar_arrive(&bar.turn[x ^ 1]);
-            }
+            if (lane == 0) mbar_arrive(&bar.p_ready[b]);
             float l0, l1;
             unpack2(sum2, l0, l1);
             l += l0 + l1;
@@ -758,8 +721,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
             prevp = ph;
         }
         seq0 += 2 * s.nt;
-        if (!alt) n0 += s.nt, nboth += s.nt;
-        else if (x == 0) n0 += (s.nt + 1) / 2, n2 += s.nt / 2;
+        if (!alt || x == 0) n += s.nt;
         if (!(alt && x)) {
             float sum = 0.f;
             if (prev) {
@@ -797,10 +759,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(&bar.q_full[i], 1);
             mbar_init(&bar.q_empty[i], 2);
             mbar_init(&bar.o_free[i], 8);
-            mbar_init(&bar.turn[i], SOFT / 2);
-            mbar_init(&bar.hand[i], 1);
         }
-        for (int i = 0; i < 3; ++i) {
+        for (int i = 0; i < 4; ++i) {
             mbar_init(&bar.s_full[i], 1);
             mbar_init(&bar.p_ready[i], 8);
             mbar_init(&bar.pv_done[i], 1);
@@ -835,11 +795,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     // read 23 times from HBM otherwise); each part should be worth the pieces that its
     // borders cost.
     auto parts = [&](int64_t total) -> int {
-        const int64_t by_size = (kv_tiles * (2 * SLOT) + (64 << 20) - 1) >> 26, by_work = total / (gridDim.x * 256);
+        const int64_t by_size = (kv_tiles * (2 * SLOT) + (64 << 20) - 1) >> 26, by_work = total / (gridDim.x * 128);
         const int64_t n = by_size < by_work ? by_size : by_work;
         return n < 1 ? 1 : n > max_parts ? max_parts : (int)n;
     };
-    const PagedLine line = paged_line<THREADS>(a, scratch, min_per, 2, units, parts);
+    const PagedLine line = paged_line<THREADS>(a, scratch, min_per, units, parts);
     const int64_t P0 = line.P0, P1 = line.P1;
     if (P0 >= P1) {
         asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -852,10 +812,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t tmem = sh->tmem;
     const Gate gate{&sh->abort, a.err};
     if (warp < SOFT) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFT));
         softmax_role(a, sm, tmem, th, gate);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_AUX));
         if (warp < SOFT + 2)
             mma_role(a, sm, tmem, warp - SOFT, gate);
         else if (warp == SOFT + 2)
@@ -908,7 +866,7 @@ int launch_paged_tile(PagedAttn a, const void *k, const void *v, int64_t page_st
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = after_rows ? 1 : 0;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_tile_kernel, maps, qmap, a, th, 8, max_parts);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_tile_kernel, maps, qmap, a, th, 4, max_parts);
     note_launch("paged_tile", s);
     return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
