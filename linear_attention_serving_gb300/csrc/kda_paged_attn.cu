@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) paged_join_kernel(PagedAttn a
     }
 }
 
-constexpr int FEW_ROWS = 32;
+constexpr int FEW_ROWS = 16;
 
 int launch_join(const PagedAttn &a, const JoinSet &s0, const JoinSet &s1, int64_t max_rows, bool f32, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
@@ -227,23 +227,22 @@ int kda_paged_attn(const void *q, const void *k_cache, const void *v_cache, cons
         if ((rc = launch_paged_rows(a, k_cache, v_cache, page_stride, s))) return rc;
         return launch_join(a, js[0], js[1], max_rows, true, s);
     }
-    // Up to 32 rows of a kv head fit the few-rows kernel at once; over that the tile
-    // kernel, which has room for 128 rows at one cost, is faster (256 windows of 60 rows:
-    // 311 us against 470 us in pieces of 64).  With longer requests in the call it takes
-    // them, and the few-rows kernel the single tokens (rows up to the next of 16, 32 from
-    // G on).
+    // Up to 16 rows of a kv head fit the few-rows kernel at once; over that the tile
+    // kernel, which has room for 128 rows at one cost, is faster (256 windows over up to
+    // 4,096 keys of 8 heads: 255 us for 16 rows in the one, then for 20, 24 and 32 rows 251,
+    // 254 and 253 us in the other, against 279, 296 and 319 us).  With longer requests in
+    // the call it takes them, and the few-rows kernel the single tokens.
     const bool tiles = cache_dtype == KDA_BF16 && a.G <= 128 && max_rows > FEW_ROWS;
-    const int few_rows = a.G <= 16 ? 16 : FEW_ROWS;
     // every request long enough for the tile kernel: one of T_total tokens, or all
     // of max_q (the offsets may still say less: the tile kernel then takes that too)
     const bool few = !tiles || (a.G <= FEW_ROWS && n_seqs > 1 && T_total != (int64_t)n_seqs * a.max_q);
     if (few) {
-        if (tiles) a.row_hi = few_rows;
+        if (tiles) a.row_hi = FEW_ROWS;
         js[0] = use(w.rows, paged_few_blocks());
-        if ((rc = launch_paged_few(a, cache_dtype, k_cache, v_cache, page_stride, tiles ? few_rows : max_rows, s))) return rc;
+        if ((rc = launch_paged_few(a, cache_dtype, k_cache, v_cache, page_stride, tiles ? FEW_ROWS : max_rows, s))) return rc;
     }
     if (tiles) {
-        a.row_lo = few ? few_rows : 0;
+        a.row_lo = few ? FEW_ROWS : 0;
         a.row_hi = INT32_MAX;
         // (the kernel takes parts by the bytes that the lengths say; a table that cannot
         // hold as many asks for none, which spares the join their leads)

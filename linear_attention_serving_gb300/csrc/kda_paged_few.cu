@@ -1,5 +1,6 @@
 // kda_paged_few.cu -- paged attention on tcgen05 for few rows (single tokens,
-// draft windows; bf16 and e4m3 caches): NR = 16 or 32 rows of one kv head at a time.
+// draft windows; bf16 and e4m3 caches): NR = 16 or 32 rows of one kv head at a time (32
+// for e4m3 caches, and for bf16 where a token alone has more rows than a tile has).
 // Each key and value is read for few rows, so the time is the pages' bytes over HBM;
 // what the kernel has to do is keep copies in flight and stay out of their way.
 //

@@ -217,6 +217,13 @@ def test_attn_row_tiles_of_both_kinds_in_one_block():
     attn_close(o, lse, attn_ref(d["q"], d["k_cache"], d["v_cache"], d["table"], d["cu"], d["kv"]), BF16, BF16)
 
 
+@pytest.mark.parametrize("new,ctx", [([1], [40]), ([3, 0, 1], [0, 9, 200])])
+@pytest.mark.parametrize("g", [16, 17, 24, 130])
+def test_attn_wide_groups(g, new, ctx):
+    """Groups at and over the rows of the kernel for few, and over a tile's: bf16."""
+    check(new, ctx, 2, g, 16, BF16, seed=18)
+
+
 @pytest.mark.parametrize("new,ctx", [([197, 100], [3, 19]), ([132, 20, 196, 32], [500, 700, 0, 1000])])
 def test_attn_row_tiles_of_both_kinds_in_turn(new, ctx):
     """Items of one half, over several tiles, right before and after items of two halves,
