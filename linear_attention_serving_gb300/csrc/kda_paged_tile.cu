@@ -16,7 +16,7 @@
 // keys, whose S stand side by side: while it works out the probabilities of one, the
 // tensor cores run the other's P V and, over the same columns, the next S.  (Whole
 // tiles, one S a group: prompt 242 us, windows 311 us; the groups made to take turns:
-// 234 and 292 us.)
+// 234 and 292 us; registers given out by role: 226 and 267 us.)
 //
 // The reference `ref` of a row's exponents follows its maximum only when that
 // has grown by more than 2^8: until then probabilities up to 256 are as precise
@@ -27,8 +27,8 @@
 // TFLOP/s of the pairs that the mask leaves; some tiles more are multiplied where it
 // crosses them); 2,048 tokens, 32 heads, over 65,536 keys 1,515 us (1,430 TFLOP/s, the
 // clock falling under the load); 256 windows of 60 rows 258 us (5.8 TB/s).  Bound by the
-// products, of which S for 64 keys is fed by shared memory at three quarters of its
-// rate, and by what the way from S to P leaves between them.  (A share of the
+// products (S for 64 keys reads its operands, by their bytes, at three quarters of the
+// rate) and by what the way from S to P leaves between them.  (A share of the
 // exponentials by a polynomial made it slower, 250 to 276 us for 242 us: the special
 // function unit is not what it waits for.)
 #include "kda_paged_tc.cuh"
