@@ -1,12 +1,12 @@
 // kda_paged_rows.cu -- paged attention in fp32.
 //
-// A block has four consumer warps and one producer warp.  The producer walks the
+// A block has eight consumer warps (four, where a call has few rows) and one producer warp.  The producer walks the
 // block's line of key tiles (16 keys: 8 KB of K and 8 KB of V), looks pages up in
 // the block table, and has the tensor memory accelerator fill a ring of four tiles,
-// two blocks on an SM: 128 KB in flight.  A consumer warp holds up to 16 rows.  Few
-// rows (<= 16): the four warps take every fourth tile, each with its own running
-// maximum and sum, merged in shared memory at the item's end.  More rows: the warps
-// take a quarter each (two by two, a half, up to 32) and share the tiles.
+// two blocks on an SM: 128 KB in flight.  A consumer warp holds up to 8 rows.  Few
+// rows (<= 8): the warps take every eighth tile, each with its own running maximum
+// and sum, merged in shared memory at the item's end.  More rows: two, four or eight
+// warps take a share each of up to 16, 32 or 64, and the others other tiles.
 //
 // Products are plain fp32 multiply-adds: tf32 parts would lose digits that the fp32
 // path of this library keeps (three products of two parts each left 2.5e-6 where this
@@ -14,30 +14,35 @@
 // of all keys for the output, so a warp reads each key and value once from shared
 // memory whatever its rows are.
 //
-// Measured: one token of 16 requests, 16 heads of up to 3,000 keys, 4.6 TB/s (46 us), where the copies in flight and the
-// start and the join bound it.  Many rows are bound by the chains of loads and shuffles of
-// two warps a scheduler (8 requests of 40 rows over 2,040 keys of 8 heads: 10.9 TFLOP/s,
-// 244 us; a row at a time 320 us).
+// Measured: one token of 16 requests, 16 heads of up to 3,000 keys, 4.8 TB/s (45 us), where
+// the copies in flight and the start and the join bound it.  Many rows are bound by loads
+// from shared memory and the shuffles between the products (8 requests of 40 rows over 2,040
+// keys of 8 heads: 16 TFLOP/s, 166 us, and of 320 rows 27 TFLOP/s, 798 us; four warps of 16
+// rows 246 and 1,358 us).
 #include "kda_paged.cuh"
 
 namespace kda {
 namespace {
 using namespace tc;
 
-constexpr int CONS = 4;                      // consumer warps
-constexpr int THREADS = (CONS + 1) * 32;
+constexpr int RW = 8;                        // rows a warp holds at most
 constexpr int STAGES = 4;
 constexpr int HALF = 8192;                   // bytes of K (and of V) of one tile
 constexpr int STAGE = 2 * HALF;
-constexpr int OFF_RED = STAGES * STAGE;      // [4][16][128] fp32
-constexpr int OFF_P = OFF_RED + CONS * 16 * D * 4;  // probabilities [4][16][16]
-constexpr int OFF_ML = OFF_P + CONS * 16 * 16 * 4;
-constexpr int OFF_DESC = OFF_ML + CONS * 16 * 8;
-constexpr int OFF_BAR = OFF_DESC + STAGES * 64;
-constexpr int OFF_MEET = OFF_BAR + 2 * STAGES * 8;  // the consumer warps' meeting at an item's end
-constexpr int OFF_ABORT = OFF_MEET + 8;
-constexpr int SMEM = OFF_ABORT + 16;
-static_assert(OFF_RED % 1024 == 0 && OFF_ML % 16 == 0 && OFF_DESC % 16 == 0 && OFF_BAR % 8 == 0, "shared memory layout");
+// CONS: consumer warps, eight, or four in calls of up to 8 rows (45 us instead of 48 for
+// one token of 16 requests: fewer pieces to merge, fewer warps to give a tile back)
+template <int CONS_> struct Cfg {
+    static constexpr int CONS = CONS_, THREADS = (CONS + 1) * 32;
+    static constexpr int OFF_RED = STAGES * STAGE;                 // [CONS][RW][128] fp32
+    static constexpr int OFF_P = OFF_RED + CONS * RW * D * 4;      // probabilities [CONS][RW][16]
+    static constexpr int OFF_ML = OFF_P + CONS * RW * 16 * 4;
+    static constexpr int OFF_DESC = OFF_ML + CONS * RW * 8;
+    static constexpr int OFF_BAR = OFF_DESC + STAGES * 64;
+    static constexpr int OFF_MEET = OFF_BAR + 2 * STAGES * 8;      // the consumer warps' meeting at an item's end
+    static constexpr int OFF_ABORT = OFF_MEET + 8;
+    static constexpr int SMEM = OFF_ABORT + 16;
+    static_assert(OFF_RED % 1024 == 0 && OFF_ML % 16 == 0 && OFF_DESC % 16 == 0 && OFF_BAR % 8 == 0, "shared memory layout");
+};
 
 constexpr int TK = 16;                       // keys of a tile
 constexpr int NSUB = D * 4 / 128;            // 128-byte pieces of a row, each a block of its own
@@ -49,16 +54,18 @@ struct __align__(16) Desc {
 static_assert(sizeof(Desc) == 64, "descriptor size");
 constexpr int FIRST = 1, LAST = 2, WHOLE = 4, END = 8, MASK = 16;
 
-__device__ __forceinline__ int row_group(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+template <class C> __device__ __forceinline__ int row_group(int rows) {
+    return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 || C::CONS == 4 ? 32 : 64;
+}
 
 __device__ __forceinline__ int req_tiles(const PagedReq &r) {
     const int keys = r.kend - r.k0;
     return keys > 0 ? (keys + TK - 1) / TK : 1;
 }
-__device__ __forceinline__ int64_t line_tiles(const PagedAttn &a, int i, int *err) {
+template <class C> __device__ __forceinline__ int64_t line_tiles(const PagedAttn &a, int i, int *err) {
     const PagedReq r = paged_req(a, i, err);
     if (r.rows == 0) return 0;
-    const int grp = row_group(r.rows);
+    const int grp = row_group<C>(r.rows);
     return (int64_t)a.Hkv * ((r.rows + grp - 1) / grp) * req_tiles(r);
 }
 
@@ -72,11 +79,12 @@ __device__ __forceinline__ void load_tile(void *dst, const void *map, int y, int
         "l"(map), "r"(0), "r"(y), "r"(0), "r"(z), "r"(smem_u32(bar))
         : "memory");
 }
+template <class C>
 __device__ __forceinline__ void produce(const PagedAttn &a, const PagedMaps &maps, uint8_t *sm, int64_t P0, int64_t P1,
                                         int64_t per, int req, int64_t before) {
     const int lane = threadIdx.x & 31;
-    uint64_t *full = reinterpret_cast<uint64_t *>(sm + OFF_BAR), *empty = full + STAGES;
-    volatile int *abort = reinterpret_cast<volatile int *>(sm + OFF_ABORT);
+    uint64_t *full = reinterpret_cast<uint64_t *>(sm + C::OFF_BAR), *empty = full + STAGES;
+    volatile int *abort = reinterpret_cast<volatile int *>(sm + C::OFF_ABORT);
     int stage = 0, phase = 0, issued = 0;
     auto next_stage = [&]() -> bool {
         const bool ok = mbar_wait_ab(&empty[stage], phase ^ 1, abort);
@@ -110,7 +118,7 @@ __device__ __forceinline__ void produce(const PagedAttn &a, const PagedMaps &map
             ++req;  // (the totals say that a request with tiles follows)
             continue;
         }
-        const int nt = req_tiles(r), grp = row_group(r.rows), ngrp = (r.rows + grp - 1) / grp;
+        const int nt = req_tiles(r), grp = row_group<C>(r.rows), ngrp = (r.rows + grp - 1) / grp;
         const int64_t in = pos - before, item = in / nt;
         const int h = (int)(item / ngrp), g = (int)(item - (int64_t)h * ngrp);
         const int64_t A = before + item * nt, B = A + nt;
@@ -127,7 +135,7 @@ __device__ __forceinline__ void produce(const PagedAttn &a, const PagedMaps &map
             te = min(te, (hi - r.k0 + TK - 1) / TK);
         }
         Desc d;
-        d.wr = grp / 16;
+        d.wr = grp / RW;
         d.rpw = (R + d.wr - 1) / d.wr;  // (the same for each, or one waits for the others)
         d.tok0 = r.tok0;
         d.h = h;
@@ -145,7 +153,7 @@ __device__ __forceinline__ void produce(const PagedAttn &a, const PagedMaps &map
                 d.ord = 0;
                 d.key0 = 0;
                 d.kvalid = 0;
-                *reinterpret_cast<Desc *>(sm + OFF_DESC + stage * 64) = d;
+                *reinterpret_cast<Desc *>(sm + C::OFF_DESC + stage * 64) = d;
                 mbar_arrive(&full[stage]);
             }
             advance();
@@ -174,7 +182,7 @@ __device__ __forceinline__ void produce(const PagedAttn &a, const PagedMaps &map
                 d.ord = t - tb;
                 d.key0 = key0;
                 d.kvalid = kvalid;
-                *reinterpret_cast<Desc *>(sm + OFF_DESC + stage * 64) = d;
+                *reinterpret_cast<Desc *>(sm + C::OFF_DESC + stage * 64) = d;
                 mbar_expect_tx(&full[stage], 2 * HALF);
                 load_tile(sm + stage * STAGE, &maps.k, y, pg, &full[stage]);
                 load_tile(sm + stage * STAGE + HALF, &maps.v, y, pg, &full[stage]);
@@ -190,7 +198,7 @@ __device__ __forceinline__ void produce(const PagedAttn &a, const PagedMaps &map
     }
     if (!next_stage()) return;
     if (lane == 0) {
-        reinterpret_cast<Desc *>(sm + OFF_DESC + stage * 64)->flags = END;
+        reinterpret_cast<Desc *>(sm + C::OFF_DESC + stage * 64)->flags = END;
         mbar_arrive(&full[stage]);
     }
 }
@@ -199,72 +207,70 @@ __device__ __forceinline__ void produce(const PagedAttn &a, const PagedMaps &map
 // fp32: lane = (key lane % 16, half of the channels lane / 16) for the scores, four
 // channels for the output; maxima and sums of row r in lane r.
 struct RowsF32 {
-    float o[16][4], m, l;
+    float o[RW][4], m, l;
     // RM: rows that the code is laid out for (R <= RM)
     template <int RM>
     __device__ __forceinline__ void tile(const float *q, float *ps, const uint8_t *k, const uint8_t *v, int lane, int R, float sc,
                                          const Desc &d, int row0, int G, int window, bool mask) {
         const int key = lane & 15, hf = lane >> 4;
-        float4 kr[16];
+        // All rows at once, so that a chain of sums or shuffles does not wait for itself, and
+        // half of the lane's channels at a time, which the registers hold (rows past R hold an
+        // earlier item's queries; nothing of theirs is read).
+        float2 acc[RM];
+        float s[RM], top[RM];
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-            const int ch = 16 * hf + c;
-            kr[c] = *reinterpret_cast<const float4 *>(k + (ch >> 3) * 2048 + key * 128 + (((ch & 7) ^ (key & 7)) << 4));
+        for (int r = 0; r < RM; ++r) acc[r] = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+            float4 kr[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                kr[c] = *reinterpret_cast<const float4 *>(k + (2 * hf + part) * 2048 + key * 128 + ((c ^ (key & 7)) << 4));
+            const float4 *qr = reinterpret_cast<const float4 *>(q) + 16 * hf + 8 * part;
+#pragma unroll
+            for (int r = 0; r < RM; ++r) {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const float4 x = qr[r * (D / 4) + c];
+                    acc[r].x = fmaf(x.x, kr[c].x, acc[r].x);
+                    acc[r].y = fmaf(x.y, kr[c].y, acc[r].y);
+                    acc[r].x = fmaf(x.z, kr[c].z, acc[r].x);
+                    acc[r].y = fmaf(x.w, kr[c].w, acc[r].y);
+                }
+            }
         }
         float corr = 1.f;  // of row `lane`
-        // Four rows at a time, so that a chain of sums or shuffles does not wait for itself
-        // (rows past R hold an earlier item's queries; nothing of theirs is read).
-        constexpr int U = RM == 1 ? 1 : 4;
-#pragma unroll 1
-        for (int r0 = 0; r0 < (RM <= 4 ? 1 : R); r0 += U) {
-            const float4 *qr = reinterpret_cast<const float4 *>(q + r0 * D) + 16 * hf;
-            float2 acc[U];
-            float s[U], top[U], p[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) acc[u] = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int c = 0; c < 16; ++c) {
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const float4 x = qr[u * (D / 4) + c];
-                    acc[u].x = fmaf(x.x, kr[c].x, acc[u].x);
-                    acc[u].y = fmaf(x.y, kr[c].y, acc[u].y);
-                    acc[u].x = fmaf(x.z, kr[c].z, acc[u].x);
-                    acc[u].y = fmaf(x.w, kr[c].w, acc[u].y);
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                s[u] = acc[u].x + acc[u].y;
-                s[u] += __shfl_xor_sync(0xffffffffu, s[u], 16);
-            }
-            if (mask) {
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int pos = d.pos0 + (row0 + r0 + u) / G, at = d.key0 + key;
-                    if (!(at <= pos && (window <= 0 || at > pos - window) && key < d.kvalid)) s[u] = -INFINITY;
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) top[u] = s[u];
-#pragma unroll
-            for (int x = 8; x; x >>= 1)
-#pragma unroll
-                for (int u = 0; u < U; ++u) top[u] = fmaxf(top[u], __shfl_xor_sync(0xffffffffu, top[u], x));
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const float old = __shfl_sync(0xffffffffu, m, r0 + u), mn = fmaxf(old, top[u] * sc);
-                const float ref = mn == -INFINITY ? 0.f : mn;
-                if (lane == r0 + u) {
-                    corr = ex2(m - ref);
-                    m = mn;
-                }
-                p[u] = ex2(fmaf(s[u], sc, -ref));
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (lane < 16) ps[(r0 + u) * 16 + lane] = p[u];
+        for (int r = 0; r < RM; ++r) {
+            s[r] = acc[r].x + acc[r].y;
+            s[r] += __shfl_xor_sync(0xffffffffu, s[r], 16);
         }
+        if (mask) {
+#pragma unroll
+            for (int r = 0; r < RM; ++r) {
+                const int pos = d.pos0 + (row0 + r) / G, at = d.key0 + key;
+                if (!(at <= pos && (window <= 0 || at > pos - window) && key < d.kvalid)) s[r] = -INFINITY;
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < RM; ++r) top[r] = s[r];
+#pragma unroll
+        for (int x = 8; x; x >>= 1)
+#pragma unroll
+            for (int r = 0; r < RM; ++r) top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], x));
+#pragma unroll
+        for (int r = 0; r < RM; ++r) {
+            const float old = __shfl_sync(0xffffffffu, m, r), mn = fmaxf(old, top[r] * sc);
+            const float ref = mn == -INFINITY ? 0.f : mn;
+            if (lane == r) {
+                corr = ex2(m - ref);
+                m = mn;
+            }
+            s[r] = ex2(fmaf(s[r], sc, -ref));
+        }
+#pragma unroll
+        for (int r = 0; r < RM; ++r)
+            if (lane < 16) ps[r * 16 + lane] = s[r];
         __syncwarp();
         const bool moved = __any_sync(0xffffffffu, corr != 1.f);
         l *= corr;
@@ -323,7 +329,7 @@ struct Work {
         }
         __syncwarp();
 #pragma unroll
-        for (int r = 0; r < 16; ++r)
+        for (int r = 0; r < RW; ++r)
 #pragma unroll
             for (int e = 0; e < 4; ++e) w.o[r][e] = 0.f;
     }
@@ -337,28 +343,29 @@ struct Work {
         else if (R <= 4)
             w.tile<4>(q, ps, kt, vt, lane, R, a.scale_log2, d, row0, a.G, a.window, mask);
         else
-            w.tile<16>(q, ps, kt, vt, lane, R, a.scale_log2, d, row0, a.G, a.window, mask);
+            w.tile<RW>(q, ps, kt, vt, lane, R, a.scale_log2, d, row0, a.G, a.window, mask);
     }
     __device__ __forceinline__ void end(int lane, float *red, float2 *ml) {
-        if (lane < 16) ml[lane] = make_float2(w.m, w.l);
+        if (lane < RW) ml[lane] = make_float2(w.m, w.l);
         __syncwarp();
 #pragma unroll
-        for (int r = 0; r < 16; ++r)
+        for (int r = 0; r < RW; ++r)
             *reinterpret_cast<float4 *>(red + r * D + ((lane ^ (r & 7)) << 2)) = make_float4(w.o[r][0], w.o[r][1], w.o[r][2], w.o[r][3]);
     }
 };
 
+template <class C>
 __device__ __forceinline__ void consume(const PagedAttn &a, uint8_t *sm) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    uint64_t *full = reinterpret_cast<uint64_t *>(sm + OFF_BAR), *empty = full + STAGES;
-    volatile int *abort = reinterpret_cast<volatile int *>(sm + OFF_ABORT);
-    float *red = reinterpret_cast<float *>(sm + OFF_RED), *mine = red + warp * 16 * D;
-    float *ps = reinterpret_cast<float *>(sm + OFF_P) + warp * 256;
-    float2 *ml = reinterpret_cast<float2 *>(sm + OFF_ML);
+    uint64_t *full = reinterpret_cast<uint64_t *>(sm + C::OFF_BAR), *empty = full + STAGES;
+    volatile int *abort = reinterpret_cast<volatile int *>(sm + C::OFF_ABORT);
+    float *red = reinterpret_cast<float *>(sm + C::OFF_RED), *mine = red + warp * RW * D;
+    float *ps = reinterpret_cast<float *>(sm + C::OFF_P) + warp * RW * 16;
+    float2 *ml = reinterpret_cast<float2 *>(sm + C::OFF_ML);
 
     Work work;
     int stage = 0, phase = 0;
-    uint64_t *meet = reinterpret_cast<uint64_t *>(sm + OFF_MEET);
+    uint64_t *meet = reinterpret_cast<uint64_t *>(sm + C::OFF_MEET);
     int meet_phase = 0;
     // (a bounded wait, unlike a named barrier: a warp that gave up never comes)
     auto meet_all = [&]() -> bool {
@@ -378,11 +385,11 @@ __device__ __forceinline__ void consume(const PagedAttn &a, uint8_t *sm) {
             }
             break;
         }
-        const Desc *ds = reinterpret_cast<const Desc *>(sm + OFF_DESC + stage * 64);
+        const Desc *ds = reinterpret_cast<const Desc *>(sm + C::OFF_DESC + stage * 64);
         const int4 head = *reinterpret_cast<const int4 *>(ds);  // flags, ord, wr, key0
         if (head.x & END) break;
-        // wr = 1, 2 or 4 warps side by side on the rows, wk = 4 / wr on the tiles in turn
-        const int wl = head.z >> 1, wrow = warp & (head.z - 1), wk = CONS >> wl, wpart = warp >> wl;
+        // wr = 1, 2, 4 or 8 warps side by side on the rows, wk = CONS / wr on the tiles in turn
+        const int wl = __ffs(head.z) - 1, wrow = warp & (head.z - 1), wk = C::CONS >> wl, wpart = warp >> wl;
         if (!(head.x & (FIRST | LAST)) && (head.y & (wk - 1)) != wpart) {  // another warp's tile
             if (lane == 0) mbar_arrive(&empty[stage]);
             if (++stage == STAGES) {
@@ -406,18 +413,18 @@ __device__ __forceinline__ void consume(const PagedAttn &a, uint8_t *sm) {
         }
         if (d.flags & LAST) {
             // merge the warps that share rows, in warp order
-            work.end(lane, mine, ml + warp * 16);
+            work.end(lane, mine, ml + warp * RW);
             if (!meet_all()) break;
             float *slot = paged_slot(a, d.slot);
             const float vs = 1.f;
-            for (int r = warp; r < d.R; r += CONS) {
+            for (int r = warp; r < d.R; r += C::CONS) {
                 const int rb = r / d.rpw, rl = r - rb * d.rpw;
                 float M = -INFINITY, L = 0.f;
-                for (int w = 0; w < wk; ++w) M = fmaxf(M, ml[(rb + w * d.wr) * 16 + rl].x);
+                for (int w = 0; w < wk; ++w) M = fmaxf(M, ml[(rb + w * d.wr) * RW + rl].x);
                 const float refm = M == -INFINITY ? 0.f : M;
                 float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
                 for (int w = 0; w < wk; ++w) {
-                    const int src = (rb + w * d.wr) * 16 + rl;
+                    const int src = (rb + w * d.wr) * RW + rl;
                     const float2 x = ml[src];
                     const float f = ex2(x.x - refm);
                     const float4 y = *reinterpret_cast<const float4 *>(red + src * D + ((lane ^ (rl & 7)) << 2));
@@ -444,48 +451,54 @@ __device__ __forceinline__ void consume(const PagedAttn &a, uint8_t *sm) {
     }
 }
 
-__global__ void __launch_bounds__(THREADS, 2)
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, 2)
     paged_rows_kernel(const __grid_constant__ PagedMaps maps, const PagedAttn a, int min_per) {
     extern __shared__ __align__(1024) uint8_t sm[];
     // the join may be scheduled as soon as blocks end; it waits for this grid's writes by itself
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x;
-    uint64_t *full = reinterpret_cast<uint64_t *>(sm + OFF_BAR), *empty = full + STAGES;
+    uint64_t *full = reinterpret_cast<uint64_t *>(sm + C::OFF_BAR), *empty = full + STAGES;
     if (tid == 0) {
         for (int i = 0; i < STAGES; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], CONS);
+            mbar_init(&empty[i], C::CONS);
         }
-        mbar_init(reinterpret_cast<uint64_t *>(sm + OFF_MEET), CONS);
+        mbar_init(reinterpret_cast<uint64_t *>(sm + C::OFF_MEET), C::CONS);
         mbar_fence_init();
-        *reinterpret_cast<int *>(sm + OFF_ABORT) = 0;
+        *reinterpret_cast<int *>(sm + C::OFF_ABORT) = 0;
         a.lead[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);  // (no piece of this block leads, so far)
     }
-    int64_t *scratch = reinterpret_cast<int64_t *>(sm + OFF_RED);
-    auto tiles = [&](int i, int *err) { return line_tiles(a, i, err); };
-    const PagedLine line = paged_line<THREADS>(a, scratch, min_per, tiles, [](int64_t) { return 1; });
+    int64_t *scratch = reinterpret_cast<int64_t *>(sm + C::OFF_RED);
+    auto tiles = [&](int i, int *err) { return line_tiles<C>(a, i, err); };
+    const PagedLine line = paged_line<C::THREADS>(a, scratch, min_per, tiles, [](int64_t) { return 1; });
     if (line.P0 >= line.P1) return;
     __syncthreads();  // (the sums stood where the consumers' rows will)
-    if (tid >= CONS * 32)
-        produce(a, maps, sm, line.P0, line.P1, line.per, line.req, line.before);
+    if (tid >= C::CONS * 32)
+        produce<C>(a, maps, sm, line.P0, line.P1, line.per, line.req, line.before);
     else
-        consume(a, sm);
+        consume<C>(a, sm);
 }
 
 }  // namespace
 
 int paged_rows_blocks() { return 2 * device_sm_count(); }
 
+template <class C> static int launch(const PagedAttn &a, const PagedMaps &maps, cudaStream_t s) {
+    const int rc = prepare_kernel((const void *)paged_rows_kernel<C>, C::SMEM, C::THREADS, nullptr);
+    if (rc) return rc;
+    // at least 8 tiles a block: below that the pieces cost more than they save
+    paged_rows_kernel<C><<<paged_rows_blocks(), C::THREADS, C::SMEM, s>>>(maps, a, 8);
+    note_launch("paged_rows", s);
+    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
 int launch_paged_rows(PagedAttn a, const void *k, const void *v, int64_t page_stride, cudaStream_t s) {
     a.box = TK;  // (page sizes are multiples of 16)
     PagedMaps maps;
-    int rc = make_paged_row_maps(k, v, a.Hkv, a.page_size, a.n_pages, page_stride, TK, &maps);
+    const int rc = make_paged_row_maps(k, v, a.Hkv, a.page_size, a.n_pages, page_stride, TK, &maps);
     if (rc) return rc;
-    if ((rc = prepare_kernel((const void *)paged_rows_kernel, SMEM, THREADS, nullptr))) return rc;
-    // at least 8 tiles a block (two for each warp): below that the pieces cost more than they save
-    paged_rows_kernel<<<paged_rows_blocks(), THREADS, SMEM, s>>>(maps, a, 8);
-    note_launch("paged_rows", s);
-    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    return (int64_t)a.max_q * a.G <= RW ? launch<Cfg<4>>(a, maps, s) : launch<Cfg<8>>(a, maps, s);
 }
 
 }  // namespace kda
