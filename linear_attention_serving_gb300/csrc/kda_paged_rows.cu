@@ -14,10 +14,10 @@
 // of all keys for the output, so a warp reads each key and value once from shared
 // memory whatever its rows are.
 //
-// Measured: one token of 16 requests, 16 heads of up to 3,000 keys, 4.8 TB/s (45 us), where
+// Measured: one token of 16 requests, 16 heads of up to 3,000 keys, 5.1 TB/s (42 us), where
 // the copies in flight and the start and the join bound it.  Many rows are bound by loads
 // from shared memory and the shuffles between the products (8 requests of 40 rows over 2,040
-// keys of 8 heads: 16 TFLOP/s, 166 us, and of 320 rows 27 TFLOP/s, 798 us; four warps of 16
+// keys of 8 heads: 16 TFLOP/s, 162 us, and of 320 rows 27 TFLOP/s, 800 us; four warps of 16
 // rows 246 and 1,358 us).
 #include "kda_paged.cuh"
 
@@ -29,7 +29,7 @@ constexpr int RW = 8;                        // rows a warp holds at most
 constexpr int STAGES = 4;
 constexpr int HALF = 8192;                   // bytes of K (and of V) of one tile
 constexpr int STAGE = 2 * HALF;
-// CONS: consumer warps, eight, or four in calls of up to 8 rows (45 us instead of 48 for
+// CONS: consumer warps, eight, or four in calls of up to 8 rows (45 us instead of 48 then for
 // one token of 16 requests: fewer pieces to merge, fewer warps to give a tile back)
 template <int CONS_> struct Cfg {
     static constexpr int CONS = CONS_, THREADS = (CONS + 1) * 32;
@@ -45,6 +45,10 @@ template <int CONS_> struct Cfg {
 };
 
 constexpr int TK = 16;                       // keys of a tile
+// What an item costs besides its tiles (queries in, pieces merged, output), in tiles: short
+// items are spread over the blocks by it (4 requests of up to 40 tokens over up to 66 keys,
+// 64 heads: 28 us, without it 98; 3, 4 and 6 are within 3% on long ones).
+constexpr int HEAD = 6;
 constexpr int NSUB = D * 4 / 128;            // 128-byte pieces of a row, each a block of its own
 
 // what the producer says about a tile
@@ -66,7 +70,7 @@ template <class C> __device__ __forceinline__ int64_t line_tiles(const PagedAttn
     const PagedReq r = paged_req(a, i, err);
     if (r.rows == 0) return 0;
     const int grp = row_group<C>(r.rows);
-    return (int64_t)a.Hkv * ((r.rows + grp - 1) / grp) * req_tiles(r);
+    return (int64_t)a.Hkv * ((r.rows + grp - 1) / grp) * (HEAD + req_tiles(r));
 }
 
 // ---------------------------------------------------------------- producer
@@ -119,11 +123,12 @@ __device__ __forceinline__ void produce(const PagedAttn &a, const PagedMaps &map
             continue;
         }
         const int nt = req_tiles(r), grp = row_group<C>(r.rows), ngrp = (r.rows + grp - 1) / grp;
-        const int64_t in = pos - before, item = in / nt;
+        const int64_t in = pos - before, item = in / (HEAD + nt);
         const int h = (int)(item / ngrp), g = (int)(item - (int64_t)h * ngrp);
-        const int64_t A = before + item * nt, B = A + nt;
+        const int64_t A = before + item * (HEAD + nt), B = A + HEAD + nt;
         const int64_t seg_end = B < P1 ? B : P1;
-        const int t_begin = (int)(pos - A), t_end = (int)(seg_end - A);
+        const int t_begin = max(0, (int)(pos - A) - HEAD), t_end = (int)(seg_end - A) - HEAD;
+        if (t_end <= 0) break;  // a cut before the first tile leaves the item to the next block
         const int r0 = g * grp, R = min(grp, r.rows - r0);
         const int posf = r.pos0 + r0 / a.G, posl = r.pos0 + (r0 + R - 1) / a.G;
         const int lo = a.window > 0 ? max(0, posf - a.window + 1) : 0, hi = posl + 1;  // keys that the group sees
@@ -142,10 +147,10 @@ __device__ __forceinline__ void produce(const PagedAttn &a, const PagedMaps &map
         d.r0 = r0;
         d.R = R;
         d.pos0 = r.pos0;
-        d.c0 = (int)(A / per);
+        d.c0 = (int)((A + HEAD) / per);
         d.c1 = (int)((B - 1) / per);
         d.slot = 2 * (int)blockIdx.x + (pos == P0 ? 0 : 1);
-        const int whole = pos == A && seg_end == B ? WHOLE : 0;
+        const int whole = t_begin == 0 && seg_end == B ? WHOLE : 0;
         if (te <= tb) {  // nothing to read: one empty tile so that the segment is finished all the same
             if (!next_stage()) return;
             if (lane == 0) {
@@ -322,10 +327,17 @@ struct Work {
         w.m = -INFINITY;
         w.l = 0.f;
         const int R = min(d.rpw, d.R - d.rpw * wrow);
-        for (int r = 0; r < R; ++r) {  // the queries stand where the output goes at the end
-            const int rr = d.r0 + d.rpw * wrow + r, j = rr / a.G;
-            const float4 *src = (const float4 *)a.q + ((int64_t)(d.tok0 + j) * a.Hq + d.h * a.G + (rr - j * a.G)) * (D / 4);
-            reinterpret_cast<float4 *>(q + r * D)[lane] = src[lane];
+        // the queries stand where the output goes at the end (four loads in flight at once)
+#pragma unroll 1
+        for (int r0 = 0; r0 < R; r0 += 4) {
+            float4 x[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int rr = d.r0 + d.rpw * wrow + min(r0 + u, R - 1), j = rr / a.G;
+                x[u] = ((const float4 *)a.q + ((int64_t)(d.tok0 + j) * a.Hq + d.h * a.G + (rr - j * a.G)) * (D / 4))[lane];
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) reinterpret_cast<float4 *>(q + (r0 + u) * D)[lane] = x[u];
         }
         __syncwarp();
 #pragma unroll
@@ -487,8 +499,8 @@ int paged_rows_blocks() { return 2 * device_sm_count(); }
 template <class C> static int launch(const PagedAttn &a, const PagedMaps &maps, cudaStream_t s) {
     const int rc = prepare_kernel((const void *)paged_rows_kernel<C>, C::SMEM, C::THREADS, nullptr);
     if (rc) return rc;
-    // at least 8 tiles a block: below that the pieces cost more than they save
-    paged_rows_kernel<C><<<paged_rows_blocks(), C::THREADS, C::SMEM, s>>>(maps, a, 8);
+    // (a block of fewer tiles would only wait for its first)
+    paged_rows_kernel<C><<<paged_rows_blocks(), C::THREADS, C::SMEM, s>>>(maps, a, HEAD + 1);
     note_launch("paged_rows", s);
     return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
