@@ -121,6 +121,20 @@ at::Tensor part(const at::Tensor &x, int64_t first, int64_t numel) {
     return at::Tensor(std::move(impl));
 }
 
+PyObject *tuple_of(std::initializer_list<const at::Tensor *> ts) {
+    PyObject *r = PyTuple_New((Py_ssize_t)ts.size());
+    Py_ssize_t i = 0;
+    for (const at::Tensor *t : ts) {
+        PyObject *o = r ? THPVariable_Wrap(*t) : nullptr;
+        if (!o) {
+            Py_XDECREF(r);
+            return nullptr;
+        }
+        PyTuple_SET_ITEM(r, i++, o);
+    }
+    return r;
+}
+
 template <class F> PyObject *guarded(F f) {
     try {
         return f();
@@ -154,14 +168,7 @@ PyObject *tables(PyObject *, PyObject *const *args, Py_ssize_t n_args) {
                                 (int32_t *)pos.data_ptr(), (int32_t *)cu.data_ptr(), (int32_t *)kv.data_ptr(), (int32_t *)err,
                                 stream_of(dev));
         if (rc != KDA_OK) throw No();
-        PyObject *r = PyTuple_New(5);
-        if (!r) return nullptr;
-        PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(std::move(slots)));
-        PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(std::move(pos)));
-        PyTuple_SET_ITEM(r, 2, THPVariable_Wrap(std::move(cu)));
-        PyTuple_SET_ITEM(r, 3, THPVariable_Wrap(std::move(kv)));
-        PyTuple_SET_ITEM(r, 4, THPVariable_Wrap(std::move(head)));
-        return r;
+        return tuple_of({&slots, &pos, &cu, &kv, &head});
     });
 }
 
@@ -232,11 +239,7 @@ PyObject *attn(PyObject *, PyObject *const *args, Py_ssize_t n_args) {
                               (float)a[7].real(), as_int(a[8].integer()), out.data_ptr(), (float *)lse.data_ptr(),
                               ws.data_ptr(), ws.nbytes(), (int32_t *)err, stream_of(dev));
         if (rc != KDA_OK) throw No();
-        PyObject *r = PyTuple_New(2);
-        if (!r) return nullptr;
-        PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(std::move(out)));
-        PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(std::move(lse)));
-        return r;
+        return tuple_of({&out, &lse});
     });
 }
 
