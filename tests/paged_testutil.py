@@ -94,10 +94,10 @@ def make(new, ctx, hkv, g, ps, cache=torch.bfloat16, seed=0, device="cpu", spare
 
 
 def attn_close(o, lse, ref, q_dtype, cache_dtype):
-    """Holds every value to the roundings on its way: the scores' fp32 sums (and,
-    fp32, what two tf32 parts drop) move log p by `ds`; each probability is rounded
-    to bf16 (2^-8), fp16 (2^-11) or two tf32 parts (2^-21) before its product; the
-    output is rounded once."""
+    """Holds every value to the roundings on its way: the scores' fp32 sums move log p
+    by `ds`; each probability is rounded to bf16 (2^-8) or fp16 (2^-11) before its
+    product, or, fp32, the sums over the keys are held to 2^-21; the output is rounded
+    once."""
     o_ref, lse_ref, a, mag = ref
     assert torch.equal(torch.isinf(lse.double().cpu()), torch.isinf(lse_ref)), "rows that see no key"
     p_step = {torch.bfloat16: 2.0 ** -8, torch.float8_e4m3fn: 2.0 ** -11, torch.float32: 2.0 ** -21}[cache_dtype]
