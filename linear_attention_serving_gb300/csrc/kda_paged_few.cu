@@ -27,9 +27,9 @@
 // warps beside the copies (K too would be too much: the conversions run at 16 a cycle
 // and SM, some 500 cycles a tile).
 //
-// Measured: one token of 256 requests over up to 16,384 keys of 4 kv heads 343 to 347 us
+// Measured: one token of 256 requests over up to 16,384 keys of 4 kv heads 343 to 349 us
 // (6.7 TB/s, a copy's rate), e4m3 409 to 415 us (6.6 TB/s), one request over 8,192 keys
-// 13.8 us with the join, which is starts, first copies and the pieces' way through memory.
+// 13.9 us with the join, which is starts, first copies and the pieces' way through memory.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -43,7 +43,10 @@ constexpr int BK = KEY_TILE;
 constexpr int TILE = BK * D * 2;       // an operand tile: two 64-channel blocks of 128 rows x 128 B
 constexpr int RAW = BK * D;            // an e4m3 tile as loaded
 constexpr int SEGS = 4;                // segments ahead of the roles
-constexpr int HEAD = 1;                // an item's cost besides its tiles, in tiles
+// An item's cost besides its tiles, in tiles (1: 17 e4m3 requests of up to 7,629 keys 40 us
+// for 34, 116 windows over short contexts 82 us for 78, no better where contexts are long;
+// 3: the bf16 batch of 256 352 us for 349).
+constexpr int HEAD = 2;
 constexpr float GROW = 8.f, NOTHING = -1e30f;
 // Warps: two softmax groups of four, then one each for the products of S, loads, the
 // walk and the products of O, and those that widen V.
