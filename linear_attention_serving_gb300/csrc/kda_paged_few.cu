@@ -373,7 +373,14 @@ __device__ __forceinline__ void load_role(const PagedAttn &a, const PagedMaps &m
     Tile prev{0, 0, 0, 0, 0};
     bool have = false;
     while (next_seg<C>(sm, bar, iseg, gate, s)) {
-        if (s.nt == 0) continue;
+        if (s.nt == 0) {
+            // The last item's V does not wait for the next K here: the walk goes SEGS segments ahead of
+            // the softmax, so behind SEGS - 1 items without keys that K is told of only after this V
+            // has been used.
+            if (have && !load(prev, true)) return drain();
+            have = false;
+            continue;
+        }
         int cbase = 0, page = 0, off = 0;
         const int lob = s.lo & ~(box - 1);  // boxes before this one hold no seen key (their pages may be gone)
         for (int j = 0; j < s.nt; ++j) {

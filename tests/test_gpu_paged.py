@@ -290,6 +290,16 @@ def test_attn_rows_that_see_nothing(cache):
 
 
 @pytest.mark.parametrize("cache", CACHES, ids=NAMES)
+@pytest.mark.parametrize("new", [1, 5, 20])
+def test_attn_items_without_keys_between_others(new, cache):
+    """Lines so long that a block has an item with keys, several without any, and items with keys again."""
+    n, kind = 1190, [0, 1, 1, 1, 2, 1, 1]
+    ctx = [900 + i % 50 if kind[i % 7] == 0 else 0 for i in range(n)]
+    kv = [c + new if kind[i % 7] == 0 else 0 if kind[i % 7] == 1 else min(new, 3) for i, c in enumerate(ctx)]
+    check([new] * n, ctx, 1, 2, 64, cache, kv=kv, seed=19)
+
+
+@pytest.mark.parametrize("cache", CACHES, ids=NAMES)
 def test_attn_split_over_blocks(cache):
     """Long contexts beside short ones: items cut by many block borders, and whole ones between."""
     check([1, 1, 2, 1], [9000, 10, 4100, 0], 2, 4, 64, cache, seed=3)
