@@ -47,6 +47,18 @@ struct PagedReq {
     int tok0, rows, pos0, k0, kend;  // first token, rows, first query's position, keys [k0, kend)
 };
 
+// The first key that a query at position pos sees (pos < 0: it sees none, and pos - window may be
+// below -2^31).
+__device__ __forceinline__ int first_seen(const PagedAttn &a, int pos) {
+    return a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
+}
+// window - 1 - pos0, which may be past 2^31 for a position before 0; a request has under 2^30 rows, so
+// none is further from its first than 2^30.
+__device__ __forceinline__ int window_from(const PagedAttn &a, int pos0) {
+    const int64_t d = (int64_t)a.window - 1 - pos0;
+    return d < (1 << 30) ? (int)d : 1 << 30;
+}
+
 // `err` collects what is wrong (only one block records it).
 __device__ __forceinline__ PagedReq paged_req(const PagedAttn &a, int i, int *err) {
     PagedReq r{0, 0, 0, 0, 0};
@@ -66,7 +78,7 @@ __device__ __forceinline__ PagedReq paged_req(const PagedAttn &a, int i, int *er
     r.rows = (int)rows;
     r.pos0 = kv - (e - b);
     r.kend = kv;
-    if (a.window > 0 && r.pos0 >= a.window) r.k0 = (r.pos0 - a.window + 1) & ~(a.box - 1);
+    r.k0 = first_seen(a, r.pos0) & ~(a.box - 1);
     return r;
 }
 

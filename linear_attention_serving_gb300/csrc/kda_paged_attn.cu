@@ -209,7 +209,9 @@ int kda_paged_attn(const void *q, const void *k_cache, const void *v_cache, cons
     a.page_size = page_size;
     a.n_pages = n_pages;
     a.max_blocks = max_blocks;
-    a.window = window;
+    // (no position is further back than the table reaches: such a window is none, and what is left
+    // stays clear of 2^31 where positions are added to it)
+    a.window = window >= (int64_t)max_blocks * page_size ? 0 : window;
     a.scale_log2 = sm_scale * 1.4426950408889634f;
     char *ws = (char *)workspace;
     const int64_t max_rows = (int64_t)a.max_q * a.G;

@@ -125,7 +125,7 @@ __device__ __forceinline__ int64_t units_before(const PagedAttn &a, const Req &q
     if (full > neg) {
         u += floor_sum(full - neg, BK, w.th, pos0 + (neg + 1) * w.th + BK - 1);
         if (a.window > 0) {
-            const int d = a.window - 1 - pos0;  // lo > 0 from g th > d on
+            const int d = window_from(a, pos0);  // lo > 0 from g th > d on
             int gw = d < 0 ? 0 : d / w.th + 1;
             if (gw < neg) gw = neg;
             if (gw < full) u -= floor_sum(full - gw, BK, w.th, gw * w.th - d);

@@ -131,7 +131,7 @@ __device__ __forceinline__ void produce(const PagedAttn &a, const PagedMaps &map
         if (t_end <= 0) break;  // a cut before the first tile leaves the item to the next block
         const int r0 = g * grp, R = min(grp, r.rows - r0);
         const int posf = r.pos0 + r0 / a.G, posl = r.pos0 + (r0 + R - 1) / a.G;
-        const int lo = a.window > 0 ? max(0, posf - a.window + 1) : 0, hi = posl + 1;  // keys that the group sees
+        const int lo = first_seen(a, posf), hi = posl + 1;  // keys that the group sees
         int tb = t_begin, te = t_end;
         if (hi <= lo) {
             te = tb;

@@ -40,7 +40,7 @@ __device__ __forceinline__ int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a,
 // Key tiles [t0, t1) of the tokens j0 .. j1 of a request (none: t1 = t0).
 __device__ __forceinline__ void key_tiles(const PagedAttn &a, const PagedReq &r, int j0, int j1, int &lo, int &hi, int &t0, int &t1) {
     hi = r.pos0 + j1 + 1;
-    lo = a.window > 0 ? max(0, r.pos0 + j0 - a.window + 1) : 0;
+    lo = first_seen(a, r.pos0 + j0);
     if (hi <= 0) {
         t0 = t1 = 0;
         return;

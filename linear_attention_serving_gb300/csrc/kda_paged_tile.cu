@@ -113,7 +113,7 @@ __device__ __forceinline__ int64_t units_before(const PagedAttn &a, const TileRe
     if (neg > full) neg = full;
     int64_t tiles = neg + floor_sum(full - neg, BK, TT, pos0 + (neg + 1) * TT + BK - 1);
     if (a.window > 0) {
-        const int d = a.window - 1 - pos0;  // lo > 0 from g TT > d on
+        const int d = window_from(a, pos0);  // lo > 0 from g TT > d on
         int gw = d < 0 ? 0 : d / TT + 1;
         if (gw < neg) gw = neg;
         if (gw < full) tiles -= floor_sum(full - gw, BK, TT, gw * TT - d);
@@ -614,7 +614,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
         }
         const bool alt = seg->alt;
         const int pos = seg->pos + (alt ? 0 : x) * th + row / a.G;
-        const int first_key = a.window > 0 ? pos - a.window + 1 : 0;  // keys first_key .. pos, all below hi
+        const int first_key = first_seen(a, pos);  // keys first_key .. pos, all below hi
         float ref = 0.f, l = 0.f, top = -INFINITY;  // (top: of all the row's keys at the last change of ref, then of this half's)
         // ref follows the maximum once that has passed this (never for the half's rows past the
         // item's tokens: they hold the next request's queries, or what was there before)

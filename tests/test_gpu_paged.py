@@ -270,6 +270,36 @@ def test_attn_window(window, cache):
 
 
 @pytest.mark.parametrize("cache", CACHES, ids=NAMES)
+@pytest.mark.parametrize("new,ctx,kv", [([2, 5, 1], [300, 40, 9], None), ([5, 3, 30], [0, 0, 0], [2, 0, 7]),
+                                        ([1, 140, 3], [90, 0, 64], None)])
+def test_attn_window_without_limit(new, ctx, kv, cache):
+    """A window that no position reaches, up to the largest number, is none."""
+    d = make(new, ctx, 2, 2, 16, cache, seed=23)
+    if kv is not None:
+        d["kv"] = kv
+    o, lse, e = run_attn(d)
+    room = 16 * len(d["table"][0])
+    for window in (max(d["kv"]), room - 1, room, 2 ** 31 - 65536, 2 ** 31 - 1):
+        o2, lse2, e2 = run_attn(d, window=window)
+        assert e == 0 and e2 == 0 and torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("cache", CACHES, ids=NAMES)
+def test_attn_window_as_wide_as_the_widest_table(cache):
+    """Queries so far before position 0 that their distance to the window's end passes 2^31."""
+    ps, T = 65536, 140000
+    d = make([5], [0], 1, 1, ps, cache, seed=24)
+    width = (2 ** 31 - 65537) // ps
+    d["table"] = [[d["table"][0][0]] + [-1] * (width - 1)]
+    d["q"] = torch.cat([torch.zeros(T - 5, 1, D, dtype=d["q"].dtype), d["q"]])
+    d["cu"] = [0, T]
+    o, lse, e = run_attn(d)
+    o2, lse2, e2 = run_attn(d, window=width * ps - 1)
+    assert e == 0 and e2 == 0 and torch.equal(o, o2) and torch.equal(lse, lse2)
+    assert (o[:-5] == 0).all() and torch.isinf(lse[:-5]).all() and torch.isfinite(lse[-5:]).all()
+
+
+@pytest.mark.parametrize("cache", CACHES, ids=NAMES)
 def test_attn_window_pages_given_back(cache):
     """Pages that hold no seen key may have left the table."""
     d = make([1, 3], [500, 201], 2, 2, 16, cache)
