@@ -98,7 +98,9 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) paged_join_kernel(PagedAttn a
             M = m;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                if (ml[i].x == -INFINITY) continue;  // (what an empty piece holds has no say)
+                // what an empty piece holds has no say; one whose scores are all NaN has no maximum
+                // either, but a NaN for its sum
+                if (ml[i].y == 0.f) continue;
                 const float f = tc::ex2(ml[i].x - ref);
                 L += f * ml[i].y;
                 acc.x += f * v[i].x;

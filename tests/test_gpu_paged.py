@@ -365,6 +365,19 @@ def test_attn_nan_stays_in_its_request(cache):
 
 
 @pytest.mark.parametrize("cache", CACHES, ids=NAMES)
+@pytest.mark.parametrize("new", [1, 20])
+def test_attn_nan_query_of_a_cut_item(new, cache):
+    """A row whose scores are all NaN is NaN, whole or cut by block borders."""
+    d = make([new, 1], [20000, 30], 1, 2, 64, cache, seed=20)
+    d["q"][0, 1, 7] = d["q"][new, 0, 3] = float("nan")
+    o, lse, e = run_attn(d, max_q=new)
+    bad = torch.zeros(new + 1, 2, dtype=torch.bool)
+    bad[0, 1] = bad[new, 0] = True
+    assert e == 0 and torch.equal(torch.isnan(lse).cpu(), bad)
+    assert torch.equal(torch.isnan(o).cpu(), bad[..., None].expand(-1, -1, D))
+
+
+@pytest.mark.parametrize("cache", CACHES, ids=NAMES)
 def test_attn_pages_apart_and_same_bits(cache):
     """K and V as halves of one pool give the same bits as separate caches, run after run."""
     d = make([1, 40, 3], [3000, 60, 500], 2, 4, 32, cache, filler=0.0)
