@@ -434,8 +434,10 @@ int kda_decode_step_fused(float *state,
  *   cu_q         (device) int32 [n_seqs + 1], written;  kv_len (device) int32
  *                [n_seqs], written: ctx + new
  * Lengths that are negative, exceed max_blocks * page_size or do not add up to
- * T_total record KDA_DEVERR_LENGTHS, too few free pages KDA_DEVERR_NO_PAGES;
- * either leaves every output unwritten but free_head_next = *free_head.  A page
+ * T_total record KDA_DEVERR_LENGTHS, too few free pages KDA_DEVERR_NO_PAGES.
+ * Either makes the step an empty one: slot_map -1, positions 0, cu_q 0, kv_len =
+ * ctx_len, free_head_next = *free_head, block_table as it was, so that
+ * kda_paged_append writes nothing after it and kda_paged_attn has no rows.  A page
  * outside 0 .. n_pages - 1 records KDA_DEVERR_PAGE; its tokens get slot -1 and
  * a new entry becomes -1.
  * ------------------------------------------------------------------------ */

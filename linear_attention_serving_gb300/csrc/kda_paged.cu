@@ -105,9 +105,18 @@ __global__ void __launch_bounds__(TAB_THREADS) tables_kernel(const TablesArgs a)
         *a.free_head_next = why ? head : (int)(head + page0);
         if (why && a.err) atomicOr(a.err, why);
     }
-    if (why) return;
-
     const int gid = blockIdx.x * TAB_THREADS + tid, gsize = gridDim.x * TAB_THREADS;
+    if (why) {  // a step without tokens: what follows on the stream writes and reads no page by what stood here
+        for (int i = gid; i <= n; i += gsize) {
+            a.cu_q[i] = 0;
+            if (i < n) a.kv_len[i] = a.ctx_len[i];
+        }
+        for (int64_t t = gid; t < a.T; t += gsize) {
+            a.slot_map[t] = -1;
+            if (a.positions) a.positions[t] = 0;
+        }
+        return;
+    }
     for (int i = gid; i <= n; i += gsize) {
         a.cu_q[i] = cu[i];
         if (i < n) a.kv_len[i] = ctx[i] + cu[i + 1] - cu[i];

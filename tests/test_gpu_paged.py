@@ -91,6 +91,32 @@ def test_tables_refuses_on_the_device(new, ctx, T, free_n, expect):
     assert torch.equal(before, t) and head.tolist() == [0]
 
 
+@pytest.mark.parametrize("new,ctx,T,free_n,expect", [
+    ([3, -1], [0, 0], 2, 9, paged.DEVERR_LENGTHS), ([3], [-2], 3, 9, paged.DEVERR_LENGTHS),
+    ([3, 3], [1, 7], 7, 9, paged.DEVERR_LENGTHS), ([100], [100], 100, 99, paged.DEVERR_LENGTHS),
+    ([40, 1], [0, 5], 41, 2, paged.DEVERR_NO_PAGES), ([40, 1], [0, 0], 700001, 9, paged.DEVERR_LENGTHS),
+    ([1] * 600, [16] * 600, 600, 599, paged.DEVERR_NO_PAGES)])
+def test_tables_failed_call_leaves_an_empty_step(new, ctx, T, free_n, expect):
+    """Whatever stood in the outputs: append writes nothing after it, attention has no rows, the lengths stay."""
+    n, ps, pages = len(new), 16, 64
+    nw, cx, table, free, head = i32(new), i32(ctx), i32([[50] * 8] * n), i32([i % pages for i in range(free_n)]), i32([0])
+    slots = torch.arange(T, device=DEV) % (pages * ps)
+    pos, cu, kv, nxt, e = i32([7] * T), i32(list(range(n + 1))), i32([9] * n), i32([5]), errw()
+    p = lambda x: x.data_ptr()  # noqa: E731
+    rc = paged._lib().kda_paged_tables(p(nw), p(cx), n, T, p(table), 8, p(free), free_n, p(head), p(nxt), ps, pages, p(slots),
+                                       p(pos), p(cu), p(kv), p(e), torch.cuda.current_stream().cuda_stream)
+    assert rc == 0 and int(e) == expect and int(nxt) == 0 and (table == 50).all()
+    assert (slots == -1).all() and (pos == 0).all() and (cu == 0).all() and kv.tolist() == ctx
+    T = min(T, 600)
+    kc = torch.randn(pages, 1, ps, D, device=DEV).bfloat16()
+    vc, x = kc.clone(), torch.zeros(T, 1, D, device=DEV, dtype=BF16)
+    before = kc.clone()
+    kda.paged_append(x, x, slots[:T].contiguous(), kc, vc)
+    out = torch.full_like(x, 7.0)
+    kda.paged_attn(x, kc, vc, table, cu, kv, out=out)
+    assert torch.equal(kc, before) and torch.equal(vc, before) and (out == 7).all()
+
+
 def test_tables_bad_pages():
     """A page outside the cache: its tokens get slot -1 and nothing else changes."""
     t = i32([[2, -1, -1], [99, -1, -1]])
