@@ -22,10 +22,11 @@
 // maximum over their keys at all, which would go across lanes, and no rescaling; one
 // barrier tells a group's warps whether any of them saw such growth.
 //
-// e4m3 caches: S^T multiplies K as it was loaded (8-bit products) by two e4m3 parts of
-// q, which hold a bf16 value's eight bits; V is widened to fp16, which is exact, by
-// warps beside the copies (K too would be too much: the conversions run at 16 a cycle
-// and SM, some 500 cycles a tile).
+// e4m3 caches: S^T multiplies K as it was loaded (8-bit products) by three e5m2 parts of
+// q, three bits each, which hold a bf16 value's eight bits (two e4m3 parts do so only for
+// values over 2^-9 of the row's largest; the third costs 1.6% on single tokens).  V is
+// widened to fp16, which is exact, by warps beside the copies (K too would be too much:
+// the conversions run at 16 a cycle and SM, some 500 cycles a tile).
 //
 // Measured: one token of 256 requests over up to 16,384 keys of 4 kv heads 343 to 349 us
 // (6.7 TB/s, a copy's rate), e4m3 409 to 415 us (6.6 TB/s), one request over 8,192 keys
@@ -55,8 +56,8 @@ template <bool E4, int NR> struct Cfg {
     static constexpr int SOFT = 8, W_S = 8, W_LOAD = 9, W_WALK = 10, W_O = 11, W_WIDEN = 12;
     static constexpr int WIDEN = !E4 ? 0 : NR == 16 ? 8 : 4;  // (512 threads leave 128 registers for NR = 32)
     static constexpr int KT = E4 ? RAW : TILE;                // bytes of a K tile
-    static constexpr int KS = E4 ? (NR == 32 ? 4 : 5) : 3, VS = E4 ? 2 : 3, RS = E4 ? 4 : 0;
-    static constexpr int PB = BK * NR * 2, QB = NR * D * 2;
+    static constexpr int KS = E4 ? (NR == 32 ? 3 : 4) : 3, VS = E4 ? 2 : 3, RS = E4 ? 4 : 0;
+    static constexpr int PB = BK * NR * 2, QB = NR * 128 * (E4 ? 3 : 2);  // (three 8-bit parts, two 64-channel blocks)
     static constexpr int OFF_K = 0, OFF_V = OFF_K + KS * KT, OFF_R = OFF_V + VS * TILE, OFF_Q = OFF_R + RS * RAW,
                          OFF_P = OFF_Q + 2 * QB, OFF_REF = OFF_P + 2 * PB, OFF_FAC = OFF_REF + 2 * NR * 4,
                          OFF_MRG = OFF_FAC + 2 * NR * 4, OFF_SUM = OFF_MRG + 2 * NR * 4, OFF_SC = OFF_SUM + 8 * NR * 4, OFF_SEG = OFF_SC + SEGS * NR * 4,
@@ -271,41 +272,44 @@ __device__ __forceinline__ void walk_role(const PagedAttn &a, uint8_t *sm, Walk 
                     for (int k = 0; k < 4; ++k) {
                         y[2 * k] = bf_lo(u[k]);
                         y[2 * k + 1] = bf_hi(u[k]);
-                        // (e4m3 has no infinity: NaN says that there is no answer)
+                        // (the parts are cut at the largest value: NaN says that there is no answer)
                         if (fabsf(y[2 * k]) == INFINITY) y[2 * k] = NAN;
                         if (fabsf(y[2 * k + 1]) == INFINITY) y[2 * k + 1] = NAN;
                         top = fmaxf(top, fmaxf(fabsf(y[2 * k]), fabsf(y[2 * k + 1])));
                     }
 #pragma unroll
                     for (int o = 8; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    // the row's largest value goes to 128 .. 256 (not for 0, inf and the ends of the
-                    // range): parts of 2^-9 and more are then exact for values over 2^-9 of it
-                    const int e = (int)(__float_as_uint(top) >> 23) - 127;
-                    const bool ok = e > -110 && e < 110;
-                    const float down = ok ? __uint_as_float((uint32_t)(127 + 7 - e) << 23) : 1.f;
-                    if (c == 0) sc[r] = ks * (ok ? __uint_as_float((uint32_t)(127 + e - 7) << 23) : 1.f);
-                    uint32_t p1[2], p2[2];
+                    // The row's largest value goes to 2^14 .. 2^15 (rows under 2^-110: 2^124 times
+                    // theirs).  Parts go down to 2^-16, so values over 2^-23 of the largest are exact,
+                    // and what smaller ones lose is 2^-31 of it, far below the sums' own rounding.
+                    // (Two e4m3 parts end 2^-16 below the largest: with one channel 2^12 times the
+                    // others, scores were off by 0.2.)
+                    const int e = max((int)(__float_as_uint(top) >> 23) - 127, -110);
+                    const float down = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+                    if (c == 0) sc[r] = ks * __uint_as_float((uint32_t)(127 + e - 14) << 23);
+                    uint32_t w[3][2];
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        uint32_t a1 = 0, a2 = 0;
+#pragma unroll
+                        for (int p = 0; p < 3; ++p) w[p][k] = 0;
 #pragma unroll
                         for (int g = 0; g < 2; ++g) {
-                            const float2 z = make_float2(y[4 * k + 2 * g] * down, y[4 * k + 2 * g + 1] * down);
-                            const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(z, __NV_SATFINITE, __NV_E4M3);
-                            const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(hi, __NV_E4M3);
-                            const float2 back = __half22float2(*reinterpret_cast<const __half2 *>(&hr));
-                            const __nv_fp8x2_storage_t lo =
-                                __nv_cvt_float2_to_fp8x2(make_float2(z.x - back.x, z.y - back.y), __NV_SATFINITE, __NV_E4M3);
-                            a1 |= (uint32_t)hi << (16 * g);
-                            a2 |= (uint32_t)lo << (16 * g);
+                            float2 z = make_float2(y[4 * k + 2 * g] * down, y[4 * k + 2 * g + 1] * down);
+#pragma unroll
+                            for (int p = 0; p < 3; ++p) {
+                                const __nv_fp8x2_storage_t b = __nv_cvt_float2_to_fp8x2(z, __NV_SATFINITE, __NV_E5M2);
+                                const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(b, __NV_E5M2);
+                                const float2 back = __half22float2(*reinterpret_cast<const __half2 *>(&hr));
+                                w[p][k] |= (uint32_t)b << (16 * g);
+                                z.x -= back.x;
+                                z.y -= back.y;
+                            }
                         }
-                        p1[k] = a1;
-                        p2[k] = a2;
                     }
-                    // two [row][channel] e4m3 operands, 128 bytes a row: this lane's 8 channels
+                    // three [row][channel] e5m2 operands, 128 bytes a row: this lane's 8 channels
                     uint8_t *at = qb + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + 8 * (c & 1);
-                    *reinterpret_cast<uint2 *>(at) = make_uint2(p1[0], p1[1]);
-                    *reinterpret_cast<uint2 *>(at + NR * 128) = make_uint2(p2[0], p2[1]);
+#pragma unroll
+                    for (int p = 0; p < 3; ++p) *reinterpret_cast<uint2 *>(at + p * NR * 128) = make_uint2(w[p][0], w[p][1]);
                 } else {
                     if (c == 0) sc[r] = ks;
                     *reinterpret_cast<uint4 *>(qb + (c >> 3) * NR * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
@@ -501,21 +505,25 @@ __device__ __forceinline__ void issue_s(uint32_t d, uint64_t k, uint64_t q, uint
         "l"(k), "l"(q), "l"(q2), "r"(idesc)
         : "memory");
 }
-// The same with 8-bit K and the two parts of Q: four steps of 32 channels each.
-__device__ __forceinline__ void issue_s8(uint32_t d, uint64_t k, uint64_t q, uint64_t q2, uint32_t idesc) {
+// The same with 8-bit K and the three parts of Q: four steps of 32 channels each.
+__device__ __forceinline__ void issue_s8(uint32_t d, uint64_t k, uint64_t q, uint64_t q2, uint64_t q3, uint32_t idesc) {
     asm volatile(
         "{\n .reg .pred e, t, f;\n .reg .b64 a, b;\n"
         " setp.eq.u32 t, 0, 0;\n setp.ne.u32 f, 0, 0;\n elect.sync _|e, 0xffffffff;\n"
-        " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %4, f;\n"
-        " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %3, %4, t;\n"
-        " add.s64 a, %1, 2;\n add.s64 b, %2, 2;\n @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %4, t;\n"
-        " add.s64 b, %3, 2;\n @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %4, t;\n"
-        " add.s64 a, %1, 4;\n add.s64 b, %2, 4;\n @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %4, t;\n"
-        " add.s64 b, %3, 4;\n @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %4, t;\n"
-        " add.s64 a, %1, 6;\n add.s64 b, %2, 6;\n @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %4, t;\n"
-        " add.s64 b, %3, 6;\n @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %4, t;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %5, f;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %3, %5, t;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %4, %5, t;\n"
+        " add.s64 a, %1, 2;\n add.s64 b, %2, 2;\n @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, t;\n"
+        " add.s64 b, %3, 2;\n @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, t;\n"
+        " add.s64 b, %4, 2;\n @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, t;\n"
+        " add.s64 a, %1, 4;\n add.s64 b, %2, 4;\n @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, t;\n"
+        " add.s64 b, %3, 4;\n @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, t;\n"
+        " add.s64 b, %4, 4;\n @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, t;\n"
+        " add.s64 a, %1, 6;\n add.s64 b, %2, 6;\n @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, t;\n"
+        " add.s64 b, %3, 6;\n @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, t;\n"
+        " add.s64 b, %4, 6;\n @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, t;\n"
         "}\n" ::"r"(d),
-        "l"(k), "l"(q), "l"(q2), "r"(idesc)
+        "l"(k), "l"(q), "l"(q2), "l"(q3), "r"(idesc)
         : "memory");
 }
 // O^T (+)= V^T P^T: eight steps of 16 keys, V 2 KB on, P 512 bytes on.
@@ -536,11 +544,12 @@ __device__ __forceinline__ void issue_o(uint32_t d, uint64_t v, uint64_t p, uint
         : "memory");
 }
 
-// types: e4m3 0 (8-bit products), fp16 0, bf16 1 (16-bit ones); K and Q are K-major, V^T
-// and P^T run along M and N
+// types: e4m3 0 and e5m2 1 (8-bit products), fp16 0, bf16 1 (16-bit ones); K and Q are K-major,
+// V^T and P^T run along M and N
 template <bool E4, int NR>
-constexpr uint32_t ID_S = (1u << 4) | (E4 ? 0u : (1u << 7) | (1u << 10)) | ((uint32_t)(NR >> 3) << 17) | ((128u >> 4) << 24);
-template <bool E4, int NR> constexpr uint32_t ID_O = ID_S<E4, NR> | (1u << 15) | (1u << 16);
+constexpr uint32_t ID_S = (1u << 4) | (E4 ? 0u : 1u << 7) | (1u << 10) | ((uint32_t)(NR >> 3) << 17) | ((128u >> 4) << 24);
+template <bool E4, int NR>
+constexpr uint32_t ID_O = (1u << 4) | (E4 ? 0u : (1u << 7) | (1u << 10)) | (1u << 15) | (1u << 16) | ((uint32_t)(NR >> 3) << 17) | ((128u >> 4) << 24);
 
 template <class C>
 __device__ __forceinline__ void drain_products(const Bars<C> &bar, int i) {  // before TMEM is given back
@@ -569,7 +578,7 @@ __device__ __forceinline__ void s_role(uint8_t *sm, uint32_t tmem, const Gate &g
             tc_fence_after();
             const uint64_t k = dk + (uint32_t)slot * (C::KT >> 4);
             if constexpr (E4)
-                issue_s8(tmem + b * NR, k, q, q + (NR * 128 >> 4), ID_S<E4, NR>);
+                issue_s8(tmem + b * NR, k, q, q + (NR * 128 >> 4), q + (2 * NR * 128 >> 4), ID_S<E4, NR>);
             else
                 issue_s(tmem + b * NR, k, q, q + (NR * 128 >> 4), ID_S<E4, NR>);
             mma_commit_w(&bar.s_full[b]);

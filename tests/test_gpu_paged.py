@@ -380,6 +380,29 @@ def test_attn_small_queries_e4m3():
                                 d["v_scale"]), BF16, E4M3)
 
 
+@pytest.mark.parametrize("new", [2, 5])
+@pytest.mark.parametrize("outlier", [2.0 ** 6, 2.0 ** 8, 2.0 ** 10, 2.0 ** 12, 2.0 ** 14])
+def test_attn_e4m3_query_with_one_large_channel(outlier, new):
+    """The other channels keep their bits (its keys are zero there, so the others decide)."""
+    d = make([new], [300], 2, 4, 16, E4M3, seed=21)
+    d["q"][..., 5] *= outlier
+    d["k_cache"][..., 5] = 0
+    o, lse, e = run_attn(d)
+    assert e == 0
+    attn_close(o, lse, attn_ref(d["q"], d["k_cache"], d["v_cache"], d["table"], d["cu"], d["kv"], k_scale=d["k_scale"],
+                                v_scale=d["v_scale"]), BF16, E4M3)
+
+
+def test_attn_large_queries_e4m3():
+    """q near the end of bf16's range: scaled by powers of two, nothing is cut."""
+    d = make([2], [100], 1, 4, 16, E4M3)
+    d["q"] = (d["q"].float() * 2.0 ** 114).bfloat16()
+    scale = D ** -0.5 * 2.0 ** -114
+    o, lse, e = run_attn(d, scale=scale)
+    attn_close(o, lse, attn_ref(d["q"], d["k_cache"], d["v_cache"], d["table"], d["cu"], d["kv"], scale, 0, d["k_scale"],
+                                d["v_scale"]), BF16, E4M3)
+
+
 @pytest.mark.parametrize("cache", CACHES, ids=NAMES)
 def test_attn_nan_stays_in_its_request(cache):
     d = make([1, 2], [50, 70], 1, 2, 16, cache)
