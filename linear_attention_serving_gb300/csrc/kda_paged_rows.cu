@@ -403,6 +403,7 @@ __device__ __forceinline__ void consume(const PagedAttn &a, uint8_t *sm) {
         // wr = 1, 2, 4 or 8 warps side by side on the rows, wk = CONS / wr on the tiles in turn
         const int wl = __ffs(head.z) - 1, wrow = warp & (head.z - 1), wk = C::CONS >> wl, wpart = warp >> wl;
         if (!(head.x & (FIRST | LAST)) && (head.y & (wk - 1)) != wpart) {  // another warp's tile
+            __syncwarp();  // (every lane has read the descriptor, which the producer may write next)
             if (lane == 0) mbar_arrive(&empty[stage]);
             if (++stage == STAGES) {
                 stage = 0;

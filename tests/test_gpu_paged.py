@@ -438,6 +438,18 @@ def test_attn_pages_apart_and_same_bits(cache):
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("new", [1, 2, 12])
+def test_attn_f32_same_bits(new):
+    """Tiles that most warps pass over, short items and cut ones: the same bits run after run."""
+    n = 150
+    d = make([new] * n, [(37 * i) % 400 for i in range(n - 1)] + [6000], 2, 2, 16, F32, seed=25)
+    first = run_attn(d)
+    attn_close(first[0], first[1], attn_ref(d["q"], d["k_cache"], d["v_cache"], d["table"], d["cu"], d["kv"]), F32, F32)
+    for _ in range(40):
+        o, lse, e = run_attn(d)
+        assert e == 0 and torch.equal(o, first[0]) and torch.equal(lse, first[1])
+
+
 def test_attn_other_stream_and_graph():
     d = make([1, 33], [700, 100], 2, 4, 16, BF16)
     o, lse, _ = run_attn(d)
