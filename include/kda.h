@@ -473,7 +473,10 @@ int kda_paged_append(const void *k, const void *v, const int64_t *slot_map, int6
  *
  *   q            (device) [T_total, Hq, D] dtype, 16-byte aligned
  *   k_cache, v_cache, k_scale, v_scale, page_size, page_stride: as above; what
- *                the pages hold past kv_len (NaN included) has no influence
+ *                the pages hold besides the keys that a new token of the request
+ *                sees (NaN included) has no influence.  New tokens share products:
+ *                a value that is not finite may make outputs of the request's other
+ *                new tokens NaN too, where the mask hides it from them
  *   block_table  (device) int32 [n_seqs, max_blocks]; only the entries of pages
  *                that hold a seen key are read
  *   cu_q         (device) int32 [n_seqs + 1];  kv_len (device) int32 [n_seqs]

@@ -347,7 +347,7 @@ __device__ __forceinline__ void load_role(const PagedAttn &a, const PagedMaps &m
     };
     // boxes f .. e - 1 of a tile: this lane's page and row
     struct Tile {
-        int f, e, page, y, z;  // z: first and one past the last row that holds a key (e4m3)
+        int f, e, page, y, z;  // z: first and one past the last row that holds a seen key (e4m3)
     };
     auto load = [&](const Tile &t, bool v) -> bool {
         const int slot = v ? vslot : kslot;
@@ -407,7 +407,7 @@ __device__ __forceinline__ void load_role(const PagedAttn &a, const PagedMaps &m
             t.e = min(nbx, (s.hi - key0 + box - 1) >> lg);
             t.page = __shfl_sync(0xffffffffu, page, (b0 - cbase + lane) & 31);
             t.y = __shfl_sync(0xffffffffu, off, (b0 - cbase + lane) & 31);
-            t.z = max(0, lob - key0) | (min(BK, s.hi - key0) << 8);
+            t.z = max(0, s.lo - key0) | (min(BK, s.hi - key0) << 8);
             if (!load(t, false)) return drain();
             if (have && !load(prev, true)) return drain();
             prev = t;
@@ -427,7 +427,7 @@ __device__ __forceinline__ void load_role(const PagedAttn &a, const PagedMaps &m
 }
 
 // ---------------------------------------------------------------- widening
-// V from e4m3 to fp16, 32 WIDEN / 128 threads to a row.  Rows that no key stands in
+// V from e4m3 to fp16, 32 WIDEN / 128 threads to a row.  Rows that no seen key stands in
 // become zeros (0 x NaN is NaN).
 template <int NR>
 __device__ __forceinline__ void widen_role(uint8_t *sm, const Gate &gate) {
@@ -811,8 +811,8 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
                 *reinterpret_cast<uint4 *>(pb + (c >> 1) * BK * 32 + tid * 32 + (((c & 1) ^ ((tid >> 2) & 1)) << 4)) =
                     make_uint4(p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]);
             if (!E4) {
-                // a row of V that no key stands in may hold anything: zero it (0 x NaN is NaN)
-                const bool none = key >= hi || key < (lo & ~(a.box - 1));
+                // a row of V that no seen key stands in may hold anything: zero it (0 x NaN is NaN)
+                const bool none = key >= hi || key < lo;
                 if (__any_sync(0xffffffffu, none)) {
                     const int v = n + j;
                     if (!gate(&bar.v_full[v % C::VS], (v / C::VS) & 1)) failed = true;

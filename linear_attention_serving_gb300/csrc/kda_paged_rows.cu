@@ -53,7 +53,8 @@ constexpr int NSUB = D * 4 / 128;            // 128-byte pieces of a row, each a
 
 // what the producer says about a tile
 struct __align__(16) Desc {
-    int flags, ord, wr, key0, kvalid, tok0, h, r0, R, pos0, slot, c0, c1, rpw, pad0, pad1;  // rpw: rows of a warp
+    int flags, ord, wr, key0, kvalid, tok0, h, r0, R, pos0, slot, c0, c1, rpw;  // rpw: rows of a warp
+    int kfirst, pad;         // the tile's rows [kfirst, kvalid) hold keys that the item sees
 };
 static_assert(sizeof(Desc) == 64, "descriptor size");
 constexpr int FIRST = 1, LAST = 2, WHOLE = 4, END = 8, MASK = 16;
@@ -157,7 +158,7 @@ __device__ __forceinline__ void produce(const PagedAttn &a, const PagedMaps &map
                 d.flags = FIRST | LAST | MASK | whole;
                 d.ord = 0;
                 d.key0 = 0;
-                d.kvalid = 0;
+                d.kvalid = d.kfirst = 0;
                 *reinterpret_cast<Desc *>(sm + C::OFF_DESC + stage * 64) = d;
                 mbar_arrive(&full[stage]);
             }
@@ -187,6 +188,7 @@ __device__ __forceinline__ void produce(const PagedAttn &a, const PagedMaps &map
                 d.ord = t - tb;
                 d.key0 = key0;
                 d.kvalid = kvalid;
+                d.kfirst = max(0, lo - key0);
                 *reinterpret_cast<Desc *>(sm + C::OFF_DESC + stage * 64) = d;
                 mbar_expect_tx(&full[stage], 2 * HALF);
                 load_tile(sm + stage * STAGE, &maps.k, y, pg, &full[stage]);
@@ -311,10 +313,10 @@ struct RowsF32 {
 };
 
 // ---------------------------------------------------------------- consumers
-// V rows past the keys may hold anything (0 x NaN is NaN): zero them.
-__device__ __forceinline__ void zero_past(uint8_t *vt, int kvalid, int lane) {
-    for (int x = lane; x < (TK - kvalid) * NSUB * 8; x += 32) {
-        const int row = kvalid + x / (NSUB * 8), c = x % (NSUB * 8);
+// V rows outside the keys that are seen may hold anything (0 x NaN is NaN): zero them.
+__device__ __forceinline__ void zero_outside(uint8_t *vt, int kfirst, int kvalid, int lane) {
+    for (int x = lane; x < (kfirst + TK - kvalid) * NSUB * 8; x += 32) {
+        const int i = x / (NSUB * 8), row = i < kfirst ? i : kvalid + i - kfirst, c = x % (NSUB * 8);
         *reinterpret_cast<uint4 *>(vt + (c >> 3) * TK * 128 + row * 128 + ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
     }
     fence_async_smem();
@@ -415,7 +417,7 @@ __device__ __forceinline__ void consume(const PagedAttn &a, uint8_t *sm) {
         if (d.flags & FIRST) work.begin(a, d, wrow, lane, mine);
         if ((d.ord & (wk - 1)) == wpart && d.kvalid > 0) {
             uint8_t *kt = sm + stage * STAGE, *vt = kt + HALF;
-            if (d.kvalid < TK) zero_past(vt, d.kvalid, lane);
+            if (d.kfirst > 0 || d.kvalid < TK) zero_outside(vt, d.kfirst, d.kvalid, lane);
             work.tile(a, d, wrow, lane, kt, vt, mine, ps);
         }
         __syncwarp();

@@ -681,9 +681,9 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
                     }
                 }
             }
-            // rows of V that no key of this item stands in may hold anything: zero
+            // rows of V that no key seen by this item stands in may hold anything: zero
             // them (0 x NaN is NaN); each group before its own product
-            const int z0 = max(0, (s.lo & ~(a.box - 1)) - key0), z1 = min(BK, s.hi - key0);
+            const int z0 = max(0, s.lo - key0), z1 = min(BK, s.hi - key0);
             if (u == 0 && (z0 > 0 || z1 < BK)) {
                 const uint32_t q = seq0 + 2 * j + 1;
                 if (!gate(&bar.kv_full[q % SLOTS], (int)((q / SLOTS) & 1))) failed = true;

@@ -339,6 +339,21 @@ def test_attn_window_pages_given_back(cache):
 
 
 @pytest.mark.parametrize("cache", CACHES, ids=NAMES)
+@pytest.mark.parametrize("new", [1, 3, 20])
+@pytest.mark.parametrize("ps", [16, 128])
+def test_attn_window_hides_what_is_not_finite(ps, new, cache):
+    """Keys and values before the window of the first new token, in its page too, have no influence."""
+    window, ctx = 50, 310
+    d = make([new], [ctx], 2, 2, ps, cache, seed=22)
+    o, lse, e = run_attn(d, window=window)
+    for key in range(ctx - window + 1):
+        for c, x in (("k_cache", float("nan")), ("v_cache", float("nan") if cache == E4M3 or key % 2 else float("-inf"))):
+            d[c][d["table"][0][key // ps], :, key % ps] = x
+    o2, lse2, e2 = run_attn(d, window=window)
+    assert e == 0 and e2 == 0 and torch.isfinite(o).all() and torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("cache", CACHES, ids=NAMES)
 def test_attn_rows_that_see_nothing(cache):
     """Fewer keys than new tokens: the first queries stand before position 0."""
     d, o, lse = check([5, 3, 40], [0, 0, 0], 2, 3, 16, cache, kv=[2, 0, 7])
