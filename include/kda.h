@@ -426,13 +426,13 @@ int kda_decode_step_fused(float *state,
  *                had .. have - 1 are written, the others are left alone
  *   free_pages   (device) int32 [n_free] (may be NULL when n_free is 0)
  *   free_head    (device) int32 [1]: entries of free_pages already taken
- *   free_head_next (device) int32 [1], written: free_head plus the pages taken;
- *                must not be free_head itself (blocks of one launch read the one
- *                while another writes the other)
+ *   free_head_next (device) int32 [1], written: free_head plus the pages taken
  *   slot_map     (device) int64 [T_total], written
  *   positions    (device) int32 [T_total] or NULL
  *   cu_q         (device) int32 [n_seqs + 1], written;  kv_len (device) int32
  *                [n_seqs], written: ctx + new
+ * No output may be new_len, ctx_len, free_pages or free_head (blocks of one launch
+ * read the one while another writes the other).
  * Lengths that are negative, exceed max_blocks * page_size or do not add up to
  * T_total record KDA_DEVERR_LENGTHS, too few free pages KDA_DEVERR_NO_PAGES.
  * Either makes the step an empty one: slot_map -1, positions 0, cu_q 0, kv_len =

@@ -323,6 +323,11 @@ int kda_paged_tables(const int32_t *new_len, const int32_t *ctx_len, int n_seqs,
     if (free_head == free_head_next || (n_free > 0 && !free_pages) || (T_total > 0 && !slot_map))
         return KDA_ERR_INVALID_ARG;
     if (((uintptr_t)slot_map & 15u) || ((uintptr_t)positions & 15u)) return KDA_ERR_INVALID_ARG;
+    // every block reads all lengths and pages, some while others write already
+    const void *in[] = {new_len, ctx_len, free_pages, free_head};
+    for (const void *x : in)
+        if (x && (x == cu_q || x == kv_len || x == positions || x == slot_map || x == free_head_next || x == block_table))
+            return KDA_ERR_INVALID_ARG;
     cudaStream_t s = (cudaStream_t)stream;
     note_begin(s);
     const TablesArgs a{new_len,  ctx_len,   free_pages, free_head,  block_table, free_head_next, positions,

@@ -47,6 +47,15 @@ def test_tables_refusals(kw, rc):
     assert tables(**kw) == rc
 
 
+@pytest.mark.parametrize("name", ["new", "ctx", "free", "head"])
+@pytest.mark.parametrize("out", ["table", "head_next", "slots", "pos", "cu", "kv"])
+def test_tables_refuses_an_input_as_output(out, name):
+    """Blocks read the lengths and pages while others write already."""
+    apart = {k: ctypes.c_void_p((i + 1) << 20) for i, k in enumerate(
+        ["new", "ctx", "free", "head", "table", "head_next", "slots", "pos", "cu", "kv"])}
+    assert tables(**{**apart, out: apart[name]}) == INVALID
+
+
 @pytest.mark.parametrize("kw,rc", [
     (dict(D=64), UNSUPPORTED), (dict(dt=2), INVALID), (dict(cdt=7), INVALID), (dict(cdt=1), UNSUPPORTED),
     (dict(dt=1, cdt=2, ks=FAKE, vs=FAKE), UNSUPPORTED), (dict(cdt=2), INVALID), (dict(ks=FAKE, vs=FAKE), INVALID),
