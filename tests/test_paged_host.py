@@ -84,6 +84,23 @@ def test_workspace_size():
     assert f(-1, 1, 8, 8) == 0 and f(1, 0, 8, 8) == 0 and f(1, 1, 8, 3) == 0 and f(1, 1, 2, 4) == 0
 
 
+@pytest.mark.parametrize("fails", [RuntimeError("g++ failed"), PermissionError("read-only"), ImportError("headers")])
+def test_binding_without_the_compiled_way(fails, monkeypatch):
+    """The plain binding stands alone, and says once that it does."""
+    def no(*a, **k):
+        raise fails
+
+    monkeypatch.setattr(paged._build, "build_fast", no)
+    monkeypatch.setattr(paged, "_declared", None)
+    for f in ("tables", "append", "attn"):
+        monkeypatch.setattr(paged, "_fast_" + f, paged._not_loaded)
+    with pytest.warns(RuntimeWarning, match="plain binding") as said:
+        assert kda.paged_attn_workspace_size(1, 1, 8, 8) > 0
+        assert tables(n=0) == INVALID
+        test_binding_refuses_host_tensors()
+    assert len(said) == 1
+
+
 def test_binding_refuses_host_tensors():
     z = torch.zeros
     i = z(2, dtype=torch.int32)
