@@ -153,10 +153,11 @@ def paged_tables(new_len, ctx_len, block_table, free_pages, free_head, T_total, 
         raise KDAError("T_total must not be negative")
     slot_map = new_len.new_empty(T, dtype=_I64)
     positions, cu_q, kv_len, head = new_len.new_empty(T + 2 * n + 2).split_with_sizes((T, n + 1, n, 1))
-    rc = lib.kda_paged_tables(new_len.data_ptr(), ctx_len.data_ptr(), n, T, block_table.data_ptr(), block_table.shape[1],
-                              free_pages.data_ptr(), free_pages.numel(), free_head.data_ptr(), head.data_ptr(), page_size,
-                              n_pages, slot_map.data_ptr(), positions.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(),
-                              _p(error_word), _raw_stream(index))
+    with torch.cuda.device(index):  # (the library launches on the current device)
+        rc = lib.kda_paged_tables(new_len.data_ptr(), ctx_len.data_ptr(), n, T, block_table.data_ptr(), block_table.shape[1],
+                                  free_pages.data_ptr(), free_pages.numel(), free_head.data_ptr(), head.data_ptr(),
+                                  page_size, n_pages, slot_map.data_ptr(), positions.data_ptr(), cu_q.data_ptr(),
+                                  kv_len.data_ptr(), _p(error_word), _raw_stream(index))
     if rc:
         _check(rc, "kda_paged_tables")
     return slot_map, positions, cu_q, kv_len, head
@@ -181,9 +182,10 @@ def paged_append(k, v, slot_map, k_cache, v_cache, k_scale=None, v_scale=None, e
     T = shape[0]
     if slot_map.numel() != T:
         raise KDAError("slot_map must be [T]")
-    rc = lib.kda_paged_append(k.data_ptr(), v.data_ptr(), slot_map.data_ptr(), T, h, D, _CODE[k.dtype], code, _p(k_scale),
-                              _p(v_scale), k_cache.data_ptr(), v_cache.data_ptr(), n, ps, stride, _p(error_word),
-                              _raw_stream(index))
+    with torch.cuda.device(index):
+        rc = lib.kda_paged_append(k.data_ptr(), v.data_ptr(), slot_map.data_ptr(), T, h, D, _CODE[k.dtype], code, _p(k_scale),
+                                  _p(v_scale), k_cache.data_ptr(), v_cache.data_ptr(), n, ps, stride, _p(error_word),
+                                  _raw_stream(index))
     if rc:
         _check(rc, "kda_paged_append")
 
@@ -226,10 +228,11 @@ def paged_attn(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q=0, sm_scale
         raise KDAError("lse must be float32 [T, heads]")
     if workspace is None:
         workspace = q.new_empty(lib.kda_paged_attn_workspace_size(T, n, hq, hkv), dtype=torch.uint8)
-    rc = lib.kda_paged_attn(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), cu_q.data_ptr(),
-                            kv_len.data_ptr(), n, T, max_q, hq, hkv, D, _CODE[dtype], code, _p(k_scale), _p(v_scale), n_pages,
-                            ps, stride, block_table.shape[1], sm_scale, window, out.data_ptr(), lse.data_ptr(),
-                            workspace.data_ptr(), workspace.nbytes, _p(error_word), _raw_stream(index))
+    with torch.cuda.device(index):
+        rc = lib.kda_paged_attn(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), cu_q.data_ptr(),
+                                kv_len.data_ptr(), n, T, max_q, hq, hkv, D, _CODE[dtype], code, _p(k_scale), _p(v_scale),
+                                n_pages, ps, stride, block_table.shape[1], sm_scale, window, out.data_ptr(), lse.data_ptr(),
+                                workspace.data_ptr(), workspace.nbytes, _p(error_word), _raw_stream(index))
     if rc:
         _check(rc, "kda_paged_attn")
     return out, lse

@@ -625,6 +625,39 @@ def test_compiled_and_plain_binding_agree(cache, monkeypatch):
         assert x.dtype == y.dtype and x.shape == y.shape and torch.equal(x, y)
 
 
+def test_plain_binding_launches_on_the_tensors_device(monkeypatch):
+    """Every call of the library is made with the tensors' device current, whichever was."""
+    entered, real = [], torch.cuda.device
+
+    class Device(real):
+        def __enter__(self):
+            entered.append(self.idx)
+            super().__enter__()
+
+    for name in ("tables", "append", "attn"):
+        monkeypatch.setattr(paged, "_fast_" + name, lambda *a: None)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    lib, made = paged._lib(), []
+
+    class Library:
+        def __getattr__(self, name):
+            made.append((name, list(entered)))
+            return getattr(lib, name)
+
+    monkeypatch.setattr(paged, "_declared", Library())
+    e = errw()
+    table = i32([[0, -1]])
+    slots, pos, cu, kv, head = kda.paged_tables(i32([2]), i32([3]), table, i32([1]), i32([0]), 2, 16, 2, error_word=e)
+    x, c = torch.ones(2, 1, D, dtype=BF16, device=DEV), torch.ones(2, 1, 16, D, dtype=BF16, device=DEV)
+    kda.paged_append(x, x, slots, c, c.clone(), error_word=e)
+    o, lse = kda.paged_attn(x, c, c, table, cu, kv, sm_scale=1, error_word=e)
+    calls = [(n, d) for n, d in made if n in ("kda_paged_tables", "kda_paged_append", "kda_paged_attn")]
+    index = torch.cuda.current_device()
+    assert [n for n, _ in calls] == ["kda_paged_tables", "kda_paged_append", "kda_paged_attn"]
+    assert [d for _, d in calls] == [[index] * (k + 1) for k in range(3)]
+    assert int(e) == 0 and (o == 1).all()
+
+
 def test_refusals_of_both_ways():
     """What the compiled way leaves undone, the plain one refuses, with its message."""
     d = make([2], [20], 2, 2, 16, BF16)
