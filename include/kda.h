@@ -528,10 +528,11 @@ long long kda_launch_count(void);
 
 /* kda_set_wait_budget -- the clock-cycle limit of the library's waits on
  * flags that other blocks of the same launch raise (the fused prefill's
- * record-ready flags) and of the decode's waits on its own copies, for every
- * call made afterwards in this process (not thread-safe against calls in
+ * record-ready flags), of the decode's waits on its own copies and, where it is
+ * under 10^6, of the paged attention's waits within its blocks, for every call
+ * made afterwards in this process (not thread-safe against calls in
  * flight on other host threads).  A wait that runs out records
- * KDA_DEVERR_TIMEOUT (workspace error word, decode error word), its block
+ * KDA_DEVERR_TIMEOUT (workspace error word, the call's error word), its block
  * stops, lets its own copies and tensor-core work finish and frees its TMEM,
  * and the call's outputs are then undefined.  cycles <= 0 restores the
  * default (2e9 cycles, about one second).  Returns the previous limit.  Meant

@@ -36,7 +36,10 @@ struct PagedAttn {
     int4 *lead;
     float *parts;
     int slot_rows;                   // rows per slot
+    long long wait_budget;           // clock cycles that a wait may take, where it is under SHORT_BUDGET
 };
+
+constexpr long long SHORT_BUDGET = 1000000;  // clock cycles; launches with less take kernels that look at it
 
 struct PagedMaps {
     CUtensorMap k, v;

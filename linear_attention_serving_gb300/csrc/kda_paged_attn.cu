@@ -215,6 +215,7 @@ int kda_paged_attn(const void *q, const void *k_cache, const void *v_cache, cons
     // stays clear of 2^31 where positions are added to it)
     a.window = window >= (int64_t)max_blocks * page_size ? 0 : window;
     a.scale_log2 = sm_scale * 1.4426950408889634f;
+    a.wait_budget = wait_budget();
     char *ws = (char *)workspace;
     const int64_t max_rows = (int64_t)a.max_q * a.G;
     JoinSet js[2] = {{nullptr, nullptr, 0, 1}, {nullptr, nullptr, 0, 1}};

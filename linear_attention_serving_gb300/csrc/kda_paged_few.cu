@@ -86,7 +86,7 @@ template <class C> struct Bars {
         pv_done = p_ready + 2;
         o_free = pv_done + 2;      // [2] by item
         last = o_free + 2;
-        joint = last + 2;          // (last: products in flight when a wait ran out)
+        joint = last + 2;          // (last: the products of S, of O)
         seg_full = joint + 1;      // (joint: the two groups at an item's end)
         seg_ready = seg_full + SEGS;  // its queries and their scales are there too
         seg_empty = seg_ready + SEGS;
@@ -209,7 +209,7 @@ struct Shared {
     int64_t A;
 };
 
-template <class C>
+template <class C, class Gate>
 __device__ __forceinline__ bool next_seg(uint8_t *sm, const Bars<C> &bar, int &i, const Gate &gate, Seg &s) {
     if (!gate(&bar.seg_full[i % SEGS], (i / SEGS) & 1)) return false;
     s = *reinterpret_cast<const Seg *>(sm + C::OFF_SEG + (i % SEGS) * 64);
@@ -233,7 +233,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float x, float y) {
 // ---------------------------------------------------------------- walk, queries
 // One warp walks the line, tells the others of each segment (the loads begin on it) and
 // puts its queries (rows past R zero) into the buffer of their turn.
-template <bool E4, int NR>
+template <bool E4, int NR, class Gate>
 __device__ __forceinline__ void walk_role(const PagedAttn &a, uint8_t *sm, Walk w, int64_t P0, const Gate &gate) {
     using C = Cfg<E4, NR>;
     const int lane = threadIdx.x & 31;
@@ -329,7 +329,7 @@ __device__ __forceinline__ void walk_role(const PagedAttn &a, uint8_t *sm, Walk 
 // Tiles go in the order K0, K1, V0, K2, V1 .. through all items: K is used two tiles
 // before V is.  e4m3's V goes into a ring of its own, with a word that says which rows
 // hold keys.
-template <bool E4, int NR>
+template <bool E4, int NR, class Gate>
 __device__ __forceinline__ void load_role(const PagedAttn &a, const PagedMaps &maps, uint8_t *sm, const Gate &gate) {
     using C = Cfg<E4, NR>;
     constexpr int ES = E4 ? 1 : 2, NV = E4 ? C::RS : C::VS;
@@ -340,9 +340,11 @@ __device__ __forceinline__ void load_role(const PagedAttn &a, const PagedMaps &m
     uint8_t *kb = sm + C::OFF_K, *vb = sm + (E4 ? C::OFF_R : C::OFF_V);
     int nk = 0, nv = 0;                                 // tiles of K and V so far
     int kslot = 0, kph = 1, vslot = 0, vph = 1;         // their places in the rings, and the parity to wait for
-    auto drain = [&]() {   // a wait ran out: let the copies in flight land before the block ends
+    // The block ends only when its copies have landed, also where a wait of another role runs
+    // out after this one has issued its last.  v: tiles of V that may be in flight.
+    auto drain = [&](int v) {
         for (int u = nk - 1; u >= 0 && u >= nk - C::KS; --u) mbar_wait(&bar.k_full[u % C::KS], (u / C::KS) & 1);
-        for (int u = nv - 1; u >= 0 && u >= nv - NV; --u) mbar_wait(&vf[u % NV], (u / NV) & 1);
+        for (int u = nv - 1; u >= 0 && u >= nv - v; --u) mbar_wait(&vf[u % NV], (u / NV) & 1);
         __syncwarp();
     };
     // boxes f .. e - 1 of a tile: this lane's page and row
@@ -381,7 +383,7 @@ __device__ __forceinline__ void load_role(const PagedAttn &a, const PagedMaps &m
             // The last item's V does not wait for the next K here: the walk goes SEGS segments ahead of
             // the softmax, so behind SEGS - 1 items without keys that K is told of only after this V
             // has been used.
-            if (have && !load(prev, true)) return drain();
+            if (have && !load(prev, true)) return drain(NV);
             have = false;
             continue;
         }
@@ -408,28 +410,29 @@ __device__ __forceinline__ void load_role(const PagedAttn &a, const PagedMaps &m
             t.page = __shfl_sync(0xffffffffu, page, (b0 - cbase + lane) & 31);
             t.y = __shfl_sync(0xffffffffu, off, (b0 - cbase + lane) & 31);
             t.z = max(0, s.lo - key0) | (min(BK, s.hi - key0) << 8);
-            if (!load(t, false)) return drain();
-            if (have && !load(prev, true)) return drain();
+            if (!load(t, false)) return drain(NV);
+            if (have && !load(prev, true)) return drain(NV);
             prev = t;
             have = true;
         }
     }
-    if (have && !*gate.abort && !load(prev, true)) return drain();
+    if (have && !*gate.abort && !load(prev, true)) return drain(NV);
     if (E4) {  // the end, for the widening warps
-        if (!gate(&ve[vslot], vph)) return drain();
+        if (!gate(&ve[vslot], vph)) return drain(NV);
         if (lane == 0) {
             reinterpret_cast<int *>(sm + C::OFF_DESC)[vslot] = -1;
             mbar_arrive(&vf[vslot]);
         }
         __syncwarp();
+        return drain(NV - 1);  // (the tile that stood where the end does has been used)
     }
-    if (*gate.abort) drain();
+    drain(NV);
 }
 
 // ---------------------------------------------------------------- widening
 // V from e4m3 to fp16, 32 WIDEN / 128 threads to a row.  Rows that no seen key stands in
 // become zeros (0 x NaN is NaN).
-template <int NR>
+template <int NR, class Gate>
 __device__ __forceinline__ void widen_role(uint8_t *sm, const Gate &gate) {
     using C = Cfg<true, NR>;
     constexpr int W = 32 / C::WIDEN;  // 16-byte pieces of a row for one thread: 8 of them to a row
@@ -551,14 +554,15 @@ constexpr uint32_t ID_S = (1u << 4) | (E4 ? 0u : 1u << 7) | (1u << 10) | ((uint3
 template <bool E4, int NR>
 constexpr uint32_t ID_O = (1u << 4) | (E4 ? 0u : (1u << 7) | (1u << 10)) | (1u << 15) | (1u << 16) | ((uint32_t)(NR >> 3) << 17) | ((128u >> 4) << 24);
 
+// Before TMEM is given back and the block ends, whichever wait ran out or none.
 template <class C>
-__device__ __forceinline__ void drain_products(const Bars<C> &bar, int i) {  // before TMEM is given back
+__device__ __forceinline__ void drain_products(const Bars<C> &bar, int i) {
     mma_commit_w(bar.last + i);
     mbar_wait(bar.last + i, 0);
     __syncwarp();
 }
 
-template <bool E4, int NR>
+template <bool E4, int NR, class Gate>
 __device__ __forceinline__ void s_role(uint8_t *sm, uint32_t tmem, const Gate &gate) {
     using C = Cfg<E4, NR>;
     const Bars<C> bar(sm);
@@ -592,9 +596,9 @@ __device__ __forceinline__ void s_role(uint8_t *sm, uint32_t tmem, const Gate &g
         mma_commit_w(&bar.q_empty[x]);
         ++item;
     }
-    if (*gate.abort) drain_products<C>(bar, 0);
+    drain_products<C>(bar, 0);
 }
-template <bool E4, int NR>
+template <bool E4, int NR, class Gate>
 __device__ __forceinline__ void o_role(uint8_t *sm, uint32_t tmem, const Gate &gate) {
     using C = Cfg<E4, NR>;
     const Bars<C> bar(sm);
@@ -624,7 +628,7 @@ __device__ __forceinline__ void o_role(uint8_t *sm, uint32_t tmem, const Gate &g
         if (!ok) break;
         ++item;
     }
-    if (*gate.abort) drain_products<C>(bar, 1);
+    drain_products<C>(bar, 1);
 }
 
 // ---------------------------------------------------------------- softmax
@@ -675,7 +679,7 @@ __device__ __forceinline__ void tmem_row(uint32_t taddr, float *o) {
 // that runs out is passed on at the group's next meeting (every segment begins with one,
 // every meeting looks for it), so that a group's warps leave together; the groups wait
 // for each other with bounded waits only.
-template <bool E4, int NR>
+template <bool E4, int NR, class Gate>
 __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, uint32_t tmem, const Gate &gate) {
     using C = Cfg<E4, NR>;
     const Bars<C> bar(sm);
@@ -926,7 +930,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
     }
 }
 
-template <bool E4, int NR>
+template <bool E4, int NR, bool SHORT>
 __global__ void __launch_bounds__(Cfg<E4, NR>::THREADS, 1)
     paged_few_kernel(const __grid_constant__ PagedMaps maps, const __grid_constant__ PagedAttn a, int min_per) {
     using C = Cfg<E4, NR>;
@@ -999,7 +1003,7 @@ __global__ void __launch_bounds__(Cfg<E4, NR>::THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh->tmem;
-    const Gate gate{&sh->abort, a.err};
+    const Waits<SHORT> gate{&sh->abort, a.err, a.wait_budget};
     if (warp < C::SOFT) {
         softmax_role<E4, NR>(a, sm, tmem, gate);
     } else if (warp == C::W_S) {
@@ -1030,14 +1034,18 @@ __global__ void __launch_bounds__(Cfg<E4, NR>::THREADS, 1)
     }
 }
 
-template <bool E4, int NR>
-int launch(const PagedAttn &a, const PagedMaps &maps, cudaStream_t s) {
+template <bool E4, int NR, bool SHORT>
+int launch_for(const PagedAttn &a, const PagedMaps &maps, cudaStream_t s) {
     using C = Cfg<E4, NR>;
-    const int rc = prepare_kernel((const void *)paged_few_kernel<E4, NR>, C::SMEM, C::THREADS, nullptr);
+    const int rc = prepare_kernel((const void *)paged_few_kernel<E4, NR, SHORT>, C::SMEM, C::THREADS, nullptr);
     if (rc) return rc;
-    paged_few_kernel<E4, NR><<<paged_few_blocks(), C::THREADS, C::SMEM, s>>>(maps, a, 3);
+    paged_few_kernel<E4, NR, SHORT><<<paged_few_blocks(), C::THREADS, C::SMEM, s>>>(maps, a, 3);
     note_launch("paged_few", s);
     return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+template <bool E4, int NR>
+int launch(const PagedAttn &a, const PagedMaps &maps, cudaStream_t s) {
+    return a.wait_budget < SHORT_BUDGET ? launch_for<E4, NR, true>(a, maps, s) : launch_for<E4, NR, false>(a, maps, s);
 }
 
 }  // namespace

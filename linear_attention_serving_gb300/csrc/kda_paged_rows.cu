@@ -31,7 +31,8 @@ constexpr int HALF = 8192;                   // bytes of K (and of V) of one til
 constexpr int STAGE = 2 * HALF;
 // CONS: consumer warps, eight, or four in calls of up to 8 rows (45 us instead of 48 then for
 // one token of 16 requests: fewer pieces to merge, fewer warps to give a tile back)
-template <int CONS_> struct Cfg {
+template <int CONS_, bool SHORT_> struct Cfg {
+    static constexpr bool SHORT = SHORT_;
     static constexpr int CONS = CONS_, THREADS = (CONS + 1) * 32;
     static constexpr int OFF_RED = STAGES * STAGE;                 // [CONS][RW][128] fp32
     static constexpr int OFF_P = OFF_RED + CONS * RW * D * 4;      // probabilities [CONS][RW][16]
@@ -74,6 +75,21 @@ template <class C> __device__ __forceinline__ int64_t line_tiles(const PagedAttn
     return (int64_t)a.Hkv * ((r.rows + grp - 1) / grp) * (HEAD + req_tiles(r));
 }
 
+// A bounded wait of a whole warp that also gives up once *abort is set.  SHORT: as for the
+// tensor-core kernels, the launch's budget, and no try that sleeps.
+template <class C>
+__device__ __forceinline__ bool wait_for(const PagedAttn &a, uint64_t *bar, uint32_t parity, const volatile int *abort) {
+    bool ok;
+    if constexpr (C::SHORT) {
+        const long long t0 = clock64();
+        while (!(ok = mbar_test_wait(bar, parity)) && !*abort && clock64() - t0 <= a.wait_budget) {
+        }
+    } else {
+        ok = mbar_wait_ab(bar, parity, abort);
+    }
+    return __all_sync(0xffffffffu, ok);
+}
+
 // ---------------------------------------------------------------- producer
 // One tile (16 keys of one head of one page) in one copy: the map's third dimension is
 // the row's four 128-byte pieces, which land in blocks of their own.
@@ -91,19 +107,23 @@ __device__ __forceinline__ void produce(const PagedAttn &a, const PagedMaps &map
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + C::OFF_BAR), *empty = full + STAGES;
     volatile int *abort = reinterpret_cast<volatile int *>(sm + C::OFF_ABORT);
     int stage = 0, phase = 0, issued = 0;
+    // the block ends only when its copies have landed, also where a wait of the consumers runs
+    // out after the last was issued
+    auto drain = [&]() {
+        for (int i = 1; i <= STAGES && i <= issued; ++i) {
+            const int u = issued - i;
+            mbar_wait(&full[u % STAGES], (u / STAGES) & 1);
+        }
+        __syncwarp();
+    };
     auto next_stage = [&]() -> bool {
-        const bool ok = mbar_wait_ab(&empty[stage], phase ^ 1, abort);
-        if (!__all_sync(0xffffffffu, ok)) {
+        if (!wait_for<C>(a, &empty[stage], phase ^ 1, abort)) {
             if (lane == 0) {
                 *abort = 1;
                 if (a.err) atomicOr(a.err, KDA_DEVERR_TIMEOUT);
-                // let the copies in flight land before the block ends
-                for (int i = 1; i <= STAGES && i <= issued; ++i) {
-                    const int u = issued - i;
-                    mbar_wait(&full[u % STAGES], (u / STAGES) & 1);
-                }
             }
             __syncwarp();
+            drain();
             return false;
         }
         ++issued;
@@ -208,6 +228,8 @@ __device__ __forceinline__ void produce(const PagedAttn &a, const PagedMaps &map
         reinterpret_cast<Desc *>(sm + C::OFF_DESC + stage * 64)->flags = END;
         mbar_arrive(&full[stage]);
     }
+    __syncwarp();
+    drain();
 }
 
 // ---------------------------------------------------------------- a warp's rows
@@ -381,22 +403,24 @@ __device__ __forceinline__ void consume(const PagedAttn &a, uint8_t *sm) {
     int stage = 0, phase = 0;
     uint64_t *meet = reinterpret_cast<uint64_t *>(sm + C::OFF_MEET);
     int meet_phase = 0;
+    auto stop = [&]() {
+        if (lane == 0) {
+            *abort = 1;
+            if (a.err) atomicOr(a.err, KDA_DEVERR_TIMEOUT);
+        }
+    };
     // (a bounded wait, unlike a named barrier: a warp that gave up never comes)
     auto meet_all = [&]() -> bool {
         __syncwarp();
         if (lane == 0) mbar_arrive(meet);
-        const bool ok = __all_sync(0xffffffffu, mbar_wait_ab(meet, meet_phase, abort));
+        const bool ok = wait_for<C>(a, meet, meet_phase, abort);
         meet_phase ^= 1;
         if (!ok && lane == 0) *abort = 1;
         return ok;
     };
     while (true) {
-        const bool ok = mbar_wait_ab(&full[stage], phase, abort);
-        if (!__all_sync(0xffffffffu, ok)) {
-            if (lane == 0) {
-                *abort = 1;
-                if (a.err) atomicOr(a.err, KDA_DEVERR_TIMEOUT);
-            }
+        if (!wait_for<C>(a, &full[stage], phase, abort)) {
+            stop();
             break;
         }
         const Desc *ds = reinterpret_cast<const Desc *>(sm + C::OFF_DESC + stage * 64);
@@ -513,7 +537,9 @@ int launch_paged_rows(PagedAttn a, const void *k, const void *v, int64_t page_st
     PagedMaps maps;
     const int rc = make_paged_row_maps(k, v, a.Hkv, a.page_size, a.n_pages, page_stride, TK, &maps);
     if (rc) return rc;
-    return (int64_t)a.max_q * a.G <= RW ? launch<Cfg<4>>(a, maps, s) : launch<Cfg<8>>(a, maps, s);
+    const bool brief = a.wait_budget < SHORT_BUDGET, few = (int64_t)a.max_q * a.G <= RW;
+    if (brief) return few ? launch<Cfg<4, true>>(a, maps, s) : launch<Cfg<8, true>>(a, maps, s);
+    return few ? launch<Cfg<4, false>>(a, maps, s) : launch<Cfg<8, false>>(a, maps, s);
 }
 
 }  // namespace kda

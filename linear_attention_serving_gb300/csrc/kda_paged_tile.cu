@@ -72,7 +72,7 @@ struct Bars {
         p_ready = s_full + 4;        // the same
         pv_done = p_ready + 4;       // the same
         o_free = pv_done + 4;        // [2]
-        last = o_free + 2;           // [2] products in flight when a wait ran out
+        last = o_free + 2;           // [2] a warp's products
         seg_full = last + 2;
         seg_empty = seg_full + SEGS;
     }
@@ -282,11 +282,17 @@ struct Shared {
 // One warp walks the line ahead of the others, and has each segment's queries
 // loaded; a segment with nt < 0 ends it.  Items of one half take the two halves of
 // the buffer in turn, so the next one's queries arrive while this one is worked on.
+template <class Gate>
 __device__ __forceinline__ void walk_role(const PagedAttn &a, const CUtensorMap &qmap, uint8_t *sm, Walk w, int th, int64_t P0,
                                           int64_t total, const Gate &gate) {
     const int lane = threadIdx.x & 31;
     const Bars bar(sm);
     int n0 = 0, n1 = 0;  // loads of each half of Q
+    auto landed = [&]() {  // the block ends only when its copies have
+        if (n0) mbar_wait(&bar.q_full[0], (n0 - 1) & 1);
+        if (n1) mbar_wait(&bar.q_full[1], (n1 - 1) & 1);
+        __syncwarp();
+    };
     for (int i = 0;; ++i) {
         Seg s;
         bool more = w.next(a, th, P0, s);
@@ -305,7 +311,7 @@ __device__ __forceinline__ void walk_role(const PagedAttn &a, const CUtensorMap 
             mbar_arrive(&bar.seg_full[i % SEGS]);
         }
         __syncwarp();
-        if (ok && !more) return;
+        if (ok && !more) return landed();
         for (int x = 0; ok && s.nt > 0 && x < 2; ++x) {
             if (s.alt && x != s.half) continue;
             ok = gate(&bar.q_empty[x], ((x ? n1 : n0) & 1) ^ 1);
@@ -321,15 +327,11 @@ __device__ __forceinline__ void walk_role(const PagedAttn &a, const CUtensorMap 
             if (x) ++n1;
             else ++n0;
         }
-        if (!ok) {  // let the copies in flight land
-            if (n0) mbar_wait(&bar.q_full[0], (n0 - 1) & 1);
-            if (n1) mbar_wait(&bar.q_full[1], (n1 - 1) & 1);
-            __syncwarp();
-            return;
-        }
+        if (!ok) return landed();
     }
 }
 // The next segment, for a whole warp; false at the line's end.
+template <class Gate>
 __device__ __forceinline__ bool next_seg(uint8_t *sm, const Bars &bar, int &i, const Gate &gate, Seg &s) {
     if (!gate(&bar.seg_full[i % SEGS], (i / SEGS) & 1)) return false;
     s = *reinterpret_cast<const Seg *>(sm + OFF_SEG + (i % SEGS) * 64);
@@ -341,13 +343,16 @@ __device__ __forceinline__ bool next_seg(uint8_t *sm, const Bars &bar, int &i, c
 
 // ---------------------------------------------------------------- loads
 // Keys and values.
+template <class Gate>
 __device__ __forceinline__ void load_role(const PagedAttn &a, const PagedMaps &maps, uint8_t *sm, const Gate &gate) {
     const int lane = threadIdx.x & 31;
     const Bars bar(sm);
     const int box = a.box, lg = a.box_log, nbx = BK >> lg;
     int ring = 0, ringp = 0;
     uint32_t seq = 0;  // K / V tiles so far
-    auto drain = [&]() {  // a wait ran out: let the copies in flight land before the block ends
+    // the block ends only when its copies have landed, also where a wait of another role runs out
+    // after this one has issued its last
+    auto drain = [&]() {
         for (uint32_t i = 1; i <= SLOTS && i <= seq; ++i) mbar_wait(&bar.kv_full[(seq - i) % SLOTS], ((seq - i) / SLOTS) & 1);
         __syncwarp();
     };
@@ -398,6 +403,7 @@ __device__ __forceinline__ void load_role(const PagedAttn &a, const PagedMaps &m
             if (!tile(j, false) || !tile(j, true)) return drain();
         }
     }
+    drain();
 }
 
 // ---------------------------------------------------------------- products
@@ -405,6 +411,7 @@ __device__ __forceinline__ void load_role(const PagedAttn &a, const PagedMaps &m
 // alone): what one of them spends on waits and on issuing hides behind the other's
 // products.  Both see every K, V and Q tile, so that no barrier's phase passes one
 // of them by: whoever has no product on a tile gives it back as soon as it came.
+template <class Gate>
 __device__ __forceinline__ void mma_role(const PagedAttn &a, uint8_t *sm, uint32_t tmem, int x, const Gate &gate) {
     const Bars bar(sm);
     constexpr uint32_t ID_QK = idesc_bf16_f32(BM, BK / 2), ID_PV = idesc_bf16_f32_bmn(BM, D);
@@ -502,11 +509,10 @@ __device__ __forceinline__ void mma_role(const PagedAttn &a, uint8_t *sm, uint32
             }
         }
     }
-    if (!ok || *gate.abort) {  // let the products in flight end before TMEM is given back
-        mma_commit_w(bar.last + x);
-        mbar_wait(bar.last + x, 0);
-        __syncwarp();
-    }
+    // TMEM is given back only after the products, whichever wait ran out or none
+    mma_commit_w(bar.last + x);
+    mbar_wait(bar.last + x, 0);
+    __syncwarp();
 }
 
 // ---------------------------------------------------------------- softmax
@@ -586,6 +592,7 @@ __device__ __forceinline__ void finish(const PagedAttn &a, uint32_t to, int th, 
 
 // Two threads, of two warps that meet at a barrier of their own, share a row.  A
 // wait that runs out is passed on at the next meeting, so both leave together.
+template <class Gate>
 __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, uint32_t tmem, int th, const Gate &gate) {
     constexpr int HK = BK / 4;  // keys of one thread: a half of half a tile
     const Bars bar(sm);
@@ -741,6 +748,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
     }
 }
 
+template <bool SHORT>
 __global__ void __launch_bounds__(THREADS, 1)
     paged_tile_kernel(const __grid_constant__ PagedMaps maps, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ PagedAttn a, int th,
                       int min_per, int max_parts) {
@@ -810,7 +818,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh->tmem;
-    const Gate gate{&sh->abort, a.err};
+    const Waits<SHORT> gate{&sh->abort, a.err, a.wait_budget};
     if (warp < SOFT) {
         softmax_role(a, sm, tmem, th, gate);
     } else {
@@ -854,8 +862,8 @@ int launch_paged_tile(PagedAttn a, const void *k, const void *v, int64_t page_st
     int rc = make_paged_maps(k, v, KDA_BF16, a.Hkv, a.page_size, a.n_pages, page_stride, box, &maps);
     if (rc) return rc;
     if ((rc = make_paged_q_map(a.q, a.T, a.Hq, a.G, th, &qmap))) return rc;
-    const void *f = (const void *)paged_tile_kernel;
-    if ((rc = prepare_kernel(f, SMEM, THREADS, nullptr))) return rc;
+    const auto kernel = a.wait_budget < SHORT_BUDGET ? paged_tile_kernel<true> : paged_tile_kernel<false>;
+    if ((rc = prepare_kernel((const void *)kernel, SMEM, THREADS, nullptr))) return rc;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(paged_tile_blocks());
     cfg.blockDim = dim3(THREADS);
@@ -866,7 +874,7 @@ int launch_paged_tile(PagedAttn a, const void *k, const void *v, int64_t page_st
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = after_rows ? 1 : 0;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_tile_kernel, maps, qmap, a, th, 4, max_parts);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, maps, qmap, a, th, 4, max_parts);
     note_launch("paged_tile", s);
     return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }

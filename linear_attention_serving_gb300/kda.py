@@ -319,9 +319,9 @@ def segment_scan_auto_segments(T_total: int, H: int, n_seqs: int = 1) -> int:
 
 
 def set_wait_budget(cycles: int) -> int:
-    """kda_set_wait_budget: clock-cycle limit of the waits on other blocks' flags and of
-    the decode's copy waits for the calls that follow (<= 0: the default, about one
-    second).  Returns the previous limit."""
+    """kda_set_wait_budget: clock-cycle limit of the waits on other blocks' flags, of the
+    decode's copy waits and, under 10^6, of the paged attention's waits for the calls
+    that follow (<= 0: the default, about one second).  Returns the previous limit."""
     return int(load().kda_set_wait_budget(int(cycles)))
 
 

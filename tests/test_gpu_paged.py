@@ -590,6 +590,30 @@ def test_attn_context_longer_than_the_cache_of_the_gpu_holds(window):
     attn_close(o, lse, (o_ref, l_ref[..., 0], a, mag[..., 0]), BF16, BF16)
 
 
+# ------------------------------------------------------------------ waits that run out
+@pytest.mark.parametrize("g,new,cache", [(4, [1] * 24, BF16), (4, [1] * 24, E4M3), (4, [7] * 24, E4M3), (130, [1] * 24, BF16),
+                                         (4, [60] * 24, BF16), (4, [200, 1, 40] * 8, BF16), (2, [1] * 24, F32), (2, [9] * 24, F32)])
+def test_attn_wait_times_out_then_recovers(g, new, cache):
+    """Waits of every role run out, early and late: the call records it, stays in its buffers
+    and returns, and the next call is right."""
+    d = make(new, [3000, 9000, 17, 500] * 6, 1, g, 64, cache, seed=26)
+    o, lse, e = run_attn(d, max_q=max(new))
+    out, ol = Guarded(o.shape, o.dtype), Guarded(lse.shape, F32)
+    ws = Guarded((kda.paged_attn_workspace_size(sum(new), len(new), g, 1),), torch.uint8)
+    codes = []
+    for budget in (1, 100, 300, 700, 1500, 3000, 6000, 12000, 50000):
+        old = kda.set_wait_budget(budget)
+        try:
+            codes.append(run_attn(d, max_q=max(new), out=out.t, lse=ol.t, workspace=ws.t)[2])
+        finally:
+            kda.set_wait_budget(old)
+        assert codes[-1] in (0, 4) and out.intact() and ol.intact() and ws.intact()
+        assert codes[-1] or (torch.equal(out.t, o) and torch.equal(ol.t, lse))
+    assert e == 0 and codes[0] == 4
+    o2, lse2, e = run_attn(d, max_q=max(new), out=out.t, lse=ol.t, workspace=ws.t)
+    assert e == 0 and torch.equal(o2, o) and torch.equal(lse2, lse)
+
+
 # ------------------------------------------------------------------ the two ways into the library
 @pytest.mark.parametrize("cache", CACHES, ids=NAMES)
 def test_compiled_and_plain_binding_agree(cache, monkeypatch):
