@@ -415,7 +415,7 @@ __device__ __forceinline__ void consume(const PagedAttn &a, uint8_t *sm) {
         if (lane == 0) mbar_arrive(meet);
         const bool ok = wait_for<C>(a, meet, meet_phase, abort);
         meet_phase ^= 1;
-        if (!ok && lane == 0) *abort = 1;
+        if (!ok) stop();
         return ok;
     };
     while (true) {
