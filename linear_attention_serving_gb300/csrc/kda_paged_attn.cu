@@ -255,7 +255,7 @@ int kda_paged_attn(const void *q, const void *k_cache, const void *v_cache, cons
         js[1] = use(w.tile, paged_tile_blocks() * parts);
         if ((rc = launch_paged_tile(a, k_cache, v_cache, page_stride, parts, few, s))) return rc;
     }
-    return launch_join(a, js[0], js[1], max_rows, dtype == KDA_F32, s);
+    return launch_join(a, js[0], js[1], max_rows, false, s);
 }
 
 }  // extern "C"

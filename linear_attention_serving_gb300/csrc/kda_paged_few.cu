@@ -1,6 +1,7 @@
 // kda_paged_few.cu -- paged attention on tcgen05 for few rows (single tokens,
-// draft windows; bf16 and e4m3 caches): NR = 16 or 32 rows of one kv head at a time (32
-// for e4m3 caches, and for bf16 where a token alone has more rows than a tile has).
+// draft windows; bf16 and e4m3 caches): NR rows of one kv head at a time, 16 where no
+// request of the call can have more, else 32 (e4m3 caches; bf16 with more heads to a kv
+// head than a tile of the other kernel has rows).
 // Each key and value is read for few rows, so the time is the pages' bytes over HBM;
 // what the kernel has to do is keep copies in flight and stay out of their way.
 //
@@ -328,7 +329,7 @@ __device__ __forceinline__ void walk_role(const PagedAttn &a, uint8_t *sm, Walk 
 // ---------------------------------------------------------------- loads
 // Tiles go in the order K0, K1, V0, K2, V1 .. through all items: K is used two tiles
 // before V is.  e4m3's V goes into a ring of its own, with a word that says which rows
-// hold keys.
+// hold seen keys.
 template <bool E4, int NR, class Gate>
 __device__ __forceinline__ void load_role(const PagedAttn &a, const PagedMaps &maps, uint8_t *sm, const Gate &gate) {
     using C = Cfg<E4, NR>;

@@ -455,7 +455,6 @@ __device__ __forceinline__ void consume(const PagedAttn &a, uint8_t *sm) {
             work.end(lane, mine, ml + warp * RW);
             if (!meet_all()) break;
             float *slot = paged_slot(a, d.slot);
-            const float vs = 1.f;
             for (int r = warp; r < d.R; r += C::CONS) {
                 const int rb = r / d.rpw, rl = r - rb * d.rpw;
                 float M = -INFINITY, L = 0.f;
@@ -475,7 +474,7 @@ __device__ __forceinline__ void consume(const PagedAttn &a, uint8_t *sm) {
                 }
                 if (d.flags & WHOLE) {
                     const int rr = d.r0 + r, j = rr / a.G;
-                    paged_store_row(a, true, d.tok0 + j, d.h * a.G + (rr - j * a.G), lane, acc, M, L, vs);
+                    paged_store_row(a, true, d.tok0 + j, d.h * a.G + (rr - j * a.G), lane, acc, M, L, 1.f);
                 } else {
                     if (lane == 0) reinterpret_cast<float2 *>(slot)[r] = make_float2(M, L);
                     reinterpret_cast<float4 *>(slot + 2 * a.slot_rows)[r * (D / 4) + lane] = acc;

@@ -16,7 +16,8 @@
 // keys, whose S stand side by side: while it works out the probabilities of one, the
 // tensor cores run the other's P V and, over the same columns, the next S.  (Whole
 // tiles, one S a group: prompt 242 us, windows 311 us; the groups made to take turns:
-// 234 and 292 us; registers given out by role: 226 and 267 us.)
+// 234 and 292 us.  Registers given out by role: 229 and 268 us, when it was 223 and 262
+// without.)
 //
 // The reference `ref` of a row's exponents follows its maximum only when that
 // has grown by more than 2^8: until then probabilities up to 256 are as precise
@@ -49,7 +50,7 @@ constexpr int OFF_SCAN = OFF_KV + SLOTS * SLOT;  // the start's sums
 constexpr int OFF_BAR = OFF_SCAN + 256;
 constexpr int SEGS = 4;                        // ring of segments ahead of the roles
 constexpr int NBAR = 2 * SLOTS + 20 + 2 * SEGS;
-constexpr int OFF_MISC = (OFF_BAR + NBAR * 8 + 63) / 64 * 64;  // TMEM address, abort flag, start of the block's line
+constexpr int OFF_MISC = (OFF_BAR + NBAR * 8 + 63) / 64 * 64;  // TMEM address, abort flag
 constexpr int OFF_SEG = OFF_MISC + 64;
 constexpr int OFF_MX = OFF_SEG + SEGS * 64;    // [group][half of the keys][row] maximum, sum
 constexpr int SMEM = OFF_MX + 4 * BM * 4;
@@ -412,7 +413,7 @@ __device__ __forceinline__ void load_role(const PagedAttn &a, const PagedMaps &m
 // products.  Both see every K, V and Q tile, so that no barrier's phase passes one
 // of them by: whoever has no product on a tile gives it back as soon as it came.
 template <class Gate>
-__device__ __forceinline__ void mma_role(const PagedAttn &a, uint8_t *sm, uint32_t tmem, int x, const Gate &gate) {
+__device__ __forceinline__ void mma_role(uint8_t *sm, uint32_t tmem, int x, const Gate &gate) {
     const Bars bar(sm);
     constexpr uint32_t ID_QK = idesc_bf16_f32(BM, BK / 2), ID_PV = idesc_bf16_f32_bmn(BM, D);
     const int lane = threadIdx.x & 31;
@@ -823,7 +824,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         softmax_role(a, sm, tmem, th, gate);
     } else {
         if (warp < SOFT + 2)
-            mma_role(a, sm, tmem, warp - SOFT, gate);
+            mma_role(sm, tmem, warp - SOFT, gate);
         else if (warp == SOFT + 2)
             load_role(a, maps, sm, gate);
         else {

@@ -59,16 +59,14 @@ int make_input_maps(const void *q, const void *k, const void *v, const float *z,
     return encode_rows(&out->z, z, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, T, H);
 }
 
-// Paged caches: {D, Hkv * page_size, pages}, one tile = box_rows keys of one
+// bf16 and e4m3 caches: {D, Hkv * page_size, pages}, one tile = box_rows keys of one
 // head of one page, 128 bytes of each row, stored with the 128-byte swizzle.
 int make_paged_maps(const void *k, const void *v, int cache_dtype, int Hkv, int page_size, int n_pages,
                     int64_t page_stride, int box_rows, PagedMaps *out) {
     const EncodeTiledFn fn = encode_tiled();
     if (!fn) return KDA_ERR_CUDA;
-    const int el = cache_dtype == KDA_BF16 ? 2 : cache_dtype == KDA_F32 ? 4 : 1;
-    const CUtensorMapDataType type = cache_dtype == KDA_BF16  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                     : cache_dtype == KDA_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-                                                              : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    const int el = cache_dtype == KDA_BF16 ? 2 : 1;
+    const CUtensorMapDataType type = cache_dtype == KDA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8;
     const cuuint64_t dim[3] = {(cuuint64_t)D, (cuuint64_t)Hkv * page_size, (cuuint64_t)n_pages};
     const cuuint64_t stride[2] = {(cuuint64_t)D * el, (cuuint64_t)page_stride * el};
     const cuuint32_t box[3] = {(cuuint32_t)(128 / el), (cuuint32_t)box_rows, 1u};
