@@ -453,7 +453,7 @@ int kda_paged_tables(const int32_t *new_len, const int32_t *ctx_len, int n_seqs,
  *   slot_map     (device) int64 [T_total]; a negative slot is skipped, one at or
  *                past n_pages * page_size is skipped and records KDA_DEVERR_PAGE;
  *                two tokens must not share a slot
- *   k_scale, v_scale (device) fp32 [Hkv], KDA_E4M3 only (else NULL), > 0
+ *   k_scale, v_scale (device) fp32 [Hkv], KDA_E4M3 only (else NULL), > 0 and finite
  *   k_cache, v_cache (device) the caches, written at the slots
  * ------------------------------------------------------------------------ */
 int kda_paged_append(const void *k, const void *v, const int64_t *slot_map, int64_t T_total, int Hkv, int D,
@@ -492,6 +492,11 @@ int kda_paged_append(const void *k, const void *v, const int64_t *slot_map, int6
  * page_size records KDA_DEVERR_LENGTHS and counts as 0 (o = 0); a page outside
  * the cache records KDA_DEVERR_PAGE and that request's outputs are undefined.
  * The result does not depend on timing: the same call gives the same bits.
+ * Roundings: o once, to dtype.  Over bf16 caches the probabilities are rounded to
+ * bf16 before their product with V, over e4m3 caches to fp16 (2^-8 and 2^-11 of
+ * each at most); the scores, their sums, the statistics, lse and o until its
+ * rounding are fp32.  Over e4m3 caches q loses what is below 2^-31 of the largest
+ * value of its row.  With dtype KDA_F32 everything is fp32.
  * ------------------------------------------------------------------------ */
 size_t kda_paged_attn_workspace_size(int64_t T_total, int n_seqs, int Hq, int Hkv);
 

@@ -22,12 +22,14 @@
 // The reference `ref` of a row's exponents follows its maximum only when that
 // has grown by more than 2^8: until then probabilities up to 256 are as precise
 // in bf16 and the sums stay in fp32, and O needs no rescaling (which would mean
-// reading and writing 128 columns of TMEM between two products).
+// reading and writing 128 columns of TMEM between two products).  Probabilities are
+// bf16 because a product's operands have one type, and V is bf16; the sums take them
+// unrounded.
 //
-// Measured: a prompt of 8,192 tokens, 16 heads over two kv heads, 223 us (1,230
+// Measured: a prompt of 8,192 tokens, 16 heads over two kv heads, 224 us (1,225
 // TFLOP/s of the pairs that the mask leaves; some tiles more are multiplied where it
-// crosses them); 2,048 tokens, 32 heads, over 65,536 keys 1,515 us (1,430 TFLOP/s, the
-// clock falling under the load); 256 windows of 60 rows 258 us (5.8 TB/s).  Bound by the
+// crosses them); 2,048 tokens, 32 heads, over 65,536 keys 1,501 to 1,541 us (1,405 to
+// 1,442 TFLOP/s, by the box: the clock falls under the load); 256 windows of 60 rows 258 us (5.8 TB/s).  Bound by the
 // products (S for 64 keys reads its operands, by their bytes, at three quarters of the
 // rate) and by what the way from S to P leaves between them.  (A share of the
 // exponentials by a polynomial made it slower, 250 to 276 us for 242 us: the special
