@@ -5,8 +5,8 @@
 // and the caller records KDA_DEVERR_TIMEOUT and leaves its loop, so no kernel
 // of this library can spin forever.  Waits on data that the block itself
 // brings in or computes use the fixed budget below; waits on flags that other
-// blocks raise, the decode's waits on its copies and the paged attention's (short
-// budgets only) take that of the launch (kda_set_wait_budget, the same by default).
+// blocks raise, and the decode's waits on its copies, take the budget of the
+// launch (kda_set_wait_budget, the same fixed value by default).
 #pragma once
 
 #include <stdint.h>
