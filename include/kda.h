@@ -86,7 +86,9 @@ enum kda_device_error {
     KDA_DEVERR_LENGTHS = 8,        /* a length of the paged calls is negative, past the block table, or the
                                       new tokens do not add up to T_total           */
     KDA_DEVERR_NO_PAGES = 16,      /* the list of free pages is too short          */
-    KDA_DEVERR_PAGE = 32           /* a page or slot outside the cache             */
+    KDA_DEVERR_PAGE = 32,          /* a page or slot outside the cache             */
+    KDA_DEVERR_TOKEN = 64,         /* a drafted token outside the vocabulary       */
+    KDA_DEVERR_PROBS = 128         /* a row of probabilities without any weight    */
 };
 
 /* Human-readable name of a kda_status. Never NULL. */
@@ -506,6 +508,127 @@ int kda_paged_attn(const void *q, const void *k_cache, const void *v_cache, cons
                    int n_pages, int page_size, int64_t page_stride, int max_blocks, float sm_scale, int window,
                    void *o, float *lse, void *workspace, size_t workspace_bytes, int32_t *error_word,
                    kda_stream_t stream);
+
+/* --------------------------------------------------------------------------
+ * kda_paged_attn_sinks -- kda_paged_attn whose window leaves the first `sinks`
+ * tokens of every request visible: the query at position p sees the keys
+ *   0 .. min(sinks, p + 1) - 1  and  max(0, p - window + 1) .. p.
+ * Everything else is as for kda_paged_attn (same workspace); sinks >= 0, and
+ * sinks without a window change nothing.  A page that holds neither a sink nor
+ * a key of some query's window is never read, and its table entry neither.
+ * ------------------------------------------------------------------------ */
+int kda_paged_attn_sinks(const void *q, const void *k_cache, const void *v_cache, const int32_t *block_table,
+                         const int32_t *cu_q, const int32_t *kv_len, int n_seqs, int64_t T_total, int max_q, int Hq,
+                         int Hkv, int D, int dtype, int cache_dtype, const float *k_scale, const float *v_scale,
+                         int n_pages, int page_size, int64_t page_stride, int max_blocks, float sm_scale, int window,
+                         int sinks, void *o, float *lse, void *workspace, size_t workspace_bytes,
+                         int32_t *error_word, kda_stream_t stream);
+
+/* ==========================================================================
+ * Rotary positions and per-head norms of queries and keys, for the same
+ * full-attention layers: kda_qk_rope alone, or kda_paged_rope_append, which also
+ * does what kda_paged_append does.
+ *
+ * Per token t and head, over the 128 channels of a row x of q or k:
+ *   1. with a weight w: x <- x / sqrt(mean(x^2) + eps) * w   (RMS norm)
+ *   2. the first rot_dim channels are rot_dim / 2 pairs; pair i at position p
+ *      is turned by the angle p f_i and multiplied by `amplitude`:
+ *        (a, b) <- amplitude (a cos - b sin, a sin + b cos)
+ *      KDA_ROPE_HALF: pair i is channels (i, i + rot_dim / 2);
+ *      KDA_ROPE_INTERLEAVED: channels (2 i, 2 i + 1)
+ * in fp32, rounded once at the end.  freq[i] is f_i in turns a position, times
+ * 2^64 (kda_rope_frequencies): position times frequency is then exact modulo a
+ * whole turn in 64-bit integers, at any position (negative ones too), and an
+ * angle is off by less than 2^-25 radians however far the position.
+ * ========================================================================== */
+enum kda_rope_layout { KDA_ROPE_HALF = 0, KDA_ROPE_INTERLEAVED = 1 };
+enum kda_rope_scaling { KDA_ROPE_NONE = 0, KDA_ROPE_LINEAR = 1, KDA_ROPE_NTK = 2, KDA_ROPE_YARN = 3 };
+
+/* --------------------------------------------------------------------------
+ * kda_rope_frequencies -- frequencies and amplitude, on the host, once per model.
+ *   f_i = base^(-2 i / rot_dim), amplitude 1, for contexts stretched by `factor` (>= 1):
+ *   KDA_ROPE_LINEAR  f_i / factor
+ *   KDA_ROPE_NTK     base * factor^(rot_dim / (rot_dim - 2)) instead of base
+ *   KDA_ROPE_YARN    f_i (g_i + (1 - g_i) / factor), where g_i goes linearly from 0 to 1
+ *                    as the pair's turns over the original length, original_len f_i / 2 pi,
+ *                    go from beta_slow to beta_fast; amplitude 0.1 ln(factor) + 1
+ *                    (Peng et al., "YaRN: Efficient Context Window Extension of Large
+ *                    Language Models", section 3)
+ *   rot_dim      a multiple of 8, 8 .. 128;  base > 1
+ *   original_len, beta_fast, beta_slow   KDA_ROPE_YARN only: > 0, beta_fast > beta_slow >= 0
+ *   freq         (host) int64 [rot_dim / 2], written;  amplitude (host), written
+ * ------------------------------------------------------------------------ */
+int kda_rope_frequencies(int rot_dim, double base, int scaling, double factor, double original_len, double beta_fast,
+                         double beta_slow, int64_t *freq, float *amplitude);
+
+/* --------------------------------------------------------------------------
+ * kda_qk_rope
+ *   q            (device) [T_total, Hq, D] dtype, tokens q_stride elements apart (>= Hq * D,
+ *                a multiple of 16 bytes), so that q and k may be parts of one projection;
+ *   k            (device) [T_total, Hkv, D], k_stride likewise
+ *   positions    (device) int32 [T_total]
+ *   freq         (device) int64 [rot_dim / 2]; rot_dim 0 (no rotation; freq and positions
+ *                may be NULL) or a multiple of 8 up to 128
+ *   amplitude    finite
+ *   q_weight, k_weight  (device) fp32 [D] or NULL: no norm
+ *   eps          >= 0
+ *   q_out, k_out (device) as q and k, with strides of their own; may be q and k themselves
+ *                (with their strides), and must not overlap the inputs otherwise
+ * q, k, q_out, k_out, the weights and freq must be 16-byte aligned.
+ * ------------------------------------------------------------------------ */
+int kda_qk_rope(const void *q, const void *k, const int32_t *positions, const int64_t *freq, float amplitude,
+                const float *q_weight, const float *k_weight, float eps, int64_t T_total, int Hq, int Hkv, int D,
+                int rot_dim, int layout, int dtype, int64_t q_stride, int64_t k_stride, void *q_out, void *k_out,
+                int64_t q_out_stride, int64_t k_out_stride, kda_stream_t stream);
+
+/* --------------------------------------------------------------------------
+ * kda_paged_rope_append -- kda_qk_rope with the keys written to their slots of the
+ * paged cache instead of k_out, beside the values v (device) [T_total, Hkv, D] (v_stride
+ * apart, as they are).  slot_map, caches, scales, page geometry and error_word as for
+ * kda_paged_append; a skipped slot's query is still written to q_out.  An e4m3 cache
+ * holds (the turned key) / scale, rounded once.
+ * ------------------------------------------------------------------------ */
+int kda_paged_rope_append(const void *q, const void *k, const void *v, const int32_t *positions,
+                          const int64_t *slot_map, const int64_t *freq, float amplitude, const float *q_weight,
+                          const float *k_weight, float eps, int64_t T_total, int Hq, int Hkv, int D, int rot_dim,
+                          int layout, int dtype, int cache_dtype, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                          void *q_out, int64_t q_out_stride, const float *k_scale, const float *v_scale, void *k_cache,
+                          void *v_cache, int n_pages, int page_size, int64_t page_stride, int32_t *error_word,
+                          kda_stream_t stream);
+
+/* --------------------------------------------------------------------------
+ * kda_verify_drafts -- how many of each request's drafted tokens stand against the
+ * target model's probabilities, and the token that follows them, by given uniform
+ * numbers.  num_accepted is what the next kda_decode_step takes.
+ * Request n with m drafts (d_0 .. d_{m-1}; p_j = target[n][j], the distribution after
+ * d_0 .. d_{j-1}; q_j = draft[n][j], the distribution that d_j was drawn from):
+ *   draft j stands when  u_j q_j(d_j) < p_j(d_j)  and all before it stand; a is their
+ *   number.  The token after them is drawn by r = uniforms[n][W-1] from
+ *     w = max(p_a - q_a, 0)   when draft a was refused (a < m; p_a where that is 0 all over),
+ *     w = p_a                 when all stood (a = m):
+ *   the lowest i with  sum_{k <= i} w_k > r sum_k w_k.
+ * Without `draft` every draft is certain: q_j = 1 at d_j and 0 elsewhere.
+ *   target       (device) [N, W, V] dtype, requests target_seq_stride and rows
+ *                target_row_stride elements apart (>= V; padded vocabularies)
+ *   draft        (device) [N, W-1, V] dtype, likewise, or NULL
+ *   draft_tokens (device) int32 [N, W-1] (may be NULL when W is 1)
+ *   uniforms     (device) fp32 [N, W], in [0, 1): u_0 .. u_{W-2}, r (r outside counts as 0
+ *                below, as the largest number under 1 above)
+ *   n_draft      (device) int32 [N], 0 .. W-1, or NULL: W-1 for all
+ *   N >= 1, 1 <= W <= 32, 1 <= V < 2^31; dtype KDA_F32 or KDA_BF16, values 0 .. 1
+ *   num_accepted (device) int32 [N], written: a
+ *   tokens       (device) int32 [N, W], written: d_0 .. d_{a-1}, the token drawn, then -1
+ * The tests are exact.  Weights are summed as multiples of 2^-60 (each rounded once),
+ * so sums do not depend on their order and the same call gives the same tokens; values below
+ * 0 or NaN count as 0, over 1 as 1.  A row that sums to 8 or more has no answer (some token).
+ * A drafted token outside 0 .. V-1 records KDA_DEVERR_TOKEN and is refused.  An n_draft out
+ * of range records KDA_DEVERR_NUM_ACCEPTED: that request gets num_accepted 0 and tokens -1.
+ * Rows without weight record KDA_DEVERR_PROBS, and the token drawn is -1.
+ * ------------------------------------------------------------------------ */
+int kda_verify_drafts(const void *target, const void *draft, const int32_t *draft_tokens, const float *uniforms,
+                      const int32_t *n_draft, int N, int W, int V, int dtype, int64_t target_seq_stride,
+                      int64_t target_row_stride, int64_t draft_seq_stride, int64_t draft_row_stride,
+                      int32_t *num_accepted, int32_t *tokens, int32_t *error_word, kda_stream_t stream);
 
 /* --------------------------------------------------------------------------
  * kda_read_device_error -- synchronise `stream` and read the device error

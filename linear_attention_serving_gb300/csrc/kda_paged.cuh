@@ -30,6 +30,10 @@ struct PagedAttn {
     int n_seqs, T, max_q, Hq, Hkv, G, page_size, n_pages, max_blocks, window;
     float scale_log2;                // sm_scale * log2(e)
     int row_lo, row_hi;              // this launch takes the requests with row_lo < rows <= row_hi
+    // Sinks (0: none; the kernels of calls with sinks are instances of their own, SINK): the first
+    // `sinks` keys, sink_tiles key tiles, stay visible beside the last `near`; `window` then is near and
+    // the sinks' tiles together (see sink_tile).
+    int near, sinks, sink_tiles;
     int box, box_log;                // keys that one copy takes from a page (a power of two, divides page_size)
     // pieces: lead[c] describes the item whose first piece block c left last;
     // slot 2 c is the piece of block c's first segment, 2 c + 1 of its last
@@ -60,6 +64,23 @@ __device__ __forceinline__ int first_seen(const PagedAttn &a, int pos) {
 __device__ __forceinline__ int window_from(const PagedAttn &a, int pos0) {
     const int64_t d = (int64_t)a.window - 1 - pos0;
     return d < (1 << 30) ? (int)d : 1 << 30;
+}
+
+// The same for the window alone, in calls with sinks.
+__device__ __forceinline__ int first_near(const PagedAttn &a, int pos) { return pos >= a.near ? pos - a.near + 1 : 0; }
+// Key tiles in calls with sinks.  What a window and sink_tiles tiles of sinks see has as many tiles as
+// a window that is wider by them, so the line is counted and cut with that wider window.  Of an item's
+// tiles base, base + 1 .. the first sink_tiles then stand for the sinks' and the others for
+// themselves; where base is 0 the window reaches the sinks, and all tiles stand for themselves.
+__device__ __forceinline__ int sink_tile(const PagedAttn &a, int base, int t) {
+    return base > 0 && t - base < a.sink_tiles ? t - base : t;
+}
+// Sets that up for tiles of `tile` keys (on the host; a.window is the window, a.sinks > 0).
+inline void sinks_of(PagedAttn &a, int tile) {
+    a.near = a.window;
+    a.sink_tiles = (a.sinks + tile - 1) / tile;
+    const int64_t wide = (int64_t)a.window + (int64_t)a.sink_tiles * tile;
+    a.window = wide >= (int64_t)a.max_blocks * a.page_size ? 0 : (int)wide;
 }
 
 // `err` collects what is wrong (only one block records it).

@@ -175,10 +175,21 @@ int kda_paged_attn(const void *q, const void *k_cache, const void *v_cache, cons
                    int n_pages, int page_size, int64_t page_stride, int max_blocks, float sm_scale, int window,
                    void *o, float *lse, void *workspace, size_t workspace_bytes, int32_t *error_word,
                    kda_stream_t stream) {
+    return kda_paged_attn_sinks(q, k_cache, v_cache, block_table, cu_q, kv_len, n_seqs, T_total, max_q, Hq, Hkv, Dm, dtype,
+                                cache_dtype, k_scale, v_scale, n_pages, page_size, page_stride, max_blocks, sm_scale, window, 0,
+                                o, lse, workspace, workspace_bytes, error_word, stream);
+}
+
+int kda_paged_attn_sinks(const void *q, const void *k_cache, const void *v_cache, const int32_t *block_table,
+                   const int32_t *cu_q, const int32_t *kv_len, int n_seqs, int64_t T_total, int max_q, int Hq,
+                   int Hkv, int Dm, int dtype, int cache_dtype, const float *k_scale, const float *v_scale,
+                   int n_pages, int page_size, int64_t page_stride, int max_blocks, float sm_scale, int window,
+                   int sinks, void *o, float *lse, void *workspace, size_t workspace_bytes, int32_t *error_word,
+                   kda_stream_t stream) {
     int rc = check_paged_cache(Hkv, Dm, dtype, cache_dtype, k_scale, v_scale, k_cache, v_cache, n_pages, page_size,
                                page_stride);
     if (rc) return rc;
-    if (Hq < Hkv || Hq % Hkv || n_seqs < 1 || max_blocks < 1 || max_q < 0 || window < 0) return KDA_ERR_INVALID_ARG;
+    if (Hq < Hkv || Hq % Hkv || n_seqs < 1 || max_blocks < 1 || max_q < 0 || window < 0 || sinks < 0) return KDA_ERR_INVALID_ARG;
     if (T_total < 0 || T_total * (Hq / Hkv) >= (int64_t)INT32_MAX / 2) return KDA_ERR_INVALID_ARG;
     // key positions are int32, with room for a tile past the end
     if ((int64_t)max_blocks * page_size > (int64_t)INT32_MAX - 65536) return KDA_ERR_INVALID_ARG;
@@ -214,6 +225,9 @@ int kda_paged_attn(const void *q, const void *k_cache, const void *v_cache, cons
     // (no position is further back than the table reaches: such a window is none, and what is left
     // stays clear of 2^31 where positions are added to it)
     a.window = window >= (int64_t)max_blocks * page_size ? 0 : window;
+    // (without a window, or where the sinks reach past the table, every key is seen)
+    if (sinks >= (int64_t)max_blocks * page_size) a.window = 0;
+    a.sinks = a.window > 0 ? sinks : 0;
     a.scale_log2 = sm_scale * 1.4426950408889634f;
     a.wait_budget = wait_budget();
     char *ws = (char *)workspace;

@@ -151,7 +151,7 @@ struct __align__(16) Seg {
     int tok, R, h, r0;
     int pos, lo, hi, t0;     // first token's position; keys seen, first key tile
     int nt, req, whole, slot;
-    int c0, c1, pad0, pad1;
+    int c0, c1, base, pad;   // base: the item's first key tile (SINK: see sink_tile; lo is the window's)
 };
 static_assert(sizeof(Seg) == 64, "segment size");
 
@@ -160,7 +160,7 @@ struct Walk {
     int req, vh, g;          // vh = kv head x parts + part
     Req q;
     bool fresh;
-    __device__ bool next(const PagedAttn &a, const Rows &w, int NR, int64_t P0, Seg &s) {
+    template <bool SINK> __device__ bool next(const PagedAttn &a, const Rows &w, int NR, int64_t P0, Seg &s) {
         while (pos < end) {
             if (fresh) {
                 while (true) {
@@ -182,6 +182,8 @@ struct Walk {
             s.R = w.parts > 1 ? min(NR, a.G - s.r0) : (j1 - j0 + 1) * a.G;
             s.tok = q.r.tok0 + j0;
             s.pos = q.r.pos0 + j0;
+            s.base = t0;
+            if (SINK) s.lo = first_near(a, s.pos);
             s.t0 = t0 + b;
             s.nt = max(0, e - b);
             s.req = req;
@@ -238,7 +240,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float x, float y) {
 // ---------------------------------------------------------------- walk, queries
 // One warp walks the line, tells the others of each segment (the loads begin on it) and
 // puts its queries (rows past R zero) into the buffer of their turn.
-template <bool E4, int NR, class Gate>
+template <bool E4, int NR, bool SINK, class Gate>
 __device__ __forceinline__ void walk_role(const PagedAttn &a, uint8_t *sm, Walk w, int64_t P0, const Gate &gate) {
     using C = Cfg<E4, NR>;
     const int lane = threadIdx.x & 31;
@@ -247,7 +249,7 @@ __device__ __forceinline__ void walk_role(const PagedAttn &a, uint8_t *sm, Walk 
     int item = 0;  // items with tiles
     for (int i = 0;; ++i) {
         Seg s;
-        const bool more = w.next(a, rw, NR, P0, s);
+        const bool more = w.next<SINK>(a, rw, NR, P0, s);
         if (!more) s.nt = -1;
         if (!gate(&bar.seg_empty[i % SEGS], ((i / SEGS) & 1) ^ 1)) return;
         if (lane == 0) {
@@ -334,7 +336,7 @@ __device__ __forceinline__ void walk_role(const PagedAttn &a, uint8_t *sm, Walk 
 // Tiles go in the order K0, K1, V0, K2, V1 .. through all items: K is used two tiles
 // before V is.  e4m3's V goes into a ring of its own, with a word that says which rows
 // hold seen keys.
-template <bool E4, int NR, class Gate>
+template <bool E4, int NR, bool SINK, class Gate>
 __device__ __forceinline__ void load_role(const PagedAttn &a, const PagedMaps &maps, uint8_t *sm, const Gate &gate) {
     using C = Cfg<E4, NR>;
     constexpr int ES = E4 ? 1 : 2, NV = E4 ? C::RS : C::VS;
@@ -354,7 +356,9 @@ __device__ __forceinline__ void load_role(const PagedAttn &a, const PagedMaps &m
     };
     // boxes f .. e - 1 of a tile: this lane's page and row
     struct Tile {
-        int f, e, page, y, z;  // z: first and one past the last row that holds a seen key (e4m3)
+        int f, e, page, y, z;  // z: first and one past the last row that holds a seen key, and sinks' rows (e4m3)
+        // (SINK: the boxes between the sinks and the window hold no seen key either; f .. e - 1 and those below s)
+        int s;
     };
     auto load = [&](const Tile &t, bool v) -> bool {
         const int slot = v ? vslot : kslot;
@@ -369,9 +373,10 @@ __device__ __forceinline__ void load_role(const PagedAttn &a, const PagedMaps &m
             ++nk;
             if (++kslot == C::KS) kslot = 0, kph ^= 1;
         }
-        if (lane == 0) mbar_expect_tx(full, (uint32_t)((t.e - t.f) << lg) * (D * ES));
+        const int boxes = SINK ? max(0, t.e - max(t.f, t.s)) + min(t.s, t.e) : t.e - t.f;
+        if (lane == 0) mbar_expect_tx(full, (uint32_t)(boxes << lg) * (D * ES));
         __syncwarp();
-        if (lane >= t.f && lane < t.e) {
+        if ((lane >= t.f || (SINK && lane < t.s)) && lane < t.e) {
             const CUtensorMap *m = v ? &maps.v : &maps.k;
             tma_load_3d(dst + (lane << lg) * 128, m, 0, t.y, t.page, full);
             if (!E4) tma_load_3d(dst + TILE / 2 + (lane << lg) * 128, m, 64, t.y, t.page, full);
@@ -381,7 +386,7 @@ __device__ __forceinline__ void load_role(const PagedAttn &a, const PagedMaps &m
     };
     Seg s;
     int iseg = 0;
-    Tile prev{0, 0, 0, 0, 0};
+    Tile prev{0, 0, 0, 0, 0, 0};
     bool have = false;
     while (next_seg<C>(sm, bar, iseg, gate, s)) {
         if (s.nt == 0) {
@@ -395,13 +400,13 @@ __device__ __forceinline__ void load_role(const PagedAttn &a, const PagedMaps &m
         int cbase = 0, page = 0, off = 0;
         const int lob = s.lo & ~(box - 1);  // boxes before this one hold no seen key (their pages may be gone)
         for (int j = 0; j < s.nt; ++j) {
-            const int key0 = (s.t0 + j) * BK, b0 = key0 >> lg;
+            const int key0 = (SINK ? sink_tile(a, s.base, s.t0 + j) : s.t0 + j) * BK, b0 = key0 >> lg;
             if (j == 0 || b0 + nbx > cbase + 32) {  // pages of the next 32 boxes, one per lane
                 cbase = b0;
                 const int key = (cbase + lane) << lg, blk = key / a.page_size;
                 page = 0;
                 off = s.h * a.page_size + key - blk * a.page_size;
-                if (key >= lob && key < s.hi) {
+                if ((key >= lob || (SINK && key < a.sinks)) && key < s.hi) {
                     page = a.table[(int64_t)s.req * a.max_blocks + blk];
                     if (page < 0 || page >= a.n_pages) {
                         if (a.err) atomicOr(a.err, KDA_DEVERR_PAGE);
@@ -415,6 +420,11 @@ __device__ __forceinline__ void load_role(const PagedAttn &a, const PagedMaps &m
             t.page = __shfl_sync(0xffffffffu, page, (b0 - cbase + lane) & 31);
             t.y = __shfl_sync(0xffffffffu, off, (b0 - cbase + lane) & 31);
             t.z = max(0, s.lo - key0) | (min(BK, s.hi - key0) << 8);
+            if (SINK) {
+                const int n = max(0, min(BK, a.sinks - key0));
+                t.s = (n + box - 1) >> lg;
+                t.z = max(0, min(BK, s.lo - key0)) | (min(BK, s.hi - key0) << 8) | (n << 16);
+            }
             if (!load(t, false)) return drain(NV);
             if (have && !load(prev, true)) return drain(NV);
             prev = t;
@@ -437,7 +447,7 @@ __device__ __forceinline__ void load_role(const PagedAttn &a, const PagedMaps &m
 // ---------------------------------------------------------------- widening
 // V from e4m3 to fp16, 32 WIDEN / 128 threads to a row.  Rows that no seen key stands in
 // become zeros (0 x NaN is NaN).
-template <int NR, class Gate>
+template <int NR, bool SINK, class Gate>
 __device__ __forceinline__ void widen_role(uint8_t *sm, const Gate &gate) {
     using C = Cfg<true, NR>;
     constexpr int W = 32 / C::WIDEN;  // 16-byte pieces of a row for one thread: 8 of them to a row
@@ -455,7 +465,7 @@ __device__ __forceinline__ void widen_role(uint8_t *sm, const Gate &gate) {
         uint4 w[W];
 #pragma unroll
         for (int i = 0; i < W; ++i) w[i] = *reinterpret_cast<const uint4 *>(src + (((p0 + i) ^ x) << 4));
-        if (row < (z & 255) || row >= (z >> 8)) {
+        if (SINK ? (row < (z & 255) && row >= (z >> 16)) || row >= ((z >> 8) & 255) : row < (z & 255) || row >= (z >> 8)) {
 #pragma unroll
             for (int i = 0; i < W; ++i) w[i] = make_uint4(0, 0, 0, 0);
         }
@@ -684,7 +694,7 @@ __device__ __forceinline__ void tmem_row(uint32_t taddr, float *o) {
 // that runs out is passed on at the group's next meeting (every segment begins with one,
 // every meeting looks for it), so that a group's warps leave together; the groups wait
 // for each other with bounded waits only.
-template <bool E4, int NR, class Gate>
+template <bool E4, int NR, bool SINK, class Gate>
 __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, uint32_t tmem, const Gate &gate) {
     using C = Cfg<E4, NR>;
     const Bars<C> bar(sm);
@@ -710,22 +720,24 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
         const int nt = sg->nt;
         if (nt < 0) return;
         const float *sc = reinterpret_cast<const float *>(sm + C::OFF_SC) + (iseg % SEGS) * NR;
-        const int lo = sg->lo, hi = sg->hi, t0 = sg->t0, pos = sg->pos, R = sg->R, r0 = sg->r0;
+        const int lo = sg->lo, hi = sg->hi, t0 = sg->t0, pos = sg->pos, R = sg->R, r0 = sg->r0, base = SINK ? sg->base : 0;
         const uint32_t to = tmem + lanes + 2 * NR + (item & 1) * 2 * NR;  // + NR g
         float l[NR], top = -INFINITY;  // sums of this thread's keys; row tid's maximum at the last change of ref
 #pragma unroll
         for (int r = 0; r < NR; ++r) l[r] = 0.f;
         int mine = 0;
         for (int j = (n & 1) ^ g; j < nt; j += 2, ++k, ++mine) {
-            const int key0 = (t0 + j) * BK, key = key0 + tid;
+            const int key0 = (SINK ? sink_tile(a, base, t0 + j) : t0 + j) * BK, key = key0 + tid;
             if (!gate(&bar.s_full[g], k & 1)) failed = true;
             tc_fence_after();
             float t[NR];
             // scores; -inf where a row does not see this key (rows that do: [first, last))
             auto scores = [&]() {
                 tmem_row<NR>(ts, t);
-                if (key0 + BK - 1 > pos || key0 + BK > hi || a.window > 0) {
-                    const int d = min(max(key - pos, 0), NR + 1), u = a.window > 0 ? min(max(key - pos + a.window, 0), NR + 1) : NR + 1;
+                if (key0 + BK - 1 > pos || key0 + BK > hi || SINK || a.window > 0) {
+                    const int window = SINK ? a.near : a.window;
+                    const bool far = SINK ? key >= a.sinks : window > 0;  // (a key that leaves the window)
+                    const int d = min(max(key - pos, 0), NR + 1), u = far ? min(max(key - pos + window, 0), NR + 1) : NR + 1;
                     const int first = key < hi ? d * G - r0 : NR, last = u > NR ? NR : u * G - r0;
 #pragma unroll
                     for (int r = 0; r < NR; ++r) t[r] = r >= first && r < last ? t[r] : -INFINITY;
@@ -821,7 +833,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
                     make_uint4(p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]);
             if (!E4) {
                 // a row of V that no seen key stands in may hold anything: zero it (0 x NaN is NaN)
-                const bool none = key >= hi || key < lo;
+                const bool none = key >= hi || (key < lo && !(SINK && key < a.sinks));
                 if (__any_sync(0xffffffffu, none)) {
                     const int v = n + j;
                     if (!gate(&bar.v_full[v % C::VS], (v / C::VS) & 1)) failed = true;
@@ -935,7 +947,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
     }
 }
 
-template <bool E4, int NR, bool SHORT>
+template <bool E4, int NR, bool SHORT, bool SINK>
 __global__ void __launch_bounds__(Cfg<E4, NR>::THREADS, 1)
     paged_few_kernel(const __grid_constant__ PagedMaps maps, const __grid_constant__ PagedAttn a, int min_per) {
     using C = Cfg<E4, NR>;
@@ -1010,13 +1022,13 @@ __global__ void __launch_bounds__(Cfg<E4, NR>::THREADS, 1)
     const uint32_t tmem = sh->tmem;
     const Waits<SHORT> gate{&sh->abort, a.err, a.wait_budget};
     if (warp < C::SOFT) {
-        softmax_role<E4, NR>(a, sm, tmem, gate);
+        softmax_role<E4, NR, SINK>(a, sm, tmem, gate);
     } else if (warp == C::W_S) {
         s_role<E4, NR>(sm, tmem, gate);
     } else if (warp == C::W_O) {
         o_role<E4, NR>(sm, tmem, gate);
     } else if (warp == C::W_LOAD) {
-        load_role<E4, NR>(a, maps, sm, gate);
+        load_role<E4, NR, SINK>(a, maps, sm, gate);
     } else if (warp == C::W_WALK) {
         Walk w;
         w.pos = line.P0;
@@ -1027,9 +1039,9 @@ __global__ void __launch_bounds__(Cfg<E4, NR>::THREADS, 1)
         w.vh = sh->vh;
         w.g = sh->g;
         w.fresh = true;
-        walk_role<E4, NR>(a, sm, w, line.P0, gate);
+        walk_role<E4, NR, SINK>(a, sm, w, line.P0, gate);
     } else {
-        if constexpr (E4) widen_role<NR>(sm, gate);
+        if constexpr (E4) widen_role<NR, SINK>(sm, gate);
     }
     tc_fence_before();
     __syncthreads();
@@ -1039,18 +1051,20 @@ __global__ void __launch_bounds__(Cfg<E4, NR>::THREADS, 1)
     }
 }
 
-template <bool E4, int NR, bool SHORT>
+template <bool E4, int NR, bool SHORT, bool SINK>
 int launch_for(const PagedAttn &a, const PagedMaps &maps, cudaStream_t s) {
     using C = Cfg<E4, NR>;
-    const int rc = prepare_kernel((const void *)paged_few_kernel<E4, NR, SHORT>, C::SMEM, C::THREADS, nullptr);
+    const int rc = prepare_kernel((const void *)paged_few_kernel<E4, NR, SHORT, SINK>, C::SMEM, C::THREADS, nullptr);
     if (rc) return rc;
-    paged_few_kernel<E4, NR, SHORT><<<paged_few_blocks(), C::THREADS, C::SMEM, s>>>(maps, a, 3);
+    paged_few_kernel<E4, NR, SHORT, SINK><<<paged_few_blocks(), C::THREADS, C::SMEM, s>>>(maps, a, 3);
     note_launch("paged_few", s);
     return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 template <bool E4, int NR>
 int launch(const PagedAttn &a, const PagedMaps &maps, cudaStream_t s) {
-    return a.wait_budget < SHORT_BUDGET ? launch_for<E4, NR, true>(a, maps, s) : launch_for<E4, NR, false>(a, maps, s);
+    const bool brief = a.wait_budget < SHORT_BUDGET;
+    if (a.sinks > 0) return brief ? launch_for<E4, NR, true, true>(a, maps, s) : launch_for<E4, NR, false, true>(a, maps, s);
+    return brief ? launch_for<E4, NR, true, false>(a, maps, s) : launch_for<E4, NR, false, false>(a, maps, s);
 }
 
 }  // namespace
@@ -1066,6 +1080,7 @@ int launch_paged_few(PagedAttn a, int cache_dtype, const void *k, const void *v,
     PagedMaps maps;
     const int rc = make_paged_maps(k, v, cache_dtype, a.Hkv, a.page_size, a.n_pages, page_stride, box, &maps);
     if (rc) return rc;
+    if (a.sinks > 0) sinks_of(a, BK);
     const bool e4 = cache_dtype == KDA_E4M3;
     if (max_rows <= 16) return e4 ? launch<true, 16>(a, maps, s) : launch<false, 16>(a, maps, s);
     return e4 ? launch<true, 32>(a, maps, s) : launch<false, 32>(a, maps, s);

@@ -31,8 +31,8 @@ constexpr int HALF = 8192;                   // bytes of K (and of V) of one til
 constexpr int STAGE = 2 * HALF;
 // CONS: consumer warps, eight, or four in calls of up to 8 rows (45 us instead of 48 then for
 // one token of 16 requests: fewer pieces to merge, fewer warps to give a tile back)
-template <int CONS_, bool SHORT_> struct Cfg {
-    static constexpr bool SHORT = SHORT_;
+template <int CONS_, bool SHORT_, bool SINK_> struct Cfg {
+    static constexpr bool SHORT = SHORT_, SINK = SINK_;
     static constexpr int CONS = CONS_, THREADS = (CONS + 1) * 32;
     static constexpr int OFF_RED = STAGES * STAGE;                 // [CONS][RW][128] fp32
     static constexpr int OFF_P = OFF_RED + CONS * RW * D * 4;      // probabilities [CONS][RW][16]
@@ -55,7 +55,7 @@ constexpr int NSUB = D * 4 / 128;            // 128-byte pieces of a row, each a
 // what the producer says about a tile
 struct __align__(16) Desc {
     int flags, ord, wr, key0, kvalid, tok0, h, r0, R, pos0, slot, c0, c1, rpw;  // rpw: rows of a warp
-    int kfirst, pad;         // the tile's rows [kfirst, kvalid) hold keys that the item sees
+    int kfirst, ksink;       // the tile's rows [kfirst, kvalid), and [0, ksink), hold keys that the item sees
 };
 static_assert(sizeof(Desc) == 64, "descriptor size");
 constexpr int FIRST = 1, LAST = 2, WHOLE = 4, END = 8, MASK = 16;
@@ -153,6 +153,8 @@ __device__ __forceinline__ void produce(const PagedAttn &a, const PagedMaps &map
         const int r0 = g * grp, R = min(grp, r.rows - r0);
         const int posf = r.pos0 + r0 / a.G, posl = r.pos0 + (r0 + R - 1) / a.G;
         const int lo = first_seen(a, posf), hi = posl + 1;  // keys that the group sees
+        const int near = C::SINK ? first_near(a, posf) : lo, base = lo / TK;  // (SINK: lo counts the sinks in)
+        auto key_of = [&](int t) { return C::SINK ? sink_tile(a, base, r.k0 / TK + t) * TK : r.k0 + t * TK; };
         int tb = t_begin, te = t_end;
         if (hi <= lo) {
             te = tb;
@@ -178,7 +180,7 @@ __device__ __forceinline__ void produce(const PagedAttn &a, const PagedMaps &map
                 d.flags = FIRST | LAST | MASK | whole;
                 d.ord = 0;
                 d.key0 = 0;
-                d.kvalid = d.kfirst = 0;
+                d.kvalid = d.kfirst = d.ksink = 0;
                 *reinterpret_cast<Desc *>(sm + C::OFF_DESC + stage * 64) = d;
                 mbar_arrive(&full[stage]);
             }
@@ -188,7 +190,7 @@ __device__ __forceinline__ void produce(const PagedAttn &a, const PagedMaps &map
         for (int t = tb; t < te; ++t) {
             if (t == tb || t >= cbase + 32) {  // pages of the next 32 tiles, one per lane
                 cbase = t;
-                const int key = r.k0 + (cbase + lane) * TK, blk = key / a.page_size;
+                const int key = key_of(cbase + lane), blk = key / a.page_size;
                 page = 0;
                 off = h * a.page_size + key - blk * a.page_size;
                 if (key < hi) {
@@ -199,16 +201,18 @@ __device__ __forceinline__ void produce(const PagedAttn &a, const PagedMaps &map
                     }
                 }
             }
-            const int key0 = r.k0 + t * TK, kvalid = min(TK, hi - key0);
+            const int key0 = key_of(t), kvalid = min(TK, hi - key0);
             const int pg = __shfl_sync(0xffffffffu, page, t - cbase), y = __shfl_sync(0xffffffffu, off, t - cbase);
             if (!next_stage()) return;
             if (lane == 0) {
                 d.flags = (t == tb ? FIRST : 0) | (t == te - 1 ? LAST : 0) | whole;
-                if (kvalid < TK || key0 + TK - 1 > posf || (a.window > 0 && key0 <= posl - a.window)) d.flags |= MASK;
+                if (kvalid < TK || key0 + TK - 1 > posf || (C::SINK ? key0 <= posl - a.near : a.window > 0 && key0 <= posl - a.window))
+                    d.flags |= MASK;
                 d.ord = t - tb;
                 d.key0 = key0;
                 d.kvalid = kvalid;
-                d.kfirst = max(0, lo - key0);
+                d.kfirst = max(0, near - key0);
+                if (C::SINK) d.ksink = max(0, min(TK, a.sinks - key0));
                 *reinterpret_cast<Desc *>(sm + C::OFF_DESC + stage * 64) = d;
                 mbar_expect_tx(&full[stage], 2 * HALF);
                 load_tile(sm + stage * STAGE, &maps.k, y, pg, &full[stage]);
@@ -238,7 +242,8 @@ __device__ __forceinline__ void produce(const PagedAttn &a, const PagedMaps &map
 struct RowsF32 {
     float o[RW][4], m, l;
     // RM: rows that the code is laid out for (R <= RM)
-    template <int RM>
+    // window: calls with sinks, the window beside them
+    template <int RM, bool SINK>
     __device__ __forceinline__ void tile(const float *q, float *ps, const uint8_t *k, const uint8_t *v, int lane, int R, float sc,
                                          const Desc &d, int row0, int G, int window, bool mask) {
         const int key = lane & 15, hf = lane >> 4;
@@ -278,7 +283,7 @@ struct RowsF32 {
 #pragma unroll
             for (int r = 0; r < RM; ++r) {
                 const int pos = d.pos0 + (row0 + r) / G, at = d.key0 + key;
-                if (!(at <= pos && (window <= 0 || at > pos - window) && key < d.kvalid)) s[r] = -INFINITY;
+                if (!(at <= pos && ((!SINK && window <= 0) || at > pos - window || (SINK && key < d.ksink)) && key < d.kvalid)) s[r] = -INFINITY;
             }
         }
 #pragma unroll
@@ -345,7 +350,18 @@ __device__ __forceinline__ void zero_outside(uint8_t *vt, int kfirst, int kvalid
     __syncwarp();
 }
 
-struct Work {
+// The same where rows [0, ksink) are seen too.
+__device__ __forceinline__ void zero_between(uint8_t *vt, int ksink, int kfirst, int kvalid, int lane) {
+    for (int x = lane; x < TK * NSUB * 8; x += 32) {
+        const int row = x / (NSUB * 8), c = x % (NSUB * 8);
+        if (row >= kvalid || (row >= ksink && row < kfirst))
+            *reinterpret_cast<uint4 *>(vt + (c >> 3) * TK * 128 + row * 128 + ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
+    }
+    fence_async_smem();
+    __syncwarp();
+}
+
+template <bool SINK> struct Work {
     RowsF32 w;
     __device__ __forceinline__ void begin(const PagedAttn &a, const Desc &d, int wrow, int lane, float *q) {
         w.m = -INFINITY;
@@ -373,13 +389,14 @@ struct Work {
                                          const float *q, float *ps) {
         const int R = min(d.rpw, d.R - d.rpw * wrow), row0 = d.r0 + d.rpw * wrow;
         const bool mask = d.flags & MASK;
+        const int window = SINK ? a.near : a.window;
         if (R <= 0) return;  // (a last, short row group)
         if (R == 1)
-            w.tile<1>(q, ps, kt, vt, lane, R, a.scale_log2, d, row0, a.G, a.window, mask);
+            w.template tile<1, SINK>(q, ps, kt, vt, lane, R, a.scale_log2, d, row0, a.G, window, mask);
         else if (R <= 4)
-            w.tile<4>(q, ps, kt, vt, lane, R, a.scale_log2, d, row0, a.G, a.window, mask);
+            w.template tile<4, SINK>(q, ps, kt, vt, lane, R, a.scale_log2, d, row0, a.G, window, mask);
         else
-            w.tile<RW>(q, ps, kt, vt, lane, R, a.scale_log2, d, row0, a.G, a.window, mask);
+            w.template tile<RW, SINK>(q, ps, kt, vt, lane, R, a.scale_log2, d, row0, a.G, window, mask);
     }
     __device__ __forceinline__ void end(int lane, float *red, float2 *ml) {
         if (lane < RW) ml[lane] = make_float2(w.m, w.l);
@@ -399,7 +416,7 @@ __device__ __forceinline__ void consume(const PagedAttn &a, uint8_t *sm) {
     float *ps = reinterpret_cast<float *>(sm + C::OFF_P) + warp * RW * 16;
     float2 *ml = reinterpret_cast<float2 *>(sm + C::OFF_ML);
 
-    Work work;
+    Work<C::SINK> work;
     int stage = 0, phase = 0;
     uint64_t *meet = reinterpret_cast<uint64_t *>(sm + C::OFF_MEET);
     int meet_phase = 0;
@@ -441,7 +458,11 @@ __device__ __forceinline__ void consume(const PagedAttn &a, uint8_t *sm) {
         if (d.flags & FIRST) work.begin(a, d, wrow, lane, mine);
         if ((d.ord & (wk - 1)) == wpart && d.kvalid > 0) {
             uint8_t *kt = sm + stage * STAGE, *vt = kt + HALF;
-            if (d.kfirst > 0 || d.kvalid < TK) zero_outside(vt, d.kfirst, d.kvalid, lane);
+            if constexpr (C::SINK) {
+                if (d.kfirst > d.ksink || d.kvalid < TK) zero_between(vt, d.ksink, d.kfirst, d.kvalid, lane);
+            } else if (d.kfirst > 0 || d.kvalid < TK) {
+                zero_outside(vt, d.kfirst, d.kvalid, lane);
+            }
             work.tile(a, d, wrow, lane, kt, vt, mine, ps);
         }
         __syncwarp();
@@ -537,8 +558,13 @@ int launch_paged_rows(PagedAttn a, const void *k, const void *v, int64_t page_st
     const int rc = make_paged_row_maps(k, v, a.Hkv, a.page_size, a.n_pages, page_stride, TK, &maps);
     if (rc) return rc;
     const bool brief = a.wait_budget < SHORT_BUDGET, few = (int64_t)a.max_q * a.G <= RW;
-    if (brief) return few ? launch<Cfg<4, true>>(a, maps, s) : launch<Cfg<8, true>>(a, maps, s);
-    return few ? launch<Cfg<4, false>>(a, maps, s) : launch<Cfg<8, false>>(a, maps, s);
+    if (a.sinks > 0) {
+        sinks_of(a, TK);
+        if (brief) return few ? launch<Cfg<4, true, true>>(a, maps, s) : launch<Cfg<8, true, true>>(a, maps, s);
+        return few ? launch<Cfg<4, false, true>>(a, maps, s) : launch<Cfg<8, false, true>>(a, maps, s);
+    }
+    if (brief) return few ? launch<Cfg<4, true, false>>(a, maps, s) : launch<Cfg<8, true, false>>(a, maps, s);
+    return few ? launch<Cfg<4, false, false>>(a, maps, s) : launch<Cfg<8, false, false>>(a, maps, s);
 }
 
 }  // namespace kda

@@ -136,6 +136,7 @@ struct __align__(16) Seg {
     int h, pos;              // kv head, first token's position
     int lo, hi, t0, nt;      // keys seen, first key tile of the segment, its tiles (0: nothing to read)
     int req, alt, whole, slot, c0, c1, half;  // half of Q's buffer (alt)
+    int base;                // the item's first key tile (SINK: see sink_tile; lo is the window's)
 };
 static_assert(sizeof(Seg) == 64, "segment size");
 
@@ -146,7 +147,7 @@ struct Walk {
     int req, h, g, alts;
     TileReq q;
     bool fresh;
-    __device__ bool next(const PagedAttn &a, int th, int64_t P0, Seg &s) {
+    template <bool SINK> __device__ bool next(const PagedAttn &a, int th, int64_t P0, Seg &s) {
       while (true) {
         if (pos >= end) return false;
         if (fresh) {
@@ -172,6 +173,8 @@ struct Walk {
         s.ntok = j1 - j0 + 1;
         s.h = h;
         s.pos = q.r.pos0 + j0;
+        s.base = t0;
+        if (SINK) s.lo = first_near(a, s.pos);
         s.req = req;
         s.whole = b == 0 && stop == B;
         s.slot = 2 * vb + (pos == P0 ? 0 : 1);
@@ -285,7 +288,7 @@ struct Shared {
 // One warp walks the line ahead of the others, and has each segment's queries
 // loaded; a segment with nt < 0 ends it.  Items of one half take the two halves of
 // the buffer in turn, so the next one's queries arrive while this one is worked on.
-template <class Gate>
+template <bool SINK, class Gate>
 __device__ __forceinline__ void walk_role(const PagedAttn &a, const CUtensorMap &qmap, uint8_t *sm, Walk w, int th, int64_t P0,
                                           int64_t total, const Gate &gate) {
     const int lane = threadIdx.x & 31;
@@ -298,14 +301,14 @@ __device__ __forceinline__ void walk_role(const PagedAttn &a, const CUtensorMap 
     };
     for (int i = 0;; ++i) {
         Seg s;
-        bool more = w.next(a, th, P0, s);
+        bool more = w.next<SINK>(a, th, P0, s);
         while (!more) {  // the block's next part, if there is one
             P0 += gridDim.x * w.per;
             if (P0 >= total) break;
             w.vb += gridDim.x;
             w.end = P0 + w.per < total ? P0 + w.per : total;
             walk_to(a, w, th, P0);
-            more = w.next(a, th, P0, s);
+            more = w.next<SINK>(a, th, P0, s);
         }
         if (!more) s.nt = -1;
         bool ok = gate(&bar.seg_empty[i % SEGS], ((i / SEGS) & 1) ^ 1);
@@ -346,7 +349,7 @@ __device__ __forceinline__ bool next_seg(uint8_t *sm, const Bars &bar, int &i, c
 
 // ---------------------------------------------------------------- loads
 // Keys and values.
-template <class Gate>
+template <bool SINK, class Gate>
 __device__ __forceinline__ void load_role(const PagedAttn &a, const PagedMaps &maps, uint8_t *sm, const Gate &gate) {
     const int lane = threadIdx.x & 31;
     const Bars bar(sm);
@@ -367,13 +370,13 @@ __device__ __forceinline__ void load_role(const PagedAttn &a, const PagedMaps &m
         const int lob = s.lo & ~(box - 1);  // boxes before this one hold no seen key (their pages may be gone)
         // one K or V tile
         auto tile = [&](int j, bool v) -> bool {
-            const int key0 = (s.t0 + j) * BK, b0 = key0 >> lg;
+            const int key0 = (SINK ? sink_tile(a, s.base, s.t0 + j) : s.t0 + j) * BK, b0 = key0 >> lg;
             if (cbase < 0 || b0 < cbase || b0 + nbx > cbase + 32) {  // pages of the next 32 boxes, one per lane
                 cbase = b0;
                 const int key = (cbase + lane) << lg, blk = key / a.page_size;
                 page = 0;
                 off = s.h * a.page_size + key - blk * a.page_size;
-                if (key >= lob && key < s.hi) {
+                if ((key >= lob || (SINK && key < a.sinks)) && key < s.hi) {
                     page = a.table[(int64_t)s.req * a.max_blocks + blk];
                     if (page < 0 || page >= a.n_pages) {
                         if (a.err) atomicOr(a.err, KDA_DEVERR_PAGE);
@@ -384,11 +387,15 @@ __device__ __forceinline__ void load_role(const PagedAttn &a, const PagedMaps &m
             const int slot = ring;
             if (!gate(&bar.kv_empty[slot], ringp ^ 1)) return false;
             const int f = max(0, (lob - key0) >> lg), e = min(nbx, (s.hi - key0 + box - 1) >> lg);
-            if (lane == 0) mbar_expect_tx(&bar.kv_full[slot], (uint32_t)((e - f) << lg) * (D * 2));
+            // (SINK: the boxes between the sinks and the window hold no seen key either)
+            const int key = key0 + (lane << lg);
+            const bool on = SINK ? lane < e && (lane >= f || key < a.sinks) : lane >= f && lane < e;
+            const int boxes = SINK ? __popc(__ballot_sync(0xffffffffu, on)) : e - f;
+            if (lane == 0) mbar_expect_tx(&bar.kv_full[slot], (uint32_t)(boxes << lg) * (D * 2));
             __syncwarp();
             const int pg = __shfl_sync(0xffffffffu, page, (b0 - cbase + lane) & 31);
             const int y = __shfl_sync(0xffffffffu, off, (b0 - cbase + lane) & 31);
-            if (lane >= f && lane < e) {
+            if (on) {
                 uint8_t *dst = sm + OFF_KV + slot * SLOT + (lane << lg) * 128;
                 const CUtensorMap *m = v ? &maps.v : &maps.k;
                 tma_load_3d(dst, m, 0, y, pg, &bar.kv_full[slot]);
@@ -595,7 +602,7 @@ __device__ __forceinline__ void finish(const PagedAttn &a, uint32_t to, int th, 
 
 // Two threads, of two warps that meet at a barrier of their own, share a row.  A
 // wait that runs out is passed on at the next meeting, so both leave together.
-template <class Gate>
+template <bool SINK, class Gate>
 __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, uint32_t tmem, int th, const Gate &gate) {
     constexpr int HK = BK / 4;  // keys of one thread: a half of half a tile
     const Bars bar(sm);
@@ -618,13 +625,14 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
         struct {
             int lo, hi, t0, nt;
         } s{seg->lo, seg->hi, seg->t0, seg->nt};
+        const int base = SINK ? seg->base : 0;
         if (s.nt < 0) {
             meet_count<64>(id, false);
             return;
         }
         const bool alt = seg->alt;
         const int pos = seg->pos + (alt ? 0 : x) * th + row / a.G;
-        const int first_key = first_seen(a, pos);  // keys first_key .. pos, all below hi
+        const int first_key = SINK ? first_near(a, pos) : first_seen(a, pos);  // keys first_key .. pos, all below hi
         float ref = 0.f, l = 0.f, top = -INFINITY;  // (top: of all the row's keys at the last change of ref, then of this half's)
         // ref follows the maximum once that has passed this (never for the half's rows past the
         // item's tokens: they hold the next request's queries, or what was there before)
@@ -635,7 +643,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
         for (int e = 0; e < ne; ++e) {
             const int j = e >> 1, u = e & 1, b = 2 * x + u, ph = (n + j) & 1;
             const uint32_t ts = tmem + lanes + COL_S + x * 128 + u * 64 + HK * hf;  // this thread's scores, and P
-            const int key0 = (s.t0 + j) * BK + u * (BK / 2);
+            const int key0 = (SINK ? sink_tile(a, base, s.t0 + j) : s.t0 + j) * BK + u * (BK / 2);
             if (!gate(&bar.s_full[b], ph)) failed = true;
             tc_fence_after();
             float v[HK];
@@ -643,9 +651,10 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
             tmem_arrived(v);
             // of this thread's keys, the row sees [c0, c1)
             const int c1 = min(pos + 1, s.hi) - key0 - HK * hf, c0 = first_key - key0 - HK * hf;
-            if (__any_sync(0xffffffffu, c1 < HK || c0 > 0)) {
+            const int cs = SINK ? a.sinks - key0 - HK * hf : 0;  // and [0, cs)
+            if (__any_sync(0xffffffffu, c1 < HK || (c0 > 0 && cs < HK))) {
 #pragma unroll
-                for (int c = 0; c < HK; ++c) v[c] = c < c1 && c >= c0 ? v[c] : -INFINITY;
+                for (int c = 0; c < HK; ++c) v[c] = c < c1 && (c >= c0 || (SINK && c < cs)) ? v[c] : -INFINITY;
             }
             float m0 = max3(v[0], v[1], v[2]), m1 = max3(v[3], v[4], v[5]), m2 = max3(v[6], v[7], v[8]), m3 = max3(v[9], v[10], v[11]);
 #pragma unroll
@@ -693,14 +702,14 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
             }
             // rows of V that no key seen by this item stands in may hold anything: zero
             // them (0 x NaN is NaN); each group before its own product
-            const int z0 = max(0, s.lo - key0), z1 = min(BK, s.hi - key0);
-            if (u == 0 && (z0 > 0 || z1 < BK)) {
+            const int z0 = max(0, s.lo - key0), z1 = min(BK, s.hi - key0), zs = SINK ? a.sinks - key0 : 0;
+            if (u == 0 && ((z0 > 0 && zs < BK) || z1 < BK)) {
                 const uint32_t q = seq0 + 2 * j + 1;
                 if (!gate(&bar.kv_full[q % SLOTS], (int)((q / SLOTS) & 1))) failed = true;
                 uint8_t *vt = sm + OFF_KV + (q % SLOTS) * SLOT;
                 for (int w = threadIdx.x & (2 * BM - 1); w < BK * 16; w += 2 * BM) {
                     const int r = w >> 4, c = w & 15;
-                    if (r < z0 || r >= z1)
+                    if ((r < z0 && r >= zs) || r >= z1)
                         *reinterpret_cast<uint4 *>(vt + (c >> 3) * (SLOT / 2) + r * 128 + ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
                 }
                 fence_async_smem();
@@ -751,7 +760,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
     }
 }
 
-template <bool SHORT>
+template <bool SHORT, bool SINK>
 __global__ void __launch_bounds__(THREADS, 1)
     paged_tile_kernel(const __grid_constant__ PagedMaps maps, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ PagedAttn a, int th,
                       int min_per, int max_parts) {
@@ -823,12 +832,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t tmem = sh->tmem;
     const Waits<SHORT> gate{&sh->abort, a.err, a.wait_budget};
     if (warp < SOFT) {
-        softmax_role(a, sm, tmem, th, gate);
+        softmax_role<SINK>(a, sm, tmem, th, gate);
     } else {
         if (warp < SOFT + 2)
             mma_role(sm, tmem, warp - SOFT, gate);
         else if (warp == SOFT + 2)
-            load_role(a, maps, sm, gate);
+            load_role<SINK>(a, maps, sm, gate);
         else {
             Walk w;
             w.end = P1;
@@ -836,7 +845,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             w.vb = blockIdx.x;
             w.alts = 0;
             walk_from(a, w, th, P0, line.req, line.before, line.units);
-            walk_role(a, qmap, sm, w, th, P0, line.total, gate);
+            walk_role<SINK>(a, qmap, sm, w, th, P0, line.total, gate);
         }
     }
     tc_fence_before();
@@ -865,7 +874,10 @@ int launch_paged_tile(PagedAttn a, const void *k, const void *v, int64_t page_st
     int rc = make_paged_maps(k, v, KDA_BF16, a.Hkv, a.page_size, a.n_pages, page_stride, box, &maps);
     if (rc) return rc;
     if ((rc = make_paged_q_map(a.q, a.T, a.Hq, a.G, th, &qmap))) return rc;
-    const auto kernel = a.wait_budget < SHORT_BUDGET ? paged_tile_kernel<true> : paged_tile_kernel<false>;
+    const bool brief = a.wait_budget < SHORT_BUDGET, sink = a.sinks > 0;
+    if (sink) sinks_of(a, BK);
+    const auto kernel = sink ? (brief ? paged_tile_kernel<true, true> : paged_tile_kernel<false, true>)
+                             : (brief ? paged_tile_kernel<true, false> : paged_tile_kernel<false, false>);
     if ((rc = prepare_kernel((const void *)kernel, SMEM, THREADS, nullptr))) return rc;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(paged_tile_blocks());

@@ -22,8 +22,11 @@ namespace {
 
 decltype(&kda_paged_tables) f_tables = nullptr;
 decltype(&kda_paged_append) f_append = nullptr;
-decltype(&kda_paged_attn) f_attn = nullptr;
+decltype(&kda_paged_attn_sinks) f_attn = nullptr;
 decltype(&kda_paged_attn_workspace_size) f_workspace = nullptr;
+decltype(&kda_qk_rope) f_rope = nullptr;
+decltype(&kda_paged_rope_append) f_rope_append = nullptr;
+decltype(&kda_verify_drafts) f_verify = nullptr;
 
 constexpr int64_t HEAD = 128;
 
@@ -196,10 +199,11 @@ PyObject *append(PyObject *, PyObject *const *args, Py_ssize_t n_args) {
     });
 }
 
-// attn(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q, sm_scale, window, k_scale, v_scale, out, lse, workspace, error_word)
+// attn(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q, sm_scale, window, k_scale, v_scale, out, lse, workspace, error_word,
+// sinks)
 PyObject *attn(PyObject *, PyObject *const *args, Py_ssize_t n_args) {
     return guarded([&]() -> PyObject * {
-        if (n_args != 15 || !f_attn) throw No();
+        if (n_args != 16 || !f_attn) throw No();
         const Arg *a = reinterpret_cast<const Arg *>(args);
         int dev = -1;
         const at::ScalarType t = a[0].tensor().scalar_type();
@@ -236,21 +240,152 @@ PyObject *attn(PyObject *, PyObject *const *args, Py_ssize_t n_args) {
         const int rc = f_attn(q.data_ptr(), c.k, c.v, (const int32_t *)tab.data_ptr(), (const int32_t *)cu.data_ptr(),
                               (const int32_t *)kv.data_ptr(), as_int(n), T, as_int(a[6].integer()), as_int(hq), c.heads,
                               (int)HEAD, code_of(t), c.code, ks, vs, c.pages, c.page_size, c.stride, as_int(tab.size(1)),
-                              (float)a[7].real(), as_int(a[8].integer()), out.data_ptr(), (float *)lse.data_ptr(),
+                              (float)a[7].real(), as_int(a[8].integer()), as_int(a[15].integer()), out.data_ptr(), (float *)lse.data_ptr(),
                               ws.data_ptr(), ws.nbytes(), (int32_t *)err, stream_of(dev));
         if (rc != KDA_OK) throw No();
         return tuple_of({&out, &lse});
     });
 }
 
-// init(tables, append, attn, workspace size): addresses of the library's functions
+// A [T, heads, 128] tensor of this type on this device whose tokens may lie apart.
+struct Rows {
+    void *p;
+    int64_t T, stride;
+    int heads;
+};
+Rows rows_of(const at::Tensor &x, at::ScalarType t, int device) {
+    if (!x.is_cuda() || x.get_device() != device || x.scalar_type() != t || x.dim() != 3 || x.size(2) != HEAD) throw No();
+    Rows r{x.data_ptr(), x.size(0), x.size(1) * HEAD, as_int(x.size(1))};
+    if (!x.is_contiguous()) {
+        if (r.T < 2 || x.stride(2) != 1 || x.stride(1) != HEAD) throw No();
+        r.stride = x.stride(0);
+    }
+    return r;
+}
+Rows rows_like(const Arg &a, at::Tensor &out, const at::Tensor &x, at::ScalarType t, int device) {
+    out = a.none() ? at::empty(x.sizes(), x.options()) : a.tensor();
+    if (!out.sizes().equals(x.sizes())) throw No();
+    return rows_of(out, t, device);
+}
+bool truth(const Arg &a) {
+    if (a.o != Py_True && a.o != Py_False) throw No();
+    return a.o == Py_True;
+}
+// freq: NULL and 0, or the frequencies and the channels they turn
+int turned(const Arg &a, const int64_t *&freq, int &device) {
+    freq = nullptr;
+    if (a.none()) return 0;
+    const at::Tensor &f = given(a, at::kLong, device);
+    freq = (const int64_t *)f.data_ptr();
+    return as_int(2 * f.numel());
+}
+
+// rope(q, k, positions, freq, amplitude, interleaved, q_weight, k_weight, eps, q_out, k_out)
+PyObject *rope(PyObject *, PyObject *const *args, Py_ssize_t n_args) {
+    return guarded([&]() -> PyObject * {
+        if (n_args != 11 || !f_rope) throw No();
+        const Arg *a = reinterpret_cast<const Arg *>(args);
+        const at::Tensor &q = a[0].tensor(), &k = a[1].tensor();
+        if (!q.is_cuda()) throw No();
+        int dev = q.get_device();
+        const at::ScalarType t = q.scalar_type();
+        const Rows qr = rows_of(q, t, dev), kr = rows_of(k, t, dev);
+        const at::Tensor &pos = given(a[2], at::kInt, dev);
+        if (kr.T != qr.T || pos.numel() != qr.T) throw No();
+        const int64_t *freq;
+        const int rot = turned(a[3], freq, dev);
+        const float *qw = (const float *)optional(a[6], at::kFloat, dev, HEAD), *kw = (const float *)optional(a[7], at::kFloat, dev, HEAD);
+        const c10::cuda::OptionalCUDAGuard guard(q.device());
+        at::Tensor qo, ko;
+        const Rows qor = rows_like(a[9], qo, q, t, dev), kor = rows_like(a[10], ko, k, t, dev);
+        const int rc = f_rope(qr.p, kr.p, (const int32_t *)pos.data_ptr(), freq, (float)a[4].real(), qw, kw, (float)a[8].real(), qr.T,
+                              qr.heads, kr.heads, (int)HEAD, rot, truth(a[5]) ? KDA_ROPE_INTERLEAVED : KDA_ROPE_HALF, code_of(t),
+                              qr.stride, kr.stride, qor.p, kor.p, qor.stride, kor.stride, stream_of(dev));
+        if (rc != KDA_OK) throw No();
+        return tuple_of({&qo, &ko});
+    });
+}
+
+// rope_append(q, k, v, positions, slot_map, freq, k_cache, v_cache, amplitude, interleaved, q_weight, k_weight, eps, k_scale,
+// v_scale, q_out, error_word): q_out
+PyObject *rope_append(PyObject *, PyObject *const *args, Py_ssize_t n_args) {
+    return guarded([&]() -> PyObject * {
+        if (n_args != 17 || !f_rope_append) throw No();
+        const Arg *a = reinterpret_cast<const Arg *>(args);
+        const at::Tensor &q = a[0].tensor();
+        if (!q.is_cuda()) throw No();
+        int dev = q.get_device();
+        const at::ScalarType t = q.scalar_type();
+        const Rows qr = rows_of(q, t, dev), kr = rows_of(a[1].tensor(), t, dev), vr = rows_of(a[2].tensor(), t, dev);
+        const at::Tensor &pos = given(a[3], at::kInt, dev), &slots = given(a[4], at::kLong, dev);
+        const Cache c = cache_of(a[6], a[7], dev);
+        if (kr.T != qr.T || vr.T != qr.T || kr.heads != c.heads || vr.heads != c.heads || pos.numel() != qr.T || slots.numel() != qr.T)
+            throw No();
+        const int64_t *freq;
+        const int rot = turned(a[5], freq, dev);
+        const float *qw = (const float *)optional(a[10], at::kFloat, dev, HEAD), *kw = (const float *)optional(a[11], at::kFloat, dev, HEAD);
+        const float *ks = scale_of(a[13], c, dev), *vs = scale_of(a[14], c, dev);
+        void *err = optional(a[16], at::kInt, dev);
+        const c10::cuda::OptionalCUDAGuard guard(q.device());
+        at::Tensor qo;
+        const Rows qor = rows_like(a[15], qo, q, t, dev);
+        const int rc = f_rope_append(qr.p, kr.p, vr.p, (const int32_t *)pos.data_ptr(), (const int64_t *)slots.data_ptr(), freq,
+                                     (float)a[8].real(), qw, kw, (float)a[12].real(), qr.T, qr.heads, kr.heads, (int)HEAD, rot,
+                                     truth(a[9]) ? KDA_ROPE_INTERLEAVED : KDA_ROPE_HALF, code_of(t), c.code, qr.stride, kr.stride,
+                                     vr.stride, qor.p, qor.stride, ks, vs, c.k, c.v, c.pages, c.page_size, c.stride, (int32_t *)err,
+                                     stream_of(dev));
+        if (rc != KDA_OK) throw No();
+        return THPVariable_Wrap(qo);
+    });
+}
+
+// verify(target, draft_tokens, uniforms, draft, n_draft, error_word)
+PyObject *verify(PyObject *, PyObject *const *args, Py_ssize_t n_args) {
+    return guarded([&]() -> PyObject * {
+        if (n_args != 6 || !f_verify) throw No();
+        const Arg *a = reinterpret_cast<const Arg *>(args);
+        const at::Tensor &p = a[0].tensor();
+        if (!p.is_cuda() || p.dim() != 3 || p.size(1) < 2) throw No();
+        int dev = p.get_device();
+        const at::ScalarType t = p.scalar_type();
+        const int64_t n = p.size(0), w = p.size(1), v = p.size(2);
+        auto rows = [&](const at::Tensor &x, int64_t width, int64_t &seq, int64_t &row) {
+            if (!x.is_cuda() || x.get_device() != dev || x.scalar_type() != t || x.dim() != 3 || x.size(0) != n || x.size(1) != width ||
+                x.size(2) != v)
+                throw No();
+            seq = width * v;
+            row = v;
+            if (!x.is_contiguous()) {
+                if (n < 2 || width < 2 || v < 2 || x.stride(2) != 1) throw No();
+                seq = x.stride(0);
+                row = x.stride(1);
+            }
+            return x.data_ptr();
+        };
+        int64_t ts, tr, ds = 0, dr = 0;
+        const void *tp = rows(p, w, ts, tr), *dp = a[3].none() ? nullptr : rows(a[3].tensor(), w - 1, ds, dr);
+        const at::Tensor &d = given(a[1], at::kInt, dev), &u = given(a[2], at::kFloat, dev);
+        if (d.dim() != 2 || d.size(0) != n || d.size(1) != w - 1 || u.dim() != 2 || u.size(0) != n || u.size(1) != w) throw No();
+        const int32_t *m = (const int32_t *)optional(a[4], at::kInt, dev, n);
+        void *err = optional(a[5], at::kInt, dev);
+        const c10::cuda::OptionalCUDAGuard guard(p.device());
+        at::Tensor acc = at::empty({n}, d.options()), out = at::empty({n, w}, d.options());
+        const int rc = f_verify(tp, dp, (const int32_t *)d.data_ptr(), (const float *)u.data_ptr(), m, as_int(n), as_int(w), as_int(v),
+                                code_of(t), ts, tr, ds, dr, (int32_t *)acc.data_ptr(), (int32_t *)out.data_ptr(), (int32_t *)err,
+                                stream_of(dev));
+        if (rc != KDA_OK) throw No();
+        return tuple_of({&acc, &out});
+    });
+}
+
+// init(tables, append, attn, workspace size, rope, rope_append, verify): addresses of the library's functions
 PyObject *init(PyObject *, PyObject *const *args, Py_ssize_t n) {
-    void *p[4];
-    if (n != 4) {
-        PyErr_SetString(PyExc_TypeError, "init takes four addresses");
+    void *p[7];
+    if (n != 7) {
+        PyErr_SetString(PyExc_TypeError, "init takes seven addresses");
         return nullptr;
     }
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 7; ++i) {
         p[i] = PyLong_AsVoidPtr(args[i]);
         if (PyErr_Occurred()) return nullptr;
     }
@@ -258,12 +393,17 @@ PyObject *init(PyObject *, PyObject *const *args, Py_ssize_t n) {
     f_append = reinterpret_cast<decltype(f_append)>(p[1]);
     f_attn = reinterpret_cast<decltype(f_attn)>(p[2]);
     f_workspace = reinterpret_cast<decltype(f_workspace)>(p[3]);
+    f_rope = reinterpret_cast<decltype(f_rope)>(p[4]);
+    f_rope_append = reinterpret_cast<decltype(f_rope_append)>(p[5]);
+    f_verify = reinterpret_cast<decltype(f_verify)>(p[6]);
     Py_RETURN_NONE;
 }
 
 #define FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(f)), METH_FASTCALL, nullptr
 PyMethodDef methods[] = {{"init", FAST(init)},     {"tables", FAST(tables)}, {"append", FAST(append)},
-                         {"attn", FAST(attn)},     {nullptr, nullptr, 0, nullptr}};
+                         {"attn", FAST(attn)},     {"rope", FAST(rope)},
+                         {"rope_append", FAST(rope_append)},               {"verify", FAST(verify)},
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_paged_fast", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -35,17 +35,19 @@ def _not_loaded(*args):
     _lib()
 
 
-_fast_tables = _fast_append = _fast_attn = _not_loaded
+_fast_tables = _fast_append = _fast_attn = _fast_rope = _fast_rope_append = _fast_verify = _not_loaded
 
 
 def _load_fast(lib):
-    global _fast_tables, _fast_append, _fast_attn
+    global _fast_tables, _fast_append, _fast_attn, _fast_rope, _fast_rope_append, _fast_verify
     spec = importlib.util.spec_from_file_location("_paged_fast", _build.build_fast())
     fast = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(fast)
     fast.init(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
-        lib.kda_paged_tables, lib.kda_paged_append, lib.kda_paged_attn, lib.kda_paged_attn_workspace_size)))
+        lib.kda_paged_tables, lib.kda_paged_append, lib.kda_paged_attn_sinks, lib.kda_paged_attn_workspace_size,
+        lib.kda_qk_rope, lib.kda_paged_rope_append, lib.kda_verify_drafts)))
     _fast_tables, _fast_append, _fast_attn = fast.tables, fast.append, fast.attn
+    _fast_rope, _fast_rope_append, _fast_verify = fast.rope, fast.rope_append, fast.verify
 
 
 def _lib():
@@ -53,9 +55,16 @@ def _lib():
     if _declared is None:
         lib = load()
         P, I, L, F, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
+        G = ctypes.c_double
         lib.kda_paged_tables.argtypes = [P, P, I, L, P, I, P, I, P, P, I, I, P, P, P, P, P, P]
         lib.kda_paged_append.argtypes = [P, P, P, L, I, I, I, I, P, P, P, P, I, I, L, P, P]
         lib.kda_paged_attn.argtypes = [P, P, P, P, P, P, I, L, I, I, I, I, I, I, P, P, I, I, L, I, F, I, P, P, P, S, P, P]
+        lib.kda_paged_attn_sinks.argtypes = [P, P, P, P, P, P, I, L, I, I, I, I, I, I, P, P, I, I, L, I, F, I, I, P, P, P, S, P, P]
+        lib.kda_rope_frequencies.argtypes = [I, G, I, G, G, G, G, P, P]
+        lib.kda_qk_rope.argtypes = [P, P, P, P, F, P, P, F, L, I, I, I, I, I, I, L, L, P, P, L, L, P]
+        lib.kda_paged_rope_append.argtypes = [P, P, P, P, P, P, F, P, P, F, L, I, I, I, I, I, I, I, L, L, L, P, L, P, P, P, P, I,
+                                              I, L, P, P]
+        lib.kda_verify_drafts.argtypes = [P, P, P, P, P, I, I, I, I, L, L, L, L, P, P, P, P]
         lib.kda_paged_attn_workspace_size.argtypes = [L, I, I, I]
         lib.kda_paged_attn_workspace_size.restype = S
         try:
@@ -196,13 +205,14 @@ def paged_attn_workspace_size(T_total: int, n_seqs: int, Hq: int, Hkv: int) -> i
 
 
 def paged_attn(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q=0, sm_scale=D ** -0.5, window=0, k_scale=None,
-               v_scale=None, out=None, lse=None, workspace=None, error_word=None):
+               v_scale=None, out=None, lse=None, workspace=None, error_word=None, sinks=0):
     """kda_paged_attn: q [T, Hq, 128] over the caches [pages, Hkv, page size, 128]
     through block_table int32 [n, max_blocks]; cu_q int32 [n + 1] and kv_len int32 [n]
     as paged_tables gives them.  max_q: the most new tokens of one request (0: not
-    known).  Returns (o in q's dtype, lse float32 [T, Hq])."""
+    known).  sinks: the first tokens of each request, which a window leaves visible.
+    Returns (o in q's dtype, lse float32 [T, Hq])."""
     done = _fast_attn(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q, sm_scale, window, k_scale, v_scale, out, lse,
-                      workspace, error_word)
+                      workspace, error_word, sinks)
     if done is not None:
         return done
     lib = _declared or _lib()
@@ -229,10 +239,10 @@ def paged_attn(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q=0, sm_scale
     if workspace is None:
         workspace = q.new_empty(lib.kda_paged_attn_workspace_size(T, n, hq, hkv), dtype=torch.uint8)
     with torch.cuda.device(index):
-        rc = lib.kda_paged_attn(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), cu_q.data_ptr(),
-                                kv_len.data_ptr(), n, T, max_q, hq, hkv, D, _CODE[dtype], code, _p(k_scale), _p(v_scale),
-                                n_pages, ps, stride, block_table.shape[1], sm_scale, window, out.data_ptr(), lse.data_ptr(),
-                                workspace.data_ptr(), workspace.nbytes, _p(error_word), _raw_stream(index))
+        rc = lib.kda_paged_attn_sinks(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), cu_q.data_ptr(),
+                                      kv_len.data_ptr(), n, T, max_q, hq, hkv, D, _CODE[dtype], code, _p(k_scale), _p(v_scale),
+                                      n_pages, ps, stride, block_table.shape[1], sm_scale, window, sinks, out.data_ptr(),
+                                      lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, _p(error_word), _raw_stream(index))
     if rc:
         _check(rc, "kda_paged_attn")
     return out, lse

@@ -1,0 +1,226 @@
+"""Verification of drafted tokens against exact fractions, and its law."""
+import pytest
+import torch
+
+import linear_attention_serving_gb300 as kda
+from linear_attention_serving_gb300 import drafts, paged
+from serving_testutil import draft_inputs, verify_ref
+from test_gpu_canaries import Guarded
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def dev(*ts):
+    return [None if t is None else t.to(DEV) for t in ts]
+
+
+def verify(target, draft, tokens, uniforms, n_draft=None):
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    t, q, d, u, m = dev(target, draft, tokens, uniforms, n_draft)
+    acc, out = kda.verify_drafts(t, d, u, draft=q, n_draft=m, error_word=err)
+    return acc.tolist(), out.tolist(), int(err)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("certain", [False, True])
+@pytest.mark.parametrize("n,w,V", [(1, 1, 1), (1, 2, 1), (3, 1, 37), (5, 4, 16), (40, 5, 33), (7, 8, 1000), (2, 32, 64), (300, 3, 8),
+                                   (3, 5, 4099)])
+def test_against_fractions(n, w, V, certain, dtype):
+    target, draft, tokens, u = draft_inputs(n, w, V, seed=n * w + V, dtype=dtype, certain=certain)
+    if w == 1:
+        draft = None
+    acc, out, err = verify(target, draft, tokens, u)
+    ref = verify_ref(target, tokens, u, draft)
+    assert err == 0 and acc == ref[0] and out == ref[1]
+
+
+def test_ragged_drafts():
+    target, draft, tokens, u = draft_inputs(50, 6, 40, seed=1)
+    m = (torch.arange(50) % 6).int()
+    for q in (draft, None):
+        acc, out, err = verify(target, q, tokens, u, m)
+        ref = verify_ref(target, tokens, u, q, m)
+        assert err == 0 and acc == ref[0] and out == ref[1]
+        assert all(a <= b for a, b in zip(acc, m.tolist()))
+
+
+def by_sums(target, draft, tokens, u):
+    """64-bit sums, for large vocabularies."""
+    n, w, V = target.shape
+    p, i = target.double(), torch.arange(n, device=DEV)
+    pd = p[:, :-1].gather(2, tokens.long()[..., None])[..., 0]
+    qd = 1.0 if draft is None else draft.double().gather(2, tokens.long()[..., None])[..., 0]
+    acc = (u.double()[:, :-1] * qd < pd).int().cumprod(1).sum(1)
+    rest = p[i, acc].clone()
+    refused = acc < w - 1
+    at = acc.clamp(max=w - 2)
+    if draft is None:
+        rest[i[refused], tokens.long()[i, at][refused]] = 0
+    else:
+        rest = torch.where(refused[:, None], (rest - draft[i, at].double()).clamp(min=0), rest)
+    c = rest.cumsum(1)
+    return acc, (c <= u.double()[:, -1:] * c[:, -1:]).sum(1)
+
+
+@pytest.mark.parametrize("n,w,V,certain,dtype", [
+    (1, 5, 32768, False, F32), (1, 5, 200_003, False, F32), (3, 3, 1_000_001, False, F32), (300, 4, 5000, False, F32),
+    (40, 5, 131_072, False, BF16), (700, 2, 20_000, True, F32), (9, 6, 50_001, True, BF16), (2, 2, 9_000_000, False, F32)])
+def test_large_vocabularies(n, w, V, certain, dtype):
+    """Every split of a row over blocks and segments; odd sizes go without vector loads."""
+    g = torch.Generator(device=DEV).manual_seed(V + n)
+    logits = 3 * torch.randn(n, w, V, generator=g, device=DEV)
+    target = logits.softmax(2).to(dtype)
+    near = (logits[:, :-1] + 0.5 * torch.randn(n, w - 1, V, generator=g, device=DEV)).softmax(2).to(dtype)
+    draft = None if certain else near
+    tokens = near.float().argmax(2).int()
+    u = torch.rand(n, w, generator=g, device=DEV)
+    u[: n // 2, :-1] = 0.999
+    acc, out = kda.verify_drafts(target, tokens, u, draft=draft)
+    ref, token = by_sums(target, draft, tokens, u)
+    assert torch.equal(acc.long(), ref)
+    assert torch.equal(out.gather(1, ref[:, None])[:, 0].long(), token)
+
+
+def test_padded_and_shifted_rows():
+    """Rows that lie apart, on 16 bytes and not: the same tokens."""
+    target, draft, tokens, u = draft_inputs(6, 4, 3001, seed=3)
+    want = verify(target, draft, tokens, u)
+    for pad, shift in ((7, 0), (7, 1), (1, 3), (71, 2)):
+        t = torch.full((6, 4, 3001 + pad + shift), float("nan"))
+        q = torch.full((6, 3, 3001 + pad + shift), float("nan"))
+        t[:, :, shift:shift + 3001] = target
+        q[:, :, shift:shift + 3001] = draft
+        t, q = t.to(DEV)[:, :, shift:shift + 3001], q.to(DEV)[:, :, shift:shift + 3001]
+        acc, out = kda.verify_drafts(t, tokens.to(DEV), u.to(DEV), draft=q)
+        assert acc.tolist() == want[0] and out.tolist() == want[1]
+
+
+def test_edges_of_the_uniform_numbers():
+    """r = 0: the first token with weight; the largest number under 1, 1 and more: the last; below 0 and NaN: as 0."""
+    p = torch.tensor([0.0, 0.25, 0.0, 0.5, 0.25, 0.0]).view(1, 1, 6).repeat(6, 1, 1)
+    u = torch.tensor([0.0, 1 - 2.0 ** -24, 1.0, 7.0, -3.0, float("nan")]).view(6, 1)
+    acc, out, err = verify(p, None, torch.empty(6, 0, dtype=torch.int32), u)
+    assert err == 0 and acc == [0] * 6 and [x[0] for x in out] == [1, 4, 4, 4, 1, 1]
+    # on a border the sum has to pass the bound
+    p = torch.tensor([0.25, 0.25, 0.5]).view(1, 1, 3).repeat(4, 1, 1)
+    u = torch.tensor([0.25, 0.5, 0.25 - 2.0 ** -26, 0.75]).view(4, 1)
+    assert [x[0] for x in verify(p, None, torch.empty(4, 0, dtype=torch.int32), u)[1]] == [1, 2, 0, 2]
+
+
+def test_edges_of_the_tests():
+    """u q < p: equal is refused; p = 0 is refused even by u = 0; q = 0 stands where p > 0."""
+    p = torch.tensor([[[0.5, 0.5], [0.5, 0.5]]]).repeat(4, 1, 1)
+    q = torch.tensor([[[1.0, 0.0]]]).repeat(4, 1, 1)
+    tokens = torch.tensor([[0], [0], [1], [0]], dtype=torch.int32)
+    u = torch.tensor([[0.5, 0.3], [0.5 - 2.0 ** -25, 0.3], [0.9, 0.3], [0.0, 0.9]])
+    acc, out, err = verify(p, q, tokens, u)
+    assert err == 0 and acc == [0, 1, 1, 1] and out == [[1, -1], [0, 0], [1, 0], [0, 1]]
+    zero = torch.tensor([[[0.0, 1.0], [1.0, 0.0]]])
+    acc, out, err = verify(zero, None, torch.tensor([[0]], dtype=torch.int32), torch.zeros(1, 2))
+    assert err == 0 and acc == [0] and out == [[1, -1]]
+
+
+def test_nothing_left_beside_the_draft():
+    """p covered by q all over (or on the certain draft alone): drawn from p itself."""
+    p = torch.tensor([[[0.5, 0.5, 0.0], [0.0, 0.0, 1.0]]])
+    acc, out, err = verify(p, p[:, :1] * 1.0, torch.tensor([[2]], dtype=torch.int32), torch.tensor([[0.5, 0.7]]))
+    assert err == 0 and acc == [0] and out == [[1, -1]]
+    p = torch.tensor([[[0.25, 0.0, 0.0], [0.0, 0.0, 1.0]]])
+    acc, out, err = verify(p, None, torch.tensor([[0]], dtype=torch.int32), torch.tensor([[0.5, 0.7]]))
+    assert err == 0 and acc == [0] and out == [[0, -1]]
+
+
+def test_what_is_wrong_on_the_device():
+    target, draft, tokens, u = draft_inputs(4, 3, 50, seed=7)
+    tokens[0, 0], tokens[1, 1], u[1, 0] = 50, -1, 0.0
+    for q in (draft, None):
+        acc, out, err = verify(target, q, tokens, u)
+        assert err == drafts.DEVERR_TOKEN
+        assert acc[0] == 0 and acc[1] <= 1 and 0 <= out[0][0] < 50
+        ref = verify_ref(target[2:], tokens[2:], u[2:], None if q is None else q[2:])
+        assert acc[2:] == ref[0] and out[2:] == ref[1]
+    target, draft, tokens, u = draft_inputs(4, 3, 50, seed=8)
+    acc, out, err = verify(target, draft, tokens, u, torch.tensor([2, 3, -1, 0], dtype=torch.int32))
+    assert err == 2  # KDA_DEVERR_NUM_ACCEPTED
+    assert acc[1:3] == [0, 0] and out[1] == out[2] == [-1] * 3
+    ref = verify_ref(target[[0, 3]], tokens[[0, 3]], u[[0, 3]], draft[[0, 3]], [2, 0])
+    assert [acc[0], acc[3]] == ref[0] and [out[0], out[3]] == ref[1]
+    target[2] = 0
+    acc, out, err = verify(target, draft, tokens, u)
+    assert err == drafts.DEVERR_PROBS and acc[2] == 0 and out[2] == [-1] * 3
+
+
+def test_values_that_are_no_probabilities():
+    """NaN and negative values weigh nothing, and a test against NaN is refused."""
+    nan = float("nan")
+    p = torch.tensor([[[nan, 0.5, -1.0, 0.5], [0.0, 0.0, nan, 1.0]]])
+    q = torch.tensor([[[0.5, nan, 0.0, 0.5]]])
+    acc, out, err = verify(p, q, torch.tensor([[0]], dtype=torch.int32), torch.tensor([[0.0, 0.9]]))
+    assert err == 0 and acc == [0] and out == [[1, -1]]
+    acc, out, err = verify(p, None, torch.tensor([[1]], dtype=torch.int32), torch.tensor([[0.1, 0.0]]))
+    assert err == 0 and acc == [1] and out == [[1, 3]]
+
+
+def test_the_law():
+    """Whatever the draft, the first token is distributed as the target says: 200,000 requests, every share within
+    5 standard deviations."""
+    n = 200_000
+    g = torch.Generator().manual_seed(12)
+    p = torch.tensor([0.4, 0.3, 0.05, 0.2, 0.05, 0.0])
+    q = torch.tensor([0.1, 0.5, 0.1, 0.0, 0.1, 0.2])
+    tokens = torch.multinomial(q.repeat(n, 1), 1, generator=g).int()
+    u = torch.rand(n, 2, generator=g)
+    t, d = p.view(1, 1, 6).expand(n, 2, 6).contiguous(), q.view(1, 1, 6).expand(n, 1, 6).contiguous()
+    acc, out = kda.verify_drafts(t.to(DEV), tokens.to(DEV), u.to(DEV), draft=d.to(DEV))
+    share = torch.bincount(out[:, 0].cpu(), minlength=6).double() / n
+    assert ((share - p.double()).abs() <= 5 * (p.double() * (1 - p.double()) / n).sqrt()).all()
+    kept = torch.minimum(p, q).sum().item()  # accepted with this probability
+    assert abs(acc.double().mean().item() - kept) <= 5 * (kept * (1 - kept) / n) ** 0.5
+
+
+def test_writes_nothing_else_and_replays():
+    target, draft, tokens, u = dev(*draft_inputs(9, 5, 20_000, seed=5))
+    lib = paged._lib()
+    acc, out = Guarded((9,), torch.int32), Guarded((9, 5), torch.int32)
+    p = lambda x: x.data_ptr()  # noqa: E731
+
+    def call():
+        rc = lib.kda_verify_drafts(p(target), p(draft), p(tokens), p(u), None, 9, 5, 20_000, 1, 100_000, 20_000, 80_000, 20_000, p(acc.t),
+                                   p(out.t), None, torch.cuda.current_stream().cuda_stream)
+        assert rc == 0
+
+    call()
+    want = kda.verify_drafts(target, tokens, u, draft=draft)
+    assert acc.intact() and out.intact()
+    assert torch.equal(acc.t, want[0]) and torch.equal(out.t, want[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    fresh = draft_inputs(9, 5, 20_000, seed=6)
+    for a, b in zip((target, draft, tokens, u), fresh):
+        a.copy_(b)
+    graph.replay()
+    torch.cuda.synchronize()
+    want = kda.verify_drafts(target, tokens, u, draft=draft)
+    assert torch.equal(acc.t, want[0]) and torch.equal(out.t, want[1])
+
+
+def test_plain_binding_and_refusals(monkeypatch):
+    target, draft, tokens, u = dev(*draft_inputs(6, 4, 500, seed=2))
+    want = kda.verify_drafts(target, tokens, u, draft=draft)
+    bad = [dict(target=target.half()), dict(target=target[0]), dict(draft=draft.bfloat16()), dict(draft=draft[:, :2]),
+           dict(draft_tokens=tokens.long()), dict(draft_tokens=tokens[:, :2].contiguous()), dict(uniforms=u.double()),
+           dict(uniforms=u[:, :3].contiguous()), dict(n_draft=tokens[0].contiguous()), dict(n_draft=u[0].contiguous()),
+           dict(target=target.cpu()), dict(target=target.transpose(1, 2)), dict(target=target[:, :, ::2].expand(6, 4, 250)),
+           dict(target=torch.zeros(6, 33, 4, device=DEV), draft_tokens=torch.zeros(6, 32, dtype=torch.int32, device=DEV),
+                uniforms=torch.zeros(6, 33, device=DEV), draft=None)]
+    for kw in bad:
+        a = dict(target=target, draft_tokens=tokens, uniforms=u, draft=draft)
+        a.update(kw)
+        with pytest.raises(kda.KDAError):
+            kda.verify_drafts(**a)
+    monkeypatch.setattr(paged, "_fast_verify", lambda *a: None)
+    got = kda.verify_drafts(target, tokens, u, draft=draft)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
