@@ -618,7 +618,7 @@ int kda_paged_rope_append(const void *q, const void *k, const void *v, const int
  *   N >= 1, 1 <= W <= 32, 1 <= V < 2^31; dtype KDA_F32 or KDA_BF16, values 0 .. 1
  *   num_accepted (device) int32 [N], written: a
  *   tokens       (device) int32 [N, W], written: d_0 .. d_{a-1}, the token drawn, then -1
- * The tests are exact.  Weights are summed as multiples of 2^-60 (each rounded once),
+ * The tests are exact.  Weights are summed as multiples of 2^-60 (p and q each rounded down),
  * so sums do not depend on their order and the same call gives the same tokens; values below
  * 0 or NaN count as 0, over 1 as 1.  A row that sums to 8 or more has no answer (some token).
  * A drafted token outside 0 .. V-1 records KDA_DEVERR_TOKEN and is refused.  An n_draft out

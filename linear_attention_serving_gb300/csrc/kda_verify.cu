@@ -8,8 +8,8 @@
 //
 // Weights are summed as 64-bit integers, multiples of 2^-60: sums are then exact whatever
 // their order, so the pieces that warps and blocks add up meet without rounding, and the
-// place found is the same in every split.  (A value over 2^-36 loses nothing; V = 2^17
-// smaller ones are off by 2^-44 together.)
+// place found is the same in every split.  (A value over 2^-37 loses nothing; V = 2^17
+// smaller ones are off by under 2^-43 together.)
 //
 // The row is cut into segments of four vector loads (16 scalar ones) a lane; each warp keeps a segment's sum
 // in shared memory.  The blocks tell each other their totals through distributed shared
@@ -24,9 +24,10 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int THREADS = 512, WARPS = THREADS / 32;
+constexpr int THREADS = 256, WARPS = THREADS / 32;
+constexpr int BLOCKS = 4;  // an SM
 constexpr int MAX_CLUSTER = 8;
-constexpr int MAX_SEGS = 2048;  // of one block
+constexpr int MAX_SEGS = 1024;  // of one block
 constexpr int KEEP = MAX_SEGS / THREADS;
 // loads of a lane at a time, by their elements
 __host__ __device__ constexpr int loads_of(int n) { return n == 1 ? 16 : 4; }
@@ -44,11 +45,31 @@ template <typename T> __device__ __forceinline__ float as_float(T x);
 template <> __device__ __forceinline__ float as_float(float x) { return x; }
 template <> __device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-// a weight in multiples of 2^-60 (NaN and what is below 0: none)
-__device__ __forceinline__ int64_t fixed(float x) { return (int64_t)__float2ull_rn(__saturatef(x) * 0x1p60f); }
+// A weight in multiples of 2^-60, rounded down (NaN and what is below 0: none).  Shifts of the
+// significand: conversions to 64-bit integers run at a few a cycle and SM.
+__device__ __forceinline__ int64_t fixed(float x) {
+    const uint32_t b = __float_as_uint(__saturatef(x));
+    uint64_t m = (uint64_t)((b << 5 & 0x0fffffffu) | 0x10000000u) << 32, r;  // 2^60 for 1.0
+    asm("shr.u64 %0, %1, %2;" : "=l"(r) : "l"(m), "r"(127 - (b >> 23)));     // (64 and more: 0)
+    return (int64_t)r;
+}
 
-template <typename T, int N> struct __align__(sizeof(T) * N) Vec {
-    T x[N];
+// N elements in 16 bytes, or one.
+template <typename T, int N> struct Load {
+    uint4 x;
+    __device__ __forceinline__ void get(const T *p) { x = __ldg(reinterpret_cast<const uint4 *>(p)); }
+    __device__ __forceinline__ void none() { x = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ float operator[](int i) const {
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        if (sizeof(T) == 4) return __uint_as_float(w[i & 3]);
+        return __uint_as_float(i & 1 ? w[(i >> 1) & 3] & 0xffff0000u : w[(i >> 1) & 3] << 16);
+    }
+};
+template <typename T> struct Load<T, 1> {
+    T x;
+    __device__ __forceinline__ void get(const T *p) { x = *p; }
+    __device__ __forceinline__ void none() { x = T(0.f); }
+    __device__ __forceinline__ float operator[](int) const { return as_float(x); }
 };
 
 __device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
@@ -74,41 +95,37 @@ template <typename T> struct Row {
         const int64_t w = fixed(as_float(p[i])) - (q ? fixed(as_float(q[i])) : 0);
         return w > 0 ? (uint64_t)w : 0;
     }
+    __device__ __forceinline__ uint64_t over(float x, float y) const {
+        const int64_t w = fixed(x) - fixed(y);
+        return w > 0 ? (uint64_t)w : 0;
+    }
     // this lane's part of the elements [e0, e0 + LOADS x 32 x N), vector loads where they end before V
     template <int N, bool Q> __device__ __forceinline__ uint64_t part(int64_t e0, int V, int lane) const {
         constexpr int LOADS = loads_of(N);
-        Vec<T, N> a[LOADS], b[LOADS];
+        Load<T, N> a[LOADS], b[LOADS];
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) {
             const int64_t e = e0 + (i * 32 + lane) * N;
-            if (e + N <= V) {
-                a[i] = *reinterpret_cast<const Vec<T, N> *>(p + e);
-                if (Q) b[i] = *reinterpret_cast<const Vec<T, N> *>(q + e);
-            }
+            const bool in = e + N <= V;
+            in ? a[i].get(p + e) : a[i].none();
+            if (Q) in ? b[i].get(q + e) : b[i].none();
         }
         uint64_t sum = 0;
 #pragma unroll
-        for (int i = 0; i < LOADS; ++i) {
-            const int64_t e = e0 + (i * 32 + lane) * N;
-            if (e + N <= V) {
+        for (int i = 0; i < LOADS; ++i)
 #pragma unroll
-                for (int j = 0; j < N; ++j) {
-                    const int64_t w = fixed(as_float(a[i].x[j])) - (Q ? fixed(as_float(b[i].x[j])) : 0);
-                    sum += Q ? (uint64_t)(w > 0 ? w : 0) : (uint64_t)w;
-                }
-                if (gone >= e && gone < e + N) {  // (certain drafts only)
-                    sum -= fixed(as_float(p[gone]));
-                }
-            } else if (N > 1) {
-                for (int64_t k = e; k < V; ++k) sum += weight((int)k);
-            }
+            for (int j = 0; j < N; ++j) sum += Q ? over(a[i][j], b[i][j]) : (uint64_t)fixed(a[i][j]);
+        if (N > 1 && e0 + LOADS * 32 * N > V) {  // the row's last elements, fewer than a vector's
+            const int64_t e = V / N * N + lane;
+            if (e < V && e >= e0) sum += Q ? over(as_float(p[e]), as_float(q[e])) : (uint64_t)fixed(as_float(p[e]));
         }
+        if (gone >= e0 && gone < e0 + LOADS * 32 * N && lane == 0) sum -= fixed(as_float(p[gone]));  // (certain drafts)
         return sum;
     }
 };
 
 template <typename T, int N>
-__global__ void __launch_bounds__(THREADS) verify_kernel(const VerifyArgs a) {
+__global__ void __launch_bounds__(THREADS, BLOCKS) verify_kernel(const VerifyArgs a) {
     __shared__ uint64_t seg_sum[MAX_SEGS];
     __shared__ uint64_t warp_tot[WARPS], block_tot[2][MAX_CLUSTER];
     __shared__ uint64_t found_left;
@@ -155,7 +172,7 @@ __global__ void __launch_bounds__(THREADS) verify_kernel(const VerifyArgs a) {
     row.gone = acc < m && !a.draft ? refused : -1;
     const int s0 = c * a.segs, total_segs = (int)(((int64_t)a.V + a.per_seg - 1) / a.per_seg);
     const int ns = max(0, min(a.segs, total_segs - s0));
-    uint64_t before, mine, all, left[KEEP], incl, excl;
+    uint64_t before, mine, all, incl, excl;
     for (int pass = 0;; ++pass) {
         for (int s = warp; s < ns; s += WARPS) {
             uint64_t sum = 0;
@@ -170,10 +187,8 @@ __global__ void __launch_bounds__(THREADS) verify_kernel(const VerifyArgs a) {
         // scan: a thread has KEEP segments
         uint64_t sum = 0;
 #pragma unroll
-        for (int i = 0; i < KEEP; ++i) {
-            left[i] = tid * KEEP + i < ns ? seg_sum[tid * KEEP + i] : 0;
-            sum += left[i];
-        }
+        for (int i = 0; i < KEEP; ++i)
+            if (tid * KEEP + i < ns) sum += seg_sum[tid * KEEP + i];
         incl = warp_scan(sum, lane);
         if (lane == 31) warp_tot[warp] = incl;
         __syncthreads();
@@ -213,14 +228,9 @@ __global__ void __launch_bounds__(THREADS) verify_kernel(const VerifyArgs a) {
     const uint64_t at = bound - before;
     if (at >= excl && at < incl) {
         uint64_t rest = at - excl;
-        int s = 0;
-#pragma unroll
-        for (int i = 0; i < KEEP; ++i)
-            if (s == i && rest >= left[i]) {
-                rest -= left[i];
-                ++s;
-            }
-        found_seg = s0 + tid * KEEP + s;
+        int s = tid * KEEP;
+        while (rest >= seg_sum[s]) rest -= seg_sum[s++];  // (the thread's sums are more than rest)
+        found_seg = s0 + s;
         found_left = rest;
     }
     __syncthreads();
@@ -228,25 +238,21 @@ __global__ void __launch_bounds__(THREADS) verify_kernel(const VerifyArgs a) {
     uint64_t rest = found_left;
     const int64_t e0 = (int64_t)found_seg * a.per_seg;
     for (int64_t e = e0; e < e0 + a.per_seg; e += 32 * 16) {  // 16 elements a lane, in order
-        uint64_t w[16], sum = 0;
+        const int k0 = (int)min((int64_t)a.V, e + lane * 16), k1 = min(a.V, k0 + 16);
+        uint64_t sum = 0;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int64_t k = e + lane * 16 + i;
-            w[i] = k < a.V ? row.weight((int)k) : 0;
-            sum += w[i];
-        }
+        for (int i = 0; i < 16; ++i)
+            if (k0 + i < k1) sum += row.weight(k0 + i);
         const uint64_t in = warp_scan(sum, lane), total = __shfl_sync(0xffffffffu, in, 31);
         if (rest < total) {
-            if (rest >= in - sum && rest < in) {
-                uint64_t left = rest - (in - sum);
-                int i = 0;
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    if (i == j && left >= w[j]) {
-                        left -= w[j];
-                        ++i;
-                    }
-                *out = (int)(e + lane * 16 + i);
+            if (rest < in && rest >= in - sum) {
+                uint64_t left = rest - (in - sum), w;
+                int k = k0;
+                while (left >= (w = row.weight(k))) {
+                    left -= w;
+                    ++k;
+                }
+                *out = k;
             }
             break;
         }
