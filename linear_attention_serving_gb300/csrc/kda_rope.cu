@@ -12,8 +12,17 @@
 // is the exact angle modulo a turn (fp32 products lose whole radians at positions of
 // a million).  Its nearest quarter turn is taken off in integers, and what is left, at most
 // an eighth of a turn, rounded to fp32: off by at most 2^-27 half turns, under 2^-25 radians.
-// A block works the sines and cosines of its tokens out once, in shared memory, for all
-// their heads.
+// The sines and cosines of a token are worked out once, in shared memory, for all its heads
+// (by each unit for itself where a unit has a token of its own), and multiplied with the norms'
+// weights once for each kind of row, so that a row costs a scale and two packed products and
+// sums for each two channels.
+//
+// Bound by HBM once there are some thousand tokens, by the launch and the chain position, angle,
+// row below: 23,100 packed tokens of 32 + 2 x 8 heads (bf16, norms) into their pages 92 us, 6.2
+// TB/s; 9,900 of 16 + 16 heads (fp32) 48 us, 6.4 TB/s; 1,280 tokens into an e4m3 cache 9.8 us; one
+// token 2.9 us.  Two rows a unit in flight and two ahead of them, 64 registers: with four
+// of each, 80 registers and three blocks an SM, the first is 92 to 109 us; with rows of all
+// kinds in one stream of batches, 111.
 #include <cuda_fp8.h>
 
 #include <cmath>
@@ -28,8 +37,8 @@ int check_paged_cache(int Hkv, int Dm, int dtype, int cache_dtype, const float *
 namespace {
 
 constexpr int THREADS = 256, UNITS = THREADS / 16;  // a unit of 16 lanes takes a row at a time
-constexpr int AHEAD = 4;                            // rows of a unit in flight
 constexpr int PAIRS = D / 2;
+constexpr int SOME = 2, MANY = 3, EACH = 4;         // tokens of a block (their logarithm; EACH: one for each unit)
 
 enum { TO_ROWS = 0, TO_PAGES = 1, TO_E4M3 = 2 };
 
@@ -43,11 +52,34 @@ struct RopeArgs {
     int32_t *err;
     int64_t q_stride, k_stride, v_stride, q_out_stride, k_out_stride;  // elements
     int64_t page_stride, n_slots;
-    int T, Hq, Hkv, rot, page_size, tok_log, rows_per_y;
+    int T, Hq, Hkv, rot, page_size, rows_per_y;
     float amplitude, eps;
 };
 
-// Eight channels of a row: chunks of four, c0 and c1.
+// Two fp32 operations at once.
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t r) {
+    float2 x;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x.x), "=f"(x.y) : "l"(r));
+    return x;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+    return r;
+}
+
+// Eight channels of a row, two chunks of four (c0 and c1), as they are held; and as four packed
+// pairs of neighbours (a lane's pair i of y is channels 2 i, 2 i + 1 of the eight).
 template <typename T> struct Eight;
 template <> struct Eight<__nv_bfloat16> {
     uint2 a, b;
@@ -69,19 +101,17 @@ template <> struct Eight<__nv_bfloat16> {
             *(reinterpret_cast<uint2 *>(row) + c1) = b;
         }
     }
-    __device__ __forceinline__ void get(float *x) const {
+    __device__ __forceinline__ void get(uint64_t *y) const {
         const uint32_t w[4] = {a.x, a.y, b.x, b.y};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(w[i] << 16);
-            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
+        for (int i = 0; i < 4; ++i) y[i] = pack2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
     }
-    __device__ __forceinline__ void set(const float *x) {
+    __device__ __forceinline__ void set(const uint64_t *y) {
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 p = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+            const float2 f = unpack2(y[i]);
+            const __nv_bfloat162 p = __floats2bfloat162_rn(f.x, f.y);
             w[i] = *reinterpret_cast<const uint32_t *>(&p);
         }
         a = make_uint2(w[0], w[1]);
@@ -98,23 +128,25 @@ template <> struct Eight<float> {
         *(reinterpret_cast<float4 *>(row) + c0) = a;
         *(reinterpret_cast<float4 *>(row) + c1) = b;
     }
-    __device__ __forceinline__ void get(float *x) const {
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    __device__ __forceinline__ void get(uint64_t *y) const {
+        y[0] = pack2(a.x, a.y), y[1] = pack2(a.z, a.w), y[2] = pack2(b.x, b.y), y[3] = pack2(b.z, b.w);
     }
-    __device__ __forceinline__ void set(const float *x) {
-        a = make_float4(x[0], x[1], x[2], x[3]);
-        b = make_float4(x[4], x[5], x[6], x[7]);
+    __device__ __forceinline__ void set(const uint64_t *y) {
+        const float2 p = unpack2(y[0]), q = unpack2(y[1]), r = unpack2(y[2]), t = unpack2(y[3]);
+        a = make_float4(p.x, p.y, q.x, q.y);
+        b = make_float4(r.x, r.y, t.x, t.y);
     }
 };
 
 // x / scale in fp32, then one rounding to e4m3 (a true division: a product with 1 / scale
 // would round twice and move values across a border)
-__device__ __forceinline__ uint32_t e4m3_4(const float *x, float scale) {
+__device__ __forceinline__ uint32_t e4m3_4(const uint64_t *y, float scale) {
     uint32_t r = 0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const __nv_fp8x2_storage_t b = __nv_cvt_float2_to_fp8x2(
-            make_float2(__fdiv_rn(x[2 * i], scale), __fdiv_rn(x[2 * i + 1], scale)), __NV_SATFINITE, __NV_E4M3);
+        const float2 x = unpack2(y[i]);
+        const __nv_fp8x2_storage_t b =
+            __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(x.x, scale), __fdiv_rn(x.y, scale)), __NV_SATFINITE, __NV_E4M3);
         r |= (uint32_t)b << (16 * i);
     }
     return r;
@@ -132,47 +164,164 @@ __device__ __forceinline__ float2 turn_of(int pos, int64_t f, float amplitude) {
     return quarter & 2 ? make_float2(-x * amplitude, -y * amplitude) : make_float2(x * amplitude, y * amplitude);
 }
 
-template <typename T, int TO, bool INTER>
-__global__ void __launch_bounds__(THREADS) rope_kernel(const RopeArgs a) {
-    __shared__ float2 turn[UNITS][PAIRS];
-    const int tid = threadIdx.x, l = tid & 15, unit = tid >> 4;
-    const int per_tok = UNITS >> a.tok_log;  // units of one token
-    const int mine = unit / per_tok, step0 = unit - mine * per_tok;
-    const int t0 = blockIdx.x << a.tok_log, tok = t0 + mine;
-    const int rows = a.Hq + (TO == TO_ROWS ? 1 : 2) * a.Hkv;
-    const int r0 = blockIdx.y * a.rows_per_y, r1 = min(rows, r0 + a.rows_per_y);
-    const bool live = tok < a.T;
-    // this lane's chunks of four channels; lanes under `turning` hold pairs 4 l .. 4 l + 3
-    const int turning = a.rot >> 3;
-    const int c0 = INTER ? 2 * l : l < turning ? l : 2 * l, c1 = INTER ? c0 + 1 : l < turning ? l + turning : 2 * l + 1;
-
-    auto source = [&](int r) -> const void * {
-        const T *p = r < a.Hq ? (const T *)a.q + (int64_t)tok * a.q_stride + r * D
-                     : r < a.Hq + a.Hkv ? (const T *)a.k + (int64_t)tok * a.k_stride + (r - a.Hq) * D
-                                        : (const T *)a.v + (int64_t)tok * a.v_stride + (r - a.Hq - a.Hkv) * D;
-        return p;
-    };
-    Eight<T> x[AHEAD];
-    auto load = [&](int base) {
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-            const int r = base + i * per_tok;
-            if (live && r < r1) x[i].template load<INTER>(source(r), c0, c1);
+// What a lane multiplies its channels by, from the weights w (NULL: ones) and the token's angles:
+//   lanes that turn: y0 <- y0 m[0] + y1 n[0] ..: the pair (a, b) of weights (u, v) becomes
+//   (a (u c) - b (v s), a (u s) + b (v c)), four numbers for each pair; others: y <- y m.
+struct Turn {
+    uint64_t m[4], n[4];
+    template <bool INTER> __device__ __forceinline__ void set(const float *w, const float2 *turn, bool turns, int c0, int c1) {
+        float4 u = make_float4(1.f, 1.f, 1.f, 1.f), v = u;
+        if (w) {
+            u = __ldg(reinterpret_cast<const float4 *>(w) + c0);
+            v = __ldg(reinterpret_cast<const float4 *>(w) + c1);
         }
-    };
-    load(r0 + step0);
-    // the tokens' angles, meanwhile
-    const int pairs = a.rot >> 1;
-    for (int i = tid; i < (pairs << a.tok_log); i += THREADS) {
-        const int w = i / pairs, p = i - w * pairs;
-        if (t0 + w < a.T) turn[w][p] = turn_of(a.positions[t0 + w], a.freq[p], a.amplitude);
+        m[0] = pack2(u.x, u.y), m[1] = pack2(u.z, u.w), m[2] = pack2(v.x, v.y), m[3] = pack2(v.z, v.w);
+        if (!turns) return;
+        const float4 p = reinterpret_cast<const float4 *>(turn)[0], q = reinterpret_cast<const float4 *>(turn)[1];
+        if constexpr (INTER) {  // pairs (0, 1), (2, 3), ..: y + its swap
+            n[0] = pack2(-u.y * p.y, u.x * p.y), n[1] = pack2(-u.w * p.w, u.z * p.w);
+            n[2] = pack2(-v.y * q.y, v.x * q.y), n[3] = pack2(-v.w * q.w, v.z * q.w);
+            m[0] = pack2(u.x * p.x, u.y * p.x), m[1] = pack2(u.z * p.z, u.w * p.z);
+            m[2] = pack2(v.x * q.x, v.y * q.x), m[3] = pack2(v.z * q.z, v.w * q.z);
+        } else {                // pairs (0, 4), (1, 5), ..
+            n[0] = pack2(-v.x * p.y, -v.y * p.w), n[1] = pack2(-v.z * q.y, -v.w * q.w);
+            n[2] = pack2(u.x * p.y, u.y * p.w), n[3] = pack2(u.z * q.y, u.w * q.w);
+            m[0] = pack2(u.x * p.x, u.y * p.z), m[1] = pack2(u.z * q.x, u.w * q.z);
+            m[2] = pack2(v.x * p.x, v.y * p.z), m[3] = pack2(v.z * q.x, v.w * q.z);
+        }
+    }
+    template <bool INTER> __device__ __forceinline__ void apply(uint64_t *y, bool turns) const {
+        if (!turns) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[i] = mul2(y[i], m[i]);
+        } else if constexpr (INTER) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = unpack2(y[i]);
+                y[i] = fma2(y[i], m[i], mul2(pack2(f.y, f.x), n[i]));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint64_t a = y[i], b = y[i + 2];
+                y[i] = fma2(a, m[i], mul2(b, n[i]));
+                y[i + 2] = fma2(b, m[i + 2], mul2(a, n[i + 2]));
+            }
+        }
+    }
+};
+
+// Rows of a unit in flight (two batches of them: the next one's loads are issued before this one is worked on).
+template <typename T> constexpr int AHEAD = sizeof(T) == 2 ? 2 : 1;
+
+// `n` rows of one kind, `step` elements apart in `in` and `out_step` in `out`: normed (where w), turned
+// (TURN) and stored; E4M3: as x / scale, the rows' scales `scale_step` apart.
+template <typename T, bool INTER, bool TURN, bool E4M3>
+__device__ __forceinline__ void unit_rows(const T *in, int step, char *out, int64_t out_step, int n, bool w, float eps, const Turn &tm,
+                                          bool turns, int c0, int c1, uint32_t lanes, const float *scale, int scale_step) {
+    constexpr int N = AHEAD<T>;
+    if (n <= 0) return;
+    Eight<T> x[N], next[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (i < n) x[i].template load<INTER>(in + i * step, c0, c1);
+    for (; n > 0; n -= N) {
+        in += N * step;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i + N < n) next[i].template load<INTER>(in + i * step, c0, c1);
+        float f[N];
+        if (TURN && w) {  // the norms of the batch's rows side by side
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                uint64_t y[4], ss;
+                x[i].get(y);
+                ss = mul2(y[0], y[0]);
+#pragma unroll
+                for (int e = 1; e < 4; ++e) ss = fma2(y[e], y[e], ss);
+                const float2 s = unpack2(ss);
+                f[i] = s.x + s.y;
+            }
+#pragma unroll
+            for (int o = 8; o; o >>= 1)
+#pragma unroll
+                for (int i = 0; i < N; ++i) f[i] += __shfl_xor_sync(lanes, f[i], o);
+#pragma unroll
+            for (int i = 0; i < N; ++i) f[i] = rsqrtf(fmaf(f[i], 1.f / D, eps));
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            uint64_t y[4];
+            if (TURN || E4M3) x[i].get(y);
+            if (TURN) {
+                if (w) {
+                    const uint64_t f2 = pack2(f[i], f[i]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y[e] = mul2(y[e], f2);
+                }
+                tm.apply<INTER>(y, turns);
+            }
+            if (i < n) {
+                if constexpr (E4M3) {
+                    const float sc = __ldg(scale + i * scale_step);
+                    const uint32_t lo = e4m3_4(y, sc), hi = e4m3_4(y + 2, sc);
+                    if constexpr (INTER) {
+                        *(reinterpret_cast<uint2 *>(out) + (c0 >> 1)) = make_uint2(lo, hi);
+                    } else {
+                        *(reinterpret_cast<uint32_t *>(out) + c0) = lo;
+                        *(reinterpret_cast<uint32_t *>(out) + c1) = hi;
+                    }
+                } else {
+                    if (TURN) x[i].set(y);
+                    x[i].template store<INTER>(out, c0, c1);
+                }
+            }
+            out += out_step;
+        }
+        if (E4M3) scale += N * scale_step;
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = next[i];
+    }
+}
+
+// LOG: a block takes 1 << LOG tokens, each by UNITS >> LOG units.
+template <typename T, int TO, bool INTER, int LOG>
+__global__ void __launch_bounds__(THREADS, 4) rope_kernel(const RopeArgs a) {
+    constexpr int PER = UNITS >> LOG;  // units of a token: each takes every PER-th row
+    __shared__ __align__(16) float2 turn[LOG == EACH ? 1 : 1 << LOG][PAIRS];
+    __align__(16) float2 own[4];
+    const float2 *angles = own;
+    const int tid = threadIdx.x, l = tid & 15, unit = tid >> 4;
+    const int mine = unit / PER, t0 = blockIdx.x << LOG, tok = t0 + mine;
+    // this lane's chunks of four channels; lanes under rot / 8 hold pairs 4 l .. 4 l + 3
+    const int turning = a.rot >> 3;
+    const bool turns = l < turning, live = tok < a.T;
+    const int c0 = INTER ? 2 * l : turns ? l : 2 * l, c1 = INTER ? c0 + 1 : turns ? l + turning : 2 * l + 1;
+    const int r0 = blockIdx.y * a.rows_per_y + (unit - mine * PER), r1 = (blockIdx.y + 1) * a.rows_per_y;
+    // the first row is on its way to the L2 cache while the angles are worked out
+    if (live && r0 < a.Hq)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"((const T *)a.q + (int64_t)tok * a.q_stride + (int64_t)r0 * D + c0 * 4));
+    // the tokens' angles
+    if constexpr (LOG == EACH) {
+        if (live && turns) {
+            const int pos = a.positions[tok];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) own[i] = turn_of(pos, a.freq[4 * l + i], a.amplitude);
+        }
+    } else {
+        const int pairs = a.rot >> 1;
+        for (int i = tid; i < (pairs << LOG); i += THREADS) {
+            const int w = i / pairs, p = i - w * pairs;
+            if (t0 + w < a.T) turn[w][p] = turn_of(a.positions[t0 + w], a.freq[p], a.amplitude);
+        }
+        angles = turn[mine] + 4 * l;
     }
     int64_t page = -1;
     int off = 0;
     if (TO != TO_ROWS && live) {
         const int64_t slot = a.slot_map[tok];
         if (slot >= a.n_slots) {
-            if (unit == mine * per_tok && l == 0 && blockIdx.y == 0 && a.err) atomicOr(a.err, KDA_DEVERR_PAGE);
+            if (unit == mine * PER && l == 0 && blockIdx.y == 0 && a.err) atomicOr(a.err, KDA_DEVERR_PAGE);
         } else if (slot >= 0) {
             if (a.n_slots <= (int64_t)UINT32_MAX) {
                 page = (uint32_t)slot / (uint32_t)a.page_size;
@@ -183,85 +332,55 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const RopeArgs a) {
             }
         }
     }
-    __syncthreads();
-    if (!live) return;  // (a whole unit: shuffles stay among its 16 lanes)
-    const uint32_t lanes = tid & 16 ? 0xffff0000u : 0x0000ffffu;
-    float2 cs[4];
-    if (l < turning) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) cs[i] = turn[mine][4 * l + i];
+    if (LOG != EACH) __syncthreads();
+    if (!live) return;
+    const uint32_t lanes = tid & 16 ? 0xffff0000u : 0x0000ffffu;  // (shuffles stay among a unit's lanes)
+    // the unit's rows among the block's, up to r1, of queries, keys and values, one kind after the other
+    auto first = [&](int from) { return r0 >= from ? r0 - from : (PER - 1) & (r0 - from); };  // within a kind that begins at `from`
+    auto count = [&](int f, int from, int rows) { return (min(rows, r1 - from) - f + PER - 1) / PER; };
+    constexpr int ES = (int)sizeof(T);
+    Turn tm;
+    {
+        const int h = first(0), n = count(h, 0, a.Hq);
+        tm.set<INTER>(a.q_weight, angles, turns, c0, c1);
+        unit_rows<T, INTER, true, false>((const T *)a.q + (int64_t)tok * a.q_stride + h * D, PER * D,
+                                         (char *)a.q_out + ((int64_t)tok * a.q_out_stride + h * D) * ES, PER * D * ES, n, a.q_weight,
+                                         a.eps, tm, turns, c0, c1, lanes, nullptr, 0);
     }
-    for (int base = r0 + step0; base < r1; base += AHEAD * per_tok) {
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-            const int r = base + i * per_tok;
-            if (r >= r1) break;
-            const bool is_q = r < a.Hq, is_v = TO != TO_ROWS && r >= a.Hq + a.Hkv;
-            float y[8];
-            const float *w = is_q ? a.q_weight : a.k_weight;
-            if (!is_v) {
-                x[i].get(y);
-                if (w) {
-                    float ss = 0.f;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
-#pragma unroll
-                    for (int o = 8; o; o >>= 1) ss += __shfl_xor_sync(lanes, ss, o);
-                    const float f = rsqrtf(fmaf(ss, 1.f / D, a.eps));
-                    const float4 wa = __ldg(reinterpret_cast<const float4 *>(w) + c0), wb = __ldg(reinterpret_cast<const float4 *>(w) + c1);
-                    y[0] *= f * wa.x, y[1] *= f * wa.y, y[2] *= f * wa.z, y[3] *= f * wa.w;
-                    y[4] *= f * wb.x, y[5] *= f * wb.y, y[6] *= f * wb.z, y[7] *= f * wb.w;
-                }
-                if (l < turning) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int u = INTER ? 2 * e : e, v = INTER ? 2 * e + 1 : e + 4;
-                        const float p = y[u], q = y[v];
-                        y[u] = p * cs[e].x - q * cs[e].y;
-                        y[v] = p * cs[e].y + q * cs[e].x;
-                    }
-                }
-            } else if (TO == TO_E4M3) {
-                x[i].get(y);
-            }
-            if (is_q) {
-                x[i].set(y);
-                x[i].template store<INTER>((T *)a.q_out + (int64_t)tok * a.q_out_stride + r * D, c0, c1);
-            } else if (TO == TO_ROWS) {
-                x[i].set(y);
-                x[i].template store<INTER>((T *)a.k_out + (int64_t)tok * a.k_out_stride + (r - a.Hq) * D, c0, c1);
-            } else if (page >= 0) {
-                const int h = r - a.Hq - (is_v ? a.Hkv : 0);
-                const int64_t at = page * a.page_stride + ((int64_t)h * a.page_size + off) * D;
-                if constexpr (TO == TO_E4M3) {
-                    char *row = (char *)(is_v ? a.v_cache : a.k_out) + at;
-                    const float sc = is_v ? a.v_scale[h] : a.k_scale[h];
-                    const uint32_t lo = e4m3_4(y, sc), hi = e4m3_4(y + 4, sc);
-                    if constexpr (INTER) {
-                        *(reinterpret_cast<uint2 *>(row) + l) = make_uint2(lo, hi);
-                    } else {
-                        *(reinterpret_cast<uint32_t *>(row) + c0) = lo;
-                        *(reinterpret_cast<uint32_t *>(row) + c1) = hi;
-                    }
-                } else {
-                    if (!is_v) x[i].set(y);
-                    x[i].template store<INTER>((T *)(is_v ? a.v_cache : a.k_out) + at, c0, c1);
-                }
-            }
-        }
-        load(base + AHEAD * per_tok);
+    if (TO != TO_ROWS && page < 0) return;
+    constexpr bool E4 = TO == TO_E4M3;
+    constexpr int CS = E4 ? 1 : ES;
+    const int h = first(a.Hq), n = count(h, a.Hq, a.Hkv);
+    if (n > 0) {
+        tm.set<INTER>(a.k_weight, angles, turns, c0, c1);
+        const T *in = (const T *)a.k + (int64_t)tok * a.k_stride + h * D;
+        if constexpr (TO == TO_ROWS)
+            unit_rows<T, INTER, true, false>(in, PER * D, (char *)a.k_out + ((int64_t)tok * a.k_out_stride + h * D) * ES, PER * D * ES, n,
+                                             a.k_weight, a.eps, tm, turns, c0, c1, lanes, nullptr, 0);
+        else
+            unit_rows<T, INTER, true, E4>(in, PER * D, (char *)a.k_out + (page * a.page_stride + ((int64_t)h * a.page_size + off) * D) * CS,
+                                          (int64_t)PER * a.page_size * D * CS, n, a.k_weight, a.eps, tm, turns, c0, c1, lanes,
+                                          E4 ? a.k_scale + h : nullptr, PER);
+    }
+    if constexpr (TO != TO_ROWS) {
+        const int from = a.Hq + a.Hkv, g = first(from);
+        unit_rows<T, INTER, false, E4>((const T *)a.v + (int64_t)tok * a.v_stride + g * D, PER * D,
+                                       (char *)a.v_cache + (page * a.page_stride + ((int64_t)g * a.page_size + off) * D) * CS,
+                                       (int64_t)PER * a.page_size * D * CS, count(g, from, a.Hkv), false, a.eps, tm, turns, c0, c1, lanes,
+                                       E4 ? a.v_scale + g : nullptr, PER);
     }
 }
 
 template <typename T, int TO>
-void launch_rope(const RopeArgs &a, bool inter, dim3 grid, cudaStream_t s) {
+void launch_rope(const RopeArgs &a, bool inter, int log, dim3 grid, cudaStream_t s) {
+    auto go = [&](auto kernel) { kernel<<<grid, THREADS, 0, s>>>(a); };
     if (inter)
-        rope_kernel<T, TO, true><<<grid, THREADS, 0, s>>>(a);
+        go(log == EACH ? rope_kernel<T, TO, true, EACH> : log == MANY ? rope_kernel<T, TO, true, MANY> : log == SOME ? rope_kernel<T, TO, true, SOME> : rope_kernel<T, TO, true, 0>);
     else
-        rope_kernel<T, TO, false><<<grid, THREADS, 0, s>>>(a);
+        go(log == EACH ? rope_kernel<T, TO, false, EACH> : log == MANY ? rope_kernel<T, TO, false, MANY> : log == SOME ? rope_kernel<T, TO, false, SOME> : rope_kernel<T, TO, false, 0>);
 }
 
-// The shape of a call, and what both calls check.
+// What both calls check.
 int check_rope(const void *q, const void *k, const int32_t *positions, const int64_t *freq, float amplitude,
                const float *q_weight, const float *k_weight, float eps, int64_t T, int Hq, int Hkv, int Dm, int rot,
                int layout, int dtype, int64_t q_stride, int64_t k_stride, const void *q_out, int64_t q_out_stride) {
@@ -282,20 +401,25 @@ int check_rope(const void *q, const void *k, const int32_t *positions, const int
     return KDA_OK;
 }
 
-// Tokens of a block and blocks of a token.
-dim3 rope_grid(RopeArgs &a, int rows) {
+// Tokens of a block (their logarithm) and blocks of a token.
+dim3 rope_grid(RopeArgs &a, int rows, int &log) {
     const int sms = device_sm_count();
-    a.tok_log = 0;
+    log = 0;
     a.rows_per_y = rows;
     int y = 1;
-    if ((int64_t)a.T * rows >= (int64_t)sms * 8 * UNITS * 12) {
-        a.tok_log = 2;
+    if (a.T >= 16 * sms) {
+        // Few rows: a unit works its token's angles out alone and waits for no other (20,000 tokens of 24 rows 42
+        // and 48 us, of 6 rows 17 us; eight tokens to a block 46, 47 and 26).  With 48 rows there are too few units
+        // left to fill the last wave (84 us eight tokens to a block, 89 one to a unit).
+        log = rows <= 24 ? EACH : MANY;
+    } else if (a.T >= 4 * sms) {  // (1,280 tokens of 48 rows: 8.9 us; 12.1 a block to each, 11.0 eight to a block)
+        log = SOME;
     } else {
         // a block to a token, or several to one where there are few: a row for each unit
         while (y * UNITS < rows && (int64_t)a.T * y < sms) ++y;
         a.rows_per_y = (rows + y - 1) / y;
     }
-    return dim3((unsigned)((a.T + (1 << a.tok_log) - 1) >> a.tok_log), (unsigned)y);
+    return dim3((unsigned)((a.T + (1 << log) - 1) >> log), (unsigned)y);
 }
 
 }  // namespace
@@ -355,13 +479,14 @@ int kda_qk_rope(const void *q, const void *k, const int32_t *positions, const in
     a.positions = positions, a.freq = freq, a.q_weight = q_weight, a.k_weight = k_weight;
     a.q_stride = q_stride, a.k_stride = k_stride, a.q_out_stride = q_out_stride, a.k_out_stride = k_out_stride;
     a.T = (int)T_total, a.Hq = Hq, a.Hkv = Hkv, a.rot = rot_dim, a.amplitude = amplitude, a.eps = eps;
-    const dim3 grid = rope_grid(a, Hq + Hkv);
+    int log;
+    const dim3 grid = rope_grid(a, Hq + Hkv, log);
     // (without rotation a lane's channels lie side by side)
     const bool inter = layout == KDA_ROPE_INTERLEAVED || rot_dim == 0;
     if (dtype == KDA_BF16)
-        launch_rope<__nv_bfloat16, TO_ROWS>(a, inter, grid, s);
+        launch_rope<__nv_bfloat16, TO_ROWS>(a, inter, log, grid, s);
     else
-        launch_rope<float, TO_ROWS>(a, inter, grid, s);
+        launch_rope<float, TO_ROWS>(a, inter, log, grid, s);
     note_launch("qk_rope", s);
     return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
@@ -392,14 +517,15 @@ int kda_paged_rope_append(const void *q, const void *k, const void *v, const int
     a.page_stride = page_stride, a.n_slots = (int64_t)n_pages * page_size;
     a.T = (int)T_total, a.Hq = Hq, a.Hkv = Hkv, a.rot = rot_dim, a.page_size = page_size;
     a.amplitude = amplitude, a.eps = eps;
-    const dim3 grid = rope_grid(a, Hq + 2 * Hkv);
+    int log;
+    const dim3 grid = rope_grid(a, Hq + 2 * Hkv, log);
     const bool inter = layout == KDA_ROPE_INTERLEAVED || rot_dim == 0;
     if (cache_dtype == KDA_E4M3)
-        launch_rope<__nv_bfloat16, TO_E4M3>(a, inter, grid, s);
+        launch_rope<__nv_bfloat16, TO_E4M3>(a, inter, log, grid, s);
     else if (dtype == KDA_BF16)
-        launch_rope<__nv_bfloat16, TO_PAGES>(a, inter, grid, s);
+        launch_rope<__nv_bfloat16, TO_PAGES>(a, inter, log, grid, s);
     else
-        launch_rope<float, TO_PAGES>(a, inter, grid, s);
+        launch_rope<float, TO_PAGES>(a, inter, log, grid, s);
     note_launch("paged_rope_append", s);
     return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
