@@ -620,7 +620,7 @@ int kda_paged_rope_append(const void *q, const void *k, const void *v, const int
  *   tokens       (device) int32 [N, W], written: d_0 .. d_{a-1}, the token drawn, then -1
  * The tests are exact.  Weights are summed as multiples of 2^-60 (p and q each rounded down),
  * so sums do not depend on their order and the same call gives the same tokens; values below
- * 0 or NaN count as 0, over 1 as 1.  A row that sums to 8 or more has no answer (some token).
+ * 0, of 2 and more, and NaN count as 0.  A row that sums to 8 or more has no answer (some token).
  * A drafted token outside 0 .. V-1 records KDA_DEVERR_TOKEN and is refused.  An n_draft out
  * of range records KDA_DEVERR_NUM_ACCEPTED: that request gets num_accepted 0 and tokens -1.
  * Rows without weight record KDA_DEVERR_PROBS, and the token drawn is -1.

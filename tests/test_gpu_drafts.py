@@ -83,16 +83,22 @@ def test_large_vocabularies(n, w, V, certain, dtype):
     assert torch.equal(out.gather(1, ref[:, None])[:, 0].long(), token)
 
 
-def test_padded_and_shifted_rows():
-    """Rows that lie apart, on 16 bytes and not: the same tokens."""
-    target, draft, tokens, u = draft_inputs(6, 4, 3001, seed=3)
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("certain", [False, True])
+@pytest.mark.parametrize("V", [3001, 2048, 5])
+def test_padded_and_shifted_rows(V, certain, dtype):
+    """Rows that lie apart, that begin on 16 bytes or not, p and q on the same place of them or not: the same tokens."""
+    target, draft, tokens, u = draft_inputs(6, 4, V, seed=3, dtype=dtype, certain=certain)
     want = verify(target, draft, tokens, u)
-    for pad, shift in ((7, 0), (7, 1), (1, 3), (71, 2)):
-        t = torch.full((6, 4, 3001 + pad + shift), float("nan"))
-        q = torch.full((6, 3, 3001 + pad + shift), float("nan"))
-        t[:, :, shift:shift + 3001] = target
-        q[:, :, shift:shift + 3001] = draft
-        t, q = t.to(DEV)[:, :, shift:shift + 3001], q.to(DEV)[:, :, shift:shift + 3001]
+    assert list(want[:2]) == list(verify_ref(target, tokens, u, draft))
+    for pad, shift, other in ((7, 0, 0), (7, 1, 1), (1, 3, 0), (71, 2, 5), (0, 7, 6), (8, 0, 1), (13, 4, 4)):
+        t = torch.full((6, 4, V + pad + shift), float("nan"), dtype=dtype)
+        t[:, :, shift:shift + V] = target
+        t, q = t.to(DEV)[:, :, shift:shift + V], None
+        if draft is not None:
+            q = torch.full((6, 3, V + pad + other), float("nan"), dtype=dtype)
+            q[:, :, other:other + V] = draft
+            q = q.to(DEV)[:, :, other:other + V]
         acc, out = kda.verify_drafts(t, tokens.to(DEV), u.to(DEV), draft=q)
         assert acc.tolist() == want[0] and out.tolist() == want[1]
 

@@ -56,6 +56,33 @@ def test_many_tokens_and_few_make_the_same_bits():
             assert torch.equal(a, q2[s]) and torch.equal(b, k2[s])
 
 
+@pytest.mark.parametrize("dtype,cache", [(BF16, BF16), (BF16, E4M3), (F32, F32)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_many_tokens_of_few_heads(interleaved, dtype, cache):
+    """A token to each unit of a block: the bits of a block for each token."""
+    T, hq, hkv, ps = 2501, 3, 1, 16
+    qkv, pos, qw, kw = inputs(T, hq, hkv, dtype, seed=13)
+    q, k, v = split(qkv, hq, hkv)
+    freq, _ = kda.rope_frequencies(96, device=DEV)
+    opts = dict(interleaved=interleaved, q_weight=qw, k_weight=kw)
+    q2, k2 = kda.qk_rope(q, k, pos, freq, **opts)
+    rope_close(q2[:50], *rope_ref(q[:50], pos[:50], freq.tolist(), 1.0, interleaved, qw, 1e-6), dtype)
+    ks = vs = None
+    if cache == E4M3:
+        ks, vs = torch.full((hkv,), 0.02, device=DEV), torch.full((hkv,), 0.03, device=DEV)
+    slots = torch.randperm(160 * ps, generator=torch.Generator().manual_seed(1))[:T].to(DEV)
+    (kc, vc), (kc2, vc2) = caches(160, hkv, ps, cache), caches(160, hkv, ps, cache)
+    q3 = kda.paged_rope_append(q, k, v, pos, slots, freq, kc, vc, k_scale=ks, v_scale=vs, **opts)
+    assert torch.equal(q3, q2)
+    for at in range(0, T, 500):
+        s = slice(at, at + 500)
+        a, b = kda.qk_rope(q[s], k[s], pos[s].contiguous(), freq, **opts)
+        assert torch.equal(a, q2[s]) and torch.equal(b, k2[s])
+        kda.paged_rope_append(q[s], k[s], v[s], pos[s].contiguous(), slots[s].contiguous(), freq, kc2, vc2, k_scale=ks, v_scale=vs, **opts)
+    raw = torch.uint8 if cache == E4M3 else cache
+    assert torch.equal(kc.view(raw), kc2.view(raw)) and torch.equal(vc.view(raw), vc2.view(raw))
+
+
 def test_far_positions_stretched():
     """Angles are exact modulo a turn at any position, negative ones too."""
     pos = torch.tensor([0, 1, -1, 999_999, 16_777_217, 2 ** 31 - 1, -2 ** 31, 123_456_789], dtype=torch.int32, device=DEV)
