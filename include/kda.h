@@ -618,17 +618,23 @@ int kda_paged_rope_append(const void *q, const void *k, const void *v, const int
  *   N >= 1, 1 <= W <= 32, 1 <= V < 2^31; dtype KDA_F32 or KDA_BF16, values 0 .. 1
  *   num_accepted (device) int32 [N], written: a
  *   tokens       (device) int32 [N, W], written: d_0 .. d_{a-1}, the token drawn, then -1
- * The tests are exact.  Weights are summed as multiples of 2^-60 (p and q each rounded down),
- * so sums do not depend on their order and the same call gives the same tokens; values below
- * 0, of 2 and more, and NaN count as 0.  A row that sums to 8 or more has no answer (some token).
+ *   workspace    kda_verify_drafts_workspace_size() bytes, 8-byte aligned; needs no initialisation, not
+ *                shared by calls in flight
+ * The tests are exact.  Weights are summed as multiples of 2^-60 (each, p - q exactly, rounded once),
+ * so sums do not depend on their order and the same call gives the same tokens; negative values
+ * and NaN count as 0.  A row with values of 2 and more, or one that sums to 8 or more, has no
+ * answer (some token, or -1).
  * A drafted token outside 0 .. V-1 records KDA_DEVERR_TOKEN and is refused.  An n_draft out
  * of range records KDA_DEVERR_NUM_ACCEPTED: that request gets num_accepted 0 and tokens -1.
  * Rows without weight record KDA_DEVERR_PROBS, and the token drawn is -1.
  * ------------------------------------------------------------------------ */
+size_t kda_verify_drafts_workspace_size(int N, int W, int V, int dtype);
+
 int kda_verify_drafts(const void *target, const void *draft, const int32_t *draft_tokens, const float *uniforms,
                       const int32_t *n_draft, int N, int W, int V, int dtype, int64_t target_seq_stride,
                       int64_t target_row_stride, int64_t draft_seq_stride, int64_t draft_row_stride,
-                      int32_t *num_accepted, int32_t *tokens, int32_t *error_word, kda_stream_t stream);
+                      int32_t *num_accepted, int32_t *tokens, void *workspace, size_t workspace_bytes,
+                      int32_t *error_word, kda_stream_t stream);
 
 /* --------------------------------------------------------------------------
  * kda_read_device_error -- synchronise `stream` and read the device error

@@ -15,7 +15,7 @@ from .kda import (KDAError, chunk_fwd, chunk_fwd_ckpt, chunk_fwd_noalloc, chunk_
                   chunk_fwd_workspace_size, decode_step, decode_step_fused, launch_count, library_path, load,
                   noalloc_read_device_error, planner_model, profile_collect, profile_enable, read_device_error,
                   segment_scan, segment_scan_auto_segments, segment_scan_workspace_size, set_wait_budget)
-from .drafts import verify_drafts
+from .drafts import verify_drafts, verify_drafts_workspace_size
 from .paged import paged_append, paged_attn, paged_attn_workspace_size, paged_tables
 from .rope import paged_rope_append, qk_rope, rope_frequencies
 
@@ -24,4 +24,4 @@ __all__ = ["KDAError", "chunk_fwd", "chunk_fwd_ckpt", "chunk_fwd_noalloc", "chun
            "noalloc_read_device_error", "paged_append", "paged_attn", "paged_attn_workspace_size", "paged_rope_append", "paged_tables",
            "planner_model", "profile_collect", "profile_enable", "qk_rope", "read_device_error", "rope_frequencies",
            "segment_scan", "segment_scan_auto_segments", "segment_scan_workspace_size", "set_wait_budget",
-           "verify_drafts"]
+           "verify_drafts", "verify_drafts_workspace_size"]

@@ -27,6 +27,7 @@ decltype(&kda_paged_attn_workspace_size) f_workspace = nullptr;
 decltype(&kda_qk_rope) f_rope = nullptr;
 decltype(&kda_paged_rope_append) f_rope_append = nullptr;
 decltype(&kda_verify_drafts) f_verify = nullptr;
+decltype(&kda_verify_drafts_workspace_size) f_verify_ws = nullptr;
 
 constexpr int64_t HEAD = 128;
 
@@ -339,10 +340,10 @@ PyObject *rope_append(PyObject *, PyObject *const *args, Py_ssize_t n_args) {
     });
 }
 
-// verify(target, draft_tokens, uniforms, draft, n_draft, error_word)
+// verify(target, draft_tokens, uniforms, draft, n_draft, workspace, error_word)
 PyObject *verify(PyObject *, PyObject *const *args, Py_ssize_t n_args) {
     return guarded([&]() -> PyObject * {
-        if (n_args != 6 || !f_verify) throw No();
+        if (n_args != 7 || !f_verify) throw No();
         const Arg *a = reinterpret_cast<const Arg *>(args);
         const at::Tensor &p = a[0].tensor();
         if (!p.is_cuda() || p.dim() != 3 || p.size(1) < 2) throw No();
@@ -367,25 +368,36 @@ PyObject *verify(PyObject *, PyObject *const *args, Py_ssize_t n_args) {
         const at::Tensor &d = given(a[1], at::kInt, dev), &u = given(a[2], at::kFloat, dev);
         if (d.dim() != 2 || d.size(0) != n || d.size(1) != w - 1 || u.dim() != 2 || u.size(0) != n || u.size(1) != w) throw No();
         const int32_t *m = (const int32_t *)optional(a[4], at::kInt, dev, n);
-        void *err = optional(a[5], at::kInt, dev);
+        void *err = optional(a[6], at::kInt, dev);
         const c10::cuda::OptionalCUDAGuard guard(p.device());
-        at::Tensor acc = at::empty({n}, d.options()), out = at::empty({n, w}, d.options());
+        at::Tensor acc = at::empty({n}, d.options()), out = at::empty({n, w}, d.options()), ws;
+        void *work = nullptr;
+        size_t bytes = 0;
+        if (!a[5].none()) {
+            const at::Tensor &given_ws = a[5].tensor();
+            if (!given_ws.is_cuda() || !given_ws.is_contiguous() || given_ws.get_device() != dev) throw No();
+            work = given_ws.data_ptr();
+            bytes = given_ws.nbytes();
+        } else if ((bytes = f_verify_ws(as_int(n), as_int(w), as_int(v), code_of(t)))) {
+            ws = at::empty({(int64_t)bytes}, d.options().dtype(at::kByte));
+            work = ws.data_ptr();
+        }
         const int rc = f_verify(tp, dp, (const int32_t *)d.data_ptr(), (const float *)u.data_ptr(), m, as_int(n), as_int(w), as_int(v),
-                                code_of(t), ts, tr, ds, dr, (int32_t *)acc.data_ptr(), (int32_t *)out.data_ptr(), (int32_t *)err,
+                                code_of(t), ts, tr, ds, dr, (int32_t *)acc.data_ptr(), (int32_t *)out.data_ptr(), work, bytes, (int32_t *)err,
                                 stream_of(dev));
         if (rc != KDA_OK) throw No();
         return tuple_of({&acc, &out});
     });
 }
 
-// init(tables, append, attn, workspace size, rope, rope_append, verify): addresses of the library's functions
+// init(tables, append, attn, workspace size, rope, rope_append, verify, workspace size): addresses of the library's functions
 PyObject *init(PyObject *, PyObject *const *args, Py_ssize_t n) {
-    void *p[7];
-    if (n != 7) {
-        PyErr_SetString(PyExc_TypeError, "init takes seven addresses");
+    void *p[8];
+    if (n != 8) {
+        PyErr_SetString(PyExc_TypeError, "init takes eight addresses");
         return nullptr;
     }
-    for (int i = 0; i < 7; ++i) {
+    for (int i = 0; i < 8; ++i) {
         p[i] = PyLong_AsVoidPtr(args[i]);
         if (PyErr_Occurred()) return nullptr;
     }
@@ -396,6 +408,7 @@ PyObject *init(PyObject *, PyObject *const *args, Py_ssize_t n) {
     f_rope = reinterpret_cast<decltype(f_rope)>(p[4]);
     f_rope_append = reinterpret_cast<decltype(f_rope_append)>(p[5]);
     f_verify = reinterpret_cast<decltype(f_verify)>(p[6]);
+    f_verify_ws = reinterpret_cast<decltype(f_verify_ws)>(p[7]);
     Py_RETURN_NONE;
 }
 

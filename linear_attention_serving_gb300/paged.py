@@ -45,7 +45,7 @@ def _load_fast(lib):
     spec.loader.exec_module(fast)
     fast.init(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
         lib.kda_paged_tables, lib.kda_paged_append, lib.kda_paged_attn_sinks, lib.kda_paged_attn_workspace_size,
-        lib.kda_qk_rope, lib.kda_paged_rope_append, lib.kda_verify_drafts)))
+        lib.kda_qk_rope, lib.kda_paged_rope_append, lib.kda_verify_drafts, lib.kda_verify_drafts_workspace_size)))
     _fast_tables, _fast_append, _fast_attn = fast.tables, fast.append, fast.attn
     _fast_rope, _fast_rope_append, _fast_verify = fast.rope, fast.rope_append, fast.verify
 
@@ -64,7 +64,9 @@ def _lib():
         lib.kda_qk_rope.argtypes = [P, P, P, P, F, P, P, F, L, I, I, I, I, I, I, L, L, P, P, L, L, P]
         lib.kda_paged_rope_append.argtypes = [P, P, P, P, P, P, F, P, P, F, L, I, I, I, I, I, I, I, L, L, L, P, L, P, P, P, P, I,
                                               I, L, P, P]
-        lib.kda_verify_drafts.argtypes = [P, P, P, P, P, I, I, I, I, L, L, L, L, P, P, P, P]
+        lib.kda_verify_drafts.argtypes = [P, P, P, P, P, I, I, I, I, L, L, L, L, P, P, P, S, P, P]
+        lib.kda_verify_drafts_workspace_size.argtypes = [I, I, I, I]
+        lib.kda_verify_drafts_workspace_size.restype = S
         lib.kda_paged_attn_workspace_size.argtypes = [L, I, I, I]
         lib.kda_paged_attn_workspace_size.restype = S
         try:

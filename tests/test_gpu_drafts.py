@@ -169,6 +169,43 @@ def test_values_that_are_no_probabilities():
     assert err == 0 and acc == [1] and out == [[1, 3]]
 
 
+@pytest.mark.parametrize("n", [3, 100])
+def test_rows_that_sum_to_too_much(n):
+    """No answer, but a token or -1, and nothing read or written elsewhere."""
+    target = torch.ones(n, 2, 5000, device=DEV)
+    tokens = torch.zeros(n, 1, dtype=torch.int32, device=DEV)
+    for draft in (None, 0.5 * target[:, :1]):
+        for r in (0.0, 0.3, 0.77, 1.0):
+            acc, out = kda.verify_drafts(target, tokens, torch.full((n, 2), r, device=DEV), draft=draft)
+            assert ((out >= -1) & (out < 5000)).all() and ((acc >= 0) & (acc <= 1)).all()
+
+
+@pytest.mark.parametrize("V", [7, 600, 5003])
+@pytest.mark.parametrize("n", [77, 1000])
+def test_many_requests(n, V):
+    """Over the number that get a cluster each: a line of all their segments."""
+    target, draft, tokens, u = draft_inputs(n, 3, V, seed=n + V)
+    target[5], target[n - 1, 2] = 0, 0
+    draft[7] = target[7, :2]  # (refused with nothing left beside: p itself)
+    u[7, 0], tokens[9, 1] = 0.9999999, V
+    m = (torch.arange(n) % 3).int()
+    m[11], m[13] = 3, -1
+    acc, out, err = verify(target, draft, tokens, u, m)
+    keep = [i for i in range(min(n, 150)) if i not in (5, 9, 11, 13)]
+    ref = verify_ref(target[keep], tokens[keep], u[keep], draft[keep], m[keep])
+    assert [acc[i] for i in keep] == ref[0] and [out[i] for i in keep] == ref[1]
+    assert acc[5] == 0 and out[5] == out[11] == out[13] == [-1] * 3
+    assert err & ~drafts.DEVERR_TOKEN == 2 | drafts.DEVERR_PROBS
+    # as in calls of few requests
+    for at in range(0, n, 70):
+        s = slice(at, at + 70)
+        a, o, _ = verify(target[s], draft[s], tokens[s], u[s], m[s])
+        assert a == acc[s] and o == out[s]
+    p = draft_inputs(n, 3, V, seed=3, certain=True)
+    assert list(verify(*p)[:2]) == [sum(x, []) for x in zip(*(verify(*(None if t is None else t[i:i + 60] for t in p))[:2]
+                                                              for i in range(0, n, 60)))]
+
+
 def test_the_law():
     """Whatever the draft, the first token is distributed as the target says: 200,000 requests, every share within
     5 standard deviations."""
@@ -190,16 +227,17 @@ def test_writes_nothing_else_and_replays():
     target, draft, tokens, u = dev(*draft_inputs(9, 5, 20_000, seed=5))
     lib = paged._lib()
     acc, out = Guarded((9,), torch.int32), Guarded((9, 5), torch.int32)
+    ws = Guarded((kda.verify_drafts_workspace_size(9, 5, 20_000),), torch.uint8)
     p = lambda x: x.data_ptr()  # noqa: E731
 
     def call():
         rc = lib.kda_verify_drafts(p(target), p(draft), p(tokens), p(u), None, 9, 5, 20_000, 1, 100_000, 20_000, 80_000, 20_000, p(acc.t),
-                                   p(out.t), None, torch.cuda.current_stream().cuda_stream)
+                                   p(out.t), p(ws.t), ws.t.nbytes, None, torch.cuda.current_stream().cuda_stream)
         assert rc == 0
 
     call()
     want = kda.verify_drafts(target, tokens, u, draft=draft)
-    assert acc.intact() and out.intact()
+    assert acc.intact() and out.intact() and ws.intact()
     assert torch.equal(acc.t, want[0]) and torch.equal(out.t, want[1])
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):

@@ -41,7 +41,7 @@ def sinks(**kw):
 
 def verify(**kw):
     a = dict(p=ADDR[0], q=ADDR[1], tokens=ADDR[2], u=ADDR[3], m=None, n=2, w=5, V=100, dt=1, ts=500, tr=100, ds=400, dr=100, acc=ADDR[4],
-             out=ADDR[5], err=None, s=None)
+             out=ADDR[5], ws=None, wsb=0, err=None, s=None)
     a.update(kw)
     return paged._lib().kda_verify_drafts(*a.values())
 
@@ -84,7 +84,8 @@ def test_sinks_refusals(kw, rc):
     (dict(out=None), INVALID), (dict(tokens=None), INVALID), (dict(p=ctypes.c_void_p((1 << 20) + 2)), INVALID),
     (dict(q=ctypes.c_void_p((1 << 20) + 1), dt=0), INVALID), (dict(tr=99), INVALID), (dict(dr=99), INVALID), (dict(ts=-1), INVALID),
     (dict(ds=-1), INVALID), (dict(acc=ADDR[5]), INVALID), (dict(out=ADDR[2]), INVALID), (dict(acc=ADDR[3]), INVALID),
-    (dict(m=ADDR[4]), INVALID), (dict(out=ADDR[0]), INVALID)])
+    (dict(m=ADDR[4]), INVALID), (dict(out=ADDR[0]), INVALID), (dict(), WORKSPACE), (dict(ws=FAKE, wsb=15), WORKSPACE),
+    (dict(ws=ODD, wsb=1 << 30), WORKSPACE)])
 def test_verify_refusals(kw, rc):
     assert verify(**kw) == rc
 
@@ -113,6 +114,12 @@ def test_frequencies(rot, kw):
 def test_frequencies_refusals(kw):
     with pytest.raises(kda.KDAError):
         kda.rope_frequencies(**{"rot_dim": 64, **kw})
+
+
+def test_verify_workspace_size():
+    f = kda.verify_drafts_workspace_size
+    assert 0 < f(1, 5, 32768) < f(500, 5, 32768) < f(500, 5, 65536) and f(500, 5, 65536, torch.bfloat16) > 0
+    assert f(0, 5, 100) == f(5, 0, 100) == f(5, 33, 100) == f(5, 5, 0) == f(500, 5, 100, torch.float16) == 0
 
 
 def test_binding_refuses_host_tensors():
