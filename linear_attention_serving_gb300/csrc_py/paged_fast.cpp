@@ -116,12 +116,12 @@ kda_stream_t stream_of(int device) {
     return (kda_stream_t)c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream();
 }
 
-// numel elements of x from `first` on, of the same storage (the integers below: nothing
-// to differentiate, so the tensor is made without the dispatcher)
-at::Tensor part(const at::Tensor &x, int64_t first, int64_t numel) {
+// The elements of x from `first` on, of the same storage, in a shape of their own (results of
+// these calls: nothing to differentiate, so the tensor is made without the dispatcher)
+at::Tensor part(const at::Tensor &x, int64_t first, at::IntArrayRef sizes) {
     auto impl = c10::make_intrusive<c10::TensorImpl>(c10::Storage(x.storage()), x.key_set(), x.dtype());
     impl->set_storage_offset(x.storage_offset() + first);
-    impl->set_sizes_contiguous({numel});
+    impl->set_sizes_contiguous(sizes);
     return at::Tensor(std::move(impl));
 }
 
@@ -163,8 +163,8 @@ PyObject *tables(PyObject *, PyObject *const *args, Py_ssize_t n_args) {
         const c10::cuda::OptionalCUDAGuard guard(nw.device());
         const auto i32 = nw.options();
         at::Tensor slots = at::empty({T}, i32.dtype(at::kLong)), ints = at::empty({T + 2 * n + 2}, i32);
-        at::Tensor pos = part(ints, 0, T), cu = part(ints, T, n + 1), kv = part(ints, T + n + 1, n),
-                   head = part(ints, T + 2 * n + 1, 1);
+        at::Tensor pos = part(ints, 0, {T}), cu = part(ints, T, {n + 1}), kv = part(ints, T + n + 1, {n}),
+                   head = part(ints, T + 2 * n + 1, {1});
         const int rc = f_tables((const int32_t *)nw.data_ptr(), (const int32_t *)cx.data_ptr(), as_int(n), T,
                                 (int32_t *)tab.data_ptr(), as_int(tab.size(1)), (const int32_t *)fp.data_ptr(),
                                 as_int(fp.numel()), (const int32_t *)fh.data_ptr(), (int32_t *)head.data_ptr(),
@@ -298,7 +298,17 @@ PyObject *rope(PyObject *, PyObject *const *args, Py_ssize_t n_args) {
         const float *qw = (const float *)optional(a[6], at::kFloat, dev, HEAD), *kw = (const float *)optional(a[7], at::kFloat, dev, HEAD);
         const c10::cuda::OptionalCUDAGuard guard(q.device());
         at::Tensor qo, ko;
-        const Rows qor = rows_like(a[9], qo, q, t, dev), kor = rows_like(a[10], ko, k, t, dev);
+        Rows qor, kor;
+        if (a[9].none() && a[10].none()) {  // (one allocation for both)
+            const at::Tensor buf = at::empty({q.numel() + k.numel()}, q.options());
+            qo = part(buf, 0, q.sizes());
+            ko = part(buf, q.numel(), k.sizes());
+            qor = rows_of(qo, t, dev);
+            kor = rows_of(ko, t, dev);
+        } else {
+            qor = rows_like(a[9], qo, q, t, dev);
+            kor = rows_like(a[10], ko, k, t, dev);
+        }
         const int rc = f_rope(qr.p, kr.p, (const int32_t *)pos.data_ptr(), freq, (float)a[4].real(), qw, kw, (float)a[8].real(), qr.T,
                               qr.heads, kr.heads, (int)HEAD, rot, truth(a[5]) ? KDA_ROPE_INTERLEAVED : KDA_ROPE_HALF, code_of(t),
                               qr.stride, kr.stride, qor.p, kor.p, qor.stride, kor.stride, stream_of(dev));
@@ -370,7 +380,8 @@ PyObject *verify(PyObject *, PyObject *const *args, Py_ssize_t n_args) {
         const int32_t *m = (const int32_t *)optional(a[4], at::kInt, dev, n);
         void *err = optional(a[6], at::kInt, dev);
         const c10::cuda::OptionalCUDAGuard guard(p.device());
-        at::Tensor acc = at::empty({n}, d.options()), out = at::empty({n, w}, d.options()), ws;
+        const at::Tensor ints = at::empty({n * (w + 1)}, d.options());
+        at::Tensor acc = part(ints, 0, {n}), out = part(ints, n, {n, w}), ws;
         void *work = nullptr;
         size_t bytes = 0;
         if (!a[5].none()) {
