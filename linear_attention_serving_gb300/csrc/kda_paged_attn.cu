@@ -141,6 +141,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) paged_join_kernel(PagedAttn a
 }
 
 constexpr int FEW_ROWS = 16;
+constexpr int KEY_TILE = 128, ALONE_TILES = 16384;
 
 int launch_join(const PagedAttn &a, const JoinSet &s0, const JoinSet &s1, int64_t max_rows, bool f32, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
@@ -254,7 +255,11 @@ int kda_paged_attn_sinks(const void *q, const void *k_cache, const void *v_cache
     const bool tiles = cache_dtype == KDA_BF16 && a.G <= 128 && max_rows > FEW_ROWS;
     // every request long enough for the tile kernel: one of T_total tokens, or all
     // of max_q (the offsets may still say less: the tile kernel then takes that too)
-    const bool few = !tiles || (a.G <= FEW_ROWS && n_seqs > 1 && T_total != (int64_t)n_seqs * a.max_q);
+    // or, in calls with sinks, whose windows bound what there is to read: single tokens cost the tile kernel
+    // some 0.14 us a key tile and SM more, and a launch of their own 15 to 20 us (24 of them beside 8
+    // chunks, window 700, 91 us for 107; 200 over 800 keys beside one chunk 173 for 177; 100 over 4,000 keys 468 for 454).
+    const bool alone = a.sinks > 0 && (int64_t)n_seqs * Hkv * (((int64_t)a.window + a.sinks) / KEY_TILE + 2) <= ALONE_TILES;
+    const bool few = !tiles || (!alone && a.G <= FEW_ROWS && n_seqs > 1 && T_total != (int64_t)n_seqs * a.max_q);
     if (few) {
         if (tiles) a.row_hi = FEW_ROWS;
         js[0] = use(w.rows, paged_few_blocks());

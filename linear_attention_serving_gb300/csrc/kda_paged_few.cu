@@ -734,7 +734,9 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
             // scores; -inf where a row does not see this key (rows that do: [first, last))
             auto scores = [&]() {
                 tmem_row<NR>(ts, t);
-                if (key0 + BK - 1 > pos || key0 + BK > hi || SINK || a.window > 0) {
+                // (SINK: only where a key outside the sinks leaves the last query's window)
+                const bool leaves = SINK ? key0 + BK > a.sinks && key0 <= hi - 1 - a.near : a.window > 0;
+                if (key0 + BK - 1 > pos || key0 + BK > hi || leaves) {
                     const int window = SINK ? a.near : a.window;
                     const bool far = SINK ? key >= a.sinks : window > 0;  // (a key that leaves the window)
                     const int d = min(max(key - pos, 0), NR + 1), u = far ? min(max(key - pos + window, 0), NR + 1) : NR + 1;
