@@ -241,10 +241,11 @@ def paged_attn(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q=0, sm_scale
     if workspace is None:
         workspace = q.new_empty(lib.kda_paged_attn_workspace_size(T, n, hq, hkv), dtype=torch.uint8)
     with torch.cuda.device(index):
-        rc = lib.kda_paged_attn_sinks(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), cu_q.data_ptr(),
-                                      kv_len.data_ptr(), n, T, max_q, hq, hkv, D, _CODE[dtype], code, _p(k_scale), _p(v_scale),
-                                      n_pages, ps, stride, block_table.shape[1], sm_scale, window, sinks, out.data_ptr(),
-                                      lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, _p(error_word), _raw_stream(index))
+        call, beside = (lib.kda_paged_attn_sinks, (sinks,)) if sinks else (lib.kda_paged_attn, ())
+        rc = call(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(),
+                  n, T, max_q, hq, hkv, D, _CODE[dtype], code, _p(k_scale), _p(v_scale), n_pages, ps, stride,
+                  block_table.shape[1], sm_scale, window, *beside, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+                  workspace.nbytes, _p(error_word), _raw_stream(index))
     if rc:
         _check(rc, "kda_paged_attn")
     return out, lse
