@@ -713,7 +713,7 @@ __device__ __forceinline__ void tmem_row(uint32_t taddr, float *o) {
 // that runs out is passed on at the group's next meeting (every segment begins with one,
 // every meeting looks for it), so that a group's warps leave together; the groups wait
 // for each other with bounded waits only.
-template <bool E4, int NR, bool SINK, class Gate>
+template <bool E4, int NR, int U, bool SINK, class Gate>
 __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, uint32_t tmem, const Gate &gate) {
     using C = Cfg<E4, NR>;
     const Bars<C> bar(sm);
@@ -761,13 +761,13 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
                     const int d = min(max(key - pos, 0), NR + 1), u = far ? min(max(key - pos + window, 0), NR + 1) : NR + 1;
                     const int first = key < hi ? d * G - r0 : NR, last = u > NR ? NR : u * G - r0;
 #pragma unroll
-                    for (int r = 0; r < NR; ++r) t[r] = r >= first && r < last ? t[r] : -INFINITY;
+                    for (int r = 0; r < U; ++r) t[r] = r >= first && r < last ? t[r] : -INFINITY;
                 }
             };
             // the exponents: t sc - ref
             auto exponents = [&]() {
 #pragma unroll
-                for (int r = 0; r < NR; r += 4) {
+                for (int r = 0; r < U; r += 4) {
                     const float4 y = *reinterpret_cast<const float4 *>(ref + r);
                     const float4 f = E4 ? *reinterpret_cast<const float4 *>(sc + r)
                                         : make_float4(a.scale_log2, a.scale_log2, a.scale_log2, a.scale_log2);
@@ -783,7 +783,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
                 exponents();
                 float m0 = max3(t[0], t[1], t[2]), m1 = t[3];
 #pragma unroll
-                for (int r = 4; r < NR; r += 4) {
+                for (int r = 4; r < U; r += 4) {
                     m0 = max3(m0, t[r], t[r + 1]);
                     m1 = max3(m1, t[r + 2], t[r + 3]);
                 }
@@ -800,7 +800,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
                 {
                     float m[NR];
 #pragma unroll
-                    for (int r = 0; r < NR; ++r) m[r] = t[r] * (E4 ? sc[r] : a.scale_log2);
+                    for (int r = 0; r < NR; ++r) m[r] = r < U ? t[r] * (E4 ? sc[r] : a.scale_log2) : -INFINITY;
                     across<NR, true>(m, lane);
                     reinterpret_cast<float *>(pb)[warp * NR + first_of<NR>(lane)] = m[0];
                 }
@@ -835,13 +835,15 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
                     }
                     tmem_st_wait();
 #pragma unroll
-                    for (int r = 0; r < NR; ++r) l[r] *= fac[r];
+                    for (int r = 0; r < U; ++r) l[r] *= fac[r];
                 }
                 exponents();
             }
             uint32_t p[NR / 2];
 #pragma unroll
-            for (int r = 0; r < NR; r += 2) {
+            for (int r = U; r < NR; r += 2) p[r / 2] = 0;
+#pragma unroll
+            for (int r = 0; r < U; r += 2) {
                 const float e0 = ex2(t[r]), e1 = ex2(t[r + 1]);
                 l[r] += e0;
                 l[r + 1] += e1;
@@ -968,7 +970,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttn &a, uint8_t *sm, ui
     }
 }
 
-template <bool E4, int NR, bool SHORT, bool SINK>
+template <bool E4, int NR, int U, bool SHORT, bool SINK>
 __global__ void __launch_bounds__(Cfg<E4, NR>::THREADS, 1)
     paged_few_kernel(const __grid_constant__ PagedMaps maps, const __grid_constant__ PagedAttn a, int min_per) {
     using C = Cfg<E4, NR>;
@@ -1043,7 +1045,7 @@ __global__ void __launch_bounds__(Cfg<E4, NR>::THREADS, 1)
     const uint32_t tmem = sh->tmem;
     const Waits<SHORT> gate{&sh->abort, a.err, a.wait_budget};
     if (warp < C::SOFT) {
-        softmax_role<E4, NR, SINK>(a, sm, tmem, gate);
+        softmax_role<E4, NR, U, SINK>(a, sm, tmem, gate);
     } else if (warp == C::W_S) {
         s_role<E4, NR>(sm, tmem, gate);
     } else if (warp == C::W_O) {
@@ -1072,20 +1074,20 @@ __global__ void __launch_bounds__(Cfg<E4, NR>::THREADS, 1)
     }
 }
 
-template <bool E4, int NR, bool SHORT, bool SINK>
+template <bool E4, int NR, int U, bool SHORT, bool SINK>
 int launch_for(const PagedAttn &a, const PagedMaps &maps, cudaStream_t s) {
     using C = Cfg<E4, NR>;
-    const int rc = prepare_kernel((const void *)paged_few_kernel<E4, NR, SHORT, SINK>, C::SMEM, C::THREADS, nullptr);
+    const int rc = prepare_kernel((const void *)paged_few_kernel<E4, NR, U, SHORT, SINK>, C::SMEM, C::THREADS, nullptr);
     if (rc) return rc;
-    paged_few_kernel<E4, NR, SHORT, SINK><<<paged_few_blocks(), C::THREADS, C::SMEM, s>>>(maps, a, 3);
+    paged_few_kernel<E4, NR, U, SHORT, SINK><<<paged_few_blocks(), C::THREADS, C::SMEM, s>>>(maps, a, 3);
     note_launch("paged_few", s);
     return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
-template <bool E4, int NR>
+template <bool E4, int NR, int U = NR>
 int launch(const PagedAttn &a, const PagedMaps &maps, cudaStream_t s) {
     const bool brief = a.wait_budget < SHORT_BUDGET;
-    if (a.sinks > 0) return brief ? launch_for<E4, NR, true, true>(a, maps, s) : launch_for<E4, NR, false, true>(a, maps, s);
-    return brief ? launch_for<E4, NR, true, false>(a, maps, s) : launch_for<E4, NR, false, false>(a, maps, s);
+    if (a.sinks > 0) return brief ? launch_for<E4, NR, U, true, true>(a, maps, s) : launch_for<E4, NR, U, false, true>(a, maps, s);
+    return brief ? launch_for<E4, NR, U, true, false>(a, maps, s) : launch_for<E4, NR, U, false, false>(a, maps, s);
 }
 
 }  // namespace
@@ -1104,6 +1106,7 @@ int launch_paged_few(PagedAttn a, int cache_dtype, const void *k, const void *v,
     if (a.sinks > 0) sinks_of(a, BK);
     const bool e4 = cache_dtype == KDA_E4M3;
     if (max_rows <= 16) return e4 ? launch<true, 16>(a, maps, s) : launch<false, 16>(a, maps, s);
+    if (e4 && max_rows <= 24) return launch<true, 32, 24>(a, maps, s);
     return e4 ? launch<true, 32>(a, maps, s) : launch<false, 32>(a, maps, s);
 }
 
