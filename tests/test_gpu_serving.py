@@ -1,0 +1,74 @@
+"""The calls of a served step with drafts together: projections turned and appended, attention through a
+window beside sinks, verification, and the decode step that takes what it says."""
+import importlib.util
+import os
+
+import pytest
+import torch
+
+from serving_testutil import verify_ref
+
+pytestmark = pytest.mark.gpu
+
+
+def example():
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "draft_serving.py")
+    spec = importlib.util.spec_from_file_location("draft_serving", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
+def test_drafts_step_by_step_against_one_pass():
+    """Refused drafts leave no trace: the committed streams' probabilities are those of one pass, up to a few
+    roundings to bf16 (2^-9 of each value on average) on the way, and a replayed step commits the same tokens as a
+    launched one."""
+    e = example()
+    off, streams, stood = e.main()
+    assert off < 2e-2
+    assert 0.05 < stood < 0.95  # both refused and accepted drafts are met
+    off2, streams2, _ = e.main(replay=False)
+    assert streams2 == streams and off2 < 2e-2
+
+
+def test_each_step_verifies_as_the_plain_form_does():
+    e = example()
+    w = e.Weights(seed=4)
+    server = e.Server(w, 3, 4, 12)
+    g = torch.Generator().manual_seed(8)
+    ctx = [0] * 3
+    for _ in range(12):
+        u = torch.rand(3, 9, generator=g).cuda()
+        window, p, accepted, tokens = server.step(u[:, :4].contiguous(), u[:, 4:].contiguous())
+        prob = torch.stack([w.draft[window[:, j].long()] for j in range(4)], 1)
+        ref = verify_ref(p.cpu(), window[:, 1:].cpu(), u[:, 4:].cpu(), prob.cpu())
+        assert accepted.tolist() == ref[0] and tokens.tolist() == ref[1]
+        ctx = [c + 1 + a for c, a in zip(ctx, ref[0])]
+        assert server.ctx.tolist() == ctx and server.token.tolist() == [t[a] for t, a in zip(ref[1], ref[0])]
+    assert int(server.error) == 0
+
+
+def test_two_streams_do_not_mix():
+    """Calls of two servers on streams of their own, enqueued in turn: each as alone."""
+    e = example()
+    w = e.Weights(seed=1)
+    g = torch.Generator().manual_seed(2)
+    u = torch.rand(10, 2, 4, 5, generator=g).cuda()
+
+    def run(streams):
+        torch.manual_seed(0)
+        servers = [e.Server(w, 4, 2, 10) for _ in range(2)]
+        torch.cuda.synchronize()
+        out = [[], []]
+        for i in range(10):
+            for k in range(2):
+                with torch.cuda.stream(streams[k]):
+                    out[k].append(servers[k].step(u[i, k, :, :2].contiguous(), u[i, k, :, 2:].contiguous()))
+        torch.cuda.synchronize()
+        assert all(int(s.error) == 0 for s in servers)
+        return [[t for step in o for t in step] for o in out]
+
+    one = torch.cuda.current_stream()
+    alone, beside = run([one, one]), run([torch.cuda.Stream(), torch.cuda.Stream()])
+    for a, b in zip(alone, beside):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
