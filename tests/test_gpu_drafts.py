@@ -268,3 +268,33 @@ def test_plain_binding_and_refusals(monkeypatch):
     monkeypatch.setattr(paged, "_fast_verify", lambda *a: None)
     got = kda.verify_drafts(target, tokens, u, draft=draft)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_calls_on_two_streams_at_once():
+    """Each with a workspace of its own (the binding's, or the caller's)."""
+    sets = [dev(*draft_inputs(150, 4, 30_000, seed=i)) for i in range(2)]
+    want = [kda.verify_drafts(t, d, u, draft=q) for t, q, d, u in sets]
+    size = kda.verify_drafts_workspace_size(150, 4, 30_000)
+    ws = [torch.empty(size, dtype=torch.uint8, device=DEV) for _ in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    out = [[], []]
+    for i in range(20):
+        for k, (t, q, d, u) in enumerate(sets):
+            with torch.cuda.stream(streams[k]):
+                out[k].append(kda.verify_drafts(t, d, u, draft=q, workspace=ws[k] if i % 2 else None))
+    torch.cuda.synchronize()
+    for k in range(2):
+        for acc, tokens in out[k]:
+            assert torch.equal(acc, want[k][0]) and torch.equal(tokens, want[k][1])
+
+
+def test_requests_that_share_their_rows():
+    """A stride of zero: one distribution for all requests."""
+    p, q, tokens, u = draft_inputs(1, 3, 5000, seed=4)
+    n = 200
+    g = torch.Generator().manual_seed(1)
+    u, tokens = torch.rand(n, 3, generator=g), tokens.repeat(n, 1)
+    wide = verify(p.repeat(n, 1, 1), q.repeat(n, 1, 1), tokens, u)
+    acc, out = kda.verify_drafts(p.to(DEV).expand(n, 3, 5000), tokens.to(DEV), u.to(DEV), draft=q.to(DEV).expand(n, 2, 5000))
+    assert acc.tolist() == wide[0] and out.tolist() == wide[1]

@@ -28,7 +28,8 @@ def split(qkv, hq, hkv):
 @pytest.mark.parametrize("T,hq,hkv,rot,interleaved,norm", [
     (1, 1, 1, 128, False, False), (1, 96, 8, 128, True, True), (3, 16, 2, 64, False, True), (257, 5, 1, 96, False, False),
     (33, 8, 8, 32, True, False), (50, 7, 3, 8, False, True), (50, 7, 3, 8, True, True), (21, 4, 2, 0, False, True),
-    (64, 2, 2, 120, False, True), (64, 2, 2, 120, True, True), (1501, 32, 8, 128, False, True), (40, 3, 1, 56, True, False)])
+    (64, 2, 2, 120, False, True), (64, 2, 2, 120, True, True), (1501, 32, 8, 128, False, True), (40, 3, 1, 56, True, False), (2, 300, 20, 128, False, True),
+    (610, 70, 1, 16, True, True)])
 def test_rope(T, hq, hkv, rot, interleaved, norm, dtype):
     qkv, pos, qw, kw = inputs(T, hq, hkv, dtype, seed=T + rot)
     q, k, _ = split(qkv, hq, hkv)
@@ -208,6 +209,25 @@ def test_rope_append_writes_nothing_else():
         live = torch.zeros(pages * ps, dtype=torch.bool, device=DEV)
         live[slots[(slots >= 0) & (slots < pages * ps)]] = True
         assert torch.equal(rows, live)
+
+
+@pytest.mark.parametrize("cache", [BF16, E4M3])
+def test_offsets_past_32_bits(cache):
+    """Pages whose places in the cache pass 2^31 elements."""
+    T, hq, hkv, ps, pages = 150, 4, 8, 64, 40_000
+    qkv, pos, qw, kw = inputs(T, hq, hkv, BF16, seed=21)
+    q, k, v = split(qkv, hq, hkv)
+    freq, _ = kda.rope_frequencies(128, device=DEV)
+    big, small = ([torch.empty(n, hkv, ps, D, device=DEV, dtype=cache) for _ in range(2)] for n in (pages, 4))
+    near = torch.randperm(4 * ps, generator=torch.Generator().manual_seed(1))[:T].to(DEV)
+    far = near + (pages - 4) * ps
+    ks = vs = torch.full((hkv,), 0.03, device=DEV) if cache == E4M3 else None
+    for kc, vc, slots in ((*big, far), (*small, near)):
+        for c in (kc, vc):
+            c[-4:].view(torch.uint8).zero_()
+        kda.paged_rope_append(q, k, v, pos, slots, freq, kc, vc, q_weight=qw, k_weight=kw, k_scale=ks, v_scale=vs)
+    for a, b in zip(big, small):
+        assert torch.equal(a[-4:].view(torch.uint8), b.view(torch.uint8)) and (b.view(torch.uint8) != 0).any()
 
 
 def test_no_tokens():

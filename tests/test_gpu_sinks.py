@@ -166,6 +166,34 @@ def test_graph_and_short_wait_budget():
         assert torch.equal(out, want)
 
 
+@pytest.mark.parametrize("cache", [BF16, E4M3, F32])
+def test_offsets_past_32_bits(cache):
+    """The same content on pages whose places in the cache pass 2^31 elements: the same bits."""
+    new, ctx, ps, hkv = [1, 70, 3], [900, 300, 500], 64, 8
+    d = make(new, ctx, hkv, 2, ps, cache=cache, seed=6)
+    n = d["k_cache"].shape[0]
+    pages = 40_000 if cache != F32 else 34_000
+    out = []
+    for total in (n, pages):
+        kc, vc = (torch.empty(total, hkv, ps, D, device=DEV, dtype=cache) for _ in range(2))
+        for a, b in ((kc, d["k_cache"]), (vc, d["v_cache"])):
+            a[-n:].view(torch.uint8).copy_(b.to(DEV).view(torch.uint8))
+        table = [[x + total - n if x >= 0 else x for x in row] for row in d["table"]]
+        sc = [None if d[k] is None else d[k].to(DEV) for k in ("k_scale", "v_scale")]
+        out.append(kda.paged_attn(d["q"].to(DEV), kc, vc, i32(table), i32(d["cu"]), i32(d["kv"]), max_q=70, window=90, sinks=20,
+                                  k_scale=sc[0], v_scale=sc[1]))
+        del kc, vc
+    assert torch.equal(out[0][0], out[1][0]) and torch.equal(out[0][1], out[1][1])
+
+
+@pytest.mark.parametrize("n", [20, 700])
+def test_single_tokens_beside_a_chunk(n):
+    """Where windows are short the tile kernel takes them all, else the kernel for few rows the single tokens."""
+    new, ctx = [1] * n + [40], [(37 * i) % 500 for i in range(n)] + [77]
+    for window in (20, 2500):
+        run(new, ctx, 2, 2, 16, BF16, window, 9, hidden=False)
+
+
 def test_bad_page_among_the_sinks():
     d = make([1], [900], 1, 1, 16, cache=BF16, seed=1)
     d["table"][0][0] = 10 ** 6
