@@ -265,81 +265,81 @@ __device__ __forceinline__ void walk_role(const PagedAttn &a, uint8_t *sm, Walk 
             float *sc = reinterpret_cast<float *>(sm + C::OFF_SC) + (i % SEGS) * NR;
             const float ks = E4 ? a.scale_log2 * a.k_scale[s.h] : a.scale_log2;
             const int c = lane & 15;  // 16-byte piece of a row; two rows at a time
-            // eight rows at a time, their loads all in flight (one after the other they held up e4m3 items
-            // of up to some 30 tiles: 64 requests of five tokens over 4,224 keys 183 us)
+            // eight rows at a time, their loads all in flight, and none converted past R (64 e4m3 requests
+            // of a token over 4,224 keys 115 us, one row after the other 122)
 #pragma unroll 1
             for (int r8 = 0; r8 < NR; r8 += 8) {
-            uint4 rows[4];
+                uint4 rows[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int r = r8 + 2 * k + (lane >> 4);
-                rows[k] = make_uint4(0, 0, 0, 0);
-                if (r < s.R) {
-                    const int rr = s.r0 + r, j = rr / a.G;
-                    rows[k] = __ldg((const uint4 *)a.q + ((int64_t)(s.tok + j) * a.Hq + s.h * a.G + (rr - j * a.G)) * (D / 8) + c);
-                }
-            }
-#pragma unroll
-            for (int k4 = 0; k4 < 4; ++k4) {
-                const int r = r8 + 2 * k4 + (lane >> 4);
-                const uint4 v = rows[k4];
-                if (E4 && r8 + 2 * k4 >= s.R) {  // (rows past R)
-                    if (c == 0) sc[r] = ks;
-                    uint8_t *at = qb + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + 8 * (c & 1);
-#pragma unroll
-                    for (int p = 0; p < 3; ++p) *reinterpret_cast<uint2 *>(at + p * NR * 128) = make_uint2(0, 0);
-                    continue;
-                }
-                if (E4) {
-                    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-                    float y[8], top = 0.f;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        y[2 * k] = bf_lo(u[k]);
-                        y[2 * k + 1] = bf_hi(u[k]);
-                        // (the parts are cut at the largest value: NaN says that there is no answer)
-                        if (fabsf(y[2 * k]) == INFINITY) y[2 * k] = NAN;
-                        if (fabsf(y[2 * k + 1]) == INFINITY) y[2 * k + 1] = NAN;
-                        top = fmaxf(top, fmaxf(fabsf(y[2 * k]), fabsf(y[2 * k + 1])));
+                for (int k = 0; k < 4; ++k) {
+                    const int r = r8 + 2 * k + (lane >> 4);
+                    rows[k] = make_uint4(0, 0, 0, 0);
+                    if (r < s.R) {
+                        const int rr = s.r0 + r, j = rr / a.G;
+                        rows[k] = __ldg((const uint4 *)a.q + ((int64_t)(s.tok + j) * a.Hq + s.h * a.G + (rr - j * a.G)) * (D / 8) + c);
                     }
+                }
 #pragma unroll
-                    for (int o = 8; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    // The row's largest value goes to 2^14 .. 2^15 (rows under 2^-110: 2^124 times
-                    // theirs).  Parts go down to 2^-16, so values over 2^-23 of the largest are exact,
-                    // and what smaller ones lose is 2^-31 of it, far below the sums' own rounding.
-                    // (Two e4m3 parts end 2^-16 below the largest: with one channel 2^12 times the
-                    // others, scores were off by 0.2.)
-                    const int e = max((int)(__float_as_uint(top) >> 23) - 127, -110);
-                    const float down = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-                    if (c == 0) sc[r] = ks * __uint_as_float((uint32_t)(127 + e - 14) << 23);
-                    uint32_t w[3][2];
+                for (int k4 = 0; k4 < 4; ++k4) {
+                    const int r = r8 + 2 * k4 + (lane >> 4);
+                    const uint4 v = rows[k4];
+                    if (E4 && r8 + 2 * k4 >= s.R) {  // (rows past R)
+                        if (c == 0) sc[r] = ks;
+                        uint8_t *at = qb + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + 8 * (c & 1);
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
+                        for (int p = 0; p < 3; ++p) *reinterpret_cast<uint2 *>(at + p * NR * 128) = make_uint2(0, 0);
+                        continue;
+                    }
+                    if (E4) {
+                        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+                        float y[8], top = 0.f;
 #pragma unroll
-                        for (int p = 0; p < 3; ++p) w[p][k] = 0;
+                        for (int k = 0; k < 4; ++k) {
+                            y[2 * k] = bf_lo(u[k]);
+                            y[2 * k + 1] = bf_hi(u[k]);
+                            // (the parts are cut at the largest value: NaN says that there is no answer)
+                            if (fabsf(y[2 * k]) == INFINITY) y[2 * k] = NAN;
+                            if (fabsf(y[2 * k + 1]) == INFINITY) y[2 * k + 1] = NAN;
+                            top = fmaxf(top, fmaxf(fabsf(y[2 * k]), fabsf(y[2 * k + 1])));
+                        }
 #pragma unroll
-                        for (int g = 0; g < 2; ++g) {
-                            float2 z = make_float2(y[4 * k + 2 * g] * down, y[4 * k + 2 * g + 1] * down);
+                        for (int o = 8; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                        // The row's largest value goes to 2^14 .. 2^15 (rows under 2^-110: 2^124 times
+                        // theirs).  Parts go down to 2^-16, so values over 2^-23 of the largest are exact,
+                        // and what smaller ones lose is 2^-31 of it, far below the sums' own rounding.
+                        // (Two e4m3 parts end 2^-16 below the largest: with one channel 2^12 times the
+                        // others, scores were off by 0.2.)
+                        const int e = max((int)(__float_as_uint(top) >> 23) - 127, -110);
+                        const float down = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+                        if (c == 0) sc[r] = ks * __uint_as_float((uint32_t)(127 + e - 14) << 23);
+                        uint32_t w[3][2];
 #pragma unroll
-                            for (int p = 0; p < 3; ++p) {
-                                const __nv_fp8x2_storage_t b = __nv_cvt_float2_to_fp8x2(z, __NV_SATFINITE, __NV_E5M2);
-                                const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(b, __NV_E5M2);
-                                const float2 back = __half22float2(*reinterpret_cast<const __half2 *>(&hr));
-                                w[p][k] |= (uint32_t)b << (16 * g);
-                                z.x -= back.x;
-                                z.y -= back.y;
+                        for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                            for (int p = 0; p < 3; ++p) w[p][k] = 0;
+#pragma unroll
+                            for (int g = 0; g < 2; ++g) {
+                                float2 z = make_float2(y[4 * k + 2 * g] * down, y[4 * k + 2 * g + 1] * down);
+#pragma unroll
+                                for (int p = 0; p < 3; ++p) {
+                                    const __nv_fp8x2_storage_t b = __nv_cvt_float2_to_fp8x2(z, __NV_SATFINITE, __NV_E5M2);
+                                    const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(b, __NV_E5M2);
+                                    const float2 back = __half22float2(*reinterpret_cast<const __half2 *>(&hr));
+                                    w[p][k] |= (uint32_t)b << (16 * g);
+                                    z.x -= back.x;
+                                    z.y -= back.y;
+                                }
                             }
                         }
-                    }
-                    // three [row][channel] e5m2 operands, 128 bytes a row: this lane's 8 channels
-                    uint8_t *at = qb + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + 8 * (c & 1);
+                        // three [row][channel] e5m2 operands, 128 bytes a row: this lane's 8 channels
+                        uint8_t *at = qb + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + 8 * (c & 1);
 #pragma unroll
-                    for (int p = 0; p < 3; ++p) *reinterpret_cast<uint2 *>(at + p * NR * 128) = make_uint2(w[p][0], w[p][1]);
-                } else {
-                    if (c == 0) sc[r] = ks;
-                    *reinterpret_cast<uint4 *>(qb + (c >> 3) * NR * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+                        for (int p = 0; p < 3; ++p) *reinterpret_cast<uint2 *>(at + p * NR * 128) = make_uint2(w[p][0], w[p][1]);
+                    } else {
+                        if (c == 0) sc[r] = ks;
+                        *reinterpret_cast<uint4 *>(qb + (c >> 3) * NR * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+                    }
                 }
-            }
             }
             fence_async_smem();
             __syncwarp();
