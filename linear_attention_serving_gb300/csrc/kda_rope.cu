@@ -18,10 +18,10 @@
 // sums for each two channels.
 //
 // Bound by HBM once there are some thousand tokens, by the launch and the chain position, angle,
-// row below: 23,100 packed tokens of 32 + 2 x 8 heads (bf16, norms) into their pages 92 us, 6.2
-// TB/s; 9,900 of 16 + 16 heads (fp32) 48 us, 6.4 TB/s; 1,280 tokens into an e4m3 cache 9.8 us; one
-// token 2.9 us.  Two rows a unit in flight and two ahead of them, 64 registers: with four
-// of each, 80 registers and three blocks an SM, the first is 92 to 109 us; with rows of all
+// row below: 23,100 packed tokens of 32 + 2 x 8 heads (bf16, norms) into their pages 89 us, 6.4
+// TB/s; 9,300 of 16 + 16 heads (fp32) 48 us, 6.3 TB/s; 1,280 tokens into an e4m3 cache 9.7 us; one
+// token 2.8 us.  Two rows a unit in flight and two ahead of them, 64 registers: with four
+// of each, 80 registers and three blocks an SM, the first was 92 to 109 us; with rows of all
 // kinds in one stream of batches, 111.
 #include <cuda_fp8.h>
 
@@ -215,16 +215,19 @@ struct Turn {
 template <typename T> constexpr int AHEAD = sizeof(T) == 2 ? 2 : 1;
 
 // `n` rows of one kind, `step` elements apart in `in` and `out_step` in `out`: normed (where w), turned
-// (TURN) and stored; E4M3: as x / scale, the rows' scales `scale_step` apart.
-template <typename T, bool INTER, bool TURN, bool E4M3>
-__device__ __forceinline__ void unit_rows(const T *in, int step, char *out, int64_t out_step, int n, bool w, float eps, const Turn &tm,
-                                          bool turns, int c0, int c1, uint32_t lanes, const float *scale, int scale_step) {
-    constexpr int N = AHEAD<T>;
-    if (n <= 0) return;
-    Eight<T> x[N], next[N];
+// (TURN) and stored; E4M3: as x / scale, the rows' scales `scale_step` apart.  x: the first batch.
+template <typename T, bool INTER>
+__device__ __forceinline__ void first_rows(Eight<T> (&x)[AHEAD<T>], const T *in, int step, int n, int c0, int c1) {
 #pragma unroll
-    for (int i = 0; i < N; ++i)
+    for (int i = 0; i < AHEAD<T>; ++i)
         if (i < n) x[i].template load<INTER>(in + i * step, c0, c1);
+}
+template <typename T, bool INTER, bool TURN, bool E4M3>
+__device__ __forceinline__ void unit_rows(Eight<T> (&x)[AHEAD<T>], const T *in, int step, char *out, int64_t out_step, int n, bool w,
+                                          float eps, const Turn &tm, bool turns, int c0, int c1, uint32_t lanes, const float *scale,
+                                          int scale_step) {
+    constexpr int N = AHEAD<T>;
+    Eight<T> next[N];
     for (; n > 0; n -= N) {
         in += N * step;
 #pragma unroll
@@ -298,9 +301,14 @@ __global__ void __launch_bounds__(THREADS, 4) rope_kernel(const RopeArgs a) {
     const bool turns = l < turning, live = tok < a.T;
     const int c0 = INTER ? 2 * l : turns ? l : 2 * l, c1 = INTER ? c0 + 1 : turns ? l + turning : 2 * l + 1;
     const int r0 = blockIdx.y * a.rows_per_y + (unit - mine * PER), r1 = (blockIdx.y + 1) * a.rows_per_y;
-    // the first row is on its way to the L2 cache while the angles are worked out
-    if (live && r0 < a.Hq)
-        asm volatile("prefetch.global.L2 [%0];" ::"l"((const T *)a.q + (int64_t)tok * a.q_stride + (int64_t)r0 * D + c0 * 4));
+    // the unit's rows among the block's, up to r1, of queries, keys and values, one kind after the other
+    auto first = [&](int from) { return r0 >= from ? r0 - from : (PER - 1) & (r0 - from); };  // within a kind that begins at `from`
+    auto count = [&](int f, int from, int rows) { return live ? (min(rows, r1 - from) - f + PER - 1) / PER : 0; };
+    // the first queries are on their way while the angles are worked out
+    const int hq = first(0), nq = count(hq, 0, a.Hq);
+    const T *q = (const T *)a.q + (int64_t)tok * a.q_stride + hq * D;
+    Eight<T> x[AHEAD<T>];
+    first_rows<T, INTER>(x, q, PER * D, nq, c0, c1);
     // the tokens' angles
     if constexpr (LOG == EACH) {
         if (live && turns) {
@@ -335,17 +343,12 @@ __global__ void __launch_bounds__(THREADS, 4) rope_kernel(const RopeArgs a) {
     if (LOG != EACH) __syncthreads();
     if (!live) return;
     const uint32_t lanes = tid & 16 ? 0xffff0000u : 0x0000ffffu;  // (shuffles stay among a unit's lanes)
-    // the unit's rows among the block's, up to r1, of queries, keys and values, one kind after the other
-    auto first = [&](int from) { return r0 >= from ? r0 - from : (PER - 1) & (r0 - from); };  // within a kind that begins at `from`
-    auto count = [&](int f, int from, int rows) { return (min(rows, r1 - from) - f + PER - 1) / PER; };
     constexpr int ES = (int)sizeof(T);
     Turn tm;
-    {
-        const int h = first(0), n = count(h, 0, a.Hq);
+    if (nq > 0) {
         tm.set<INTER>(a.q_weight, angles, turns, c0, c1);
-        unit_rows<T, INTER, true, false>((const T *)a.q + (int64_t)tok * a.q_stride + h * D, PER * D,
-                                         (char *)a.q_out + ((int64_t)tok * a.q_out_stride + h * D) * ES, PER * D * ES, n, a.q_weight,
-                                         a.eps, tm, turns, c0, c1, lanes, nullptr, 0);
+        unit_rows<T, INTER, true, false>(x, q, PER * D, (char *)a.q_out + ((int64_t)tok * a.q_out_stride + hq * D) * ES, PER * D * ES, nq,
+                                         a.q_weight, a.eps, tm, turns, c0, c1, lanes, nullptr, 0);
     }
     if (TO != TO_ROWS && page < 0) return;
     constexpr bool E4 = TO == TO_E4M3;
@@ -354,19 +357,22 @@ __global__ void __launch_bounds__(THREADS, 4) rope_kernel(const RopeArgs a) {
     if (n > 0) {
         tm.set<INTER>(a.k_weight, angles, turns, c0, c1);
         const T *in = (const T *)a.k + (int64_t)tok * a.k_stride + h * D;
+        first_rows<T, INTER>(x, in, PER * D, n, c0, c1);
         if constexpr (TO == TO_ROWS)
-            unit_rows<T, INTER, true, false>(in, PER * D, (char *)a.k_out + ((int64_t)tok * a.k_out_stride + h * D) * ES, PER * D * ES, n,
+            unit_rows<T, INTER, true, false>(x, in, PER * D, (char *)a.k_out + ((int64_t)tok * a.k_out_stride + h * D) * ES, PER * D * ES, n,
                                              a.k_weight, a.eps, tm, turns, c0, c1, lanes, nullptr, 0);
         else
-            unit_rows<T, INTER, true, E4>(in, PER * D, (char *)a.k_out + (page * a.page_stride + ((int64_t)h * a.page_size + off) * D) * CS,
+            unit_rows<T, INTER, true, E4>(x, in, PER * D, (char *)a.k_out + (page * a.page_stride + ((int64_t)h * a.page_size + off) * D) * CS,
                                           (int64_t)PER * a.page_size * D * CS, n, a.k_weight, a.eps, tm, turns, c0, c1, lanes,
                                           E4 ? a.k_scale + h : nullptr, PER);
     }
     if constexpr (TO != TO_ROWS) {
-        const int from = a.Hq + a.Hkv, g = first(from);
-        unit_rows<T, INTER, false, E4>((const T *)a.v + (int64_t)tok * a.v_stride + g * D, PER * D,
+        const int from = a.Hq + a.Hkv, g = first(from), m = count(g, from, a.Hkv);
+        const T *in = (const T *)a.v + (int64_t)tok * a.v_stride + g * D;
+        first_rows<T, INTER>(x, in, PER * D, m, c0, c1);
+        unit_rows<T, INTER, false, E4>(x, in, PER * D,
                                        (char *)a.v_cache + (page * a.page_stride + ((int64_t)g * a.page_size + off) * D) * CS,
-                                       (int64_t)PER * a.page_size * D * CS, count(g, from, a.Hkv), false, a.eps, tm, turns, c0, c1, lanes,
+                                       (int64_t)PER * a.page_size * D * CS, m, false, a.eps, tm, turns, c0, c1, lanes,
                                        E4 ? a.v_scale + g : nullptr, PER);
     }
 }
@@ -408,11 +414,11 @@ dim3 rope_grid(RopeArgs &a, int rows, int &log) {
     a.rows_per_y = rows;
     int y = 1;
     if (a.T >= 16 * sms) {
-        // Few rows: a unit works its token's angles out alone and waits for no other (20,000 tokens of 24 rows 42
-        // and 48 us, of 6 rows 17 us; eight tokens to a block 46, 47 and 26).  With 48 rows there are too few units
-        // left to fill the last wave (84 us eight tokens to a block, 89 one to a unit).
+        // Few rows: a unit works its token's angles out alone and waits for no other (20,000 tokens of 20 rows 41
+        // us, of 24 46, of 6 16; eight tokens to a block 46, 47 and 26).  With 48 rows there are too few units
+        // left to fill the last wave (81 us eight tokens to a block, 87 one to a unit).
         log = rows <= 24 ? EACH : MANY;
-    } else if (a.T >= 4 * sms) {  // (1,280 tokens of 48 rows: 8.9 us; 12.1 a block to each, 11.0 eight to a block)
+    } else if (a.T >= 4 * sms) {  // (1,280 tokens of 48 rows: 8.6 us; 11.2 a block to each, 10.4 eight to a block)
         log = SOME;
     } else {
         // a block to a token, or several to one where there are few: a row for each unit
