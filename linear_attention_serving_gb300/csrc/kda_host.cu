@@ -68,8 +68,11 @@ int prepare_kernel(const void *func, int smem_bytes, int threads, int *blocks_pe
             return KDA_OK;
         }
     }
-    if (cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes) != cudaSuccess)
-        return KDA_ERR_CUDA;
+    // (never lowered: a kernel is launched with different sizes in turn, whose entries above say no more)
+    int most = smem_bytes;
+    for (int i = 0; i < g_nsetup; ++i)
+        if (g_setup[i].func == func && g_setup[i].dev == dev && g_setup[i].smem > most) most = g_setup[i].smem;
+    if (cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess) return KDA_ERR_CUDA;
     int per_sm = 0;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, func, threads, (size_t)smem_bytes) != cudaSuccess)
         return KDA_ERR_CUDA;

@@ -6,6 +6,7 @@ import os
 import pytest
 import torch
 
+import linear_attention_serving_gb300 as kda
 from serving_testutil import verify_ref
 
 pytestmark = pytest.mark.gpu
@@ -46,6 +47,24 @@ def test_each_step_verifies_as_the_plain_form_does():
         ctx = [c + 1 + a for c, a in zip(ctx, ref[0])]
         assert server.ctx.tolist() == ctx and server.token.tolist() == [t[a] for t, a in zip(ref[1], ref[0])]
     assert int(server.error) == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_windows_of_different_lengths_in_turn(dtype):
+    """A decode step of a long window after one of a short window: the kernel keeps the shared memory that it was
+    once given (the long window's launch failed after the short one's)."""
+    def step(W):
+        x = lambda *size: torch.randn(2, W, *size, device="cuda")  # noqa: E731
+        row = (2, W - 1, 1, 128)
+        cache = tuple(torch.zeros(row, device="cuda", dtype=t) for t in (dtype, dtype, dtype, torch.float32)) + (
+            torch.zeros(row[:3], device="cuda"),)
+        q, k, v = (x(1, 128).to(dtype) for _ in range(3))
+        o = kda.decode_step(torch.zeros(2, 1, 128, 128, device="cuda"), q, k, v, x(1, 128), x(1), torch.zeros(1, device="cuda"),
+                            cache, qk_l2norm=True, beta_sigmoid=True)
+        assert torch.isfinite(o).all()
+
+    for W in (7, 3, 7, 2, 6, 7):
+        step(W)
 
 
 def test_two_streams_do_not_mix():
