@@ -29,10 +29,11 @@
 // Measured: a prompt of 8,192 tokens, 16 heads over two kv heads, 224 us (1,225
 // TFLOP/s of the pairs that the mask leaves; some tiles more are multiplied where it
 // crosses them); 2,048 tokens, 32 heads, over 65,536 keys 1,501 to 1,541 us (1,405 to
-// 1,442 TFLOP/s, by the box: the clock falls under the load); 256 windows of 60 rows 258 us (5.8 TB/s).  Bound by the
-// products (S for 64 keys reads its operands, by their bytes, at three quarters of the
-// rate) and by what the way from S to P leaves between them.  (A share of the
-// exponentials by a polynomial made it slower, 250 to 276 us for 242 us: the special
+// 1,442 TFLOP/s, by the box: the clock falls under the load); 256 windows of 60 rows 258 us
+// (5.8 TB/s); 2,048 tokens, 32 heads, through windows of 4,096 beside 4 sinks 145 us (136 without
+// sinks, whose tile each item reads).  Bound by the products (S for 64 keys reads its operands, by
+// their bytes, at three quarters of the rate) and by what the way from S to P leaves between them.
+// (A share of the exponentials by a polynomial made it slower, 250 to 276 us for 242 us: the special
 // function unit is not what it waits for.)
 #include "kda_paged_tc.cuh"
 
