@@ -32,12 +32,12 @@
 // Probabilities are rounded to 16 bits because their product with V needs V's type (bf16)
 // or one that holds V exactly (fp16); the sums take them unrounded.
 //
-// Measured: one token of 256 requests over up to 16,384 keys of 4 kv heads 343 to 349 us
-// (6.7 TB/s, a copy's rate), of 64 requests over up to 65,536 e4m3 keys of 8 kv heads 420 us
-// (6.5 TB/s), one request over 8,192 keys 13.8 us with the join, which is starts, first
+// Measured: one token of 256 requests over up to 16,384 keys of 4 kv heads 340 to 349 us
+// (6.7 TB/s, a copy's rate), of 64 requests over up to 65,536 e4m3 keys of 8 kv heads 405 to 411 us
+// (6.7 TB/s), one request over 8,192 keys 13.8 us with the join, which is starts, first
 // copies and the pieces' way through memory.  One token of 256 requests through a window of 2,048
 // beside 4 sinks, 4 kv heads 149 us (5.9 TB/s; 147 without sinks); five tokens of 64 requests over
-// e4m3 windows of 4,096 and 64 sinks, 8 kv heads 171 us (3.2 TB/s), where the softmax of the
+// e4m3 windows of 4,096 and 64 sinks, 8 kv heads 150 us (3.7 TB/s), where the softmax of the
 // 20 rows is what each tile waits for.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -282,10 +282,12 @@ __device__ __forceinline__ void walk_role(const PagedAttn &a, uint8_t *sm, Walk 
                         rows[k] = __ldg((const uint4 *)a.q + ((int64_t)(s.tok + j) * a.Hq + s.h * a.G + (rr - j * a.G)) * (D / 8) + c);
                     }
                 }
-#pragma unroll
+                // (e4m3: short code, the conversions' four times over pushed the other roles' out of the instruction cache:
+                // 64 requests of a token 411 us for 421, of five 162 for 171)
+#pragma unroll(E4 ? 1 : 4)
                 for (int k4 = 0; k4 < 4; ++k4) {
                     const int r = r8 + 2 * k4 + (lane >> 4);
-                    const uint4 v = rows[k4];
+                    const uint4 v = k4 == 0 ? rows[0] : k4 == 1 ? rows[1] : k4 == 2 ? rows[2] : rows[3];
                     if (E4 && r8 + 2 * k4 >= s.R) {  // (rows past R)
                         if (c == 0) sc[r] = ks;
                         uint8_t *at = qb + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + 8 * (c & 1);
@@ -473,6 +475,9 @@ template <int NR, bool SINK, class Gate>
 __device__ __forceinline__ void widen_role(uint8_t *sm, const Gate &gate) {
     using C = Cfg<true, NR>;
     constexpr int W = 32 / C::WIDEN;  // 16-byte pieces of a row for one thread: 8 of them to a row
+    // So many at a time: with eight the code is so long that the roles push each other's out of the
+    // instruction cache (64 requests of five tokens, window 4,096, 150 us for 165; 16,896 keys 372 us for 377, two at a time 417)
+    constexpr int CH = 4;
     const Bars<C> bar(sm);
     const int tid = threadIdx.x - C::W_WIDEN * 32, row = tid & 127, lane = tid & 31, x = row & 7, p0 = (tid >> 7) * W;
     const uint8_t *raw = sm + C::OFF_R + row * 128;
@@ -484,30 +489,37 @@ __device__ __forceinline__ void widen_role(uint8_t *sm, const Gate &gate) {
         const int z = desc[slot];
         if (z < 0) return;
         const uint8_t *src = raw + slot * RAW;
-        uint4 w[W];
+        const bool none = SINK ? (row < (z & 255) && row >= (z >> 16)) || row >= ((z >> 8) & 255) : row < (z & 255) || row >= (z >> 8);
+        uint4 w[CH];
+        auto load = [&](int i0) {
 #pragma unroll
-        for (int i = 0; i < W; ++i) w[i] = *reinterpret_cast<const uint4 *>(src + (((p0 + i) ^ x) << 4));
-        if (SINK ? (row < (z & 255) && row >= (z >> 16)) || row >= ((z >> 8) & 255) : row < (z & 255) || row >= (z >> 8)) {
-#pragma unroll
-            for (int i = 0; i < W; ++i) w[i] = make_uint4(0, 0, 0, 0);
-        }
+            for (int i = 0; i < CH; ++i) {
+                w[i] = *reinterpret_cast<const uint4 *>(src + (((p0 + i0 + i) ^ x) << 4));
+                if (none) w[i] = make_uint4(0, 0, 0, 0);
+            }
+        };
+        load(0);
         if (!gate(&bar.v_empty[os], oph ^ 1)) return;
         uint8_t *dst = out + os * TILE;
+#pragma unroll 1
+        for (int i0 = 0; i0 < W; i0 += CH) {
+            if (i0) load(i0);
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
-            const uint32_t y[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-            uint32_t h[8];
+            for (int i = 0; i < CH; ++i) {
+                const uint32_t y[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+                uint32_t h[8];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(y[k] & 0xffff), __NV_E4M3);
-                const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(y[k] >> 16), __NV_E4M3);
-                h[2 * k] = (uint32_t)lo.x | ((uint32_t)lo.y << 16);
-                h[2 * k + 1] = (uint32_t)hi.x | ((uint32_t)hi.y << 16);
+                for (int k = 0; k < 4; ++k) {
+                    const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(y[k] & 0xffff), __NV_E4M3);
+                    const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(y[k] >> 16), __NV_E4M3);
+                    h[2 * k] = (uint32_t)lo.x | ((uint32_t)lo.y << 16);
+                    h[2 * k + 1] = (uint32_t)hi.x | ((uint32_t)hi.y << 16);
+                }
+                const int p = p0 + i0 + i;  // piece of 16 channels: two of the 16-bit row
+                uint8_t *at = dst + (p >> 2) * (TILE / 2);
+                *reinterpret_cast<uint4 *>(at + (((2 * (p & 3)) ^ x) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint4 *>(at + (((2 * (p & 3) + 1) ^ x) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
             }
-            const int p = p0 + i;  // piece of 16 channels: two of the 16-bit row
-            uint8_t *at = dst + (p >> 2) * (TILE / 2);
-            *reinterpret_cast<uint4 *>(at + (((2 * (p & 3)) ^ x) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-            *reinterpret_cast<uint4 *>(at + (((2 * (p & 3) + 1) ^ x) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
         }
         fence_async_smem();
         __syncwarp();
@@ -1100,8 +1112,11 @@ int paged_few_blocks() { return device_sm_count(); }
 
 int launch_paged_few(PagedAttn a, int cache_dtype, const void *k, const void *v, int64_t page_stride, int64_t max_rows,
                      cudaStream_t s) {
+    // (copies of 32 keys at most where sinks are few keys of a page: bf16, a window of 2,048 beside 4 sinks, 144 to
+    // 149 us for 147 to 151; of 16 158 us; e4m3 1 us slower)
+    const int most = a.sinks > 0 && cache_dtype != KDA_E4M3 ? 32 : BK;
     int box = 16;
-    while (box < BK && a.page_size % (2 * box) == 0) box *= 2;
+    while (box < most && a.page_size % (2 * box) == 0) box *= 2;
     a.box = box;
     a.box_log = __builtin_ctz(box);
     PagedMaps maps;
@@ -1110,7 +1125,7 @@ int launch_paged_few(PagedAttn a, int cache_dtype, const void *k, const void *v,
     if (a.sinks > 0) sinks_of(a, BK);
     const bool e4 = cache_dtype == KDA_E4M3;
     if (max_rows <= 16) return e4 ? launch<true, 16>(a, maps, s) : launch<false, 16>(a, maps, s);
-    // (of 32 columns only those that rows can be in: 171 us for 192 with five tokens of four heads)
+    // (of 32 columns only those that rows can be in: five tokens of four heads, 171 us for 192)
     if (e4 && max_rows <= 24) return launch<true, 32, 24>(a, maps, s);
     return e4 ? launch<true, 32>(a, maps, s) : launch<false, 32>(a, maps, s);
 }
