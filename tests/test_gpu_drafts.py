@@ -66,7 +66,8 @@ def by_sums(target, draft, tokens, u):
 
 @pytest.mark.parametrize("n,w,V,certain,dtype", [
     (1, 5, 32768, False, F32), (1, 5, 200_003, False, F32), (3, 3, 1_000_001, False, F32), (300, 4, 5000, False, F32),
-    (40, 5, 131_072, False, BF16), (700, 2, 20_000, True, F32), (9, 6, 50_001, True, BF16), (2, 2, 9_000_000, False, F32)])
+    (40, 5, 131_072, False, BF16), (700, 2, 20_000, True, F32), (9, 6, 50_001, True, BF16), (2, 2, 9_000_000, False, F32),
+    (300, 3, 50_001, False, BF16), (100, 3, 60_003, False, F32), (100, 4, 60_002, True, BF16)])
 def test_large_vocabularies(n, w, V, certain, dtype):
     """Every split of a row over blocks and segments; odd sizes go without vector loads."""
     g = torch.Generator(device=DEV).manual_seed(V + n)

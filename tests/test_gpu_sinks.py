@@ -65,6 +65,13 @@ def test_few_rows(new, ctx, hkv, g, ps, window, sinks, cache):
     run(new, ctx, hkv, g, ps, cache, window, sinks, seed=len(ctx) + window)
 
 
+@pytest.mark.parametrize("window,sinks", [(0, 0), (90, 11)])
+@pytest.mark.parametrize("rows,g", [(17, 1), (20, 4), (24, 8), (24, 1), (25, 5), (28, 4), (32, 16), (33, 3)])
+def test_e4m3_windows_of_up_to_two_tiles_of_rows(rows, g, window, sinks):
+    """Over 16 rows of a kv head: 24 columns of 32 are worked on where no request has more."""
+    run([rows // g, 1, 2], [700, 130, 40], 2, g, 64, E4M3, window, sinks, seed=rows, hidden=window > 0)
+
+
 TILES = [
     ([200], [0], 1, 1, 16, 64, 4), ([130], [1000], 2, 2, 64, 100, 20), ([300, 33], [700, 129], 1, 4, 16, 128, 128),
     ([65, 400], [513, 2], 1, 3, 32, 200, 129), ([257], [640], 2, 1, 128, 31, 64), ([40], [900], 1, 8, 48, 900, 10),
