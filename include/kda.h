@@ -615,7 +615,7 @@ int kda_paged_rope_append(const void *q, const void *k, const void *v, const int
  *   uniforms     (device) fp32 [N, W], in [0, 1): u_0 .. u_{W-2}, r (r outside counts as 0
  *                below, as the largest number under 1 above)
  *   n_draft      (device) int32 [N], 0 .. W-1, or NULL: W-1 for all
- *   N >= 1, 1 <= W <= 32, 1 <= V < 2^31; dtype KDA_F32 or KDA_BF16, values 0 .. 1
+ *   1 <= N <= 2^24, 1 <= W <= 32, 1 <= V < 2^31 - 4096; dtype KDA_F32 or KDA_BF16, values 0 .. 1
  *   num_accepted (device) int32 [N], written: a
  *   tokens       (device) int32 [N, W], written: d_0 .. d_{a-1}, the token drawn, then -1
  *   workspace    kda_verify_drafts_workspace_size() bytes, 8-byte aligned; needs no initialisation, not

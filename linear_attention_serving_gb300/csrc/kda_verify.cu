@@ -37,6 +37,7 @@ template <int PIECE> constexpr int ROOM_OF = 2 * PIECE + 16;
 constexpr int MAX_SEGS = 1024;       // of a request
 constexpr int KEEP = MAX_SEGS / THREADS;
 constexpr int MAX_N = 1 << 24, MAX_W = 32;
+constexpr int MAX_V = INT32_MAX - 4096;  // (a piece past the row's end stays clear of 2^31)
 
 struct VerifyArgs {
     const void *target, *draft;
@@ -500,7 +501,7 @@ using namespace kda;
 extern "C" {
 
 size_t kda_verify_drafts_workspace_size(int N, int W, int V, int dtype) {
-    if (N < 1 || N > MAX_N || W < 1 || W > MAX_W || V < 1 || (dtype != KDA_F32 && dtype != KDA_BF16)) return 0;
+    if (N < 1 || N > MAX_N || W < 1 || W > MAX_W || V < 1 || V > MAX_V || (dtype != KDA_F32 && dtype != KDA_BF16)) return 0;
     return (size_t)N * plan_verify(N, V, dtype == KDA_BF16 ? 2 : 4).segs * sizeof(uint64_t);
 }
 
@@ -510,7 +511,7 @@ int kda_verify_drafts(const void *target, const void *draft, const int32_t *draf
                       int32_t *tokens, void *workspace, size_t workspace_bytes, int32_t *error_word, kda_stream_t stream) {
     if (dtype != KDA_BF16 && dtype != KDA_F32) return KDA_ERR_INVALID_ARG;
     if (N < 1 || W < 1 || V < 1) return KDA_ERR_INVALID_ARG;
-    if (W > MAX_W || N > MAX_N) return KDA_ERR_UNSUPPORTED;
+    if (W > MAX_W || N > MAX_N || V > MAX_V) return KDA_ERR_UNSUPPORTED;
     if (!target || !uniforms || !num_accepted || !tokens || (W > 1 && !draft_tokens)) return KDA_ERR_INVALID_ARG;
     const int es = dtype == KDA_BF16 ? 2 : 4;
     if (((uintptr_t)target | (uintptr_t)draft) & (es - 1)) return KDA_ERR_INVALID_ARG;

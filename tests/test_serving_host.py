@@ -80,7 +80,7 @@ def test_sinks_refusals(kw, rc):
 
 @pytest.mark.parametrize("kw,rc", [
     (dict(dt=2), INVALID), (dict(n=0), INVALID), (dict(w=0), INVALID), (dict(V=0), INVALID), (dict(w=33), UNSUPPORTED),
-    (dict(n=(1 << 24) + 1), UNSUPPORTED), (dict(p=None), INVALID), (dict(u=None), INVALID), (dict(acc=None), INVALID),
+    (dict(n=(1 << 24) + 1), UNSUPPORTED), (dict(V=2 ** 31 - 4096, tr=1 << 31, dr=1 << 31), UNSUPPORTED), (dict(p=None), INVALID), (dict(u=None), INVALID), (dict(acc=None), INVALID),
     (dict(out=None), INVALID), (dict(tokens=None), INVALID), (dict(p=ctypes.c_void_p((1 << 20) + 2)), INVALID),
     (dict(q=ctypes.c_void_p((1 << 20) + 1), dt=0), INVALID), (dict(tr=99), INVALID), (dict(dr=99), INVALID), (dict(ts=-1), INVALID),
     (dict(ds=-1), INVALID), (dict(acc=ADDR[5]), INVALID), (dict(out=ADDR[2]), INVALID), (dict(acc=ADDR[3]), INVALID),
@@ -119,7 +119,7 @@ def test_frequencies_refusals(kw):
 def test_verify_workspace_size():
     f = kda.verify_drafts_workspace_size
     assert 0 < f(1, 5, 32768) < f(500, 5, 32768) < f(500, 5, 65536) and f(500, 5, 65536, torch.bfloat16) > 0
-    assert f(0, 5, 100) == f(5, 0, 100) == f(5, 33, 100) == f(5, 5, 0) == f(500, 5, 100, torch.float16) == 0
+    assert f(0, 5, 100) == f(5, 0, 100) == f(5, 33, 100) == f(5, 5, 0) == f(5, 5, 2 ** 31 - 4096) == f(500, 5, 100, torch.float16) == 0
 
 
 def test_binding_refuses_host_tensors():
