@@ -29,7 +29,8 @@ def rope_frequencies(rot_dim, base=10000.0, scaling="none", factor=1.0, original
                                   freq.data_ptr(), ctypes.byref(amplitude))
     if rc:
         _check(rc, "kda_rope_frequencies")
-    return freq.to(device) if device is not None else freq, amplitude.value
+    # (from pageable memory the copy is staged before the call returns)
+    return freq if device is None else freq.to(device, non_blocking=True), amplitude.value
 
 
 def _rows(name, t, index, shape=None, dtype=None):
