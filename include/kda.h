@@ -624,7 +624,8 @@ int kda_paged_rope_append(const void *q, const void *k, const void *v, const int
  * so sums do not depend on their order and the same call gives the same tokens; negative values
  * and NaN count as 0.  A row with values of 2 and more, or one that sums to 8 or more, has no
  * answer (some token, or -1).
- * A drafted token outside 0 .. V-1 records KDA_DEVERR_TOKEN and is refused.  An n_draft out
+ * A drafted token outside 0 .. V-1 records KDA_DEVERR_TOKEN and is refused; its q_j counts as the row of
+ * `draft` where there is one, and as 0 all over where drafts are certain.  An n_draft out
  * of range records KDA_DEVERR_NUM_ACCEPTED: that request gets num_accepted 0 and tokens -1.
  * Rows without weight record KDA_DEVERR_PROBS, and the token drawn is -1.
  * ------------------------------------------------------------------------ */

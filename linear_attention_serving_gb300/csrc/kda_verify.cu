@@ -141,7 +141,8 @@ __device__ __forceinline__ uint64_t warp_scan(uint64_t x, int lane) {
 template <typename T, int PIECE> constexpr int PER_PIECE = PIECE / (int)sizeof(T);  // elements
 template <typename T, int PIECE> constexpr int PER_LANE = PER_PIECE<T, PIECE> / 32;
 
-// The row that the token is drawn from.  q NULL: the weights are p's; gone: a token of no weight (-1: none).
+// The row that the token is drawn from.  q NULL: the weights are p's; gone: a token of no weight (-1: none;
+// a certain draft that is no token, which may be any number, takes no weight from anything).
 // Places count from the 16 bytes that p begins in: element i stands at place i + skip.
 template <typename T> struct Row {
     const T *p, *q;
@@ -189,7 +190,7 @@ template <typename T> __device__ __forceinline__ Row<T> row_of(const VerifyArgs 
     Row<T> r;
     r.p = (const T *)a.target + n * a.t_seq + t.acc * a.t_row;
     r.q = t.acc < t.m && a.draft ? (const T *)a.draft + n * a.d_seq + t.acc * a.d_row : nullptr;
-    r.gone = t.acc < t.m && !a.draft ? t.d : -1;
+    r.gone = t.acc < t.m && !a.draft && t.d >= 0 && t.d < a.V ? t.d : -1;
     r.skip = (int)((uintptr_t)r.p & 15u) / (int)sizeof(T);
     return r;
 }

@@ -299,3 +299,56 @@ def test_requests_that_share_their_rows():
     wide = verify(p.repeat(n, 1, 1), q.repeat(n, 1, 1), tokens, u)
     acc, out = kda.verify_drafts(p.to(DEV).expand(n, 3, 5000), tokens.to(DEV), u.to(DEV), draft=q.to(DEV).expand(n, 2, 5000))
     assert acc.tolist() == wide[0] and out.tolist() == wide[1]
+
+
+def padded(x, pad, value, shift=0):
+    """x on the device, its rows between others' values."""
+    wide = torch.full((*x.shape[:2], shift + x.shape[2] + pad), value, dtype=x.dtype)
+    wide[:, :, shift:shift + x.shape[2]] = x
+    return wide.to(DEV)[:, :, shift:shift + x.shape[2]]
+
+
+def with_no_token(x):
+    """One place more, of no weight: what a drafted token outside the vocabulary stands for."""
+    return torch.cat((x, x.new_zeros(*x.shape[:2], 1)), 2)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("certain", [True, False])
+@pytest.mark.parametrize("V", [1, 16, 50, 250, 1030])
+def test_drafted_tokens_past_the_vocabulary(V, certain, dtype):
+    """Refused, recorded, and without a say in the token that follows, whatever stands behind the row: places up to
+    the end of its last piece, the next row's, far ones."""
+    away = [V, V + 1, V + 2, 255, 256, 511, 512, 1023, 1024, 2047, 2048, 2 ** 31 - 1, 2 ** 31 - 8, -1, -2 ** 31]
+    away = [d for d in away if d < 0 or d >= V]
+    n, w = 3 * len(away), 3
+    target, draft, tokens, u = draft_inputs(n, w, V, seed=V, dtype=dtype, certain=certain)
+    for i, d in enumerate(3 * away):
+        at = i % 2
+        tokens[i, at], u[i, :at] = d, 0.0
+        u[i, w - 1] = (1 - 2.0 ** -24, 0.5, 0.97)[i // len(away)]
+    outside = (tokens < 0) | (tokens >= V)
+    ref = verify_ref(with_no_token(target), torch.where(outside, V, tokens), u, None if draft is None else with_no_token(draft))
+    assert all(a <= i % 2 for i, a in enumerate(ref[0]))
+    for pad, value, shift in ((0, 0.0, 0), (40, 1.0, 0), (3, 1.0, 1), (2100, 0.25, 4), (2100, float("nan"), 0)):
+        err = torch.zeros(1, dtype=torch.int32, device=DEV)
+        acc, out = kda.verify_drafts(padded(target, pad, value, shift), tokens.to(DEV), u.to(DEV),
+                                     draft=None if draft is None else padded(draft, pad, value), error_word=err)
+        assert int(err) == drafts.DEVERR_TOKEN
+        assert acc.tolist() == ref[0] and out.tolist() == ref[1]
+
+
+@pytest.mark.parametrize("n,V,dtype", [(60, 70_001, F32), (110, 70_001, BF16), (3, 70_001, F32)])
+def test_drafted_tokens_past_a_large_vocabulary(n, V, dtype):
+    """The same in rows of many pieces, of either size."""
+    g = torch.Generator(device=DEV).manual_seed(n)
+    target = (2 * torch.randn(n, 2, V, generator=g, device=DEV)).softmax(2).to(dtype)
+    tokens = (V + torch.arange(n, device=DEV) % 3 * 300).int()[:, None]
+    u = torch.rand(n, 2, generator=g, device=DEV)
+    u[: n // 2, 1] = 1 - 2.0 ** -24
+    wide = torch.full((n, 2, V + 700), 0.5, dtype=dtype, device=DEV)
+    wide[:, :, :V] = target
+    acc, out = kda.verify_drafts(wide[:, :, :V], tokens, u)
+    ref, token = by_sums(with_no_token(target), None, torch.full_like(tokens, V), u)
+    assert (acc == 0).all() and (ref == 0).all()
+    assert torch.equal(out[:, 0].long(), token)
