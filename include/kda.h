@@ -619,7 +619,7 @@ int kda_paged_rope_append(const void *q, const void *k, const void *v, const int
  *   num_accepted (device) int32 [N], written: a
  *   tokens       (device) int32 [N, W], written: d_0 .. d_{a-1}, the token drawn, then -1
  *   workspace    kda_verify_drafts_workspace_size() bytes, 8-byte aligned; needs no initialisation, not
- *                shared by calls in flight
+ *                shared by calls in flight.  The size for N requests does for fewer (of this V and dtype) too
  * The tests are exact.  Weights are summed as multiples of 2^-60 (each, p - q exactly, rounded once),
  * so sums do not depend on their order and the same call gives the same tokens; negative values
  * and NaN count as 0.  A row with values of 2 and more, or one that sums to 8 or more, has no

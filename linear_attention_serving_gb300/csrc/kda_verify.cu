@@ -19,6 +19,8 @@
 // 47 us, of which the second launch's part 3; 64 of 100,003 in bf16, no draft probabilities, 13 us, and one of
 // 32,768 5.8 us, which are the chain of launch, tests, row, sums, place.  (A cluster of blocks to a
 // request, registers for what is under way, took 59, 13.7 and 7.2 us.)
+#include <algorithm>
+
 #include "kda_internal.cuh"
 #include "kda_tc.cuh"
 
@@ -456,12 +458,13 @@ __global__ void __launch_bounds__(THREADS, 2) verify_place_kernel(const VerifyAr
 // Small pieces up to four for each warp of a full card (a constant, so that the workspace's size does not
 // depend on the device).  Segments of a request: pieces, two, four .. of them where a row has over
 // MAX_SEGS (places, which count from the 16 bytes that a row begins in, go up to V + 7).
+constexpr int64_t SMALL_BYTES = (int64_t)4 * 152 * BLOCKS * WARPS * SMALL;
 struct VerifyPlan {
     int piece, pieces, segs;
 };
 VerifyPlan plan_verify(int N, int V, int es) {
     VerifyPlan p;
-    p.piece = (int64_t)N * V * es <= (int64_t)4 * 152 * BLOCKS * WARPS * SMALL ? SMALL : LARGE;
+    p.piece = (int64_t)N * V * es <= SMALL_BYTES ? SMALL : LARGE;
     p.pieces = 1;
     auto segs = [&] {
         const int64_t n = (int64_t)p.pieces * (p.piece / es);
@@ -470,6 +473,13 @@ VerifyPlan plan_verify(int N, int V, int es) {
     while (segs() > MAX_SEGS) p.pieces *= 2;
     p.segs = (int)segs();
     return p;
+}
+// Fewer requests may take small pieces and then have more segments: the most segments of a call of up to N requests
+// (28 requests of 131,072 fp32 tokens have 14,364, 29 have 7,453), so that one workspace serves a shrinking batch.
+int64_t most_segments(int N, int V, int es) {
+    const VerifyPlan p = plan_verify(N, V, es);
+    const int64_t small = std::min<int64_t>(N, SMALL_BYTES / ((int64_t)V * es));  // requests that take small pieces
+    return small < 1 ? (int64_t)N * p.segs : std::max((int64_t)N * p.segs, small * plan_verify((int)small, V, es).segs);
 }
 template <typename T, int PIECE> int launch_verify(const VerifyArgs &a, cudaStream_t s) {
     constexpr int SMEM = WARPS * STAGES * ROOM_OF<PIECE>;
@@ -503,7 +513,7 @@ extern "C" {
 
 size_t kda_verify_drafts_workspace_size(int N, int W, int V, int dtype) {
     if (N < 1 || N > MAX_N || W < 1 || W > MAX_W || V < 1 || V > MAX_V || (dtype != KDA_F32 && dtype != KDA_BF16)) return 0;
-    return (size_t)N * plan_verify(N, V, dtype == KDA_BF16 ? 2 : 4).segs * sizeof(uint64_t);
+    return (size_t)most_segments(N, V, dtype == KDA_BF16 ? 2 : 4) * sizeof(uint64_t);
 }
 
 int kda_verify_drafts(const void *target, const void *draft, const int32_t *draft_tokens, const float *uniforms,

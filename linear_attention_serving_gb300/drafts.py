@@ -28,7 +28,7 @@ def _rows(name, t, n, w, v, dtype, index):
 
 
 def verify_drafts_workspace_size(n: int, W: int, vocabulary: int, dtype=torch.float32) -> int:
-    """Bytes of workspace that verify_drafts needs (0 for shapes it does not take)."""
+    """Bytes of workspace that verify_drafts needs for up to n requests (0 for shapes it does not take)."""
     if dtype not in _CODE:
         return 0
     return int((paged._declared or paged._lib()).kda_verify_drafts_workspace_size(n, W, vocabulary, _CODE[dtype]))

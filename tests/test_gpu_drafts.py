@@ -352,3 +352,17 @@ def test_drafted_tokens_past_a_large_vocabulary(n, V, dtype):
     ref, token = by_sums(with_no_token(target), None, torch.full_like(tokens, V), u)
     assert (acc == 0).all() and (ref == 0).all()
     assert torch.equal(out[:, 0].long(), token)
+
+
+def test_one_workspace_for_shrinking_batches():
+    """That of 40 requests does for 28, which take smaller pieces and more of them, and for one."""
+    V, w = 131_072, 2
+    ws = torch.empty(kda.verify_drafts_workspace_size(40, w, V), dtype=torch.uint8, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(4)
+    target = (2 * torch.randn(40, w, V, generator=g, device=DEV)).softmax(2)
+    tokens, u = target[:, :1].argmax(2).int(), torch.rand(40, w, generator=g, device=DEV)
+    u[:20, 0] = 0.9999
+    ref, token = by_sums(target, None, tokens, u)
+    for n in (40, 28, 29, 7, 1):
+        acc, out = kda.verify_drafts(target[:n], tokens[:n], u[:n], workspace=ws)
+        assert torch.equal(acc.long(), ref[:n]) and torch.equal(out.gather(1, ref[:n, None])[:, 0].long(), token[:n])

@@ -157,3 +157,11 @@ def test_plain_form_of_one_certain_draft():
     acc, out = verify_ref(target, tokens, u)
     for a, row, d in zip(acc, out, tokens[:, 0].tolist()):
         assert row[0] == d if a else (row[0] != d and row[1] == -1)
+
+
+@pytest.mark.parametrize("V,dtype", [(131_072, torch.float32), (32_768, torch.float32), (100_003, torch.bfloat16), (7, torch.float32),
+                                     (5_000_000, torch.float32), (1_900_000, torch.bfloat16)])
+def test_a_workspace_does_for_fewer_requests(V, dtype):
+    """Sizes never fall as requests come (a server keeps one for its largest batch)."""
+    size = [kda.verify_drafts_workspace_size(n, 5, V, dtype) for n in range(1, 700)]
+    assert size[0] > 0 and all(a <= b for a, b in zip(size, size[1:]))
