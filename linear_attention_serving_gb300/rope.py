@@ -29,8 +29,8 @@ def rope_frequencies(rot_dim, base=10000.0, scaling="none", factor=1.0, original
                                   freq.data_ptr(), ctypes.byref(amplitude))
     if rc:
         _check(rc, "kda_rope_frequencies")
-    # (from pageable memory the copy is staged before the call returns)
-    return freq if device is None else freq.to(device, non_blocking=True), amplitude.value
+    # (once per model: the copy is waited for, so that any stream may read the table)
+    return freq if device is None else freq.to(device), amplitude.value
 
 
 def _rows(name, t, index, shape=None, dtype=None):

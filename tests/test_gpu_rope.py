@@ -315,3 +315,21 @@ def test_binding_refusals():
         a.update(kw_)
         with pytest.raises(kda.KDAError):
             kda.paged_rope_append(**a)
+
+
+def test_frequencies_are_there_for_every_stream():
+    """The table is read at once on a stream that nothing orders behind the one it was made on."""
+    want, _ = kda.rope_frequencies(128)
+    side, work = torch.cuda.Stream(), torch.cuda.Stream()
+    got = torch.empty(20, 64, dtype=torch.int64, device=DEV)
+    stale = [torch.full((64,), -1, dtype=torch.int64, device=DEV) for _ in range(40)]
+    torch.cuda.synchronize()
+    del stale  # (memory that holds something else)
+    for i in range(20):
+        with torch.cuda.stream(work):
+            torch.cuda._sleep(20_000_000)
+            freq, _ = kda.rope_frequencies(128, device=DEV)
+        with torch.cuda.stream(side):
+            got[i].copy_(freq)
+    torch.cuda.synchronize()
+    assert torch.equal(got.cpu(), want.expand(20, 64))
