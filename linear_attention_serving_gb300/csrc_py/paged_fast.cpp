@@ -280,6 +280,13 @@ int turned(const Arg &a, const int64_t *&freq, int &device) {
     freq = (const int64_t *)f.data_ptr();
     return as_int(2 * f.numel());
 }
+// one for each token; none are needed where nothing turns
+const int32_t *positions_of(const Arg &a, int rot, int64_t T, int &device) {
+    if (a.none() && rot == 0) return nullptr;
+    const at::Tensor &x = given(a, at::kInt, device);
+    if (x.numel() != T) throw No();
+    return (const int32_t *)x.data_ptr();
+}
 
 // rope(q, k, positions, freq, amplitude, interleaved, q_weight, k_weight, eps, q_out, k_out)
 PyObject *rope(PyObject *, PyObject *const *args, Py_ssize_t n_args) {
@@ -291,10 +298,10 @@ PyObject *rope(PyObject *, PyObject *const *args, Py_ssize_t n_args) {
         int dev = q.get_device();
         const at::ScalarType t = q.scalar_type();
         const Rows qr = rows_of(q, t, dev), kr = rows_of(k, t, dev);
-        const at::Tensor &pos = given(a[2], at::kInt, dev);
-        if (kr.T != qr.T || pos.numel() != qr.T) throw No();
+        if (kr.T != qr.T) throw No();
         const int64_t *freq;
         const int rot = turned(a[3], freq, dev);
+        const int32_t *pos = positions_of(a[2], rot, qr.T, dev);
         const float *qw = (const float *)optional(a[6], at::kFloat, dev, HEAD), *kw = (const float *)optional(a[7], at::kFloat, dev, HEAD);
         const c10::cuda::OptionalCUDAGuard guard(q.device());
         at::Tensor qo, ko;
@@ -309,7 +316,7 @@ PyObject *rope(PyObject *, PyObject *const *args, Py_ssize_t n_args) {
             qor = rows_like(a[9], qo, q, t, dev);
             kor = rows_like(a[10], ko, k, t, dev);
         }
-        const int rc = f_rope(qr.p, kr.p, (const int32_t *)pos.data_ptr(), freq, (float)a[4].real(), qw, kw, (float)a[8].real(), qr.T,
+        const int rc = f_rope(qr.p, kr.p, pos, freq, (float)a[4].real(), qw, kw, (float)a[8].real(), qr.T,
                               qr.heads, kr.heads, (int)HEAD, rot, truth(a[5]) ? KDA_ROPE_INTERLEAVED : KDA_ROPE_HALF, code_of(t),
                               qr.stride, kr.stride, qor.p, kor.p, qor.stride, kor.stride, stream_of(dev));
         if (rc != KDA_OK) throw No();
@@ -328,19 +335,19 @@ PyObject *rope_append(PyObject *, PyObject *const *args, Py_ssize_t n_args) {
         int dev = q.get_device();
         const at::ScalarType t = q.scalar_type();
         const Rows qr = rows_of(q, t, dev), kr = rows_of(a[1].tensor(), t, dev), vr = rows_of(a[2].tensor(), t, dev);
-        const at::Tensor &pos = given(a[3], at::kInt, dev), &slots = given(a[4], at::kLong, dev);
+        const at::Tensor &slots = given(a[4], at::kLong, dev);
         const Cache c = cache_of(a[6], a[7], dev);
-        if (kr.T != qr.T || vr.T != qr.T || kr.heads != c.heads || vr.heads != c.heads || pos.numel() != qr.T || slots.numel() != qr.T)
-            throw No();
+        if (kr.T != qr.T || vr.T != qr.T || kr.heads != c.heads || vr.heads != c.heads || slots.numel() != qr.T) throw No();
         const int64_t *freq;
         const int rot = turned(a[5], freq, dev);
+        const int32_t *pos = positions_of(a[3], rot, qr.T, dev);
         const float *qw = (const float *)optional(a[10], at::kFloat, dev, HEAD), *kw = (const float *)optional(a[11], at::kFloat, dev, HEAD);
         const float *ks = scale_of(a[13], c, dev), *vs = scale_of(a[14], c, dev);
         void *err = optional(a[16], at::kInt, dev);
         const c10::cuda::OptionalCUDAGuard guard(q.device());
         at::Tensor qo;
         const Rows qor = rows_like(a[15], qo, q, t, dev);
-        const int rc = f_rope_append(qr.p, kr.p, vr.p, (const int32_t *)pos.data_ptr(), (const int64_t *)slots.data_ptr(), freq,
+        const int rc = f_rope_append(qr.p, kr.p, vr.p, pos, (const int64_t *)slots.data_ptr(), freq,
                                      (float)a[8].real(), qw, kw, (float)a[12].real(), qr.T, qr.heads, kr.heads, (int)HEAD, rot,
                                      truth(a[9]) ? KDA_ROPE_INTERLEAVED : KDA_ROPE_HALF, code_of(t), c.code, qr.stride, kr.stride,
                                      vr.stride, qor.p, qor.stride, ks, vs, c.k, c.v, c.pages, c.page_size, c.stride, (int32_t *)err,

@@ -55,7 +55,9 @@ def _common(q, k, positions, freq, q_weight, k_weight, q_out, index):
         raise KDAError(f"unsupported dtype {q.dtype}: q and k must be bfloat16 or float32")
     qs, ks = _rows("q", q, index), _rows("k", k, index, dtype=q.dtype)
     T = q.shape[0]
-    if k.shape[0] != T or positions.numel() != T:
+    if positions is None and freq is not None and freq.numel() > 0:
+        raise KDAError("positions may be None only without a rotation")
+    if k.shape[0] != T or (positions is not None and positions.numel() != T):
         raise KDAError("q and k must be [T, heads, 128], positions [T]")
     for t in (positions, freq, q_weight, k_weight):
         if t is not None and (t.get_device() != index or not t.is_contiguous()):
@@ -76,7 +78,8 @@ def qk_rope(q, k, positions, freq, amplitude=1.0, interleaved=False, q_weight=No
     """kda_qk_rope: q [T, Hq, 128] and k [T, Hkv, 128] (parts of one projection, say)
     normed for each head where a weight float32 [128] is given, and turned by
     positions int32 [T].  freq and amplitude from rope_frequencies; freq None: no
-    rotation.  Returns (q_out, k_out), which may be q and k themselves."""
+    rotation (positions may be None then).  Returns (q_out, k_out), which may be q and k
+    themselves."""
     done = paged._fast_rope(q, k, positions, freq, amplitude, interleaved, q_weight, k_weight, eps, q_out, k_out)
     if done is not None:
         return done
@@ -87,7 +90,7 @@ def qk_rope(q, k, positions, freq, amplitude=1.0, interleaved=False, q_weight=No
         k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
     kos = _rows("k_out", k_out, index, k.shape, q.dtype)
     with torch.cuda.device(index):
-        rc = lib.kda_qk_rope(q.data_ptr(), k.data_ptr(), positions.data_ptr(), _p(freq), amplitude, _p(q_weight), _p(k_weight),
+        rc = lib.kda_qk_rope(q.data_ptr(), k.data_ptr(), _p(positions), _p(freq), amplitude, _p(q_weight), _p(k_weight),
                              eps, q.shape[0], q.shape[1], k.shape[1], D, 0 if freq is None else 2 * freq.numel(),
                              int(interleaved), _CODE[q.dtype], qs, ks, q_out.data_ptr(), k_out.data_ptr(), qos, kos,
                              _raw_stream(index))
@@ -119,7 +122,7 @@ def paged_rope_append(q, k, v, positions, slot_map, freq, k_cache, v_cache, ampl
     if slot_map.numel() != q.shape[0]:
         raise KDAError("slot_map must be [T]")
     with torch.cuda.device(index):
-        rc = lib.kda_paged_rope_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), positions.data_ptr(), slot_map.data_ptr(),
+        rc = lib.kda_paged_rope_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), _p(positions), slot_map.data_ptr(),
                                        _p(freq), amplitude, _p(q_weight), _p(k_weight), eps, q.shape[0], q.shape[1], h, D,
                                        0 if freq is None else 2 * freq.numel(), int(interleaved), _CODE[q.dtype], code, qs, ks,
                                        vs, q_out.data_ptr(), qos, _p(k_scale), _p(v_scale), k_cache.data_ptr(),

@@ -333,3 +333,27 @@ def test_frequencies_are_there_for_every_stream():
             got[i].copy_(freq)
     torch.cuda.synchronize()
     assert torch.equal(got.cpu(), want.expand(20, 64))
+
+
+@pytest.mark.parametrize("plain", [False, True])
+def test_norms_without_positions(plain, monkeypatch):
+    """Nothing turns: no positions are needed; with a rotation they are."""
+    if plain:
+        monkeypatch.setattr(paged, "_fast_rope", lambda *a: None)
+        monkeypatch.setattr(paged, "_fast_rope_append", lambda *a: None)
+    qkv, pos, qw, kw = inputs(40, 4, 2, BF16, seed=31)
+    q, k, v = split(qkv, 4, 2)
+    slots = torch.arange(40, device=DEV)
+    want = kda.qk_rope(q, k, pos, None, q_weight=qw, k_weight=kw)
+    got = kda.qk_rope(q, k, None, None, q_weight=qw, k_weight=kw)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    rope_close(got[0], *rope_ref(q, pos, None, 1.0, False, qw, 1e-6), BF16)
+    (kc, vc), (kc2, vc2) = caches(4, 2, 16, BF16), caches(4, 2, 16, BF16)
+    want = kda.paged_rope_append(q, k, v, pos, slots, None, kc, vc, q_weight=qw, k_weight=kw)
+    got = kda.paged_rope_append(q, k, v, None, slots, None, kc2, vc2, q_weight=qw, k_weight=kw)
+    assert torch.equal(got, want) and torch.equal(kc, kc2) and torch.equal(vc, vc2)
+    freq, _ = kda.rope_frequencies(64, device=DEV)
+    with pytest.raises(kda.KDAError, match="positions"):
+        kda.qk_rope(q, k, None, freq)
+    with pytest.raises(kda.KDAError, match="positions"):
+        kda.paged_rope_append(q, k, v, None, slots, freq, kc, vc)
