@@ -8,7 +8,7 @@ import torch
 
 from . import paged
 from .kda import KDAError, _check
-from .paged import _CODE, _F32, _I32, _p, _raw_stream, _typed
+from .paged import _CODE, _F32, _I32, _fit, _ints, _p, _raw_stream, _typed
 
 DEVERR_TOKEN, DEVERR_PROBS = 64, 128
 
@@ -29,7 +29,7 @@ def _rows(name, t, n, w, v, dtype, index):
 
 def verify_drafts_workspace_size(n: int, W: int, vocabulary: int, dtype=torch.float32) -> int:
     """Bytes of workspace that verify_drafts needs for up to n requests (0 for shapes it does not take)."""
-    if dtype not in _CODE:
+    if dtype not in _CODE or not (_fit(n) and _fit(W) and _fit(vocabulary)):
         return 0
     return int((paged._declared or paged._lib()).kda_verify_drafts_workspace_size(n, W, vocabulary, _CODE[dtype]))
 
@@ -49,6 +49,7 @@ def verify_drafts(target, draft_tokens, uniforms, draft=None, n_draft=None, work
     if target.dim() != 3 or target.dtype not in _CODE:
         raise KDAError("target must be [n, W, vocabulary], float32 or bfloat16")
     n, w, v = target.shape
+    _ints("n W vocabulary", n, w, v)
     ts, tr = _rows("target", target, n, w, v, target.dtype, index)
     ds, dr = (0, 0) if draft is None else _rows("draft", draft, n, w - 1, v, target.dtype, index)
     for t in (draft_tokens, uniforms, n_draft, workspace, error_word):

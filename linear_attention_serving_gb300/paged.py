@@ -107,6 +107,17 @@ def _typed(dtype, names, *ts):
             raise KDAError(f"{name} must be {str(dtype).replace('torch.', '')}")
 
 
+def _fit(x, bits=32):
+    return -2 ** (bits - 1) <= x < 2 ** (bits - 1)
+
+
+def _ints(names, *xs):
+    """What the library takes as 32 bits fits them (ctypes would cut it down to them)."""
+    for name, x in zip(names.split(), xs):
+        if not _fit(x):
+            raise KDAError(f"{name} must fit 32 bits")
+
+
 def _p(t):
     return None if t is None else t.data_ptr()
 
@@ -162,6 +173,7 @@ def paged_tables(new_len, ctx_len, block_table, free_pages, free_head, T_total, 
     T = int(T_total)
     if T < 0:
         raise KDAError("T_total must not be negative")
+    _ints("n max_blocks n_free page_size n_pages", n, block_table.shape[1], free_pages.numel(), page_size, n_pages)
     slot_map = new_len.new_empty(T, dtype=_I64)
     positions, cu_q, kv_len, head = new_len.new_empty(T + 2 * n + 2).split_with_sizes((T, n + 1, n, 1))
     with torch.cuda.device(index):  # (the library launches on the current device)
@@ -203,6 +215,8 @@ def paged_append(k, v, slot_map, k_cache, v_cache, k_scale=None, v_scale=None, e
 
 def paged_attn_workspace_size(T_total: int, n_seqs: int, Hq: int, Hkv: int) -> int:
     """Bytes of workspace that paged_attn needs (0 for shapes it does not take)."""
+    if not (_fit(T_total, 64) and _fit(n_seqs) and _fit(Hq) and _fit(Hkv)):
+        return 0
     return int(_lib().kda_paged_attn_workspace_size(T_total, n_seqs, Hq, Hkv))
 
 
@@ -230,6 +244,7 @@ def paged_attn(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q=0, sm_scale
     n = kv_len.numel()
     if cu_q.numel() != n + 1 or block_table.dim() != 2 or block_table.shape[0] != n:
         raise KDAError("cu_q must be [n + 1], kv_len [n] and block_table [n, max_blocks]")
+    _ints("n heads max_blocks max_q window sinks", n, hq, block_table.shape[1], max_q, window, sinks)
     if out is None:
         out = torch.empty_like(q)
     elif out.shape != shape or out.dtype is not dtype:

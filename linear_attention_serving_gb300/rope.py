@@ -11,7 +11,7 @@ import torch
 
 from . import paged
 from .kda import D, KDAError, _check
-from .paged import _CODE, _F32, _I32, _I64, _cache, _p, _raw_stream, _typed
+from .paged import _CODE, _F32, _I32, _I64, _cache, _ints, _p, _raw_stream, _typed
 
 SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
@@ -22,6 +22,7 @@ def rope_frequencies(rot_dim, base=10000.0, scaling="none", factor=1.0, original
     model.  scaling: "none", "linear", "ntk" or "yarn" (contexts stretched by `factor`)."""
     if scaling not in SCALINGS:
         raise KDAError(f"unsupported scaling {scaling!r}: one of {', '.join(SCALINGS)}")
+    _ints("rot_dim", rot_dim)
     lib = paged._declared or paged._lib()
     freq = torch.empty(max(0, rot_dim // 2), dtype=_I64)
     amplitude = ctypes.c_float()
@@ -59,6 +60,7 @@ def _common(q, k, positions, freq, q_weight, k_weight, q_out, index):
         raise KDAError("positions may be None only without a rotation")
     if k.shape[0] != T or (positions is not None and positions.numel() != T):
         raise KDAError("q and k must be [T, heads, 128], positions [T]")
+    _ints("Hq Hkv rot_dim", q.shape[1], k.shape[1], 0 if freq is None else 2 * freq.numel())
     for t in (positions, freq, q_weight, k_weight):
         if t is not None and (t.get_device() != index or not t.is_contiguous()):
             raise KDAError("all tensors must be contiguous CUDA tensors on one device")

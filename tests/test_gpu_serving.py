@@ -91,3 +91,29 @@ def test_two_streams_do_not_mix():
     alone, beside = run([one, one]), run([torch.cuda.Stream(), torch.cuda.Stream()])
     for a, b in zip(alone, beside):
         assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("far", [2 ** 32 + 5, 2 ** 40, 2 ** 31, -2 ** 32 + 5])
+def test_numbers_past_32_bits_are_refused(far):
+    """A window, sinks or a size that the library's 32 bits do not hold is not cut down to what they do."""
+    def i32(*x):
+        return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+    new, ctx, table, free, head = i32(2), i32(3), i32(0, 1, -1, -1)[None], i32(1, 2, 3), i32(0)
+    kda.paged_tables(new, ctx, table, free, head, 2, 16, 8)
+    for page_size, n_pages in ((far - far % 16 + 16, 8), (16, far)):
+        with pytest.raises(kda.KDAError, match="32 bits"):
+            kda.paged_tables(new, ctx, table, free, head, 2, page_size, n_pages)
+    q = torch.randn(2, 2, 128, device="cuda")
+    cache = torch.randn(2, 1, 16, 128, device="cuda")
+    a = (q, cache, cache.flip(0), i32(0, 1)[None], i32(0, 2), i32(20))
+    kda.paged_attn(*a, max_q=2, window=5, sinks=5)
+    for kw in (dict(window=far), dict(window=5, sinks=far), dict(max_q=far)):
+        with pytest.raises(kda.KDAError, match="32 bits"):
+            kda.paged_attn(*a, **kw)
+
+
+def test_a_vocabulary_past_32_bits_is_refused():
+    p = torch.empty(1, 1, 2 ** 32 + 5, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(kda.KDAError, match="32 bits"):
+        kda.verify_drafts(p, torch.empty(1, 0, dtype=torch.int32, device="cuda"), torch.zeros(1, 1, device="cuda"))

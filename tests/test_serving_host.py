@@ -165,3 +165,22 @@ def test_a_workspace_does_for_fewer_requests(V, dtype):
     """Sizes never fall as requests come (a server keeps one for its largest batch)."""
     size = [kda.verify_drafts_workspace_size(n, 5, V, dtype) for n in range(1, 700)]
     assert size[0] > 0 and all(a <= b for a, b in zip(size, size[1:]))
+
+
+FAR = [2 ** 32 + 5, 2 ** 31, 2 ** 40, -2 ** 32 + 5]
+
+
+@pytest.mark.parametrize("far", FAR)
+def test_numbers_past_32_bits_on_the_host(far):
+    """Not cut down to their last 32 bits."""
+    assert kda.verify_drafts_workspace_size(5, 5, 100) > 0 and kda.paged_attn_workspace_size(5, 5, 8, 2) > 0
+    for at in range(3):
+        a = [5, 5, 100]
+        a[at] = far
+        assert kda.verify_drafts_workspace_size(*a) == 0
+        a = [5, 8, 2]
+        a[at] = far
+        assert kda.paged_attn_workspace_size(5, *a) == 0
+    assert kda.paged_attn_workspace_size(2 ** 64 + 5, 5, 8, 2) == 0
+    with pytest.raises(kda.KDAError, match="rot_dim"):
+        kda.rope_frequencies(far + 59)  # (64 in the last 32 bits of two of them)
