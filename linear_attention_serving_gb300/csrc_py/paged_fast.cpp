@@ -305,17 +305,7 @@ PyObject *rope(PyObject *, PyObject *const *args, Py_ssize_t n_args) {
         const float *qw = (const float *)optional(a[6], at::kFloat, dev, HEAD), *kw = (const float *)optional(a[7], at::kFloat, dev, HEAD);
         const c10::cuda::OptionalCUDAGuard guard(q.device());
         at::Tensor qo, ko;
-        Rows qor, kor;
-        if (a[9].none() && a[10].none()) {  // (one allocation for both)
-            const at::Tensor buf = at::empty({q.numel() + k.numel()}, q.options());
-            qo = part(buf, 0, q.sizes());
-            ko = part(buf, q.numel(), k.sizes());
-            qor = rows_of(qo, t, dev);
-            kor = rows_of(ko, t, dev);
-        } else {
-            qor = rows_like(a[9], qo, q, t, dev);
-            kor = rows_like(a[10], ko, k, t, dev);
-        }
+        const Rows qor = rows_like(a[9], qo, q, t, dev), kor = rows_like(a[10], ko, k, t, dev);
         const int rc = f_rope(qr.p, kr.p, pos, freq, (float)a[4].real(), qw, kw, (float)a[8].real(), qr.T,
                               qr.heads, kr.heads, (int)HEAD, rot, truth(a[5]) ? KDA_ROPE_INTERLEAVED : KDA_ROPE_HALF, code_of(t),
                               qr.stride, kr.stride, qor.p, kor.p, qor.stride, kor.stride, stream_of(dev));

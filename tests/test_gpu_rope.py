@@ -357,3 +357,18 @@ def test_norms_without_positions(plain, monkeypatch):
         kda.qk_rope(q, k, None, freq)
     with pytest.raises(kda.KDAError, match="positions"):
         kda.paged_rope_append(q, k, v, None, slots, freq, kc, vc)
+
+
+@pytest.mark.parametrize("plain", [False, True])
+@pytest.mark.parametrize("T", [1, 60, 2000])
+def test_keys_do_not_hold_the_queries_memory(T, plain, monkeypatch):
+    """The two results are tensors of their own."""
+    if plain:
+        monkeypatch.setattr(paged, "_fast_rope", lambda *a: None)
+    qkv, pos, qw, kw = inputs(T, 16, 2, BF16, seed=T)
+    q, k, _ = split(qkv, 16, 2)
+    freq, _ = kda.rope_frequencies(128, device=DEV)
+    want = rope_ref(k[-3:], pos[-3:], freq.tolist(), 1.0, False, kw, 1e-6)
+    for x in kda.qk_rope(q, k, pos, freq, q_weight=qw, k_weight=kw):
+        assert x.untyped_storage().nbytes() == x.nbytes
+    rope_close(x[-3:], *want, BF16)
