@@ -222,3 +222,21 @@ def test_refuses_negative_sinks():
     with pytest.raises(kda.KDAError):
         kda.paged_attn(d["q"].to(DEV), d["k_cache"].to(DEV), d["v_cache"].to(DEV), i32(d["table"]), i32(d["cu"]), i32(d["kv"]), window=5,
                        sinks=-1)
+
+
+@pytest.mark.parametrize("window,sinks,hidden", [(300, 9, True), (257, 140, False)])
+def test_single_tokens_by_the_kernel_for_few_rows_beside_chunks(window, sinks, hidden):
+    """Over 16,384 key tiles of windows and sinks the single tokens have a launch of their own: the requests of up to 16
+    rows of one kernel, the others' of the tile kernel, and the pieces of both in one join."""
+    n = 700
+    new, ctx = [1] * n + [150, 20], [400 + (37 * i) % 501 for i in range(n)] + [333, 805]
+    for i in range(0, n, 90):
+        new[i] = 1 + i // 90  # (up to 8 tokens of two heads)
+    kda.profile_enable(True)
+    try:
+        kda.profile_collect()
+        run(new, ctx, 8, 2, 16, BF16, window, sinks, seed=window, hidden=hidden)
+        names = [name for name, _ in kda.profile_collect()]
+    finally:
+        kda.profile_enable(False)
+    assert names == ["paged_few", "paged_tile", "paged_join"]
