@@ -539,7 +539,8 @@ int kda_paged_attn_sinks(const void *q, const void *k_cache, const void *v_cache
  * in fp32, rounded once at the end.  freq[i] is f_i in turns a position, times
  * 2^64 (kda_rope_frequencies): position times frequency is then exact modulo a
  * whole turn in 64-bit integers, at any position (negative ones too), and an
- * angle is off by less than 2^-25 radians however far the position.
+ * angle is off by less than 2^-25 radians from that however far the position.
+ * Any table of frequencies will do, a model's own too.
  * ========================================================================== */
 enum kda_rope_layout { KDA_ROPE_HALF = 0, KDA_ROPE_INTERLEAVED = 1 };
 enum kda_rope_scaling { KDA_ROPE_NONE = 0, KDA_ROPE_LINEAR = 1, KDA_ROPE_NTK = 2, KDA_ROPE_YARN = 3 };
@@ -553,7 +554,13 @@ enum kda_rope_scaling { KDA_ROPE_NONE = 0, KDA_ROPE_LINEAR = 1, KDA_ROPE_NTK = 2
  *                    as the pair's turns over the original length, original_len f_i / 2 pi,
  *                    go from beta_slow to beta_fast; amplitude 0.1 ln(factor) + 1
  *                    (Peng et al., "YaRN: Efficient Context Window Extension of Large
- *                    Language Models", section 3)
+ *                    Language Models", section 3).  This is the paper's text.  Many
+ *                    checkpoints are trained with another ramp, linear in the pair's
+ *                    number i between two whole pairs, and get frequencies from here that are
+ *                    not theirs (base 10^6, factor 4, 32,768 positions, 128 channels: 16 of 64
+ *                    pairs by over 1%, one by 42%): they take a table of their own, their f_i
+ *                    / 2 pi times 2^64
+ *   worked out in 64-bit floating point: within 2^-50 of f_i (2^-25 radians at p f_i = 2^25)
  *   rot_dim      a multiple of 8, 8 .. 128;  base > 1
  *   original_len, beta_fast, beta_slow   KDA_ROPE_YARN only: > 0, beta_fast > beta_slow >= 0
  *   freq         (host) int64 [rot_dim / 2], written;  amplitude (host), written
@@ -621,8 +628,8 @@ int kda_paged_rope_append(const void *q, const void *k, const void *v, const int
  *   workspace    kda_verify_drafts_workspace_size() bytes, 8-byte aligned; needs no initialisation, not
  *                shared by calls in flight.  The size for N requests does for fewer (of this V and dtype) too
  * The tests are exact.  Weights are summed as multiples of 2^-60 (each, p - q exactly, rounded once),
- * so sums do not depend on their order and the same call gives the same tokens; negative values
- * and NaN count as 0.  A row with values of 2 and more, or one that sums to 8 or more, has no
+ * so sums do not depend on their order and the same call gives the same tokens; as weights negative
+ * values and NaN count as 0, and a test against NaN is refused.  A row with values of 2 and more, or one that sums to 8 or more, has no
  * answer (some token, or -1).
  * A drafted token outside 0 .. V-1 records KDA_DEVERR_TOKEN and is refused; its q_j counts as the row of
  * `draft` where there is one, and as 0 all over where drafts are certain.  An n_draft out

@@ -19,7 +19,9 @@ SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 def rope_frequencies(rot_dim, base=10000.0, scaling="none", factor=1.0, original_len=0, beta_fast=32.0, beta_slow=1.0,
                      device=None):
     """kda_rope_frequencies: (freq int64 [rot_dim / 2] on `device`, amplitude), once per
-    model.  scaling: "none", "linear", "ntk" or "yarn" (contexts stretched by `factor`)."""
+    model.  scaling: "none", "linear", "ntk" or "yarn" (contexts stretched by `factor`).
+    "yarn" is the ramp of the paper's text, over a pair's turns; checkpoints trained with the
+    ramp over the pair's number take a table of their own, round(f_i / 2 pi * 2^64) in int64."""
     if scaling not in SCALINGS:
         raise KDAError(f"unsupported scaling {scaling!r}: one of {', '.join(SCALINGS)}")
     _ints("rot_dim", rot_dim)

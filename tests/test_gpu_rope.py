@@ -1,4 +1,6 @@
 """Rotary positions and per-head norms against their 64-bit form, alone and with the append."""
+import math
+
 import pytest
 import torch
 
@@ -372,3 +374,27 @@ def test_keys_do_not_hold_the_queries_memory(T, plain, monkeypatch):
     for x in kda.qk_rope(q, k, pos, freq, q_weight=qw, k_weight=kw):
         assert x.untyped_storage().nbytes() == x.nbytes
     rope_close(x[-3:], *want, BF16)
+
+
+def test_a_table_of_the_models_own():
+    """Frequencies whose ramp is linear in the pair's number (base 10^6, factor 4, 32,768 positions), as int64 turns
+    times 2^64: the rotation by p f_i in 64 bits, whose own angles are off by 2^-53 of p f_i."""
+    rot, base, factor, length = 128, 1e6, 4.0, 32768
+    low, high = (rot * math.log(length / (turns * 2 * math.pi)) / (2 * math.log(base)) for turns in (32.0, 1.0))
+    low, high = math.floor(low), math.ceil(high)
+    f = []
+    for i in range(rot // 2):
+        x, g = base ** (-2 * i / rot), 1 - min(1.0, max(0.0, (i - low) / (high - low)))
+        f.append(x * (g + (1 - g) / factor))
+    paper, amp = kda.rope_frequencies(rot, base=base, scaling="yarn", factor=factor, original_len=length)
+    off = [abs(a / 2.0 ** 64 * 2 * math.pi / b - 1) for a, b in zip(paper.tolist(), f)]
+    assert sum(x > 0.01 for x in off) == 16 and 0.41 < max(off) < 0.43  # (what include/kda.h says of the other ramp)
+    table = torch.tensor([round(x / (2 * math.pi) * 2 ** 64) for x in f], dtype=torch.int64)
+    qkv, pos, _, _ = inputs(500, 3, 1, F32, seed=41, top=131_072)
+    q, k, _ = split(qkv, 3, 1)
+    got, _ = kda.qk_rope(q, k, pos, table.to(DEV), amplitude=amp)
+    angle = pos.cpu().double()[:, None] * torch.tensor(f, dtype=torch.float64)
+    c, s = (amp * angle.cos())[:, None], (amp * angle.sin())[:, None]
+    a, b = q.double().cpu().split(rot // 2, 2)
+    size = amp * (a.abs() + b.abs()).repeat(1, 1, 2)
+    rope_close(got, torch.cat((a * c - b * s, a * s + b * c), 2), size, F32)

@@ -1,6 +1,7 @@
 """Refusals of the rotary, sinks and verification calls before anything is launched (no GPU needed), the
 frequencies, and the binding's own checks."""
 import ctypes
+import decimal
 import math
 
 import pytest
@@ -184,3 +185,26 @@ def test_numbers_past_32_bits_on_the_host(far):
     assert kda.paged_attn_workspace_size(2 ** 64 + 5, 5, 8, 2) == 0
     with pytest.raises(kda.KDAError, match="rot_dim"):
         kda.rope_frequencies(far + 59)  # (64 in the last 32 bits of two of them)
+
+
+@pytest.mark.parametrize("rot", [8, 96, 128])
+@pytest.mark.parametrize("kw", [dict(), dict(base=1e6), dict(base=500000.0, scaling="ntk", factor=32.0),
+                                dict(scaling="yarn", factor=16.0, original_len=4096)])
+def test_frequencies_to_more_digits(rot, kw):
+    """Within 2^-50 of the formula in 50 digits, and half a unit: the power, the ramp's two differences and quotient, the
+    sum of its parts and the quotient by a turn are under 8 roundings of 2^-53 or their like."""
+    d = decimal.Decimal
+    with decimal.localcontext() as ctx:
+        ctx.prec = 50
+        turn = 2 * d("3.14159265358979323846264338327950288419716939937510582")
+        base, factor = d(kw.get("base", 10000.0)), d(kw.get("factor", 1.0))
+        if kw.get("scaling") == "ntk":
+            base *= (factor.ln() * rot / (rot - 2)).exp()
+        freq, _ = kda.rope_frequencies(rot, **kw)
+        for i, got in enumerate(freq.tolist()):
+            f = (base.ln() * -2 * i / rot).exp()
+            if kw.get("scaling") == "yarn":
+                g = min(d(1), max(d(0), (kw["original_len"] * f / turn - 1) / 31))
+                f *= g + (1 - g) / factor
+            want = f / turn * 2 ** 64
+            assert abs(got - want) <= want * d(2) ** -50 + 1
