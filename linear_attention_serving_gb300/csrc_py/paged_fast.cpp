@@ -30,6 +30,7 @@ decltype(&kda_verify_drafts) f_verify = nullptr;
 decltype(&kda_verify_drafts_workspace_size) f_verify_ws = nullptr;
 
 constexpr int64_t HEAD = 128;
+constexpr int64_t SMALL_RESULTS = 1 << 20;  // bytes: what torch's allocator keeps with other small blocks
 
 struct No {};  // not for us: None
 
@@ -305,7 +306,19 @@ PyObject *rope(PyObject *, PyObject *const *args, Py_ssize_t n_args) {
         const float *qw = (const float *)optional(a[6], at::kFloat, dev, HEAD), *kw = (const float *)optional(a[7], at::kFloat, dev, HEAD);
         const c10::cuda::OptionalCUDAGuard guard(q.device());
         at::Tensor qo, ko;
-        const Rows qor = rows_like(a[9], qo, q, t, dev), kor = rows_like(a[10], ko, k, t, dev);
+        Rows qor, kor;
+        // Small results share an allocation (a token of 16 + 2 heads, its results kept: 15.9 us a call, with two 17.3);
+        // who keeps a prompt's keys does not keep its queries' memory too.
+        if (a[9].none() && a[10].none() && (q.numel() + k.numel()) * (int64_t)q.element_size() <= SMALL_RESULTS) {
+            const at::Tensor buf = at::empty({q.numel() + k.numel()}, q.options());
+            qo = part(buf, 0, q.sizes());
+            ko = part(buf, q.numel(), k.sizes());
+            qor = rows_of(qo, t, dev);
+            kor = rows_of(ko, t, dev);
+        } else {
+            qor = rows_like(a[9], qo, q, t, dev);
+            kor = rows_like(a[10], ko, k, t, dev);
+        }
         const int rc = f_rope(qr.p, kr.p, pos, freq, (float)a[4].real(), qw, kw, (float)a[8].real(), qr.T,
                               qr.heads, kr.heads, (int)HEAD, rot, truth(a[5]) ? KDA_ROPE_INTERLEAVED : KDA_ROPE_HALF, code_of(t),
                               qr.stride, kr.stride, qor.p, kor.p, qor.stride, kor.stride, stream_of(dev));
