@@ -258,6 +258,7 @@ int kda_paged_attn_sinks(const void *q, const void *k_cache, const void *v_cache
     // or, in calls with sinks, whose windows bound what there is to read: single tokens cost the tile kernel
     // some 0.14 us a key tile and SM more, and a launch of their own 15 to 20 us (24 of them beside 8
     // chunks, window 700, 91 us for 107; 200 over 800 keys beside one chunk 173 for 177; 100 over 4,000 keys 468 for 454).
+    // (Windows without sinks bound it as well, and keep the two launches that they had: the first of these 108 us.)
     const bool alone = a.sinks > 0 && (int64_t)n_seqs * Hkv * (((int64_t)a.window + a.sinks) / KEY_TILE + 2) <= ALONE_TILES;
     const bool few = !tiles || (!alone && a.G <= FEW_ROWS && n_seqs > 1 && T_total != (int64_t)n_seqs * a.max_q);
     if (few) {

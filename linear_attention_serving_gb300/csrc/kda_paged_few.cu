@@ -36,8 +36,8 @@
 // (6.7 TB/s, a copy's rate), of 64 requests over up to 65,536 e4m3 keys of 8 kv heads 405 to 411 us
 // (6.7 TB/s), one request over 8,192 keys 13.8 us with the join, which is starts, first
 // copies and the pieces' way through memory.  One token of 256 requests through a window of 2,048
-// beside 4 sinks, 4 kv heads 149 us (5.9 TB/s; 147 without sinks); five tokens of 64 requests over
-// e4m3 windows of 4,096 and 64 sinks, 8 kv heads 150 us (3.7 TB/s), where the softmax of the
+// beside 4 sinks, 4 kv heads 144 to 146 us (6.0 TB/s; 142 without sinks); five tokens of 64 requests over
+// e4m3 windows of 4,096 and 64 sinks, 8 kv heads 150 us (3.7 TB/s; a window of 4,160 alone the same), where the softmax of the
 // 20 rows is what each tile waits for.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>

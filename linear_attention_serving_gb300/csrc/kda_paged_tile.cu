@@ -30,7 +30,7 @@
 // TFLOP/s of the pairs that the mask leaves; some tiles more are multiplied where it
 // crosses them); 2,048 tokens, 32 heads, over 65,536 keys 1,501 to 1,541 us (1,405 to
 // 1,442 TFLOP/s, by the box: the clock falls under the load); 256 windows of 60 rows 258 us
-// (5.8 TB/s); 2,048 tokens, 32 heads, through windows of 4,096 beside 4 sinks 145 us (136 without
+// (5.8 TB/s); 2,048 tokens, 32 heads, through windows of 4,096 beside 4 sinks 145 us (137 without
 // sinks, whose tile each item reads).  Bound by the products (S for 64 keys reads its operands, by
 // their bytes, at three quarters of the rate) and by what the way from S to P leaves between them.
 // (A share of the exponentials by a polynomial made it slower, 250 to 276 us for 242 us: the special

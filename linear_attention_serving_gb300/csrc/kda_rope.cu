@@ -19,7 +19,7 @@
 //
 // Bound by HBM once there are some thousand tokens, by the launch and the chain position, angle,
 // row below: 23,100 packed tokens of 32 + 2 x 8 heads (bf16, norms) into their pages 89 us, 6.4
-// TB/s; 9,300 of 16 + 16 heads (fp32) 48 us, 6.3 TB/s; 1,280 tokens into an e4m3 cache 9.7 us; one
+// TB/s; 9,300 of 16 + 16 heads (fp32) 48 us, 6.3 TB/s; 1,280 tokens into an e4m3 cache 9.6 us; one
 // token 2.8 us.  Two rows a unit in flight and two ahead of them, 64 registers: with four
 // of each, 80 registers and three blocks an SM, the first was 92 to 109 us; with rows of all
 // kinds in one stream of batches, 111.
@@ -418,7 +418,7 @@ dim3 rope_grid(RopeArgs &a, int rows, int &log) {
         // us, of 24 46, of 6 16; eight tokens to a block 46, 47 and 26).  With 48 rows there are too few units
         // left to fill the last wave (81 us eight tokens to a block, 87 one to a unit).
         log = rows <= 24 ? EACH : MANY;
-    } else if (a.T >= 4 * sms) {  // (1,280 tokens of 48 rows: 8.6 us; 11.2 a block to each, 10.4 eight to a block)
+    } else if (a.T >= 4 * sms) {  // (1,280 tokens of 48 rows, bf16 and e4m3 caches: 8.3 and 9.6 us; 11.0 and 11.9 a block to each, 10.2 and 12.1 eight to a block)
         log = SOME;
     } else {
         // a block to a token, or several to one where there are few: a row for each unit

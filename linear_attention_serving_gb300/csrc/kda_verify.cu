@@ -16,8 +16,8 @@
 // Bound by HBM (one row of p, or of p and q, for each request), which takes copies in flight:
 // each warp has bulk copies of its next pieces under way into shared memory, and neither
 // registers nor other warps have a part in it.  256 requests of 131,072 tokens (four drafts, fp32, 234 MB read)
-// 47 us, of which the second launch's part 3; 64 of 100,003 in bf16, no draft probabilities, 13 us, and one of
-// 32,768 5.8 us, which are the chain of launch, tests, row, sums, place.  (A cluster of blocks to a
+// 45 us, of which the second launch's part 3; 64 of 100,003 in bf16, no draft probabilities, 13 us, and one of
+// 32,768 5.8 to 6.3 us, which are the chain of launch, tests, row, sums, place.  (A cluster of blocks to a
 // request, registers for what is under way, took 59, 13.7 and 7.2 us.)
 #include <algorithm>
 
